@@ -381,7 +381,7 @@ def _run_own(st):
         h, y, stats = gb.gattn_norm_fwd(st["res"], st["x"], st["gate"], eps=st["eps"], **par)
         res = {"h": h, "y": y}
         if c["train"]:
-            got = gb.gattn_norm_bwd(h, stats, st["dh"], st["dy"], st["x"], st["gate"], **par)
+            got = gb.gattn_norm_bwd(st["res"], stats, st["dh"], st["dy"], st["x"], st["gate"], **par)
             res.update({k: v for k, v in got.items() if v is not None})
         return res
     lay = {"block": c["block"], "q_block": c["q_block"], "len_k": st["len_k"], "causal": c["causal"]}
@@ -415,7 +415,7 @@ def work(case):
         moved = (4 + tok) * n * es                               # res, x, gate in; h, y out
         flops = 20 * n
         if case["train"]:
-            moved += (4 + tok + 2 + tok) * n * es                # h, x, dh, dy, gate in; dres, dx, dgate out
+            moved += (4 + tok + 2 + tok) * n * es                # res, x, dh, dy, gate in; dres, dx, dgate out
             flops += 40 * n
         return {"bytes": moved, "flops": flops}
     sq, sk, lk = _layout(case)
