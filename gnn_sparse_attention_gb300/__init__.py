@@ -11,7 +11,10 @@ __all__ = ["Score", "Plan", "GattnError", "gattn_plan_create", "gattn_plan_get_i
            "gattn_workspace_size", "gattn_fwd", "gattn_bwd", "gattn_bwd_dq", "gattn_bwd_dkdv",
            "gattn_plan_check_errors", "gattn_fwd_noalloc", "gattn_reorder", "gattn_permute_csr",
            "gattn_permute_rows", "gattn_pool_workspace_size", "gattn_pool_fwd", "gattn_pool_bwd",
-           "gattn_spmm_workspace_size", "gattn_spmm", "gattn_version", "load_library"]
+           "gattn_spmm_workspace_size", "gattn_spmm", "gattn_block_units", "gattn_block_count",
+           "gattn_block_sums", "gattn_block_select", "gattn_block_fwd", "gattn_block_bwd",
+           "gattn_block_check_errors", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_version",
+           "load_library"]
 
 
 def __getattr__(name):

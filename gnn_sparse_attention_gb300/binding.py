@@ -28,7 +28,11 @@ EXPORTED = ("gattn_plan_create", "gattn_plan_destroy", "gattn_plan_get_info",
             "gattn_plan_export_tiles", "gattn_plan_export_tile_bwd", "gattn_reorder", "gattn_permute_csr",
             "gattn_permute_rows", "gattn_pool_workspace_size", "gattn_pool_fwd",
             "gattn_pool_bwd", "gattn_spmm_workspace_size", "gattn_spmm",
-            "gattn_plan_set_wait_test", "gattn_last_error", "gattn_version")
+            "gattn_plan_set_wait_test", "gattn_block_sums", "gattn_block_select_workspace_size",
+            "gattn_block_select", "gattn_block_fwd_workspace_size", "gattn_block_fwd",
+            "gattn_block_bwd_workspace_size", "gattn_block_bwd", "gattn_block_check_errors",
+            "gattn_norm_workspace_size", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_last_error",
+            "gattn_version")
 
 
 class GattnError(RuntimeError):
@@ -57,6 +61,21 @@ class _PlanInfo(ctypes.Structure):
                 ("device_bytes", ctypes.c_size_t), ("n_tiles", ctypes.c_int64),
                 ("n_tile_rows", ctypes.c_int64), ("tile_edges", ctypes.c_int64),
                 ("tile_min_edges", ctypes.c_int32)]
+
+
+class _BlockDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "Nq", "Nk", "H", "Hkv", "D", "dtype", "block",
+                                              "q_block", "topk", "causal")]
+    _fields_ += [("scale", ctypes.c_float), ("max_len_k", ctypes.c_int32),
+                 ("seq_q", ctypes.c_void_p), ("seq_k", ctypes.c_void_p),
+                 ("len_k", ctypes.c_void_p), ("idx_stride", ctypes.c_int64 * 2)]
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("gate", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("b_pre", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -114,8 +133,21 @@ def load_library(path: str | None = None):
         lib.gattn_spmm_workspace_size.argtypes = [P, i32, ctypes.c_int, ctypes.POINTER(sz)]
         lib.gattn_spmm.argtypes = [P, i32, ctypes.c_int, P, P, P, i32, P, sz, P]
         lib.gattn_plan_set_wait_test.argtypes = [P, i32]
-        for name in EXPORTED[:22]:
-            getattr(lib, name).restype = st
+        bd, nd, psz = ctypes.POINTER(_BlockDesc), ctypes.POINTER(_NormDesc), ctypes.POINTER(sz)
+        lib.gattn_block_sums.argtypes = [bd, P, P, P, P]
+        lib.gattn_block_select_workspace_size.argtypes = [bd, psz]
+        lib.gattn_block_select.argtypes = [bd, P, P, P, P, sz, P]
+        lib.gattn_block_fwd_workspace_size.argtypes = [bd, psz]
+        lib.gattn_block_fwd.argtypes = [bd] + [P] * 7 + [sz, P]
+        lib.gattn_block_bwd_workspace_size.argtypes = [bd, psz]
+        lib.gattn_block_bwd.argtypes = [bd] + [P] * 11 + [sz, P]
+        lib.gattn_block_check_errors.argtypes = []
+        lib.gattn_norm_workspace_size.argtypes = [nd, psz]
+        lib.gattn_norm_fwd.argtypes = [nd] + [P] * 7
+        lib.gattn_norm_bwd.argtypes = [nd] + [P] * 14 + [sz, P]
+        for name in EXPORTED:
+            if name not in ("gattn_last_error", "gattn_version"):
+                getattr(lib, name).restype = st
         lib.gattn_last_error.restype = ctypes.c_char_p
         lib.gattn_last_error.argtypes = []
         lib.gattn_version.restype = ctypes.c_char_p
@@ -514,3 +546,295 @@ def gattn_fwd_noalloc(plan: Plan, Q, K, V, score: Score, out, lse, stream=None):
                                             _ptr(K), _ptr(V), ctypes.byref(sc), _ptr(out),
                                             _ptr(lse), _stream(stream)), "gattn_fwd_noalloc")
     return out, lse
+
+
+# ----------------------------------------------------------------------------
+# attention over selected blocks, and the gated residual norm
+# ----------------------------------------------------------------------------
+def _cuda(dtype, **tensors):
+    """Contiguous CUDA tensors of one device (None is skipped); returns the device."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor"
+                             + (f" of {dtype}" if dtype is not None else ""))
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _same(shape, dtype, dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)} on {dev}")
+
+
+class _Launch:
+    """Current device and stream of one call; what the call allocates is tied to its stream."""
+
+    def __init__(self, dev, stream):
+        self._guard = torch.cuda.device(dev)
+        self.dev, self._given = dev, stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        self.current = torch.cuda.current_stream()
+        self.stream = self.current if self._given is None else self._given
+        if self.stream.device != self.dev:
+            self._guard.__exit__(None, None, None)
+            raise ValueError(f"stream of {self.stream.device} for tensors on {self.dev}")
+        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        self._guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.stream != self.current:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, given, size_fn, desc):
+        """(pointer, bytes, keep-alive) of the caller's workspace, or of a new one."""
+        if given is None:
+            n = ctypes.c_size_t()
+            fn = getattr(load_library(), size_fn)
+            _check(fn(ctypes.byref(desc), ctypes.byref(n)), size_fn)
+            given = self.empty((max(n.value, 16),), torch.uint8)
+        elif not given.is_cuda or given.device != self.dev or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.dev}")
+        return _ptr(given), given.numel() * given.element_size(), given
+
+
+def _block_desc(Nq, Nk, H, Hkv, D, dtype, seq_q, seq_k, len_k, block, q_block=1, topk=1,
+                scale=0.0, causal=False, max_len_k=0):
+    seqs = {"seq_q": seq_q, "seq_k": seq_k, "len_k": len_k}
+    for name, t in seqs.items():
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
+                              or not t.is_cuda):
+            raise ValueError(f"{name} must be a contiguous one-dimensional int32 CUDA tensor")
+    S = seq_k.numel() - 1
+    if S < 0 or seq_q.numel() != S + 1 or (len_k is not None and len_k.numel() != S):
+        raise ValueError("seq_q and seq_k need S + 1 entries and len_k S")
+    return _BlockDesc(S, Nq, Nk, H, Hkv, D, _dtype_code(dtype), int(block), int(q_block),
+                      int(topk), int(bool(causal)), float(scale), int(max_len_k),
+                      seq_q.data_ptr(), seq_k.data_ptr(),
+                      len_k.data_ptr() if len_k is not None else None)
+
+
+def gattn_block_units(Nq: int, S: int, q_block: int) -> int:
+    """Rows of idx: table rows of the query units of S sequences with Nq rows together."""
+    return Nq // q_block + (S if q_block > 1 else 0)
+
+
+def gattn_block_count(Nk: int, S: int, block: int) -> int:
+    """Rows of sums: table rows of the key blocks of S sequences with Nk rows together."""
+    return Nk // block + S
+
+
+def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None, since=None,
+                     sums=None, stream=None) -> torch.Tensor:
+    """fp64 sums [blocks, Hkv, D] of the keys of each block (include/gattn.h).
+
+    ``since`` (int32 [S]) renews only the blocks with positions from there on
+    and needs ``sums``, the table to renew.
+    """
+    if K.dim() != 3:
+        raise ValueError("K must have the shape [Nk, Hkv, D]")
+    Nk, Hkv, D = K.shape
+    dev = _cuda(None, K=K, seq_k=seq_k, lens=lens, since=since, sums=sums)
+    desc = _block_desc(0, Nk, Hkv, Hkv, D, K.dtype, seq_k, seq_k, lens, block)
+    if since is not None and (sums is None or since.dtype != torch.int32
+                              or since.numel() != desc.S):
+        raise ValueError("since must be int32 [S] and needs sums")
+    shape = (gattn_block_count(Nk, desc.S, block) if desc.S else 0, Hkv, D)
+    _same(shape, torch.float64, dev, sums=sums)
+    with _Launch(dev, stream) as run:
+        out = run.empty(shape, torch.float64) if sums is None else sums
+        _check(load_library().gattn_block_sums(ctypes.byref(desc), _ptr(K), _ptr(since),
+                                               _ptr(out), run.handle), "gattn_block_sums")
+    return out
+
+
+def gattn_block_select(Q: torch.Tensor, sums: torch.Tensor, seq_q: torch.Tensor,
+                       seq_k: torch.Tensor, topk: int, block: int, q_block: int, nk: int,
+                       len_k=None, causal: bool = False, max_len_k: int = 0, idx=None,
+                       workspace=None, stream=None) -> torch.Tensor:
+    """The topk blocks of highest score of every unit and key head: int32 [units, Hkv, topk].
+
+    ``nk`` is the number of key rows that ``sums`` was built from and
+    ``max_len_k`` the most keys of one sequence (0: nk).
+    """
+    if Q.dim() != 3 or sums.dim() != 3:
+        raise ValueError("Q must have the shape [Nq, H, D] and sums [blocks, Hkv, D]")
+    Nq, H, D = Q.shape
+    Hkv = sums.shape[1]
+    dev = _cuda(None, Q=Q, sums=sums, seq_q=seq_q, seq_k=seq_k, len_k=len_k, idx=idx)
+    desc = _block_desc(Nq, nk, H, Hkv, D, Q.dtype, seq_q, seq_k, len_k, block, q_block, topk,
+                       0.0, causal, max_len_k)
+    _same((gattn_block_count(nk, desc.S, block) if desc.S else 0, Hkv, D), torch.float64, dev,
+          sums=sums)
+    shape = (gattn_block_units(Nq, desc.S, q_block) if desc.S else 0, Hkv, topk)
+    _same(shape, torch.int32, dev, idx=idx)
+    with _Launch(dev, stream) as run:
+        out = run.empty(shape, torch.int32) if idx is None else idx
+        ws, n, _keep = run.workspace(workspace, "gattn_block_select_workspace_size", desc)
+        _check(load_library().gattn_block_select(ctypes.byref(desc), _ptr(Q), _ptr(sums),
+                                                 _ptr(out), ws, n, run.handle),
+               "gattn_block_select")
+    return out
+
+
+def _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k, **more):
+    if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape or idx.dim() != 3:
+        raise ValueError("need Q [Nq, H, D], K and V [Nk, Hkv, D] and idx [units, Hkv, topk]")
+    Nq, H, D = Q.shape
+    Nk, Hkv, _ = K.shape
+    dev = _cuda(None, Q=Q, K=K, V=V, seq_q=seq_q, seq_k=seq_k, len_k=len_k, **more)
+    _same((Nk, Hkv, D), Q.dtype, dev, K=K, V=V)
+    desc = _block_desc(Nq, Nk, H, Hkv, D, Q.dtype, seq_q, seq_k, len_k, block, q_block,
+                       idx.shape[2], scale, causal)
+    units = gattn_block_units(Nq, desc.S, q_block) if desc.S else 0
+    if (idx.device != dev or idx.dtype != torch.int32 or tuple(idx.shape[:2]) != (units, Hkv)
+            or (idx.shape[2] > 1 and idx.stride(2) != 1)):
+        raise ValueError(f"idx must be int32 of shape ({units}, {Hkv}, topk) on {dev}, each list "
+                         "contiguous")
+    su, sh = idx.stride()[:2]
+    if su == 0 and sh == 0 and units * Hkv > 1:
+        raise ValueError("idx repeats one list for all units and heads; make it contiguous")
+    desc.idx_stride[0], desc.idx_stride[1] = su, sh
+    return desc, dev
+
+
+def gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block: int, q_block: int, scale: float = 0.0,
+                    causal: bool = False, len_k=None, out=None, lse=None, workspace=None,
+                    stream=None):
+    """Softmax attention over the blocks that idx lists: (out [Nq, H, D], lse fp32 [Nq, H]).
+
+    Rows of no sequence are not written; tensors that the call allocates hold
+    anything there.
+    """
+    desc, dev = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
+    _same(Q.shape, Q.dtype, dev, out=out)
+    _same(Q.shape[:2], torch.float32, dev, lse=lse)
+    with _Launch(dev, stream) as run:
+        out = run.empty(Q.shape, Q.dtype) if out is None else out
+        lse = run.empty(Q.shape[:2], torch.float32) if lse is None else lse
+        ws, n, _keep = run.workspace(workspace, "gattn_block_fwd_workspace_size", desc)
+        _check(load_library().gattn_block_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V),
+                                              _ptr(idx), _ptr(out), _ptr(lse), ws, n, run.handle),
+               "gattn_block_fwd")
+    return out, lse
+
+
+def gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout, lse, block: int, q_block: int,
+                    scale: float = 0.0, causal: bool = False, len_k=None, dQ=None, dK=None,
+                    dV=None, workspace=None, stream=None):
+    """Gradients (dQ, dK, dV) of gattn_block_fwd; rows of no sequence are not written."""
+    desc, dev = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
+    _same(Q.shape, Q.dtype, dev, out=out, dout=dout, dQ=dQ)
+    _same(Q.shape[:2], torch.float32, dev, lse=lse)
+    _same(K.shape, Q.dtype, dev, dK=dK, dV=dV)
+    with _Launch(dev, stream) as run:
+        dQ = run.empty(Q.shape, Q.dtype) if dQ is None else dQ
+        dK = run.empty(K.shape, K.dtype) if dK is None else dK
+        dV = run.empty(K.shape, K.dtype) if dV is None else dV
+        ws, n, _keep = run.workspace(workspace, "gattn_block_bwd_workspace_size", desc)
+        _check(load_library().gattn_block_bwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V),
+                                              _ptr(idx), _ptr(out), _ptr(dout), _ptr(lse),
+                                              _ptr(dQ), _ptr(dK), _ptr(dV), ws, n, run.handle),
+               "gattn_block_bwd")
+    return dQ, dK, dV
+
+
+def gattn_block_check_errors() -> None:
+    """Raise GattnError(GATTN_ERR_TIMEOUT) if a block-attention kernel gave up a bounded wait."""
+    _check(load_library().gattn_block_check_errors(), "gattn_block_check_errors")
+
+
+NORM = {"rms": 0, "layer": 1}
+
+
+def _norm_desc(ref, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps, dev):
+    if ref.dim() != 2:
+        raise ValueError("rows must be a tensor [N, F]")
+    if kind not in NORM:
+        raise ValueError(f"unknown norm kind {kind!r}")
+    N, F = ref.shape
+    mode = 0
+    if gate is not None:
+        mode = 1 if gate.dim() == 1 else 2
+        _same((F,) if mode == 1 else (N, F), torch.float32 if mode == 1 else ref.dtype, dev,
+              gate=gate)
+    _same((F,), torch.float32, dev, w_post=w_post, b_post=b_post, w_pre=w_pre, b_pre=b_pre)
+    ptr = [t.data_ptr() if t is not None else None for t in (w_post, b_post, w_pre, b_pre)]
+    return _NormDesc(N, F, _dtype_code(ref.dtype), NORM[kind], mode, float(alpha), float(eps),
+                     *ptr)
+
+
+def gattn_norm_fwd(res, x=None, gate=None, w_post=None, b_post=None, w_pre=None, b_pre=None,
+                   alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6, h=None, y=None,
+                   stats=None, stream=None):
+    """h = res + alpha * gate * norm(x; w_post, b_post), y = norm(h; w_pre, b_pre).
+
+    res, x: [N, F]; gate: [N, F] in their dtype, or fp32 [F], or None for 1;
+    weights and biases fp32 [F].  Without w_post the first norm is left out,
+    without w_pre the second (y is None), without x h is res itself.  Returns
+    (h, y, stats); stats (fp32 [N, 4]) goes to gattn_norm_bwd.
+    """
+    dev = _cuda(None, res=res, x=x, gate=gate, w_post=w_post, b_post=b_post, w_pre=w_pre,
+                b_pre=b_pre)
+    desc = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps, dev)
+    _same(res.shape, res.dtype, dev, x=x, h=h, y=y)
+    _same((res.shape[0], 4), torch.float32, dev, stats=stats)
+    with _Launch(dev, stream) as run:
+        if x is None:
+            h = res
+        elif h is None:
+            h = run.empty(res.shape, res.dtype)
+        if w_pre is None:
+            y = None
+        elif y is None:
+            y = run.empty(res.shape, res.dtype)
+        stats = run.empty((res.shape[0], 4), torch.float32) if stats is None else stats
+        _check(load_library().gattn_norm_fwd(ctypes.byref(desc), _ptr(res), _ptr(x), _ptr(gate),
+                                             _ptr(h) if x is not None else None, _ptr(y),
+                                             _ptr(stats), run.handle), "gattn_norm_fwd")
+    return h, y, stats
+
+
+def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None, b_post=None,
+                   w_pre=None, b_pre=None, alpha: float = 1.0, kind: str = "rms",
+                   workspace=None, stream=None) -> dict:
+    """Gradients of gattn_norm_fwd from dh (of h, or None) and dy (of y), at the forward's
+    res, x, gate and stats.
+
+    Returns a dict of dres, dx, dgate, dw_post, db_post, dw_pre, db_pre; None
+    where the operand is absent.
+    """
+    dev = _cuda(None, res=res, stats=stats, dh=dh, dy=dy, x=x, gate=gate, w_post=w_post,
+                b_post=b_post, w_pre=w_pre, b_pre=b_pre)
+    desc = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, 0.0, dev)
+    _same(res.shape, res.dtype, dev, dh=dh, dy=dy, x=x)
+    _same((res.shape[0], 4), torch.float32, dev, stats=stats)
+    F = res.shape[1]
+    with _Launch(dev, stream) as run:
+        def like(t, shape, dtype):
+            return None if t is None else run.empty(shape, dtype)
+
+        g = {"dres": run.empty(res.shape, res.dtype), "dx": like(x, res.shape, res.dtype),
+             "dgate": None if gate is None else run.empty(gate.shape, gate.dtype)}
+        for n, t in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre),
+                     ("db_pre", b_pre)):
+            g[n] = like(t, (F,), torch.float32)
+        ws, n, _keep = run.workspace(workspace, "gattn_norm_workspace_size", desc)
+        _check(load_library().gattn_norm_bwd(ctypes.byref(desc), _ptr(res), _ptr(stats), _ptr(dh),
+                                             _ptr(dy), _ptr(x), _ptr(gate),
+                                             *[_ptr(t) for t in g.values()], ws, n, run.handle),
+               "gattn_norm_bwd")
+    return g

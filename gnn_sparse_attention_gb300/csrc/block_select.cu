@@ -1,0 +1,480 @@
+// block_select.cu -- the cheap score that chooses blocks: 64-bit sums of
+// every block of keys and every unit of queries, scores, and the topk best.
+//
+// The choice is a whole number that must not hang on the order of a sum, so
+// it is defined by scores in 64 bits.  Sums run as pairs of fp32 (each
+// addition keeps its exact rounding error in the second member, about 48
+// bits, at fp32 rates: this GPU's fp64 units would take four times as long as
+// the memory).  Scores run in fp32 FMAs with an error bound
+//   |score - exact| <= e = (D + 32) 2^-23 |q| max|k / n|   (Cauchy-Schwarz),
+// a radix select finds the topk-th score T, blocks above T + 2e are in, below
+// T - 2e out, and only blocks in between are scored again in fp64.
+#include <algorithm>
+
+#include "attn_launch.cuh"
+#include "block.cuh"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kThr = 256;
+
+// 16 bytes of a row as fp32
+template <class T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int V = 4;
+  __device__ static void load(const float* p, float* f) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int V = 8;
+  __device__ static void load(const __nv_bfloat16* p, float* f) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+struct SumParams {
+  BlockGeom g;
+  const void* x;
+  const int32_t* since;
+  double* sums;
+  int per, heads;  // rows per piece, rows of one head group
+  bool queries;
+  int cx;          // 16-byte columns a CTA covers (a power of two)
+};
+
+// One CTA: piece blockIdx.x, columns [blockIdx.y * cx, + cx) of the Hkv * D
+// sums.  256 / cx strands share the piece's (row, head) pairs; their pairs
+// meet in shared memory in strand order.
+template <class T>
+__global__ void __launch_bounds__(kThr) piece_sums_kernel(const SumParams p) {
+  constexpr int V = Vec16<T>::V;
+  __shared__ double sh[kThr * V];
+  const BlockGeom& g = p.g;
+  const int32_t* beg = p.queries ? g.seq_q : g.seq_k;
+  const int piece = blockIdx.x;
+  const int s = piece_seq(beg, g.S, p.per, piece);
+  const Span sp = p.queries ? span_q(g, s) : span_k(g, s);
+  const int64_t pos = int64_t(piece - piece_base(beg, s, p.per)) * p.per;
+  const int n = pos >= 0 && pos < sp.len ? (int)min(int64_t(p.per), sp.len - pos) : 0;
+  if (p.since && (n == 0 || pos + p.per <= p.since[s])) return;
+  const int cx = p.cx, tx = threadIdx.x & (cx - 1), ty = threadIdx.x / cx, ny = kThr / cx;
+  const int col = (blockIdx.y * cx + tx) * V;  // of Hkv * D
+  const int W = g.Hkv * g.D;
+  float a[V], e[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) a[i] = e[i] = 0.f;
+  if (col < W) {
+    const int kh = col / g.D, d = col - kh * g.D;
+    const T* x = static_cast<const T*>(p.x) + (sp.beg + pos) * int64_t(W) * p.heads +
+                 int64_t(kh) * p.heads * g.D + d;
+    const int total = n * p.heads;
+#pragma unroll 4
+    for (int i = ty; i < total; i += ny) {
+      const int r = i / p.heads, h = i - r * p.heads;
+      float f[V];
+      Vec16<T>::load(x + int64_t(r) * W * p.heads + h * g.D, f);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {  // a + f = t exactly, up to what e keeps
+        const float t = a[k] + f[k];
+        const float b = t - a[k];
+        e[k] += (a[k] - (t - b)) + (f[k] - b);
+        a[k] = t;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    sh[ty * cx * V + tx * V + i] =
+        fabsf(a[i]) <= 3.4e38f ? double(a[i]) + double(e[i]) : double(a[i]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < cx * V; c += kThr) {
+    double t = 0.0;
+    for (int y = 0; y < ny; ++y) t += sh[y * cx * V + c];
+    const int o = blockIdx.y * cx * V + c;
+    if (o < W) p.sums[int64_t(piece) * W + o] = t;
+  }
+}
+
+// --------------------------------------------------------------------------
+// scores and the topk best
+// --------------------------------------------------------------------------
+struct SelParams {
+  BlockGeom g;
+  const void* Q;         // used when units are single rows
+  const double* qsum;    // [U][Hkv][D] else
+  const double* sums;    // [B][Hkv][D]
+  int32_t* idx;
+  int cap;               // blocks of a sequence that are looked at
+};
+
+// fp64 to fp32, rounded towards zero, with integer instructions (the
+// conversion instruction runs at the fp64 rate).
+__device__ __forceinline__ float trunc32(double x) {
+  const uint32_t hi = __double2hiint(x), lo = __double2loint(x);
+  const uint32_t ex = (hi >> 20) & 0x7ff;
+  uint32_t m = (__funnelshift_l(lo, hi, 3) - (896u << 23)) & 0x7fffffffu;
+  m = ex <= 896 ? 0u : ex >= 1151 ? 0x7f800000u : m;
+  if (ex == 0x7ff && ((hi & 0xfffff) | lo)) m = 0x7fc00000u;
+  return __uint_as_float(m | (hi & 0x80000000u));
+}
+
+__device__ __forceinline__ uint32_t order_key(float x) {  // larger score, larger key; NaN lowest
+  if (!(x > neg_inf())) return 0u;
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are one score
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return k == 0u ? neg_inf() : __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The k-th largest of n keys (k <= number of nonzero keys), by one warp; hist: 256 words.
+__device__ uint32_t kth_key(const double* sc, int n, int k, uint32_t* hist) {
+  const int lane = threadIdx.x & 31;
+  uint32_t prefix = 0, mask = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hist[lane * 8 + i] = 0;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) {
+      const uint32_t key = order_key(reinterpret_cast<const float*>(sc + i)[0]);
+      if ((key & mask) == prefix) atomicAdd(hist + ((key >> shift) & 255), 1u);
+    }
+    __syncwarp();
+    uint32_t mine = 0;  // lane l: bins [8 l, 8 l + 8)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += hist[lane * 8 + i];
+    uint32_t above = mine;  // suffix sum over lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_down_sync(0xffffffffu, above, o);
+      if (lane + o < 32) above += t;
+    }
+    const unsigned reach = __ballot_sync(0xffffffffu, above >= uint32_t(k));
+    const int who = 31 - __clz(reach);  // highest lane whose suffix holds k keys
+    uint32_t bin = 0, left = 0;
+    if (lane == who) {
+      uint32_t c = above - mine;
+      int b = 7;
+      for (; b > 0 && c + hist[lane * 8 + b] < uint32_t(k); --b) c += hist[lane * 8 + b];
+      bin = lane * 8 + b;
+      left = k - c;
+    }
+    bin = __shfl_sync(0xffffffffu, bin, who);
+    k = __shfl_sync(0xffffffffu, left, who);
+    prefix |= bin << shift;
+    mask |= 255u << shift;
+    __syncwarp();
+  }
+  return prefix;
+}
+
+// UT consecutive units of one key head per CTA.  A score entry is 8 bytes:
+// the fp32 score, or the fp64 score of a block near the last place.
+template <class T, int UT>
+__global__ void __launch_bounds__(kThr) select_kernel(const SelParams p) {
+  extern __shared__ __align__(16) double sm[];
+  const BlockGeom& g = p.g;
+  const int D = g.D, kh = blockIdx.y;
+  double* q64 = sm;                                        // [UT][D]
+  float* q32 = reinterpret_cast<float*>(q64 + UT * D);     // [UT][D]
+  uint32_t* hist = reinterpret_cast<uint32_t*>(q32 + UT * D);  // [UT][256]
+  double* sc = reinterpret_cast<double*>(hist + UT * 256);     // [UT][cap]
+  __shared__ float wmax[kThr / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u0 = blockIdx.x * UT, u1 = min(u0 + UT, g.U);
+
+  for (int ub = u0; ub < u1;) {
+    // the units from ub on that belong to ub's sequence
+    const Unit un = unit_at(g, ub);
+    const int end = un.s + 1 < g.S ? piece_base(g.seq_q, un.s + 1, g.qb) : g.U;
+    const int cnt = max(1, min(u1, end) - ub);
+    const Span qs = span_q(g, un.s), ks = span_k(g, un.s);
+    const int b0 = piece_base(g.seq_k, un.s, g.block);
+    const int nb = max(0, min(min((ks.len + g.block - 1) / g.block, p.cap), g.B - b0));
+    const int first_unit = piece_base(g.seq_q, un.s, g.qb);
+    __syncthreads();
+    for (int i = threadIdx.x; i < UT * D; i += kThr) {
+      const int j = i / D, d = i - j * D, u = ub + j;
+      double v = 0.0;
+      const int64_t off = int64_t(u - first_unit) * g.qb;
+      if (j < cnt && off >= 0 && off < qs.len) {
+        if (p.qsum) {
+          v = p.qsum[(int64_t(u) * g.Hkv + kh) * D + d];
+        } else {
+          const T* q = static_cast<const T*>(p.Q) + ((qs.beg + off) * g.H + kh * g.G) * D + d;
+          for (int h = 0; h < g.G; ++h) v += double(float(q[h * D]));
+        }
+      }
+      q64[i] = v;
+      q32[i] = trunc32(v);
+    }
+    __syncthreads();
+
+    // scores: 8 lanes per block, each D / 8 of its columns (pairs)
+    float big = 0.f;  // largest |k|^2 / n^2
+    const int sub = threadIdx.x & 7;
+    for (int b = threadIdx.x >> 3; b < ((nb + 31) & ~31); b += kThr / 8) {
+      float acc[UT];
+#pragma unroll
+      for (int j = 0; j < UT; ++j) acc[j] = 0.f;
+      float nn = 0.f;
+      const bool in = b < nb;
+      const double* k = p.sums + (int64_t(b0 + (in ? b : 0)) * g.Hkv + kh) * D;
+      if (in) {
+        if (D >= 16) {
+#pragma unroll 4
+          for (int d = sub * 2; d < D; d += 16) {
+            const double2 kk = *reinterpret_cast<const double2*>(k + d);
+            const float x = trunc32(kk.x), y = trunc32(kk.y);
+            nn = fmaf(x, x, fmaf(y, y, nn));
+#pragma unroll
+            for (int j = 0; j < UT; ++j) {
+              const float2 q = *reinterpret_cast<const float2*>(q32 + j * D + d);
+              acc[j] = fmaf(x, q.x, fmaf(y, q.y, acc[j]));
+            }
+          }
+        } else if (sub < D) {
+          const float x = trunc32(k[sub]);
+          nn = x * x;
+#pragma unroll
+          for (int j = 0; j < UT; ++j) acc[j] = x * q32[j * D + sub];
+        }
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        nn += __shfl_xor_sync(0xffffffffu, nn, o);
+#pragma unroll
+        for (int j = 0; j < UT; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      }
+      if (in) {
+        const int kp = b * g.block;
+        const float inv = 1.f / float(min(g.block, ks.len - kp));
+        big = fmaxf(big, nn * inv * inv);
+        if (nn != nn) big = __int_as_float(0x7f800000);
+        if (sub == 0) {
+#pragma unroll
+          for (int j = 0; j < UT; ++j) {
+            const int64_t off = int64_t(ub + j - first_unit) * g.qb;
+            float v = acc[j] * inv;
+            if (g.causal) {
+              const int64_t lo = off + ks.len - qs.len;
+              const int64_t hi = min(off + g.qb, int64_t(qs.len)) + ks.len - qs.len - 1;
+              if (kp + g.block > lo) v = -neg_inf();
+              if (kp > hi) v = neg_inf();
+            }
+            if (j >= cnt || off < 0 || off >= qs.len) v = neg_inf();
+            reinterpret_cast<float*>(sc + j * p.cap + b)[0] = v;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    if (lane == 0) wmax[warp] = big;
+    __syncthreads();
+
+    // one warp per unit
+    for (int j = warp; j < cnt; j += kThr / 32) {
+      double* s = sc + j * p.cap;
+      int valid = 0;
+      for (int i = lane; i < nb; i += 32)
+        valid += order_key(reinterpret_cast<const float*>(s + i)[0]) != 0u;
+      valid = __reduce_add_sync(0xffffffffu, valid);
+      const int k = min(g.topk, valid);
+      int32_t* out = p.idx + (int64_t(ub + j) * g.Hkv + kh) * g.topk;
+      float lo = neg_inf(), hi = neg_inf();  // below lo: out; above hi: in; between: by fp64
+      if (valid > k) {
+        const float kth = key_score(kth_key(s, nb, k, hist + j * 256));
+        float qn = 0.f, kn = 0.f;
+        for (int d = lane; d < D; d += 32) qn = fmaf(q32[j * D + d], q32[j * D + d], qn);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, o);
+#pragma unroll
+        for (int w = 0; w < kThr / 32; ++w) kn = fmaxf(kn, wmax[w]);
+        const float e = float(D + 32) * 0x1p-23f * sqrtf(qn) * sqrtf(kn) * 1.0001f;
+        lo = kth - 2.f * e;
+        hi = kth + 2.f * e;
+        if (!(lo == lo) || !(hi == hi)) {  // a non-finite bound: every block by fp64
+          lo = neg_inf();
+          hi = -neg_inf();
+        }
+        if (kth == -neg_inf()) lo = hi = kth;
+        // count the sure ones; when those between are exactly what is missing, take them all
+        int sure = 0, mid = 0;
+        for (int i = lane; i < nb; i += 32) {
+          const float v = reinterpret_cast<const float*>(s + i)[0];
+          sure += v > hi;
+          mid += v >= lo && v <= hi && v > neg_inf();
+        }
+        sure = __reduce_add_sync(0xffffffffu, sure);
+        mid = __reduce_add_sync(0xffffffffu, mid);
+        int need = k - sure;
+        if (mid > need) {
+          // score those between in fp64: one block at a time, the lanes over D
+          for (int i0 = 0; i0 < nb; i0 += 32) {
+            const int i = i0 + lane;
+            const float v = i < nb ? reinterpret_cast<const float*>(s + i)[0] : neg_inf();
+            unsigned todo = __ballot_sync(0xffffffffu, v >= lo && v <= hi && v > neg_inf());
+            double mine = v > hi ? 2.0 : 0.0;  // tag: 2 sure, 0 out
+            bool scored = false;
+            while (todo) {
+              const int l = __ffs(todo) - 1;
+              todo &= todo - 1;
+              const int b = i0 + l;
+              const double* kk = p.sums + (int64_t(b0 + b) * g.Hkv + kh) * D;
+              double t = 0.0;
+              for (int d = lane; d < D; d += 32) t = fma(q64[j * D + d], kk[d], t);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+              t /= double(min(g.block, ks.len - b * g.block));
+              if (lane == l) {
+                mine = v == -neg_inf() ? 1.0 / 0.0 : t;
+                scored = true;
+              }
+            }
+            // keep the fp64 score of a scored block; others as quiet tags
+            if (i < nb) {
+              s[i] = scored ? mine : __longlong_as_double(mine != 0.0 ? 0x7ff8000000000002LL
+                                                                      : 0x7ff8000000000001LL);
+            }
+          }
+          __syncwarp();
+          // the `need` best by (score, lower id): take the maximum `need` times
+          for (; need > 0; --need) {
+            double best = -1.0 / 0.0;
+            int at = INT32_MAX;
+            for (int i = lane; i < nb; i += 32) {
+              const double v = s[i];
+              if (v == v && (at == INT32_MAX || v > best)) {
+                best = v;
+                at = i;
+              }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+              const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+              if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) {
+                best = ob;
+                at = oa;
+              }
+            }
+            if (at == INT32_MAX) break;  // scores that are NaN in 64 bits are never chosen
+            __syncwarp();
+            if (lane == 0) s[at] = __longlong_as_double(0x7ff8000000000002LL);
+            __syncwarp();
+          }
+          int n = 0;
+          for (int i0 = 0; i0 < nb; i0 += 32) {
+            const int i = i0 + lane;
+            const bool in = i < nb && __double_as_longlong(s[i]) == 0x7ff8000000000002LL;
+            const unsigned m = __ballot_sync(0xffffffffu, in);
+            if (in) out[n + __popc(m & ((1u << lane) - 1))] = i;
+            n += __popc(m);
+          }
+          for (int i = n + lane; i < g.topk; i += 32) out[i] = -1;
+          continue;
+        }
+      }
+      int n = 0;
+      for (int i0 = 0; i0 < nb; i0 += 32) {
+        const int i = i0 + lane;
+        const float v = i < nb ? reinterpret_cast<const float*>(s + i)[0] : neg_inf();
+        const bool in = v >= lo && v > neg_inf();
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (in) out[n + __popc(m & ((1u << lane) - 1))] = i;
+        n += __popc(m);
+      }
+      for (int i = n + lane; i < g.topk; i += 32) out[i] = -1;
+    }
+    ub += cnt;
+  }
+}
+
+gattn_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("%s launch failed: %s", what, cudaGetErrorString(e));
+    return GATTN_ERR_CUDA;
+  }
+  return GATTN_OK;
+}
+
+size_t select_smem(int UT, int D, int cap) {
+  return size_t(UT) * (D * 12 + 1024 + size_t(cap) * 8);
+}
+
+}  // namespace
+
+gattn_status launch_block_sums(const BlockGeom& g, gattn_dtype dt, const void* x, bool queries,
+                               const int32_t* since, double* sums, cudaStream_t st) {
+  SumParams p{};
+  p.g = g;
+  p.x = x;
+  p.since = since;
+  p.sums = sums;
+  p.queries = queries;
+  p.per = queries ? g.qb : g.block;
+  p.heads = queries ? g.G : 1;
+  const int V = dt == GATTN_F32 ? 4 : 8;
+  const int cols = g.Hkv * g.D / V;  // a power of two
+  p.cx = std::min(cols, 64);
+  const int pieces = queries ? g.U : g.B;
+  if (pieces <= 0) return GATTN_OK;
+  const dim3 grid(pieces, (cols + p.cx - 1) / p.cx);
+  if (dt == GATTN_F32) piece_sums_kernel<float><<<grid, kThr, 0, st>>>(p);
+  else piece_sums_kernel<__nv_bfloat16><<<grid, kThr, 0, st>>>(p);
+  return launched("gattn_block_sums");
+}
+
+gattn_status launch_block_select(const BlockGeom& g, gattn_dtype dt, const void* Q,
+                                 const double* qsum, const double* sums, int max_blocks,
+                                 int32_t* idx, cudaStream_t st) {
+  SelParams p{};
+  p.g = g;
+  p.Q = Q;
+  p.qsum = qsum;
+  p.sums = sums;
+  p.idx = idx;
+  p.cap = std::max(1, max_blocks);
+  // eight units share a pass over the sums where that leaves every SM work;
+  // single units otherwise (few units, or more blocks than fit eight times)
+  const int sms = sm_count();
+  const bool eight = int64_t(g.U) * g.Hkv >= int64_t(16) * sms &&
+                     select_smem(8, g.D, p.cap) <= size_t(200) * 1024;
+  const int UT = eight ? 8 : 1;
+  const size_t bytes = select_smem(UT, g.D, p.cap);
+  if (bytes > size_t(220) * 1024) {
+    set_error("gattn_block_select: %d blocks in a sequence are too many (at most %d)", p.cap,
+              int((220 * 1024 - g.D * 12 - 1024) / 8));
+    return GATTN_ERR_UNSUPPORTED;
+  }
+  const dim3 grid((g.U + UT - 1) / UT, g.Hkv);
+  auto go = [&](auto kern) -> gattn_status {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) {
+      set_error("gattn_block_select: %s", cudaGetErrorString(e));
+      return GATTN_ERR_CUDA;
+    }
+    kern<<<grid, kThr, bytes, st>>>(p);
+    return launched("gattn_block_select");
+  };
+  if (dt == GATTN_F32) return eight ? go(select_kernel<float, 8>) : go(select_kernel<float, 1>);
+  return eight ? go(select_kernel<__nv_bfloat16, 8>) : go(select_kernel<__nv_bfloat16, 1>);
+}
+
+}  // namespace gattn

@@ -1,0 +1,644 @@
+// norm.cu -- the step between two blocks of a transformer layer, fused:
+//   u = norm(x; w_post, b_post)        (or u = x)
+//   h = res + alpha * gate * u
+//   y = norm(h; w_pre, b_pre)          (optional)
+// and its backward.  norm is x / rms(x) * w + b or (x - mean) / deviation * w + b.
+//
+// Both directions are bound by HBM: about 60 flops per element against 4 to
+// 11 tensor elements moved.  Each row is read once, kept in registers as fp32
+// through both norms, and written once; means, variances, h (before its one
+// rounding) and every column sum are fp32.  Variances are sums of squared
+// deviations from the mean (two passes over registers, not
+// over memory).  The backward forms h
+// again from res, x and gate, which costs no traffic over reading h and keeps
+// its rounding out of the normalised row (for rows whose mean is large against
+// their deviation that rounding would be as large as the row).
+//
+// A row belongs to W warps; a thread holds E of its elements as 16-byte
+// vectors (single elements when a row is no multiple of 16 bytes).  The
+// forward takes E = 32 so that one warp covers 1,024 elements and needs no
+// block barrier; the backward takes E = 8 because it also carries five fp32
+// column sums per element (dw, db of both norms and the channel gate) over
+// all rows of its CTA, and fetches its next row while it reduces the current
+// one.  The column sums of the CTAs meet in a second small kernel, in CTA
+// order, so results do not vary from run to run.
+#include <algorithm>
+
+#include "attn_launch.cuh"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kGateNone = GATTN_GATE_NONE, kGateChannel = GATTN_GATE_CHANNEL,
+              kGateToken = GATTN_GATE_TOKEN;
+constexpr int kMaxF = 16384;
+constexpr int kSums = 5;  // dw_post, db_post, dw_pre, db_pre, dgate (channel)
+
+struct NormParams {
+  int64_t N;
+  int F;
+  float alpha, eps, inv_f;
+  int gate_mode;
+  const void *res, *x, *gate, *dh, *dy;
+  const float *w_post, *b_post, *w_pre, *b_pre;
+  void *h, *y, *dres, *dx, *dgate;
+  float4* stats;       // [N] (mean, 1/dev) of x, then of h
+  const float4* cstats;
+  float* part;         // backward: [slots][kSums][F]
+  int want;            // bit s: column sum s is wanted
+};
+
+// V consecutive elements of a row (16 bytes, or one element) as fp32.
+template <class T, int V>
+struct Vec;
+template <>
+struct Vec<float, 4> {
+  using Raw = float4;
+  __device__ static Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ static void get(const Raw& r, float* f) { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
+  __device__ static Raw put(const float* f) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+  using Raw = uint4;
+  __device__ static Raw zero() { return make_uint4(0, 0, 0, 0); }
+  __device__ static void get(const Raw& r, float* f) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static Raw put(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Vec<float, 1> {
+  using Raw = float;
+  __device__ static Raw zero() { return 0.f; }
+  __device__ static void get(const Raw& r, float* f) { f[0] = r; }
+  __device__ static Raw put(const float* f) { return f[0]; }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  using Raw = __nv_bfloat16;
+  __device__ static Raw zero() { return __float2bfloat16(0.f); }
+  __device__ static void get(const Raw& r, float* f) { f[0] = __bfloat162float(r); }
+  __device__ static Raw put(const float* f) { return __float2bfloat16(f[0]); }
+};
+
+// Sums of K values over the W warps of a row.  Warps of one row are a whole
+// CTA when W > 1; `turn` alternates the slots so that one barrier per sum is
+// enough (a slot is written again only after the next sum's barrier).
+template <int W, int K>
+__device__ __forceinline__ void row_sums(float* v, float* red, int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if constexpr (W > 1) {
+    float* slot = red + turn * W * 2;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) slot[warp * 2 + k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += slot[w * 2 + k];
+      v[k] = s;
+    }
+    turn ^= 1;
+  }
+}
+
+template <class T, int V, int E, int W>
+struct Row {
+  static constexpr int NV = E / V;
+  using R = typename Vec<T, V>::Raw;
+  // column of this thread's vector n, and whether the row has it
+  __device__ static int col(int n, int t) { return (n * W * 32 + t) * V; }
+  __device__ static void load(R* r, const void* base, int64_t row, int F, int t) {
+    const T* p = static_cast<const T*>(base) + row * F;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = col(n, t);
+      r[n] = c < F ? *reinterpret_cast<const R*>(p + c) : Vec<T, V>::zero();
+    }
+  }
+  __device__ static void store(void* base, int64_t row, int F, int t, const float* f) {
+    T* p = static_cast<T*>(base) + row * F;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = col(n, t);
+      if (c < F) *reinterpret_cast<R*>(p + c) = Vec<T, V>::put(f + n * V);
+    }
+  }
+  // fp32 channel vector (rows of V elements at column c); `none` where absent
+  __device__ static void channel(const float* w, int n, int F, int t, float none, float* f) {
+    const int c = col(n, t);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = none;
+    if (w && c < F) {
+      if constexpr (V == 1) {
+        f[0] = w[c];
+      } else {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+          const float4 a = reinterpret_cast<const float4*>(w + c)[q];
+          f[4 * q] = a.x; f[4 * q + 1] = a.y; f[4 * q + 2] = a.z; f[4 * q + 3] = a.w;
+        }
+      }
+    }
+  }
+};
+
+// mean and 1 / deviation (root mean square when LN is false) of a row
+template <class T, int V, int E, int W, bool LN>
+__device__ __forceinline__ float2 row_stats(const float* f, const NormParams& p, int t, float* red,
+                                            int& turn) {
+  using RW = Row<T, V, E, W>;
+  float mean = 0.f;
+  if constexpr (LN) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[0] += f[e];
+    row_sums<W, 1>(s, red, turn);
+    mean = s[0] * p.inv_f;
+  }
+  float q[1] = {0.f};
+#pragma unroll
+  for (int n = 0; n < RW::NV; ++n)
+    if (RW::col(n, t) < p.F)  // absent columns hold 0, which is no deviation of 0 under a mean
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = f[n * V + e] - mean;
+        q[0] = fmaf(d, d, q[0]);
+      }
+  row_sums<W, 1>(q, red, turn);
+  return make_float2(mean, rsqrtf(q[0] * p.inv_f + p.eps));
+}
+
+template <class T, int V, int E, int W, bool LN>
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_fwd_kernel(const NormParams p) {
+  using RW = Row<T, V, E, W>;
+  __shared__ float red[W > 1 ? 4 * W : 1];
+  int turn = 0;
+  const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t row = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= p.N) return;
+  float h[E];
+  {
+    typename RW::R r[RW::NV], xr[RW::NV], gr[RW::NV];
+    RW::load(r, p.res, row, p.F, t);
+    if (p.x) RW::load(xr, p.x, row, p.F, t);
+    if (p.x && p.gate_mode == kGateToken) RW::load(gr, p.gate, row, p.F, t);
+#pragma unroll
+    for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(r[n], h + n * V);
+    if (p.x) {
+      float u[E];
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(xr[n], u + n * V);
+      if (p.w_post) {
+        const float2 s = row_stats<T, V, E, W, LN>(u, p, t, red, turn);
+        if (t == 0) reinterpret_cast<float2*>(p.stats + row)[0] = s;
+#pragma unroll
+        for (int n = 0; n < RW::NV; ++n) {
+          float w[V], b[V];
+          RW::channel(p.w_post, n, p.F, t, 0.f, w);
+          RW::channel(p.b_post, n, p.F, t, 0.f, b);
+#pragma unroll
+          for (int e = 0; e < V; ++e) u[n * V + e] = fmaf((u[n * V + e] - s.x) * s.y, w[e], b[e]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n) {
+        float g[V];
+        if (p.gate_mode == kGateToken) {
+          Vec<T, V>::get(gr[n], g);
+        } else {
+          RW::channel(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr, n,
+                      p.F, t, 1.f, g);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          h[n * V + e] = fmaf(p.alpha * g[e], u[n * V + e], h[n * V + e]);
+      }
+      RW::store(p.h, row, p.F, t, h);
+    }
+  }
+  if (p.w_pre) {  // on h as it stands in fp32, not as rounded for the store
+    const float2 s = row_stats<T, V, E, W, LN>(h, p, t, red, turn);
+    if (t == 0) reinterpret_cast<float2*>(p.stats + row)[1] = s;
+#pragma unroll
+    for (int n = 0; n < RW::NV; ++n) {
+      float w[V], b[V];
+      RW::channel(p.w_pre, n, p.F, t, 0.f, w);
+      RW::channel(p.b_pre, n, p.F, t, 0.f, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) h[n * V + e] = fmaf((h[n * V + e] - s.x) * s.y, w[e], b[e]);
+    }
+    RW::store(p.y, row, p.F, t, h);
+  }
+}
+
+// dx of a norm: g = dy * w, xh the normalised row, r = 1 / deviation
+//   dx = r (g - xh mean(g xh) - [LN] mean(g));  absent columns hold g = xh = 0
+template <int E, int W, bool LN>
+__device__ __forceinline__ void norm_dx(float* g, const float* xh, float r, float inv_f, float* red,
+                                        int& turn) {
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    s[0] = fmaf(g[e], xh[e], s[0]);
+    if (LN) s[1] += g[e];
+  }
+  row_sums<W, LN ? 2 : 1>(s, red, turn);
+  const float c1 = s[0] * inv_f, c2 = LN ? s[1] * inv_f : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) g[e] = r * (g[e] - fmaf(xh[e], c1, c2));
+}
+
+template <class T, int V, int E, int W, bool LN>
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_bwd_kernel(const NormParams p) {
+  using RW = Row<T, V, E, W>;
+  constexpr int NV = RW::NV;
+  using R = typename RW::R;
+  __shared__ float red[W > 1 ? 4 * W : 1];
+  int turn = 0;
+  const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t slot = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = W == 1 ? int64_t(gridDim.x) * 4 : gridDim.x;
+  const bool has_x = p.x != nullptr, token = p.gate_mode == kGateToken;
+  float acc[kSums][E];
+#pragma unroll
+  for (int k = 0; k < kSums; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+
+  R rr[NV], dhr[NV], dyr[NV], xr[NV], gr[NV];
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fetch = [&](int64_t row) {
+    st = p.cstats[row];
+    if (p.w_pre) {
+      RW::load(rr, p.res, row, p.F, t);
+      RW::load(dyr, p.dy, row, p.F, t);
+    }
+    if (p.dh) RW::load(dhr, p.dh, row, p.F, t);
+    if (has_x) {
+      RW::load(xr, p.x, row, p.F, t);
+      if (token) RW::load(gr, p.gate, row, p.F, t);
+    }
+  };
+  if (slot < p.N) fetch(slot);
+  for (int64_t row = slot; row < p.N; row += step) {
+    // unpack this row (x becomes its normalised row, hh that of h, formed
+    // again as the forward did), then start on the next one's loads
+    float d[E], x[E], g[E], gy[E], hh[E];
+    const float4 s = st;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const bool on = RW::col(n, t) < p.F;
+      float u[V], dy[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) u[e] = 0.f;
+      if (has_x) {
+        Vec<T, V>::get(xr[n], x + n * V);
+        if (token)
+          Vec<T, V>::get(gr[n], g + n * V);
+        else
+          RW::channel(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr, n,
+                      p.F, t, 1.f, g + n * V);
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] = x[n * V + e];
+        if (p.w_post) {
+          float w[V], b[V];
+          RW::channel(p.w_post, n, p.F, t, 0.f, w);
+          RW::channel(p.b_post, n, p.F, t, 0.f, b);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            x[n * V + e] = on ? (x[n * V + e] - s.x) * s.y : 0.f;
+            u[e] = fmaf(x[n * V + e], w[e], b[e]);
+          }
+        }
+      }
+      if (p.w_pre) {
+        float h[V], w[V];
+        Vec<T, V>::get(rr[n], h);
+        Vec<T, V>::get(dyr[n], dy);
+        RW::channel(p.w_pre, n, p.F, t, 0.f, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int i = n * V + e;
+          if (has_x) h[e] = fmaf(p.alpha * g[i], u[e], h[e]);
+          hh[i] = on ? (h[e] - s.z) * s.w : 0.f;
+          gy[i] = dy[e] * w[e];
+          acc[2][i] = fmaf(dy[e], hh[i], acc[2][i]);
+          acc[3][i] += dy[e];
+        }
+      }
+      if (p.dh) {
+        Vec<T, V>::get(dhr[n], d + n * V);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[n * V + e] = 0.f;
+      }
+    }
+    if (row + step < p.N) fetch(row + step);
+    if (p.w_pre) {
+      norm_dx<E, W, LN>(gy, hh, s.w, p.inv_f, red, turn);
+#pragma unroll
+      for (int e = 0; e < E; ++e) d[e] += gy[e];
+    }
+    if (p.dres) RW::store(p.dres, row, p.F, t, d);
+    if (!has_x) continue;
+    // d = gradient of h; du = alpha gate d, u = norm(x)
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      float w[V], b[V];
+      RW::channel(p.w_post, n, p.F, t, 0.f, w);
+      RW::channel(p.b_post, n, p.F, t, 0.f, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int i = n * V + e;
+        const float ad = p.alpha * d[i];
+        const float u = p.w_post ? fmaf(x[i], w[e], b[e]) : x[i];
+        const float du = ad * g[i];
+        g[i] = ad * u;  // the gate's gradient
+        acc[4][i] += g[i];
+        acc[0][i] = fmaf(du, x[i], acc[0][i]);
+        acc[1][i] += du;
+        d[i] = p.w_post ? du * w[e] : du;
+      }
+    }
+    if (token && p.dgate) RW::store(p.dgate, row, p.F, t, g);
+    if (p.w_post) norm_dx<E, W, LN>(d, x, s.y, p.inv_f, red, turn);
+    if (p.dx) RW::store(p.dx, row, p.F, t, d);
+  }
+#pragma unroll
+  for (int k = 0; k < kSums; ++k)
+    if ((p.want >> k) & 1) {
+      float* o = p.part + (slot * kSums + k) * p.F;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int c = RW::col(n, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c < p.F) o[c + e] = acc[k][n * V + e];
+      }
+    }
+}
+
+// Column sums over the slots, in slot order within each of 8 fixed strands.
+struct NormOut {
+  float* o[kSums];
+};
+__global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int slots, int F,
+                                                        NormOut out) {
+  __shared__ float sh[8][33];
+  const int k = blockIdx.y, lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
+  if (!out.o[k]) return;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < F) {
+#pragma unroll 4
+    for (int i = strand; i < slots; i += 8) s += part[(int64_t(i) * kSums + k) * F + c];
+  }
+  sh[strand][lane] = s;
+  __syncthreads();
+  if (strand == 0 && c < F) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sh[i][lane];
+    out.o[k][c] = s;
+  }
+}
+
+// --------------------------------------------------------------------------
+// host side
+// --------------------------------------------------------------------------
+bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+gattn_status fail(gattn_status s, const char* msg) {
+  set_error("gattn_norm: %s", msg);
+  return s;
+}
+
+gattn_status check_desc(const gattn_norm_desc* d) {
+  if (!d) return fail(GATTN_ERR_INVALID_ARG, "desc is NULL");
+  if (d->dtype != GATTN_F32 && d->dtype != GATTN_BF16)
+    return fail(GATTN_ERR_INVALID_ARG, "unknown dtype");
+  if (d->kind != GATTN_NORM_RMS && d->kind != GATTN_NORM_LAYER)
+    return fail(GATTN_ERR_INVALID_ARG, "unknown kind");
+  if (d->gate != kGateNone && d->gate != kGateChannel && d->gate != kGateToken)
+    return fail(GATTN_ERR_INVALID_ARG, "unknown gate mode");
+  if (d->N < 0 || d->F <= 0 || d->N > INT32_MAX)
+    return fail(GATTN_ERR_INVALID_ARG, "need 0 <= N < 2^31 and F > 0");
+  if (d->F > kMaxF) return fail(GATTN_ERR_UNSUPPORTED, "F must be at most 16384");
+  if ((d->b_post && !d->w_post) || (d->b_pre && !d->w_pre))
+    return fail(GATTN_ERR_INVALID_ARG, "a bias needs its weight");
+  if (!al(d->w_post, 16) || !al(d->b_post, 16) || !al(d->w_pre, 16) || !al(d->b_pre, 16))
+    return fail(GATTN_ERR_INVALID_ARG, "weights and biases must be 16-byte aligned");
+  return GATTN_OK;
+}
+
+NormParams params(const gattn_norm_desc* d) {
+  NormParams p{};
+  p.N = d->N;
+  p.F = d->F;
+  p.alpha = d->alpha;
+  p.eps = d->eps;
+  p.inv_f = 1.f / float(d->F);
+  p.gate_mode = d->gate;
+  p.w_post = d->w_post;
+  p.b_post = d->b_post;
+  p.w_pre = d->w_pre;
+  p.b_pre = d->b_pre;
+  return p;
+}
+
+// Whole 16-byte vectors fit when the row size is a multiple of 16 bytes.
+bool vectors(const gattn_norm_desc* d) {
+  return (int64_t(d->F) * (d->dtype == GATTN_F32 ? 4 : 2)) % 16 == 0;
+}
+
+gattn_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("%s launch failed: %s", what, cudaGetErrorString(e));
+    return GATTN_ERR_CUDA;
+  }
+  return GATTN_OK;
+}
+
+template <class T, int V, bool LN>
+void fwd_launch(const NormParams& p, cudaStream_t st) {
+  const unsigned rows = unsigned(p.N), quads = unsigned((p.N + 3) / 4);
+  if (p.F <= 256) norm_fwd_kernel<T, V, 8, 1, LN><<<quads, 128, 0, st>>>(p);
+  else if (p.F <= 1024) norm_fwd_kernel<T, V, 32, 1, LN><<<quads, 128, 0, st>>>(p);
+  else if (p.F <= 4096) norm_fwd_kernel<T, V, 32, 4, LN><<<rows, 128, 0, st>>>(p);
+  else norm_fwd_kernel<T, V, 32, 16, LN><<<rows, 512, 0, st>>>(p);
+}
+
+template <class T, int V>
+void fwd_kind(const NormParams& p, bool ln, cudaStream_t st) {
+  if (ln) fwd_launch<T, V, true>(p, st);
+  else fwd_launch<T, V, false>(p, st);
+}
+
+// Shape of the backward: warps per row and rows in flight.
+struct BwdShape {
+  int warps, slots;  // slots: partial column sums (one per row in flight)
+  unsigned grid;
+};
+BwdShape bwd_shape(const gattn_norm_desc* d) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  else
+    cudaGetLastError();
+  BwdShape s{};
+  s.warps = d->F <= 256 ? 1 : d->F <= 1024 ? 4 : d->F <= 4096 ? 16 : 32;
+  // as many CTAs as are resident at once: 4 of 128 threads, 1 of 512 or 1024
+  const int64_t per_sm = s.warps <= 4 ? 4 : 1;
+  const int64_t rows = s.warps == 1 ? (d->N + 3) / 4 : d->N;
+  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, per_sm * sms)));
+  s.slots = int(s.grid) * (s.warps == 1 ? 4 : 1);
+  return s;
+}
+
+template <class T, int V, bool LN>
+void bwd_launch(const NormParams& p, const BwdShape& s, cudaStream_t st) {
+  if (s.warps == 1) norm_bwd_kernel<T, V, 8, 1, LN><<<s.grid, 128, 0, st>>>(p);
+  else if (s.warps == 4) norm_bwd_kernel<T, V, 8, 4, LN><<<s.grid, 128, 0, st>>>(p);
+  else if (s.warps == 16) norm_bwd_kernel<T, V, 8, 16, LN><<<s.grid, 512, 0, st>>>(p);
+  else if (p.F <= 8192) norm_bwd_kernel<T, V, 8, 32, LN><<<s.grid, 1024, 0, st>>>(p);
+  else norm_bwd_kernel<T, V, 16, 32, LN><<<s.grid, 1024, 0, st>>>(p);
+}
+
+template <class T, int V>
+void bwd_kind(const NormParams& p, const BwdShape& s, bool ln, cudaStream_t st) {
+  if (ln) bwd_launch<T, V, true>(p, s, st);
+  else bwd_launch<T, V, false>(p, s, st);
+}
+
+}  // namespace
+
+}  // namespace gattn
+
+using namespace gattn;
+
+extern "C" {
+
+gattn_status gattn_norm_fwd(const gattn_norm_desc* d, const void* res, const void* x,
+                            const void* gate, void* h, void* y, float* stats,
+                            gattn_stream_t stream) {
+  gattn_status s = check_desc(d);
+  if (s != GATTN_OK) return s;
+  if (d->N == 0) return GATTN_OK;
+  if (!x && (d->w_post || d->gate != kGateNone || gate))
+    return fail(GATTN_ERR_INVALID_ARG, "w_post and gate need x");
+  if (!x && !d->w_pre) return fail(GATTN_ERR_INVALID_ARG, "nothing to compute: give x or w_pre");
+  if (!res || !al(res, 16) || !al(x, 16) || (x && (!h || !al(h, 16))) ||
+      (d->w_pre && (!y || !al(y, 16))) || !stats || !al(stats, 16) ||
+      (d->gate != kGateNone && (!gate || !al(gate, 16))))
+    return fail(GATTN_ERR_INVALID_ARG,
+                "res, x, gate, h, y and stats must be 16-byte aligned device pointers");
+  NormParams p = params(d);
+  p.res = res;
+  p.x = x;
+  p.gate = gate;
+  p.h = h;
+  p.y = y;
+  p.stats = reinterpret_cast<float4*>(stats);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool ln = d->kind == GATTN_NORM_LAYER;
+  if (d->dtype == GATTN_F32) {
+    if (vectors(d)) fwd_kind<float, 4>(p, ln, st);
+    else fwd_kind<float, 1>(p, ln, st);
+  } else {
+    if (vectors(d)) fwd_kind<__nv_bfloat16, 8>(p, ln, st);
+    else fwd_kind<__nv_bfloat16, 1>(p, ln, st);
+  }
+  return launched("gattn_norm_fwd");
+}
+
+gattn_status gattn_norm_workspace_size(const gattn_norm_desc* d, size_t* bytes) {
+  const gattn_status s = check_desc(d);
+  if (s != GATTN_OK) return s;
+  if (!bytes) return fail(GATTN_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = size_t(bwd_shape(d).slots) * kSums * d->F * sizeof(float);
+  return GATTN_OK;
+}
+
+gattn_status gattn_norm_bwd(const gattn_norm_desc* d, const void* res, const float* stats,
+                            const void* dh, const void* dy, const void* x, const void* gate,
+                            void* dres, void* dx, void* dgate, float* dw_post, float* db_post,
+                            float* dw_pre, float* db_pre, void* workspace, size_t workspace_bytes,
+                            gattn_stream_t stream) {
+  gattn_status s = check_desc(d);
+  if (s != GATTN_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  float* chan = d->gate == kGateChannel ? static_cast<float*>(dgate) : nullptr;
+  const NormOut out{{dw_post, db_post, dw_pre, db_pre, chan}};
+  if (d->N == 0) {  // sums over no rows
+    for (float* o : out.o)
+      if (o && cudaMemsetAsync(o, 0, size_t(d->F) * 4, st) != cudaSuccess)
+        return fail(GATTN_ERR_CUDA, "cudaMemsetAsync failed");
+    return GATTN_OK;
+  }
+  if (!x && (d->w_post || d->gate != kGateNone || gate || dx || dgate))
+    return fail(GATTN_ERR_INVALID_ARG, "w_post, gate, dx and dgate need x");
+  if ((!d->w_post && (dw_post || db_post)) || (!d->w_pre && (dw_pre || db_pre || dy)) ||
+      (d->gate == kGateNone && dgate))
+    return fail(GATTN_ERR_INVALID_ARG, "a gradient is asked for that has no operand");
+  if (d->w_pre && !dy) return fail(GATTN_ERR_INVALID_ARG, "dy is NULL");
+  if (!dh && !d->w_pre) return fail(GATTN_ERR_INVALID_ARG, "neither dh nor dy is given");
+  const BwdShape sh = bwd_shape(d);
+  const size_t need = size_t(sh.slots) * kSums * d->F * sizeof(float);
+  if ((d->w_pre && (!res || !al(res, 16))) || !stats || !al(stats, 16) || !al(dh, 16) || !al(dy, 16) ||
+      !al(x, 16) || (d->gate != kGateNone && (!gate || !al(gate, 16))) || !al(dres, 16) ||
+      !al(dx, 16) || !al(dgate, 16) || !al(dw_post, 4) || !al(db_post, 4) || !al(dw_pre, 4) ||
+      !al(db_pre, 4))
+    return fail(GATTN_ERR_INVALID_ARG, "tensors must be 16-byte aligned device pointers");
+  if (!workspace || !al(workspace, 16) || workspace_bytes < need) {
+    set_error("gattn_norm_bwd: workspace needs %zu bytes (16-byte aligned), got %zu", need,
+              workspace_bytes);
+    return GATTN_ERR_INVALID_ARG;
+  }
+  NormParams p = params(d);
+  p.res = res;
+  p.cstats = reinterpret_cast<const float4*>(stats);
+  p.dh = dh;
+  p.dy = dy;
+  p.x = x;
+  p.gate = gate;
+  p.dres = dres;
+  p.dx = dx;
+  p.dgate = dgate;
+  p.part = static_cast<float*>(workspace);
+  for (int k = 0; k < kSums; ++k) p.want |= out.o[k] ? 1 << k : 0;
+  const bool ln = d->kind == GATTN_NORM_LAYER;
+  if (d->dtype == GATTN_F32) {
+    if (vectors(d)) bwd_kind<float, 4>(p, sh, ln, st);
+    else bwd_kind<float, 1>(p, sh, ln, st);
+  } else {
+    if (vectors(d)) bwd_kind<__nv_bfloat16, 8>(p, sh, ln, st);
+    else bwd_kind<__nv_bfloat16, 1>(p, sh, ln, st);
+  }
+  if ((s = launched("gattn_norm_bwd")) != GATTN_OK || !p.want) return s;
+  norm_cols_kernel<<<dim3((d->F + 31) / 32, kSums), 256, 0, st>>>(p.part, sh.slots, d->F, out);
+  return launched("gattn_norm_bwd (column sums)");
+}
+
+}  // extern "C"

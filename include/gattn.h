@@ -432,6 +432,185 @@ GATTN_API gattn_status gattn_permute_rows(const void* src, void* dst, const int3
                                           int32_t N, int64_t row_bytes, int32_t inverse,
                                           gattn_stream_t stream);
 
+/*
+ * Attention over blocks of nodes that a cheap score selects ("Methodology",
+ * attention-based layers: fused softmax attention with only a log-sum-exp
+ * kept; here the pattern is not a given graph but chosen from the data, the
+ * global attention of a graph transformer or of a language model).
+ *
+ * Sequences.  Q holds S sequences (the graphs of a batch, the requests of a
+ * server) one after another: sequence s owns the rows [seq_q[s], seq_q[s+1])
+ * of Q, out, dout and dQ, and the rows [seq_k[s], seq_k[s] + len_k[s]) of K,
+ * V, dK and dV.  len_k NULL means seq_k[s+1] - seq_k[s]; a smaller length
+ * leaves room behind a sequence, as in a cache that grows.  Sequences may be
+ * empty.  The offsets and lengths are DEVICE arrays and are read by the
+ * kernels alone, so one captured graph serves changing lengths.  They must
+ * be non-decreasing and inside the tensors; offsets that are not give
+ * undefined results, but no call reads or writes outside its tensors.
+ *
+ * Units and blocks.  The queries of a sequence are cut into units of q_block
+ * rows and its keys into blocks of `block` rows (the last of each may be
+ * short).  Unit j of sequence s has the table row
+ *     seq_q[s] / q_block + s + j   (q_block > 1; for q_block = 1: seq_q[s] + j)
+ * and block j the row seq_k[s] / block + s + j of `sums`.  The tables have
+ *     units  = Nq / q_block + (q_block > 1 ? S : 0)   and
+ *     blocks = Nk / block + S
+ * rows; some rows may belong to nothing.  idx[units][Hkv][topk] lists for each
+ * unit and key head the chosen blocks of its own sequence (j, not the table
+ * row), in any order; an entry outside the sequence (-1 by convention) names
+ * nothing, and an id that occurs twice counts once.
+ *
+ * Heads.  Query head h uses key head h / (H / Hkv).
+ *
+ * Masking.  Query i of a sequence with lq queries and lk keys stands at
+ * position i + lk - lq; with `causal` it sees the keys at positions up to its
+ * own.  A query that sees no key gets out = 0, lse = -inf and no gradient.
+ * Values outside what a query sees, non-finite ones too, do not reach its
+ * outputs in the forward; the backward needs finite rows within a sequence
+ * (other rows do not matter).  Rows of no sequence are never written by the
+ * forward and backward.
+ *
+ * Supported: D a power of two with D * sizeof(dtype) >= 16 and D <= 128, H and
+ * Hkv powers of two with Hkv <= H <= 128 * Hkv, block 16, 32, 64 or 128,
+ * q_block a power of two up to 128, topk up to 128.
+ */
+typedef struct {
+  int32_t S;               /* sequences */
+  int32_t Nq, Nk;          /* rows of Q and of K, V */
+  int32_t H, Hkv, D;       /* query heads, key and value heads, head width */
+  int32_t dtype;           /* gattn_dtype of Q, K, V, out and the gradients */
+  int32_t block, q_block;  /* keys per block, queries per unit */
+  int32_t topk;            /* entries of idx per unit and key head */
+  int32_t causal;
+  float scale;             /* multiplier of q.k, > 0; 0 selects 1/sqrt(D) */
+  int32_t max_len_k;       /* select: no sequence has more keys (those beyond are not
+                              chosen); 0: Nk */
+  const int32_t* seq_q;    /* device [S + 1] */
+  const int32_t* seq_k;    /* device [S + 1] */
+  const int32_t* len_k;    /* device [S] or NULL */
+  int64_t idx_stride[2];   /* forward, backward: elements of idx between units and between key
+                              heads (a list itself is contiguous), as for lists kept head by
+                              head or shared by heads; {0, 0} selects {Hkv * topk, topk} */
+} gattn_block_desc;
+
+/*
+ * Sums of the keys of each block in 64 bits: sums[blocks][Hkv][D] (device
+ * double; bf16 keys add up to better than 2^-44 of the largest partial sum).
+ *   since : device int32 [S] or NULL.  NULL writes every row of `sums` (zeros in rows of
+ *           no block); otherwise only blocks that hold a position >= since[s] are
+ *           renewed, as after appending to a cache.
+ * Uses S, Nk, Hkv, D, dtype, block, seq_k and len_k of the descriptor.
+ */
+GATTN_API gattn_status gattn_block_sums(const gattn_block_desc* desc, const void* K,
+                                        const int32_t* since, double* sums,
+                                        gattn_stream_t stream);
+
+/*
+ * Choose blocks: score(unit, block) = (sum of the unit's queries over its rows and
+ * the heads of the group) . (sum of the block's keys) / (keys in the block);
+ * idx receives the topk blocks of highest score in ascending order of id,
+ * then -1 (rows of no unit are all -1).  Equal scores go to the lower id.
+ * With `causal`, blocks that start after the unit's last position are out and
+ * blocks that reach the unit's own positions come before all others.  The
+ * choice is that of scores in 64 bits: scores are computed in 32 bits with an
+ * error bound, and blocks within that bound of the last place are scored again
+ * in 64.  Non-finite scores rank as -inf (NaN) or by their sign.
+ */
+GATTN_API gattn_status gattn_block_select_workspace_size(const gattn_block_desc* desc,
+                                                         size_t* bytes);
+GATTN_API gattn_status gattn_block_select(const gattn_block_desc* desc, const void* Q,
+                                          const double* sums, int32_t* idx, void* workspace,
+                                          size_t workspace_bytes, gattn_stream_t stream);
+
+/*
+ * Softmax attention of every query over the keys of the blocks that idx names
+ * for its unit: out[Nq][H][D], lse fp32 [Nq][H] (natural log).  Units with few
+ * rows are split over their blocks and joined when there are fewer of them
+ * than the GPU has SMs.  `workspace` (16-byte aligned, no initialisation) may
+ * be NULL when the size is 0; calls that may overlap need their own.
+ */
+GATTN_API gattn_status gattn_block_fwd_workspace_size(const gattn_block_desc* desc, size_t* bytes);
+GATTN_API gattn_status gattn_block_fwd(const gattn_block_desc* desc, const void* Q, const void* K,
+                                       const void* V, const int32_t* idx, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes,
+                                       gattn_stream_t stream);
+
+/*
+ * Backward of gattn_block_fwd (idx is not differentiated): dQ[Nq][H][D],
+ * dK, dV[Nk][Hkv][D] (written, not accumulated; keys that no query sees get 0).
+ * The weights are recomputed from lse.  Sums over queries run in a fixed
+ * order, so results do not vary from run to run.
+ */
+GATTN_API gattn_status gattn_block_bwd_workspace_size(const gattn_block_desc* desc, size_t* bytes);
+GATTN_API gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const void* K,
+                                       const void* V, const int32_t* idx, const void* out,
+                                       const void* dout, const float* lse, void* dQ, void* dK,
+                                       void* dV, void* workspace, size_t workspace_bytes,
+                                       gattn_stream_t stream);
+
+/*
+ * Synchronise the current device and report whether a block-attention kernel
+ * on it gave up a bounded wait since the last check (GATTN_ERR_TIMEOUT; its
+ * outputs are undefined, the library stays usable).  Clears the record.
+ */
+GATTN_API gattn_status gattn_block_check_errors(void);
+
+/*
+ * The step between two blocks of a transformer layer, fused:
+ *   u = norm(x; w_post, b_post)   (u = x without w_post)
+ *   h = res + alpha * gate * u    (h = res without x)
+ *   y = norm(h; w_pre, b_pre)     (nothing without w_pre)
+ * norm(v; w, b) = v / sqrt(mean(v^2) + eps) * w + b             (GATTN_NORM_RMS)
+ *               = (v - mean(v)) / sqrt(var(v) + eps) * w + b    (GATTN_NORM_LAYER)
+ * over the F elements of a row; statistics, h before its one rounding and all
+ * sums are fp32.  res, x, y, h (and gate per token) are device [N, F] in
+ * `dtype`, weights and biases fp32 [F]; all 16-byte aligned.  1 <= F <= 16384,
+ * any F; rows that are a multiple of 16 bytes move as 16-byte vectors.
+ */
+typedef enum { GATTN_NORM_RMS = 0, GATTN_NORM_LAYER = 1 } gattn_norm_kind;
+typedef enum {
+  GATTN_GATE_NONE = 0,    /* gate = 1 */
+  GATTN_GATE_CHANNEL = 1, /* gate: fp32 [F] */
+  GATTN_GATE_TOKEN = 2    /* gate: [N, F] in `dtype` */
+} gattn_gate_mode;
+
+typedef struct {
+  int64_t N;
+  int32_t F;
+  int32_t dtype; /* gattn_dtype */
+  int32_t kind;  /* gattn_norm_kind of both norms */
+  int32_t gate;  /* gattn_gate_mode */
+  float alpha;
+  float eps;
+  const float *w_post, *b_post, *w_pre, *b_pre; /* device fp32 [F], each nullable */
+} gattn_norm_desc;
+
+/*
+ * Forward: writes h (when x is given; may be res itself where the backward
+ * is not wanted), y (with w_pre) and
+ * stats, fp32 [N][4]: mean and 1 / deviation of x, then of h (an absent norm
+ * leaves its pair unwritten).
+ */
+GATTN_API gattn_status gattn_norm_fwd(const gattn_norm_desc* desc, const void* res, const void* x,
+                                      const void* gate, void* h, void* y, float* stats,
+                                      gattn_stream_t stream);
+
+/*
+ * Backward from dh (gradient of h, nullable for none) and dy (gradient of y).
+ * res, x, gate and stats are the forward's (h is formed again from them).  Each
+ * output is nullable: dres,
+ * dx, dgate ([N, F] per token, fp32 [F] per channel), dw_*, db_* (fp32 [F];
+ * written, not accumulated).  Column sums run in a fixed order.
+ *   workspace : device, gattn_norm_workspace_size bytes, 16-byte aligned.
+ */
+GATTN_API gattn_status gattn_norm_workspace_size(const gattn_norm_desc* desc, size_t* bytes);
+GATTN_API gattn_status gattn_norm_bwd(const gattn_norm_desc* desc, const void* res,
+                                      const float* stats, const void* dh, const void* dy,
+                                      const void* x, const void* gate, void* dres, void* dx,
+                                      void* dgate, float* dw_post, float* db_post, float* dw_pre,
+                                      float* db_pre, void* workspace, size_t workspace_bytes,
+                                      gattn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
