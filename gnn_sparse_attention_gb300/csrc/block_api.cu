@@ -12,7 +12,7 @@
 #include <cmath>
 
 #include "attn_launch.cuh"
-#include "block.cuh"
+#include "block_tc.cuh"
 
 namespace gattn {
 
@@ -381,7 +381,7 @@ gattn_status gattn_block_fwd_workspace_size(const gattn_block_desc* desc, size_t
   const gattn_status s = geom(desc, &g);
   if (s != GATTN_OK) return s;
   BLOCK_REQUIRE(bytes, GATTN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = 0;
+  *bytes = desc->dtype == GATTN_BF16 && g.U > 0 ? block_fwd_tc_workspace(g) : 0;
   return GATTN_OK;
 }
 
@@ -397,8 +397,13 @@ gattn_status gattn_block_fwd(const gattn_block_desc* desc, const void* Q, const 
     return s;
   BLOCK_REQUIRE(idx && al(idx, 4) && lse && al(lse, 4), GATTN_ERR_INVALID_ARG,
                 "idx and lse must be device pointers");
-  return launch_block_fwd_simt(g, gattn_dtype(desc->dtype), Q, K, V, idx, out, lse,
-                               reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (desc->dtype == GATTN_F32)
+    return launch_block_fwd_simt(g, GATTN_F32, Q, K, V, idx, out, lse, st);
+  if ((s = check_ws("gattn_block_fwd", workspace, workspace_bytes, block_fwd_tc_workspace(g))) !=
+      GATTN_OK)
+    return s;
+  return launch_block_fwd_tc(g, Q, K, V, idx, out, lse, workspace, st);
 }
 
 gattn_status gattn_block_bwd_workspace_size(const gattn_block_desc* desc, size_t* bytes) {
@@ -458,10 +463,16 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
 }
 
 gattn_status gattn_block_check_errors(void) {
-  const cudaError_t e = cudaDeviceSynchronize();
+  cudaError_t e = cudaDeviceSynchronize();
+  int fwd = 0;
+  if (e == cudaSuccess) e = block_fwd_tc_take_error(&fwd);
   if (e != cudaSuccess) {
     set_error("gattn_block_check_errors: %s", cudaGetErrorString(e));
     return GATTN_ERR_CUDA;
+  }
+  if (fwd) {
+    set_error("a block-attention kernel gave up a bounded wait");
+    return GATTN_ERR_TIMEOUT;
   }
   return GATTN_OK;
 }

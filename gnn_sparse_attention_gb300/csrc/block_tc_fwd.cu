@@ -1,0 +1,636 @@
+// block_tc_fwd.cu -- forward of block attention on the tensor cores
+// (bf16, D = 8 .. 128; heads narrower than 64 are padded with zeros by TMA).
+//
+// A tile is up to 128 (query row, head) pairs of one unit and key head: they
+// share the unit's block list.  A step is 128 keys, i.e. 128 / block blocks
+// of the list, each fetched by a TMA box of its own rows:
+//   S = Q K^T  (128 x 128 x D)      -> TMEM, two buffers
+//   p = 2^(s - m) as bf16           -> shared memory, two buffers
+//   O += P V   (128 x D x 128)      -> TMEM, two buffers (tiles in turn)
+// Roles: warps 0-7 softmax (thread = row and half of its 128 columns), warp 8
+// issues the products, warp 9 resolves block lists and issues TMA.  S of
+// step i + 1 runs while the softmax works on step i, and a tile's first
+// steps run while the tile before it is written out; every hand-over is an
+// mbarrier, every wait is bounded.
+//
+// With the list ascending, the keys that a row sees are the first columns of
+// its steps (list_keys), so the mask is one number per row and only the
+// steps around it compare.  The running maximum is exchanged between the two
+// halves of a row rounded up to bf16: it is a scale, any value at least as
+// large serves, and both halves use the same.  O is rescaled only when the
+// maximum grew by more than 2^8 (p stays below 2^8, far from overflow).
+//
+// Rows of V that no row may see (behind the sequence's end, or of no block)
+// are zeroed in shared memory, because 0 * NaN is NaN in the product.  Under
+// the causal mask some rows see a value that others must not: in those steps
+// non-finite values are taken out of V and added back to the rows that see
+// them when the tile is written.
+//
+// When there are fewer tiles than SMs (one new token per sequence), each
+// tile's steps are split over several CTAs and a second kernel joins them.
+#include <algorithm>
+
+#include "attn_launch.cuh"
+#include "attn_pipe.cuh"
+#include "block_tc.cuh"
+
+namespace gattn {
+
+namespace {
+
+__device__ int g_err;  // a bounded wait gave up
+
+constexpr int kT = kBlkTile;
+constexpr int kPiece = kT * 128;       // 128 rows x 64 bf16 columns
+constexpr int kSoftWarps = 8;
+constexpr int kThr = (kSoftWarps + 2) * 32;
+
+struct TcFwdParams {
+  CUtensorMap mq, mk, mv;
+  BlockGeom g;
+  const int32_t* idx;
+  const __nv_bfloat16* V;
+  __nv_bfloat16* out;
+  float* lse;
+  float *part_o, *part_l;  // nsplit > 1: [tile][split][rows][D], [tile][split][rows]
+  int ht, hs, rows;        // heads per tile, tiles per unit and key head, rows per tile
+  int nsplit;
+  int64_t n_tiles;         // splits counted
+};
+
+// What the producer tells the other warps about a tile.
+struct TileInfo {
+  int s0, s1;          // steps [s0, s1) of the list
+  int n, total;        // blocks in the list, keys in them
+  int least;           // keys that the tile's first row sees
+  int row, rows;       // first query row, query rows
+  int pos;             // position of the first query row
+  int kbeg, len;       // the sequence's keys
+  int kh, h0;          // key head, first query head
+  int poison;          // a non-finite value was taken out of V
+  int64_t part;        // index of its partial result
+};
+
+template <int DP>
+struct Sm {
+  static constexpr int KB = DP / 64;
+  static constexpr int NQ = DP == 64 ? 2 : 1;   // Q buffers
+  static constexpr int NS = DP == 64 ? 3 : 2;   // K and V stages
+  static constexpr int OP = KB * kPiece;         // one operand tile
+  static constexpr int Q = 0;
+  static constexpr int K = Q + NQ * OP;
+  static constexpr int V = K + NS * OP;
+  static constexpr int P = V + NS * OP;
+  static constexpr int RED = P + 2 * 2 * kPiece;  // [2][256] bf16 maxima, or [256] fp32 sums
+  static constexpr int IDS = RED + 1024;
+  static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
+  static constexpr int BAR = INFO + 2 * int(sizeof(TileInfo));
+  static constexpr int NBAR = 2 + 2 + 2 * NQ + 4 * NS + 2 + 2 + 2 + 2 + 2 + 4;
+  static constexpr int END = BAR + NBAR * 8 + 8;
+  static constexpr int BYTES = END + 1024 <= 227 * 1024 ? END + 1024 : 227 * 1024;
+  static_assert(END <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ uint32_t bf16_up(float x) {  // bf16 bits of x rounded towards +inf
+  const uint32_t b = __float_as_uint(x);
+  return ((int32_t(b) >= 0 && b < 0x7f800000u ? b + 0xffffu : b) >> 16);
+}
+
+}  // namespace
+
+template <int DP>
+__global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ TcFwdParams p) {
+  using namespace tc;
+  using M = Sm<DP>;
+  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, OP = M::OP;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
+  if (pad + M::END > M::BYTES) {  // the swizzled tiles need a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicOr(&g_err, 1);
+    return;
+  }
+  uint8_t* sm = smem_raw + pad;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
+  uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
+           *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
+           *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
+           *s_empty = s_full + 2, *p_full = s_empty + 2, *pv_done = p_full + 2,
+           *o_empty = pv_done + 2, *pair = o_empty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
+  TileInfo* info = reinterpret_cast<TileInfo*>(sm + M::INFO);
+  int* ids = reinterpret_cast<int*>(sm + M::IDS);
+  const BlockGeom& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tile_full + i, 1);
+      mbar_init(tile_empty + i, kSoftWarps + 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, kSoftWarps);
+      mbar_init(p_full + i, kSoftWarps);
+      mbar_init(pv_done + i, 1);
+      mbar_init(o_empty + i, kSoftWarps);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(pair + i, 2);
+    mbar_init_fence();
+  }
+  if (warp == kSoftWarps) tmem_alloc512(s_tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t tS = tmem, tO = tmem + 2 * kT;
+  bool ok = true;  // false: a wait gave up, leave
+
+  if (warp == kSoftWarps + 1) {
+    // ---------------------------------------------------------------- producer
+    const int per = kT / g.block;  // blocks per step
+    const uint32_t blk_bytes = uint32_t(g.block) * 128;
+    int gi = 0, ti = 0, tq = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
+      int64_t x = t;
+      const int sp = int(x % p.nsplit);
+      x /= p.nsplit;
+      const int hsub = int(x % p.hs);
+      x /= p.hs;
+      const int u = int(x % g.U), kh = int(x / g.U);
+      const Unit un = unit_at(g, u);
+      const Span ks = span_k(g, un.s);
+      int* list = ids + slot * kBlkMaxTopk;
+      int n = 0;
+      if (un.n > 0)
+        n = block_list(p.idx + u * g.is_u + kh * g.is_h, g.topk,
+                       (ks.len + g.block - 1) / g.block, list);
+      const int total = list_keys(list, n, g.block, ks.len);
+      // keys that the tile's last row sees bound its steps
+      const int seen =
+          g.causal ? list_keys(list, n, g.block, min(un.pos + un.n, ks.len)) : total;
+      const int steps = (seen + kT - 1) / kT;
+      const int each = (steps + p.nsplit - 1) / p.nsplit;
+      const int s0 = min(sp * each, steps), s1 = min(s0 + each, steps);
+      if (lane == 0) {
+        TileInfo& f = info[slot];
+        f.s0 = s0;
+        f.s1 = s1;
+        f.n = n;
+        f.total = total;
+        f.least = g.causal ? list_keys(list, n, g.block, min(un.pos + 1, ks.len)) : total;
+        f.row = un.row;
+        f.rows = un.n;
+        f.pos = un.pos;
+        f.kbeg = ks.beg;
+        f.len = ks.len;
+        f.kh = kh;
+        f.h0 = kh * g.G + hsub * p.ht;
+        f.poison = 0;
+        f.part = t;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_full + slot);
+      if (s1 <= s0) continue;
+      const int qs = tq % NQ;
+      if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+      if (!ok) break;
+      ++tq;
+      if (lane == 0) {
+        mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 128 * KB);
+        for (int kb = 0; kb < KB; ++kb)
+          tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, kh * g.G + hsub * p.ht,
+                     un.row, q_full + qs);
+      }
+      for (int st = s0; st < s1; ++st, ++gi) {
+        const int ks_i = gi % NS;
+        const int nb = min(per, n - st * per);  // blocks of this step
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* full = (kv ? v_full : k_full) + ks_i;
+          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + ks_i, ((gi / NS) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
+          __syncwarp();
+          for (int e = lane; e < nb * KB; e += 32) {
+            const int b = e / KB, kb = e % KB;
+            tma_tile3d(sm + (kv ? M::V : M::K) + ks_i * OP + kb * kPiece + b * blk_bytes,
+                       kv ? &p.mv : &p.mk, kb * 64, kh, ks.beg + list[st * per + b] * g.block,
+                       full);
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok) {  // the copies in flight must land before the CTA's memory is given up
+      for (int i = 1; i <= NQ && i <= tq; ++i)
+        warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
+      for (int c = gi; c > gi - NS && c >= 0; --c) {  // the newest use of each stage
+        warp_wait(k_full + c % NS, (c / NS) & 1, 200);
+        warp_wait(v_full + c % NS, (c / NS) & 1, 200);
+      }
+    }
+  } else if (warp == kSoftWarps) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_O = f16_idesc(kT, DP, true);
+      int gi = 0, ti = 0, tq = 0;
+      int pi = -1, po = 0;  // the step whose P V is due, its O buffer's tile count
+      bool pfirst = false;
+      auto product_pv = [&]() {
+        const int ks_i = pi % NS, b = pi & 1;
+        ok = ok && mbar_wait(p_full + b, (pi >> 1) & 1) && mbar_wait(v_full + ks_i, (pi / NS) & 1);
+        if (pfirst && po >= 2) ok = ok && mbar_wait(o_empty + (po & 1), ((po >> 1) - 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        mma_km<kT>(tO + (po & 1) * DP, sm + M::P + b * 2 * kPiece, kPiece,
+                   sm + M::V + ks_i * OP, kPiece, IDESC_O, !pfirst);
+        mma_commit(pv_done + b);
+        mma_commit(v_empty + ks_i);
+      };
+      for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+        const int slot = ti & 1;
+        ok = mbar_wait(tile_full + slot, (ti >> 1) & 1);
+        if (!ok) break;
+        const int n = info[slot].s1 - info[slot].s0;
+        mbar_arrive(tile_empty + slot);
+        if (n <= 0) {  // the softmax may wait for the last product before it moves on
+          if (pi >= 0) product_pv();
+          pi = -1;
+          continue;
+        }
+        const int qs = tq % NQ;
+        ok = mbar_wait(q_full + qs, (tq / NQ) & 1);
+        for (int i = 0; i < n && ok; ++i, ++gi) {
+          const int ks_i = gi % NS, b = gi & 1;
+          ok = mbar_wait(k_full + ks_i, (gi / NS) & 1);
+          if (gi >= 2) ok = ok && mbar_wait(s_empty + b, ((gi >> 1) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk<KB>(tS + b * kT, sm + M::Q + qs * OP, kPiece, sm + M::K + ks_i * OP, kPiece,
+                     IDESC_S);
+          mma_commit(s_full + b);
+          mma_commit(k_empty + ks_i);
+          if (i == n - 1) mma_commit(q_empty + qs);
+          if (pi >= 0) product_pv();
+          pi = gi;
+          po = tq;
+          pfirst = i == 0;
+        }
+        ++tq;
+      }
+      if (ok && pi >= 0) product_pv();
+      // every product has completed before TMEM is given up
+      if (ok && gi > 0) ok = mbar_wait(pv_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+      if (!ok && gi > 0) {
+        mbar_wait(s_full + ((gi - 1) & 1), ((gi - 1) >> 1) & 1, 200);
+        if (pi >= 0) mbar_wait(pv_done + (pi & 1), (pi >> 1) & 1, 200);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    uint16_t* red = reinterpret_cast<uint16_t*>(sm + M::RED);
+    float* redf = reinterpret_cast<float*>(sm + M::RED);
+    int gi = 0, ti = 0, to = 0, xc = 0;  // steps, tiles, tiles with steps, exchanges
+    const int th = r % p.ht, tt = r / p.ht;
+    // the two warps of a row have written; both may read
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair + (warp & 3));
+      ok = ok && warp_wait(pair + (warp & 3), xc & 1);
+      ++xc;
+    };
+    for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const TileInfo f = info[slot];
+      const int* list = ids + slot * kBlkMaxTopk;
+      const bool valid = r < p.rows && tt < f.rows;
+      const int lim = !valid ? 0
+                      : g.causal ? list_keys(list, f.n, g.block, min(f.pos + tt + 1, f.len))
+                                 : f.total;
+      float m = neg_inf(), l = 0.f;
+      for (int st = f.s0; st < f.s1; ++st, ++gi) {
+        const int b = gi & 1, ks_i = gi % NS;
+        ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float sv[64];
+        tmem_ld32(tS + b * kT + lane_off + half * 64, sv);
+        tmem_ld32(tS + b * kT + lane_off + half * 64 + 32, sv + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + b);
+        const int mine = lim - st * kT - half * 64;  // columns of this half the row sees
+        if (__any_sync(0xffffffffu, mine < 64)) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = j < mine ? sv[j] : neg_inf();
+        }
+        float c0 = sv[0], c1 = sv[1], c2 = sv[2], c3 = sv[3];
+#pragma unroll
+        for (int j = 4; j < 64; j += 4) {
+          c0 = fmaxf(c0, sv[j]);
+          c1 = fmaxf(c1, sv[j + 1]);
+          c2 = fmaxf(c2, sv[j + 2]);
+          c3 = fmaxf(c3, sv[j + 3]);
+        }
+        const uint32_t up = bf16_up(fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)));
+        uint16_t* rd = red + (xc & 1) * 256;
+        rd[half * 128 + r] = uint16_t(up);
+        meet();
+        if (!ok) break;
+        const float mx = fmaxf(m, fmaxf(__uint_as_float(up << 16),
+                                        __uint_as_float(uint32_t(rd[(half ^ 1) * 128 + r]) << 16)));
+        // keep the old scale while p stays below 2^8
+        const bool grow = !((mx - m) * g.qmul <= 8.f) && mx != m;
+        const float old = m;
+        if (grow) m = mx;
+        const float mq = m == neg_inf() ? 0.f : m * g.qmul;
+        // P's buffer is free once the product of two steps ago is done
+        if (gi >= 2) ok = ok && warp_wait(pv_done + b, ((gi >> 1) - 1) & 1);
+        const int end = (st + 1) * kT;
+        const bool tail = f.total < end;
+        const bool mixed = f.least < min(f.total, end);
+        if (tail || mixed) {
+          ok = ok && warp_wait(v_full + ks_i, (gi / NS) & 1);
+          if (!ok) break;
+          const int nv = min(f.total - st * kT, kT);
+          const int tid = threadIdx.x;
+          for (int kb = 0; kb < KB; ++kb) {
+            uint4* v = reinterpret_cast<uint4*>(sm + M::V + ks_i * OP + kb * kPiece);
+            for (int i = nv * 8 + tid; i < kT * 8; i += kSoftWarps * 32)
+              v[i] = make_uint4(0, 0, 0, 0);
+            if (mixed)
+              for (int i = tid; i < nv * 8; i += kSoftWarps * 32) {
+                uint4 x = v[i];
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                bool hit = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7f80u) == 0x7f80u) {
+                    w[e] &= 0xffff0000u;
+                    hit = true;
+                  }
+                  if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+                    w[e] &= 0xffffu;
+                    hit = true;
+                  }
+                }
+                if (hit) {
+                  v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                  *const_cast<volatile int*>(&info[slot].poison) = 1;
+                }
+              }
+          }
+        }
+        if (st > f.s0 && __any_sync(0xffffffffu, grow)) {
+          // O holds the steps before this one at the old scale
+          ok = ok && warp_wait(pv_done + (b ^ 1), ((gi - 1) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const float corr = grow ? ex2((old - m) * g.qmul) : 1.f;  // 0 from -inf
+          l *= corr;
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c) {
+            float o[32];
+            const uint32_t a = tO + (to & 1) * DP + lane_off + half * (DP / 2) + c * 32;
+            tmem_ld32(a, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= corr;
+            tmem_st32(a, o);
+            tmem_wait_st();
+          }
+        }
+        if (!ok) break;
+        uint8_t* pr = sm + M::P + b * 2 * kPiece + half * kPiece + r * 128;
+        float2 sum = make_float2(0.f, 0.f);
+        const float2 qm = f2s(g.qmul), nm = f2s(-mq);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 z =
+                f2fma(make_float2(sv[q * 8 + 2 * e], sv[q * 8 + 2 * e + 1]), qm, nm);
+            const float2 y = make_float2(ex2(z.x), ex2(z.y));
+            sum = f2add(sum, y);
+            w[e] = bf16x2_bits(y.x, y.y);
+          }
+          *reinterpret_cast<uint4*>(pr + ((q ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        l += sum.x + sum.y;
+        fence_proxy_async();  // P (and V's zeros) -> visible to the tensor cores
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + b);
+      }
+      if (!ok) break;
+      // ---- write the tile out
+      float lt = 0.f;
+      const bool some = f.s1 > f.s0;
+      if (some) {
+        // the last product waited for every warp's P, so for its reads of the maxima
+        ok = ok && warp_wait(pv_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        redf[half * 128 + r] = l;
+        meet();
+        lt = l + redf[(half ^ 1) * 128 + r];
+        meet();  // both have read before either writes a maximum there again
+        if (!ok) break;
+      }
+      const float inv = lt != 0.f ? 1.f / lt : 0.f;
+      const bool poison = some && *const_cast<volatile int*>(&info[slot].poison);
+      const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const int col = half * (DP / 2) + c * 32;
+        float o[32];
+        __syncwarp();
+        if (some) {
+          tmem_ld32(tO + (to & 1) * DP + lane_off + col, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * inv : 0.f;
+        if (poison && valid && lt != 0.f) {  // values that were taken out of V
+          for (int k = f.s0 * kT; k < min(lim, f.s1 * kT); ++k) {
+            const __nv_bfloat16* v =
+                p.V + (int64_t(f.kbeg + list[k / g.block] * g.block + k % g.block) * g.Hkv + f.kh) *
+                          g.D;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = col + i < g.D ? __bfloat162float(v[col + i]) : 0.f;
+              if (!(fabsf(x) <= 3.4e38f)) o[i] += x;
+            }
+          }
+        }
+        if (valid && p.nsplit > 1) {
+          float* d = p.part_o + (f.part * p.rows + r) * g.D + col;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (col + q * 4 < g.D)
+              *reinterpret_cast<float4*>(d + q * 4) =
+                  make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+        } else if (valid) {
+          __nv_bfloat16* d = p.out + qrow * g.D + col;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (col + q * 8 < g.D)
+              *reinterpret_cast<uint4*>(d + q * 8) = make_uint4(
+                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
+                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+        }
+      }
+      if (valid && half == 0) {
+        const float L = lt != 0.f ? m * g.qmul + lg2(lt) : neg_inf();  // base 2
+        if (p.nsplit > 1) p.part_l[f.part * p.rows + r] = L;
+        else p.lse[qrow] = L * kLn2;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (some) mbar_arrive(o_empty + (to & 1));
+        mbar_arrive(tile_empty + slot);
+      }
+      to += some;
+    }
+  }
+  if (!ok) atomicOr(&g_err, 2);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kSoftWarps) tmem_free512(tmem);
+}
+
+namespace {
+
+// Splits of a tile joined: out = sum_i 2^(L_i - L) o_i, L = log2 sum_i 2^L_i.
+__global__ void __launch_bounds__(128) block_join(const TcFwdParams p) {
+  const BlockGeom& g = p.g;
+  const int64_t tile = blockIdx.x;  // (key head, unit, head group)
+  const int hsub = int(tile % p.hs), u = int((tile / p.hs) % g.U), kh = int(tile / p.hs / g.U);
+  const Unit un = unit_at(g, u);
+  const int vec = g.D / 4;
+  for (int i = threadIdx.x; i < p.rows * vec; i += 128) {
+    const int r = i / vec, c = i - r * vec, t = r / p.ht;
+    if (t >= un.n) continue;
+    const float* L = p.part_l + tile * p.nsplit * p.rows + r;
+    float mx = neg_inf();
+    for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, L[s * p.rows]);
+    const float base = mx == neg_inf() ? 0.f : mx;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float w = ex2(L[s * p.rows] - base);
+      if (w == 0.f) continue;  // a split that saw nothing
+      const float4 x = reinterpret_cast<const float4*>(
+          p.part_o + ((tile * p.nsplit + s) * p.rows + r) * g.D)[c];
+      sum += w;
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const int64_t row = int64_t(un.row + t) * g.H + kh * g.G + hsub * p.ht + r % p.ht;
+    *reinterpret_cast<uint2*>(p.out + row * g.D + c * 4) =
+        make_uint2(tc::bf16x2_bits(o.x * inv, o.y * inv), tc::bf16x2_bits(o.z * inv, o.w * inv));
+    if (c == 0) p.lse[row] = sum != 0.f ? (base + lg2(sum)) * kLn2 : neg_inf();
+  }
+}
+
+struct Shape {
+  int ht, hs, rows, nsplit;
+  int64_t tiles;
+};
+Shape shape(const BlockGeom& g) {
+  Shape s{};
+  s.ht = tile_heads(g);
+  s.hs = g.G / s.ht;
+  s.rows = s.ht * g.qb;
+  s.tiles = int64_t(g.U) * g.Hkv * s.hs;
+  // Fewer tiles than SMs: split each over its steps so that most SMs work.
+  // One step a split at least; never more CTAs than SMs (a second round of
+  // one CTA costs as much as the first).
+  const int64_t steps = (int64_t(g.topk) * g.block + kT - 1) / kT;
+  s.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(steps, sm_count() / std::max<int64_t>(1, s.tiles))));
+  return s;
+}
+
+}  // namespace
+
+size_t block_fwd_tc_workspace(const BlockGeom& g) {
+  const Shape s = shape(g);
+  return s.nsplit > 1 ? size_t(s.tiles) * s.nsplit * s.rows * (g.D + 1) * 4 : 0;
+}
+
+gattn_status launch_block_fwd_tc(const BlockGeom& g, const void* Q, const void* K, const void* V,
+                                 const int32_t* idx, void* out, float* lse, void* ws,
+                                 cudaStream_t st) {
+  const Shape s = shape(g);
+  TcFwdParams p{};
+  p.g = g;
+  if (!encode_heads_map(&p.mq, Q, g.Nq, g.H, g.D, s.ht, g.qb) ||
+      !encode_heads_map(&p.mk, g.Nk ? K : Q, g.Nk, g.Hkv, g.D, 1, g.block) ||
+      !encode_heads_map(&p.mv, g.Nk ? V : Q, g.Nk, g.Hkv, g.D, 1, g.block))
+    return GATTN_ERR_CUDA;
+  p.idx = idx;
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.ht = s.ht;
+  p.hs = s.hs;
+  p.rows = s.rows;
+  p.nsplit = s.nsplit;
+  p.n_tiles = s.tiles * s.nsplit;
+  p.part_o = static_cast<float*>(ws);
+  p.part_l = p.part_o + (s.nsplit > 1 ? s.tiles * s.nsplit * s.rows * g.D : 0);
+  const unsigned grid = unsigned(std::min<int64_t>(p.n_tiles, sm_count()));
+  auto go = [&](auto kern, int bytes) -> gattn_status {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) {
+      kern<<<grid, kThr, bytes, st>>>(p);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+      set_error("gattn_block_fwd launch failed: %s", cudaGetErrorString(e));
+      return GATTN_ERR_CUDA;
+    }
+    return GATTN_OK;
+  };
+  gattn_status r = g.D <= 64 ? go(block_fwd_tc<64>, Sm<64>::BYTES)
+                             : go(block_fwd_tc<128>, Sm<128>::BYTES);
+  if (r != GATTN_OK || s.nsplit == 1) return r;
+  block_join<<<unsigned(s.tiles), 128, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("gattn_block_fwd (join) launch failed: %s", cudaGetErrorString(e));
+    return GATTN_ERR_CUDA;
+  }
+  return GATTN_OK;
+}
+
+cudaError_t block_fwd_tc_take_error(int* err) {
+  cudaError_t e = cudaMemcpyFromSymbol(err, g_err, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *err) e = cudaMemcpyToSymbol(g_err, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace gattn

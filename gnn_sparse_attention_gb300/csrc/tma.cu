@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "attn_tile.cuh"
+#include "block_tc.cuh"
 #include "tma.cuh"
 
 namespace gattn {
@@ -69,6 +70,29 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t w
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d) for a %lld x %lld tile map", int(r),
               (long long)rows, (long long)width);
+    return false;
+  }
+  return true;
+}
+
+bool encode_heads_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D,
+                      int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) {
+    set_error("cuTensorMapEncodeTiled is not available from the driver");
+    return false;
+  }
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(D) * 2 * heads};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d) for %lld x %d x %d", int(r), (long long)rows,
+              heads, D);
     return false;
   }
   return true;
