@@ -160,7 +160,7 @@ inline int tile_heads(const BlockGeom& g) { return g.G < kBlkTile / g.qb ? g.G :
 
 // Workspace of the backward (byte offsets).
 struct BlockBwdWs {
-  size_t delta, bits, head, cnt, items, part, total;
+  size_t stat, bits, head, cnt, items, part, total;
   int words;         // 32-bit words of a bitmap row (units)
   int chunk;         // units per work item
   int64_t max_items, slots;
@@ -172,7 +172,7 @@ struct BlockBwdParams {
   const int32_t* idx;
   const float* lse;
   void *dQ, *dK, *dV;
-  float* delta;      // [Nq][H]
+  float2* stat;      // [Nq][H]: lse log2(e), Delta
   uint32_t* bits;    // [B][Hkv][words]: units that chose the block
   int32_t* head;     // [4]: items, next item, slots
   int32_t* cnt;      // [KT * Hkv][2]: units of the key tile, first partial slot

@@ -143,8 +143,8 @@ BlockBwdWs bwd_ws(const BlockGeom& g) {
   w.slots = entries / w.chunk * 2 + 2;
   w.max_items = int64_t(g.KT) * g.Hkv + w.slots;
   size_t o = 0;
-  w.delta = o;
-  o = up256(o + size_t(g.Nq) * g.H * 4);
+  w.stat = o;
+  o = up256(o + size_t(g.Nq) * g.H * 8);
   w.bits = o;
   o += size_t(g.B) * g.Hkv * w.words * 4;
   w.head = o = up256(o);  // cleared together with the bits
@@ -159,10 +159,12 @@ BlockBwdWs bwd_ws(const BlockGeom& g) {
   return w;
 }
 
-// Delta[row][head] = dout . out: 16 bytes a lane, D / lanes a head
+// The backward's statistics of a (row, head): lse log2(e) and Delta = dout . out;
+// 16 bytes a lane, D / V lanes a head.
 template <class T, int V>
-__global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o,
-                                                    const T* __restrict__ go, float* delta,
+__global__ void __launch_bounds__(256) stat_kernel(const T* __restrict__ o,
+                                                    const T* __restrict__ go,
+                                                    const float* __restrict__ lse, float2* stat,
                                                     int64_t n, int D) {
   const int tpr = D / V;
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* __restrict__ o,
     }
   }
   for (int x = tpr >> 1; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-  if (i < n * tpr && threadIdx.x % tpr == 0) delta[i / tpr] = s;
+  if (i < n * tpr && threadIdx.x % tpr == 0) stat[i / tpr] = make_float2(lse[i / tpr] * kLog2e, s);
 }
 
 // one warp per unit: its bit in every block it lists
@@ -308,12 +310,13 @@ gattn_status bwd_prepare(const BlockBwdParams& p, gattn_dtype dt, const BlockBwd
   const int V = dt == GATTN_F32 ? 4 : 8;
   const unsigned grid = unsigned((n * (g.D / V) + 255) / 256);
   if (n > 0 && dt == GATTN_F32)
-    delta_kernel<float, 4><<<grid, 256, 0, st>>>(static_cast<const float*>(p.O),
-                                                 static_cast<const float*>(p.dO), p.delta, n, g.D);
+    stat_kernel<float, 4><<<grid, 256, 0, st>>>(static_cast<const float*>(p.O),
+                                                 static_cast<const float*>(p.dO), p.lse, p.stat, n,
+                                                 g.D);
   else if (n > 0)
-    delta_kernel<__nv_bfloat16, 8><<<grid, 256, 0, st>>>(
-        static_cast<const __nv_bfloat16*>(p.O), static_cast<const __nv_bfloat16*>(p.dO), p.delta,
-        n, g.D);
+    stat_kernel<__nv_bfloat16, 8><<<grid, 256, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(p.O), static_cast<const __nv_bfloat16*>(p.dO), p.lse,
+        p.stat, n, g.D);
   if (g.U > 0) mark_kernel<<<(g.U + 7) / 8, 256, 0, st>>>(p);
   count_kernel<<<(g.KT * g.Hkv + 7) / 8, 256, 0, st>>>(p);
   items_kernel<<<1, 1024, 0, st>>>(p, w.slots);
@@ -443,7 +446,7 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   p.dQ = dQ;
   p.dK = dK;
   p.dV = dV;
-  p.delta = reinterpret_cast<float*>(ws + w.delta);
+  p.stat = reinterpret_cast<float2*>(ws + w.stat);
   p.bits = reinterpret_cast<uint32_t*>(ws + w.bits);
   p.head = reinterpret_cast<int32_t*>(ws + w.head);
   p.cnt = reinterpret_cast<int32_t*>(ws + w.cnt);
@@ -455,7 +458,8 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const gattn_dtype dt = gattn_dtype(desc->dtype);
   if ((s = bwd_prepare(p, dt, w, ws, st)) != GATTN_OK ||
-      (s = launch_block_bwd_simt(p, dt, st)) != GATTN_OK)
+      (s = dt == GATTN_F32 ? launch_block_bwd_simt(p, dt, st) : launch_block_bwd_tc(p, st)) !=
+          GATTN_OK)
     return s;
   if (dt == GATTN_F32) join_kv_kernel<float><<<g.KT * g.Hkv, 256, 0, st>>>(p);
   else join_kv_kernel<__nv_bfloat16><<<g.KT * g.Hkv, 256, 0, st>>>(p);
@@ -464,13 +468,14 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
 
 gattn_status gattn_block_check_errors(void) {
   cudaError_t e = cudaDeviceSynchronize();
-  int fwd = 0;
+  int fwd = 0, bwd = 0;
   if (e == cudaSuccess) e = block_fwd_tc_take_error(&fwd);
+  if (e == cudaSuccess) e = block_bwd_tc_take_error(&bwd);
   if (e != cudaSuccess) {
     set_error("gattn_block_check_errors: %s", cudaGetErrorString(e));
     return GATTN_ERR_CUDA;
   }
-  if (fwd) {
+  if (fwd || bwd) {
     set_error("a block-attention kernel gave up a bounded wait");
     return GATTN_ERR_TIMEOUT;
   }

@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
     lim[i] = !g.causal ? total : list_keys(ids, n, g.block, min(un.pos + t + 1, ks.len));
     if (t >= un.n) lim[i] = 0;
     const int64_t at = q_off(g, un, kh, r);
-    L[i] = at >= 0 ? p.lse[at / D] * kLog2e : 0.f;
-    Dl[i] = at >= 0 ? p.delta[at / D] : 0.f;
+    const float2 stat = at >= 0 ? p.stat[at / D] : make_float2(0.f, 0.f);
+    L[i] = stat.x;
+    Dl[i] = stat.y;
 #pragma unroll
     for (int q = 0; q < DQ; ++q)
 #pragma unroll
@@ -395,16 +396,15 @@ __global__ void __launch_bounds__(kThr) block_dkv_simt(const BlockBwdParams p) {
           for (int i = 0; i < 4; ++i) {
             const int r = r0 + ty * 4 + i, t = r / g.G;
             const int64_t at = q_off(g, un, kh, r);
-            const float L = at >= 0 ? p.lse[at / D] * kLog2e : 0.f;
-            const float Dl = at >= 0 ? p.delta[at / D] : 0.f;
+            const float2 stat = at >= 0 ? p.stat[at / D] : make_float2(0.f, 0.f);
             const int end = at < 0 ? 0 : g.causal ? min(un.pos + t + 1, ks.len) : ks.len;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int c = tx + 16 * j, pos = pos0 + c;
               const bool in = pos < end && ((mk >> ((half * kC + c) / g.block)) & 1u);
-              const float w = in ? ex2(fmaf(sc[i][j], g.qmul, -L)) : 0.f;
+              const float w = in ? ex2(fmaf(sc[i][j], g.qmul, -stat.x)) : 0.f;
               sP[(ty * 4 + i) * kPS + c] = w;
-              sS[(ty * 4 + i) * kPS + c] = in ? w * (dp[i][j] - Dl) : 0.f;
+              sS[(ty * 4 + i) * kPS + c] = in ? w * (dp[i][j] - stat.y) : 0.f;
             }
           }
           __syncthreads();

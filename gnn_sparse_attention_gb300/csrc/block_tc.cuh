@@ -74,7 +74,9 @@ size_t block_fwd_tc_workspace(const BlockGeom& g);
 gattn_status launch_block_fwd_tc(const BlockGeom& g, const void* Q, const void* K, const void* V,
                                  const int32_t* idx, void* out, float* lse, void* ws,
                                  cudaStream_t st);
-// Whether a kernel of the unit gave up a bounded wait on this device; clears the record.
+gattn_status launch_block_bwd_tc(const BlockBwdParams& p, cudaStream_t st);
+// Whether a forward (backward) kernel gave up a bounded wait on this device; clears the record.
 cudaError_t block_fwd_tc_take_error(int* err);
+cudaError_t block_bwd_tc_take_error(int* err);
 
 }  // namespace gattn

@@ -1,0 +1,897 @@
+// block_tc_bwd.cu -- backward of block attention on the tensor cores (bf16).
+//
+// Two kernels, both with the forward's division of labour (compute warps, one
+// warp that issues products, one that resolves lists and issues TMA; every
+// hand-over an mbarrier, every wait bounded):
+//
+// dQ: a tile of up to 128 (query row, head) pairs walks its unit's block list
+//   in steps of 128 keys,
+//     S = Q K^T, dP = dO V^T                          -> TMEM
+//     ds = 2^(S scale log2e - lse log2e) (dP - Delta)  -> bf16, shared memory
+//     dQ += ds K                                       -> TMEM
+//   The next step's S and dP run while ds of this one is formed.
+//
+// dK, dV: a work item is a tile of 128 keys and up to `chunk` of the units that
+//   chose one of its blocks (block_api.cu builds the items), walked in steps
+//   of 64 (query row, head) pairs,
+//     S^T = K Q^T, dP^T = V dO^T                       -> TMEM, two buffers
+//     p, ds as bf16 [key][query]                       -> shared memory
+//     dV += p dO, dK += ds Q                           -> TMEM
+//   64 rather than 128 queries a step leave room for three or four stages of
+//   Q and dO and a second score buffer next to the two accumulators.  Units
+//   of fewer than 64 pairs share a step, each in a box of its own; a box
+//   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
+//   its mask within a box is a range of columns.
+//
+// Rows that must not count but sit in an operand of the last products (keys
+// behind the list's end, queries behind a unit's end) are zeroed in shared
+// memory, because 0 * NaN is NaN there.
+#include <algorithm>
+
+#include "attn_launch.cuh"
+#include "attn_pipe.cuh"
+#include "block_tc.cuh"
+
+namespace gattn {
+
+namespace {
+
+__device__ int g_err;  // a bounded wait gave up
+
+constexpr int kT = kBlkTile;
+constexpr int kPiece = kT * 128;  // 128 rows x 64 bf16 columns
+
+struct DqParams {
+  CUtensorMap mq, mo, mk, mv;  // Q, dO, K, V
+  BlockBwdParams b;
+  int ht, hs, rows;
+  int64_t n_tiles;
+};
+
+struct DqInfo {
+  int steps, n, total;
+  int row, rows, pos;
+  int len, h0;
+};
+
+template <int DP>
+struct DqSm {
+  static constexpr int KB = DP / 64;
+  static constexpr int NQ = DP == 64 ? 2 : 1;   // Q and dO buffers
+  static constexpr int NS = DP == 64 ? 3 : 2;   // K and V stages
+  static constexpr int ND = DP == 64 ? 2 : 1;   // ds buffers
+  static constexpr int OP = KB * kPiece;
+  static constexpr int Q = 0;
+  static constexpr int O = Q + NQ * OP;
+  static constexpr int K = O + NQ * OP;
+  static constexpr int V = K + NS * OP;
+  static constexpr int DS = V + NS * OP;
+  static constexpr int IDS = DS + ND * 2 * kPiece;
+  static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
+  static constexpr int BAR = INFO + 2 * int(sizeof(DqInfo));
+  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 2 + 2 * ND + 2;
+  static constexpr int END = BAR + NBAR * 8 + 8;
+  static constexpr int BYTES = END + 1024 <= 227 * 1024 ? END + 1024 : 227 * 1024;
+  static_assert(END <= 227 * 1024, "shared memory of one CTA");
+};
+
+constexpr int kDqWarps = 16;
+constexpr int kDqThr = (kDqWarps + 2) * 32;
+
+}  // namespace
+
+template <int DP>
+__global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__ DqParams p) {
+  using namespace tc;
+  using M = DqSm<DP>;
+  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, ND = M::ND, OP = M::OP;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
+  if (pad + M::END > M::BYTES) {
+    if (threadIdx.x == 0) atomicOr(&g_err, 1);
+    return;
+  }
+  uint8_t* sm = smem_raw + pad;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
+  uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
+           *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
+           *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
+           *s_empty = s_full + 1, *d_full = s_empty + 1, *d_done = d_full + ND,
+           *g_empty = d_done + ND;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
+  DqInfo* info = reinterpret_cast<DqInfo*>(sm + M::INFO);
+  int* ids = reinterpret_cast<int*>(sm + M::IDS);
+  const BlockGeom& g = p.b.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tile_full + i, 1);
+      mbar_init(tile_empty + i, kDqWarps + 1);
+      mbar_init(g_empty + i, kDqWarps);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(v_empty + i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, kDqWarps);
+    for (int i = 0; i < ND; ++i) {
+      mbar_init(d_full + i, kDqWarps);
+      mbar_init(d_done + i, 1);
+    }
+    mbar_init_fence();
+  }
+  if (warp == kDqWarps) tmem_alloc512(s_tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t tS = tmem, tP = tmem + kT, tG = tmem + 2 * kT;
+  bool ok = true;
+
+  if (warp == kDqWarps + 1) {
+    // ---------------------------------------------------------------- producer
+    const int per = kT / g.block;
+    const uint32_t blk_bytes = uint32_t(g.block) * 128;
+    int gi = 0, ti = 0, tq = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
+      const int hsub = int(t % p.hs), u = int((t / p.hs) % g.U), kh = int(t / p.hs / g.U);
+      const Unit un = unit_at(g, u);
+      const Span ks = span_k(g, un.s);
+      int* list = ids + slot * kBlkMaxTopk;
+      int n = 0;
+      if (un.n > 0)
+        n = block_list(p.b.idx + u * g.is_u + kh * g.is_h, g.topk,
+                       (ks.len + g.block - 1) / g.block, list);
+      const int total = list_keys(list, n, g.block, ks.len);
+      const int seen =
+          g.causal ? list_keys(list, n, g.block, min(un.pos + un.n, ks.len)) : total;
+      const int steps = (seen + kT - 1) / kT;
+      if (lane == 0) {
+        DqInfo& f = info[slot];
+        f.steps = steps;
+        f.n = n;
+        f.total = total;
+        f.row = un.row;
+        f.rows = un.n;
+        f.pos = un.pos;
+        f.len = ks.len;
+        f.h0 = kh * g.G + hsub * p.ht;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_full + slot);
+      if (steps <= 0) continue;
+      const int qs = tq % NQ;
+      if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+      if (!ok) break;
+      ++tq;
+      if (lane == 0) {
+        mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 256 * KB);
+        for (int kb = 0; kb < KB; ++kb) {
+          const int h0 = kh * g.G + hsub * p.ht;
+          tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, h0, un.row, q_full + qs);
+          tma_tile3d(sm + M::O + qs * OP + kb * kPiece, &p.mo, kb * 64, h0, un.row, q_full + qs);
+        }
+      }
+      for (int st = 0; st < steps; ++st, ++gi) {
+        const int si = gi % NS;
+        const int nb = min(per, n - st * per);
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* full = (kv ? v_full : k_full) + si;
+          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / NS) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
+          __syncwarp();
+          for (int e = lane; e < nb * KB; e += 32) {
+            const int b = e / KB, kb = e % KB;
+            tma_tile3d(sm + (kv ? M::V : M::K) + si * OP + kb * kPiece + b * blk_bytes,
+                       kv ? &p.mv : &p.mk, kb * 64, kh, ks.beg + list[st * per + b] * g.block,
+                       full);
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok) {  // the copies in flight must land before the CTA's memory is given up
+      for (int i = 1; i <= NQ && i <= tq; ++i)
+        warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
+      for (int c = gi; c > gi - NS && c >= 0; --c) {
+        warp_wait(k_full + c % NS, (c / NS) & 1, 200);
+        warp_wait(v_full + c % NS, (c / NS) & 1, 200);
+      }
+    }
+  } else if (warp == kDqWarps) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_G = f16_idesc(kT, DP, true);
+      int gi = 0, ti = 0, tq = 0;
+      int pi = -1, po = 0;  // the step whose dQ product is due, its tile
+      bool pfirst = false;
+      auto product_dq = [&]() {
+        const int si = pi % NS, d = pi % ND;
+        ok = ok && mbar_wait(d_full + d, (pi / ND) & 1);
+        if (pfirst && po >= 2) ok = ok && mbar_wait(g_empty + (po & 1), ((po >> 1) - 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        mma_km<kT>(tG + (po & 1) * DP, sm + M::DS + d * 2 * kPiece, kPiece, sm + M::K + si * OP,
+                   kPiece, IDESC_G, !pfirst);
+        mma_commit(d_done + d);
+        mma_commit(k_empty + si);
+      };
+      for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+        const int slot = ti & 1;
+        ok = mbar_wait(tile_full + slot, (ti >> 1) & 1);
+        if (!ok) break;
+        const int n = info[slot].steps;
+        mbar_arrive(tile_empty + slot);
+        if (n <= 0) {  // the compute warps may wait for the last product before they move on
+          if (pi >= 0) product_dq();
+          pi = -1;
+          continue;
+        }
+        const int qs = tq % NQ;
+        ok = mbar_wait(q_full + qs, (tq / NQ) & 1);
+        for (int i = 0; i < n && ok; ++i, ++gi) {
+          const int si = gi % NS;
+          ok = mbar_wait(k_full + si, (gi / NS) & 1) && mbar_wait(v_full + si, (gi / NS) & 1);
+          if (gi >= 1) ok = ok && mbar_wait(s_empty, (gi - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk<KB>(tS, sm + M::Q + qs * OP, kPiece, sm + M::K + si * OP, kPiece, IDESC_S);
+          mma_kk<KB>(tP, sm + M::O + qs * OP, kPiece, sm + M::V + si * OP, kPiece, IDESC_S);
+          mma_commit(s_full);
+          mma_commit(v_empty + si);
+          if (i == n - 1) mma_commit(q_empty + qs);
+          if (pi >= 0) product_dq();
+          pi = gi;
+          po = tq;
+          pfirst = i == 0;
+        }
+        ++tq;
+      }
+      if (ok && pi >= 0) product_dq();
+      if (ok && gi > 0) ok = mbar_wait(d_done + (gi - 1) % ND, ((gi - 1) / ND) & 1);
+      if (!ok && gi > 0) {
+        mbar_wait(s_full, (gi - 1) & 1, 200);
+        if (pi >= 0) mbar_wait(d_done + pi % ND, (pi / ND) & 1, 200);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- p and ds
+    const int r = (warp & 3) * 32 + lane, cc = warp >> 2;  // row, 32-column chunk
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const int th = r % p.ht, tt = r / p.ht;
+    int gi = 0, ti = 0, to = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const DqInfo f = info[slot];
+      const bool valid = r < p.rows && tt < f.rows;
+      const int lim = !valid ? 0
+                      : g.causal ? list_keys(ids + slot * kBlkMaxTopk, f.n, g.block,
+                                             min(f.pos + tt + 1, f.len))
+                                 : f.total;
+      const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
+      float2 stat = make_float2(0.f, 0.f);
+      if (valid) stat = p.b.stat[qrow];
+      for (int st = 0; st < f.steps; ++st, ++gi) {
+        const int si = gi % NS, d = gi % ND;
+        ok = ok && warp_wait(s_full, gi & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float sv[32], dv[32];
+        tmem_ld32(tS + lane_off + cc * 32, sv);
+        tmem_ld32(tP + lane_off + cc * 32, dv);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        if (gi >= ND) ok = ok && warp_wait(d_done + d, ((gi / ND) - 1) & 1);
+        if (!ok) break;
+        if (f.total < (st + 1) * kT) {  // keys behind the list's end: zeros in K
+          const int nv = f.total - st * kT;
+          for (int kb = 0; kb < KB; ++kb) {
+            uint4* k = reinterpret_cast<uint4*>(sm + M::K + si * OP + kb * kPiece);
+            for (int i = nv * 8 + threadIdx.x; i < kT * 8; i += kDqWarps * 32)
+              k[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        const int mine = lim - st * kT - cc * 32;
+        const float2 qm = f2s(g.qmul), nl = f2s(-stat.x), nd = f2s(-stat.y);
+        uint8_t* dr = sm + M::DS + d * 2 * kPiece + (cc >> 1) * kPiece + r * 128;
+        const bool full = __all_sync(0xffffffffu, mine >= 32);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = q * 8 + 2 * e;
+            const float2 z = f2fma(make_float2(sv[j], sv[j + 1]), qm, nl);
+            float2 y = f2mul(make_float2(ex2(z.x), ex2(z.y)),
+                             f2add(make_float2(dv[j], dv[j + 1]), nd));
+            if (!full) {
+              y.x = j < mine ? y.x : 0.f;
+              y.y = j + 1 < mine ? y.y : 0.f;
+            }
+            w[e] = bf16x2_bits(y.x, y.y);
+          }
+          *reinterpret_cast<uint4*>(dr + ((((cc & 1) * 4 + q) ^ (r & 7)) * 16)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_full + d);
+      }
+      if (!ok) break;
+      const bool some = f.steps > 0;
+      if (some) {
+        ok = warp_wait(d_done + (gi - 1) % ND, ((gi - 1) / ND) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (cc * 32 < DP) {
+        float o[32];
+        if (some) {
+          tmem_ld32(tG + (to & 1) * DP + lane_off + cc * 32, o);
+          tmem_wait_ld();
+        }
+        if (valid) {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.b.dQ) + qrow * g.D + cc * 32;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * g.scale : 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (cc * 32 + q * 8 < g.D)
+              *reinterpret_cast<uint4*>(out + q * 8) = make_uint4(
+                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
+                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (some) mbar_arrive(g_empty + (to & 1));
+        mbar_arrive(tile_empty + slot);
+      }
+      to += some;
+    }
+  }
+  if (!ok) atomicOr(&g_err, 2);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kDqWarps) tmem_free512(tmem);
+}
+
+namespace {
+
+constexpr int kNR = 64;               // query pairs per step
+constexpr int kQPiece = kNR * 128;    // 64 rows x 64 bf16 columns
+constexpr int kKvWarps = 8;
+constexpr int kKvThr = (kKvWarps + 2) * 32;
+constexpr int kList = 256;            // units resolved at a time (8 bitmap words)
+
+struct DkvParams {
+  CUtensorMap mq, mo, mk, mv;
+  BlockBwdParams b;
+  int bh, bt;      // heads and query rows of a box
+  int br, boxes;   // pairs of a box, boxes of a step
+  int ub;          // boxes of a unit
+};
+
+struct Box {
+  int mask;        // blocks of the key tile that the unit chose
+  int end;         // first position that the box's first query does not see
+  int rows;        // pairs of the box that exist
+};
+
+struct KvInfo {
+  int item;        // -1: no more items
+  int steps;
+  int kbeg, pos, n;  // first key row, its position, keys of the tile
+  int kh, slot;
+};
+
+template <int DP>
+struct KvSm {
+  static constexpr int KB = DP / 64;
+  static constexpr int NS = DP == 64 ? 4 : 3;  // Q and dO stages
+  static constexpr int NP = DP == 64 ? 2 : 1;  // p and ds buffers
+  static constexpr int OP = KB * kPiece, QP = KB * kQPiece;
+  static constexpr int K = 0;
+  static constexpr int V = OP;
+  static constexpr int Q = 2 * OP;
+  static constexpr int O = Q + NS * QP;
+  static constexpr int P = O + NS * QP;          // [NP][128][128 B]
+  static constexpr int DS = P + NP * kPiece;
+  static constexpr int STAT = DS + NP * kPiece;  // [NS][64] (lse log2e, Delta)
+  static constexpr int BOX = STAT + NS * kNR * 8;
+  static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
+  static constexpr int INFO = LIST + kList * 8;
+  static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
+  static constexpr int NBAR = 4 + 2 + 2 * NS + 4 + 2 * NP + 2;
+  static constexpr int END = BAR + NBAR * 8 + 8;
+  static constexpr int BYTES = END + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+// more bytes to wait for in the barrier's phase, without an arrival
+__device__ __forceinline__ void mbar_add_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// arrive once this thread's cp.async copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+}  // namespace
+
+template <int DP>
+__global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
+  using namespace tc;
+  using M = KvSm<DP>;
+  constexpr int KB = M::KB, NS = M::NS, NP = M::NP, QP = M::QP;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
+  uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
+           *kv_empty = kv_full + 1, *q_full = kv_empty + 1, *q_empty = q_full + NS,
+           *s_full = q_empty + NS, *s_empty = s_full + 2, *p_full = s_empty + 2,
+           *p_done = p_full + NP, *g_empty = p_done + NP;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
+  KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
+  int2* list = reinterpret_cast<int2*>(sm + M::LIST);
+  const BlockGeom& g = p.b.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, kKvWarps + 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, kKvWarps);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(q_full + i, 1 + 32);  // the copies' bytes, and each lane's statistics
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < NP; ++i) {
+      mbar_init(p_full + i, kKvWarps);
+      mbar_init(p_done + i, 1);
+    }
+    mbar_init(g_empty, kKvWarps);
+    mbar_init_fence();
+  }
+  if (warp == kKvWarps) tmem_alloc512(s_tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t tS = tmem, tP = tmem + 2 * kNR, tV = tmem + 4 * kNR, tK = tV + DP;
+  bool ok = true;
+
+  if (warp == kKvWarps + 1) {
+    // ---------------------------------------------------------------- producer
+    const int64_t n_items = p.b.head[0];
+    int gi = 0, ti = 0, tk = 0;
+    for (;; ++ti) {
+      int it = 0;
+      if (lane == 0) it = atomicAdd(p.b.head + 1, 1);
+      it = __shfl_sync(0xffffffffu, it, 0);
+      const int slot = ti & 1;
+      if (ti >= 2) ok = warp_wait(item_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
+      if (it >= n_items) {
+        if (lane == 0) {
+          info[slot].item = -1;
+          mbar_arrive(item_full + slot);
+        }
+        break;
+      }
+      const int4 q = p.b.items[it];
+      const int kt = q.x / g.Hkv, kh = q.x - kt * g.Hkv;
+      const int s = piece_seq(g.seq_k, g.S, kT, kt);
+      const Span ks = span_k(g, s), qs = span_q(g, s);
+      const int pos = (kt - piece_base(g.seq_k, s, kT)) * kT;
+      const int nb = min(kT / g.block, (ks.len + g.block - 1) / g.block - pos / g.block);
+      const int brow = min(piece_base(g.seq_k, s, g.block) + pos / g.block, g.B - nb);
+      const int ub = piece_base(g.seq_q, s, g.qb), nu = (qs.len + g.qb - 1) / g.qb;
+      const int64_t all_boxes = int64_t(q.z) * p.ub;
+      const int steps = int((all_boxes + p.boxes - 1) / p.boxes);
+      if (lane == 0) {
+        KvInfo& f = info[slot];
+        f.item = it;
+        f.steps = steps;
+        f.kbeg = ks.beg + pos;
+        f.pos = pos;
+        f.n = min(kT, ks.len - pos);
+        f.kh = kh;
+        f.slot = q.w;
+        mbar_arrive(item_full + slot);
+      }
+      if (steps == 0) continue;
+      if (tk >= 1) ok = warp_wait(kv_empty, (tk - 1) & 1);
+      if (!ok) break;
+      ++tk;
+      if (lane == 0) {
+        mbar_expect_tx(kv_full, 2 * KB * kPiece);
+        for (int kb = 0; kb < KB; ++kb) {
+          tma_tile3d(sm + M::K + kb * kPiece, &p.mk, kb * 64, kh, ks.beg + pos, kv_full);
+          tma_tile3d(sm + M::V + kb * kPiece, &p.mv, kb * 64, kh, ks.beg + pos, kv_full);
+        }
+      }
+      // units in ascending order: the set bits of the blocks' rows, 8 words at a time
+      int w0 = ub / 32, seen = 0;   // next word, units before it
+      int have = 0, next = 0;       // resolved units, the next one of them
+      int sub = 0;                  // boxes of that unit already issued
+      for (int st = 0; st < steps && ok; ++st, ++gi) {
+        const int si = gi % NS;
+        if (gi >= NS) ok = warp_wait(q_empty + si, ((gi / NS) - 1) & 1);
+        if (!ok) break;
+        // each box announces its bytes; lane 0's own arrival comes last
+        Box* box = reinterpret_cast<Box*>(sm + M::BOX) + si * kNR;
+        for (int j = 0; j < p.boxes; ++j) {
+          while (next >= have && seen < q.y + q.z && w0 <= (ub + nu - 1) / 32) {
+            // resolve the next 8 words: lanes 0-7
+            const int w = w0 + lane;
+            uint32_t bits[8], any = 0;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              bits[b] = lane < 8 && b < nb && w < p.b.words
+                            ? p.b.bits[(int64_t(brow + b) * g.Hkv + kh) * p.b.words + w] : 0u;
+              any |= bits[b];
+            }
+            const int c = __popc(any);
+            int before = c;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+              const int x = __shfl_up_sync(0xffffffffu, before, o);
+              if (lane >= o) before += x;
+            }
+            const int all = __shfl_sync(0xffffffffu, before, 7);
+            int at = seen + before - c;
+            const int lo = max(seen, q.y), hi = min(seen + all, q.y + q.z);
+            __syncwarp();
+            for (uint32_t a = any; a; a &= a - 1, ++at) {
+              if (at < lo || at >= hi) continue;
+              const int bit = __ffs(a) - 1;
+              int mk = 0;
+#pragma unroll
+              for (int b = 0; b < 8; ++b) mk |= int((bits[b] >> bit) & 1u) << b;
+              list[at - lo] = make_int2(w * 32 + bit, mk);
+            }
+            __syncwarp();
+            have = max(0, hi - lo);
+            next = 0;
+            seen += all;
+            w0 += 8;
+          }
+          Box x{0, 0, 0};
+          int64_t qrow = 0;
+          int h0 = kh * g.G;
+          if (next < have) {
+            const int2 e = list[next];
+            const int64_t off = int64_t(e.x - ub) * g.qb;
+            const int hn = g.G / p.bh;                       // head groups of a unit
+            const int t0 = (sub / hn) * p.bt;
+            h0 += (sub % hn) * p.bh;
+            // (a unit outside the sequence: only where offsets lie about the tables)
+            const int n = off >= 0 && off < qs.len
+                              ? clampi(min(g.qb, qs.len - int(off)) - t0, 0, p.bt) : 0;
+            x.mask = e.y;
+            x.rows = n * p.bh;
+            x.end = g.causal ? int(off) + t0 + ks.len - qs.len + 1 : INT32_MAX / 2;
+            qrow = n > 0 ? qs.beg + off + t0 : 0;
+            if (++sub == p.ub) {
+              sub = 0;
+              ++next;
+            }
+          }
+          if (lane == 0) box[j] = x;
+          if (x.rows > 0) {
+            const int at = j * p.br;
+            if (lane == 0) {
+              mbar_add_tx(q_full + si, uint32_t(p.br) * 256 * KB);
+              for (int kb = 0; kb < KB; ++kb) {
+                tma_tile3d(sm + M::Q + si * QP + kb * kQPiece + at * 128, &p.mq, kb * 64, h0,
+                           int(qrow), q_full + si);
+                tma_tile3d(sm + M::O + si * QP + kb * kQPiece + at * 128, &p.mo, kb * 64, h0,
+                           int(qrow), q_full + si);
+              }
+            }
+            for (int i = lane; i < x.rows; i += 32)
+              cp_async8(sm + M::STAT + (si * kNR + at + i) * 8,
+                        p.b.stat + (qrow + i / p.bh) * g.H + h0 + i % p.bh);
+          }
+        }
+        __syncwarp();
+        cp_async_arrive(q_full + si);
+        if (lane == 0) mbar_arrive(q_full + si);
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      if (tk > 0) warp_wait(kv_full, (tk - 1) & 1, 200);
+      for (int c = gi; c > gi - NS && c >= 0; --c) warp_wait(q_full + c % NS, (c / NS) & 1, 200);
+    }
+    cp_async_wait<0>();
+  } else if (warp == kKvWarps) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false), IDESC_G = f16_idesc(kT, DP, true);
+      int gi = 0, tk = 0;
+      int pi = -1, pk = 0;
+      bool pfirst = false;
+      auto product_g = [&]() {
+        const int si = pi % NS, b = pi % NP;
+        ok = ok && mbar_wait(p_full + b, (pi / NP) & 1);
+        if (pfirst && pk >= 1) ok = ok && mbar_wait(g_empty, (pk - 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        mma_km<kNR>(tV, sm + M::P + b * kPiece, kPiece, sm + M::O + si * QP, kQPiece, IDESC_G,
+                    !pfirst);
+        mma_km<kNR>(tK, sm + M::DS + b * kPiece, kPiece, sm + M::Q + si * QP, kQPiece, IDESC_G,
+                    !pfirst);
+        mma_commit(p_done + b);
+        mma_commit(q_empty + si);
+      };
+      for (int ti = 0; ok; ++ti) {
+        const int slot = ti & 1;
+        ok = mbar_wait(item_full + slot, (ti >> 1) & 1);
+        if (!ok) break;
+        const int it = info[slot].item, n = info[slot].steps;
+        mbar_arrive(item_empty + slot);
+        if (it < 0) break;
+        if (n <= 0) {
+          if (pi >= 0) product_g();
+          pi = -1;
+          continue;
+        }
+        ok = mbar_wait(kv_full, tk & 1);
+        for (int i = 0; i < n && ok; ++i, ++gi) {
+          const int si = gi % NS, b = gi & 1;
+          ok = mbar_wait(q_full + si, (gi / NS) & 1);
+          if (gi >= 2) ok = ok && mbar_wait(s_empty + b, ((gi >> 1) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk<KB>(tS + b * kNR, sm + M::K, kPiece, sm + M::Q + si * QP, kQPiece, IDESC_S);
+          mma_kk<KB>(tP + b * kNR, sm + M::V, kPiece, sm + M::O + si * QP, kQPiece, IDESC_S);
+          mma_commit(s_full + b);
+          if (i == n - 1) mma_commit(kv_empty);
+          if (pi >= 0) product_g();
+          pi = gi;
+          pk = tk;
+          pfirst = i == 0;
+        }
+        ++tk;
+      }
+      if (ok && pi >= 0) product_g();
+      if (ok && gi > 0) ok = mbar_wait(p_done + (gi - 1) % NP, ((gi - 1) / NP) & 1);
+      if (!ok && gi > 0) {
+        mbar_wait(s_full + ((gi - 1) & 1), ((gi - 1) >> 1) & 1, 200);
+        if (pi >= 0) mbar_wait(p_done + pi % NP, (pi / NP) & 1, 200);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- p and ds
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2;  // key, 32 of the 64 columns
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const int blk = r / g.block;
+    int gi = 0;
+    for (int ti = 0;; ++ti) {
+      const int slot = ti & 1;
+      ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const KvInfo f = info[slot];
+      if (f.item < 0) break;
+      const int pos = f.pos + r;
+      const bool valid = r < f.n;
+      for (int st = 0; st < f.steps; ++st, ++gi) {
+        const int si = gi % NS, b = gi & 1, pb = gi % NP;
+        ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
+        ok = ok && warp_wait(q_full + si, (gi / NS) & 1);  // the statistics and boxes
+        if (!ok) break;
+        tc_fence_after();
+        float sv[32], dv[32];
+        tmem_ld32(tS + b * kNR + lane_off + half * 32, sv);
+        tmem_ld32(tP + b * kNR + lane_off + half * 32, dv);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + b);
+        const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
+        // this key's columns of the step
+        uint32_t see = 0;
+        for (int j = 0; j < p.boxes; ++j) {
+          const int c0 = j * p.br - half * 32;
+          if (c0 >= 32 || c0 + p.br <= 0) continue;
+          const Box x = box[j];
+          if (!valid || !((x.mask >> blk) & 1)) continue;
+          // query t of the box sees positions below end + t
+          const int t0 = max(0, pos - x.end + 1);
+          const int lo = max(c0 + (t0 < p.bt ? t0 * p.bh : p.br), 0), hi = min(c0 + x.rows, 32);
+          if (hi > lo) see |= (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1) << lo);
+        }
+        if (gi >= NP) ok = ok && warp_wait(p_done + pb, ((gi / NP) - 1) & 1);
+        if (!ok) break;
+        // pairs that do not exist: zeros in Q and dO
+        for (int j = 0; j < p.boxes; ++j) {
+          const int n = box[j].rows;
+          if (n == p.br) continue;
+          for (int o = 0; o < 2 * KB; ++o) {
+            uint4* x = reinterpret_cast<uint4*>(sm + (o < KB ? M::Q : M::O) + si * QP +
+                                                (o % KB) * kQPiece + j * p.br * 128);
+            for (int i = n * 8 + threadIdx.x; i < p.br * 8; i += kKvWarps * 32)
+              x[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        const float4* stat = reinterpret_cast<const float4*>(sm + M::STAT + (si * kNR + half * 32) * 8);
+        uint8_t* pr = sm + M::P + pb * kPiece + r * 128;
+        uint8_t* dr = sm + M::DS + pb * kPiece + r * 128;
+        const bool full = __all_sync(0xffffffffu, see == 0xffffffffu);
+        const float2 qm = f2s(g.qmul);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t wp[4], wd[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = q * 8 + 2 * e;
+            const float4 a = stat[j / 2];  // (lse, Delta) of columns j, j + 1
+            const float2 z = f2fma(make_float2(sv[j], sv[j + 1]), qm, make_float2(-a.x, -a.z));
+            float2 y = make_float2(ex2(z.x), ex2(z.y));
+            float2 ds = f2mul(y, f2add(make_float2(dv[j], dv[j + 1]), make_float2(-a.y, -a.w)));
+            if (!full) {
+              const bool s0 = (see >> j) & 1u, s1 = (see >> (j + 1)) & 1u;
+              y.x = s0 ? y.x : 0.f;
+              y.y = s1 ? y.y : 0.f;
+              ds.x = s0 ? ds.x : 0.f;
+              ds.y = s1 ? ds.y : 0.f;
+            }
+            wp[e] = bf16x2_bits(y.x, y.y);
+            wd[e] = bf16x2_bits(ds.x, ds.y);
+          }
+          const int at = ((half * 4 + q) ^ (r & 7)) * 16;
+          *reinterpret_cast<uint4*>(pr + at) = make_uint4(wp[0], wp[1], wp[2], wp[3]);
+          *reinterpret_cast<uint4*>(dr + at) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + pb);
+      }
+      if (!ok) break;
+      const bool some = f.steps > 0;
+      if (some) {
+        ok = warp_wait(p_done + (gi - 1) % NP, ((gi - 1) / NP) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const int64_t krow = (int64_t(f.kbeg + r) * g.Hkv + f.kh) * g.D;
+#pragma unroll
+      for (int c = 0; c < 2 * DP / 64; ++c) {  // dV, then dK; DP / 2 columns each per half
+        const int which = c / (DP / 64);
+        const int col = half * (DP / 2) + (c % (DP / 64)) * 32;
+        float o[32];
+        __syncwarp();
+        if (some) {
+          tmem_ld32((which ? tK : tV) + lane_off + col, o);
+          tmem_wait_ld();
+        }
+        if (valid && f.slot < 0) {
+          const float mul = which ? g.scale : 1.f;
+          __nv_bfloat16* out =
+              static_cast<__nv_bfloat16*>(which ? p.b.dK : p.b.dV) + krow + col;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * mul : 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (col + q * 8 < g.D)
+              *reinterpret_cast<uint4*>(out + q * 8) = make_uint4(
+                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
+                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+        } else if (valid) {
+          float* out = p.b.part + (int64_t(f.slot) * 2 + (which ? 0 : 1)) * kT * g.D +
+                       int64_t(r) * g.D + col;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (col + q * 4 < g.D)
+              *reinterpret_cast<float4*>(out + q * 4) =
+                  make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (some) mbar_arrive(g_empty);
+        mbar_arrive(item_empty + slot);
+      }
+    }
+  }
+  if (!ok) atomicOr(&g_err, 2);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kKvWarps) tmem_free512(tmem);
+}
+
+gattn_status launch_block_bwd_tc(const BlockBwdParams& b, cudaStream_t st) {
+  const BlockGeom& g = b.g;
+  auto go = [&](auto kern, unsigned grid, int threads, int bytes, const auto& p) -> gattn_status {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) {
+      kern<<<grid, threads, bytes, st>>>(p);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+      set_error("gattn_block_bwd launch failed: %s", cudaGetErrorString(e));
+      return GATTN_ERR_CUDA;
+    }
+    return GATTN_OK;
+  };
+  const void *K = g.Nk ? b.K : b.Q, *V = g.Nk ? b.V : b.Q;  // never read when Nk is 0
+  const void *Q = g.Nq ? b.Q : b.K, *dO = g.Nq ? b.dO : b.K;
+  gattn_status s = GATTN_OK;
+  if (g.U > 0 && g.Nq > 0) {
+    DqParams p{};
+    p.b = b;
+    p.ht = tile_heads(g);
+    p.hs = g.G / p.ht;
+    p.rows = p.ht * g.qb;
+    p.n_tiles = int64_t(g.U) * g.Hkv * p.hs;
+    if (!encode_heads_map(&p.mq, Q, g.Nq, g.H, g.D, p.ht, g.qb) ||
+        !encode_heads_map(&p.mo, dO, g.Nq, g.H, g.D, p.ht, g.qb) ||
+        !encode_heads_map(&p.mk, K, g.Nk, g.Hkv, g.D, 1, g.block) ||
+        !encode_heads_map(&p.mv, V, g.Nk, g.Hkv, g.D, 1, g.block))
+      return GATTN_ERR_CUDA;
+    const unsigned grid = unsigned(std::min<int64_t>(p.n_tiles, sm_count()));
+    s = g.D <= 64 ? go(block_dq_tc<64>, grid, kDqThr, DqSm<64>::BYTES, p)
+                  : go(block_dq_tc<128>, grid, kDqThr, DqSm<128>::BYTES, p);
+    if (s != GATTN_OK) return s;
+  }
+  if (g.Nk > 0) {
+    DkvParams p{};
+    p.b = b;
+    p.bt = std::min(g.qb, kNR);
+    p.bh = std::min(g.G, kNR / p.bt);
+    p.br = p.bt * p.bh;
+    p.boxes = kNR / p.br;
+    p.ub = (g.qb / p.bt) * (g.G / p.bh);
+    if (!encode_heads_map(&p.mq, Q, g.Nq, g.H, g.D, p.bh, p.bt) ||
+        !encode_heads_map(&p.mo, dO, g.Nq, g.H, g.D, p.bh, p.bt) ||
+        !encode_heads_map(&p.mk, K, g.Nk, g.Hkv, g.D, 1, kT) ||
+        !encode_heads_map(&p.mv, V, g.Nk, g.Hkv, g.D, 1, kT))
+      return GATTN_ERR_CUDA;
+    const unsigned grid = unsigned(std::min<int64_t>(b.max_items, sm_count()));
+    s = g.D <= 64 ? go(block_dkv_tc<64>, grid, kKvThr, KvSm<64>::BYTES, p)
+                  : go(block_dkv_tc<128>, grid, kKvThr, KvSm<128>::BYTES, p);
+  }
+  return s;
+}
+
+cudaError_t block_bwd_tc_take_error(int* err) {
+  cudaError_t e = cudaMemcpyFromSymbol(err, g_err, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *err) e = cudaMemcpyToSymbol(g_err, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace gattn
