@@ -8,7 +8,9 @@ and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 import numpy as np
@@ -133,7 +135,7 @@ def load_library(path: str | None = None):
         lib.gattn_spmm_workspace_size.argtypes = [P, i32, ctypes.c_int, ctypes.POINTER(sz)]
         lib.gattn_spmm.argtypes = [P, i32, ctypes.c_int, P, P, P, i32, P, sz, P]
         lib.gattn_plan_set_wait_test.argtypes = [P, i32]
-        bd, nd, psz = ctypes.POINTER(_BlockDesc), ctypes.POINTER(_NormDesc), ctypes.POINTER(sz)
+        bd, nd, psz = P, P, ctypes.POINTER(sz)  # descriptors: packed bytes or byref
         lib.gattn_block_sums.argtypes = [bd, P, P, P, P]
         lib.gattn_block_select_workspace_size.argtypes = [bd, psz]
         lib.gattn_block_select.argtypes = [bd, P, P, P, P, sz, P]
@@ -551,92 +553,112 @@ def gattn_fwd_noalloc(plan: Plan, Q, K, V, score: Score, out, lse, stream=None):
 # ----------------------------------------------------------------------------
 # attention over selected blocks, and the gated residual norm
 # ----------------------------------------------------------------------------
-def _cuda(dtype, **tensors):
-    """Contiguous CUDA tensors of one device (None is skipped); returns the device."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor"
-                             + (f" of {dtype}" if dtype is not None else ""))
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
-        dev = t.device
-    return dev
+# These calls may take a few microseconds on the GPU (one new token), so their
+# marshalling is lean: descriptors are packed bytes, pointers plain integers,
+# and workspace sizes are kept by shape.
+_BLOCK_PACK = struct.Struct("@11ifi4xPPPqq")   # _BlockDesc
+_NORM_PACK = struct.Struct("@qiiiiffPPPP")     # _NormDesc
+assert _BLOCK_PACK.size == ctypes.sizeof(_BlockDesc)
+assert _NORM_PACK.size == ctypes.sizeof(_NormDesc)
+_sizes = {}
 
 
-def _same(shape, dtype, dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype
-                              or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)} on {dev}")
+def _want(name, t, shape, dtype, dev):
+    """Raise unless t is a contiguous tensor of this shape and dtype on device number dev."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor, {dtype}, of shape "
+                         f"{tuple(shape)}, on device {dev}")
 
 
-class _Launch:
-    """Current device and stream of one call; what the call allocates is tied to its stream."""
+def _cuda_index(name, t, dims):
+    """Device number of the tensor that a call's other tensors have to match."""
+    if not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor with {dims} dimensions, "
+                         f"has the shape {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Run:
+    """Stream of one call; what the call allocates on another stream than the current one is
+    tied to that stream.  The caller has made ``dev`` the current device."""
+    __slots__ = ("dev", "handle", "other")
 
     def __init__(self, dev, stream):
-        self._guard = torch.cuda.device(dev)
-        self.dev, self._given = dev, stream
-
-    def __enter__(self):
-        self._guard.__enter__()
-        self.current = torch.cuda.current_stream()
-        self.stream = self.current if self._given is None else self._given
-        if self.stream.device != self.dev:
-            self._guard.__exit__(None, None, None)
-            raise ValueError(f"stream of {self.stream.device} for tensors on {self.dev}")
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        self._guard.__exit__(*exc)
+        self.dev, self.other = dev, None
+        self.handle = torch._C._cuda_getCurrentRawStream(dev)
+        if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError(f"stream of {stream.device} for tensors on device {dev}")
+            if stream.cuda_stream != self.handle:
+                self.handle, self.other = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.stream != self.current:
-            t.record_stream(self.stream)
+        if self.other is not None:
+            t.record_stream(self.other)
         return t
 
-    def workspace(self, given, size_fn, desc):
-        """(pointer, bytes, keep-alive) of the caller's workspace, or of a new one."""
-        if given is None:
-            n = ctypes.c_size_t()
-            fn = getattr(load_library(), size_fn)
-            _check(fn(ctypes.byref(desc), ctypes.byref(n)), size_fn)
-            given = self.empty((max(n.value, 16),), torch.uint8)
-        elif not given.is_cuda or given.device != self.dev or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {self.dev}")
-        return _ptr(given), given.numel() * given.element_size(), given
+    def workspace(self, given, fn, desc, key):
+        """The caller's workspace, or a new one of the size that `fn` names (None for 0)."""
+        if given is not None:
+            if given.get_device() != self.dev or not given.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on device {self.dev}")
+            return given
+        n = _sizes.get((fn, self.dev, key))
+        if n is None:
+            size = ctypes.c_size_t()
+            _check(getattr(load_library(), fn)(desc, ctypes.byref(size)), fn)
+            n = size.value
+            if len(_sizes) > 4096:
+                _sizes.clear()
+            _sizes[(fn, self.dev, key)] = n
+        return self.empty((n,), torch.uint8) if n else None
 
 
-def _block_desc(Nq, Nk, H, Hkv, D, dtype, seq_q, seq_k, len_k, block, q_block=1, topk=1,
-                scale=0.0, causal=False, max_len_k=0):
-    seqs = {"seq_q": seq_q, "seq_k": seq_k, "len_k": len_k}
-    for name, t in seqs.items():
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
-                              or not t.is_cuda):
-            raise ValueError(f"{name} must be a contiguous one-dimensional int32 CUDA tensor")
+def _on_device(call):
+    """Run `call(dev, ...)` with its tensors' device as the current one."""
+    def wrapped(first, *args, **kw):
+        dev = first.get_device() if isinstance(first, torch.Tensor) else -1
+        if dev < 0 or dev == torch.cuda.current_device():
+            return call(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return call(first, *args, **kw)
+    return functools.wraps(call)(wrapped)
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _sequences(seq_q, seq_k, len_k, dev):
     S = seq_k.numel() - 1
-    if S < 0 or seq_q.numel() != S + 1 or (len_k is not None and len_k.numel() != S):
+    if S < 0:
         raise ValueError("seq_q and seq_k need S + 1 entries and len_k S")
-    return _BlockDesc(S, Nq, Nk, H, Hkv, D, _dtype_code(dtype), int(block), int(q_block),
-                      int(topk), int(bool(causal)), float(scale), int(max_len_k),
-                      seq_q.data_ptr(), seq_k.data_ptr(),
-                      len_k.data_ptr() if len_k is not None else None)
+    for name, t, n in (("seq_q", seq_q, S + 1), ("seq_k", seq_k, S + 1), ("len_k", len_k, S)):
+        if t is not None:
+            _want(name, t, (n,), torch.int32, dev)
+    return S
 
 
 def gattn_block_units(Nq: int, S: int, q_block: int) -> int:
     """Rows of idx: table rows of the query units of S sequences with Nq rows together."""
-    return Nq // q_block + (S if q_block > 1 else 0)
+    if q_block <= 0:
+        raise ValueError("q_block must be positive")
+    return (Nq // q_block + (S if q_block > 1 else 0)) if S else 0
 
 
 def gattn_block_count(Nk: int, S: int, block: int) -> int:
     """Rows of sums: table rows of the key blocks of S sequences with Nk rows together."""
-    return Nk // block + S
+    if block <= 0:
+        raise ValueError("block must be positive")
+    return (Nk // block + S) if S else 0
 
 
+@_on_device
 def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None, since=None,
                      sums=None, stream=None) -> torch.Tensor:
     """fp64 sums [blocks, Hkv, D] of the keys of each block (include/gattn.h).
@@ -644,23 +666,28 @@ def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None
     ``since`` (int32 [S]) renews only the blocks with positions from there on
     and needs ``sums``, the table to renew.
     """
-    if K.dim() != 3:
-        raise ValueError("K must have the shape [Nk, Hkv, D]")
+    dev = _cuda_index("K", K, 3)
     Nk, Hkv, D = K.shape
-    dev = _cuda(None, K=K, seq_k=seq_k, lens=lens, since=since, sums=sums)
-    desc = _block_desc(0, Nk, Hkv, Hkv, D, K.dtype, seq_k, seq_k, lens, block)
-    if since is not None and (sums is None or since.dtype != torch.int32
-                              or since.numel() != desc.S):
-        raise ValueError("since must be int32 [S] and needs sums")
-    shape = (gattn_block_count(Nk, desc.S, block) if desc.S else 0, Hkv, D)
-    _same(shape, torch.float64, dev, sums=sums)
-    with _Launch(dev, stream) as run:
-        out = run.empty(shape, torch.float64) if sums is None else sums
-        _check(load_library().gattn_block_sums(ctypes.byref(desc), _ptr(K), _ptr(since),
-                                               _ptr(out), run.handle), "gattn_block_sums")
-    return out
+    S = _sequences(seq_k, seq_k, lens, dev)
+    if since is not None:
+        _want("since", since, (S,), torch.int32, dev)
+        if sums is None:
+            raise ValueError("since needs sums, the table to renew")
+    shape = (gattn_block_count(Nk, S, block), Hkv, D)
+    run = _Run(dev, stream)
+    if sums is None:
+        sums = run.empty(shape, torch.float64)
+    else:
+        _want("sums", sums, shape, torch.float64, dev)
+    desc = _BLOCK_PACK.pack(S, 0, Nk, Hkv, Hkv, D, _dtype_code(K.dtype), block, 1, 1, 0, 0.0, 0,
+                            seq_k.data_ptr(), seq_k.data_ptr(), _at(lens) or 0, 0, 0)
+    _check((_lib or load_library()).gattn_block_sums(desc, K.data_ptr(), _at(since),
+                                                     sums.data_ptr(), run.handle),
+           "gattn_block_sums")
+    return sums
 
 
+@_on_device
 def gattn_block_select(Q: torch.Tensor, sums: torch.Tensor, seq_q: torch.Tensor,
                        seq_k: torch.Tensor, topk: int, block: int, q_block: int, nk: int,
                        len_k=None, causal: bool = False, max_len_k: int = 0, idx=None,
@@ -670,47 +697,53 @@ def gattn_block_select(Q: torch.Tensor, sums: torch.Tensor, seq_q: torch.Tensor,
     ``nk`` is the number of key rows that ``sums`` was built from and
     ``max_len_k`` the most keys of one sequence (0: nk).
     """
-    if Q.dim() != 3 or sums.dim() != 3:
-        raise ValueError("Q must have the shape [Nq, H, D] and sums [blocks, Hkv, D]")
+    dev = _cuda_index("Q", Q, 3)
     Nq, H, D = Q.shape
-    Hkv = sums.shape[1]
-    dev = _cuda(None, Q=Q, sums=sums, seq_q=seq_q, seq_k=seq_k, len_k=len_k, idx=idx)
-    desc = _block_desc(Nq, nk, H, Hkv, D, Q.dtype, seq_q, seq_k, len_k, block, q_block, topk,
-                       0.0, causal, max_len_k)
-    _same((gattn_block_count(nk, desc.S, block) if desc.S else 0, Hkv, D), torch.float64, dev,
-          sums=sums)
-    shape = (gattn_block_units(Nq, desc.S, q_block) if desc.S else 0, Hkv, topk)
-    _same(shape, torch.int32, dev, idx=idx)
-    with _Launch(dev, stream) as run:
-        out = run.empty(shape, torch.int32) if idx is None else idx
-        ws, n, _keep = run.workspace(workspace, "gattn_block_select_workspace_size", desc)
-        _check(load_library().gattn_block_select(ctypes.byref(desc), _ptr(Q), _ptr(sums),
-                                                 _ptr(out), ws, n, run.handle),
-               "gattn_block_select")
-    return out
+    Hkv = sums.shape[1] if sums.dim() == 3 else 0
+    S = _sequences(seq_q, seq_k, len_k, dev)
+    _want("sums", sums, (gattn_block_count(nk, S, block), Hkv, D), torch.float64, dev)
+    shape = (gattn_block_units(Nq, S, q_block), Hkv, topk)
+    run = _Run(dev, stream)
+    if idx is None:
+        idx = run.empty(shape, torch.int32)
+    else:
+        _want("idx", idx, shape, torch.int32, dev)
+    desc = _BLOCK_PACK.pack(S, Nq, nk, H, Hkv, D, _dtype_code(Q.dtype), block, q_block, topk,
+                            1 if causal else 0, 0.0, max_len_k, seq_q.data_ptr(),
+                            seq_k.data_ptr(), _at(len_k) or 0, 0, 0)
+    ws = run.workspace(workspace, "gattn_block_select_workspace_size", desc,
+                       (S, Nq, nk, H, Hkv, D, Q.dtype, block, q_block, topk))
+    _check((_lib or load_library()).gattn_block_select(desc, Q.data_ptr(), sums.data_ptr(),
+                                                       idx.data_ptr(), _at(ws), _bytes(ws),
+                                                       run.handle), "gattn_block_select")
+    return idx
 
 
-def _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k, **more):
-    if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape or idx.dim() != 3:
+def _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k):
+    """Checks of the forward and backward: (device, descriptor, key of their workspaces)."""
+    dev = _cuda_index("Q", Q, 3)
+    Nq, H, D = Q.shape
+    if K.dim() != 3 or idx.dim() != 3:
         raise ValueError("need Q [Nq, H, D], K and V [Nk, Hkv, D] and idx [units, Hkv, topk]")
-    Nq, H, D = Q.shape
     Nk, Hkv, _ = K.shape
-    dev = _cuda(None, Q=Q, K=K, V=V, seq_q=seq_q, seq_k=seq_k, len_k=len_k, **more)
-    _same((Nk, Hkv, D), Q.dtype, dev, K=K, V=V)
-    desc = _block_desc(Nq, Nk, H, Hkv, D, Q.dtype, seq_q, seq_k, len_k, block, q_block,
-                       idx.shape[2], scale, causal)
-    units = gattn_block_units(Nq, desc.S, q_block) if desc.S else 0
-    if (idx.device != dev or idx.dtype != torch.int32 or tuple(idx.shape[:2]) != (units, Hkv)
-            or (idx.shape[2] > 1 and idx.stride(2) != 1)):
-        raise ValueError(f"idx must be int32 of shape ({units}, {Hkv}, topk) on {dev}, each list "
-                         "contiguous")
-    su, sh = idx.stride()[:2]
+    _want("K", K, (Nk, Hkv, D), Q.dtype, dev)
+    _want("V", V, (Nk, Hkv, D), Q.dtype, dev)
+    S = _sequences(seq_q, seq_k, len_k, dev)
+    units, topk = gattn_block_units(Nq, S, q_block), idx.shape[2]
+    su, sh, sl = idx.stride()
+    if (idx.get_device() != dev or idx.dtype != torch.int32 or idx.shape[0] != units
+            or idx.shape[1] != Hkv or (topk > 1 and sl != 1)):
+        raise ValueError(f"idx must be int32 of shape ({units}, {Hkv}, topk) on device {dev}, "
+                         "each list contiguous")
     if su == 0 and sh == 0 and units * Hkv > 1:
         raise ValueError("idx repeats one list for all units and heads; make it contiguous")
-    desc.idx_stride[0], desc.idx_stride[1] = su, sh
-    return desc, dev
+    desc = _BLOCK_PACK.pack(S, Nq, Nk, H, Hkv, D, _dtype_code(Q.dtype), block, q_block, topk,
+                            1 if causal else 0, scale, 0, seq_q.data_ptr(), seq_k.data_ptr(),
+                            _at(len_k) or 0, su, sh)
+    return dev, desc, (S, Nq, Nk, H, Hkv, D, Q.dtype, block, q_block, topk)
 
 
+@_on_device
 def gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block: int, q_block: int, scale: float = 0.0,
                     causal: bool = False, len_k=None, out=None, lse=None, workspace=None,
                     stream=None):
@@ -719,37 +752,46 @@ def gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block: int, q_block: int, scale:
     Rows of no sequence are not written; tensors that the call allocates hold
     anything there.
     """
-    desc, dev = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
-    _same(Q.shape, Q.dtype, dev, out=out)
-    _same(Q.shape[:2], torch.float32, dev, lse=lse)
-    with _Launch(dev, stream) as run:
-        out = run.empty(Q.shape, Q.dtype) if out is None else out
-        lse = run.empty(Q.shape[:2], torch.float32) if lse is None else lse
-        ws, n, _keep = run.workspace(workspace, "gattn_block_fwd_workspace_size", desc)
-        _check(load_library().gattn_block_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V),
-                                              _ptr(idx), _ptr(out), _ptr(lse), ws, n, run.handle),
-               "gattn_block_fwd")
+    dev, desc, key = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
+    run = _Run(dev, stream)
+    if out is None:
+        out = run.empty(Q.shape, Q.dtype)
+    else:
+        _want("out", out, Q.shape, Q.dtype, dev)
+    if lse is None:
+        lse = run.empty(Q.shape[:2], torch.float32)
+    else:
+        _want("lse", lse, Q.shape[:2], torch.float32, dev)
+    ws = run.workspace(workspace, "gattn_block_fwd_workspace_size", desc, key)
+    _check((_lib or load_library()).gattn_block_fwd(
+        desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), _at(ws), _bytes(ws), run.handle), "gattn_block_fwd")
     return out, lse
 
 
+@_on_device
 def gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout, lse, block: int, q_block: int,
                     scale: float = 0.0, causal: bool = False, len_k=None, dQ=None, dK=None,
                     dV=None, workspace=None, stream=None):
     """Gradients (dQ, dK, dV) of gattn_block_fwd; rows of no sequence are not written."""
-    desc, dev = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
-    _same(Q.shape, Q.dtype, dev, out=out, dout=dout, dQ=dQ)
-    _same(Q.shape[:2], torch.float32, dev, lse=lse)
-    _same(K.shape, Q.dtype, dev, dK=dK, dV=dV)
-    with _Launch(dev, stream) as run:
-        dQ = run.empty(Q.shape, Q.dtype) if dQ is None else dQ
-        dK = run.empty(K.shape, K.dtype) if dK is None else dK
-        dV = run.empty(K.shape, K.dtype) if dV is None else dV
-        ws, n, _keep = run.workspace(workspace, "gattn_block_bwd_workspace_size", desc)
-        _check(load_library().gattn_block_bwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V),
-                                              _ptr(idx), _ptr(out), _ptr(dout), _ptr(lse),
-                                              _ptr(dQ), _ptr(dK), _ptr(dV), ws, n, run.handle),
-               "gattn_block_bwd")
-    return dQ, dK, dV
+    dev, desc, key = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
+    _want("out", out, Q.shape, Q.dtype, dev)
+    _want("dout", dout, Q.shape, Q.dtype, dev)
+    _want("lse", lse, Q.shape[:2], torch.float32, dev)
+    run = _Run(dev, stream)
+    grads = []
+    for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
+        if t is None:
+            t = run.empty(like.shape, like.dtype)
+        else:
+            _want(name, t, like.shape, like.dtype, dev)
+        grads.append(t)
+    ws = run.workspace(workspace, "gattn_block_bwd_workspace_size", desc, key)
+    _check((_lib or load_library()).gattn_block_bwd(
+        desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(), out.data_ptr(),
+        dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
+        grads[2].data_ptr(), _at(ws), _bytes(ws), run.handle), "gattn_block_bwd")
+    return tuple(grads)
 
 
 def gattn_block_check_errors() -> None:
@@ -760,23 +802,26 @@ def gattn_block_check_errors() -> None:
 NORM = {"rms": 0, "layer": 1}
 
 
-def _norm_desc(ref, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps, dev):
-    if ref.dim() != 2:
-        raise ValueError("rows must be a tensor [N, F]")
+def _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps):
+    """Checks of the norm's forward and backward: (device, descriptor, N, F)."""
+    dev = _cuda_index("res", res, 2)
     if kind not in NORM:
         raise ValueError(f"unknown norm kind {kind!r}")
-    N, F = ref.shape
+    N, F = res.shape
     mode = 0
     if gate is not None:
         mode = 1 if gate.dim() == 1 else 2
-        _same((F,) if mode == 1 else (N, F), torch.float32 if mode == 1 else ref.dtype, dev,
-              gate=gate)
-    _same((F,), torch.float32, dev, w_post=w_post, b_post=b_post, w_pre=w_pre, b_pre=b_pre)
-    ptr = [t.data_ptr() if t is not None else None for t in (w_post, b_post, w_pre, b_pre)]
-    return _NormDesc(N, F, _dtype_code(ref.dtype), NORM[kind], mode, float(alpha), float(eps),
-                     *ptr)
+        _want("gate", gate, (F,) if mode == 1 else (N, F),
+              torch.float32 if mode == 1 else res.dtype, dev)
+    for name, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
+        if t is not None:
+            _want(name, t, (F,), torch.float32, dev)
+    desc = _NORM_PACK.pack(N, F, _dtype_code(res.dtype), NORM[kind], mode, alpha, eps,
+                           _at(w_post) or 0, _at(b_post) or 0, _at(w_pre) or 0, _at(b_pre) or 0)
+    return dev, desc, N, F
 
 
+@_on_device
 def gattn_norm_fwd(res, x=None, gate=None, w_post=None, b_post=None, w_pre=None, b_pre=None,
                    alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6, h=None, y=None,
                    stats=None, stream=None):
@@ -787,27 +832,30 @@ def gattn_norm_fwd(res, x=None, gate=None, w_post=None, b_post=None, w_pre=None,
     without w_pre the second (y is None), without x h is res itself.  Returns
     (h, y, stats); stats (fp32 [N, 4]) goes to gattn_norm_bwd.
     """
-    dev = _cuda(None, res=res, x=x, gate=gate, w_post=w_post, b_post=b_post, w_pre=w_pre,
-                b_pre=b_pre)
-    desc = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps, dev)
-    _same(res.shape, res.dtype, dev, x=x, h=h, y=y)
-    _same((res.shape[0], 4), torch.float32, dev, stats=stats)
-    with _Launch(dev, stream) as run:
-        if x is None:
-            h = res
-        elif h is None:
-            h = run.empty(res.shape, res.dtype)
-        if w_pre is None:
-            y = None
-        elif y is None:
-            y = run.empty(res.shape, res.dtype)
-        stats = run.empty((res.shape[0], 4), torch.float32) if stats is None else stats
-        _check(load_library().gattn_norm_fwd(ctypes.byref(desc), _ptr(res), _ptr(x), _ptr(gate),
-                                             _ptr(h) if x is not None else None, _ptr(y),
-                                             _ptr(stats), run.handle), "gattn_norm_fwd")
+    dev, desc, N, F = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps)
+    run = _Run(dev, stream)
+    for name, t in (("x", x), ("h", h), ("y", y)):
+        if t is not None:
+            _want(name, t, (N, F), res.dtype, dev)
+    if x is None:
+        h = res
+    elif h is None:
+        h = run.empty((N, F), res.dtype)
+    if w_pre is None:
+        y = None
+    elif y is None:
+        y = run.empty((N, F), res.dtype)
+    if stats is None:
+        stats = run.empty((N, 4), torch.float32)
+    else:
+        _want("stats", stats, (N, 4), torch.float32, dev)
+    _check((_lib or load_library()).gattn_norm_fwd(
+        desc, res.data_ptr(), _at(x), _at(gate), None if x is None else h.data_ptr(), _at(y),
+        stats.data_ptr(), run.handle), "gattn_norm_fwd")
     return h, y, stats
 
 
+@_on_device
 def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None, b_post=None,
                    w_pre=None, b_pre=None, alpha: float = 1.0, kind: str = "rms",
                    workspace=None, stream=None) -> dict:
@@ -817,24 +865,19 @@ def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None,
     Returns a dict of dres, dx, dgate, dw_post, db_post, dw_pre, db_pre; None
     where the operand is absent.
     """
-    dev = _cuda(None, res=res, stats=stats, dh=dh, dy=dy, x=x, gate=gate, w_post=w_post,
-                b_post=b_post, w_pre=w_pre, b_pre=b_pre)
-    desc = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, 0.0, dev)
-    _same(res.shape, res.dtype, dev, dh=dh, dy=dy, x=x)
-    _same((res.shape[0], 4), torch.float32, dev, stats=stats)
-    F = res.shape[1]
-    with _Launch(dev, stream) as run:
-        def like(t, shape, dtype):
-            return None if t is None else run.empty(shape, dtype)
-
-        g = {"dres": run.empty(res.shape, res.dtype), "dx": like(x, res.shape, res.dtype),
-             "dgate": None if gate is None else run.empty(gate.shape, gate.dtype)}
-        for n, t in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre),
-                     ("db_pre", b_pre)):
-            g[n] = like(t, (F,), torch.float32)
-        ws, n, _keep = run.workspace(workspace, "gattn_norm_workspace_size", desc)
-        _check(load_library().gattn_norm_bwd(ctypes.byref(desc), _ptr(res), _ptr(stats), _ptr(dh),
-                                             _ptr(dy), _ptr(x), _ptr(gate),
-                                             *[_ptr(t) for t in g.values()], ws, n, run.handle),
-               "gattn_norm_bwd")
+    dev, desc, N, F = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, 0.0)
+    for name, t in (("dh", dh), ("dy", dy), ("x", x)):
+        if t is not None:
+            _want(name, t, (N, F), res.dtype, dev)
+    _want("stats", stats, (N, 4), torch.float32, dev)
+    run = _Run(dev, stream)
+    g = {"dres": run.empty((N, F), res.dtype),
+         "dx": None if x is None else run.empty((N, F), res.dtype),
+         "dgate": None if gate is None else run.empty(gate.shape, gate.dtype)}
+    for n, t in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre), ("db_pre", b_pre)):
+        g[n] = None if t is None else run.empty((F,), torch.float32)
+    ws = run.workspace(workspace, "gattn_norm_workspace_size", desc, (N, F, res.dtype))
+    _check((_lib or load_library()).gattn_norm_bwd(
+        desc, res.data_ptr(), stats.data_ptr(), _at(dh), _at(dy), _at(x), _at(gate),
+        *[_at(t) for t in g.values()], _at(ws), _bytes(ws), run.handle), "gattn_norm_bwd")
     return g

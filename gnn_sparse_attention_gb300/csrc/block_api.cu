@@ -289,13 +289,25 @@ __global__ void __launch_bounds__(256) join_kv_kernel(const BlockBwdParams p) {
   const int pos = (kt - piece_base(g.seq_k, s, kBlkTile)) * kBlkTile;
   const int n = (c + p.chunk - 1) / p.chunk;
   const float* part = p.part + int64_t(p.cnt[2 * i + 1]) * 2 * kBlkTile * D;
-  for (int e = threadIdx.x + blockIdx.y * 256; e < 2 * kBlkTile * D; e += 256 * gridDim.y) {
+  for (int e = (threadIdx.x + blockIdx.y * 256) * 4; e < 2 * kBlkTile * D;
+       e += 1024 * gridDim.y) {
     const int which = e / (kBlkTile * D), r = (e / D) % kBlkTile, d = e % D;
     if (pos + r >= ks.len) continue;
-    float t = 0.f;
-    for (int k = 0; k < n; ++k) t += part[int64_t(k) * 2 * kBlkTile * D + e];
-    const int64_t at = (int64_t(ks.beg + pos + r) * g.Hkv + kh) * D + d;
-    static_cast<T*>(which ? p.dV : p.dK)[at] = T(which ? t : t * g.scale);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(part + int64_t(k) * 2 * kBlkTile * D + e);
+      t.x += x.x;
+      t.y += x.y;
+      t.z += x.z;
+      t.w += x.w;
+    }
+    const float mul = which ? 1.f : g.scale;
+    T* out = static_cast<T*>(which ? p.dV : p.dK) + (int64_t(ks.beg + pos + r) * g.Hkv + kh) * D + d;
+    out[0] = T(t.x * mul);
+    out[1] = T(t.y * mul);
+    out[2] = T(t.z * mul);
+    out[3] = T(t.w * mul);
   }
 }
 
@@ -461,8 +473,11 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
       (s = dt == GATTN_F32 ? launch_block_bwd_simt(p, dt, st) : launch_block_bwd_tc(p, st)) !=
           GATTN_OK)
     return s;
-  if (dt == GATTN_F32) join_kv_kernel<float><<<g.KT * g.Hkv, 256, 0, st>>>(p);
-  else join_kv_kernel<__nv_bfloat16><<<g.KT * g.Hkv, 256, 0, st>>>(p);
+  // a key tile that most units chose may have a hundred partials: its elements
+  // are spread over several CTAs
+  const dim3 grid(g.KT * g.Hkv, std::max(1, kBlkTile * g.D * 2 / 1024));
+  if (dt == GATTN_F32) join_kv_kernel<float><<<grid, 256, 0, st>>>(p);
+  else join_kv_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
   return launched("gattn_block_bwd (join)");
 }
 

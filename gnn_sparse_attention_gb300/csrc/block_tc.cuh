@@ -14,6 +14,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Whether the phase of this parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait of a whole warp: the same answer in every lane, so that a wait
 // that gives up takes the warp out of its loop together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
@@ -61,6 +73,24 @@ __device__ __forceinline__ void mma_km(uint32_t d, const uint8_t* a, int a_piece
   for (int k = 0; k < K / 16; ++k)
     mma_bf16(d, sw128_desc(smem_u32(a + (k / 4) * a_piece) + (k % 4) * 32, 16, 1024),
              sw128_desc(smem_u32(b) + k * 2048, b_piece, 1024), idesc, (add || k > 0) ? 1u : 0u);
+}
+
+// The same with A in TMEM: lane r holds row r, a 32-bit column two consecutive
+// bf16 of K.  The K columns sit in groups of `group` bf16, `stride` TMEM columns
+// apart (a thread overwrites the scores that it has read).
+template <int K>
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, int group, int stride,
+                                       const uint8_t* b, int b_piece, uint32_t idesc, bool add) {
+#pragma unroll
+  for (int k = 0; k < K / 16; ++k) {
+    const uint32_t at = a + (k * 16 / group) * stride + (k * 16 % group) / 2;
+    const uint64_t bd = sw128_desc(smem_u32(b) + k * 2048, b_piece, 1024);
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(at), "l"(bd), "r"(idesc), "r"((add || k > 0) ? 1u : 0u)
+        : "memory");
+  }
 }
 
 }  // namespace tc

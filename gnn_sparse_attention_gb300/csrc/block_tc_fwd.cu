@@ -4,21 +4,24 @@
 // A tile is up to 128 (query row, head) pairs of one unit and key head: they
 // share the unit's block list.  A step is 128 keys, i.e. 128 / block blocks
 // of the list, each fetched by a TMA box of its own rows:
-//   S = Q K^T  (128 x 128 x D)      -> TMEM, two buffers
-//   p = 2^(s - m) as bf16           -> shared memory, two buffers
-//   O += P V   (128 x D x 128)      -> TMEM, two buffers (tiles in turn)
-// Roles: warps 0-7 softmax (thread = row and half of its 128 columns), warp 8
-// issues the products, warp 9 resolves block lists and issues TMA.  S of
-// step i + 1 runs while the softmax works on step i, and a tile's first
-// steps run while the tile before it is written out; every hand-over is an
-// mbarrier, every wait is bounded.
+//   S = Q K^T  (128 x 128 x D)      -> TMEM
+//   p = 2^(s - m) as bf16           -> TMEM, over the scores it came from
+//   O += P V   (128 x D x 128)      -> TMEM, P as the left operand
+// A softmax step is a chain of latencies (TMEM, maximum, exponentials, TMEM)
+// two to three times as long as the step's products, so two streams take the
+// steps in turn: each has its own 128 threads (thread = row), score buffer,
+// running maximum and sum, and output; they are merged when the tile is
+// written.  While one stream is in its softmax, the tensor core runs the other's
+// P V and next scores.  P in TMEM instead of shared memory takes 64 KB of the
+// step's 160 KB of shared-memory traffic away (128 bytes a clock would
+// otherwise be the bound at D = 128) and leaves room for a third stage.
+// Roles: warps 0-7 softmax, warp 8 issues the products, warp 9 resolves block
+// lists and issues TMA; every hand-over is an mbarrier, every wait is bounded.
 //
 // With the list ascending, the keys that a row sees are the first columns of
 // its steps (list_keys), so the mask is one number per row and only the
-// steps around it compare.  The running maximum is exchanged between the two
-// halves of a row rounded up to bf16: it is a scale, any value at least as
-// large serves, and both halves use the same.  O is rescaled only when the
-// maximum grew by more than 2^8 (p stays below 2^8, far from overflow).
+// steps around it compare.  O is rescaled only when the maximum grew by more
+// than 2^8 (p stays below 2^8, far from overflow).
 //
 // Rows of V that no row may see (behind the sequence's end, or of no block)
 // are zeroed in shared memory, because 0 * NaN is NaN in the product.  Under
@@ -42,7 +45,7 @@ __device__ int g_err;  // a bounded wait gave up
 
 constexpr int kT = kBlkTile;
 constexpr int kPiece = kT * 128;       // 128 rows x 64 bf16 columns
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 8;           // two streams of four
 constexpr int kThr = (kSoftWarps + 2) * 32;
 
 struct TcFwdParams {
@@ -75,26 +78,24 @@ template <int DP>
 struct Sm {
   static constexpr int KB = DP / 64;
   static constexpr int NQ = DP == 64 ? 2 : 1;   // Q buffers
-  static constexpr int NS = DP == 64 ? 3 : 2;   // K and V stages
+  static constexpr int NS = DP == 64 ? 4 : 3;   // K and V stages
+  static constexpr int NO = DP == 64 ? 2 : 1;   // output buffers of a stream (tiles in turn)
   static constexpr int OP = KB * kPiece;         // one operand tile
   static constexpr int Q = 0;
   static constexpr int K = Q + NQ * OP;
   static constexpr int V = K + NS * OP;
-  static constexpr int P = V + NS * OP;
-  static constexpr int RED = P + 2 * 2 * kPiece;  // [2][256] bf16 maxima, or [256] fp32 sums
+  static constexpr int RED = V + NS * OP;        // [2 streams][128] fp32
   static constexpr int IDS = RED + 1024;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(TileInfo));
-  static constexpr int NBAR = 2 + 2 + 2 * NQ + 4 * NS + 2 + 2 + 2 + 2 + 2 + 4;
+  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 6 + NO + 4;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024 <= 227 * 1024 ? END + 1024 : 227 * 1024;
   static_assert(END <= 227 * 1024, "shared memory of one CTA");
+  // TMEM: scores of the streams [0, 256), outputs from 256 on
+  static constexpr int out_col(int stream, int buf) { return 2 * kT + (buf * 2 + stream) * DP; }
+  static_assert(out_col(1, NO - 1) + DP <= 512, "TMEM columns");
 };
-
-__device__ __forceinline__ uint32_t bf16_up(float x) {  // bf16 bits of x rounded towards +inf
-  const uint32_t b = __float_as_uint(x);
-  return ((int32_t(b) >= 0 && b < 0x7f800000u ? b + 0xffffu : b) >> 16);
-}
 
 }  // namespace
 
@@ -102,7 +103,7 @@ template <int DP>
 __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ TcFwdParams p) {
   using namespace tc;
   using M = Sm<DP>;
-  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, OP = M::OP;
+  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, NO = M::NO, OP = M::OP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
   if (pad + M::END > M::BYTES) {  // the swizzled tiles need a 1024-byte aligned base
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
   uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
            *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
            *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
-           *s_empty = s_full + 2, *p_full = s_empty + 2, *pv_done = p_full + 2,
-           *o_empty = pv_done + 2, *pair = o_empty + 2;
+           *p_full = s_full + 2, *pv_done = p_full + 2, *o_empty = pv_done + 2,
+           *pair = o_empty + NO;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   TileInfo* info = reinterpret_cast<TileInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
@@ -127,11 +128,10 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       mbar_init(tile_full + i, 1);
       mbar_init(tile_empty + i, kSoftWarps + 1);
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, kSoftWarps);
-      mbar_init(p_full + i, kSoftWarps);
+      mbar_init(p_full + i, kSoftWarps / 2);
       mbar_init(pv_done + i, 1);
-      mbar_init(o_empty + i, kSoftWarps);
     }
+    for (int i = 0; i < NO; ++i) mbar_init(o_empty + i, kSoftWarps);
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t tS = tmem, tO = tmem + 2 * kT;
   bool ok = true;  // false: a wait gave up, leave
 
   if (warp == kSoftWarps + 1) {
@@ -243,74 +242,86 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     // ---------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_O = f16_idesc(kT, DP, true);
+      // Step gi belongs to stream gi & 1.  Its scores are issued after the P V
+      // of step gi - 2 (products run in the order of their issue), so the
+      // stream's P is no longer needed when they overwrite it.
+      struct Due {
+        int gi, tile;     // gi < 0: none
+        bool first, head;  // first of the stream in its tile, of the tile
+      } due[2] = {{-1, 0, false, false}, {-1, 0, false, false}};
       int gi = 0, ti = 0, tq = 0;
-      int pi = -1, po = 0;  // the step whose P V is due, its O buffer's tile count
-      bool pfirst = false;
-      auto product_pv = [&]() {
-        const int ks_i = pi % NS, b = pi & 1;
-        ok = ok && mbar_wait(p_full + b, (pi >> 1) & 1) && mbar_wait(v_full + ks_i, (pi / NS) & 1);
-        if (pfirst && po >= 2) ok = ok && mbar_wait(o_empty + (po & 1), ((po >> 1) - 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        mma_km<kT>(tO + (po & 1) * DP, sm + M::P + b * 2 * kPiece, kPiece,
-                   sm + M::V + ks_i * OP, kPiece, IDESC_O, !pfirst);
-        mma_commit(pv_done + b);
-        mma_commit(v_empty + ks_i);
+      auto product_pv = [&](Due& d) {
+        if (d.gi < 0) return;
+        const int si = d.gi % NS, x = d.gi & 1, buf = d.tile % NO;
+        ok = ok && mbar_wait(p_full + x, (d.gi >> 1) & 1) &&
+             mbar_wait(v_full + si, (d.gi / NS) & 1);
+        if (d.head && d.tile >= NO) ok = ok && mbar_wait(o_empty + buf, (d.tile / NO - 1) & 1);
+        if (ok) {
+          tc_fence_after();
+          mma_tm<kT>(tmem + M::out_col(x, buf), tmem + x * kT, 64, 64, sm + M::V + si * OP, kPiece,
+                     IDESC_O, !d.first);
+          mma_commit(pv_done + x);
+          mma_commit(v_empty + si);
+        }
+        d.gi = -1;
+      };
+      auto drain = [&]() {
+        product_pv(due[gi & 1]);
+        product_pv(due[(gi & 1) ^ 1]);
       };
       for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
         const int slot = ti & 1;
-        ok = mbar_wait(tile_full + slot, (ti >> 1) & 1);
+        if (!mbar_test(tile_full + slot, (ti >> 1) & 1)) {
+          drain();  // the producer may wait for the tiles that these belong to
+          ok = ok && mbar_wait(tile_full + slot, (ti >> 1) & 1);
+        }
         if (!ok) break;
         const int n = info[slot].s1 - info[slot].s0;
         mbar_arrive(tile_empty + slot);
-        if (n <= 0) {  // the softmax may wait for the last product before it moves on
-          if (pi >= 0) product_pv();
-          pi = -1;
-          continue;
-        }
+        if (n <= 0) continue;
         const int qs = tq % NQ;
         ok = mbar_wait(q_full + qs, (tq / NQ) & 1);
         for (int i = 0; i < n && ok; ++i, ++gi) {
-          const int ks_i = gi % NS, b = gi & 1;
-          ok = mbar_wait(k_full + ks_i, (gi / NS) & 1);
-          if (gi >= 2) ok = ok && mbar_wait(s_empty + b, ((gi >> 1) - 1) & 1);
+          const int si = gi % NS, x = gi & 1;
+          product_pv(due[x]);
+          ok = ok && mbar_wait(k_full + si, (gi / NS) & 1);
           if (!ok) break;
           tc_fence_after();
-          mma_kk<KB>(tS + b * kT, sm + M::Q + qs * OP, kPiece, sm + M::K + ks_i * OP, kPiece,
+          mma_kk<KB>(tmem + x * kT, sm + M::Q + qs * OP, kPiece, sm + M::K + si * OP, kPiece,
                      IDESC_S);
-          mma_commit(s_full + b);
-          mma_commit(k_empty + ks_i);
+          mma_commit(s_full + x);
+          mma_commit(k_empty + si);
           if (i == n - 1) mma_commit(q_empty + qs);
-          if (pi >= 0) product_pv();
-          pi = gi;
-          po = tq;
-          pfirst = i == 0;
+          due[x] = Due{gi, tq, i < 2, i == 0};
         }
         ++tq;
       }
-      if (ok && pi >= 0) product_pv();
+      if (ok) drain();
       // every product has completed before TMEM is given up
-      if (ok && gi > 0) ok = mbar_wait(pv_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
-      if (!ok && gi > 0) {
-        mbar_wait(s_full + ((gi - 1) & 1), ((gi - 1) >> 1) & 1, 200);
-        if (pi >= 0) mbar_wait(pv_done + (pi & 1), (pi >> 1) & 1, 200);
+      for (int k = 1; k <= 2 && k <= gi; ++k) {
+        const int c = gi - k;
+        if (ok) ok = mbar_wait(pv_done + (c & 1), (c >> 1) & 1);
+        if (!ok) {
+          mbar_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+          mbar_wait(pv_done + (c & 1), (c >> 1) & 1, 200);
+        }
       }
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax
-    const int r = (warp & 3) * 32 + lane, half = warp >> 2;
-    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    uint16_t* red = reinterpret_cast<uint16_t*>(sm + M::RED);
-    float* redf = reinterpret_cast<float*>(sm + M::RED);
-    int gi = 0, ti = 0, to = 0, xc = 0;  // steps, tiles, tiles with steps, exchanges
+    const int quad = warp & 3, x = warp >> 2;  // TMEM lane quarter, stream
+    const int r = quad * 32 + lane;
+    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    const uint32_t tS = tmem + lanes + x * kT;
+    float* red = reinterpret_cast<float*>(sm + M::RED);
+    int gi = 0, ti = 0, to = 0;  // steps, tiles, tiles with steps
     const int th = r % p.ht, tt = r / p.ht;
-    // the two warps of a row have written; both may read
-    auto meet = [&]() {
+    // the two warps of these rows (one per stream) have written; both may read
+    auto meet = [&](int phase) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair + (warp & 3));
-      ok = ok && warp_wait(pair + (warp & 3), xc & 1);
-      ++xc;
+      if (lane == 0) mbar_arrive(pair + quad);
+      ok = ok && warp_wait(pair + quad, phase);
     };
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
@@ -322,62 +333,55 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       const int lim = !valid ? 0
                       : g.causal ? list_keys(list, f.n, g.block, min(f.pos + tt + 1, f.len))
                                  : f.total;
+      const int buf = to % NO, steps = f.s1 - f.s0;
+      const int head = (gi ^ x) & 1;  // the stream's first step of the tile
       float m = neg_inf(), l = 0.f;
-      for (int st = f.s0; st < f.s1; ++st, ++gi) {
-        const int b = gi & 1, ks_i = gi % NS;
-        ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
+      for (int i = head; i < steps; i += 2) {
+        const int c = gi + i, st = f.s0 + i, si = c % NS;
+        ok = ok && warp_wait(s_full + x, (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
+        const int mine = lim - st * kT;  // columns of the step that the row sees
+        const bool cut = __any_sync(0xffffffffu, mine < kT);
+        // the maximum over columns [0, 64), then [64, 128), which stay in registers
         float sv[64];
-        tmem_ld32(tS + b * kT + lane_off + half * 64, sv);
-        tmem_ld32(tS + b * kT + lane_off + half * 64 + 32, sv + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + b);
-        const int mine = lim - st * kT - half * 64;  // columns of this half the row sees
-        if (__any_sync(0xffffffffu, mine < 64)) {
+        float c0 = neg_inf(), c1 = c0, c2 = c0, c3 = c0;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = j < mine ? sv[j] : neg_inf();
-        }
-        float c0 = sv[0], c1 = sv[1], c2 = sv[2], c3 = sv[3];
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld32(tS + h * 64, sv);
+          tmem_ld32(tS + h * 64 + 32, sv + 32);
+          tmem_wait_ld();
+          if (cut) {
 #pragma unroll
-        for (int j = 4; j < 64; j += 4) {
-          c0 = fmaxf(c0, sv[j]);
-          c1 = fmaxf(c1, sv[j + 1]);
-          c2 = fmaxf(c2, sv[j + 2]);
-          c3 = fmaxf(c3, sv[j + 3]);
+            for (int j = 0; j < 64; ++j) sv[j] = j < mine - h * 64 ? sv[j] : neg_inf();
+          }
+#pragma unroll
+          for (int j = 0; j < 64; j += 4) {
+            c0 = fmaxf(c0, sv[j]);
+            c1 = fmaxf(c1, sv[j + 1]);
+            c2 = fmaxf(c2, sv[j + 2]);
+            c3 = fmaxf(c3, sv[j + 3]);
+          }
         }
-        const uint32_t up = bf16_up(fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)));
-        uint16_t* rd = red + (xc & 1) * 256;
-        rd[half * 128 + r] = uint16_t(up);
-        meet();
-        if (!ok) break;
-        const float mx = fmaxf(m, fmaxf(__uint_as_float(up << 16),
-                                        __uint_as_float(uint32_t(rd[(half ^ 1) * 128 + r]) << 16)));
+        const float mx = fmaxf(m, fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)));
         // keep the old scale while p stays below 2^8
         const bool grow = !((mx - m) * g.qmul <= 8.f) && mx != m;
         const float old = m;
         if (grow) m = mx;
         const float mq = m == neg_inf() ? 0.f : m * g.qmul;
-        // P's buffer is free once the product of two steps ago is done
-        if (gi >= 2) ok = ok && warp_wait(pv_done + b, ((gi >> 1) - 1) & 1);
         const int end = (st + 1) * kT;
-        const bool tail = f.total < end;
-        const bool mixed = f.least < min(f.total, end);
+        const bool tail = f.total < end, mixed = f.least < min(f.total, end);
         if (tail || mixed) {
-          ok = ok && warp_wait(v_full + ks_i, (gi / NS) & 1);
+          ok = ok && warp_wait(v_full + si, (c / NS) & 1);
           if (!ok) break;
-          const int nv = min(f.total - st * kT, kT);
-          const int tid = threadIdx.x;
+          const int nv = min(f.total - st * kT, kT), tid = threadIdx.x & 127;
           for (int kb = 0; kb < KB; ++kb) {
-            uint4* v = reinterpret_cast<uint4*>(sm + M::V + ks_i * OP + kb * kPiece);
-            for (int i = nv * 8 + tid; i < kT * 8; i += kSoftWarps * 32)
-              v[i] = make_uint4(0, 0, 0, 0);
+            uint4* v = reinterpret_cast<uint4*>(sm + M::V + si * OP + kb * kPiece);
+            for (int k = nv * 8 + tid; k < kT * 8; k += 128) v[k] = make_uint4(0, 0, 0, 0);
             if (mixed)
-              for (int i = tid; i < nv * 8; i += kSoftWarps * 32) {
-                uint4 x = v[i];
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              for (int k = tid; k < nv * 8; k += 128) {
+                const uint4 y = v[k];
+                uint32_t w[4] = {y.x, y.y, y.z, y.w};
                 bool hit = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -391,92 +395,117 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
                   }
                 }
                 if (hit) {
-                  v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                  v[k] = make_uint4(w[0], w[1], w[2], w[3]);
                   *const_cast<volatile int*>(&info[slot].poison) = 1;
                 }
               }
           }
+          fence_proxy_async();  // -> visible to the tensor cores
+          __syncwarp();
         }
-        if (st > f.s0 && __any_sync(0xffffffffu, grow)) {
-          // O holds the steps before this one at the old scale
-          ok = ok && warp_wait(pv_done + (b ^ 1), ((gi - 1) >> 1) & 1);
+        if (i > head && __any_sync(0xffffffffu, grow)) {
+          // O holds the stream's steps before this one at the old scale
+          ok = ok && warp_wait(pv_done + x, ((c >> 1) - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const float corr = grow ? ex2((old - m) * g.qmul) : 1.f;  // 0 from -inf
           l *= corr;
-#pragma unroll
-          for (int c = 0; c < DP / 64; ++c) {
+          const uint32_t tO = tmem + lanes + M::out_col(x, buf);
+#pragma unroll 1
+          for (int k = 0; k < DP / 32; ++k) {
             float o[32];
-            const uint32_t a = tO + (to & 1) * DP + lane_off + half * (DP / 2) + c * 32;
-            tmem_ld32(a, o);
+            tmem_ld32(tO + k * 32, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= corr;
-            tmem_st32(a, o);
-            tmem_wait_st();
+            for (int j = 0; j < 32; ++j) o[j] *= corr;
+            tmem_st32(tO + k * 32, o);
           }
         }
-        if (!ok) break;
-        uint8_t* pr = sm + M::P + b * 2 * kPiece + half * kPiece + r * 128;
         float2 sum = make_float2(0.f, 0.f);
         const float2 qm = f2s(g.qmul), nm = f2s(-mq);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t w[4];
+        for (int h = 1; h >= 0; --h) {
+          if (h == 0) {
+            tmem_ld32(tS, sv);
+            tmem_ld32(tS + 32, sv + 32);
+            tmem_wait_ld();
+            if (cut) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 z =
-                f2fma(make_float2(sv[q * 8 + 2 * e], sv[q * 8 + 2 * e + 1]), qm, nm);
+              for (int j = 0; j < 64; ++j) sv[j] = j < mine ? sv[j] : neg_inf();
+            }
+          }
+          float w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 z = f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, nm);
             const float2 y = make_float2(ex2(z.x), ex2(z.y));
             sum = f2add(sum, y);
-            w[e] = bf16x2_bits(y.x, y.y);
+            w[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
           }
-          *reinterpret_cast<uint4*>(pr + ((q ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          tmem_st32(tS + h * 64, w);
         }
         l += sum.x + sum.y;
-        fence_proxy_async();  // P (and V's zeros) -> visible to the tensor cores
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + b);
+        if (lane == 0) mbar_arrive(p_full + x);
       }
       if (!ok) break;
-      // ---- write the tile out
-      float lt = 0.f;
-      const bool some = f.s1 > f.s0;
+      gi += steps;
+      // ---- merge the streams and write the tile; each takes half of the columns
+      const bool some = steps > 0;
+      const bool has0 = steps > 1 || (some && ((gi - 1) & 1) == 0);
+      const bool has1 = steps > 1 || (some && ((gi - 1) & 1) == 1);
+      float L = neg_inf(), w0 = 0.f, w1 = 0.f;
       if (some) {
-        // the last product waited for every warp's P, so for its reads of the maxima
-        ok = ok && warp_wait(pv_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+        const float mine = l != 0.f ? m * g.qmul + lg2(l) : neg_inf();  // base 2
+        red[x * 128 + r] = mine;
+        meet(0);
+        const float other = red[(x ^ 1) * 128 + r];
+        const float big = fmaxf(mine, other);
+        if (big != neg_inf()) L = big + lg2(ex2(mine - big) + ex2(other - big));
+        if (mine != mine || other != other) L = mine + other;  // not a number
+        // O of a stream is scaled by its own 2^-m
+        const float own = l != 0.f ? ex2(m * g.qmul - L) : 0.f;
+        red[(x ^ 1) * 128 + r] = own;  // the word that only this thread has read
+        meet(1);
+        const float their = red[x * 128 + r];
+        w0 = x == 0 ? own : their;
+        w1 = x == 0 ? their : own;
+        const int last0 = (gi - 1) & 1 ? gi - 2 : gi - 1, last1 = (gi - 1) & 1 ? gi - 1 : gi - 2;
+        if (has0) ok = ok && warp_wait(pv_done, (last0 >> 1) & 1);
+        if (has1) ok = ok && warp_wait(pv_done + 1, (last1 >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        redf[half * 128 + r] = l;
-        meet();
-        lt = l + redf[(half ^ 1) * 128 + r];
-        meet();  // both have read before either writes a maximum there again
-        if (!ok) break;
       }
-      const float inv = lt != 0.f ? 1.f / lt : 0.f;
       const bool poison = some && *const_cast<volatile int*>(&info[slot].poison);
       const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < DP / 64; ++c) {
-        const int col = half * (DP / 2) + c * 32;
+        const int col = x * (DP / 2) + c * 32;
         float o[32];
-        __syncwarp();
-        if (some) {
-          tmem_ld32(tO + (to & 1) * DP + lane_off + col, o);
-          tmem_wait_ld();
-        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * inv : 0.f;
-        if (poison && valid && lt != 0.f) {  // values that were taken out of V
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        __syncwarp();
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          if (!(s ? has1 : has0)) continue;
+          float v[32];
+          tmem_ld32(tmem + lanes + M::out_col(s, buf) + col, v);
+          tmem_wait_ld();
+          const float w = s ? w1 : w0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(v[i], w, o[i]);
+        }
+        if (poison && valid && (w0 != 0.f || w1 != 0.f)) {  // values that were taken out of V
           for (int k = f.s0 * kT; k < min(lim, f.s1 * kT); ++k) {
             const __nv_bfloat16* v =
                 p.V + (int64_t(f.kbeg + list[k / g.block] * g.block + k % g.block) * g.Hkv + f.kh) *
                           g.D;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = col + i < g.D ? __bfloat162float(v[col + i]) : 0.f;
-              if (!(fabsf(x) <= 3.4e38f)) o[i] += x;
+              const float y = col + i < g.D ? __bfloat162float(v[col + i]) : 0.f;
+              if (!(fabsf(y) <= 3.4e38f)) o[i] += y;
             }
           }
         }
@@ -497,15 +526,14 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
                   bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
         }
       }
-      if (valid && half == 0) {
-        const float L = lt != 0.f ? m * g.qmul + lg2(lt) : neg_inf();  // base 2
+      if (valid && x == 0) {
         if (p.nsplit > 1) p.part_l[f.part * p.rows + r] = L;
         else p.lse[qrow] = L * kLn2;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (some) mbar_arrive(o_empty + (to & 1));
+        if (some) mbar_arrive(o_empty + buf);
         mbar_arrive(tile_empty + slot);
       }
       to += some;

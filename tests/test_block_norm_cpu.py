@@ -162,7 +162,7 @@ def test_binding_refuses_host_tensors_and_shapes(lib):
         gb.gattn_block_sums(K, seq, 16)
     with pytest.raises(ValueError, match="CUDA"):
         gb.gattn_block_fwd(K, K, K, torch.zeros(1, 2, 1, dtype=torch.int32), seq, seq, 16, 64)
-    with pytest.raises(ValueError, match="shape"):
+    with pytest.raises(ValueError, match="dimensions"):
         gb.gattn_block_sums(K[0], seq, 16)
     with pytest.raises(ValueError):
         gb.gattn_block_fwd(K, K, K[1:], torch.zeros(1, 2, 1, dtype=torch.int32), seq, seq, 16, 64)
