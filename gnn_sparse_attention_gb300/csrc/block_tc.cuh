@@ -42,6 +42,40 @@ __device__ __forceinline__ void tma_tile3d(void* dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};\n" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(
+          taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_alloc512(uint32_t* slot) {  // one whole warp
   asm volatile(
       "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(slot))
@@ -52,45 +86,90 @@ __device__ __forceinline__ void tmem_free512(uint32_t addr) {  // one whole warp
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(addr) : "memory");
 }
 
-// D[128][N] (+)= A[128][K] B[N][K]^T, bf16 operands of K = 64 KB columns in
-// 128-byte swizzled tiles [K / 64][rows][128 B]; both K-major.
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n"
+               : "=r"(p));
+  return p != 0;
+}
+// The same value in every lane, known to be so by the compiler: the products'
+// descriptors then stay in uniform registers, where a product costs a few
+// instructions (built per lane they cost more cycles than the product).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Descriptor of an operand tile: K-major (swizzled 128-byte rows), and as
+// loaded row by row and read along the rows (MN-major; 64-column pieces
+// `piece` bytes apart).  Offsets within the tile are added to the address
+// field with desc_at.
+__device__ __forceinline__ uint64_t desc_k(const void* tile) {
+  return sw128_desc(smem_u32(tile), 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_mn(const void* tile, int piece) {
+  return sw128_desc(smem_u32(tile), piece, 1024);
+}
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, int bytes) { return d + (bytes >> 4); }
+
+// D[128][N] = A[128][K] B[N][K]^T, bf16 operands of K = 64 KB columns in
+// 128-byte swizzled tiles [K / 64][rows][128 B]; both K-major.  One lane.
 template <int KB>
-__device__ __forceinline__ void mma_kk(uint32_t d, const uint8_t* a, int a_piece, const uint8_t* b,
+__device__ __forceinline__ void mma_kk(uint32_t d, uint64_t a, int a_piece, uint64_t b,
                                        int b_piece, uint32_t idesc) {
 #pragma unroll
   for (int k = 0; k < 4 * KB; ++k)
-    mma_bf16(d, sw128_desc(smem_u32(a + (k / 4) * a_piece) + (k % 4) * 32, 16, 1024),
-             sw128_desc(smem_u32(b + (k / 4) * b_piece) + (k % 4) * 32, 16, 1024), idesc, k > 0);
+    mma_bf16(d, desc_at(a, (k / 4) * a_piece + (k % 4) * 32),
+             desc_at(b, (k / 4) * b_piece + (k % 4) * 32), idesc, k > 0);
 }
 
-// D[128][N] (+)= A[128][K] B[K][N]: A K-major tiles [K / 64][128][128 B], B as
-// loaded row by row, [N / 64][K rows][128 B] (MN-major: 64-column pieces
-// b_piece bytes apart, groups of 8 rows 1024 bytes apart).
+// D[128][N] (+)= A[128][K] B[K][N]: A in TMEM (lane r holds row r, a 32-bit
+// column two consecutive bf16 of K), B MN-major.  A's K columns sit in groups of
+// `group` bf16, `stride` TMEM columns apart (a thread overwrites the scores
+// that it has read).  One lane.
 template <int K>
-__device__ __forceinline__ void mma_km(uint32_t d, const uint8_t* a, int a_piece, const uint8_t* b,
-                                       int b_piece, uint32_t idesc, bool add) {
-#pragma unroll
-  for (int k = 0; k < K / 16; ++k)
-    mma_bf16(d, sw128_desc(smem_u32(a + (k / 4) * a_piece) + (k % 4) * 32, 16, 1024),
-             sw128_desc(smem_u32(b) + k * 2048, b_piece, 1024), idesc, (add || k > 0) ? 1u : 0u);
-}
-
-// The same with A in TMEM: lane r holds row r, a 32-bit column two consecutive
-// bf16 of K.  The K columns sit in groups of `group` bf16, `stride` TMEM columns
-// apart (a thread overwrites the scores that it has read).
-template <int K>
-__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, int group, int stride,
-                                       const uint8_t* b, int b_piece, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, int group, int stride, uint64_t b,
+                                       uint32_t idesc, bool add) {
 #pragma unroll
   for (int k = 0; k < K / 16; ++k) {
     const uint32_t at = a + (k * 16 / group) * stride + (k * 16 % group) / 2;
-    const uint64_t bd = sw128_desc(smem_u32(b) + k * 2048, b_piece, 1024);
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(at), "l"(bd), "r"(idesc), "r"((add || k > 0) ? 1u : 0u)
+        "r"(at), "l"(desc_at(b, k * 2048)), "r"(idesc), "r"((add || k > 0) ? 1u : 0u)
         : "memory");
   }
+}
+
+// 16 bf16 of a row: one 32-byte store where the address allows it (a lane then
+// fills a whole sector; 16-byte stores to rows far apart take twice the time).
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// 32 columns [col, col + 32) of a row of D values at `row`
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int col, int D, const float* v,
+                                          bool wide) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (col + q * 16 + 16 <= D) {
+      store16(row + col + q * 16, v + q * 16, wide);
+    } else if (col + q * 16 < D) {  // D = 8
+      *reinterpret_cast<uint4*>(row + col) =
+          make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
+                     bf16x2_bits(v[6], v[7]));
+    }
+  }
+}
+__device__ __forceinline__ bool wide_rows(const void* base, int D) {
+  return D >= 16 && (reinterpret_cast<uintptr_t>(base) & 31) == 0;
 }
 
 }  // namespace tc

@@ -6,19 +6,25 @@
 //
 // dQ: a tile of up to 128 (query row, head) pairs walks its unit's block list
 //   in steps of 128 keys,
-//     S = Q K^T, dP = dO V^T                          -> TMEM
-//     ds = 2^(S scale log2e - lse log2e) (dP - Delta)  -> bf16, shared memory
+//     S = Q K^T, dP = dO V^T                          -> TMEM (two S buffers)
+//     ds = 2^(S scale log2e - lse log2e) (dP - Delta)  -> TMEM, over S
 //     dQ += ds K                                       -> TMEM
-//   The next step's S and dP run while ds of this one is formed.
+//   The next step's S and dP run while ds of this one is formed.  ds enters the
+//   product as the sum of two bf16: rounded once it would add as much error to
+//   dQ as dQ's own rounding, on top of that of Delta (formed from the rounded
+//   out), and dQ would be half again as far off as the rounding of the result
+//   alone; the second product costs a quarter of the kernel's tensor work.
 //
 // dK, dV: a work item is a tile of 128 keys and up to `chunk` of the units that
 //   chose one of its blocks (block_api.cu builds the items), walked in steps
 //   of 64 (query row, head) pairs,
 //     S^T = K Q^T, dP^T = V dO^T                       -> TMEM, two buffers
-//     p, ds as bf16 [key][query]                       -> shared memory
+//     p, ds as bf16                                    -> TMEM, over S^T and dP^T
 //     dV += p dO, dK += ds Q                           -> TMEM
-//   64 rather than 128 queries a step leave room for three or four stages of
-//   Q and dO and a second score buffer next to the two accumulators.  Units
+//   64 rather than 128 queries a step leave room for several stages of Q and
+//   dO and a second score buffer next to the two accumulators; two groups of
+//   eight warps take the steps in turn, so that one forms p and ds while the
+//   other waits for its products.  Units
 //   of fewer than 64 pairs share a step, each in a box of its own; a box
 //   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
 //   its mask within a box is a range of columns.
@@ -51,32 +57,33 @@ struct DqParams {
 struct DqInfo {
   int steps, n, total;
   int row, rows, pos;
-  int len, h0;
+  int kbeg, len, kh, h0;
 };
 
 template <int DP>
 struct DqSm {
   static constexpr int KB = DP / 64;
   static constexpr int NQ = DP == 64 ? 2 : 1;   // Q and dO buffers
-  static constexpr int NS = DP == 64 ? 3 : 2;   // K and V stages
-  static constexpr int ND = DP == 64 ? 2 : 1;   // ds buffers
+  static constexpr int NS = DP == 64 ? 4 : 2;   // K and V stages
+  static constexpr int NG = DP == 64 ? 2 : 1;   // dQ buffers (tiles in turn)
   static constexpr int OP = KB * kPiece;
   static constexpr int Q = 0;
   static constexpr int O = Q + NQ * OP;
   static constexpr int K = O + NQ * OP;
   static constexpr int V = K + NS * OP;
-  static constexpr int DS = V + NS * OP;
-  static constexpr int IDS = DS + ND * 2 * kPiece;
+  static constexpr int IDS = V + NS * OP;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(DqInfo));
-  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 2 + 2 * ND + 2;
+  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 2 + 1 + 2 + 2 + NG;
   static constexpr int END = BAR + NBAR * 8 + 8;
-  static constexpr int BYTES = END + 1024 <= 227 * 1024 ? END + 1024 : 227 * 1024;
-  static_assert(END <= 227 * 1024, "shared memory of one CTA");
+  static constexpr int BYTES = END + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+  // TMEM: S [0, 256) in two buffers, dP [256, 384), dQ from 384 on
+  static_assert(384 + NG * DP <= 512, "TMEM columns");
 };
 
 constexpr int kDqWarps = 16;
-constexpr int kDqThr = (kDqWarps + 2) * 32;
+constexpr int kDqThr = (kDqWarps + 3) * 32;
 
 }  // namespace
 
@@ -84,32 +91,31 @@ template <int DP>
 __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__ DqParams p) {
   using namespace tc;
   using M = DqSm<DP>;
-  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, ND = M::ND, OP = M::OP;
+  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, NG = M::NG, OP = M::OP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
-  if (pad + M::END > M::BYTES) {
-    if (threadIdx.x == 0) atomicOr(&g_err, 1);
-    return;
-  }
-  uint8_t* sm = smem_raw + pad;
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
            *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
            *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
-           *s_empty = s_full + 1, *d_full = s_empty + 1, *d_done = d_full + ND,
-           *g_empty = d_done + ND;
+           *dp_empty = s_full + 2, *d_full = dp_empty + 1, *d_done = d_full + 2,
+           *g_empty = d_done + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   DqInfo* info = reinterpret_cast<DqInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
   const BlockGeom& g = p.b.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(tile_full + i, 1);
-      mbar_init(tile_empty + i, kDqWarps + 1);
-      mbar_init(g_empty + i, kDqWarps);
+      mbar_init(tile_empty + i, kDqWarps + 2);
+      mbar_init(s_full + i, 1);
+      mbar_init(d_full + i, kDqWarps);
+      mbar_init(d_done + i, 1);
     }
+    mbar_init(dp_empty, kDqWarps);
+    for (int i = 0; i < NG; ++i) mbar_init(g_empty + i, kDqWarps);
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
@@ -120,12 +126,6 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, kDqWarps);
-    for (int i = 0; i < ND; ++i) {
-      mbar_init(d_full + i, kDqWarps);
-      mbar_init(d_done + i, 1);
-    }
     mbar_init_fence();
   }
   if (warp == kDqWarps) tmem_alloc512(s_tmem);
@@ -133,21 +133,18 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t tS = tmem, tP = tmem + kT, tG = tmem + 2 * kT;
   bool ok = true;
 
-  if (warp == kDqWarps + 1) {
-    // ---------------------------------------------------------------- producer
-    const int per = kT / g.block;
-    const uint32_t blk_bytes = uint32_t(g.block) * 128;
-    int gi = 0, ti = 0, tq = 0;
+  if (warp == kDqWarps + 2) {
+    // ---------------------------------------------------------------- lists
+    int ti = 0;
     for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
-      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
-      if (!ok) break;
       const int hsub = int(t % p.hs), u = int((t / p.hs) % g.U), kh = int(t / p.hs / g.U);
       const Unit un = unit_at(g, u);
       const Span ks = span_k(g, un.s);
+      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
       int* list = ids + slot * kBlkMaxTopk;
       int n = 0;
       if (un.n > 0)
@@ -156,31 +153,45 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       const int total = list_keys(list, n, g.block, ks.len);
       const int seen =
           g.causal ? list_keys(list, n, g.block, min(un.pos + un.n, ks.len)) : total;
-      const int steps = (seen + kT - 1) / kT;
       if (lane == 0) {
         DqInfo& f = info[slot];
-        f.steps = steps;
+        f.steps = (seen + kT - 1) / kT;
         f.n = n;
         f.total = total;
         f.row = un.row;
         f.rows = un.n;
         f.pos = un.pos;
+        f.kbeg = ks.beg;
         f.len = ks.len;
+        f.kh = kh;
         f.h0 = kh * g.G + hsub * p.ht;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(tile_full + slot);
-      if (steps <= 0) continue;
-      const int qs = tq % NQ;
-      if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+    }
+  } else if (warp == kDqWarps + 1) {
+    // ---------------------------------------------------------------- copies
+    const int per = kT / g.block;
+    const uint32_t blk_bytes = uint32_t(g.block) * 128;
+    int gi = 0, ti = 0, tq = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      ok = warp_wait(tile_full + slot, (ti >> 1) & 1);
       if (!ok) break;
-      ++tq;
-      if (lane == 0) {
-        mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 256 * KB);
-        for (int kb = 0; kb < KB; ++kb) {
-          const int h0 = kh * g.G + hsub * p.ht;
-          tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, h0, un.row, q_full + qs);
-          tma_tile3d(sm + M::O + qs * OP + kb * kPiece, &p.mo, kb * 64, h0, un.row, q_full + qs);
+      const DqInfo& f = info[slot];
+      const int* list = ids + slot * kBlkMaxTopk;
+      const int steps = f.steps, n = f.n, kbeg = f.kbeg, kh = f.kh;
+      if (steps > 0) {
+        const int qs = tq % NQ;
+        if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+        if (!ok) break;
+        ++tq;
+        if (lane == 0) {
+          mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 256 * KB);
+          for (int kb = 0; kb < KB; ++kb) {
+            tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, f.h0, f.row, q_full + qs);
+            tma_tile3d(sm + M::O + qs * OP + kb * kPiece, &p.mo, kb * 64, f.h0, f.row, q_full + qs);
+          }
         }
       }
       for (int st = 0; st < steps; ++st, ++gi) {
@@ -192,15 +203,18 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
           __syncwarp();
-          for (int e = lane; e < nb * KB; e += 32) {
-            const int b = e / KB, kb = e % KB;
+          if (lane < nb * KB) {
+            const int b = lane / KB, kb = lane % KB;
             tma_tile3d(sm + (kv ? M::V : M::K) + si * OP + kb * kPiece + b * blk_bytes,
-                       kv ? &p.mv : &p.mk, kb * 64, kh, ks.beg + list[st * per + b] * g.block,
+                       kv ? &p.mv : &p.mk, kb * 64, kh, kbeg + list[st * per + b] * g.block,
                        full);
           }
         }
         if (!ok) break;
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int i = 1; i <= NQ && i <= tq; ++i)
@@ -212,158 +226,177 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     }
   } else if (warp == kDqWarps) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_G = f16_idesc(kT, DP, true);
-      int gi = 0, ti = 0, tq = 0;
-      int pi = -1, po = 0;  // the step whose dQ product is due, its tile
-      bool pfirst = false;
-      auto product_dq = [&]() {
-        const int si = pi % NS, d = pi % ND;
-        ok = ok && mbar_wait(d_full + d, (pi / ND) & 1);
-        if (pfirst && po >= 2) ok = ok && mbar_wait(g_empty + (po & 1), ((po >> 1) - 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        mma_km<kT>(tG + (po & 1) * DP, sm + M::DS + d * 2 * kPiece, kPiece, sm + M::K + si * OP,
-                   kPiece, IDESC_G, !pfirst);
-        mma_commit(d_done + d);
+    constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_G = f16_idesc(kT, DP, true);
+    const uint64_t dQ = desc_k(sm + M::Q), dO = desc_k(sm + M::O), dK = desc_k(sm + M::K),
+                   dV = desc_k(sm + M::V), dKm = desc_mn(sm + M::K, kPiece);
+    const uint32_t tm = uniform(tmem);
+    int gi = 0, ti = 0, tq = 0, done = 0;  // steps with scores, tiles, with dQ products
+    int due_tile = 0, due_i = 0;            // of step `done`
+    auto product_dq = [&]() {
+      const int si = done % NS, b = done & 1, buf = due_tile % NG;
+      ok = ok && warp_wait(d_full + b, (done >> 1) & 1);
+      if (due_i == 0 && due_tile >= NG)
+        ok = ok && warp_wait(g_empty + buf, (due_tile / NG - 1) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t out = tm + 384 + buf * DP, ds = tm + b * kT;
+        mma_tm<kT>(out, ds, 16, 16, desc_at(dKm, si * OP), IDESC_G, due_i > 0);
+        mma_tm<kT>(out, ds + 8, 16, 16, desc_at(dKm, si * OP), IDESC_G, true);
+        mma_commit(d_done + b);
         mma_commit(k_empty + si);
-      };
-      for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
-        const int slot = ti & 1;
-        ok = mbar_wait(tile_full + slot, (ti >> 1) & 1);
+      }
+      __syncwarp();
+      ++done;
+    };
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      if (!__all_sync(0xffffffffu, mbar_test(tile_full + slot, (ti >> 1) & 1))) {
+        if (ok && done < gi) product_dq();  // the lists may wait for that tile to be written
+        ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      }
+      if (!ok) break;
+      const int n = uniform(info[slot].steps);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
+      if (n <= 0) continue;
+      const int qs = tq % NQ;
+      ok = warp_wait(q_full + qs, (tq / NQ) & 1);
+      for (int i = 0; i < n && ok; ++i, ++gi) {
+        const int si = gi % NS, b = gi & 1;
+        ok = ok && warp_wait(k_full + si, (gi / NS) & 1);
         if (!ok) break;
-        const int n = info[slot].steps;
-        mbar_arrive(tile_empty + slot);
-        if (n <= 0) {  // the compute warps may wait for the last product before they move on
-          if (pi >= 0) product_dq();
-          pi = -1;
-          continue;
-        }
-        const int qs = tq % NQ;
-        ok = mbar_wait(q_full + qs, (tq / NQ) & 1);
-        for (int i = 0; i < n && ok; ++i, ++gi) {
-          const int si = gi % NS;
-          ok = mbar_wait(k_full + si, (gi / NS) & 1) && mbar_wait(v_full + si, (gi / NS) & 1);
-          if (gi >= 1) ok = ok && mbar_wait(s_empty, (gi - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          mma_kk<KB>(tS, sm + M::Q + qs * OP, kPiece, sm + M::K + si * OP, kPiece, IDESC_S);
-          mma_kk<KB>(tP, sm + M::O + qs * OP, kPiece, sm + M::V + si * OP, kPiece, IDESC_S);
-          mma_commit(s_full);
+        tc_fence_after();
+        if (elect_one())  // over the ds of step gi - 2, whose product was issued before
+          mma_kk<KB>(tm + b * kT, desc_at(dQ, qs * OP), kPiece, desc_at(dK, si * OP), kPiece,
+                     IDESC_S);
+        __syncwarp();
+        ok = warp_wait(v_full + si, (gi / NS) & 1);
+        if (gi >= 1) ok = ok && warp_wait(dp_empty, (gi - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_kk<KB>(tm + 2 * kT, desc_at(dO, qs * OP), kPiece, desc_at(dV, si * OP), kPiece,
+                     IDESC_S);
+          mma_commit(s_full + b);
           mma_commit(v_empty + si);
           if (i == n - 1) mma_commit(q_empty + qs);
-          if (pi >= 0) product_dq();
-          pi = gi;
-          po = tq;
-          pfirst = i == 0;
         }
-        ++tq;
+        __syncwarp();
+        if (done < gi) product_dq();
+        due_tile = tq;
+        due_i = i;
       }
-      if (ok && pi >= 0) product_dq();
-      if (ok && gi > 0) ok = mbar_wait(d_done + (gi - 1) % ND, ((gi - 1) / ND) & 1);
-      if (!ok && gi > 0) {
-        mbar_wait(s_full, (gi - 1) & 1, 200);
-        if (pi >= 0) mbar_wait(d_done + pi % ND, (pi / ND) & 1, 200);
+      ++tq;
+    }
+    if (ok && done < gi) product_dq();
+    if (ok && gi > 0) ok = warp_wait(d_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+    if (!ok) {  // whatever was issued has completed before TMEM is given up
+      for (int k = 0; k <= 2 && k <= gi; ++k) {
+        const int c = gi - k;
+        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(d_done + (c & 1), (c >> 1) & 1, 200);
       }
     }
-    __syncwarp();
   } else {
-    // ---------------------------------------------------------------- p and ds
+    // ---------------------------------------------------------------- ds
     const int r = (warp & 3) * 32 + lane, cc = warp >> 2;  // row, 32-column chunk
-    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const int th = r % p.ht, tt = r / p.ht;
+    const bool wide = wide_rows(p.b.dQ, g.D);
     int gi = 0, ti = 0, to = 0;
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
       if (!ok) break;
-      const DqInfo f = info[slot];
+      const DqInfo& f = info[slot];
+      const int steps = f.steps, total = f.total;
       const bool valid = r < p.rows && tt < f.rows;
       const int lim = !valid ? 0
                       : g.causal ? list_keys(ids + slot * kBlkMaxTopk, f.n, g.block,
                                              min(f.pos + tt + 1, f.len))
-                                 : f.total;
+                                 : total;
       const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
       float2 stat = make_float2(0.f, 0.f);
-      if (valid) stat = p.b.stat[qrow];
-      for (int st = 0; st < f.steps; ++st, ++gi) {
-        const int si = gi % NS, d = gi % ND;
-        ok = ok && warp_wait(s_full, gi & 1);
+      if (lim > 0) stat = p.b.stat[qrow];  // a row that sees nothing has lse = -inf
+      for (int st = 0; st < steps; ++st, ++gi) {
+        const int si = gi % NS, b = gi & 1;
+        ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        float sv[32], dv[32];
-        tmem_ld32(tS + lane_off + cc * 32, sv);
-        tmem_ld32(tP + lane_off + cc * 32, dv);
+        const uint32_t tS = tmem + lanes + b * kT + cc * 32;
+        float dv[32];
+        tmem_ld32(tmem + lanes + 2 * kT + cc * 32, dv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty);
-        if (gi >= ND) ok = ok && warp_wait(d_done + d, ((gi / ND) - 1) & 1);
-        if (!ok) break;
-        if (f.total < (st + 1) * kT) {  // keys behind the list's end: zeros in K
-          const int nv = f.total - st * kT;
+        if (lane == 0) mbar_arrive(dp_empty);
+        if (total < (st + 1) * kT) {  // keys behind the list's end: zeros in K
+          const int nv = total - st * kT;
           for (int kb = 0; kb < KB; ++kb) {
             uint4* k = reinterpret_cast<uint4*>(sm + M::K + si * OP + kb * kPiece);
             for (int i = nv * 8 + threadIdx.x; i < kT * 8; i += kDqWarps * 32)
               k[i] = make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async();
+          __syncwarp();
         }
         const int mine = lim - st * kT - cc * 32;
+        const bool cut = __any_sync(0xffffffffu, mine < 32);
         const float2 qm = f2s(g.qmul), nl = f2s(-stat.x), nd = f2s(-stat.y);
-        uint8_t* dr = sm + M::DS + d * 2 * kPiece + (cc >> 1) * kPiece + r * 128;
-        const bool full = __all_sync(0xffffffffu, mine >= 32);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[4];
+        for (int h = 0; h < 2; ++h) {  // 16 columns: ds rounded, and what the rounding left
+          float sv[16], w[16];
+          tmem_ld16(tS + h * 16, sv);
+          tmem_wait_ld();
+          if (cut) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = q * 8 + 2 * e;
-            const float2 z = f2fma(make_float2(sv[j], sv[j + 1]), qm, nl);
-            float2 y = f2mul(make_float2(ex2(z.x), ex2(z.y)),
-                             f2add(make_float2(dv[j], dv[j + 1]), nd));
-            if (!full) {
-              y.x = j < mine ? y.x : 0.f;
-              y.y = j + 1 < mine ? y.y : 0.f;
+            for (int j = 0; j < 16; ++j) {  // p = 0, and nothing of dP
+              sv[j] = h * 16 + j < mine ? sv[j] : neg_inf();
+              dv[h * 16 + j] = h * 16 + j < mine ? dv[h * 16 + j] : stat.y;
             }
-            w[e] = bf16x2_bits(y.x, y.y);
           }
-          *reinterpret_cast<uint4*>(dr + ((((cc & 1) * 4 + q) ^ (r & 7)) * 16)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 z = f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, nl);
+            const float2 y =
+                f2mul(make_float2(ex2(z.x), ex2(z.y)),
+                      f2add(make_float2(dv[h * 16 + 2 * j], dv[h * 16 + 2 * j + 1]), nd));
+            const uint32_t hi = bf16x2_bits(y.x, y.y);
+            w[j] = __uint_as_float(hi);
+            w[8 + j] = __uint_as_float(bf16x2_bits(y.x - __uint_as_float(hi << 16),
+                                                   y.y - __uint_as_float(hi & 0xffff0000u)));
+          }
+          tmem_st16(tS + h * 16, w);
         }
-        fence_proxy_async();
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(d_full + d);
+        if (lane == 0) mbar_arrive(d_full + b);
       }
       if (!ok) break;
-      const bool some = f.steps > 0;
+      const bool some = steps > 0;
       if (some) {
-        ok = warp_wait(d_done + (gi - 1) % ND, ((gi - 1) / ND) & 1);
+        ok = warp_wait(d_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
       }
       if (cc * 32 < DP) {
         float o[32];
         if (some) {
-          tmem_ld32(tG + (to & 1) * DP + lane_off + cc * 32, o);
+          tmem_ld32(tmem + lanes + 384 + (to % NG) * DP + cc * 32, o);
           tmem_wait_ld();
         }
         if (valid) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.b.dQ) + qrow * g.D + cc * 32;
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * g.scale : 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (cc * 32 + q * 8 < g.D)
-              *reinterpret_cast<uint4*>(out + q * 8) = make_uint4(
-                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
-                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+          store_row(static_cast<__nv_bfloat16*>(p.b.dQ) + qrow * g.D, cc * 32, g.D, o, wide);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (some) mbar_arrive(g_empty + (to & 1));
+        if (some) mbar_arrive(g_empty + to % NG);
         mbar_arrive(tile_empty + slot);
       }
       to += some;
@@ -380,7 +413,7 @@ namespace {
 
 constexpr int kNR = 64;               // query pairs per step
 constexpr int kQPiece = kNR * 128;    // 64 rows x 64 bf16 columns
-constexpr int kKvWarps = 8;
+constexpr int kKvWarps = 16;          // two groups of eight, steps in turn
 constexpr int kKvThr = (kKvWarps + 2) * 32;
 constexpr int kList = 256;            // units resolved at a time (8 bitmap words)
 
@@ -408,24 +441,22 @@ struct KvInfo {
 template <int DP>
 struct KvSm {
   static constexpr int KB = DP / 64;
-  static constexpr int NS = DP == 64 ? 4 : 3;  // Q and dO stages
-  static constexpr int NP = DP == 64 ? 2 : 1;  // p and ds buffers
+  static constexpr int NS = DP == 64 ? 6 : 4;  // Q and dO stages
   static constexpr int OP = KB * kPiece, QP = KB * kQPiece;
   static constexpr int K = 0;
   static constexpr int V = OP;
   static constexpr int Q = 2 * OP;
   static constexpr int O = Q + NS * QP;
-  static constexpr int P = O + NS * QP;          // [NP][128][128 B]
-  static constexpr int DS = P + NP * kPiece;
-  static constexpr int STAT = DS + NP * kPiece;  // [NS][64] (lse log2e, Delta)
+  static constexpr int STAT = O + NS * QP;       // [NS][64] (lse log2e, Delta)
   static constexpr int BOX = STAT + NS * kNR * 8;
   static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
   static constexpr int INFO = LIST + kList * 8;
   static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
-  static constexpr int NBAR = 4 + 2 + 2 * NS + 4 + 2 * NP + 2;
+  static constexpr int NBAR = 4 + 2 + 2 * NS + 2 + 2 + 2 + 1;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+  // TMEM: S^T [0, 128) and dP^T [128, 256) in two buffers, dV, dK from 256 on
 };
 
 // more bytes to wait for in the barrier's phase, without an arrival
@@ -446,36 +477,33 @@ template <int DP>
 __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
   using namespace tc;
   using M = KvSm<DP>;
-  constexpr int KB = M::KB, NS = M::NS, NP = M::NP, QP = M::QP;
+  constexpr int KB = M::KB, NS = M::NS, QP = M::QP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
            *kv_empty = kv_full + 1, *q_full = kv_empty + 1, *q_empty = q_full + NS,
-           *s_full = q_empty + NS, *s_empty = s_full + 2, *p_full = s_empty + 2,
-           *p_done = p_full + NP, *g_empty = p_done + NP;
+           *s_full = q_empty + NS, *p_full = s_full + 2, *p_done = p_full + 2,
+           *g_empty = p_done + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
   int2* list = reinterpret_cast<int2*>(sm + M::LIST);
   const BlockGeom& g = p.b.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(item_full + i, 1);
       mbar_init(item_empty + i, kKvWarps + 1);
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, kKvWarps);
+      mbar_init(p_full + i, kKvWarps / 2);
+      mbar_init(p_done + i, 1);
     }
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(q_full + i, 1 + 32);  // the copies' bytes, and each lane's statistics
       mbar_init(q_empty + i, 1);
-    }
-    for (int i = 0; i < NP; ++i) {
-      mbar_init(p_full + i, kKvWarps);
-      mbar_init(p_done + i, 1);
     }
     mbar_init(g_empty, kKvWarps);
     mbar_init_fence();
@@ -485,7 +513,6 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t tS = tmem, tP = tmem + 2 * kNR, tV = tmem + 4 * kNR, tK = tV + DP;
   bool ok = true;
 
   if (warp == kKvWarps + 1) {
@@ -635,67 +662,86 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     cp_async_wait<0>();
   } else if (warp == kKvWarps) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false), IDESC_G = f16_idesc(kT, DP, true);
-      int gi = 0, tk = 0;
-      int pi = -1, pk = 0;
-      bool pfirst = false;
-      auto product_g = [&]() {
-        const int si = pi % NS, b = pi % NP;
-        ok = ok && mbar_wait(p_full + b, (pi / NP) & 1);
-        if (pfirst && pk >= 1) ok = ok && mbar_wait(g_empty, (pk - 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        mma_km<kNR>(tV, sm + M::P + b * kPiece, kPiece, sm + M::O + si * QP, kQPiece, IDESC_G,
-                    !pfirst);
-        mma_km<kNR>(tK, sm + M::DS + b * kPiece, kPiece, sm + M::Q + si * QP, kQPiece, IDESC_G,
-                    !pfirst);
-        mma_commit(p_done + b);
+    constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false), IDESC_G = f16_idesc(kT, DP, true);
+    const uint64_t dK = desc_k(sm + M::K), dV = desc_k(sm + M::V), dQ = desc_k(sm + M::Q),
+                   dO = desc_k(sm + M::O), dQm = desc_mn(sm + M::Q, kQPiece),
+                   dOm = desc_mn(sm + M::O, kQPiece);
+    const uint32_t tm = uniform(tmem);
+    // Step gi's scores overwrite p and ds of step gi - 2, whose products were
+    // issued before them and run in that order.
+    int gi = 0, tk = 0, done = 0;
+    int due_item[2] = {0, 0}, due_i[2] = {0, 0};
+    auto product_g = [&]() {  // of step `done`
+      const int x = done & 1, si = done % NS;
+      const int item = x ? due_item[1] : due_item[0], i = x ? due_i[1] : due_i[0];
+      ok = ok && warp_wait(p_full + x, (done >> 1) & 1);
+      if (i == 0 && item >= 1) ok = ok && warp_wait(g_empty, (item - 1) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tm<kNR>(tm + 256, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
+        mma_tm<kNR>(tm + 256 + DP, tm + 128 + x * kNR, 16, 16, desc_at(dQm, si * QP), IDESC_G,
+                    i > 0);
+        mma_commit(p_done + x);
         mma_commit(q_empty + si);
-      };
-      for (int ti = 0; ok; ++ti) {
-        const int slot = ti & 1;
-        ok = mbar_wait(item_full + slot, (ti >> 1) & 1);
-        if (!ok) break;
-        const int it = info[slot].item, n = info[slot].steps;
-        mbar_arrive(item_empty + slot);
-        if (it < 0) break;
-        if (n <= 0) {
-          if (pi >= 0) product_g();
-          pi = -1;
-          continue;
-        }
-        ok = mbar_wait(kv_full, tk & 1);
-        for (int i = 0; i < n && ok; ++i, ++gi) {
-          const int si = gi % NS, b = gi & 1;
-          ok = mbar_wait(q_full + si, (gi / NS) & 1);
-          if (gi >= 2) ok = ok && mbar_wait(s_empty + b, ((gi >> 1) - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          mma_kk<KB>(tS + b * kNR, sm + M::K, kPiece, sm + M::Q + si * QP, kQPiece, IDESC_S);
-          mma_kk<KB>(tP + b * kNR, sm + M::V, kPiece, sm + M::O + si * QP, kQPiece, IDESC_S);
-          mma_commit(s_full + b);
-          if (i == n - 1) mma_commit(kv_empty);
-          if (pi >= 0) product_g();
-          pi = gi;
-          pk = tk;
-          pfirst = i == 0;
-        }
-        ++tk;
       }
-      if (ok && pi >= 0) product_g();
-      if (ok && gi > 0) ok = mbar_wait(p_done + (gi - 1) % NP, ((gi - 1) / NP) & 1);
-      if (!ok && gi > 0) {
-        mbar_wait(s_full + ((gi - 1) & 1), ((gi - 1) >> 1) & 1, 200);
-        if (pi >= 0) mbar_wait(p_done + pi % NP, (pi / NP) & 1, 200);
+      __syncwarp();
+      ++done;
+    };
+    for (int ti = 0; ok; ++ti) {
+      const int slot = ti & 1;
+      if (!__all_sync(0xffffffffu, mbar_test(item_full + slot, (ti >> 1) & 1))) {
+        while (ok && done < gi) product_g();  // the item may wait for those before it
+        ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
+      }
+      if (!ok) break;
+      const int it = uniform(info[slot].item), n = uniform(info[slot].steps);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + slot);
+      if (it < 0) break;
+      if (n <= 0) continue;
+      ok = warp_wait(kv_full, tk & 1);
+      for (int i = 0; i < n && ok; ++i, ++gi) {
+        const int si = gi % NS, x = gi & 1;
+        if (gi - done == 2) product_g();
+        ok = ok && warp_wait(q_full + si, (gi / NS) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_kk<KB>(tm + x * kNR, dK, kPiece, desc_at(dQ, si * QP), kQPiece, IDESC_S);
+          mma_kk<KB>(tm + 128 + x * kNR, dV, kPiece, desc_at(dO, si * QP), kQPiece, IDESC_S);
+          mma_commit(s_full + x);
+          if (i == n - 1) mma_commit(kv_empty);
+        }
+        __syncwarp();
+        if (x) {
+          due_item[1] = tk;
+          due_i[1] = i;
+        } else {
+          due_item[0] = tk;
+          due_i[0] = i;
+        }
+      }
+      ++tk;
+    }
+    while (ok && done < gi) product_g();
+    for (int k = 1; k <= 2 && k <= gi; ++k) {  // every product done before TMEM is given up
+      const int c = gi - k;
+      if (ok) ok = warp_wait(p_done + (c & 1), (c >> 1) & 1);
+      if (!ok) {
+        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(p_done + (c & 1), (c >> 1) & 1, 200);
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- p and ds
-    const int r = (warp & 3) * 32 + lane, half = warp >> 2;  // key, 32 of the 64 columns
-    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const int r = (warp & 3) * 32 + lane, part = (warp >> 2) & 1;  // key, 32 of 64 columns
+    const int x = warp >> 3;                                       // group
+    const int tid = threadIdx.x & 255;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + 128;
     const int blk = r / g.block;
+    const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
     int gi = 0;
     for (int ti = 0;; ++ti) {
       const int slot = ti & 1;
@@ -705,111 +751,101 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       if (f.item < 0) break;
       const int pos = f.pos + r;
       const bool valid = r < f.n;
-      for (int st = 0; st < f.steps; ++st, ++gi) {
-        const int si = gi % NS, b = gi & 1, pb = gi % NP;
-        ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
-        ok = ok && warp_wait(q_full + si, (gi / NS) & 1);  // the statistics and boxes
+      for (int i = (gi ^ x) & 1; i < f.steps; i += 2) {
+        const int c = gi + i, si = c % NS;
+        ok = ok && warp_wait(s_full + x, (c >> 1) & 1);
+        ok = ok && warp_wait(q_full + si, (c / NS) & 1);  // the statistics and boxes
         if (!ok) break;
         tc_fence_after();
-        float sv[32], dv[32];
-        tmem_ld32(tS + b * kNR + lane_off + half * 32, sv);
-        tmem_ld32(tP + b * kNR + lane_off + half * 32, dv);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + b);
         const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
-        // this key's columns of the step
+        // this key's columns of the step; pairs that do not exist: zeros in Q and dO
         uint32_t see = 0;
+        bool zeros = false;
         for (int j = 0; j < p.boxes; ++j) {
-          const int c0 = j * p.br - half * 32;
+          const Box y = box[j];
+          zeros = zeros || y.rows < p.br;
+          const int c0 = j * p.br - part * 32;
           if (c0 >= 32 || c0 + p.br <= 0) continue;
-          const Box x = box[j];
-          if (!valid || !((x.mask >> blk) & 1)) continue;
+          if (!valid || !((y.mask >> blk) & 1)) continue;
           // query t of the box sees positions below end + t
-          const int t0 = max(0, pos - x.end + 1);
-          const int lo = max(c0 + (t0 < p.bt ? t0 * p.bh : p.br), 0), hi = min(c0 + x.rows, 32);
+          const int t0 = max(0, pos - y.end + 1);
+          const int lo = max(c0 + (t0 < p.bt ? t0 * p.bh : p.br), 0), hi = min(c0 + y.rows, 32);
           if (hi > lo) see |= (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1) << lo);
         }
-        if (gi >= NP) ok = ok && warp_wait(p_done + pb, ((gi / NP) - 1) & 1);
-        if (!ok) break;
-        // pairs that do not exist: zeros in Q and dO
-        for (int j = 0; j < p.boxes; ++j) {
-          const int n = box[j].rows;
-          if (n == p.br) continue;
-          for (int o = 0; o < 2 * KB; ++o) {
-            uint4* x = reinterpret_cast<uint4*>(sm + (o < KB ? M::Q : M::O) + si * QP +
-                                                (o % KB) * kQPiece + j * p.br * 128);
-            for (int i = n * 8 + threadIdx.x; i < p.br * 8; i += kKvWarps * 32)
-              x[i] = make_uint4(0, 0, 0, 0);
+        if (zeros) {
+          for (int j = 0; j < p.boxes; ++j) {
+            const int n = box[j].rows;
+            for (int o = 0; o < 2 * KB; ++o) {
+              uint4* q = reinterpret_cast<uint4*>(sm + (o < KB ? M::Q : M::O) + si * QP +
+                                                  (o % KB) * kQPiece + j * p.br * 128);
+              for (int k = n * 8 + tid; k < p.br * 8; k += 256) q[k] = make_uint4(0, 0, 0, 0);
+            }
           }
+          fence_proxy_async();
         }
-        const float4* stat = reinterpret_cast<const float4*>(sm + M::STAT + (si * kNR + half * 32) * 8);
-        uint8_t* pr = sm + M::P + pb * kPiece + r * 128;
-        uint8_t* dr = sm + M::DS + pb * kPiece + r * 128;
+        const float4* stat =
+            reinterpret_cast<const float4*>(sm + M::STAT + (si * kNR + part * 32) * 8);
         const bool full = __all_sync(0xffffffffu, see == 0xffffffffu);
         const float2 qm = f2s(g.qmul);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t wp[4], wd[4];
+        for (int h = 0; h < 2; ++h) {  // 16 columns
+          float sv[16], dv[16], wp[8], wd[8];
+          tmem_ld16(tS + h * 16, sv);
+          tmem_ld16(tP + h * 16, dv);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = q * 8 + 2 * e;
-            const float4 a = stat[j / 2];  // (lse, Delta) of columns j, j + 1
-            const float2 z = f2fma(make_float2(sv[j], sv[j + 1]), qm, make_float2(-a.x, -a.z));
+          for (int j = 0; j < 8; ++j) {
+            const float4 a = stat[h * 8 + j];  // (lse, Delta) of columns 2 j, 2 j + 1
+            const float2 z =
+                f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, make_float2(-a.x, -a.z));
             float2 y = make_float2(ex2(z.x), ex2(z.y));
-            float2 ds = f2mul(y, f2add(make_float2(dv[j], dv[j + 1]), make_float2(-a.y, -a.w)));
+            float2 ds =
+                f2mul(y, f2add(make_float2(dv[2 * j], dv[2 * j + 1]), make_float2(-a.y, -a.w)));
             if (!full) {
-              const bool s0 = (see >> j) & 1u, s1 = (see >> (j + 1)) & 1u;
+              const bool s0 = (see >> (h * 16 + 2 * j)) & 1u, s1 = (see >> (h * 16 + 2 * j + 1)) & 1u;
               y.x = s0 ? y.x : 0.f;
               y.y = s1 ? y.y : 0.f;
               ds.x = s0 ? ds.x : 0.f;
               ds.y = s1 ? ds.y : 0.f;
             }
-            wp[e] = bf16x2_bits(y.x, y.y);
-            wd[e] = bf16x2_bits(ds.x, ds.y);
+            wp[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
+            wd[j] = __uint_as_float(bf16x2_bits(ds.x, ds.y));
           }
-          const int at = ((half * 4 + q) ^ (r & 7)) * 16;
-          *reinterpret_cast<uint4*>(pr + at) = make_uint4(wp[0], wp[1], wp[2], wp[3]);
-          *reinterpret_cast<uint4*>(dr + at) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+          tmem_st8(tS + h * 16, wp);
+          tmem_st8(tP + h * 16, wd);
         }
-        fence_proxy_async();
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + pb);
+        if (lane == 0) mbar_arrive(p_full + x);
       }
       if (!ok) break;
+      gi += f.steps;
       const bool some = f.steps > 0;
-      if (some) {
-        ok = warp_wait(p_done + (gi - 1) % NP, ((gi - 1) / NP) & 1);
+      if (some) {  // the last product follows all others
+        ok = warp_wait(p_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
       }
+      // group 0 writes dV, group 1 dK; DP / 2 columns a thread
       const int64_t krow = (int64_t(f.kbeg + r) * g.Hkv + f.kh) * g.D;
-#pragma unroll
-      for (int c = 0; c < 2 * DP / 64; ++c) {  // dV, then dK; DP / 2 columns each per half
-        const int which = c / (DP / 64);
-        const int col = half * (DP / 2) + (c % (DP / 64)) * 32;
+#pragma unroll 1
+      for (int c = 0; c < DP / 64; ++c) {
+        const int col = part * (DP / 2) + c * 32;
         float o[32];
         __syncwarp();
         if (some) {
-          tmem_ld32((which ? tK : tV) + lane_off + col, o);
+          tmem_ld32(tmem + lanes + 256 + x * DP + col, o);
           tmem_wait_ld();
         }
         if (valid && f.slot < 0) {
-          const float mul = which ? g.scale : 1.f;
-          __nv_bfloat16* out =
-              static_cast<__nv_bfloat16*>(which ? p.b.dK : p.b.dV) + krow + col;
+          const float mul = x ? g.scale : 1.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * mul : 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (col + q * 8 < g.D)
-              *reinterpret_cast<uint4*>(out + q * 8) = make_uint4(
-                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
-                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+          store_row(static_cast<__nv_bfloat16*>(x ? p.b.dK : p.b.dV) + krow, col, g.D, o,
+                    x ? wide_k : wide_v);
         } else if (valid) {
-          float* out = p.b.part + (int64_t(f.slot) * 2 + (which ? 0 : 1)) * kT * g.D +
+          float* out = p.b.part + (int64_t(f.slot) * 2 + (x ? 0 : 1)) * kT * g.D +
                        int64_t(r) * g.D + col;
 #pragma unroll
           for (int q = 0; q < 8; ++q)

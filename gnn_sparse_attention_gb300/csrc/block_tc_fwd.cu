@@ -15,8 +15,9 @@
 // P V and next scores.  P in TMEM instead of shared memory takes 64 KB of the
 // step's 160 KB of shared-memory traffic away (128 bytes a clock would
 // otherwise be the bound at D = 128) and leaves room for a third stage.
-// Roles: warps 0-7 softmax, warp 8 issues the products, warp 9 resolves block
-// lists and issues TMA; every hand-over is an mbarrier, every wait is bounded.
+// Roles: warps 0-7 softmax, warp 8 issues the products, warp 9 issues TMA, warp
+// 10 resolves the next tile's block list meanwhile (a chain of dependent loads of
+// two microseconds); every hand-over is an mbarrier, every wait is bounded.
 //
 // With the list ascending, the keys that a row sees are the first columns of
 // its steps (list_keys), so the mask is one number per row and only the
@@ -46,7 +47,7 @@ __device__ int g_err;  // a bounded wait gave up
 constexpr int kT = kBlkTile;
 constexpr int kPiece = kT * 128;       // 128 rows x 64 bf16 columns
 constexpr int kSoftWarps = 8;           // two streams of four
-constexpr int kThr = (kSoftWarps + 2) * 32;
+constexpr int kThr = (kSoftWarps + 3) * 32;
 
 struct TcFwdParams {
   CUtensorMap mq, mk, mv;
@@ -121,12 +122,12 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
   TileInfo* info = reinterpret_cast<TileInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
   const BlockGeom& g = p.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(tile_full + i, 1);
-      mbar_init(tile_empty + i, kSoftWarps + 1);
+      mbar_init(tile_empty + i, kSoftWarps + 2);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kSoftWarps / 2);
       mbar_init(pv_done + i, 1);
@@ -152,15 +153,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
   const uint32_t tmem = *s_tmem;
   bool ok = true;  // false: a wait gave up, leave
 
-  if (warp == kSoftWarps + 1) {
-    // ---------------------------------------------------------------- producer
-    const int per = kT / g.block;  // blocks per step
-    const uint32_t blk_bytes = uint32_t(g.block) * 128;
-    int gi = 0, ti = 0, tq = 0;
+  if (warp == kSoftWarps + 2) {
+    // ---------------------------------------------------------------- lists
+    int ti = 0;
     for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
-      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
-      if (!ok) break;
       int64_t x = t;
       const int sp = int(x % p.nsplit);
       x /= p.nsplit;
@@ -169,6 +166,8 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       const int u = int(x % g.U), kh = int(x / g.U);
       const Unit un = unit_at(g, u);
       const Span ks = span_k(g, un.s);
+      if (ti >= 2) ok = warp_wait(tile_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
       int* list = ids + slot * kBlkMaxTopk;
       int n = 0;
       if (un.n > 0)
@@ -200,35 +199,52 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(tile_full + slot);
-      if (s1 <= s0) continue;
-      const int qs = tq % NQ;
-      if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+    }
+  } else if (warp == kSoftWarps + 1) {
+    // ---------------------------------------------------------------- copies
+    const int per = kT / g.block;  // blocks per step
+    const uint32_t blk_bytes = uint32_t(g.block) * 128;
+    int gi = 0, ti = 0, tq = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      ok = warp_wait(tile_full + slot, (ti >> 1) & 1);
       if (!ok) break;
-      ++tq;
-      if (lane == 0) {
-        mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 128 * KB);
-        for (int kb = 0; kb < KB; ++kb)
-          tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, kh * g.G + hsub * p.ht,
-                     un.row, q_full + qs);
+      const TileInfo& f = info[slot];
+      const int* list = ids + slot * kBlkMaxTopk;
+      const int s0 = f.s0, s1 = f.s1, n = f.n, kbeg = f.kbeg, kh = f.kh;
+      if (s1 > s0) {
+        const int qs = tq % NQ;
+        if (tq >= NQ) ok = warp_wait(q_empty + qs, ((tq / NQ) - 1) & 1);
+        if (!ok) break;
+        ++tq;
+        if (lane == 0) {
+          mbar_expect_tx(q_full + qs, uint32_t(p.rows) * 128 * KB);
+          for (int kb = 0; kb < KB; ++kb)
+            tma_tile3d(sm + M::Q + qs * OP + kb * kPiece, &p.mq, kb * 64, f.h0, f.row,
+                       q_full + qs);
+        }
       }
       for (int st = s0; st < s1; ++st, ++gi) {
-        const int ks_i = gi % NS;
+        const int si = gi % NS;
         const int nb = min(per, n - st * per);  // blocks of this step
         for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* full = (kv ? v_full : k_full) + ks_i;
-          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + ks_i, ((gi / NS) - 1) & 1);
+          uint64_t* full = (kv ? v_full : k_full) + si;
+          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / NS) - 1) & 1);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
           __syncwarp();
-          for (int e = lane; e < nb * KB; e += 32) {
-            const int b = e / KB, kb = e % KB;
-            tma_tile3d(sm + (kv ? M::V : M::K) + ks_i * OP + kb * kPiece + b * blk_bytes,
-                       kv ? &p.mv : &p.mk, kb * 64, kh, ks.beg + list[st * per + b] * g.block,
+          if (lane < nb * KB) {
+            const int b = lane / KB, kb = lane % KB;
+            tma_tile3d(sm + (kv ? M::V : M::K) + si * OP + kb * kPiece + b * blk_bytes,
+                       kv ? &p.mv : &p.mk, kb * 64, kh, kbeg + list[st * per + b] * g.block,
                        full);
           }
         }
         if (!ok) break;
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int i = 1; i <= NQ && i <= tq; ++i)
@@ -240,74 +256,78 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     }
   } else if (warp == kSoftWarps) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_O = f16_idesc(kT, DP, true);
-      // Step gi belongs to stream gi & 1.  Its scores are issued after the P V
-      // of step gi - 2 (products run in the order of their issue), so the
-      // stream's P is no longer needed when they overwrite it.
-      struct Due {
-        int gi, tile;     // gi < 0: none
-        bool first, head;  // first of the stream in its tile, of the tile
-      } due[2] = {{-1, 0, false, false}, {-1, 0, false, false}};
-      int gi = 0, ti = 0, tq = 0;
-      auto product_pv = [&](Due& d) {
-        if (d.gi < 0) return;
-        const int si = d.gi % NS, x = d.gi & 1, buf = d.tile % NO;
-        ok = ok && mbar_wait(p_full + x, (d.gi >> 1) & 1) &&
-             mbar_wait(v_full + si, (d.gi / NS) & 1);
-        if (d.head && d.tile >= NO) ok = ok && mbar_wait(o_empty + buf, (d.tile / NO - 1) & 1);
-        if (ok) {
-          tc_fence_after();
-          mma_tm<kT>(tmem + M::out_col(x, buf), tmem + x * kT, 64, 64, sm + M::V + si * OP, kPiece,
-                     IDESC_O, !d.first);
-          mma_commit(pv_done + x);
-          mma_commit(v_empty + si);
-        }
-        d.gi = -1;
-      };
-      auto drain = [&]() {
-        product_pv(due[gi & 1]);
-        product_pv(due[(gi & 1) ^ 1]);
-      };
-      for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
-        const int slot = ti & 1;
-        if (!mbar_test(tile_full + slot, (ti >> 1) & 1)) {
-          drain();  // the producer may wait for the tiles that these belong to
-          ok = ok && mbar_wait(tile_full + slot, (ti >> 1) & 1);
-        }
+    constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_O = f16_idesc(kT, DP, true);
+    const uint64_t dQ = desc_k(sm + M::Q), dK = desc_k(sm + M::K), dV = desc_mn(sm + M::V, kPiece);
+    const uint32_t tm = uniform(tmem);
+    // Step gi belongs to stream gi & 1.  Its scores are issued after the P V
+    // of step gi - 2 (products run in the order of their issue), so the
+    // stream's P is no longer needed when they overwrite it.  The last two steps'
+    // P V are due: step gi - 1 and gi - 2, in tiles of `tile` steps.
+    int gi = 0, ti = 0, tq = 0, done = 0;       // steps with scores, tiles, with P V
+    int due_tile[2] = {0, 0}, due_i[2] = {0, 0};  // by stream: the tile, the step in it
+    auto product_pv = [&]() {                   // of step `done`
+      const int x = done & 1, si = done % NS, tile = x ? due_tile[1] : due_tile[0];
+      const int i = x ? due_i[1] : due_i[0], buf = tile % NO;
+      ok = ok && warp_wait(p_full + x, (done >> 1) & 1) && warp_wait(v_full + si, (done / NS) & 1);
+      if (i == 0 && tile >= NO) ok = ok && warp_wait(o_empty + buf, (tile / NO - 1) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tm<kT>(tm + M::out_col(x, buf), tm + x * kT, 64, 64, desc_at(dV, si * OP), IDESC_O,
+                   i >= 2);
+        mma_commit(pv_done + x);
+        mma_commit(v_empty + si);
+      }
+      __syncwarp();
+      ++done;
+    };
+    for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      if (!__all_sync(0xffffffffu, mbar_test(tile_full + slot, (ti >> 1) & 1))) {
+        while (ok && done < gi) product_pv();  // the lists may wait for these tiles to be written
+        ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      }
+      if (!ok) break;
+      const int n = uniform(info[slot].s1 - info[slot].s0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
+      if (n <= 0) continue;
+      const int qs = tq % NQ;
+      ok = warp_wait(q_full + qs, (tq / NQ) & 1);
+      for (int i = 0; i < n && ok; ++i, ++gi) {
+        const int si = gi % NS, x = gi & 1;
+        if (gi - done == 2) product_pv();
+        ok = ok && warp_wait(k_full + si, (gi / NS) & 1);
         if (!ok) break;
-        const int n = info[slot].s1 - info[slot].s0;
-        mbar_arrive(tile_empty + slot);
-        if (n <= 0) continue;
-        const int qs = tq % NQ;
-        ok = mbar_wait(q_full + qs, (tq / NQ) & 1);
-        for (int i = 0; i < n && ok; ++i, ++gi) {
-          const int si = gi % NS, x = gi & 1;
-          product_pv(due[x]);
-          ok = ok && mbar_wait(k_full + si, (gi / NS) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          mma_kk<KB>(tmem + x * kT, sm + M::Q + qs * OP, kPiece, sm + M::K + si * OP, kPiece,
+        tc_fence_after();
+        if (elect_one()) {
+          mma_kk<KB>(tm + x * kT, desc_at(dQ, qs * OP), kPiece, desc_at(dK, si * OP), kPiece,
                      IDESC_S);
           mma_commit(s_full + x);
           mma_commit(k_empty + si);
           if (i == n - 1) mma_commit(q_empty + qs);
-          due[x] = Due{gi, tq, i < 2, i == 0};
         }
-        ++tq;
+        __syncwarp();
+        if (x) {
+          due_tile[1] = tq;
+          due_i[1] = i;
+        } else {
+          due_tile[0] = tq;
+          due_i[0] = i;
+        }
       }
-      if (ok) drain();
-      // every product has completed before TMEM is given up
-      for (int k = 1; k <= 2 && k <= gi; ++k) {
-        const int c = gi - k;
-        if (ok) ok = mbar_wait(pv_done + (c & 1), (c >> 1) & 1);
-        if (!ok) {
-          mbar_wait(s_full + (c & 1), (c >> 1) & 1, 200);
-          mbar_wait(pv_done + (c & 1), (c >> 1) & 1, 200);
-        }
+      ++tq;
+    }
+    while (ok && done < gi) product_pv();
+    // every product has completed before TMEM is given up
+    for (int k = 1; k <= 2 && k <= gi; ++k) {
+      const int c = gi - k;
+      if (ok) ok = warp_wait(pv_done + (c & 1), (c >> 1) & 1);
+      if (!ok) {
+        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(pv_done + (c & 1), (c >> 1) & 1, 200);
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax
     const int quad = warp & 3, x = warp >> 2;  // TMEM lane quarter, stream
@@ -315,6 +335,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     const uint32_t lanes = uint32_t(quad * 32) << 16;
     const uint32_t tS = tmem + lanes + x * kT;
     float* red = reinterpret_cast<float*>(sm + M::RED);
+    const bool wide = wide_rows(p.out, g.D);
     int gi = 0, ti = 0, to = 0;  // steps, tiles, tiles with steps
     const int th = r % p.ht, tt = r / p.ht;
     // the two warps of these rows (one per stream) have written; both may read
@@ -517,13 +538,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
               *reinterpret_cast<float4*>(d + q * 4) =
                   make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
         } else if (valid) {
-          __nv_bfloat16* d = p.out + qrow * g.D + col;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (col + q * 8 < g.D)
-              *reinterpret_cast<uint4*>(d + q * 8) = make_uint4(
-                  bf16x2_bits(o[q * 8], o[q * 8 + 1]), bf16x2_bits(o[q * 8 + 2], o[q * 8 + 3]),
-                  bf16x2_bits(o[q * 8 + 4], o[q * 8 + 5]), bf16x2_bits(o[q * 8 + 6], o[q * 8 + 7]));
+          store_row(p.out + qrow * g.D, col, g.D, o, wide);
         }
       }
       if (valid && x == 0) {
