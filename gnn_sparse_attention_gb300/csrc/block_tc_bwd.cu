@@ -414,7 +414,7 @@ namespace {
 constexpr int kNR = 64;               // query pairs per step
 constexpr int kQPiece = kNR * 128;    // 64 rows x 64 bf16 columns
 constexpr int kKvWarps = 16;          // two groups of eight, steps in turn
-constexpr int kKvThr = (kKvWarps + 2) * 32;
+constexpr int kKvThr = (kKvWarps + 3) * 32;
 constexpr int kList = 256;            // units resolved at a time (8 bitmap words)
 
 struct DkvParams {
@@ -423,12 +423,14 @@ struct DkvParams {
   int bh, bt;      // heads and query rows of a box
   int br, boxes;   // pairs of a box, boxes of a step
   int ub;          // boxes of a unit
+  int l_bh, l_hn, l_qb;  // log2 of bh, of a unit's head groups, of q_block
 };
 
 struct Box {
   int mask;        // blocks of the key tile that the unit chose
   int end;         // first position that the box's first query does not see
   int rows;        // pairs of the box that exist
+  int row, h0;     // first query row, first head
 };
 
 struct KvInfo {
@@ -452,19 +454,13 @@ struct KvSm {
   static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
   static constexpr int INFO = LIST + kList * 8;
   static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
-  static constexpr int NBAR = 4 + 2 + 2 * NS + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 4 + 2 + 3 * NS + 2 + 2 + 2;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
   // TMEM: S^T [0, 128) and dP^T [128, 256) in two buffers, dV, dK from 256 on
 };
 
-// more bytes to wait for in the barrier's phase, without an arrival
-__device__ __forceinline__ void mbar_add_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
 // arrive once this thread's cp.async copies so far have landed
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
@@ -483,8 +479,8 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
            *kv_empty = kv_full + 1, *q_full = kv_empty + 1, *q_empty = q_full + NS,
-           *s_full = q_empty + NS, *p_full = s_full + 2, *p_done = p_full + 2,
-           *g_empty = p_done + 2;
+           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + 2,
+           *g_full = p_full + 2, *g_empty = g_full + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
   int2* list = reinterpret_cast<int2*>(sm + M::LIST);
@@ -494,16 +490,17 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, kKvWarps + 1);
+      mbar_init(item_empty + i, kKvWarps + 2);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kKvWarps / 2);
-      mbar_init(p_done + i, 1);
     }
+    mbar_init(g_full, 1);
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(q_full + i, 1 + 32);  // the copies' bytes, and each lane's statistics
       mbar_init(q_empty + i, 1);
+      mbar_init(box_full + i, 1);
     }
     mbar_init(g_empty, kKvWarps);
     mbar_init_fence();
@@ -515,19 +512,18 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   const uint32_t tmem = *s_tmem;
   bool ok = true;
 
-  if (warp == kKvWarps + 1) {
-    // ---------------------------------------------------------------- producer
+  if (warp == kKvWarps + 2) {
+    // ---------------------------------------------------------------- lists
     const int64_t n_items = p.b.head[0];
-    int gi = 0, ti = 0, tk = 0;
-    for (;; ++ti) {
+    int gi = 0;
+    for (int ti = 0;; ++ti) {
       int it = 0;
       if (lane == 0) it = atomicAdd(p.b.head + 1, 1);
-      it = __shfl_sync(0xffffffffu, it, 0);
+      it = uniform(it);
       const int slot = ti & 1;
-      if (ti >= 2) ok = warp_wait(item_empty + slot, ((ti >> 1) - 1) & 1);
-      if (!ok) break;
       if (it >= n_items) {
-        if (lane == 0) {
+        if (ti >= 2) ok = warp_wait(item_empty + slot, ((ti >> 1) - 1) & 1);
+        if (ok && lane == 0) {
           info[slot].item = -1;
           mbar_arrive(item_full + slot);
         }
@@ -541,8 +537,9 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       const int nb = min(kT / g.block, (ks.len + g.block - 1) / g.block - pos / g.block);
       const int brow = min(piece_base(g.seq_k, s, g.block) + pos / g.block, g.B - nb);
       const int ub = piece_base(g.seq_q, s, g.qb), nu = (qs.len + g.qb - 1) / g.qb;
-      const int64_t all_boxes = int64_t(q.z) * p.ub;
-      const int steps = int((all_boxes + p.boxes - 1) / p.boxes);
+      const int steps = int((int64_t(q.z) * p.ub + p.boxes - 1) / p.boxes);
+      if (ti >= 2) ok = warp_wait(item_empty + slot, ((ti >> 1) - 1) & 1);
+      if (!ok) break;
       if (lane == 0) {
         KvInfo& f = info[slot];
         f.item = it;
@@ -554,17 +551,6 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         f.slot = q.w;
         mbar_arrive(item_full + slot);
       }
-      if (steps == 0) continue;
-      if (tk >= 1) ok = warp_wait(kv_empty, (tk - 1) & 1);
-      if (!ok) break;
-      ++tk;
-      if (lane == 0) {
-        mbar_expect_tx(kv_full, 2 * KB * kPiece);
-        for (int kb = 0; kb < KB; ++kb) {
-          tma_tile3d(sm + M::K + kb * kPiece, &p.mk, kb * 64, kh, ks.beg + pos, kv_full);
-          tma_tile3d(sm + M::V + kb * kPiece, &p.mv, kb * 64, kh, ks.beg + pos, kv_full);
-        }
-      }
       // units in ascending order: the set bits of the blocks' rows, 8 words at a time
       int w0 = ub / 32, seen = 0;   // next word, units before it
       int have = 0, next = 0;       // resolved units, the next one of them
@@ -573,7 +559,6 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         const int si = gi % NS;
         if (gi >= NS) ok = warp_wait(q_empty + si, ((gi / NS) - 1) & 1);
         if (!ok) break;
-        // each box announces its bytes; lane 0's own arrival comes last
         Box* box = reinterpret_cast<Box*>(sm + M::BOX) + si * kNR;
         for (int j = 0; j < p.boxes; ++j) {
           while (next >= have && seen < q.y + q.z && w0 <= (ub + nu - 1) / 32) {
@@ -611,55 +596,82 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
             seen += all;
             w0 += 8;
           }
-          Box x{0, 0, 0};
-          int64_t qrow = 0;
-          int h0 = kh * g.G;
+          Box x{0, 0, 0, 0, 0};
           if (next < have) {
             const int2 e = list[next];
-            const int64_t off = int64_t(e.x - ub) * g.qb;
-            const int hn = g.G / p.bh;                       // head groups of a unit
-            const int t0 = (sub / hn) * p.bt;
-            h0 += (sub % hn) * p.bh;
+            const int unit = e.x - ub;                       // of the sequence
+            const int off = unit << p.l_qb;
+            const int t0 = (sub >> p.l_hn) * p.bt;
             // (a unit outside the sequence: only where offsets lie about the tables)
-            const int n = off >= 0 && off < qs.len
-                              ? clampi(min(g.qb, qs.len - int(off)) - t0, 0, p.bt) : 0;
+            const int n =
+                unit >= 0 && unit < nu ? clampi(min(g.qb, qs.len - off) - t0, 0, p.bt) : 0;
             x.mask = e.y;
-            x.rows = n * p.bh;
-            x.end = g.causal ? int(off) + t0 + ks.len - qs.len + 1 : INT32_MAX / 2;
-            qrow = n > 0 ? qs.beg + off + t0 : 0;
+            x.rows = n << p.l_bh;
+            x.end = g.causal ? off + t0 + ks.len - qs.len + 1 : INT32_MAX / 2;
+            x.row = qs.beg + off + t0;
+            x.h0 = kh * g.G + ((sub & ((1 << p.l_hn) - 1)) << p.l_bh);
             if (++sub == p.ub) {
               sub = 0;
               ++next;
             }
           }
           if (lane == 0) box[j] = x;
-          if (x.rows > 0) {
-            const int at = j * p.br;
-            if (lane == 0) {
-              mbar_add_tx(q_full + si, uint32_t(p.br) * 256 * KB);
-              for (int kb = 0; kb < KB; ++kb) {
-                tma_tile3d(sm + M::Q + si * QP + kb * kQPiece + at * 128, &p.mq, kb * 64, h0,
-                           int(qrow), q_full + si);
-                tma_tile3d(sm + M::O + si * QP + kb * kQPiece + at * 128, &p.mo, kb * 64, h0,
-                           int(qrow), q_full + si);
-              }
-            }
-            for (int i = lane; i < x.rows; i += 32)
-              cp_async8(sm + M::STAT + (si * kNR + at + i) * 8,
-                        p.b.stat + (qrow + i / p.bh) * g.H + h0 + i % p.bh);
-          }
+          for (int i = lane; i < x.rows; i += 32)
+            cp_async8(sm + M::STAT + (si * kNR + j * p.br + i) * 8,
+                      p.b.stat + int64_t(x.row + (i >> p.l_bh)) * g.H + x.h0 + (i & (p.bh - 1)));
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(box_full + si);
         cp_async_arrive(q_full + si);
-        if (lane == 0) mbar_arrive(q_full + si);
       }
       if (!ok) break;
     }
-    if (!ok) {
+    cp_async_wait<0>();
+  } else if (warp == kKvWarps + 1) {
+    // ---------------------------------------------------------------- copies
+    int gi = 0, tk = 0;
+    for (int ti = 0;; ++ti) {
+      const int slot = ti & 1;
+      ok = warp_wait(item_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const KvInfo f = info[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + slot);
+      if (f.item < 0) break;
+      if (f.steps == 0) continue;
+      if (tk >= 1) ok = warp_wait(kv_empty, (tk - 1) & 1);
+      if (!ok) break;
+      ++tk;
+      if (lane == 0) mbar_expect_tx(kv_full, 2 * KB * kPiece);
+      __syncwarp();
+      if (lane < 2 * KB)
+        tma_tile3d(sm + (lane & 1 ? M::V : M::K) + (lane >> 1) * kPiece, lane & 1 ? &p.mv : &p.mk,
+                   (lane >> 1) * 64, f.kh, f.kbeg, kv_full);
+      for (int st = 0; st < f.steps; ++st, ++gi) {
+        const int si = gi % NS;
+        ok = warp_wait(box_full + si, (gi / NS) & 1);  // it waited for the stage to be free
+        if (!ok) break;
+        const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
+        int full = 0;  // boxes with pairs: all of them but at an item's end
+        for (int j = lane; j < p.boxes; j += 32) full += box[j].rows > 0;
+        full = p.boxes == 1 ? uniform(full) : __reduce_add_sync(0xffffffffu, full);
+        if (lane == 0) mbar_expect_tx(q_full + si, uint32_t(full * p.br) * 256 * KB);
+        __syncwarp();
+        for (int e = lane; e < p.boxes * 2 * KB; e += 32) {
+          const int j = e / (2 * KB), o = e & 1, kb = (e >> 1) % KB;
+          const Box x = box[j];
+          if (x.rows > 0)
+            tma_tile3d(sm + (o ? M::O : M::Q) + si * QP + kb * kQPiece + j * p.br * 128,
+                       o ? &p.mo : &p.mq, kb * 64, x.h0, x.row, q_full + si);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       if (tk > 0) warp_wait(kv_full, (tk - 1) & 1, 200);
       for (int c = gi; c > gi - NS && c >= 0; --c) warp_wait(q_full + c % NS, (c / NS) & 1, 200);
     }
-    cp_async_wait<0>();
   } else if (warp == kKvWarps) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false), IDESC_G = f16_idesc(kT, DP, true);
@@ -671,6 +683,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     // issued before them and run in that order.
     int gi = 0, tk = 0, done = 0;
     int due_item[2] = {0, 0}, due_i[2] = {0, 0};
+    bool due_last[2] = {false, false};
     auto product_g = [&]() {  // of step `done`
       const int x = done & 1, si = done % NS;
       const int item = x ? due_item[1] : due_item[0], i = x ? due_i[1] : due_i[0];
@@ -682,8 +695,10 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         mma_tm<kNR>(tm + 256, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
         mma_tm<kNR>(tm + 256 + DP, tm + 128 + x * kNR, 16, 16, desc_at(dQm, si * QP), IDESC_G,
                     i > 0);
-        mma_commit(p_done + x);
         mma_commit(q_empty + si);
+        // (a barrier of its own: a group that has no part in the last steps
+        // would otherwise wait for a phase two ahead, which reads as complete)
+        if (x ? due_last[1] : due_last[0]) mma_commit(g_full);
       }
       __syncwarp();
       ++done;
@@ -717,20 +732,22 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         if (x) {
           due_item[1] = tk;
           due_i[1] = i;
+          due_last[1] = i == n - 1;
         } else {
           due_item[0] = tk;
           due_i[0] = i;
+          due_last[0] = i == n - 1;
         }
       }
       ++tk;
     }
     while (ok && done < gi) product_g();
-    for (int k = 1; k <= 2 && k <= gi; ++k) {  // every product done before TMEM is given up
-      const int c = gi - k;
-      if (ok) ok = warp_wait(p_done + (c & 1), (c >> 1) & 1);
-      if (!ok) {
+    // every product has completed before TMEM is given up
+    if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
+    if (!ok) {
+      for (int c = gi; c >= 0 && c > gi - 3; --c) {
         warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
-        warp_wait(p_done + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
       }
     }
   } else {
@@ -742,7 +759,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + 128;
     const int blk = r / g.block;
     const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
-    int gi = 0;
+    int gi = 0, to = 0;  // steps, items with steps
     for (int ti = 0;; ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
@@ -822,8 +839,8 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       if (!ok) break;
       gi += f.steps;
       const bool some = f.steps > 0;
-      if (some) {  // the last product follows all others
-        ok = warp_wait(p_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+      if (some) {
+        ok = warp_wait(g_full, to & 1);
         if (!ok) break;
         tc_fence_after();
       }
@@ -860,6 +877,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         if (some) mbar_arrive(g_empty);
         mbar_arrive(item_empty + slot);
       }
+      to += some;
     }
   }
   if (!ok) atomicOr(&g_err, 2);
@@ -911,6 +929,10 @@ gattn_status launch_block_bwd_tc(const BlockBwdParams& b, cudaStream_t st) {
     p.br = p.bt * p.bh;
     p.boxes = kNR / p.br;
     p.ub = (g.qb / p.bt) * (g.G / p.bh);
+    const auto log2i = [](int x) { return 31 - __builtin_clz(x); };
+    p.l_bh = log2i(p.bh);
+    p.l_hn = log2i(g.G / p.bh);
+    p.l_qb = log2i(g.qb);
     if (!encode_heads_map(&p.mq, Q, g.Nq, g.H, g.D, p.bh, p.bt) ||
         !encode_heads_map(&p.mo, dO, g.Nq, g.H, g.D, p.bh, p.bt) ||
         !encode_heads_map(&p.mk, K, g.Nk, g.Hkv, g.D, 1, kT) ||
