@@ -15,16 +15,22 @@
 // their deviation that rounding would be as large as the row).
 //
 // A row belongs to W warps; a thread holds E of its elements as 16-byte
-// vectors (single elements when a row is no multiple of 16 bytes).  The
-// forward takes E = 32 so that one warp covers 1,024 elements and needs no
-// block barrier; the backward takes E = 8 because it also carries five fp32
-// column sums per element (dw, db of both norms and the channel gate) over
-// all rows of its CTA, and fetches its next row while it reduces the current
-// one.  The column sums of the CTAs meet in a second small kernel, in CTA
-// order, so results do not vary from run to run.
+// vectors (single elements when a row is no multiple of 16 bytes).  Up to
+// 1,024 elements the forward gives a row to one warp (E up to 32) and needs no
+// block barrier.  Longer rows, and the backward, run as many CTAs as fit and
+// let each walk its rows: a thread then keeps its columns' weights in
+// registers (read per row they are more L1 traffic than the row is HBM
+// traffic), and copies its own elements of the next rows into shared memory
+// with cp.async, two rows ahead -- each thread reads back only what it copied,
+// so the ring needs no barrier, and the bytes in flight (80 KB an SM) do not
+// cost registers.  The backward also carries five fp32 column sums per element
+// (dw, db of both norms and the channel gate) over all rows of its CTA; the
+// CTAs' sums meet in a second small kernel, in CTA order, so results do not
+// vary from run to run.
 #include <algorithm>
 
 #include "attn_launch.cuh"
+#include "attn_pipe.cuh"
 
 namespace gattn {
 
@@ -253,6 +259,144 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_fwd_kernel(const N
   }
 }
 
+// A thread's own elements of NT tensors' rows, kStages rows deep in shared
+// memory: three or two rows, whatever fits CTAS times on an SM; rows too long
+// for two are read from global memory where they are used (kStages 0).
+// Elements past the row's end are zeros, written once.
+template <class T, int V, int E, int W, int NT, int CTAS>
+struct Ring {
+  using RW = Row<T, V, E, W>;
+  using R = typename RW::R;
+  static constexpr bool kAsync = V * sizeof(T) >= 4;  // cp.async moves 4, 8 or 16 bytes
+  static constexpr int kThreads = W == 1 ? 128 : W * 32;
+  static constexpr int kTensor = kThreads * RW::NV * int(sizeof(R));
+  static constexpr int kRoom = 200 * 1024 / CTAS;
+  static constexpr int kStages = 3 * NT * kTensor <= kRoom ? 3 : 2 * NT * kTensor <= kRoom ? 2 : 0;
+  static constexpr int kBytes = kStages * NT * kTensor;
+  uint8_t* base;
+  __device__ R* at(int stage, int tensor, int n) const {
+    return reinterpret_cast<R*>(base + (stage * NT + tensor) * kTensor) + n * kThreads + threadIdx.x;
+  }
+  __device__ void clear(int F, int t) {
+    for (int s = 0; s < kStages; ++s)
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int n = 0; n < RW::NV; ++n)
+          if (RW::col(n, t) >= F) *at(s, k, n) = Vec<T, V>::zero();
+  }
+  __device__ void fetch(int stage, int tensor, const void* src, int64_t row, int F, int t) {
+    const T* p = static_cast<const T*>(src) + row * F;
+#pragma unroll
+    for (int n = 0; n < RW::NV; ++n) {
+      const int c = RW::col(n, t);
+      if (c >= F) continue;
+      if constexpr (!kAsync) *at(stage, tensor, n) = *reinterpret_cast<const R*>(p + c);
+      else if constexpr (sizeof(R) == 16) cp_async16(at(stage, tensor, n), p + c);
+      else cp_async4(at(stage, tensor, n), p + c);
+    }
+  }
+  // the elements of `row`, the k-th that this CTA walks
+  __device__ void get(int k, int tensor, const void* src, int64_t row, int F, int t,
+                      float* f) const {
+    if constexpr (kStages == 0) {
+      R r[RW::NV];
+      RW::load(r, src, row, F, t);
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(r[n], f + n * V);
+    } else {
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n)
+        Vec<T, V>::get(*at(k % kStages, tensor, n), f + n * V);
+    }
+  }
+  __device__ void wait() const {
+    if constexpr (kStages > 0) cp_async_wait<kStages - 2>();
+  }
+};
+
+template <class T, int V, int E, int W>
+__device__ __forceinline__ void channels(const float* w, int F, int t, float none, float* f) {
+#pragma unroll
+  for (int n = 0; n < E / V; ++n) Row<T, V, E, W>::channel(w, n, F, t, none, f + n * V);
+}
+
+// CTAs per SM of the walking kernels: 64 registers a thread forward (E = 8), 128
+// backward
+template <int E, int W>
+constexpr int fwd_ctas() {
+  return E > 8 ? 1 : 1024 / (W * 32);
+}
+template <int W>
+constexpr int bwd_ctas() {
+  return W <= 4 ? 4 : 1;
+}
+
+// Forward of long rows: W > 1 warps a row, each CTA walks its rows.
+template <class T, int V, int E, int W, bool LN>
+__global__ void __launch_bounds__(W * 32, fwd_ctas<E, W>())
+    norm_fwd_walk_kernel(const NormParams p) {
+  using RW = Row<T, V, E, W>;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ float red[4 * W];
+  using Rg = Ring<T, V, E, W, 3, fwd_ctas<E, W>()>;
+  Rg ring{ring_mem};
+  int turn = 0;
+  const int t = threadIdx.x;
+  const bool token = p.gate_mode == kGateToken;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.N) {
+      ring.fetch(stage, 0, p.res, row, p.F, t);
+      if (p.x) ring.fetch(stage, 1, p.x, row, p.F, t);
+      if (p.x && token) ring.fetch(stage, 2, p.gate, row, p.F, t);
+    }
+    cp_async_commit();
+  };
+  ring.clear(p.F, t);
+  for (int s = 0; s < Rg::kStages - 1; ++s) fetch(blockIdx.x + int64_t(s) * gridDim.x, s);
+  constexpr bool KEEP = E <= 8;  // weights stay in registers
+  float wa[E], ba[E], wb[E], bb[E], gc[E];
+  auto weights = [&]() {
+    channels<T, V, E, W>(p.w_post, p.F, t, 0.f, wa);
+    channels<T, V, E, W>(p.b_post, p.F, t, 0.f, ba);
+    channels<T, V, E, W>(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr,
+                         p.F, t, 1.f, gc);
+    channels<T, V, E, W>(p.w_pre, p.F, t, 0.f, wb);
+    channels<T, V, E, W>(p.b_pre, p.F, t, 0.f, bb);
+  };
+  if (KEEP) weights();
+  int k = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, ++k) {
+    ring.wait();
+    float h[E];
+    ring.get(k, 0, p.res, row, p.F, t, h);
+    if (!KEEP) weights();
+    if (p.x) {
+      float u[E], g[E];
+      ring.get(k, 1, p.x, row, p.F, t, u);
+      if (token) ring.get(k, 2, p.gate, row, p.F, t, g);
+      if (p.w_post) {
+        const float2 s = row_stats<T, V, E, W, LN>(u, p, t, red, turn);
+        if (t == 0) reinterpret_cast<float2*>(p.stats + row)[0] = s;
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[e] = fmaf((u[e] - s.x) * s.y, wa[e], ba[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = fmaf(p.alpha * (token ? g[e] : gc[e]), u[e], h[e]);
+      RW::store(p.h, row, p.F, t, h);
+    }
+    if constexpr (Rg::kStages > 0)
+      fetch(row + (Rg::kStages - 1) * int64_t(gridDim.x), (k + Rg::kStages - 1) % Rg::kStages);
+    if (p.w_pre) {  // on h as it stands in fp32, not as rounded for the store
+      const float2 s = row_stats<T, V, E, W, LN>(h, p, t, red, turn);
+      if (t == 0) reinterpret_cast<float2*>(p.stats + row)[1] = s;
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = fmaf((h[e] - s.x) * s.y, wb[e], bb[e]);
+      RW::store(p.y, row, p.F, t, h);
+    }
+  }
+  cp_async_wait<0>();
+}
+
 // dx of a norm: g = dy * w, xh the normalised row, r = 1 / deviation
 //   dx = r (g - xh mean(g xh) - [LN] mean(g));  absent columns hold g = xh = 0
 template <int E, int W, bool LN>
@@ -271,127 +415,128 @@ __device__ __forceinline__ void norm_dx(float* g, const float* xh, float r, floa
 }
 
 template <class T, int V, int E, int W, bool LN>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, bwd_ctas<W>())
+    norm_bwd_kernel(const NormParams p) {
   using RW = Row<T, V, E, W>;
-  constexpr int NV = RW::NV;
-  using R = typename RW::R;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[W > 1 ? 4 * W : 1];
+  using Rg = Ring<T, V, E, W, 5, bwd_ctas<W>()>;
+  Rg ring{ring_mem};
   int turn = 0;
   const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t slot = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = W == 1 ? int64_t(gridDim.x) * 4 : gridDim.x;
   const bool has_x = p.x != nullptr, token = p.gate_mode == kGateToken;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.N) {
+      if (p.w_pre) {
+        ring.fetch(stage, 0, p.res, row, p.F, t);
+        ring.fetch(stage, 1, p.dy, row, p.F, t);
+      }
+      if (p.dh) ring.fetch(stage, 2, p.dh, row, p.F, t);
+      if (has_x) {
+        ring.fetch(stage, 3, p.x, row, p.F, t);
+        if (token) ring.fetch(stage, 4, p.gate, row, p.F, t);
+      }
+    }
+    cp_async_commit();
+  };
+  ring.clear(p.F, t);
+  for (int s = 0; s < Rg::kStages - 1; ++s) fetch(slot + s * step, s);
   float acc[kSums][E];
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
-
-  R rr[NV], dhr[NV], dyr[NV], xr[NV], gr[NV];
-  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto fetch = [&](int64_t row) {
-    st = p.cstats[row];
-    if (p.w_pre) {
-      RW::load(rr, p.res, row, p.F, t);
-      RW::load(dyr, p.dy, row, p.F, t);
-    }
-    if (p.dh) RW::load(dhr, p.dh, row, p.F, t);
-    if (has_x) {
-      RW::load(xr, p.x, row, p.F, t);
-      if (token) RW::load(gr, p.gate, row, p.F, t);
-    }
+  constexpr bool KEEP = E <= 8;  // weights stay in registers
+  float wa[E], ba[E], wb[E], gc[E];
+  auto weights = [&]() {
+    channels<T, V, E, W>(p.w_post, p.F, t, 0.f, wa);
+    channels<T, V, E, W>(p.b_post, p.F, t, 0.f, ba);
+    channels<T, V, E, W>(p.w_pre, p.F, t, 0.f, wb);
+    channels<T, V, E, W>(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr,
+                         p.F, t, 1.f, gc);
   };
-  if (slot < p.N) fetch(slot);
-  for (int64_t row = slot; row < p.N; row += step) {
-    // unpack this row (x becomes its normalised row, hh that of h, formed
-    // again as the forward did), then start on the next one's loads
-    float d[E], x[E], g[E], gy[E], hh[E];
-    const float4 s = st;
+  if (KEEP) weights();
+  float4 next = slot < p.N ? p.cstats[slot] : make_float4(0.f, 0.f, 0.f, 0.f);
+  int k = 0;
+  for (int64_t row = slot; row < p.N; row += step, ++k) {
+    const float4 s = next;
+    if (row + step < p.N) next = p.cstats[row + step];
+    ring.wait();
+    if (!KEEP) weights();
+    // x becomes its normalised row, u = norm(x); hh that of h, formed again
+    // as the forward did
+    float d[E], x[E], g[E];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const bool on = RW::col(n, t) < p.F;
-      float u[V], dy[V];
+    for (int e = 0; e < E; ++e) d[e] = x[e] = 0.f;
+    if (p.dh) ring.get(k, 2, p.dh, row, p.F, t, d);
+    if (has_x) {
+      ring.get(k, 3, p.x, row, p.F, t, x);
+      if (p.w_post) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = 0.f;
-      if (has_x) {
-        Vec<T, V>::get(xr[n], x + n * V);
-        if (token)
-          Vec<T, V>::get(gr[n], g + n * V);
-        else
-          RW::channel(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr, n,
-                      p.F, t, 1.f, g + n * V);
+        for (int n = 0; n < RW::NV; ++n)
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = x[n * V + e];
-        if (p.w_post) {
-          float w[V], b[V];
-          RW::channel(p.w_post, n, p.F, t, 0.f, w);
-          RW::channel(p.b_post, n, p.F, t, 0.f, b);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            x[n * V + e] = on ? (x[n * V + e] - s.x) * s.y : 0.f;
-            u[e] = fmaf(x[n * V + e], w[e], b[e]);
-          }
-        }
+          for (int e = 0; e < V; ++e)
+            x[n * V + e] = RW::col(n, t) < p.F ? (x[n * V + e] - s.x) * s.y : 0.f;
       }
-      if (p.w_pre) {
-        float h[V], w[V];
-        Vec<T, V>::get(rr[n], h);
-        Vec<T, V>::get(dyr[n], dy);
-        RW::channel(p.w_pre, n, p.F, t, 0.f, w);
+    }
+    if (token) {
+      ring.get(k, 4, p.gate, row, p.F, t, g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) g[e] = gc[e];
+    }
+    if (p.w_pre) {
+      float hh[E], gy[E];
+      ring.get(k, 0, p.res, row, p.F, t, hh);
+      ring.get(k, 1, p.dy, row, p.F, t, gy);
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n) {
+        const bool on = RW::col(n, t) < p.F;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const int i = n * V + e;
-          if (has_x) h[e] = fmaf(p.alpha * g[i], u[e], h[e]);
-          hh[i] = on ? (h[e] - s.z) * s.w : 0.f;
-          gy[i] = dy[e] * w[e];
-          acc[2][i] = fmaf(dy[e], hh[i], acc[2][i]);
-          acc[3][i] += dy[e];
+          if (has_x)
+            hh[i] = fmaf(p.alpha * g[i], p.w_post ? fmaf(x[i], wa[i], ba[i]) : x[i], hh[i]);
+          hh[i] = on ? (hh[i] - s.z) * s.w : 0.f;
+          acc[2][i] = fmaf(gy[i], hh[i], acc[2][i]);
+          acc[3][i] += gy[i];
+          gy[i] *= wb[i];
         }
       }
-      if (p.dh) {
-        Vec<T, V>::get(dhr[n], d + n * V);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[n * V + e] = 0.f;
-      }
-    }
-    if (row + step < p.N) fetch(row + step);
-    if (p.w_pre) {
       norm_dx<E, W, LN>(gy, hh, s.w, p.inv_f, red, turn);
 #pragma unroll
       for (int e = 0; e < E; ++e) d[e] += gy[e];
     }
+    // (this stage has been read; the one refilled was read a row ago)
+    if constexpr (Rg::kStages > 0)
+      fetch(row + (Rg::kStages - 1) * step, (k + Rg::kStages - 1) % Rg::kStages);
     if (p.dres) RW::store(p.dres, row, p.F, t, d);
     if (!has_x) continue;
-    // d = gradient of h; du = alpha gate d, u = norm(x)
+    // d = gradient of h; du = alpha gate d
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      float w[V], b[V];
-      RW::channel(p.w_post, n, p.F, t, 0.f, w);
-      RW::channel(p.b_post, n, p.F, t, 0.f, b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int i = n * V + e;
-        const float ad = p.alpha * d[i];
-        const float u = p.w_post ? fmaf(x[i], w[e], b[e]) : x[i];
-        const float du = ad * g[i];
-        g[i] = ad * u;  // the gate's gradient
-        acc[4][i] += g[i];
-        acc[0][i] = fmaf(du, x[i], acc[0][i]);
-        acc[1][i] += du;
-        d[i] = p.w_post ? du * w[e] : du;
-      }
+    for (int i = 0; i < E; ++i) {
+      const float ad = p.alpha * d[i];
+      const float u = p.w_post ? fmaf(x[i], wa[i], ba[i]) : x[i];
+      const float du = ad * g[i];
+      g[i] = ad * u;  // the gate's gradient
+      acc[4][i] += g[i];
+      acc[0][i] = fmaf(du, x[i], acc[0][i]);
+      acc[1][i] += du;
+      d[i] = p.w_post ? du * wa[i] : du;
     }
     if (token && p.dgate) RW::store(p.dgate, row, p.F, t, g);
     if (p.w_post) norm_dx<E, W, LN>(d, x, s.y, p.inv_f, red, turn);
     if (p.dx) RW::store(p.dx, row, p.F, t, d);
   }
+  cp_async_wait<0>();
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
     if ((p.want >> k) & 1) {
       float* o = p.part + (slot * kSums + k) * p.F;
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
+      for (int n = 0; n < RW::NV; ++n) {
         const int c = RW::col(n, t);
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -400,28 +545,28 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_bwd_kernel(const N
     }
 }
 
-// Column sums over the slots, in slot order within each of 8 fixed strands.
+// Column sums over the slots, in slot order within each of 32 fixed strands.
 struct NormOut {
   float* o[kSums];
 };
-__global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int slots, int F,
-                                                        NormOut out) {
-  __shared__ float sh[8][33];
+__global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int slots, int F,
+                                                         NormOut out) {
+  __shared__ float sh[32][33];
   const int k = blockIdx.y, lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
   if (!out.o[k]) return;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < F) {
-#pragma unroll 4
-    for (int i = strand; i < slots; i += 8) s += part[(int64_t(i) * kSums + k) * F + c];
+#pragma unroll 8
+    for (int i = strand; i < slots; i += 32) s += part[(int64_t(i) * kSums + k) * F + c];
   }
   sh[strand][lane] = s;
   __syncthreads();
-  if (strand == 0 && c < F) {
+  // warp w adds up column w of the block's 32
+  float v = sh[lane][strand];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][lane];
-    out.o[k][c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0 && blockIdx.x * 32 + strand < F) out.o[k][blockIdx.x * 32 + strand] = v;
 }
 
 // --------------------------------------------------------------------------
@@ -481,13 +626,45 @@ gattn_status launched(const char* what) {
   return GATTN_OK;
 }
 
+int sms_here() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    n = 152;
+  }
+  return n;
+}
+
+template <class K>
+void launch_ring(K kern, unsigned grid, int threads, int bytes, const NormParams& p,
+                 cudaStream_t st) {
+  if (bytes > 40 * 1024)  // static shared memory counts towards the 48 KB too
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  kern<<<grid, threads, bytes, st>>>(p);
+}
+
+template <class T, int V, int E, int W, bool LN>
+void fwd_walk(const NormParams& p, cudaStream_t st) {
+  constexpr int CTAS = fwd_ctas<E, W>();
+  const unsigned grid = unsigned(std::min<int64_t>(p.N, int64_t(CTAS) * sms_here()));
+  launch_ring(norm_fwd_walk_kernel<T, V, E, W, LN>, grid, W * 32,
+              Ring<T, V, E, W, 3, CTAS>::kBytes, p, st);
+}
+
+// Elements a thread, for one warp a row: the fewest that cover it (in steps,
+// so that few kernels are compiled).
 template <class T, int V, bool LN>
 void fwd_launch(const NormParams& p, cudaStream_t st) {
-  const unsigned rows = unsigned(p.N), quads = unsigned((p.N + 3) / 4);
+  const unsigned quads = unsigned((p.N + 3) / 4);
   if (p.F <= 256) norm_fwd_kernel<T, V, 8, 1, LN><<<quads, 128, 0, st>>>(p);
+  else if (p.F <= 512) norm_fwd_kernel<T, V, 16, 1, LN><<<quads, 128, 0, st>>>(p);
+  else if (p.F <= 768) norm_fwd_kernel<T, V, 24, 1, LN><<<quads, 128, 0, st>>>(p);
   else if (p.F <= 1024) norm_fwd_kernel<T, V, 32, 1, LN><<<quads, 128, 0, st>>>(p);
-  else if (p.F <= 4096) norm_fwd_kernel<T, V, 32, 4, LN><<<rows, 128, 0, st>>>(p);
-  else norm_fwd_kernel<T, V, 32, 16, LN><<<rows, 512, 0, st>>>(p);
+  else if (p.F <= 2048) fwd_walk<T, V, 8, 8, LN>(p, st);
+  else if (p.F <= 4096) fwd_walk<T, V, 8, 16, LN>(p, st);
+  else if (p.F <= 8192) fwd_walk<T, V, 16, 16, LN>(p, st);
+  else fwd_walk<T, V, 32, 16, LN>(p, st);
 }
 
 template <class T, int V>
@@ -502,28 +679,30 @@ struct BwdShape {
   unsigned grid;
 };
 BwdShape bwd_shape(const gattn_norm_desc* d) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  else
-    cudaGetLastError();
   BwdShape s{};
-  s.warps = d->F <= 256 ? 1 : d->F <= 1024 ? 4 : d->F <= 4096 ? 16 : 32;
-  // as many CTAs as are resident at once: 4 of 128 threads, 1 of 512 or 1024
-  const int64_t per_sm = s.warps <= 4 ? 4 : 1;
+  s.warps = d->F <= 256 ? 1 : d->F <= 1024 ? 4 : 16;
+  const int64_t per_sm = s.warps <= 4 ? 4 : 1;  // bwd_ctas
   const int64_t rows = s.warps == 1 ? (d->N + 3) / 4 : d->N;
-  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, per_sm * sms)));
+  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, per_sm * sms_here())));
   s.slots = int(s.grid) * (s.warps == 1 ? 4 : 1);
   return s;
 }
 
+template <class T, int V, int E, int W, bool LN>
+void bwd_go(const NormParams& p, const BwdShape& s, cudaStream_t st) {
+  launch_ring(norm_bwd_kernel<T, V, E, W, LN>, s.grid, W == 1 ? 128 : W * 32,
+              Ring<T, V, E, W, 5, bwd_ctas<W>()>::kBytes, p, st);
+}
+
 template <class T, int V, bool LN>
 void bwd_launch(const NormParams& p, const BwdShape& s, cudaStream_t st) {
-  if (s.warps == 1) norm_bwd_kernel<T, V, 8, 1, LN><<<s.grid, 128, 0, st>>>(p);
-  else if (s.warps == 4) norm_bwd_kernel<T, V, 8, 4, LN><<<s.grid, 128, 0, st>>>(p);
-  else if (s.warps == 16) norm_bwd_kernel<T, V, 8, 16, LN><<<s.grid, 512, 0, st>>>(p);
-  else if (p.F <= 8192) norm_bwd_kernel<T, V, 8, 32, LN><<<s.grid, 1024, 0, st>>>(p);
-  else norm_bwd_kernel<T, V, 16, 32, LN><<<s.grid, 1024, 0, st>>>(p);
+  if (s.warps == 1) bwd_go<T, V, 8, 1, LN>(p, s, st);
+  else if (p.F <= 512 && V <= 4) bwd_go<T, V, V <= 4 ? 4 : 8, 4, LN>(p, s, st);
+  else if (p.F <= 768 && V == 1) bwd_go<T, V, V == 1 ? 6 : 8, 4, LN>(p, s, st);
+  else if (s.warps == 4) bwd_go<T, V, 8, 4, LN>(p, s, st);
+  else if (p.F <= 4096) bwd_go<T, V, 8, 16, LN>(p, s, st);
+  else if (p.F <= 8192) bwd_go<T, V, 16, 16, LN>(p, s, st);
+  else bwd_go<T, V, 32, 16, LN>(p, s, st);
 }
 
 template <class T, int V>
@@ -637,7 +816,7 @@ gattn_status gattn_norm_bwd(const gattn_norm_desc* d, const void* res, const flo
     else bwd_kind<__nv_bfloat16, 1>(p, sh, ln, st);
   }
   if ((s = launched("gattn_norm_bwd")) != GATTN_OK || !p.want) return s;
-  norm_cols_kernel<<<dim3((d->F + 31) / 32, kSums), 256, 0, st>>>(p.part, sh.slots, d->F, out);
+  norm_cols_kernel<<<dim3((d->F + 31) / 32, kSums), 1024, 0, st>>>(p.part, sh.slots, d->F, out);
   return launched("gattn_norm_bwd (column sums)");
 }
 
