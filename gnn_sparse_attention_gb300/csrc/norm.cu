@@ -15,18 +15,17 @@
 // their deviation that rounding would be as large as the row).
 //
 // A row belongs to W warps; a thread holds E of its elements as 16-byte
-// vectors (single elements when a row is no multiple of 16 bytes).  Up to
-// 1,024 elements the forward gives a row to one warp (E up to 32) and needs no
-// block barrier.  Longer rows, and the backward, run as many CTAs as fit and
-// let each walk its rows: a thread then keeps its columns' weights in
-// registers (read per row they are more L1 traffic than the row is HBM
-// traffic), and copies its own elements of the next rows into shared memory
-// with cp.async, two rows ahead -- each thread reads back only what it copied,
-// so the ring needs no barrier, and the bytes in flight (80 KB an SM) do not
-// cost registers.  The backward also carries five fp32 column sums per element
-// (dw, db of both norms and the channel gate) over all rows of its CTA; the
-// CTAs' sums meet in a second small kernel, in CTA order, so results do not
-// vary from run to run.
+// vectors (single elements when a row is no multiple of 16 bytes).  As many CTAs
+// as fit run, and each walks its rows; a thread copies its own elements of
+// the next rows into shared memory with cp.async, one or two rows ahead -- it
+// reads back only what it copied, so the ring needs no barrier, and the bytes
+// in flight (about 100 KB an SM) do not cost registers.  Arithmetic is on pairs
+// (fma.rn.f32x2): unpaired, the forward issues 30 instructions an element and
+// is bound by them.  Up to 1,024 elements the forward gives a row to one warp
+// and needs no block barrier.  The backward carries five fp32 column sums per
+// element (dw, db of both norms and the channel gate) over all rows of its
+// CTA and keeps its columns' weights in registers; the CTAs' sums meet in a
+// second small kernel, in CTA order, so results do not vary from run to run.
 #include <algorithm>
 
 #include "attn_launch.cuh"
@@ -170,100 +169,67 @@ struct Row {
   }
 };
 
-// mean and 1 / deviation (root mean square when LN is false) of a row
-template <class T, int V, int E, int W, bool LN>
-__device__ __forceinline__ float2 row_stats(const float* f, const NormParams& p, int t, float* red,
-                                            int& turn) {
-  using RW = Row<T, V, E, W>;
-  float mean = 0.f;
-  if constexpr (LN) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int e = 0; e < E; ++e) s[0] += f[e];
-    row_sums<W, 1>(s, red, turn);
-    mean = s[0] * p.inv_f;
-  }
-  float q[1] = {0.f};
-#pragma unroll
-  for (int n = 0; n < RW::NV; ++n)
-    if (RW::col(n, t) < p.F)  // absent columns hold 0, which is no deviation of 0 under a mean
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float d = f[n * V + e] - mean;
-        q[0] = fmaf(d, d, q[0]);
-      }
-  row_sums<W, 1>(q, red, turn);
-  return make_float2(mean, rsqrtf(q[0] * p.inv_f + p.eps));
+__device__ __forceinline__ float2 pair(const float* f, int i) {
+  return make_float2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void put_pair(float* f, int i, float2 v) {
+  f[2 * i] = v.x;
+  f[2 * i + 1] = v.y;
 }
 
+// zeros past the row's end (`whole`: the row fills its threads)
+template <class T, int V, int E, int W>
+__device__ __forceinline__ void clip(float* f, int F, int t, bool whole) {
+  if (whole) return;
+#pragma unroll
+  for (int n = 0; n < E / V; ++n)
+    if (Row<T, V, E, W>::col(n, t) >= F)
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[n * V + e] = 0.f;
+}
+
+// f becomes (f - mean) / deviation (f / root mean square when LN is false),
+// with zeros past the row's end; returns (mean, 1 / deviation)
 template <class T, int V, int E, int W, bool LN>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) norm_fwd_kernel(const NormParams p) {
-  using RW = Row<T, V, E, W>;
-  __shared__ float red[W > 1 ? 4 * W : 1];
-  int turn = 0;
-  const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t row = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  if (row >= p.N) return;
-  float h[E];
-  {
-    typename RW::R r[RW::NV], xr[RW::NV], gr[RW::NV];
-    RW::load(r, p.res, row, p.F, t);
-    if (p.x) RW::load(xr, p.x, row, p.F, t);
-    if (p.x && p.gate_mode == kGateToken) RW::load(gr, p.gate, row, p.F, t);
+__device__ __forceinline__ float2 normalise(float* f, const NormParams& p, int t, bool whole,
+                                            float* red, int& turn) {
+  float mean = 0.f;
+  if constexpr (LN) {
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(r[n], h + n * V);
-    if (p.x) {
-      float u[E];
+    for (int i = 0; i < E / 2; ++i) s2 = f2add(s2, pair(f, i));
+    float s[1] = {s2.x + s2.y};
+    row_sums<W, 1>(s, red, turn);
+    mean = s[0] * p.inv_f;
 #pragma unroll
-      for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(xr[n], u + n * V);
-      if (p.w_post) {
-        const float2 s = row_stats<T, V, E, W, LN>(u, p, t, red, turn);
-        if (t == 0) reinterpret_cast<float2*>(p.stats + row)[0] = s;
-#pragma unroll
-        for (int n = 0; n < RW::NV; ++n) {
-          float w[V], b[V];
-          RW::channel(p.w_post, n, p.F, t, 0.f, w);
-          RW::channel(p.b_post, n, p.F, t, 0.f, b);
-#pragma unroll
-          for (int e = 0; e < V; ++e) u[n * V + e] = fmaf((u[n * V + e] - s.x) * s.y, w[e], b[e]);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < RW::NV; ++n) {
-        float g[V];
-        if (p.gate_mode == kGateToken) {
-          Vec<T, V>::get(gr[n], g);
-        } else {
-          RW::channel(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr, n,
-                      p.F, t, 1.f, g);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          h[n * V + e] = fmaf(p.alpha * g[e], u[n * V + e], h[n * V + e]);
-      }
-      RW::store(p.h, row, p.F, t, h);
-    }
+    for (int i = 0; i < E / 2; ++i) put_pair(f, i, f2add(pair(f, i), f2s(-mean)));
+    clip<T, V, E, W>(f, p.F, t, whole);
   }
-  if (p.w_pre) {  // on h as it stands in fp32, not as rounded for the store
-    const float2 s = row_stats<T, V, E, W, LN>(h, p, t, red, turn);
-    if (t == 0) reinterpret_cast<float2*>(p.stats + row)[1] = s;
+  float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int n = 0; n < RW::NV; ++n) {
-      float w[V], b[V];
-      RW::channel(p.w_pre, n, p.F, t, 0.f, w);
-      RW::channel(p.b_pre, n, p.F, t, 0.f, b);
+  for (int i = 0; i < E / 2; ++i) q2 = f2fma(pair(f, i), pair(f, i), q2);
+  float q[1] = {q2.x + q2.y};
+  row_sums<W, 1>(q, red, turn);
+  const float r = rsqrtf(q[0] * p.inv_f + p.eps);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[n * V + e] = fmaf((h[n * V + e] - s.x) * s.y, w[e], b[e]);
-    }
-    RW::store(p.y, row, p.F, t, h);
-  }
+  for (int i = 0; i < E / 2; ++i) put_pair(f, i, f2mul(pair(f, i), f2s(r)));
+  return make_float2(mean, r);
+}
+
+// the same from statistics that the forward kept
+template <class T, int V, int E, int W>
+__device__ __forceinline__ void renormalise(float* f, float mean, float r, int F, int t,
+                                            bool whole) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) put_pair(f, i, f2mul(f2add(pair(f, i), f2s(-mean)), f2s(r)));
+  clip<T, V, E, W>(f, F, t, whole);
 }
 
 // A thread's own elements of NT tensors' rows, kStages rows deep in shared
 // memory: three or two rows, whatever fits CTAS times on an SM; rows too long
 // for two are read from global memory where they are used (kStages 0).
 // Elements past the row's end are zeros, written once.
-template <class T, int V, int E, int W, int NT, int CTAS>
+template <class T, int V, int E, int W, int NT, int CTAS, bool DIRECT = false>
 struct Ring {
   using RW = Row<T, V, E, W>;
   using R = typename RW::R;
@@ -271,7 +237,10 @@ struct Ring {
   static constexpr int kThreads = W == 1 ? 128 : W * 32;
   static constexpr int kTensor = kThreads * RW::NV * int(sizeof(R));
   static constexpr int kRoom = 200 * 1024 / CTAS;
-  static constexpr int kStages = 3 * NT * kTensor <= kRoom ? 3 : 2 * NT * kTensor <= kRoom ? 2 : 0;
+  static constexpr int kStages = DIRECT                        ? 0
+                                 : 3 * NT * kTensor <= kRoom ? 3
+                                 : 2 * NT * kTensor <= kRoom ? 2
+                                                             : 0;
   static constexpr int kBytes = kStages * NT * kTensor;
   uint8_t* base;
   __device__ R* at(int stage, int tensor, int n) const {
@@ -295,19 +264,21 @@ struct Ring {
       else cp_async4(at(stage, tensor, n), p + c);
     }
   }
-  // the elements of `row`, the k-th that this CTA walks
+  // the elements of `row`, the k-th that this CTA walks (vector n, or all)
+  __device__ void get1(int k, int tensor, int n, const void* src, int64_t row, int F, int t,
+                       float* f) const {
+    if constexpr (kStages == 0) {
+      const int c = RW::col(n, t);
+      const T* p = static_cast<const T*>(src) + row * F;
+      Vec<T, V>::get(c < F ? *reinterpret_cast<const R*>(p + c) : Vec<T, V>::zero(), f);
+    } else {
+      Vec<T, V>::get(*at(k % kStages, tensor, n), f);
+    }
+  }
   __device__ void get(int k, int tensor, const void* src, int64_t row, int F, int t,
                       float* f) const {
-    if constexpr (kStages == 0) {
-      R r[RW::NV];
-      RW::load(r, src, row, F, t);
 #pragma unroll
-      for (int n = 0; n < RW::NV; ++n) Vec<T, V>::get(r[n], f + n * V);
-    } else {
-#pragma unroll
-      for (int n = 0; n < RW::NV; ++n)
-        Vec<T, V>::get(*at(k % kStages, tensor, n), f + n * V);
-    }
+    for (int n = 0; n < RW::NV; ++n) get1(k, tensor, n, src, row, F, t, f + n * V);
   }
   __device__ void wait() const {
     if constexpr (kStages > 0) cp_async_wait<kStages - 2>();
@@ -320,29 +291,33 @@ __device__ __forceinline__ void channels(const float* w, int F, int t, float non
   for (int n = 0; n < E / V; ++n) Row<T, V, E, W>::channel(w, n, F, t, none, f + n * V);
 }
 
-// CTAs per SM of the walking kernels: 64 registers a thread forward (E = 8), 128
-// backward
+// CTAs per SM: registers a thread of about 64 (E = 8), 80 (16) and 128 forward,
+// 128 backward
 template <int E, int W>
 constexpr int fwd_ctas() {
-  return E > 8 ? 1 : 1024 / (W * 32);
+  const int threads = W == 1 ? 128 : W * 32, most = E <= 8 ? 1024 : E <= 16 ? 768 : 512;
+  return most < threads ? 1 : most / threads;
 }
 template <int W>
 constexpr int bwd_ctas() {
   return W <= 4 ? 4 : 1;
 }
 
-// Forward of long rows: W > 1 warps a row, each CTA walks its rows.
 template <class T, int V, int E, int W, bool LN>
-__global__ void __launch_bounds__(W * 32, fwd_ctas<E, W>())
-    norm_fwd_walk_kernel(const NormParams p) {
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, fwd_ctas<E, W>())
+    norm_fwd_kernel(const NormParams p) {
   using RW = Row<T, V, E, W>;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ float red[4 * W];
-  using Rg = Ring<T, V, E, W, 3, fwd_ctas<E, W>()>;
+  __shared__ float red[W > 1 ? 4 * W : 1];
+  // single bf16 elements are too small for cp.async: many short-lived CTAs
+  // read them directly
+  using Rg = Ring<T, V, E, W, 3, fwd_ctas<E, W>(), V * sizeof(T) < 4>;
   Rg ring{ring_mem};
   int turn = 0;
-  const int t = threadIdx.x;
-  const bool token = p.gate_mode == kGateToken;
+  const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t slot = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = W == 1 ? int64_t(gridDim.x) * 4 : gridDim.x;
+  const bool token = p.gate_mode == kGateToken, whole = p.F == E * W * 32;
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.N) {
       ring.fetch(stage, 0, p.res, row, p.F, t);
@@ -351,46 +326,58 @@ __global__ void __launch_bounds__(W * 32, fwd_ctas<E, W>())
     }
     cp_async_commit();
   };
-  ring.clear(p.F, t);
-  for (int s = 0; s < Rg::kStages - 1; ++s) fetch(blockIdx.x + int64_t(s) * gridDim.x, s);
-  constexpr bool KEEP = E <= 8;  // weights stay in registers
-  float wa[E], ba[E], wb[E], bb[E], gc[E];
-  auto weights = [&]() {
-    channels<T, V, E, W>(p.w_post, p.F, t, 0.f, wa);
-    channels<T, V, E, W>(p.b_post, p.F, t, 0.f, ba);
-    channels<T, V, E, W>(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr,
-                         p.F, t, 1.f, gc);
-    channels<T, V, E, W>(p.w_pre, p.F, t, 0.f, wb);
-    channels<T, V, E, W>(p.b_pre, p.F, t, 0.f, bb);
-  };
-  if (KEEP) weights();
+  if (!whole) ring.clear(p.F, t);
+  for (int s = 0; s < Rg::kStages - 1; ++s) fetch(slot + s * step, s);
   int k = 0;
-  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, ++k) {
+  for (int64_t row = slot; row < p.N; row += step, ++k) {
     ring.wait();
-    float h[E];
-    ring.get(k, 0, p.res, row, p.F, t, h);
-    if (!KEEP) weights();
-    if (p.x) {
-      float u[E], g[E];
-      ring.get(k, 1, p.x, row, p.F, t, u);
-      if (token) ring.get(k, 2, p.gate, row, p.F, t, g);
-      if (p.w_post) {
-        const float2 s = row_stats<T, V, E, W, LN>(u, p, t, red, turn);
-        if (t == 0) reinterpret_cast<float2*>(p.stats + row)[0] = s;
-#pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = fmaf((u[e] - s.x) * s.y, wa[e], ba[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) h[e] = fmaf(p.alpha * (token ? g[e] : gc[e]), u[e], h[e]);
-      RW::store(p.h, row, p.F, t, h);
-    }
+    // (the stage that is refilled was read a row ago)
     if constexpr (Rg::kStages > 0)
-      fetch(row + (Rg::kStages - 1) * int64_t(gridDim.x), (k + Rg::kStages - 1) % Rg::kStages);
+      fetch(row + (Rg::kStages - 1) * step, (k + Rg::kStages - 1) % Rg::kStages);
+    float h[E];
+    if constexpr (Rg::kStages == 0) ring.get(k, 0, p.res, row, p.F, t, h);
+    if (p.x) {
+      float u[E];
+      ring.get(k, 1, p.x, row, p.F, t, u);
+      if (p.w_post) {
+        const float2 s = normalise<T, V, E, W, LN>(u, p, t, whole, red, turn);
+        if (t == 0) reinterpret_cast<float2*>(p.stats + row)[0] = s;
+      }
+      if constexpr (Rg::kStages > 0) ring.get(k, 0, p.res, row, p.F, t, h);
+#pragma unroll
+      for (int n = 0; n < RW::NV; ++n) {
+        float w[V], b[V], g[V];
+        if (token)
+          ring.get1(k, 2, n, p.gate, row, p.F, t, g);
+        else
+          RW::channel(p.gate_mode == kGateChannel ? static_cast<const float*>(p.gate) : nullptr, n,
+                      p.F, t, 1.f, g);
+        if (p.w_post) {
+          RW::channel(p.w_post, n, p.F, t, 0.f, w);
+          RW::channel(p.b_post, n, p.F, t, 0.f, b);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int i = n * V + e;
+          if (p.w_post) u[i] = fmaf(u[i], w[e], b[e]);
+          h[i] = fmaf(g[e] * p.alpha, u[i], h[i]);
+        }
+      }
+      RW::store(p.h, row, p.F, t, h);
+    } else if constexpr (Rg::kStages > 0) {
+      ring.get(k, 0, p.res, row, p.F, t, h);
+    }
     if (p.w_pre) {  // on h as it stands in fp32, not as rounded for the store
-      const float2 s = row_stats<T, V, E, W, LN>(h, p, t, red, turn);
+      const float2 s = normalise<T, V, E, W, LN>(h, p, t, whole, red, turn);
       if (t == 0) reinterpret_cast<float2*>(p.stats + row)[1] = s;
 #pragma unroll
-      for (int e = 0; e < E; ++e) h[e] = fmaf((h[e] - s.x) * s.y, wb[e], bb[e]);
+      for (int n = 0; n < RW::NV; ++n) {
+        float w[V], b[V];
+        RW::channel(p.w_pre, n, p.F, t, 0.f, w);
+        RW::channel(p.b_pre, n, p.F, t, 0.f, b);
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[n * V + e] = fmaf(h[n * V + e], w[e], b[e]);
+      }
       RW::store(p.y, row, p.F, t, h);
     }
   }
@@ -402,16 +389,21 @@ __global__ void __launch_bounds__(W * 32, fwd_ctas<E, W>())
 template <int E, int W, bool LN>
 __device__ __forceinline__ void norm_dx(float* g, const float* xh, float r, float inv_f, float* red,
                                         int& turn) {
-  float s[2] = {0.f, 0.f};
+  float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    s[0] = fmaf(g[e], xh[e], s[0]);
-    if (LN) s[1] += g[e];
+  for (int i = 0; i < E / 2; ++i) {
+    a = f2fma(pair(g, i), pair(xh, i), a);
+    if (LN) b = f2add(b, pair(g, i));
   }
+  float s[2] = {a.x + a.y, b.x + b.y};
   row_sums<W, LN ? 2 : 1>(s, red, turn);
-  const float c1 = s[0] * inv_f, c2 = LN ? s[1] * inv_f : 0.f;
+  const float2 c1 = f2s(-s[0] * inv_f), c2 = f2s(LN ? -s[1] * inv_f : 0.f);
 #pragma unroll
-  for (int e = 0; e < E; ++e) g[e] = r * (g[e] - fmaf(xh[e], c1, c2));
+  for (int i = 0; i < E / 2; ++i) {
+    float2 v = f2fma(pair(xh, i), c1, pair(g, i));
+    if (LN) v = f2add(v, c2);
+    put_pair(g, i, f2mul(v, f2s(r)));
+  }
 }
 
 template <class T, int V, int E, int W, bool LN>
@@ -427,6 +419,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, bwd_ctas<W>())
   const int64_t slot = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = W == 1 ? int64_t(gridDim.x) * 4 : gridDim.x;
   const bool has_x = p.x != nullptr, token = p.gate_mode == kGateToken;
+  const bool whole = p.F == E * W * 32;
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.N) {
       if (p.w_pre) {
@@ -441,7 +434,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, bwd_ctas<W>())
     }
     cp_async_commit();
   };
-  ring.clear(p.F, t);
+  if (!whole) ring.clear(p.F, t);
   for (int s = 0; s < Rg::kStages - 1; ++s) fetch(slot + s * step, s);
   float acc[kSums][E];
 #pragma unroll
@@ -465,66 +458,64 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, bwd_ctas<W>())
     if (row + step < p.N) next = p.cstats[row + step];
     ring.wait();
     if (!KEEP) weights();
-    // x becomes its normalised row, u = norm(x); hh that of h, formed again
-    // as the forward did
+    // x becomes its normalised row; hh that of h, formed again as the forward did
+    // (the stage that is refilled was read a row ago)
+    if constexpr (Rg::kStages > 0)
+      fetch(row + (Rg::kStages - 1) * step, (k + Rg::kStages - 1) % Rg::kStages);
     float d[E], x[E], g[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) d[e] = x[e] = 0.f;
-    if (p.dh) ring.get(k, 2, p.dh, row, p.F, t, d);
-    if (has_x) {
-      ring.get(k, 3, p.x, row, p.F, t, x);
-      if (p.w_post) {
-#pragma unroll
-        for (int n = 0; n < RW::NV; ++n)
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            x[n * V + e] = RW::col(n, t) < p.F ? (x[n * V + e] - s.x) * s.y : 0.f;
-      }
-    }
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
+    if (has_x) ring.get(k, 3, p.x, row, p.F, t, x);
     if (token) {
       ring.get(k, 4, p.gate, row, p.F, t, g);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] = gc[e];
     }
+    if (p.w_post) renormalise<T, V, E, W>(x, s.x, s.y, p.F, t, whole);
     if (p.w_pre) {
       float hh[E], gy[E];
       ring.get(k, 0, p.res, row, p.F, t, hh);
-      ring.get(k, 1, p.dy, row, p.F, t, gy);
+      if (has_x) {
 #pragma unroll
-      for (int n = 0; n < RW::NV; ++n) {
-        const bool on = RW::col(n, t) < p.F;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int i = n * V + e;
-          if (has_x)
-            hh[i] = fmaf(p.alpha * g[i], p.w_post ? fmaf(x[i], wa[i], ba[i]) : x[i], hh[i]);
-          hh[i] = on ? (hh[i] - s.z) * s.w : 0.f;
-          acc[2][i] = fmaf(gy[i], hh[i], acc[2][i]);
-          acc[3][i] += gy[i];
-          gy[i] *= wb[i];
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 u = p.w_post ? f2fma(pair(x, i), pair(wa, i), pair(ba, i)) : pair(x, i);
+          put_pair(hh, i, f2fma(f2mul(pair(g, i), f2s(p.alpha)), u, pair(hh, i)));
         }
       }
-      norm_dx<E, W, LN>(gy, hh, s.w, p.inv_f, red, turn);
+      renormalise<T, V, E, W>(hh, s.z, s.w, p.F, t, whole);
+      ring.get(k, 1, p.dy, row, p.F, t, gy);
 #pragma unroll
-      for (int e = 0; e < E; ++e) d[e] += gy[e];
+      for (int i = 0; i < E / 2; ++i) {
+        put_pair(acc[2], i, f2fma(pair(gy, i), pair(hh, i), pair(acc[2], i)));
+        put_pair(acc[3], i, f2add(pair(acc[3], i), pair(gy, i)));
+        put_pair(gy, i, f2mul(pair(gy, i), pair(wb, i)));
+      }
+      norm_dx<E, W, LN>(gy, hh, s.w, p.inv_f, red, turn);
+      if (p.dh) {
+        ring.get(k, 2, p.dh, row, p.F, t, d);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) put_pair(d, i, f2add(pair(d, i), pair(gy, i)));
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) d[e] = gy[e];
+      }
+    } else {
+      ring.get(k, 2, p.dh, row, p.F, t, d);
     }
-    // (this stage has been read; the one refilled was read a row ago)
-    if constexpr (Rg::kStages > 0)
-      fetch(row + (Rg::kStages - 1) * step, (k + Rg::kStages - 1) % Rg::kStages);
     if (p.dres) RW::store(p.dres, row, p.F, t, d);
     if (!has_x) continue;
     // d = gradient of h; du = alpha gate d
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float ad = p.alpha * d[i];
-      const float u = p.w_post ? fmaf(x[i], wa[i], ba[i]) : x[i];
-      const float du = ad * g[i];
-      g[i] = ad * u;  // the gate's gradient
-      acc[4][i] += g[i];
-      acc[0][i] = fmaf(du, x[i], acc[0][i]);
-      acc[1][i] += du;
-      d[i] = p.w_post ? du * wa[i] : du;
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 ad = f2mul(pair(d, i), f2s(p.alpha));
+      const float2 u = p.w_post ? f2fma(pair(x, i), pair(wa, i), pair(ba, i)) : pair(x, i);
+      const float2 du = f2mul(ad, pair(g, i));
+      put_pair(g, i, f2mul(ad, u));  // the gate's gradient
+      put_pair(acc[4], i, f2add(pair(acc[4], i), pair(g, i)));
+      put_pair(acc[0], i, f2fma(du, pair(x, i), pair(acc[0], i)));
+      put_pair(acc[1], i, f2add(pair(acc[1], i), du));
+      put_pair(d, i, p.w_post ? f2mul(du, pair(wa, i)) : du);
     }
     if (token && p.dgate) RW::store(p.dgate, row, p.F, t, g);
     if (p.w_post) norm_dx<E, W, LN>(d, x, s.y, p.inv_f, red, turn);
@@ -645,26 +636,30 @@ void launch_ring(K kern, unsigned grid, int threads, int bytes, const NormParams
 }
 
 template <class T, int V, int E, int W, bool LN>
-void fwd_walk(const NormParams& p, cudaStream_t st) {
+void fwd_go(const NormParams& p, cudaStream_t st) {
   constexpr int CTAS = fwd_ctas<E, W>();
-  const unsigned grid = unsigned(std::min<int64_t>(p.N, int64_t(CTAS) * sms_here()));
-  launch_ring(norm_fwd_walk_kernel<T, V, E, W, LN>, grid, W * 32,
-              Ring<T, V, E, W, 3, CTAS>::kBytes, p, st);
+  const int64_t ctas = W == 1 ? (p.N + 3) / 4 : p.N;
+  using Rg = Ring<T, V, E, W, 3, CTAS, V * sizeof(T) < 4>;
+  const unsigned grid = unsigned(
+      Rg::kStages == 0 ? ctas : std::min<int64_t>(ctas, int64_t(CTAS) * sms_here()));
+  launch_ring(norm_fwd_kernel<T, V, E, W, LN>, grid, W == 1 ? 128 : W * 32, Rg::kBytes, p, st);
 }
 
-// Elements a thread, for one warp a row: the fewest that cover it (in steps,
-// so that few kernels are compiled).
+// Elements a thread and warps a row: the fewest elements that cover the row (in
+// steps, so that few kernels are compiled); one warp a row up to 1,024 (no
+// barriers), from there 16 elements a thread.  Rows in single elements take
+// four warps from 257 on, because 24 or 32 copies of 4 bytes a lane are slower
+// than the barriers (20,011 x 515 fp32: 84 us with one warp, 43 with four).
 template <class T, int V, bool LN>
 void fwd_launch(const NormParams& p, cudaStream_t st) {
-  const unsigned quads = unsigned((p.N + 3) / 4);
-  if (p.F <= 256) norm_fwd_kernel<T, V, 8, 1, LN><<<quads, 128, 0, st>>>(p);
-  else if (p.F <= 512) norm_fwd_kernel<T, V, 16, 1, LN><<<quads, 128, 0, st>>>(p);
-  else if (p.F <= 768) norm_fwd_kernel<T, V, 24, 1, LN><<<quads, 128, 0, st>>>(p);
-  else if (p.F <= 1024) norm_fwd_kernel<T, V, 32, 1, LN><<<quads, 128, 0, st>>>(p);
-  else if (p.F <= 2048) fwd_walk<T, V, 8, 8, LN>(p, st);
-  else if (p.F <= 4096) fwd_walk<T, V, 8, 16, LN>(p, st);
-  else if (p.F <= 8192) fwd_walk<T, V, 16, 16, LN>(p, st);
-  else fwd_walk<T, V, 32, 16, LN>(p, st);
+  if (p.F <= 256) fwd_go<T, V, 8, 1, LN>(p, st);
+  else if (p.F <= 512) fwd_go<T, V, V == 1 ? 4 : 16, V == 1 ? 4 : 1, LN>(p, st);
+  else if (p.F <= 768) fwd_go<T, V, V == 1 ? 6 : 24, V == 1 ? 4 : 1, LN>(p, st);
+  else if (p.F <= 1024) fwd_go<T, V, V == 1 ? 8 : 32, V == 1 ? 4 : 1, LN>(p, st);
+  else if (p.F <= 2048) fwd_go<T, V, 16, 4, LN>(p, st);
+  else if (p.F <= 4096) fwd_go<T, V, 16, 8, LN>(p, st);
+  else if (p.F <= 8192) fwd_go<T, V, 16, 16, LN>(p, st);
+  else fwd_go<T, V, 32, 16, LN>(p, st);
 }
 
 template <class T, int V>
