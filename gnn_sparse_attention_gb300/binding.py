@@ -8,7 +8,6 @@ and the current stream.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
 import threading
@@ -582,52 +581,46 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-class _Run:
-    """Stream of one call; what the call allocates on another stream than the current one is
-    tied to that stream.  The caller has made ``dev`` the current device."""
-    __slots__ = ("dev", "handle", "other")
-
-    def __init__(self, dev, stream):
-        self.dev, self.other = dev, None
-        self.handle = torch._C._cuda_getCurrentRawStream(dev)
-        if stream is not None:
-            if stream.device.index != dev:
-                raise ValueError(f"stream of {stream.device} for tensors on device {dev}")
-            if stream.cuda_stream != self.handle:
-                self.handle, self.other = stream.cuda_stream, stream
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
-
-    def workspace(self, given, fn, desc, key):
-        """The caller's workspace, or a new one of the size that `fn` names (None for 0)."""
-        if given is not None:
-            if given.get_device() != self.dev or not given.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous tensor on device {self.dev}")
-            return given
-        n = _sizes.get((fn, self.dev, key))
-        if n is None:
-            size = ctypes.c_size_t()
-            _check(getattr(load_library(), fn)(desc, ctypes.byref(size)), fn)
-            n = size.value
-            if len(_sizes) > 4096:
-                _sizes.clear()
-            _sizes[(fn, self.dev, key)] = n
-        return self.empty((n,), torch.uint8) if n else None
+def _stream_of(dev, stream):
+    """(handle, stream to tie allocations to or None) of a call on device number dev."""
+    handle = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None:
+        return handle, None
+    if stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on device {dev}")
+    return stream.cuda_stream, (stream if stream.cuda_stream != handle else None)
 
 
-def _on_device(call):
-    """Run `call(dev, ...)` with its tensors' device as the current one."""
-    def wrapped(first, *args, **kw):
-        dev = first.get_device() if isinstance(first, torch.Tensor) else -1
-        if dev < 0 or dev == torch.cuda.current_device():
-            return call(first, *args, **kw)
-        with torch.cuda.device(dev):
-            return call(first, *args, **kw)
-    return functools.wraps(call)(wrapped)
+def _new(dev, other, shape, dtype):
+    """A tensor that the call allocates, tied to the stream it runs on."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if other is not None:
+        t.record_stream(other)
+    return t
+
+
+def _like(t, other):
+    r = torch.empty_like(t)
+    if other is not None:
+        r.record_stream(other)
+    return r
+
+
+def _workspace(given, dev, other, fn, desc, key):
+    """The caller's workspace, or a new one of the size that `fn` names (None for 0)."""
+    if given is not None:
+        if given.get_device() != dev or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
+        return given
+    n = _sizes.get((fn, dev, key))
+    if n is None:
+        size = ctypes.c_size_t()
+        _check(getattr(load_library(), fn)(desc, ctypes.byref(size)), fn)
+        n = size.value
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[(fn, dev, key)] = n
+    return _new(dev, other, (n,), torch.uint8) if n else None
 
 
 def _bytes(t):
@@ -658,7 +651,6 @@ def gattn_block_count(Nk: int, S: int, block: int) -> int:
     return (Nk // block + S) if S else 0
 
 
-@_on_device
 def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None, since=None,
                      sums=None, stream=None) -> torch.Tensor:
     """fp64 sums [blocks, Hkv, D] of the keys of each block (include/gattn.h).
@@ -667,6 +659,9 @@ def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None
     and needs ``sums``, the table to renew.
     """
     dev = _cuda_index("K", K, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_block_sums(K, seq_k, block, lens, since, sums, stream)
     Nk, Hkv, D = K.shape
     S = _sequences(seq_k, seq_k, lens, dev)
     if since is not None:
@@ -674,20 +669,19 @@ def gattn_block_sums(K: torch.Tensor, seq_k: torch.Tensor, block: int, lens=None
         if sums is None:
             raise ValueError("since needs sums, the table to renew")
     shape = (gattn_block_count(Nk, S, block), Hkv, D)
-    run = _Run(dev, stream)
+    handle, other = _stream_of(dev, stream)
     if sums is None:
-        sums = run.empty(shape, torch.float64)
+        sums = _new(dev, other, shape, torch.float64)
     else:
         _want("sums", sums, shape, torch.float64, dev)
     desc = _BLOCK_PACK.pack(S, 0, Nk, Hkv, Hkv, D, _dtype_code(K.dtype), block, 1, 1, 0, 0.0, 0,
                             seq_k.data_ptr(), seq_k.data_ptr(), _at(lens) or 0, 0, 0)
     _check((_lib or load_library()).gattn_block_sums(desc, K.data_ptr(), _at(since),
-                                                     sums.data_ptr(), run.handle),
+                                                     sums.data_ptr(), handle),
            "gattn_block_sums")
     return sums
 
 
-@_on_device
 def gattn_block_select(Q: torch.Tensor, sums: torch.Tensor, seq_q: torch.Tensor,
                        seq_k: torch.Tensor, topk: int, block: int, q_block: int, nk: int,
                        len_k=None, causal: bool = False, max_len_k: int = 0, idx=None,
@@ -698,24 +692,28 @@ def gattn_block_select(Q: torch.Tensor, sums: torch.Tensor, seq_q: torch.Tensor,
     ``max_len_k`` the most keys of one sequence (0: nk).
     """
     dev = _cuda_index("Q", Q, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_block_select(Q, sums, seq_q, seq_k, topk, block, q_block, nk, len_k,
+                                      causal, max_len_k, idx, workspace, stream)
     Nq, H, D = Q.shape
     Hkv = sums.shape[1] if sums.dim() == 3 else 0
     S = _sequences(seq_q, seq_k, len_k, dev)
     _want("sums", sums, (gattn_block_count(nk, S, block), Hkv, D), torch.float64, dev)
     shape = (gattn_block_units(Nq, S, q_block), Hkv, topk)
-    run = _Run(dev, stream)
+    handle, other = _stream_of(dev, stream)
     if idx is None:
-        idx = run.empty(shape, torch.int32)
+        idx = _new(dev, other, shape, torch.int32)
     else:
         _want("idx", idx, shape, torch.int32, dev)
     desc = _BLOCK_PACK.pack(S, Nq, nk, H, Hkv, D, _dtype_code(Q.dtype), block, q_block, topk,
                             1 if causal else 0, 0.0, max_len_k, seq_q.data_ptr(),
                             seq_k.data_ptr(), _at(len_k) or 0, 0, 0)
-    ws = run.workspace(workspace, "gattn_block_select_workspace_size", desc,
-                       (S, Nq, nk, H, Hkv, D, Q.dtype, block, q_block, topk))
+    ws = _workspace(workspace, dev, other, "gattn_block_select_workspace_size", desc,
+                    (S, Nq, nk, H, Hkv, D, Q.dtype, block, q_block, topk))
     _check((_lib or load_library()).gattn_block_select(desc, Q.data_ptr(), sums.data_ptr(),
-                                                       idx.data_ptr(), _at(ws), _bytes(ws),
-                                                       run.handle), "gattn_block_select")
+                                                       idx.data_ptr(), _at(ws), _bytes(ws), handle),
+           "gattn_block_select")
     return idx
 
 
@@ -743,7 +741,6 @@ def _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k
     return dev, desc, (S, Nq, Nk, H, Hkv, D, Q.dtype, block, q_block, topk)
 
 
-@_on_device
 def gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block: int, q_block: int, scale: float = 0.0,
                     causal: bool = False, len_k=None, out=None, lse=None, workspace=None,
                     stream=None):
@@ -753,44 +750,51 @@ def gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block: int, q_block: int, scale:
     anything there.
     """
     dev, desc, key = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
-    run = _Run(dev, stream)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_block_fwd(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal,
+                                   len_k, out, lse, workspace, stream)
+    handle, other = _stream_of(dev, stream)
     if out is None:
-        out = run.empty(Q.shape, Q.dtype)
+        out = _like(Q, other)
     else:
         _want("out", out, Q.shape, Q.dtype, dev)
     if lse is None:
-        lse = run.empty(Q.shape[:2], torch.float32)
+        lse = _new(dev, other, Q.shape[:2], torch.float32)
     else:
         _want("lse", lse, Q.shape[:2], torch.float32, dev)
-    ws = run.workspace(workspace, "gattn_block_fwd_workspace_size", desc, key)
+    ws = _workspace(workspace, dev, other, "gattn_block_fwd_workspace_size", desc, key)
     _check((_lib or load_library()).gattn_block_fwd(
         desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(), out.data_ptr(),
-        lse.data_ptr(), _at(ws), _bytes(ws), run.handle), "gattn_block_fwd")
+        lse.data_ptr(), _at(ws), _bytes(ws), handle), "gattn_block_fwd")
     return out, lse
 
 
-@_on_device
 def gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout, lse, block: int, q_block: int,
                     scale: float = 0.0, causal: bool = False, len_k=None, dQ=None, dK=None,
                     dV=None, workspace=None, stream=None):
     """Gradients (dQ, dK, dV) of gattn_block_fwd; rows of no sequence are not written."""
     dev, desc, key = _block_attn(Q, K, V, idx, seq_q, seq_k, block, q_block, scale, causal, len_k)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout, lse, block, q_block,
+                                   scale, causal, len_k, dQ, dK, dV, workspace, stream)
     _want("out", out, Q.shape, Q.dtype, dev)
     _want("dout", dout, Q.shape, Q.dtype, dev)
     _want("lse", lse, Q.shape[:2], torch.float32, dev)
-    run = _Run(dev, stream)
+    handle, other = _stream_of(dev, stream)
     grads = []
     for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
         if t is None:
-            t = run.empty(like.shape, like.dtype)
+            t = _like(like, other)
         else:
             _want(name, t, like.shape, like.dtype, dev)
         grads.append(t)
-    ws = run.workspace(workspace, "gattn_block_bwd_workspace_size", desc, key)
+    ws = _workspace(workspace, dev, other, "gattn_block_bwd_workspace_size", desc, key)
     _check((_lib or load_library()).gattn_block_bwd(
         desc, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(), out.data_ptr(),
         dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
-        grads[2].data_ptr(), _at(ws), _bytes(ws), run.handle), "gattn_block_bwd")
+        grads[2].data_ptr(), _at(ws), _bytes(ws), handle), "gattn_block_bwd")
     return tuple(grads)
 
 
@@ -821,7 +825,6 @@ def _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps):
     return dev, desc, N, F
 
 
-@_on_device
 def gattn_norm_fwd(res, x=None, gate=None, w_post=None, b_post=None, w_pre=None, b_pre=None,
                    alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6, h=None, y=None,
                    stats=None, stream=None):
@@ -833,29 +836,36 @@ def gattn_norm_fwd(res, x=None, gate=None, w_post=None, b_post=None, w_pre=None,
     (h, y, stats); stats (fp32 [N, 4]) goes to gattn_norm_bwd.
     """
     dev, desc, N, F = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps)
-    run = _Run(dev, stream)
-    for name, t in (("x", x), ("h", h), ("y", y)):
-        if t is not None:
-            _want(name, t, (N, F), res.dtype, dev)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_norm_fwd(res, x, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps,
+                                  h, y, stats, stream)
+    handle, other = _stream_of(dev, stream)
+    shape, dtype = res.shape, res.dtype
     if x is None:
         h = res
-    elif h is None:
-        h = run.empty((N, F), res.dtype)
+    else:
+        _want("x", x, shape, dtype, dev)
+        if h is None:
+            h = _like(res, other)
+        else:
+            _want("h", h, shape, dtype, dev)
     if w_pre is None:
         y = None
     elif y is None:
-        y = run.empty((N, F), res.dtype)
+        y = _like(res, other)
+    else:
+        _want("y", y, shape, dtype, dev)
     if stats is None:
-        stats = run.empty((N, 4), torch.float32)
+        stats = _new(dev, other, (N, 4), torch.float32)
     else:
         _want("stats", stats, (N, 4), torch.float32, dev)
     _check((_lib or load_library()).gattn_norm_fwd(
         desc, res.data_ptr(), _at(x), _at(gate), None if x is None else h.data_ptr(), _at(y),
-        stats.data_ptr(), run.handle), "gattn_norm_fwd")
+        stats.data_ptr(), handle), "gattn_norm_fwd")
     return h, y, stats
 
 
-@_on_device
 def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None, b_post=None,
                    w_pre=None, b_pre=None, alpha: float = 1.0, kind: str = "rms",
                    workspace=None, stream=None) -> dict:
@@ -866,18 +876,21 @@ def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None,
     where the operand is absent.
     """
     dev, desc, N, F = _norm_desc(res, gate, w_post, b_post, w_pre, b_pre, alpha, kind, 0.0)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_norm_bwd(res, stats, dh, dy, x, gate, w_post, b_post, w_pre, b_pre,
+                                  alpha, kind, workspace, stream)
     for name, t in (("dh", dh), ("dy", dy), ("x", x)):
         if t is not None:
             _want(name, t, (N, F), res.dtype, dev)
     _want("stats", stats, (N, 4), torch.float32, dev)
-    run = _Run(dev, stream)
-    g = {"dres": run.empty((N, F), res.dtype),
-         "dx": None if x is None else run.empty((N, F), res.dtype),
-         "dgate": None if gate is None else run.empty(gate.shape, gate.dtype)}
+    handle, other = _stream_of(dev, stream)
+    g = {"dres": _like(res, other), "dx": None if x is None else _like(x, other),
+         "dgate": None if gate is None else _like(gate, other)}
     for n, t in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre), ("db_pre", b_pre)):
-        g[n] = None if t is None else run.empty((F,), torch.float32)
-    ws = run.workspace(workspace, "gattn_norm_workspace_size", desc, (N, F, res.dtype))
+        g[n] = None if t is None else _like(t, other)
+    ws = _workspace(workspace, dev, other, "gattn_norm_workspace_size", desc, (N, F, res.dtype))
     _check((_lib or load_library()).gattn_norm_bwd(
         desc, res.data_ptr(), stats.data_ptr(), _at(dh), _at(dy), _at(x), _at(gate),
-        *[_at(t) for t in g.values()], _at(ws), _bytes(ws), run.handle), "gattn_norm_bwd")
+        *[_at(t) for t in g.values()], _at(ws), _bytes(ws), handle), "gattn_norm_bwd")
     return g

@@ -16,13 +16,19 @@
 
 namespace gattn {
 
-int sm_count() {
+int sm_count() {  // of the current device; asked once per device
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
-    n = 152;
+    return 152;
   }
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -4,14 +4,15 @@
 // The choice is a whole number that must not hang on the order of a sum, so
 // it is defined by scores in 64 bits.  Sums run as pairs of fp32 (each
 // addition keeps its exact rounding error in the second member, about 48
-// bits, at fp32 rates: this GPU's fp64 units would take four times as long as
-// the memory).  Scores run in fp32 FMAs with an error bound
+// bits, at fp32 rates: this GPU's fp64 units add two numbers a clock and SM,
+// a fiftieth of what memory delivers); fp64 appears once per finished sum.  Scores run in fp32 FMAs with an error bound
 //   |score - exact| <= e = (D + 32) 2^-23 |q| max|k / n|   (Cauchy-Schwarz),
 // a radix select finds the topk-th score T, blocks above T + 2e are in, below
 // T - 2e out, and only blocks in between are scored again in fp64.
 #include <algorithm>
 
 #include "attn_launch.cuh"
+#include "attn_pipe.cuh"
 #include "block.cuh"
 
 namespace gattn {
@@ -50,61 +51,86 @@ struct SumParams {
   const void* x;
   const int32_t* since;
   double* sums;
-  int per, heads;  // rows per piece, rows of one head group
+  int per, l_heads;  // rows per piece, log2 of the heads of a group
   bool queries;
-  int cx;          // 16-byte columns a CTA covers (a power of two)
+  int cx;            // 16-byte columns a CTA covers (a power of two)
+  int zs;            // since: CTAs that share a sequence's pieces
 };
 
-// One CTA: piece blockIdx.x, columns [blockIdx.y * cx, + cx) of the Hkv * D
-// sums.  256 / cx strands share the piece's (row, head) pairs; their pairs
-// meet in shared memory in strand order.
+// (a, e) += f, with e the exact rounding errors of a's additions
+__device__ __forceinline__ void add_exact(float2& a, float2& e, float2 f) {
+  const float2 minus = f2s(-1.f);
+  const float2 t = f2add(a, f);
+  const float2 b = f2fma(a, minus, t);                     // what f became
+  const float2 c = f2fma(f2fma(b, minus, t), minus, a);    // what a lost
+  e = f2add(e, f2add(c, f2fma(b, minus, f)));
+  a = t;
+}
+
+// A CTA sums 16-byte columns [blockIdx.y * cx, + cx) of the Hkv * D sums of
+// one piece (or, with `since`, of a sequence's pieces from there on).
+// 256 / cx strands share the piece's (row, head) pairs; their (sum, error)
+// pairs meet in shared memory in strand order.
 template <class T>
 __global__ void __launch_bounds__(kThr) piece_sums_kernel(const SumParams p) {
   constexpr int V = Vec16<T>::V;
-  __shared__ double sh[kThr * V];
+  __shared__ float2 sh[kThr * V];
   const BlockGeom& g = p.g;
   const int32_t* beg = p.queries ? g.seq_q : g.seq_k;
-  const int piece = blockIdx.x;
-  const int s = piece_seq(beg, g.S, p.per, piece);
+  const int s = p.since ? blockIdx.x : piece_seq(beg, g.S, p.per, blockIdx.x);
   const Span sp = p.queries ? span_q(g, s) : span_k(g, s);
-  const int64_t pos = int64_t(piece - piece_base(beg, s, p.per)) * p.per;
-  const int n = pos >= 0 && pos < sp.len ? (int)min(int64_t(p.per), sp.len - pos) : 0;
-  if (p.since && (n == 0 || pos + p.per <= p.since[s])) return;
+  const int base = piece_base(beg, s, p.per), rows = p.queries ? g.U : g.B;
   const int cx = p.cx, tx = threadIdx.x & (cx - 1), ty = threadIdx.x / cx, ny = kThr / cx;
+  const int W = g.Hkv * g.D, heads = 1 << p.l_heads;
   const int col = (blockIdx.y * cx + tx) * V;  // of Hkv * D
-  const int W = g.Hkv * g.D;
-  float a[V], e[V];
+  int j = blockIdx.x - base, step = 1, last = j;  // pieces of the sequence
+  if (p.since) {
+    j = max(p.since[s], 0) / p.per + blockIdx.z;
+    step = p.zs;
+    last = (sp.len + p.per - 1) / p.per - 1;
+  }
+  for (; j <= last; j += step) {
+    const int piece = base + j;
+    const int64_t pos = int64_t(j) * p.per;
+    const int n = pos >= 0 && pos < sp.len ? (int)min(int64_t(p.per), sp.len - pos) : 0;
+    if (piece >= rows) break;
+    float2 a[V / 2], e[V / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) a[i] = e[i] = 0.f;
-  if (col < W) {
-    const int kh = col / g.D, d = col - kh * g.D;
-    const T* x = static_cast<const T*>(p.x) + (sp.beg + pos) * int64_t(W) * p.heads +
-                 int64_t(kh) * p.heads * g.D + d;
-    const int total = n * p.heads;
-#pragma unroll 4
-    for (int i = ty; i < total; i += ny) {
-      const int r = i / p.heads, h = i - r * p.heads;
-      float f[V];
-      Vec16<T>::load(x + int64_t(r) * W * p.heads + h * g.D, f);
+    for (int i = 0; i < V / 2; ++i) a[i] = e[i] = make_float2(0.f, 0.f);
+    if (col < W) {
+      const int kh = col / g.D, d = col - kh * g.D;
+      const T* x = static_cast<const T*>(p.x) + (((sp.beg + pos) * W) << p.l_heads) +
+                   int64_t(kh) * heads * g.D + d;
+      const int total = n << p.l_heads;
+#pragma unroll 8
+      for (int i = ty; i < total; i += ny) {
+        float f[V];
+        Vec16<T>::load(x + ((int64_t(i >> p.l_heads) * W) << p.l_heads) +
+                           int64_t(i & (heads - 1)) * g.D, f);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {  // a + f = t exactly, up to what e keeps
-        const float t = a[k] + f[k];
-        const float b = t - a[k];
-        e[k] += (a[k] - (t - b)) + (f[k] - b);
-        a[k] = t;
+        for (int k = 0; k < V / 2; ++k) add_exact(a[k], e[k], make_float2(f[2 * k], f[2 * k + 1]));
       }
     }
-  }
+    __syncthreads();  // the last piece's sums have been read
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    sh[ty * cx * V + tx * V + i] =
-        fabsf(a[i]) <= 3.4e38f ? double(a[i]) + double(e[i]) : double(a[i]);
-  __syncthreads();
-  for (int c = threadIdx.x; c < cx * V; c += kThr) {
-    double t = 0.0;
-    for (int y = 0; y < ny; ++y) t += sh[y * cx * V + c];
-    const int o = blockIdx.y * cx * V + c;
-    if (o < W) p.sums[int64_t(piece) * W + o] = t;
+    for (int i = 0; i < V / 2; ++i) {
+      sh[ty * cx * V + tx * V + 2 * i] = make_float2(a[i].x, e[i].x);
+      sh[ty * cx * V + tx * V + 2 * i + 1] = make_float2(a[i].y, e[i].y);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < cx * V; c += kThr) {
+      float2 t = sh[c];
+      for (int y = 1; y < ny; ++y) {
+        const float2 f = sh[y * cx * V + c];
+        float2 aa = make_float2(t.x, 0.f), ee = make_float2(t.y, 0.f);
+        add_exact(aa, ee, make_float2(f.x, 0.f));
+        t = make_float2(aa.x, ee.x + f.y);
+      }
+      const int o = blockIdx.y * cx * V + c;
+      // (an infinite sum has no error to add)
+      if (o < W) p.sums[int64_t(piece) * W + o] =
+          fabsf(t.x) <= 3.4e38f ? double(t.x) + double(t.y) : double(t.x);
+    }
   }
 }
 
@@ -184,7 +210,7 @@ __device__ uint32_t kth_key(const double* sc, int n, int k, uint32_t* hist) {
 // UT consecutive units of one key head per CTA.  A score entry is 8 bytes:
 // the fp32 score, or the fp64 score of a block near the last place.
 template <class T, int UT>
-__global__ void __launch_bounds__(kThr) select_kernel(const SelParams p) {
+__global__ void __launch_bounds__(kThr, 4) select_kernel(const SelParams p) {
   extern __shared__ __align__(16) double sm[];
   const BlockGeom& g = p.g;
   const int D = g.D, kh = blockIdx.y;
@@ -428,13 +454,17 @@ gattn_status launch_block_sums(const BlockGeom& g, gattn_dtype dt, const void* x
   p.sums = sums;
   p.queries = queries;
   p.per = queries ? g.qb : g.block;
-  p.heads = queries ? g.G : 1;
+  p.l_heads = queries ? 31 - __builtin_clz(g.G) : 0;
   const int V = dt == GATTN_F32 ? 4 : 8;
   const int cols = g.Hkv * g.D / V;  // a power of two
   p.cx = std::min(cols, 64);
   const int pieces = queries ? g.U : g.B;
   if (pieces <= 0) return GATTN_OK;
-  const dim3 grid(pieces, (cols + p.cx - 1) / p.cx);
+  // from a position on, a sequence has few pieces to renew (one new token: one):
+  // CTAs by sequence instead of one that looks and leaves per piece
+  p.zs = 4;
+  const unsigned ny = unsigned((cols + p.cx - 1) / p.cx);
+  const dim3 grid = since ? dim3(g.S, ny, p.zs) : dim3(pieces, ny);
   if (dt == GATTN_F32) piece_sums_kernel<float><<<grid, kThr, 0, st>>>(p);
   else piece_sums_kernel<__nv_bfloat16><<<grid, kThr, 0, st>>>(p);
   return launched("gattn_block_sums");

@@ -30,6 +30,7 @@
 
 #include "attn_launch.cuh"
 #include "attn_pipe.cuh"
+#include "block.cuh"
 
 namespace gattn {
 
@@ -617,16 +618,6 @@ gattn_status launched(const char* what) {
   return GATTN_OK;
 }
 
-int sms_here() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    n = 152;
-  }
-  return n;
-}
-
 template <class K>
 void launch_ring(K kern, unsigned grid, int threads, int bytes, const NormParams& p,
                  cudaStream_t st) {
@@ -641,7 +632,7 @@ void fwd_go(const NormParams& p, cudaStream_t st) {
   const int64_t ctas = W == 1 ? (p.N + 3) / 4 : p.N;
   using Rg = Ring<T, V, E, W, 3, CTAS, V * sizeof(T) < 4>;
   const unsigned grid = unsigned(
-      Rg::kStages == 0 ? ctas : std::min<int64_t>(ctas, int64_t(CTAS) * sms_here()));
+      Rg::kStages == 0 ? ctas : std::min<int64_t>(ctas, int64_t(CTAS) * sm_count()));
   launch_ring(norm_fwd_kernel<T, V, E, W, LN>, grid, W == 1 ? 128 : W * 32, Rg::kBytes, p, st);
 }
 
@@ -678,7 +669,7 @@ BwdShape bwd_shape(const gattn_norm_desc* d) {
   s.warps = d->F <= 256 ? 1 : d->F <= 1024 ? 4 : 16;
   const int64_t per_sm = s.warps <= 4 ? 4 : 1;  // bwd_ctas
   const int64_t rows = s.warps == 1 ? (d->N + 3) / 4 : d->N;
-  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, per_sm * sms_here())));
+  s.grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, per_sm * sm_count())));
   s.slots = int(s.grid) * (s.warps == 1 ? 4 : 1);
   return s;
 }
