@@ -1,0 +1,223 @@
+"""The block-attention and norm operators through autograd, and a transformer layer that runs
+them together with the attention over edges, against compositions in 64 bits."""
+import math
+
+import pytest
+
+from gnn_sparse_attention_gb300 import synth
+from tests.helpers import TOL, relerr
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+pytestmark = pytest.mark.gpu
+
+from gnn_sparse_attention_gb300 import binding as gb  # noqa: E402
+from gnn_sparse_attention_gb300 import layer  # noqa: E402
+from tests import block_ref as ref  # noqa: E402
+
+DEV = "cuda"
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_block_attention_autograd(dtype, causal):
+    torch.manual_seed(0)
+    sq = [0, 150, 150, 231]
+    H, Hkv, D = 4, 2, 64
+    # ten more rows than the sequences hold: they get zeros, also as gradients
+    Q, K, V = (torch.randn(241, h, D, device=DEV).to(dtype).requires_grad_() for h in (H, Hkv, Hkv))
+    G = torch.randn(241, H, D, device=DEV).to(dtype)
+    out, lse, idx = layer.block_attention(Q, K, V, i32(sq), topk=2, block=32, q_block=32, causal=causal)
+    want = ref.select(Q.detach(), K.detach(), sq, sq, 2, 32, 32, causal)
+    assert torch.equal(idx[:want.shape[0]].cpu(), want)
+    out.backward(G)
+    r = ref.attention(Q.detach(), K.detach(), V.detach(), idx, sq, sq, 32, 32, causal=causal, dout=G)
+    ref.check(out.detach(), r, "out", 0.0)
+    ref.check(lse, r, "lse", 0.0)
+    for t, n in ((Q, "dQ"), (K, "dK"), (V, "dV")):
+        ref.check(t.grad, r, n, 0.0)
+
+
+def test_block_attention_serves_a_cache():
+    """One new token per sequence against keys with room behind them, through the layer call."""
+    torch.manual_seed(1)
+    S, room, H, Hkv, D = 3, 128, 8, 2, 64
+    Q = torch.randn(S, H, D, device=DEV).to(torch.bfloat16)
+    K, V = (torch.randn(S * room, Hkv, D, device=DEV).to(torch.bfloat16) for _ in range(2))
+    lens, sk, sq = [100, 1, 128], [0, room, 2 * room, 3 * room], [0, 1, 2, 3]
+    out, lse, idx = layer.block_attention(Q, K, V, i32(sq), topk=3, block=16, q_block=1, causal=True,
+                                          seq_k=i32(sk), len_k=i32(lens))
+    assert torch.equal(idx.cpu(), ref.select(Q, K, sq, sk, 3, 16, 1, True, lens))
+    r = ref.attention(Q, K, V, idx, sq, sk, 16, 1, causal=True, lk=lens)
+    ref.check(out, r, "out")
+    ref.check(lse, r, "lse")
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_gated_residual_norm_autograd(kind):
+    torch.manual_seed(2)
+    N, F = 50, 96
+    leaf = {k: torch.randn(N, F, device=DEV, requires_grad=True) for k in ("res", "x", "gate")}
+    leaf.update({k: (torch.randn(F, device=DEV) * 0.2 + 1).requires_grad_() for k in
+                 ("w_post", "b_post", "w_pre", "b_pre")})
+    gh, gy = torch.randn(N, F, device=DEV), torch.randn(N, F, device=DEV)
+    h, y = layer.gated_residual_norm(**leaf, alpha=0.5, kind=kind, eps=1e-5)
+    torch.autograd.backward([h, y], [gh, gy])
+    d = {k: v.detach().double().requires_grad_() for k, v in leaf.items()}
+
+    def norm(v, w, b):
+        v = v - v.mean(-1, keepdim=True) if kind == "layer" else v
+        return v / torch.sqrt(v.pow(2).mean(-1, keepdim=True) + 1e-5) * w + b
+
+    h64 = d["res"] + 0.5 * d["gate"] * norm(d["x"], d["w_post"], d["b_post"])
+    y64 = norm(h64, d["w_pre"], d["b_pre"])
+    torch.autograd.backward([h64, y64], [gh.double(), gy.double()])
+    assert relerr(np64(h), np64(h64)) < TOL["f32"] and relerr(np64(y), np64(y64)) < TOL["f32"]
+    for k in leaf:
+        assert relerr(np64(leaf[k].grad), np64(d[k].grad)) < TOL["f32"], k
+
+
+def test_gated_residual_norm_parts_without_a_gradient():
+    """Only one of the two results is used; a gate or a norm is left out."""
+    torch.manual_seed(3)
+    x, r = (torch.randn(20, 64, device=DEV, requires_grad=True) for _ in range(2))
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    h, y = layer.gated_residual_norm(r, x, w_pre=w)
+    h.sum().backward()
+    assert torch.equal(r.grad, torch.ones_like(r)) and torch.equal(x.grad, torch.ones_like(x))
+    assert torch.equal(w.grad, torch.zeros_like(w))
+    x.grad = r.grad = w.grad = None
+    h, y = layer.gated_residual_norm(r, w_pre=w)
+    y.sum().backward()
+    assert r.grad is not None and w.grad is not None and torch.isfinite(r.grad).all()
+    h, y = layer.gated_residual_norm(r, x, alpha=2.0)
+    assert y is None and relerr(np64(h), np64(r) + 2 * np64(x)) < 1e-6
+
+
+def _dense_block(m, h, seq, idx, ip, ix, block, q_block, causal):
+    """GraphTransformerBlock in fp64 on the CPU: dense masks for the edges and for the blocks."""
+    P = {n: p.detach().double().cpu().requires_grad_() for n, p in m.named_parameters()}
+    h = h.detach().double().cpu().requires_grad_()
+    N, H, D = h.shape[0], m.heads, m.head_dim
+    edges = torch.zeros(N, N, dtype=torch.bool)
+    for i in range(N):
+        edges[i, ix[ip[i]:ip[i + 1]].tolist()] = True
+    blocks = torch.zeros(H, N, N, dtype=torch.bool)
+    for s in range(len(seq) - 1):
+        a, n = seq[s], seq[s + 1] - seq[s]
+        for k in range(H):
+            blocks[k, a:a + n, a:a + n] = ref.allowed(idx.cpu(), s, k, n, n, a, block, q_block, causal, "cpu")
+
+    def norm(v, name):
+        v2 = v - v.mean(-1, keepdim=True) if m.kind == "layer" else v
+        v2 = v2 / torch.sqrt(v2.pow(2).mean(-1, keepdim=True) + 1e-6) * P[f"w_{name}"]
+        return v2 + P[f"b_{name}"] if m.kind == "layer" else v2
+
+    def attend(q, k, v, ok):
+        sc = (q @ k.T / math.sqrt(D)).masked_fill(~ok, -math.inf)
+        p = torch.softmax(sc, -1)
+        return torch.where(ok.any(1, keepdim=True), torch.nan_to_num(p), 0.0) @ v
+
+    q, k, v = (t.reshape(N, H, D) for t in (norm(h, "in") @ P["qkv.weight"].T).chunk(3, -1))
+    a = torch.stack([attend(q[:, i], k[:, i], v[:, i], blocks[i]) + attend(q[:, i], k[:, i], v[:, i], edges)
+                     for i in range(H)], 1)
+    h1 = h + P["gate_attn"] * norm(a.reshape(N, -1) @ P["o.weight"].T, "attn")
+    mlp = torch.nn.functional.gelu(norm(h1, "mid") @ P["up.weight"].T) @ P["down.weight"].T
+    return h1 + P["gate_mlp"] * norm(mlp, "mlp"), h, P
+
+
+@pytest.mark.parametrize("kind,causal", [("rms", False), ("layer", True)])
+def test_transformer_block_matches_a_dense_composition(kind, causal):
+    """All operators in one layer, forward and gradients, fp32 (bar 1e-4 of the largest value)."""
+    torch.manual_seed(4)
+    seq = [0, 90, 90, 161]
+    N, dim, H, D = seq[-1], 48, 2, 16
+    ip, ix = synth.small_graph(5, N, 4.0, isolated=0.1)
+    m = layer.GraphTransformerBlock(dim, H, D, mlp_dim=64, topk=2, block=16, q_block=16, causal=causal,
+                                    kind=kind, gate_init=0.5, dtype=torch.float32, device=DEV)
+    with torch.no_grad():
+        for n, p in m.named_parameters():
+            if n.startswith(("w_", "b_", "gate")):
+                p.add_(0.1 * torch.randn_like(p))
+    h = torch.randn(N, dim, device=DEV, requires_grad=True)
+    plan = gb.gattn_plan_create(torch.from_numpy(ip).cuda(), torch.from_numpy(ix).cuda())
+    try:
+        # the choice, fixed for both sides
+        with torch.no_grad():
+            _, y = layer.gated_residual_norm(h, w_pre=m.w_in, b_pre=m.b_in, kind=kind)
+            Q, K, _ = (t.reshape(N, H, D).contiguous() for t in m.qkv(y).chunk(3, -1))
+            sums = gb.gattn_block_sums(K, i32(seq), 16)
+            idx = gb.gattn_block_select(Q, sums, i32(seq), i32(seq), 2, 16, 16, N, causal=causal)
+        out = m(h, i32(seq), plan)
+        assert torch.equal(out, m(h, i32(seq), plan, idx=idx))
+        g = torch.randn_like(out)
+        out.backward(g)
+        want, h64, P = _dense_block(m, h, seq, idx, ip, ix, 16, 16, causal)
+        want.backward(g.double().cpu())
+        assert relerr(np64(out), want.detach().numpy()) < TOL["f32"]
+        assert relerr(np64(h.grad), h64.grad.numpy()) < TOL["f32"]
+        for n, p in m.named_parameters():
+            assert relerr(np64(p.grad), P[n].grad.numpy()) < TOL["f32"], n
+    finally:
+        plan.close()
+
+
+def test_transformer_block_trains_in_bf16():
+    """Two layers, a step of training on ragged graphs: runs, and every gradient is finite."""
+    torch.manual_seed(5)
+    seq = [0, 700, 701, 1300]
+    ip, ix = synth.small_graph(6, seq[-1], 6.0)
+    plan = gb.gattn_plan_create(torch.from_numpy(ip).cuda(), torch.from_numpy(ix).cuda())
+    ms = [layer.GraphTransformerBlock(256, 4, 64, topk=4, kind=k, device=DEV) for k in ("rms", "layer")]
+    h = torch.randn(seq[-1], 256, device=DEV).to(torch.bfloat16).requires_grad_()
+    try:
+        x = h
+        for m in ms:
+            x = m(x, i32(seq), plan)
+        x.float().pow(2).mean().backward()
+        torch.cuda.synchronize()
+        gb.gattn_block_check_errors()
+        assert torch.isfinite(x).all() and torch.isfinite(h.grad).all()
+        for m in ms:
+            for n, p in m.named_parameters():
+                assert p.grad is not None and torch.isfinite(p.grad).all(), n
+    finally:
+        plan.close()
+
+
+def test_training_step_in_a_graph():
+    """A layer's forward and backward captured and replayed (its leaves used in no eager graph
+    that is still alive)."""
+    torch.manual_seed(6)
+    seq = i32([0, 300, 420])
+    m = layer.GraphTransformerBlock(128, 2, 64, topk=2, device=DEV)
+    h = torch.randn(420, 128, device=DEV).to(torch.bfloat16)
+    g = torch.randn(420, 128, device=DEV).to(torch.bfloat16)
+
+    def step():
+        grads = torch.autograd.grad(m(h, seq), list(m.parameters()), g)
+        return [t.clone() for t in grads]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            want = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert relerr(np64(b), np64(a)) < 1e-2
