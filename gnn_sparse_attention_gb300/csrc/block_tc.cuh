@@ -139,34 +139,39 @@ __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, int group, int st
   }
 }
 
-// 16 bf16 of a row: one 32-byte store where the address allows it (a lane then
-// fills a whole sector; 16-byte stores to rows far apart take twice the time).
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, bool wide) {
-  uint32_t w[8];
+// 32 fp32 columns as 16 registers of bf16 pairs
+__device__ __forceinline__ void pack_row(const float* v, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
+  for (int i = 0; i < 16; ++i) w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
 }
-// 32 columns [col, col + 32) of a row of D values at `row`
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int col, int D, const float* v,
-                                          bool wide) {
+// Packed columns [col, col + 32) of a row of D values at `row`: 32-byte stores
+// where the address allows them (a lane then fills a whole sector; 16-byte
+// stores to rows far apart take twice the time).
+__device__ __forceinline__ void store_packed(__nv_bfloat16* row, int col, int D, const uint32_t* w,
+                                             bool wide) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    if (col + q * 16 + 16 <= D) {
-      store16(row + col + q * 16, v + q * 16, wide);
-    } else if (col + q * 16 < D) {  // D = 8
-      *reinterpret_cast<uint4*>(row + col) =
-          make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
-                     bf16x2_bits(v[6], v[7]));
+    const int c = col + q * 16;
+    if (c + 16 <= D && wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(row + c),
+                   "r"(w[8 * q]), "r"(w[8 * q + 1]), "r"(w[8 * q + 2]), "r"(w[8 * q + 3]),
+                   "r"(w[8 * q + 4]), "r"(w[8 * q + 5]), "r"(w[8 * q + 6]), "r"(w[8 * q + 7])
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (c + 8 * e < D)
+          *reinterpret_cast<uint4*>(row + c + 8 * e) =
+              make_uint4(w[8 * q + 4 * e], w[8 * q + 4 * e + 1], w[8 * q + 4 * e + 2],
+                         w[8 * q + 4 * e + 3]);
     }
   }
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int col, int D, const float* v,
+                                          bool wide) {
+  uint32_t w[16];
+  pack_row(v, w);
+  store_packed(row, col, D, w, wide);
 }
 __device__ __forceinline__ bool wide_rows(const void* base, int D) {
   return D >= 16 && (reinterpret_cast<uintptr_t>(base) & 31) == 0;

@@ -15,9 +15,11 @@
 // P V and next scores.  P in TMEM instead of shared memory takes 64 KB of the
 // step's 160 KB of shared-memory traffic away (128 bytes a clock would
 // otherwise be the bound at D = 128) and leaves room for a third stage.
-// Roles: warps 0-7 softmax, warp 8 issues the products, warp 9 issues TMA, warp
-// 10 resolves the next tile's block list meanwhile (a chain of dependent loads of
-// two microseconds); every hand-over is an mbarrier, every wait is bounded.
+// Roles: warps 0-7 softmax, warps 8-11 merge a finished tile's streams and write
+// it while the softmax is at the next one, warp 12 issues the products, warp 13
+// issues TMA, warp 14 resolves the next tile's block list meanwhile (a chain of
+// dependent loads of two microseconds); every hand-over is an mbarrier, every
+// wait is bounded.
 //
 // With the list ascending, the keys that a row sees are the first columns of
 // its steps (list_keys), so the mask is one number per row and only the
@@ -47,7 +49,9 @@ __device__ int g_err;  // a bounded wait gave up
 constexpr int kT = kBlkTile;
 constexpr int kPiece = kT * 128;       // 128 rows x 64 bf16 columns
 constexpr int kSoftWarps = 8;           // two streams of four
-constexpr int kThr = (kSoftWarps + 3) * 32;
+constexpr int kOutWarps = 4;
+constexpr int kMma = kSoftWarps + kOutWarps, kCopy = kMma + 1, kLists = kMma + 2;
+constexpr int kThr = (kLists + 1) * 32;
 
 struct TcFwdParams {
   CUtensorMap mq, mk, mv;
@@ -78,21 +82,23 @@ struct TileInfo {
 template <int DP>
 struct Sm {
   static constexpr int KB = DP / 64;
-  static constexpr int NQ = DP == 64 ? 2 : 1;   // Q buffers
-  static constexpr int NS = DP == 64 ? 4 : 3;   // K and V stages
+  static constexpr int NQ = 2;                  // Q buffers
+  static constexpr int NS = DP == 64 ? 4 : 2;   // K stages
+  static constexpr int NV = DP == 64 ? 4 : 2;   // V stages
   static constexpr int NO = DP == 64 ? 2 : 1;   // output buffers of a stream (tiles in turn)
   static constexpr int OP = KB * kPiece;         // one operand tile
   static constexpr int Q = 0;
   static constexpr int K = Q + NQ * OP;
   static constexpr int V = K + NS * OP;
-  static constexpr int RED = V + NS * OP;        // [2 streams][128] fp32
-  static constexpr int IDS = RED + 1024;
+  static constexpr int ML = V + NV * OP;         // [2 tiles][2 streams][128] (m, l)
+  static constexpr int LIM = ML + 4096;          // [2 tiles][128] keys that a row sees
+  static constexpr int IDS = LIM + 2 * kT * 2;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(TileInfo));
-  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 6 + NO + 4;
+  static constexpr int NBAR = 4 + 2 * NQ + 2 * NS + 2 * NV + 6 + 2 * NO + 4;
   static constexpr int END = BAR + NBAR * 8 + 8;
-  static constexpr int BYTES = END + 1024 <= 227 * 1024 ? END + 1024 : 227 * 1024;
-  static_assert(END <= 227 * 1024, "shared memory of one CTA");
+  static constexpr int BYTES = END + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
   // TMEM: scores of the streams [0, 256), outputs from 256 on
   static constexpr int out_col(int stream, int buf) { return 2 * kT + (buf * 2 + stream) * DP; }
   static_assert(out_col(1, NO - 1) + DP <= 512, "TMEM columns");
@@ -104,35 +110,37 @@ template <int DP>
 __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ TcFwdParams p) {
   using namespace tc;
   using M = Sm<DP>;
-  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, NO = M::NO, OP = M::OP;
+  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, NV = M::NV, NO = M::NO, OP = M::OP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
-  if (pad + M::END > M::BYTES) {  // the swizzled tiles need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicOr(&g_err, 1);
-    return;
-  }
-  uint8_t* sm = smem_raw + pad;
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
            *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
-           *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
-           *p_full = s_full + 2, *pv_done = p_full + 2, *o_empty = pv_done + 2,
-           *pair = o_empty + NO;
+           *v_full = k_empty + NS, *v_empty = v_full + NV, *s_full = v_empty + NV,
+           *p_full = s_full + 2, *pv_done = p_full + 2, *o_full = pv_done + 2,
+           *o_empty = o_full + NO, *ml_full = o_empty + NO, *ml_empty = ml_full + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   TileInfo* info = reinterpret_cast<TileInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
+  int16_t* lims = reinterpret_cast<int16_t*>(sm + M::LIM);
+  float2* ml = reinterpret_cast<float2*>(sm + M::ML);
   const BlockGeom& g = p.g;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(tile_full + i, 1);
-      mbar_init(tile_empty + i, kSoftWarps + 2);
+      mbar_init(tile_empty + i, kSoftWarps + kOutWarps + 2);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kSoftWarps / 2);
       mbar_init(pv_done + i, 1);
+      mbar_init(ml_full + i, kSoftWarps);
+      mbar_init(ml_empty + i, kOutWarps);
     }
-    for (int i = 0; i < NO; ++i) mbar_init(o_empty + i, kSoftWarps);
+    for (int i = 0; i < NO; ++i) {
+      mbar_init(o_full + i, 1);
+      mbar_init(o_empty + i, kOutWarps);
+    }
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
@@ -140,20 +148,21 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     for (int i = 0; i < NS; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < NV; ++i) {
       mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(pair + i, 2);
     mbar_init_fence();
   }
-  if (warp == kSoftWarps) tmem_alloc512(s_tmem);
+  if (warp == kMma) tmem_alloc512(s_tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   bool ok = true;  // false: a wait gave up, leave
 
-  if (warp == kSoftWarps + 2) {
+  if (warp == kLists) {
     // ---------------------------------------------------------------- lists
     int ti = 0;
     for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
@@ -197,10 +206,16 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         f.poison = 0;
         f.part = t;
       }
+      for (int r = lane; r < kT; r += 32) {
+        const int tt = r / p.ht;
+        lims[slot * kT + r] = int16_t(
+            r >= p.rows || tt >= un.n ? 0
+            : g.causal ? list_keys(list, n, g.block, min(un.pos + tt + 1, ks.len)) : total);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(tile_full + slot);
     }
-  } else if (warp == kSoftWarps + 1) {
+  } else if (warp == kCopy) {
     // ---------------------------------------------------------------- copies
     const int per = kT / g.block;  // blocks per step
     const uint32_t blk_bytes = uint32_t(g.block) * 128;
@@ -225,11 +240,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         }
       }
       for (int st = s0; st < s1; ++st, ++gi) {
-        const int si = gi % NS;
         const int nb = min(per, n - st * per);  // blocks of this step
         for (int kv = 0; kv < 2; ++kv) {
+          const int ns = kv ? NV : NS, si = gi % ns;
           uint64_t* full = (kv ? v_full : k_full) + si;
-          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / NS) - 1) & 1);
+          if (gi >= ns) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / ns) - 1) & 1);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
           __syncwarp();
@@ -249,12 +264,12 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int i = 1; i <= NQ && i <= tq; ++i)
         warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
-      for (int c = gi; c > gi - NS && c >= 0; --c) {  // the newest use of each stage
+      for (int c = gi; c > gi - NS && c >= 0; --c)  // the newest use of each stage
         warp_wait(k_full + c % NS, (c / NS) & 1, 200);
-        warp_wait(v_full + c % NS, (c / NS) & 1, 200);
-      }
+      for (int c = gi; c > gi - NV && c >= 0; --c)
+        warp_wait(v_full + c % NV, (c / NV) & 1, 200);
     }
-  } else if (warp == kSoftWarps) {
+  } else if (warp == kMma) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t IDESC_S = f16_idesc(kT, kT, false), IDESC_O = f16_idesc(kT, DP, true);
     const uint64_t dQ = desc_k(sm + M::Q), dK = desc_k(sm + M::K), dV = desc_mn(sm + M::V, kPiece);
@@ -265,10 +280,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     // P V are due: step gi - 1 and gi - 2, in tiles of `tile` steps.
     int gi = 0, ti = 0, tq = 0, done = 0;       // steps with scores, tiles, with P V
     int due_tile[2] = {0, 0}, due_i[2] = {0, 0};  // by stream: the tile, the step in it
+    bool due_last[2] = {false, false};
     auto product_pv = [&]() {                   // of step `done`
-      const int x = done & 1, si = done % NS, tile = x ? due_tile[1] : due_tile[0];
+      const int x = done & 1, si = done % NV, tile = x ? due_tile[1] : due_tile[0];
       const int i = x ? due_i[1] : due_i[0], buf = tile % NO;
-      ok = ok && warp_wait(p_full + x, (done >> 1) & 1) && warp_wait(v_full + si, (done / NS) & 1);
+      ok = ok && warp_wait(p_full + x, (done >> 1) & 1) && warp_wait(v_full + si, (done / NV) & 1);
       if (i == 0 && tile >= NO) ok = ok && warp_wait(o_empty + buf, (tile / NO - 1) & 1);
       if (!ok) return;
       tc_fence_after();
@@ -277,6 +293,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
                    i >= 2);
         mma_commit(pv_done + x);
         mma_commit(v_empty + si);
+        if (x ? due_last[1] : due_last[0]) mma_commit(o_full + buf);
       }
       __syncwarp();
       ++done;
@@ -311,9 +328,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         if (x) {
           due_tile[1] = tq;
           due_i[1] = i;
+          due_last[1] = i == n - 1;
         } else {
           due_tile[0] = tq;
           due_i[0] = i;
+          due_last[0] = i == n - 1;
         }
       }
       ++tq;
@@ -328,37 +347,25 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         warp_wait(pv_done + (c & 1), (c >> 1) & 1, 200);
       }
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
     const int quad = warp & 3, x = warp >> 2;  // TMEM lane quarter, stream
     const int r = quad * 32 + lane;
     const uint32_t lanes = uint32_t(quad * 32) << 16;
     const uint32_t tS = tmem + lanes + x * kT;
-    float* red = reinterpret_cast<float*>(sm + M::RED);
-    const bool wide = wide_rows(p.out, g.D);
     int gi = 0, ti = 0, to = 0;  // steps, tiles, tiles with steps
-    const int th = r % p.ht, tt = r / p.ht;
-    // the two warps of these rows (one per stream) have written; both may read
-    auto meet = [&](int phase) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair + quad);
-      ok = ok && warp_wait(pair + quad, phase);
-    };
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
       if (!ok) break;
-      const TileInfo f = info[slot];
-      const int* list = ids + slot * kBlkMaxTopk;
-      const bool valid = r < p.rows && tt < f.rows;
-      const int lim = !valid ? 0
-                      : g.causal ? list_keys(list, f.n, g.block, min(f.pos + tt + 1, f.len))
-                                 : f.total;
-      const int buf = to % NO, steps = f.s1 - f.s0;
+      const int s0 = info[slot].s0, steps = info[slot].s1 - s0;
+      const int total = info[slot].total, least = info[slot].least;
+      const int lim = lims[slot * kT + r];
+      const int buf = to % NO;
       const int head = (gi ^ x) & 1;  // the stream's first step of the tile
       float m = neg_inf(), l = 0.f;
       for (int i = head; i < steps; i += 2) {
-        const int c = gi + i, st = f.s0 + i, si = c % NS;
+        const int c = gi + i, st = s0 + i, si = c % NV;
         ok = ok && warp_wait(s_full + x, (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -391,11 +398,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         if (grow) m = mx;
         const float mq = m == neg_inf() ? 0.f : m * g.qmul;
         const int end = (st + 1) * kT;
-        const bool tail = f.total < end, mixed = f.least < min(f.total, end);
+        const bool tail = total < end, mixed = least < min(total, end);
         if (tail || mixed) {
-          ok = ok && warp_wait(v_full + si, (c / NS) & 1);
+          ok = ok && warp_wait(v_full + si, (c / NV) & 1);
           if (!ok) break;
-          const int nv = min(f.total - st * kT, kT), tid = threadIdx.x & 127;
+          const int nv = min(total - st * kT, kT), tid = threadIdx.x & 127;
           for (int kb = 0; kb < KB; ++kb) {
             uint4* v = reinterpret_cast<uint4*>(sm + M::V + si * OP + kb * kPiece);
             for (int k = nv * 8 + tid; k < kT * 8; k += 128) v[k] = make_uint4(0, 0, 0, 0);
@@ -473,92 +480,124 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       }
       if (!ok) break;
       gi += steps;
-      // ---- merge the streams and write the tile; each takes half of the columns
+      if (steps > 0) {  // the row's scale and sum, for the warps that write the tile
+        const int par = to & 1;
+        if (to >= 2) ok = warp_wait(ml_empty + par, ((to >> 1) - 1) & 1);
+        if (!ok) break;
+        ml[(par * 2 + x) * kT + r] = make_float2(m * g.qmul, l);
+        ++to;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full + par);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
+    }
+  } else {
+    // ---------------------------------------------------------------- output
+    const int quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    const int th = r % p.ht, tt = r / p.ht;
+    const bool wide = wide_rows(p.out, g.D);
+    int gi = 0, ti = 0, to = 0;
+    for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
+      const int slot = ti & 1;
+      ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const TileInfo f = info[slot];
+      const bool valid = r < p.rows && tt < f.rows;
+      const int steps = f.s1 - f.s0, buf = to % NO, par = to & 1;
       const bool some = steps > 0;
-      const bool has0 = steps > 1 || (some && ((gi - 1) & 1) == 0);
-      const bool has1 = steps > 1 || (some && ((gi - 1) & 1) == 1);
+      // which streams had a step
+      const bool has0 = steps > 1 || (some && (gi & 1) == 0);
+      const bool has1 = steps > 1 || (some && (gi & 1) == 1);
+      gi += steps;
       float L = neg_inf(), w0 = 0.f, w1 = 0.f;
       if (some) {
-        const float mine = l != 0.f ? m * g.qmul + lg2(l) : neg_inf();  // base 2
-        red[x * 128 + r] = mine;
-        meet(0);
-        const float other = red[(x ^ 1) * 128 + r];
-        const float big = fmaxf(mine, other);
-        if (big != neg_inf()) L = big + lg2(ex2(mine - big) + ex2(other - big));
-        if (mine != mine || other != other) L = mine + other;  // not a number
-        // O of a stream is scaled by its own 2^-m
-        const float own = l != 0.f ? ex2(m * g.qmul - L) : 0.f;
-        red[(x ^ 1) * 128 + r] = own;  // the word that only this thread has read
-        meet(1);
-        const float their = red[x * 128 + r];
-        w0 = x == 0 ? own : their;
-        w1 = x == 0 ? their : own;
-        const int last0 = (gi - 1) & 1 ? gi - 2 : gi - 1, last1 = (gi - 1) & 1 ? gi - 1 : gi - 2;
-        if (has0) ok = ok && warp_wait(pv_done, (last0 >> 1) & 1);
-        if (has1) ok = ok && warp_wait(pv_done + 1, (last1 >> 1) & 1);
+        ok = warp_wait(ml_full + par, (to >> 1) & 1);
+        if (!ok) break;
+        const float2 a = ml[par * 2 * kT + r], b = ml[(par * 2 + 1) * kT + r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_empty + par);
+        // log2-sum-exp of both; O of a stream is scaled by its own 2^-m
+        const float La = a.y != 0.f ? a.x + lg2(a.y) : neg_inf();
+        const float Lb = b.y != 0.f ? b.x + lg2(b.y) : neg_inf();
+        const float big = fmaxf(La, Lb);
+        if (big != neg_inf()) L = big + lg2(ex2(La - big) + ex2(Lb - big));
+        if (La != La || Lb != Lb) L = La + Lb;  // not a number
+        if (a.y != 0.f) w0 = ex2(a.x - L);
+        if (b.y != 0.f) w1 = ex2(b.x - L);
+        ok = warp_wait(o_full + buf, (to / NO) & 1);
         if (!ok) break;
         tc_fence_after();
+        ++to;
       }
       const bool poison = some && *const_cast<volatile int*>(&info[slot].poison);
       const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
-#pragma unroll 1
-      for (int c = 0; c < DP / 64; ++c) {
-        const int col = x * (DP / 2) + c * 32;
-        float o[32];
+      uint32_t w[DP / 2];
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        const int col = c * 32;
+        float o[32], v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
         __syncwarp();
-#pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
-          if (!(s ? has1 : has0)) continue;
-          float v[32];
-          tmem_ld32(tmem + lanes + M::out_col(s, buf) + col, v);
+        if (has0) {
+          tmem_ld32(tmem + lanes + M::out_col(0, buf) + col, v);
           tmem_wait_ld();
-          const float w = s ? w1 : w0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(v[i], w, o[i]);
+          for (int i = 0; i < 32; ++i) o[i] = v[i] * w0;
+        }
+        if (has1) {
+          tmem_ld32(tmem + lanes + M::out_col(1, buf) + col, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(v[i], w1, o[i]);
         }
         if (poison && valid && (w0 != 0.f || w1 != 0.f)) {  // values that were taken out of V
+          const int* list = ids + slot * kBlkMaxTopk;
+          const int lim = lims[slot * kT + r];
           for (int k = f.s0 * kT; k < min(lim, f.s1 * kT); ++k) {
-            const __nv_bfloat16* v =
+            const __nv_bfloat16* vr =
                 p.V + (int64_t(f.kbeg + list[k / g.block] * g.block + k % g.block) * g.Hkv + f.kh) *
                           g.D;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float y = col + i < g.D ? __bfloat162float(v[col + i]) : 0.f;
+              const float y = col + i < g.D ? __bfloat162float(vr[col + i]) : 0.f;
               if (!(fabsf(y) <= 3.4e38f)) o[i] += y;
             }
           }
         }
-        if (valid && p.nsplit > 1) {
+        if (p.nsplit > 1) {
           float* d = p.part_o + (f.part * p.rows + r) * g.D + col;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (col + q * 4 < g.D)
+            if (valid && col + q * 4 < g.D)
               *reinterpret_cast<float4*>(d + q * 4) =
                   make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
-        } else if (valid) {
-          store_row(p.out + qrow * g.D, col, g.D, o, wide);
         }
+        pack_row(o, w + c * 16);
       }
-      if (valid && x == 0) {
-        if (p.nsplit > 1) p.part_l[f.part * p.rows + r] = L;
-        else p.lse[qrow] = L * kLn2;
-      }
+      // the buffer is free before the row is written
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (some) mbar_arrive(o_empty + buf);
-        mbar_arrive(tile_empty + slot);
+      if (lane == 0 && some) mbar_arrive(o_empty + buf);
+      if (valid && p.nsplit == 1) {
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c)
+          store_packed(p.out + qrow * g.D, c * 32, g.D, w + c * 16, wide);
+        p.lse[qrow] = L * kLn2;
+      } else if (valid) {
+        p.part_l[f.part * p.rows + r] = L;
       }
-      to += some;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
     }
   }
   if (!ok) atomicOr(&g_err, 2);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kSoftWarps) tmem_free512(tmem);
+  if (warp == kMma) tmem_free512(tmem);
 }
 
 namespace {
