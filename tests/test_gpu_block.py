@@ -143,6 +143,7 @@ def test_many_units_of_one_block(dtype):
 
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("dtype,H,Hkv,D", [("bf16", 8, 8, 64), ("bf16", 16, 4, 128),
+                                           ("bf16", 8, 2, 64), ("bf16", 16, 2, 32),
                                            ("f32", 4, 4, 32)])
 def test_many_tiles(dtype, H, Hkv, D, causal):
     """Ten tiles and more per CTA, with empty sequences between: buffers are used in turn; the
