@@ -8,9 +8,10 @@
 //   p = 2^(s - m) as bf16           -> TMEM, over the scores it came from
 //   O += P V   (128 x D x 128)      -> TMEM, P as the left operand
 // A softmax step is a chain of latencies (TMEM, maximum, exponentials, TMEM)
-// two to three times as long as the step's products, so two streams share the
-// work, each with its own 128 threads (thread = row), score buffer, running
-// maximum and sum, and output.  Where a key head's queries fill two tiles or
+// longer than the step's products, so two streams share the work, each with its
+// own 256 threads (thread = row and half of its 128 columns; the halves exchange
+// their maxima in shared memory), score buffer, running maximum and sum, and
+// output.  Where a key head's queries fill two tiles or
 // more (PAIR), the streams are two tiles of the same unit on the same steps, and
 // every K and V that is fetched serves both: at D = 128 a tile alone asks for
 // 64 KB a step, 18 TB/s of L2 at the tensor cores' rate, about twice what L2
@@ -19,9 +20,9 @@
 // P V and next scores.  P in TMEM instead of shared memory takes 64 KB of the
 // step's 160 KB of shared-memory traffic away (128 bytes a clock would
 // otherwise be the bound at D = 128) and leaves room for a third stage.
-// Roles: warps 0-7 softmax, warps 8-11 merge a finished tile's streams and write
-// it while the softmax is at the next one, warp 12 issues the products, warp 13
-// issues TMA, warp 14 resolves the next tile's block list meanwhile (a chain of
+// Roles: warps 0-15 softmax, warps 16-19 merge a finished tile's streams and write
+// it while the softmax is at the next one, warp 20 issues the products, warp 21
+// issues TMA, warp 22 resolves the next tile's block list meanwhile (a chain of
 // dependent loads of two microseconds); every hand-over is an mbarrier, every
 // wait is bounded.
 //
@@ -52,7 +53,7 @@ __device__ int g_err;  // a bounded wait gave up
 
 constexpr int kT = kBlkTile;
 constexpr int kPiece = kT * 128;       // 128 rows x 64 bf16 columns
-constexpr int kSoftWarps = 8;           // two streams of four
+constexpr int kSoftWarps = 16;          // two streams of eight
 constexpr int kOutWarps = 4;
 constexpr int kMma = kSoftWarps + kOutWarps, kCopy = kMma + 1, kLists = kMma + 2;
 constexpr int kThr = (kLists + 1) * 32;
@@ -96,12 +97,13 @@ struct Sm {
   static constexpr int Q = 0;
   static constexpr int K = Q + NQ * QT * OP;
   static constexpr int V = K + NS * OP;
-  static constexpr int ML = V + NV * OP;         // [2 tiles][2 streams][128] (m, l)
-  static constexpr int LIM = ML + 4096;          // [2 tiles][128] keys that a row sees
+  static constexpr int ML = V + NV * OP;         // [2 tiles][2 streams][2 halves][128] (m, l)
+  static constexpr int RED = ML + 8192;          // [2 streams][2 halves][128] maxima
+  static constexpr int LIM = RED + 2048;         // [2 tiles][128] keys that a row sees
   static constexpr int IDS = LIM + 2 * kT * 2;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(TileInfo));
-  static constexpr int NBAR = 4 + 2 * NQ + 2 * NS + 2 * NV + 6 + 2 * NO + 4;
+  static constexpr int NBAR = 4 + 2 * NQ + 2 * NS + 2 * NV + 6 + 3 * NO + 4 + 8;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -124,12 +126,14 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
            *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
            *v_full = k_empty + NS, *v_empty = v_full + NV, *s_full = v_empty + NV,
            *p_full = s_full + 2, *pv_done = p_full + 2, *o_full = pv_done + 2,
-           *o_empty = o_full + NO, *ml_full = o_empty + NO, *ml_empty = ml_full + 2;
+           *o_empty = o_full + NO, *ml_full = o_empty + 2 * NO, *ml_empty = ml_full + 2,
+           *pair = ml_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   TileInfo* info = reinterpret_cast<TileInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
   int16_t* lims = reinterpret_cast<int16_t*>(sm + M::LIM);
   float2* ml = reinterpret_cast<float2*>(sm + M::ML);
+  float* red = reinterpret_cast<float*>(sm + M::RED);
   const BlockGeom& g = p.g;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -145,8 +149,10 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     }
     for (int i = 0; i < NO; ++i) {
       mbar_init(o_full + i, 1);
-      mbar_init(o_empty + i, kOutWarps);
+      mbar_init(o_empty + 2 * i, kOutWarps);  // PAIR: by stream
+      mbar_init(o_empty + 2 * i + 1, kOutWarps);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(pair + i, 2);
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
@@ -294,11 +300,13 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       const int tile = x ? due_tile[1] : due_tile[0];
       const int i = x ? due_i[1] : due_i[0], buf = tile % NO;
       ok = ok && warp_wait(p_full + x, (done >> 1) & 1) && warp_wait(v_full + si, (kv / NV) & 1);
-      if (i == 0 && tile >= NO) ok = ok && warp_wait(o_empty + buf, (tile / NO - 1) & 1);
+      // the stream's first step of the tile overwrites its output
+      if (i < 2 && tile >= NO)
+        ok = ok && warp_wait(o_empty + 2 * buf + (PAIR ? x : 0), (tile / NO - 1) & 1);
       if (!ok) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tm<kT>(tm + M::out_col(x, buf), tm + x * kT, 64, 64, desc_at(dV, si * OP), IDESC_O,
+        mma_tm<kT>(tm + M::out_col(x, buf), tm + x * kT, 32, 32, desc_at(dV, si * OP), IDESC_O,
                    i >= 2);
         mma_commit(pv_done + x);
         if (!PAIR || x) mma_commit(v_empty + si);
@@ -358,10 +366,10 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     }
   } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
-    const int quad = warp & 3, x = warp >> 2;  // TMEM lane quarter, stream
+    const int quad = warp & 3, half = (warp >> 2) & 1, x = warp >> 3;  // lanes, columns, stream
     const int r = quad * 32 + lane;
     const uint32_t lanes = uint32_t(quad * 32) << 16;
-    const uint32_t tS = tmem + lanes + x * kT;
+    const uint32_t tS = tmem + lanes + x * kT + half * 64;
     int gi = 0, ti = 0, to = 0;  // steps, tiles, tiles with steps
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
@@ -378,29 +386,36 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         ok = ok && warp_wait(s_full + x, (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        const int mine = lim - st * kT;  // columns of the step that the row sees
-        const bool cut = __any_sync(0xffffffffu, mine < kT);
-        // the maximum over columns [0, 64), then [64, 128), which stay in registers
-        float sv[64];
+        const int mine = lim - st * kT - half * 64;  // of these 64 columns the row sees
+        const bool cut = __any_sync(0xffffffffu, mine < 64);
+        // the maximum over columns [0, 32), then [32, 64), which stay in registers
+        float sv[32];
         float c0 = neg_inf(), c1 = c0, c2 = c0, c3 = c0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          tmem_ld32(tS + h * 64, sv);
-          tmem_ld32(tS + h * 64 + 32, sv + 32);
+          tmem_ld32(tS + h * 32, sv);
           tmem_wait_ld();
           if (cut) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sv[j] = j < mine - h * 64 ? sv[j] : neg_inf();
+            for (int j = 0; j < 32; ++j) sv[j] = j < mine - h * 32 ? sv[j] : neg_inf();
           }
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             c0 = fmaxf(c0, sv[j]);
             c1 = fmaxf(c1, sv[j + 1]);
             c2 = fmaxf(c2, sv[j + 2]);
             c3 = fmaxf(c3, sv[j + 3]);
           }
         }
-        const float mx = fmaxf(m, fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)));
+        const float cm = fmaxf(fmaxf(c0, c1), fmaxf(c2, c3));
+        red[(x * 2 + half) * kT + r] = cm;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair + x * 4 + quad);
+        ok = warp_wait(pair + x * 4 + quad, (c >> 1) & 1);
+        if (!ok) break;
+        // (the word is written again in the stream's next step, whose scores
+        // wait for the P of every warp that reads it here)
+        const float mx = fmaxf(m, fmaxf(cm, red[(x * 2 + (half ^ 1)) * kT + r]));
         // keep the old scale while p stays below 2^8
         const bool grow = !((mx - m) * g.qmul <= 8.f) && mx != m;
         const float old = m;
@@ -410,53 +425,51 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         const bool tail = total < end, mixed = least < min(total, end);
         if ((tail || mixed) && (!PAIR || x == 0)) {  // (the other stream's P V comes after this one's)
           const int kv = PAIR ? c >> 1 : c, si = kv % NV;
-          ok = ok && warp_wait(v_full + si, (kv / NV) & 1);
+          ok = warp_wait(v_full + si, (kv / NV) & 1);
           if (!ok) break;
-          const int nv = min(total - st * kT, kT), tid = threadIdx.x & 127;
+          const int nv = min(total - st * kT, kT), tid = threadIdx.x & 255;
           for (int kb = 0; kb < KB; ++kb) {
             uint4* v = reinterpret_cast<uint4*>(sm + M::V + si * OP + kb * kPiece);
-            for (int k = nv * 8 + tid; k < kT * 8; k += 128) v[k] = make_uint4(0, 0, 0, 0);
-            if (mixed)
-              for (int k = tid; k < nv * 8; k += 128) {
-                const uint4 y = v[k];
-                uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                bool hit = false;
+            for (int k = nv * 8 + tid; k < kT * 8; k += 256) v[k] = make_uint4(0, 0, 0, 0);
+            if (!mixed) continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((w[e] & 0x7f80u) == 0x7f80u) {
-                    w[e] &= 0xffff0000u;
-                    hit = true;
-                  }
-                  if ((w[e] & 0x7f800000u) == 0x7f800000u) {
-                    w[e] &= 0xffffu;
-                    hit = true;
-                  }
-                }
-                if (hit) {
-                  v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                  *const_cast<volatile int*>(&info[slot].poison) = 1;
-                }
+            for (int e = 0; e < kT * 8 / 256; ++e) {
+              const int k = e * 256 + tid;
+              if (k >= nv * 8) break;
+              const uint4 y = v[k];
+              const uint32_t big =
+                  __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                           __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+              if ((big & 0xffffu) < 0x7f80u && big < 0x7f800000u) continue;  // all finite
+              uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                if ((w[z] & 0x7f80u) == 0x7f80u) w[z] &= 0xffff0000u;
+                if ((w[z] & 0x7f800000u) == 0x7f800000u) w[z] &= 0xffffu;
               }
+              v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              *const_cast<volatile int*>(&info[slot].poison) = 1;
+            }
           }
           fence_proxy_async();  // -> visible to the tensor cores
           __syncwarp();
         }
         if (i > head && __any_sync(0xffffffffu, grow)) {
           // O holds the stream's steps before this one at the old scale
-          ok = ok && warp_wait(pv_done + x, ((c >> 1) - 1) & 1);
+          ok = warp_wait(pv_done + x, ((c >> 1) - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const float corr = grow ? ex2((old - m) * g.qmul) : 1.f;  // 0 from -inf
           l *= corr;
-          const uint32_t tO = tmem + lanes + M::out_col(x, buf);
+          const uint32_t tO = tmem + lanes + M::out_col(x, buf) + half * (DP / 2);
 #pragma unroll 1
           for (int k = 0; k < DP / 32; ++k) {
-            float o[32];
-            tmem_ld32(tO + k * 32, o);
+            float o[16];
+            tmem_ld16(tO + k * 16, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] *= corr;
-            tmem_st32(tO + k * 32, o);
+            for (int j = 0; j < 16; ++j) o[j] *= corr;
+            tmem_st16(tO + k * 16, o);
           }
         }
         float2 sum = make_float2(0.f, 0.f);
@@ -465,22 +478,21 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         for (int h = 1; h >= 0; --h) {
           if (h == 0) {
             tmem_ld32(tS, sv);
-            tmem_ld32(tS + 32, sv + 32);
             tmem_wait_ld();
             if (cut) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) sv[j] = j < mine ? sv[j] : neg_inf();
+              for (int j = 0; j < 32; ++j) sv[j] = j < mine ? sv[j] : neg_inf();
             }
           }
-          float w[32];
+          float w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < 16; ++j) {
             const float2 z = f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, nm);
             const float2 y = make_float2(ex2(z.x), ex2(z.y));
             sum = f2add(sum, y);
             w[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
           }
-          tmem_st32(tS + h * 64, w);
+          tmem_st16(tS + h * 32, w);
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -494,7 +506,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         const int par = to & 1;
         if (to >= 2) ok = warp_wait(ml_empty + par, ((to >> 1) - 1) & 1);
         if (!ok) break;
-        ml[(par * 2 + x) * kT + r] = make_float2(m * g.qmul, l);
+        ml[((par * 2 + x) * 2 + half) * kT + r] = make_float2(m * g.qmul, l);
         ++to;
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full + par);
@@ -525,7 +537,9 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       if (some) {
         ok = warp_wait(ml_full + par, (to >> 1) & 1);
         if (!ok) break;
-        const float2 a = ml[par * 2 * kT + r], b = ml[(par * 2 + 1) * kT + r];
+        float2 a = ml[par * 4 * kT + r], b = ml[(par * 4 + 2) * kT + r];
+        a.y += ml[(par * 4 + 1) * kT + r].y;  // the halves of a row share m
+        b.y += ml[(par * 4 + 3) * kT + r].y;
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_empty + par);
         // log2-sum-exp; O of a stream is scaled by its own 2^-m
@@ -550,7 +564,6 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       for (int x = 0; x < QT; ++x) {  // the tiles of this unit (one, of both streams)
         const float L = x ? Lb : La;
         const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + x * p.ht + th;
-        uint32_t w[DP / 2];
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
           const int col = c * 32;
@@ -594,20 +607,16 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
                 *reinterpret_cast<float4*>(d + q * 4) =
                     make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
           }
-          pack_row(o, w + c * 16);
+          if (c == DP / 32 - 1) {  // the buffer is free before the row's end is written
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && some) mbar_arrive(o_empty + 2 * buf + x);
+          }
+          if (valid && (PAIR || p.nsplit == 1))
+            store_row(p.out + qrow * g.D, col, g.D, o, wide);
         }
-        // the buffer is free before the row is written
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && some && x == QT - 1) mbar_arrive(o_empty + buf);
-        if (valid && (PAIR || p.nsplit == 1)) {
-#pragma unroll
-          for (int c = 0; c < DP / 32; ++c)
-            store_packed(p.out + qrow * g.D, c * 32, g.D, w + c * 16, wide);
-          p.lse[qrow] = L * kLn2;
-        } else if (valid) {
-          p.part_l[f.part * p.rows + r] = L;
-        }
+        if (valid && (PAIR || p.nsplit == 1)) p.lse[qrow] = L * kLn2;
+        else if (valid) p.part_l[f.part * p.rows + r] = L;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(tile_empty + slot);
@@ -670,7 +679,7 @@ Shape shape(const BlockGeom& g) {
   s.tiles = int64_t(g.U) * g.Hkv * s.hs;
   s.nsplit = 1;
   // Two tiles of one unit at a time where there are two, and pairs enough for
-  // every SM (prompt of 32,768, 4 heads of 128 a key head: 0.89 -> 0.70 ms)
+  // every SM (prompt of 32,768, 4 heads of 128 a key head: 0.89 -> 0.81 ms)
   s.pair = s.hs > 1 && s.tiles / 2 >= sm_count();
   if (s.pair) {
     s.hs /= 2;
