@@ -22,9 +22,9 @@
 //     p, ds as bf16                                    -> TMEM, over S^T and dP^T
 //     dV += p dO, dK += ds Q                           -> TMEM
 //   64 rather than 128 queries a step leave room for several stages of Q and
-//   dO and a second score buffer next to the two accumulators; two groups of
-//   eight warps take the steps in turn, so that one forms p and ds while the
-//   other waits for its products.  Units
+//   dO and a second and, at D <= 64, third score buffer next to the two
+//   accumulators; as many groups of eight warps take the steps in turn, so that
+//   one forms p and ds while another waits for its products.  Units
 //   of fewer than 64 pairs share a step, each in a box of its own; a box
 //   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
 //   its mask within a box is a range of columns.
@@ -33,6 +33,7 @@
 // behind the list's end, queries behind a unit's end) are zeroed in shared
 // memory, because 0 * NaN is NaN there.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_launch.cuh"
 #include "attn_pipe.cuh"
@@ -413,8 +414,6 @@ namespace {
 
 constexpr int kNR = 64;               // query pairs per step
 constexpr int kQPiece = kNR * 128;    // 64 rows x 64 bf16 columns
-constexpr int kKvWarps = 16;          // two groups of eight, steps in turn
-constexpr int kKvThr = (kKvWarps + 3) * 32;
 constexpr int kList = 256;            // units resolved at a time (8 bitmap words)
 
 struct DkvParams {
@@ -423,7 +422,7 @@ struct DkvParams {
   int bh, bt;      // heads and query rows of a box
   int br, boxes;   // pairs of a box, boxes of a step
   int ub;          // boxes of a unit
-  int l_bh, l_hn, l_qb;  // log2 of bh, of a unit's head groups, of q_block
+  int l_bh, l_br, l_hn, l_qb;  // log2 of bh, br, of a unit's head groups, of q_block
 };
 
 struct Box {
@@ -443,7 +442,10 @@ struct KvInfo {
 template <int DP>
 struct KvSm {
   static constexpr int KB = DP / 64;
+  static constexpr int NG = DP == 64 ? 3 : 2;  // groups of eight warps, score buffers
+  static constexpr int WARPS = NG * 8, THR = (WARPS + 4) * 32;
   static constexpr int NS = DP == 64 ? 6 : 4;  // Q and dO stages
+  static_assert(NS % NG == 0, "a stage belongs to one group, which waits for each of its phases");
   static constexpr int OP = KB * kPiece, QP = KB * kQPiece;
   static constexpr int K = 0;
   static constexpr int V = OP;
@@ -454,11 +456,13 @@ struct KvSm {
   static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
   static constexpr int INFO = LIST + kList * 8;
   static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
-  static constexpr int NBAR = 4 + 2 + 3 * NS + 2 + 2 + 2;
+  static constexpr int NBAR = 4 + 2 + 3 * NS + 2 * NG + 2;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
-  // TMEM: S^T [0, 128) and dP^T [128, 256) in two buffers, dV, dK from 256 on
+  // TMEM: S^T and dP^T of the groups, dV, dK
+  static constexpr int T_DP = NG * kNR, T_ACC = 2 * T_DP;
+  static_assert(T_ACC + 2 * DP <= 512, "TMEM columns");
 };
 
 // arrive once this thread's cp.async copies so far have landed
@@ -470,17 +474,17 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }  // namespace
 
 template <int DP>
-__global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
+__global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
   using namespace tc;
   using M = KvSm<DP>;
-  constexpr int KB = M::KB, NS = M::NS, QP = M::QP;
+  constexpr int KB = M::KB, NS = M::NS, NG = M::NG, QP = M::QP, kKvWarps = M::WARPS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
            *kv_empty = kv_full + 1, *q_full = kv_empty + 1, *q_empty = q_full + NS,
-           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + 2,
-           *g_full = p_full + 2, *g_empty = g_full + 1;
+           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + NG,
+           *g_full = p_full + NG, *g_empty = g_full + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
   int2* list = reinterpret_cast<int2*>(sm + M::LIST);
@@ -490,9 +494,11 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, kKvWarps + 2);
+      mbar_init(item_empty + i, kKvWarps + 3);
+    }
+    for (int i = 0; i < NG; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, kKvWarps / 2);
+      mbar_init(p_full + i, 8);
     }
     mbar_init(g_full, 1);
     mbar_init(kv_full, 1);
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       mbar_init(q_empty + i, 1);
       mbar_init(box_full + i, 1);
     }
-    mbar_init(g_empty, kKvWarps);
+    mbar_init(g_empty, 16);
     mbar_init_fence();
   }
   if (warp == kKvWarps) tmem_alloc512(s_tmem);
@@ -616,12 +622,38 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
             }
           }
           if (lane == 0) box[j] = x;
-          for (int i = lane; i < x.rows; i += 32)
-            cp_async8(sm + M::STAT + (si * kNR + j * p.br + i) * 8,
+        }
+        if (lane == 0) mbar_arrive(box_full + si);
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+  } else if (warp == kKvWarps + 3) {
+    // ---------------------------------------------------------------- statistics
+    // (a warp of its own: with the lists' chain of dependent work in one warp,
+    // the two took 1,430 clocks a step, more than everything else)
+    int gi = 0;
+    for (int ti = 0;; ++ti) {
+      const int slot = ti & 1;
+      ok = warp_wait(item_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const int item = info[slot].item, steps = info[slot].steps;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + slot);
+      if (item < 0) break;
+      for (int st = 0; st < steps && ok; ++st, ++gi) {
+        const int si = gi % NS;
+        ok = warp_wait(box_full + si, (gi / NS) & 1);
+        if (!ok) break;
+        const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
+#pragma unroll
+        for (int e = 0; e < kNR / 32; ++e) {
+          const int c = e * 32 + lane, j = c >> p.l_br, i = c & (p.br - 1);
+          const Box& x = box[j];
+          if (i < x.rows)
+            cp_async8(sm + M::STAT + (si * kNR + c) * 8,
                       p.b.stat + int64_t(x.row + (i >> p.l_bh)) * g.H + x.h0 + (i & (p.bh - 1)));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(box_full + si);
         cp_async_arrive(q_full + si);
       }
       if (!ok) break;
@@ -653,8 +685,12 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         if (!ok) break;
         const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
         int full = 0;  // boxes with pairs: all of them but at an item's end
-        for (int j = lane; j < p.boxes; j += 32) full += box[j].rows > 0;
-        full = p.boxes == 1 ? uniform(full) : __reduce_add_sync(0xffffffffu, full);
+        if (p.boxes == 1) {
+          full = box[0].rows > 0;
+        } else {
+          for (int j = lane; j < p.boxes; j += 32) full += box[j].rows > 0;
+          full = __reduce_add_sync(0xffffffffu, full);
+        }
         if (lane == 0) mbar_expect_tx(q_full + si, uint32_t(full * p.br) * 256 * KB);
         __syncwarp();
         for (int e = lane; e < p.boxes * 2 * KB; e += 32) {
@@ -679,29 +715,32 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
                    dO = desc_k(sm + M::O), dQm = desc_mn(sm + M::Q, kQPiece),
                    dOm = desc_mn(sm + M::O, kQPiece);
     const uint32_t tm = uniform(tmem);
-    // Step gi's scores overwrite p and ds of step gi - 2, whose products were
+    // Step gi's scores overwrite p and ds of step gi - NG, whose products were
     // issued before them and run in that order.
-    int gi = 0, tk = 0, done = 0;
-    int due_item[2] = {0, 0}, due_i[2] = {0, 0};
-    bool due_last[2] = {false, false};
-    auto product_g = [&]() {  // of step `done`
-      const int x = done & 1, si = done % NS;
-      const int item = x ? due_item[1] : due_item[0], i = x ? due_i[1] : due_i[0];
-      ok = ok && warp_wait(p_full + x, (done >> 1) & 1);
-      if (i == 0 && item >= 1) ok = ok && warp_wait(g_empty, (item - 1) & 1);
+    int gi = 0, tk = 0;                 // steps with scores, items
+    int done = 0, item = 0, i_done = 0;  // steps with all products, items, steps of this item
+    uint32_t ends = 0;                  // bit gi % 32: step gi is its item's last
+    auto product_g = [&]() {            // of step `done`
+      const int x = done % NG, si = done % NS;
+      const bool last = (ends >> (done & 31)) & 1u;
+      ok = ok && warp_wait(p_full + x, (done / NG) & 1);
+      if (i_done == 0 && item >= 1) ok = ok && warp_wait(g_empty, (item - 1) & 1);
       if (!ok) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tm<kNR>(tm + 256, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
-        mma_tm<kNR>(tm + 256 + DP, tm + 128 + x * kNR, 16, 16, desc_at(dQm, si * QP), IDESC_G,
-                    i > 0);
+        mma_tm<kNR>(tm + M::T_ACC, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G,
+                    i_done > 0);
+        mma_tm<kNR>(tm + M::T_ACC + DP, tm + M::T_DP + x * kNR, 16, 16, desc_at(dQm, si * QP),
+                    IDESC_G, i_done > 0);
         mma_commit(q_empty + si);
         // (a barrier of its own: a group that has no part in the last steps
         // would otherwise wait for a phase two ahead, which reads as complete)
-        if (x ? due_last[1] : due_last[0]) mma_commit(g_full);
+        if (last) mma_commit(g_full);
       }
       __syncwarp();
       ++done;
+      i_done = last ? 0 : i_done + 1;
+      item += last;
     };
     for (int ti = 0; ok; ++ti) {
       const int slot = ti & 1;
@@ -717,27 +756,19 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       if (n <= 0) continue;
       ok = warp_wait(kv_full, tk & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
-        const int si = gi % NS, x = gi & 1;
-        if (gi - done == 2) product_g();
+        const int si = gi % NS, x = gi % NG;
+        if (gi - done == NG) product_g();
         ok = ok && warp_wait(q_full + si, (gi / NS) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           mma_kk<KB>(tm + x * kNR, dK, kPiece, desc_at(dQ, si * QP), kQPiece, IDESC_S);
-          mma_kk<KB>(tm + 128 + x * kNR, dV, kPiece, desc_at(dO, si * QP), kQPiece, IDESC_S);
+          mma_kk<KB>(tm + M::T_DP + x * kNR, dV, kPiece, desc_at(dO, si * QP), kQPiece, IDESC_S);
           mma_commit(s_full + x);
           if (i == n - 1) mma_commit(kv_empty);
         }
         __syncwarp();
-        if (x) {
-          due_item[1] = tk;
-          due_i[1] = i;
-          due_last[1] = i == n - 1;
-        } else {
-          due_item[0] = tk;
-          due_i[0] = i;
-          due_last[0] = i == n - 1;
-        }
+        ends = (ends & ~(1u << (gi & 31))) | (uint32_t(i == n - 1) << (gi & 31));
       }
       ++tk;
     }
@@ -745,8 +776,8 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     // every product has completed before TMEM is given up
     if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
     if (!ok) {
-      for (int c = gi; c >= 0 && c > gi - 3; --c) {
-        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+      for (int c = gi; c >= 0 && c > gi - NG - 1; --c) {
+        warp_wait(s_full + c % NG, (c / NG) & 1, 200);
         warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
       }
     }
@@ -756,7 +787,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     const int x = warp >> 3;                                       // group
     const int tid = threadIdx.x & 255;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + 128;
+    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + M::T_DP;
     const int blk = r / g.block;
     const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
     int gi = 0, to = 0;  // steps, items with steps
@@ -768,12 +799,11 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       if (f.item < 0) break;
       const int pos = f.pos + r;
       const bool valid = r < f.n;
-      for (int i = (gi ^ x) & 1; i < f.steps; i += 2) {
+      for (int i = (x + NG - gi % NG) % NG; i < f.steps; i += NG) {
         const int c = gi + i, si = c % NS;
-        ok = ok && warp_wait(s_full + x, (c >> 1) & 1);
-        ok = ok && warp_wait(q_full + si, (c / NS) & 1);  // the statistics and boxes
+        // what the statistics and boxes say, while the scores are on their way
+        ok = ok && warp_wait(q_full + si, (c / NS) & 1);
         if (!ok) break;
-        tc_fence_after();
         const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
         // this key's columns of the step; pairs that do not exist: zeros in Q and dO
         uint32_t see = 0;
@@ -800,36 +830,53 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
           }
           fence_proxy_async();
         }
+        ok = warp_wait(s_full + x, (c / NG) & 1);
+        if (!ok) break;
+        tc_fence_after();
         const float4* stat =
             reinterpret_cast<const float4*>(sm + M::STAT + (si * kNR + part * 32) * 8);
-        const bool full = __all_sync(0xffffffffu, see == 0xffffffffu);
         const float2 qm = f2s(g.qmul);
+        auto form = [&](auto all) {  // all: the warp's keys see every column
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 16 columns
-          float sv[16], dv[16], wp[8], wd[8];
-          tmem_ld16(tS + h * 16, sv);
-          tmem_ld16(tP + h * 16, dv);
-          tmem_wait_ld();
+          for (int h = 0; h < 2; ++h) {  // 16 columns
+            float sv[16], dv[16], wp[8], wd[8];
+            tmem_ld16(tS + h * 16, sv);
+            tmem_ld16(tP + h * 16, dv);
+            tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 a = stat[h * 8 + j];  // (lse, Delta) of columns 2 j, 2 j + 1
-            const float2 z =
-                f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, make_float2(-a.x, -a.z));
-            float2 y = make_float2(ex2(z.x), ex2(z.y));
-            float2 ds =
-                f2mul(y, f2add(make_float2(dv[2 * j], dv[2 * j + 1]), make_float2(-a.y, -a.w)));
-            if (!full) {
-              const bool s0 = (see >> (h * 16 + 2 * j)) & 1u, s1 = (see >> (h * 16 + 2 * j + 1)) & 1u;
-              y.x = s0 ? y.x : 0.f;
-              y.y = s1 ? y.y : 0.f;
-              ds.x = s0 ? ds.x : 0.f;
-              ds.y = s1 ? ds.y : 0.f;
+            for (int j = 0; j < 8; ++j) {
+              const float4 a = stat[h * 8 + j];  // (lse, Delta) of columns 2 j, 2 j + 1
+              const float2 z =
+                  f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, make_float2(-a.x, -a.z));
+              float2 y = make_float2(ex2(z.x), ex2(z.y));
+              float2 ds =
+                  f2mul(y, f2add(make_float2(dv[2 * j], dv[2 * j + 1]), make_float2(-a.y, -a.w)));
+              if (!decltype(all)::value) {
+                const bool s0 = (see >> (h * 16 + 2 * j)) & 1u,
+                           s1 = (see >> (h * 16 + 2 * j + 1)) & 1u;
+                y.x = s0 ? y.x : 0.f;
+                y.y = s1 ? y.y : 0.f;
+                ds.x = s0 ? ds.x : 0.f;
+                ds.y = s1 ? ds.y : 0.f;
+              }
+              wp[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
+              wd[j] = __uint_as_float(bf16x2_bits(ds.x, ds.y));
             }
-            wp[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
-            wd[j] = __uint_as_float(bf16x2_bits(ds.x, ds.y));
+            tmem_st8(tS + h * 16, wp);
+            tmem_st8(tP + h * 16, wd);
           }
-          tmem_st8(tS + h * 16, wp);
-          tmem_st8(tP + h * 16, wd);
+        };
+        if (__all_sync(0xffffffffu, see == 0xffffffffu)) {
+          form(std::true_type{});
+        } else if (__any_sync(0xffffffffu, see)) {
+          form(std::false_type{});
+        } else {  // keys of a block that the unit did not choose
+          const float none[8] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_st8(tS + h * 16, none);
+            tmem_st8(tP + h * 16, none);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -838,6 +885,11 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       }
       if (!ok) break;
       gi += f.steps;
+      if (x >= 2) {  // the third group writes nothing and waits for no result
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + slot);
+        continue;
+      }
       const bool some = f.steps > 0;
       if (some) {
         ok = warp_wait(g_full, to & 1);
@@ -852,7 +904,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         float o[32];
         __syncwarp();
         if (some) {
-          tmem_ld32(tmem + lanes + 256 + x * DP + col, o);
+          tmem_ld32(tmem + lanes + M::T_ACC + x * DP + col, o);
           tmem_wait_ld();
         }
         if (valid && f.slot < 0) {
@@ -931,6 +983,7 @@ gattn_status launch_block_bwd_tc(const BlockBwdParams& b, cudaStream_t st) {
     p.ub = (g.qb / p.bt) * (g.G / p.bh);
     const auto log2i = [](int x) { return 31 - __builtin_clz(x); };
     p.l_bh = log2i(p.bh);
+    p.l_br = log2i(p.br);
     p.l_hn = log2i(g.G / p.bh);
     p.l_qb = log2i(g.qb);
     if (!encode_heads_map(&p.mq, Q, g.Nq, g.H, g.D, p.bh, p.bt) ||
@@ -939,8 +992,8 @@ gattn_status launch_block_bwd_tc(const BlockBwdParams& b, cudaStream_t st) {
         !encode_heads_map(&p.mv, V, g.Nk, g.Hkv, g.D, 1, kT))
       return GATTN_ERR_CUDA;
     const unsigned grid = unsigned(std::min<int64_t>(b.max_items, sm_count()));
-    s = g.D <= 64 ? go(block_dkv_tc<64>, grid, kKvThr, KvSm<64>::BYTES, p)
-                  : go(block_dkv_tc<128>, grid, kKvThr, KvSm<128>::BYTES, p);
+    s = g.D <= 64 ? go(block_dkv_tc<64>, grid, KvSm<64>::THR, KvSm<64>::BYTES, p)
+                  : go(block_dkv_tc<128>, grid, KvSm<128>::THR, KvSm<128>::BYTES, p);
   }
   return s;
 }
