@@ -183,10 +183,10 @@ struct BlockBwdParams {
 };
 
 int sm_count();
-gattn_status launch_block_fwd_simt(const BlockGeom& g, gattn_dtype dt, const void* Q,
-                                   const void* K, const void* V, const int32_t* idx, void* out,
-                                   float* lse, cudaStream_t st);
-gattn_status launch_block_bwd_simt(const BlockBwdParams& p, gattn_dtype dt, cudaStream_t st);
+gattn_status launch_block_fwd_simt(const BlockGeom& g, const float* Q, const float* K,
+                                   const float* V, const int32_t* idx, float* out, float* lse,
+                                   cudaStream_t st);
+gattn_status launch_block_bwd_simt(const BlockBwdParams& p, cudaStream_t st);
 gattn_status launch_block_sums(const BlockGeom& g, gattn_dtype dt, const void* x, bool queries,
                                const int32_t* since, double* sums, cudaStream_t st);
 gattn_status launch_block_select(const BlockGeom& g, gattn_dtype dt, const void* Q,

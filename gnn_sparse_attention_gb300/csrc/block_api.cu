@@ -283,37 +283,50 @@ __global__ void __launch_bounds__(1024) items_kernel(const BlockBwdParams p, int
   }
 }
 
-// dK, dV of a key tile with several items: the sum of their partials
+// dK, dV of the key tiles with several items: the sums of their partials.
+// Most tiles have one, so a warp looks at 32 of a CTA's tiles at a time (a CTA
+// for each tile took 37 us at 64k nodes).  A tile that most units chose may have a
+// hundred partials: its elements are spread over gridDim.y CTAs.
 template <class T>
 __global__ void __launch_bounds__(256) join_kv_kernel(const BlockBwdParams p) {
   const BlockGeom& g = p.g;
-  const int i = blockIdx.x, c = p.cnt[2 * i];
-  if (c <= p.chunk) return;
-  const int kt = i / g.Hkv, kh = i - kt * g.Hkv, D = g.D;
-  const int s = piece_seq(g.seq_k, g.S, kBlkTile, kt);
-  const Span ks = span_k(g, s);
-  const int pos = (kt - piece_base(g.seq_k, s, kBlkTile)) * kBlkTile;
-  const int n = (c + p.chunk - 1) / p.chunk;
-  const float* part = p.part + int64_t(p.cnt[2 * i + 1]) * 2 * kBlkTile * D;
-  for (int e = (threadIdx.x + blockIdx.y * 256) * 4; e < 2 * kBlkTile * D;
-       e += 1024 * gridDim.y) {
-    const int which = e / (kBlkTile * D), r = (e / D) % kBlkTile, d = e % D;
-    if (pos + r >= ks.len) continue;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int D = g.D, tiles = g.KT * g.Hkv, lane = threadIdx.x & 31;
+  for (int64_t base = blockIdx.x; base < tiles; base += int64_t(gridDim.x) * 32) {
+    const int64_t mine = base + int64_t(lane) * gridDim.x;
+    const int2 own = mine < tiles ? reinterpret_cast<const int2*>(p.cnt)[mine] : make_int2(0, 0);
+    for (unsigned m = __ballot_sync(0xffffffffu, own.x > p.chunk); m; m &= m - 1) {
+      const int b = __ffs(m) - 1, i = int(base + int64_t(b) * gridDim.x);
+      const int c = __shfl_sync(0xffffffffu, own.x, b);
+      const int kt = i / g.Hkv, kh = i - kt * g.Hkv;
+      const int s = piece_seq(g.seq_k, g.S, kBlkTile, kt);
+      const Span ks = span_k(g, s);
+      const int pos = (kt - piece_base(g.seq_k, s, kBlkTile)) * kBlkTile;
+      const int n = (c + p.chunk - 1) / p.chunk;
+      const float* part =
+          p.part + int64_t(__shfl_sync(0xffffffffu, own.y, b)) * 2 * kBlkTile * D;
+      for (int e = (threadIdx.x + blockIdx.y * 256) * 4; e < 2 * kBlkTile * D;
+           e += 1024 * gridDim.y) {
+        const int which = e / (kBlkTile * D), r = (e / D) % kBlkTile, d = e % D;
+        if (pos + r >= ks.len) continue;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(part + int64_t(k) * 2 * kBlkTile * D + e);
-      t.x += x.x;
-      t.y += x.y;
-      t.z += x.z;
-      t.w += x.w;
+        for (int k = 0; k < n; ++k) {
+          const float4 x =
+              *reinterpret_cast<const float4*>(part + int64_t(k) * 2 * kBlkTile * D + e);
+          t.x += x.x;
+          t.y += x.y;
+          t.z += x.z;
+          t.w += x.w;
+        }
+        const float mul = which ? 1.f : g.scale;
+        T* out =
+            static_cast<T*>(which ? p.dV : p.dK) + (int64_t(ks.beg + pos + r) * g.Hkv + kh) * D + d;
+        out[0] = T(t.x * mul);
+        out[1] = T(t.y * mul);
+        out[2] = T(t.z * mul);
+        out[3] = T(t.w * mul);
+      }
     }
-    const float mul = which ? 1.f : g.scale;
-    T* out = static_cast<T*>(which ? p.dV : p.dK) + (int64_t(ks.beg + pos + r) * g.Hkv + kh) * D + d;
-    out[0] = T(t.x * mul);
-    out[1] = T(t.y * mul);
-    out[2] = T(t.z * mul);
-    out[3] = T(t.w * mul);
   }
 }
 
@@ -420,7 +433,9 @@ gattn_status gattn_block_fwd(const gattn_block_desc* desc, const void* Q, const 
                 "idx and lse must be device pointers");
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (desc->dtype == GATTN_F32)
-    return launch_block_fwd_simt(g, GATTN_F32, Q, K, V, idx, out, lse, st);
+    return launch_block_fwd_simt(g, static_cast<const float*>(Q), static_cast<const float*>(K),
+                                 static_cast<const float*>(V), idx, static_cast<float*>(out), lse,
+                                 st);
   if ((s = check_ws("gattn_block_fwd", workspace, workspace_bytes, block_fwd_tc_workspace(g))) !=
       GATTN_OK)
     return s;
@@ -476,12 +491,10 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const gattn_dtype dt = gattn_dtype(desc->dtype);
   if ((s = bwd_prepare(p, dt, w, ws, st)) != GATTN_OK ||
-      (s = dt == GATTN_F32 ? launch_block_bwd_simt(p, dt, st) : launch_block_bwd_tc(p, st)) !=
+      (s = dt == GATTN_F32 ? launch_block_bwd_simt(p, st) : launch_block_bwd_tc(p, st)) !=
           GATTN_OK)
     return s;
-  // a key tile that most units chose may have a hundred partials: its elements
-  // are spread over several CTAs
-  const dim3 grid(g.KT * g.Hkv, std::max(1, kBlkTile * g.D * 2 / 1024));
+  const dim3 grid(std::min(g.KT * g.Hkv, 2 * sm_count()), std::max(1, kBlkTile * g.D * 2 / 1024));
   if (dt == GATTN_F32) join_kv_kernel<float><<<grid, 256, 0, st>>>(p);
   else join_kv_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
   return launched("gattn_block_bwd (join)");

@@ -1,11 +1,13 @@
 // block_simt.cu -- block attention on the CUDA cores, for fp32 tensors (the
 // tensor cores' kinds keep fewer than 24 bits of a product's operands).
 //
-// 64 x 64 score tiles in fp32: 256 threads hold 4 x 4 scores each, operands
-// are staged in shared memory as fp32, and a thread's 4 rows of the output
-// (or gradient) stay in registers.  Bound by the FMA units: a step of 64
-// rows by 64 keys is 2 (forward), 3 (dQ) or 4 (dK, dV) products of
-// 64 x 64 x D.
+// 64 x 64 score tiles: 256 threads hold 4 x 4 scores each, operands are staged
+// in shared memory by cp.async (four threads a row), and a thread's 4 rows of
+// the output (or gradient) stay in registers.  A step of 64 rows by 64 keys is
+// 2 (forward), 3 (dQ) or 4 (dK, dV) products of 64 x 64 x D on the FMA units; up
+// to D = 64 the next step's operands are fetched meanwhile.  At D <= 32 a row
+// of the last products has 8 float4, so the other 8 threads of the 16 take every
+// second group of four keys.
 //
 // With the unit's block list ascending, the keys a row may see are the first
 // columns of its steps, so the mask of a row is one number (list_keys).
@@ -23,20 +25,11 @@ constexpr int kC = 64;     // keys of a step
 constexpr int kThr = 256;
 constexpr int kPS = kC + 4;  // row stride of the score tile
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <class T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
-
 struct FwdP {
   BlockGeom g;
-  const void *Q, *K, *V;
+  const float *Q, *K, *V;
   const int32_t* idx;
-  void* out;
+  float* out;
   float* lse;
 };
 
@@ -47,15 +40,25 @@ __device__ __forceinline__ int64_t q_off(const BlockGeom& g, const Unit& u, int 
   return (int64_t(u.row + t) * g.H + kh * g.G + (r - t * g.G)) * g.D;
 }
 
-// 64 rows of D elements to shared memory (row stride D + 4); off(r) < 0: zeros
-template <class T, class F>
-__device__ __forceinline__ void stage(float* dst, const T* src, int D, F off) {
-  const int ld = D + 4;
-  for (int i = threadIdx.x; i < kR * D; i += kThr) {
-    const int r = i / D, d = i - r * D;
-    const int64_t o = off(r);
-    dst[r * ld + d] = o >= 0 ? to_f(src[o + d]) : 0.f;
-  }
+// 64 rows of D elements to shared memory (row stride D + 4), asynchronously;
+// off(r) < 0: zeros.  Returns the offset of this thread's row, threadIdx.x / 4.
+template <class F>
+__device__ __forceinline__ int64_t stage(float* dst, const float* src, int D, F off) {
+  const int r = threadIdx.x >> 2;
+  const int64_t o = off(r);
+  const float* s = src + (o >= 0 ? o : 0);
+  const uint32_t d0 = smem_u32(dst + r * (D + 4)), bytes = o >= 0 ? 16 : 0;
+  for (int d = (threadIdx.x & 3) * 4; d < D; d += 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d0 + d * 4), "l"(s + d),
+                 "r"(bytes)
+                 : "memory");
+  return o;
+}
+__device__ __forceinline__ void staged() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void landed() {  // all groups but the last N
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+  __syncthreads();
 }
 
 // s[i][j] = a[4 ty + i] . b[tx + 16 j]
@@ -80,43 +83,64 @@ __device__ __forceinline__ void dots(const float* a, const float* b, int D, floa
   }
 }
 
-// o[i][*] += sum_k w(4 ty + i, k) b[k][cols of this thread], cols 4 tx + 64 q.
+// o[i][*] += sum_k w(4 ty + i, k) b[k][cols of this thread], cols 4 tx + 64 q;
+// DQ = 0 (D <= 32): cols 4 (tx % 8), of every second four k.
 // TR: w is stored [k][row].  GUARD: a zero weight takes nothing from its row
 // of b, which may hold non-finite values that the row must not see.
 template <int DQ, bool TR, bool GUARD>
-__device__ __forceinline__ void weighted(const float* w, const float* b, int D, float o[4][DQ][4]) {
+__device__ __forceinline__ void weighted(const float* w, const float* b, int D, float (*o)[4]) {
+  constexpr int N = DQ ? DQ : 1;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, ld = D + 4;
-  for (int k = 0; k < kC; ++k) {
-    float x[4];
-    if (TR) {
-      const float4 v = *reinterpret_cast<const float4*>(w + k * kPS + ty * 4);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
+  const int c0 = (DQ ? tx : tx & 7) * 4;
+  for (int k = DQ ? 0 : (tx >> 3) * 4; k < kC; k += DQ ? 4 : 8) {
+    float x[4][4];  // [key][row]
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = w[(ty * 4 + i) * kPS + k];
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(TR ? w + (k + i) * kPS + ty * 4
+                                                           : w + (ty * 4 + i) * kPS + k);
+      if (TR) {
+        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      } else {
+        x[0][i] = v.x; x[1][i] = v.y; x[2][i] = v.z; x[3][i] = v.w;
+      }
     }
 #pragma unroll
-    for (int q = 0; q < DQ; ++q) {
-      const int c = tx * 4 + 64 * q;
-      if (c < D) {
-        const float4 v = *reinterpret_cast<const float4*>(b + k * ld + c);
+    for (int q = 0; q < N; ++q) {
+      const int c = c0 + 64 * q;
+      if (c >= D) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (k + e) * ld + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (GUARD && x[i] == 0.f) continue;
-          o[i][q][0] = fmaf(x[i], v.x, o[i][q][0]);
-          o[i][q][1] = fmaf(x[i], v.y, o[i][q][1]);
-          o[i][q][2] = fmaf(x[i], v.z, o[i][q][2]);
-          o[i][q][3] = fmaf(x[i], v.w, o[i][q][3]);
+          if (GUARD && x[e][i] == 0.f) continue;
+          float* y = o[i * N + q];
+          y[0] = fmaf(x[e][i], v.x, y[0]);
+          y[1] = fmaf(x[e][i], v.y, y[1]);
+          y[2] = fmaf(x[e][i], v.z, y[2]);
+          y[3] = fmaf(x[e][i], v.w, y[3]);
         }
       }
     }
   }
 }
 
-template <class T, int DQ>
-__device__ __forceinline__ void put4(T* p, const float* v, float mul) {
+// row i's columns of this thread, all keys together, times mul: put(column, values)
+template <int DQ, class F>
+__device__ __forceinline__ void finish(float (*o)[4], int i, int D, float mul, F put) {
+  constexpr int N = DQ ? DQ : 1;
+  const int tx = threadIdx.x & 15;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = from_f<T>(v[e] * mul);
+  for (int q = 0; q < N; ++q) {
+    float* y = o[i * N + q];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!DQ) y[e] += __shfl_xor_sync(0xffffffffu, y[e], 8);
+      y[e] *= mul;
+    }
+    const int c = (DQ ? tx : tx & 7) * 4 + 64 * q;
+    if (c < D && (DQ || tx < 8)) put(c, make_float4(y[0], y[1], y[2], y[3]));
+  }
 }
 
 // key row (element offset of K, V) of column c of the step that starts at
@@ -128,14 +152,19 @@ __device__ __forceinline__ int64_t k_off(const BlockGeom& g, const int* ids, int
   return (int64_t(kbeg + ids[k / g.block] * g.block + k % g.block) * g.Hkv + kh) * g.D;
 }
 
-template <class T, int DQ>
+// operand buffers of a step: two where they fit
+template <int DQ>
+constexpr int kBufs = DQ < 2 ? 2 : 1;
+
+template <int DQ>
 __global__ void __launch_bounds__(kThr) block_fwd_simt(const FwdP p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int ids[kBlkMaxTopk];
   __shared__ int n_ids;
   const BlockGeom& g = p.g;
   const int D = g.D, ld = D + 4, kh = blockIdx.y, u = blockIdx.x, r0 = blockIdx.z * kR;
-  float *sQ = sm, *sK = sQ + kR * ld, *sV = sK + kC * ld, *sP = sV + kC * ld;
+  constexpr int NB = kBufs<DQ>, N = DQ ? DQ : 1;
+  float *sQ = sm, *sK = sQ + kR * ld, *sV = sK + NB * kC * ld, *sP = sV + NB * kC * ld;
   const Unit un = unit_at(g, u);
   if (r0 >= un.n * g.G) return;
   const Span ks = span_k(g, un.s);
@@ -156,27 +185,31 @@ __global__ void __launch_bounds__(kThr) block_fwd_simt(const FwdP p) {
     if (t >= un.n) lim[i] = 0;
   }
   if (g.causal) lim0 = list_keys(ids, n, g.block, min(un.pos + r0 / g.G + 1, ks.len));
-  const T* K = static_cast<const T*>(p.K);
-  const T* V = static_cast<const T*>(p.V);
-  stage(sQ, static_cast<const T*>(p.Q), D, [&](int r) { return q_off(g, un, kh, r0 + r); });
-  float m[4], l[4], o[4][DQ][4];
+  const auto fetch = [&](int k0, int buf) {
+    const auto off = [&](int c) { return k_off(g, ids, total, k0, c, ks.beg, kh); };
+    stage(sK + buf * kC * ld, p.K, D, off);
+    stage(sV + buf * kC * ld, p.V, D, off);
+    staged();
+  };
+  stage(sQ, p.Q, D, [&](int r) { return q_off(g, un, kh, r0 + r); });
+  if (NB == 2) fetch(0, 0);
+  float m[4], l[4], o[4 * N][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     m[i] = neg_inf();
     l[i] = 0.f;
 #pragma unroll
-    for (int q = 0; q < DQ; ++q)
+    for (int q = 0; q < N; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][q][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[i * N + q][e] = 0.f;
   }
-  for (int k0 = 0; k0 < total; k0 += kC) {
-    __syncthreads();
-    auto off = [&](int c) { return k_off(g, ids, total, k0, c, ks.beg, kh); };
-    stage(sK, K, D, off);
-    stage(sV, V, D, off);
-    __syncthreads();
+  for (int k0 = 0, buf = 0; k0 < total; k0 += kC, buf = NB - 1 - buf) {
+    if (k0) __syncthreads();  // the buffer has been read
+    if (NB == 1 || k0 + kC < total) fetch(NB == 2 ? k0 + kC : k0, NB - 1 - buf);
+    else staged();  // (an empty group)
+    landed<NB - 1>();
     float s[4][4];
-    dots(sQ, sK, D, s);
+    dots(sQ, sK + buf * kC * ld, D, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = m[i];
@@ -201,38 +234,37 @@ __global__ void __launch_bounds__(kThr) block_fwd_simt(const FwdP p) {
       l[i] = l[i] * corr + sum;
       m[i] = mx;
 #pragma unroll
-      for (int q = 0; q < DQ; ++q)
+      for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][q][e] *= corr;
+        for (int e = 0; e < 4; ++e) o[i * N + q][e] *= corr;
     }
     __syncwarp();  // a row's weights come from the half-warp that uses them
-    if (k0 + kC > lim0) weighted<DQ, false, true>(sP, sV, D, o);
-    else weighted<DQ, false, false>(sP, sV, D, o);
+    if (k0 + kC > lim0) weighted<DQ, false, true>(sP, sV + buf * kC * ld, D, o);
+    else weighted<DQ, false, false>(sP, sV + buf * kC * ld, D, o);
   }
-  T* out = static_cast<T*>(p.out);
+  landed<0>();  // with an empty list nothing has waited for Q
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t at = q_off(g, un, kh, r0 + ty * 4 + i);
-    if (at < 0) continue;
     const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
-    if (tx == 0) p.lse[at / D] = l[i] != 0.f ? (m[i] + lg2(l[i])) * kLn2 : neg_inf();
-#pragma unroll
-    for (int q = 0; q < DQ; ++q) {
-      const int c = tx * 4 + 64 * q;
-      if (c < D) put4<T, DQ>(out + at + c, o[i][q], inv);
-    }
+    if (tx == 0 && at >= 0) p.lse[at / D] = l[i] != 0.f ? (m[i] + lg2(l[i])) * kLn2 : neg_inf();
+    finish<DQ>(o, i, D, inv, [&](int c, float4 v) {
+      if (at >= 0) *reinterpret_cast<float4*>(p.out + at + c) = v;
+    });
   }
 }
 
 // dQ of 64 (row, head) pairs of a unit
-template <class T, int DQ>
+template <int DQ>
 __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int ids[kBlkMaxTopk];
   __shared__ int n_ids;
   const BlockGeom& g = p.g;
   const int D = g.D, ld = D + 4, kh = blockIdx.y, u = blockIdx.x, r0 = blockIdx.z * kR;
-  float *sQ = sm, *sO = sQ + kR * ld, *sK = sO + kR * ld, *sV = sK + kC * ld, *sP = sV + kC * ld;
+  constexpr int NB = kBufs<DQ>, N = DQ ? DQ : 1;
+  float *sQ = sm, *sO = sQ + kR * ld, *sK = sO + kR * ld, *sV = sK + NB * kC * ld,
+        *sP = sV + NB * kC * ld;
   const Unit un = unit_at(g, u);
   if (r0 >= un.n * g.G) return;
   const Span ks = span_k(g, un.s);
@@ -245,7 +277,7 @@ __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
   const int n = n_ids, total = list_keys(ids, n, g.block, ks.len);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int lim[4];
-  float L[4], Dl[4], o[4][DQ][4];
+  float L[4], Dl[4], o[4 * N][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + ty * 4 + i, t = r / g.G;
@@ -256,22 +288,28 @@ __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
     L[i] = stat.x;
     Dl[i] = stat.y;
 #pragma unroll
-    for (int q = 0; q < DQ; ++q)
+    for (int q = 0; q < N; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][q][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[i * N + q][e] = 0.f;
   }
+  const auto fetch = [&](int k0, int buf) {
+    const auto off = [&](int c) { return k_off(g, ids, total, k0, c, ks.beg, kh); };
+    stage(sK + buf * kC * ld, static_cast<const float*>(p.K), D, off);
+    stage(sV + buf * kC * ld, static_cast<const float*>(p.V), D, off);
+    staged();
+  };
   const auto qo = [&](int r) { return q_off(g, un, kh, r0 + r); };
-  stage(sQ, static_cast<const T*>(p.Q), D, qo);
-  stage(sO, static_cast<const T*>(p.dO), D, qo);
-  for (int k0 = 0; k0 < total; k0 += kC) {
-    __syncthreads();
-    auto off = [&](int c) { return k_off(g, ids, total, k0, c, ks.beg, kh); };
-    stage(sK, static_cast<const T*>(p.K), D, off);
-    stage(sV, static_cast<const T*>(p.V), D, off);
-    __syncthreads();
+  stage(sQ, static_cast<const float*>(p.Q), D, qo);
+  stage(sO, static_cast<const float*>(p.dO), D, qo);
+  if (NB == 2) fetch(0, 0);
+  for (int k0 = 0, buf = 0; k0 < total; k0 += kC, buf = NB - 1 - buf) {
+    if (k0) __syncthreads();  // the buffer has been read
+    if (NB == 1 || k0 + kC < total) fetch(NB == 2 ? k0 + kC : k0, NB - 1 - buf);
+    else staged();  // (an empty group)
+    landed<NB - 1>();
     float s[4][4], dp[4][4];
-    dots(sQ, sK, D, s);
-    dots(sO, sV, D, dp);
+    dots(sQ, sK + buf * kC * ld, D, s);
+    dots(sO, sV + buf * kC * ld, D, dp);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -281,32 +319,34 @@ __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
         sP[(ty * 4 + i) * kPS + tx + 16 * j] = w;
       }
     __syncwarp();
-    weighted<DQ, false, false>(sP, sK, D, o);
+    weighted<DQ, false, false>(sP, sK + buf * kC * ld, D, o);
   }
-  T* dQ = static_cast<T*>(p.dQ);
+  landed<0>();  // with an empty list nothing has waited for Q and dO
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t at = q_off(g, un, kh, r0 + ty * 4 + i);
-    if (at < 0) continue;
-#pragma unroll
-    for (int q = 0; q < DQ; ++q) {
-      const int c = tx * 4 + 64 * q;
-      if (c < D) put4<T, DQ>(dQ + at + c, o[i][q], g.scale);
-    }
+    finish<DQ>(o, i, D, g.scale, [&](int c, float4 v) {
+      if (at >= 0) *reinterpret_cast<float4*>(static_cast<float*>(p.dQ) + at + c) = v;
+    });
   }
 }
 
 // dK, dV of one half (64 keys) of a work item's key tile
-template <class T, int DQ>
+template <int DQ>
 __global__ void __launch_bounds__(kThr) block_dkv_simt(const BlockBwdParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int list[1024];
   __shared__ uint8_t mask[1024];
   __shared__ int n_list, n_all;
+  constexpr int NB = kBufs<DQ>, N = DQ ? DQ : 1;
+  __shared__ float2 row_stat[NB][kR];  // of a step's rows: (lse log2e, Delta),
+  __shared__ int row_end[NB][kR];      // the first position that the row does not see
   const BlockGeom& g = p.g;
   const int D = g.D, ld = D + 4;
-  float *sK = sm, *sV = sK + kC * ld, *sQ = sV + kC * ld, *sO = sQ + kR * ld, *sP = sO + kR * ld;
+  float *sK = sm, *sV = sK + kC * ld, *sQ = sV + kC * ld, *sO = sQ + NB * kR * ld,
+        *sP = sO + NB * kR * ld;
   float* sS = sP + kR * kPS;
+  const int parts = (g.qb * g.G + kR - 1) / kR;  // steps of a unit
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t n_items = p.head[0];
   for (int64_t it = blockIdx.x; it < 2 * n_items; it += gridDim.x) {
@@ -325,15 +365,16 @@ __global__ void __launch_bounds__(kThr) block_dkv_simt(const BlockBwdParams p) {
       return pos0 + c < ks.len ? (int64_t(ks.beg + pos0 + c) * g.Hkv + kh) * D : -1;
     };
     __syncthreads();
-    stage(sK, static_cast<const T*>(p.K), D, ko);
-    stage(sV, static_cast<const T*>(p.V), D, ko);
-    float gk[4][DQ][4], gv[4][DQ][4];
+    stage(sK, static_cast<const float*>(p.K), D, ko);
+    stage(sV, static_cast<const float*>(p.V), D, ko);
+    int blk[4];  // block of this thread's keys within the tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) blk[j] = (half * kC + tx + 16 * j) / g.block;
+    float gk[4 * N][4], gv[4 * N][4];
 #pragma unroll
-      for (int x = 0; x < DQ; ++x)
+    for (int i = 0; i < 4 * N; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) gk[i][x][e] = gv[i][x][e] = 0.f;
+      for (int e = 0; e < 4; ++e) gk[i][e] = gv[i][e] = 0.f;
     int seen = 0;  // units of the key tile before this group of bitmap words
     for (int w0 = ub / 32; w0 <= (ub + nu - 1) / 32 && nu > 0 && seen < q.y + q.z; w0 += 32) {
       __syncthreads();
@@ -373,66 +414,72 @@ __global__ void __launch_bounds__(kThr) block_dkv_simt(const BlockBwdParams p) {
       __syncthreads();
       const int nl = n_list;
       seen += n_all;
-      for (int e = 0; e < nl; ++e) {
-        const int u = list[e];
-        const uint32_t mk = mask[e];
-        const int64_t uo = int64_t(u - ub) * g.qb;
-        if (uo < 0 || uo >= qs.len) continue;  // only where offsets lie about the tables
-        Unit un;
+      const int steps = nl * parts;
+      const auto fetch = [&](int st, int buf) {
+        const int e = st / parts, r0 = (st - e * parts) * kR;
+        const int64_t uo = int64_t(list[e] - ub) * g.qb;
+        Unit un{};
         un.s = s;
-        un.row = qs.beg + int(uo);
-        un.n = min(g.qb, qs.len - int(uo));
-        un.pos = int(uo) + ks.len - qs.len;
-        for (int r0 = 0; r0 < un.n * g.G; r0 += kR) {
-          __syncthreads();
-          const auto qo = [&](int r) { return q_off(g, un, kh, r0 + r); };
-          stage(sQ, static_cast<const T*>(p.Q), D, qo);
-          stage(sO, static_cast<const T*>(p.dO), D, qo);
-          __syncthreads();
-          float sc[4][4], dp[4][4];
-          dots(sQ, sK, D, sc);
-          dots(sO, sV, D, dp);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = r0 + ty * 4 + i, t = r / g.G;
-            const int64_t at = q_off(g, un, kh, r);
-            const float2 stat = at >= 0 ? p.stat[at / D] : make_float2(0.f, 0.f);
-            const int end = at < 0 ? 0 : g.causal ? min(un.pos + t + 1, ks.len) : ks.len;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = tx + 16 * j, pos = pos0 + c;
-              const bool in = pos < end && ((mk >> ((half * kC + c) / g.block)) & 1u);
-              const float w = in ? ex2(fmaf(sc[i][j], g.qmul, -stat.x)) : 0.f;
-              sP[(ty * 4 + i) * kPS + c] = w;
-              sS[(ty * 4 + i) * kPS + c] = in ? w * (dp[i][j] - stat.y) : 0.f;
-            }
-          }
-          __syncthreads();
-          weighted<DQ, true, false>(sP, sO, D, gv);
-          weighted<DQ, true, false>(sS, sQ, D, gk);
+        // (a unit outside the sequence: only where offsets lie about the tables)
+        if (uo >= 0 && uo < qs.len) {
+          un.row = qs.beg + int(uo);
+          un.n = min(g.qb, qs.len - int(uo));
+          un.pos = int(uo) + ks.len - qs.len;
         }
+        const auto qo = [&](int r) { return q_off(g, un, kh, r0 + r); };
+        const int64_t at = stage(sQ + buf * kR * ld, static_cast<const float*>(p.Q), D, qo);
+        stage(sO + buf * kR * ld, static_cast<const float*>(p.dO), D, qo);
+        staged();
+        if ((threadIdx.x & 3) == 0) {
+          const int r = threadIdx.x >> 2;
+          row_stat[buf][r] = at >= 0 ? p.stat[at / D] : make_float2(0.f, 0.f);
+          row_end[buf][r] =
+              at < 0 ? 0 : g.causal ? min(un.pos + (r0 + r) / g.G + 1, ks.len) : ks.len;
+        }
+      };
+      if (NB == 2 && steps) fetch(0, 0);
+      for (int st = 0, buf = 0; st < steps; ++st, buf = NB - 1 - buf) {
+        const uint32_t mk = mask[st / parts];
+        if (st) __syncthreads();  // the buffer has been read
+        if (NB == 1 || st + 1 < steps) fetch(NB == 2 ? st + 1 : st, NB - 1 - buf);
+        else staged();  // (an empty group)
+        landed<NB - 1>();
+        float sc[4][4], dp[4][4];
+        dots(sQ + buf * kR * ld, sK, D, sc);
+        dots(sO + buf * kR * ld, sV, D, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 stat = row_stat[buf][ty * 4 + i];
+          const int end = row_end[buf][ty * 4 + i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = tx + 16 * j;
+            const bool in = pos0 + c < end && ((mk >> blk[j]) & 1u);
+            const float w = in ? ex2(fmaf(sc[i][j], g.qmul, -stat.x)) : 0.f;
+            sP[(ty * 4 + i) * kPS + c] = w;
+            sS[(ty * 4 + i) * kPS + c] = in ? w * (dp[i][j] - stat.y) : 0.f;
+          }
+        }
+        __syncthreads();
+        weighted<DQ, true, false>(sP, sO + buf * kR * ld, D, gv);
+        weighted<DQ, true, false>(sS, sQ + buf * kR * ld, D, gk);
       }
     }
+    landed<0>();  // an item without units has not waited for K and V
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = ty * 4 + i;
       const int64_t at = ko(c);
-      if (at < 0) continue;
-#pragma unroll
-      for (int x = 0; x < DQ; ++x) {
-        const int d = tx * 4 + 64 * x;
-        if (d >= D) continue;
-        if (q.w < 0) {
-          put4<T, DQ>(static_cast<T*>(p.dK) + at + d, gk[i][x], g.scale);
-          put4<T, DQ>(static_cast<T*>(p.dV) + at + d, gv[i][x], 1.f);
-        } else {
-          float* o = p.part + (int64_t(q.w) * 2 * kBlkTile + half * kC + c) * D + d;
-          *reinterpret_cast<float4*>(o) =
-              make_float4(gk[i][x][0], gk[i][x][1], gk[i][x][2], gk[i][x][3]);
-          *reinterpret_cast<float4*>(o + int64_t(kBlkTile) * D) =
-              make_float4(gv[i][x][0], gv[i][x][1], gv[i][x][2], gv[i][x][3]);
-        }
-      }
+      float* part = p.part + (int64_t(max(q.w, 0)) * 2 * kBlkTile + half * kC + c) * D;
+      finish<DQ>(gk, i, D, q.w < 0 ? g.scale : 1.f, [&](int d, float4 v) {
+        if (at >= 0)
+          *reinterpret_cast<float4*>((q.w < 0 ? static_cast<float*>(p.dK) + at : part) + d) = v;
+      });
+      part += int64_t(kBlkTile) * D;
+      finish<DQ>(gv, i, D, 1.f, [&](int d, float4 v) {
+        if (at >= 0)
+          *reinterpret_cast<float4*>((q.w < 0 ? static_cast<float*>(p.dV) + at : part) + d) = v;
+      });
     }
   }
 }
@@ -459,42 +506,44 @@ gattn_status go(K kern, dim3 grid, int floats, const P& p, cudaStream_t st, cons
   return launched(what);
 }
 
-template <class T>
-gattn_status fwd(const FwdP& p, dim3 grid, cudaStream_t st) {
-  const int fl = 3 * kR * (p.g.D + 4) + kR * kPS;
-  return p.g.D > 64 ? go(block_fwd_simt<T, 2>, grid, fl, p, st, "gattn_block_fwd")
-                    : go(block_fwd_simt<T, 1>, grid, fl, p, st, "gattn_block_fwd");
-}
-
-template <class T>
-gattn_status bwd(const BlockBwdParams& p, dim3 grid, cudaStream_t st) {
-  const int fl = 4 * kR * (p.g.D + 4) + kR * kPS, fk = fl + kR * kPS;
-  const dim3 gk(unsigned(std::min<int64_t>(2 * p.max_items, int64_t(sm_count()) * 2)));
-  gattn_status s = GATTN_OK;
-  if (p.g.U > 0)
-    s = p.g.D > 64 ? go(block_dq_simt<T, 2>, grid, fl, p, st, "gattn_block_bwd (dQ)")
-                   : go(block_dq_simt<T, 1>, grid, fl, p, st, "gattn_block_bwd (dQ)");
-  if (s != GATTN_OK) return s;
-  return p.g.D > 64 ? go(block_dkv_simt<T, 2>, gk, fk, p, st, "gattn_block_bwd (dK, dV)")
-                    : go(block_dkv_simt<T, 1>, gk, fk, p, st, "gattn_block_bwd (dK, dV)");
-}
-
 dim3 row_grid(const BlockGeom& g) {
   return dim3(unsigned(g.U), unsigned(g.Hkv), unsigned((g.qb * g.G + kR - 1) / kR));
 }
 
 }  // namespace
 
-gattn_status launch_block_fwd_simt(const BlockGeom& g, gattn_dtype dt, const void* Q,
-                                   const void* K, const void* V, const int32_t* idx, void* out,
-                                   float* lse, cudaStream_t st) {
+gattn_status launch_block_fwd_simt(const BlockGeom& g, const float* Q, const float* K,
+                                   const float* V, const int32_t* idx, float* out, float* lse,
+                                   cudaStream_t st) {
   const FwdP p{g, Q, K, V, idx, out, lse};
-  return dt == GATTN_F32 ? fwd<float>(p, row_grid(g), st) : fwd<__nv_bfloat16>(p, row_grid(g), st);
+  const auto run = [&](auto kern, int bufs) {
+    return go(kern, row_grid(g), (1 + 2 * bufs) * kR * (g.D + 4) + kR * kPS, p, st,
+              "gattn_block_fwd");
+  };
+  return g.D <= 32   ? run(block_fwd_simt<0>, kBufs<0>)
+         : g.D <= 64 ? run(block_fwd_simt<1>, kBufs<1>)
+                     : run(block_fwd_simt<2>, kBufs<2>);
 }
 
-gattn_status launch_block_bwd_simt(const BlockBwdParams& p, gattn_dtype dt, cudaStream_t st) {
-  return dt == GATTN_F32 ? bwd<float>(p, row_grid(p.g), st)
-                         : bwd<__nv_bfloat16>(p, row_grid(p.g), st);
+gattn_status launch_block_bwd_simt(const BlockBwdParams& p, cudaStream_t st) {
+  const BlockGeom& g = p.g;
+  const int tile = kR * (g.D + 4);
+  const auto dq = [&](auto kern, int bufs) {
+    return go(kern, row_grid(g), (2 + 2 * bufs) * tile + kR * kPS, p, st, "gattn_block_bwd (dQ)");
+  };
+  const dim3 gk(unsigned(std::min<int64_t>(2 * p.max_items, int64_t(sm_count()) * 2)));
+  const auto dkv = [&](auto kern, int bufs) {
+    return go(kern, gk, (2 + 2 * bufs) * tile + 2 * kR * kPS, p, st, "gattn_block_bwd (dK, dV)");
+  };
+  gattn_status s = GATTN_OK;
+  if (g.U > 0)
+    s = g.D <= 32   ? dq(block_dq_simt<0>, kBufs<0>)
+        : g.D <= 64 ? dq(block_dq_simt<1>, kBufs<1>)
+                    : dq(block_dq_simt<2>, kBufs<2>);
+  if (s != GATTN_OK) return s;
+  return g.D <= 32   ? dkv(block_dkv_simt<0>, kBufs<0>)
+         : g.D <= 64 ? dkv(block_dkv_simt<1>, kBufs<1>)
+                     : dkv(block_dkv_simt<2>, kBufs<2>);
 }
 
 }  // namespace gattn
