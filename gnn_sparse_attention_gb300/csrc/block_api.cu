@@ -134,15 +134,16 @@ gattn_status check_ptrs(const char* what, std::initializer_list<const void*> lis
 // --------------------------------------------------------------------------
 // backward: workspace and preparation
 // --------------------------------------------------------------------------
-BlockBwdWs bwd_ws(const BlockGeom& g) {
+BlockBwdWs bwd_ws(const BlockGeom& g, bool f32) {
   BlockBwdWs w{};
   w.words = (g.U + 31) / 32;
   // Work items: about four per SM when every unit lists topk blocks of other
-  // key tiles, at least 32 tiles of 128 rows each; more items than that cost
-  // partials (128 x 2D fp32 each) without filling the GPU better.
+  // key tiles, at least 32 tiles of 128 rows each (fp32, whose products take
+  // twenty times as long: 1); more items than that cost partials (128 x 2D fp32
+  // each) without filling the GPU better.
   const int64_t entries = int64_t(g.U) * g.Hkv * g.topk;
   const int rows = g.qb * g.G;
-  const int64_t least = std::max<int64_t>(1, int64_t(32) * kBlkTile / std::max(rows, kBlkTile));
+  const int64_t least = std::max<int64_t>(1, int64_t(f32 ? 1 : 32) * kBlkTile / std::max(rows, kBlkTile));
   const int64_t per = (entries + int64_t(sm_count()) * 4 - 1) / (int64_t(sm_count()) * 4);
   w.chunk = int(std::min<int64_t>(std::max(least, per), INT32_MAX));
   // a tile of c > chunk units has ceil(c / chunk) <= 2 c / chunk items
@@ -447,7 +448,7 @@ gattn_status gattn_block_bwd_workspace_size(const gattn_block_desc* desc, size_t
   const gattn_status s = geom(desc, &g);
   if (s != GATTN_OK) return s;
   BLOCK_REQUIRE(bytes, GATTN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = bwd_ws(g).total;
+  *bytes = bwd_ws(g, desc->dtype == GATTN_F32).total;
   return GATTN_OK;
 }
 
@@ -459,7 +460,7 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   gattn_status s = geom(desc, &g);
   if (s != GATTN_OK) return s;
   if (g.S == 0 || (g.Nq == 0 && g.Nk == 0)) return GATTN_OK;
-  const BlockBwdWs w = bwd_ws(g);
+  const BlockBwdWs w = bwd_ws(g, desc->dtype == GATTN_F32);
   if ((g.Nq > 0 && (s = check_ptrs("gattn_block_bwd", {Q, out, dout, dQ})) != GATTN_OK) ||
       (g.Nk > 0 && (s = check_ptrs("gattn_block_bwd", {K, V, dK, dV})) != GATTN_OK) ||
       (s = check_ws("gattn_block_bwd", workspace, workspace_bytes, w.total)) != GATTN_OK)

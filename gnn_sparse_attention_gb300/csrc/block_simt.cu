@@ -25,6 +25,11 @@ constexpr int kC = 64;     // keys of a step
 constexpr int kThr = 256;
 constexpr int kPS = kC + 4;  // row stride of the score tile
 
+// Operand buffers of a step, and CTAs of an SM: two up to D = 64, where shared
+// memory and registers allow them.
+template <int DQ>
+constexpr int kBufs = DQ < 2 ? 2 : 1;
+
 struct FwdP {
   BlockGeom g;
   const float *Q, *K, *V;
@@ -68,6 +73,7 @@ __device__ __forceinline__ void dots(const float* a, const float* b, int D, floa
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 2
   for (int d = 0; d < D; d += 4) {
     float4 x[4], y[4];
 #pragma unroll
@@ -92,6 +98,7 @@ __device__ __forceinline__ void weighted(const float* w, const float* b, int D, 
   constexpr int N = DQ ? DQ : 1;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, ld = D + 4;
   const int c0 = (DQ ? tx : tx & 7) * 4;
+#pragma unroll 2
   for (int k = DQ ? 0 : (tx >> 3) * 4; k < kC; k += DQ ? 4 : 8) {
     float x[4][4];  // [key][row]
 #pragma unroll
@@ -152,12 +159,8 @@ __device__ __forceinline__ int64_t k_off(const BlockGeom& g, const int* ids, int
   return (int64_t(kbeg + ids[k / g.block] * g.block + k % g.block) * g.Hkv + kh) * g.D;
 }
 
-// operand buffers of a step: two where they fit
 template <int DQ>
-constexpr int kBufs = DQ < 2 ? 2 : 1;
-
-template <int DQ>
-__global__ void __launch_bounds__(kThr) block_fwd_simt(const FwdP p) {
+__global__ void __launch_bounds__(kThr, kBufs<DQ>) block_fwd_simt(const FwdP p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int ids[kBlkMaxTopk];
   __shared__ int n_ids;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThr) block_fwd_simt(const FwdP p) {
 
 // dQ of 64 (row, head) pairs of a unit
 template <int DQ>
-__global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
+__global__ void __launch_bounds__(kThr, kBufs<DQ>) block_dq_simt(const BlockBwdParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int ids[kBlkMaxTopk];
   __shared__ int n_ids;
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kThr) block_dq_simt(const BlockBwdParams p) {
 
 // dK, dV of one half (64 keys) of a work item's key tile
 template <int DQ>
-__global__ void __launch_bounds__(kThr) block_dkv_simt(const BlockBwdParams p) {
+__global__ void __launch_bounds__(kThr, kBufs<DQ>) block_dkv_simt(const BlockBwdParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int list[1024];
   __shared__ uint8_t mask[1024];
