@@ -141,13 +141,15 @@ class _BlockAttention(torch.autograd.Function):
 def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor,
                     topk: int = 16, block: int = 64, q_block: int = 64, causal: bool = False,
                     scale: float = 0.0, seq_k: torch.Tensor | None = None,
-                    len_k: torch.Tensor | None = None, idx: torch.Tensor | None = None):
+                    len_k: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+                    max_len_k: int = 0):
     """Softmax attention of each query over the ``topk`` blocks of its own sequence that score
     highest for its unit of ``q_block`` queries.
 
     Q: [Nq, H, D]; K, V: [Nk, Hkv, D]; seq: int32 [S + 1], the sequences' (graphs') first
     rows; seq_k and len_k (both optional) give the keys their own offsets and lengths.  ``idx``
-    (int32 [units, Hkv, blocks], see gattn_block_select) replaces the choice.  Returns
+    (int32 [units, Hkv, blocks], see gattn_block_select) replaces the choice; ``max_len_k``, the
+    most keys of one sequence (0: all rows), keeps its score tables small.  Returns
     (out [Nq, H, D], lse fp32 [Nq, H], idx); differentiable in Q, K and V, not in the choice.
     Rows of no sequence get zeros.
     """
@@ -157,7 +159,7 @@ def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torc
         with torch.no_grad():
             sums = gb.gattn_block_sums(K, keys, block, lens=len_k)
             idx = gb.gattn_block_select(Q, sums, seq, keys, topk, block, q_block, K.shape[0],
-                                        len_k=len_k, causal=causal)
+                                        len_k=len_k, causal=causal, max_len_k=max_len_k)
     out, lse = _BlockAttention.apply(Q, K, V, idx, seq, keys, len_k, block, q_block,
                                      float(scale), causal)
     return out, lse, idx
@@ -210,7 +212,8 @@ class GraphTransformerBlock(nn.Module):
     h = h + gate_a * norm(W_o (local + global)), where local is the attention over the plan's
     edges (left out without a plan) and global that over the selected blocks of the node's own
     graph, both on the same heads of norm(h); then h = h + gate_m * norm(MLP(norm(h))).  The
-    gates are learned per channel.  ``seq`` holds the graphs' first node rows.
+    gates are learned per channel.  ``seq`` holds the graphs' first node rows, ``max_nodes``
+    (0: unknown) the size of the largest graph.
     """
 
     def __init__(self, dim: int, heads: int, head_dim: int, mlp_dim: int | None = None,
@@ -235,12 +238,12 @@ class GraphTransformerBlock(nn.Module):
         self.gate_attn, self.gate_mlp = vector(gate_init), vector(gate_init)
 
     def forward(self, h: torch.Tensor, seq: torch.Tensor, plan: gb.Plan | None = None,
-                idx: torch.Tensor | None = None) -> torch.Tensor:
+                idx: torch.Tensor | None = None, max_nodes: int = 0) -> torch.Tensor:
         N = h.shape[0]
         h, y = gated_residual_norm(h, w_pre=self.w_in, b_pre=self.b_in, kind=self.kind)
         Q, K, V = (t.reshape(N, self.heads, self.head_dim) for t in self.qkv(y).chunk(3, -1))
         Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
-        a, _, _ = block_attention(Q, K, V, seq, idx=idx, **self.choice)
+        a, _, _ = block_attention(Q, K, V, seq, idx=idx, max_len_k=max_nodes, **self.choice)
         if plan is not None:
             a = a + graph_attention(plan, Q, K, V, "dot", 1.0 / math.sqrt(self.head_dim))[0]
         h, y = gated_residual_norm(h, self.o(a.reshape(N, -1)), self.gate_attn, self.w_attn,

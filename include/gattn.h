@@ -495,7 +495,8 @@ typedef struct {
 
 /*
  * Sums of the keys of each block in 64 bits: sums[blocks][Hkv][D] (device
- * double; bf16 keys add up to better than 2^-44 of the largest partial sum).
+ * double; bf16 keys add up to better than 2^-44 of the largest partial sum; partial
+ * sums that leave the range of fp32 are infinite).
  *   since : device int32 [S] or NULL.  NULL writes every row of `sums` (zeros in rows of
  *           no block); otherwise only blocks that hold a position >= since[s] are
  *           renewed, as after appending to a cache.
@@ -514,7 +515,9 @@ GATTN_API gattn_status gattn_block_sums(const gattn_block_desc* desc, const void
  * blocks that reach the unit's own positions come before all others.  The
  * choice is that of scores in 64 bits: scores are computed in 32 bits with an
  * error bound, and blocks within that bound of the last place are scored again
- * in 64.  Non-finite scores rank as -inf (NaN) or by their sign.
+ * in 64.  Blocks whose score is not a number or -inf are never chosen.  The
+ * scores of a unit stay in shared memory: max_len_k (or Nk) / block may be about
+ * 27,900 at most (GATTN_ERR_UNSUPPORTED beyond).
  */
 GATTN_API gattn_status gattn_block_select_workspace_size(const gattn_block_desc* desc,
                                                          size_t* bytes);

@@ -318,6 +318,51 @@ def test_select_is_cut_at_max_len():
     assert torch.equal(idx.cpu(), ref.select(Q, K, [0, 3], [0, 1000], 4, 16, 1, max_len=100))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qb", [1, 64])
+def test_select_non_finite_keys(qb, dtype):
+    """Blocks whose score is not a number or -inf are never chosen, +inf comes first."""
+    n, block, nan, inf = 400, 16, float("nan"), float("inf")
+    K, Q = randn(75, n, 2, 32, dtype=DT[dtype]), randn(76, 128, 4, 32, dtype=DT[dtype]).abs()
+    K[3 * block, 0, 5] = nan
+    K[7 * block + 1, 0, 0] = inf           # q > 0: +inf
+    K[9 * block + 2, 0, 0] = -inf
+    K[11 * block, 0, 3], K[11 * block + 1, 0, 3] = inf, -inf
+    sums = gb.gattn_block_sums(K, i32([0, n]), block)
+    for topk in (1, 4, 30):
+        idx = gb.gattn_block_select(Q, sums, i32([0, 128]), i32([0, n]), topk, block, qb, n)
+        exp = ref.select(Q, K, [0, 128], [0, n], topk, block, qb)
+        assert torch.equal(idx.cpu(), exp)
+        first = idx[0, 0].tolist()
+        assert 7 in first and not {3, 9, 11} & set(first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_beyond_32_bits(dtype):
+    """A sequence at the end of a cache of more than 2^31 elements."""
+    Nk, n, H, Hkv, D = 2_200_000, 777, 8, 8, 128
+    if torch.cuda.mem_get_info()[0] < 6 * Nk * Hkv * D * DT[dtype].itemsize:
+        pytest.skip("needs more device memory")
+    K, V = (torch.empty(Nk, Hkv, D, dtype=DT[dtype], device=DEV) for _ in range(2))
+    K[-n:], V[-n:] = randn(77, n, Hkv, D, dtype=DT[dtype]), randn(78, n, Hkv, D, dtype=DT[dtype])
+    sk = i32([Nk - n, Nk])
+    for lq, qb in ((1, 1), (100, 64)):
+        Q = randn(79, lq, H, D, dtype=DT[dtype])
+        sums = gb.gattn_block_sums(K, sk, 64)
+        idx = gb.gattn_block_select(Q, sums, i32([0, lq]), sk, 5, 64, qb, Nk, max_len_k=n)
+        assert torch.equal(idx.cpu(), ref.select(Q, K[-n:], [0, lq], [0, n], 5, 64, qb))
+        out, lse = gb.gattn_block_fwd(Q, K, V, idx, i32([0, lq]), sk, 64, qb)
+        dout = randn(80, lq, H, D, dtype=DT[dtype])
+        grads = gb.gattn_block_bwd(Q, K, V, idx, i32([0, lq]), sk, out, dout, lse, 64, qb)
+        torch.cuda.synchronize()
+        gb.gattn_block_check_errors()
+        r = ref.attention(Q, K[-n:], V[-n:], idx, [0, lq], [0, n], 64, qb, dout=dout)
+        for t, name in ((out, "out"), (lse, "lse"), (grads[0], "dQ"), (grads[1][-n:], "dK"),
+                        (grads[2][-n:], "dV")):
+            ref.check(t, r, name)
+        del grads
+
+
 def test_sums_are_renewed_from_a_position():
     sk, lens = [0, 300, 500], [290, 1]
     K = randn(74, 500, 2, 64, dtype=torch.bfloat16)

@@ -63,6 +63,16 @@ def test_block_attention_serves_a_cache():
     ref.check(lse, r, "lse")
 
 
+def test_block_attention_told_the_longest_sequence():
+    """The most keys of a sequence bound the work of the choice, not its result."""
+    torch.manual_seed(2)
+    Q, K, V = (torch.randn(600, 2, 32, device=DEV) for _ in range(3))
+    seq = i32([0, 250, 251, 600])
+    a = layer.block_attention(Q, K, V, seq, topk=3, block=16, q_block=32)
+    b = layer.block_attention(Q, K, V, seq, topk=3, block=16, q_block=32, max_len_k=349)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_gated_residual_norm_autograd(kind):
     torch.manual_seed(2)
