@@ -223,3 +223,21 @@ def test_captured_and_repeated():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of tensors of more than 2^31 elements are those of a call on them alone."""
+    N, F, n = 2_200_000, 1000, 37
+    if torch.cuda.mem_get_info()[0] < 10 * N * F * 2:
+        pytest.skip("needs more device memory")
+    res, x, dy = (torch.zeros(N, F, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for i, t in enumerate((res, x, dy)):
+        t[-n:] = randn(30 + i, n, F, dtype=torch.bfloat16)
+    w = 1 + 0.3 * randn(33, F)
+    whole = gb.gattn_norm_fwd(res, x, None, w_post=w, w_pre=w)
+    tail = gb.gattn_norm_fwd(res[-n:].clone(), x[-n:].clone(), None, w_post=w, w_pre=w)
+    assert all(torch.equal(a[-n:], b) for a, b in zip(whole, tail))
+    a = gb.gattn_norm_bwd(res, whole[2], None, dy, x, w_post=w, w_pre=w)
+    b = gb.gattn_norm_bwd(res[-n:].clone(), tail[2], None, dy[-n:].clone(), x[-n:].clone(),
+                          w_post=w, w_pre=w)
+    assert torch.equal(a["dres"][-n:], b["dres"]) and torch.equal(a["dx"][-n:], b["dx"])
