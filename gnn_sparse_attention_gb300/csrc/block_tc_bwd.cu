@@ -640,37 +640,6 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       }
       if (!ok) break;
     }
-  } else if (warp == kKvWarps + 3) {
-    // ---------------------------------------------------------------- statistics
-    // (a warp of its own: with the lists' chain of dependent work in one warp,
-    // the two took 1,430 clocks a step, more than everything else)
-    int gi = 0;
-    for (int ti = 0;; ++ti) {
-      const int slot = ti & 1;
-      ok = warp_wait(item_full + slot, (ti >> 1) & 1);
-      if (!ok) break;
-      const int item = info[slot].item, steps = info[slot].steps;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(item_empty + slot);
-      if (item < 0) break;
-      for (int st = 0; st < steps && ok; ++st, ++gi) {
-        const int si = gi % NS;
-        ok = warp_wait(box_full + si, (gi / NS) & 1);
-        if (!ok) break;
-        const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
-#pragma unroll
-        for (int e = 0; e < kNR / 32; ++e) {
-          const int c = e * 32 + lane, j = c >> p.l_br, i = c & (p.br - 1);
-          const Box& x = box[j];
-          if (i < x.rows)
-            cp_async8(sm + M::STAT + (si * kNR + c) * 8,
-                      p.b.stat + int64_t(x.row + (i >> p.l_bh)) * g.H + x.h0 + (i & (p.bh - 1)));
-        }
-        cp_async_arrive(q_full + si);
-      }
-      if (!ok) break;
-    }
-    cp_async_wait<0>();
   } else if (warp == kKvWarps + 1) {
     // ---------------------------------------------------------------- copies
     int gi = 0, tk = 0;
@@ -712,54 +681,36 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
             tma_tile3d(sm + (o ? M::O : M::Q) + si * QP + kb * kQPiece + j * p.br * 128,
                        o ? &p.mo : &p.mq, kb * 64, x.h0, x.row, q_full + si);
         }
+#pragma unroll
+        for (int e = 0; e < kNR / 32; ++e) {  // the statistics
+          const int c = e * 32 + lane, i = c & (p.br - 1);
+          const Box& x = box[c >> p.l_br];
+          if (i < x.rows)
+            cp_async8(sm + M::STAT + (si * kNR + c) * 8,
+                      p.b.stat + int64_t(x.row + (i >> p.l_bh)) * g.H + x.h0 + (i & (p.bh - 1)));
+        }
+        cp_async_arrive(q_full + si);
         __syncwarp();
       }
       if (!ok) break;
     }
+    cp_async_wait<0>();
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       if (tk > 0) warp_wait(kv_full, (tk - 1) & 1, 200);
       for (int c = gi; c > gi - NS && c >= 0; --c) warp_wait(q_full + c % NS, (c / NS) & 1, 200);
     }
   } else if (warp == kKvWarps) {
-    // ---------------------------------------------------------------- products
-    constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false), IDESC_G = f16_idesc(kT, DP, true);
+    // ---------------------------------------------------------------- scores
+    // A warp for S and dP, another for dV and dK: at D <= 64 one warp alone is busy
+    // for 890 clocks a step with issuing what the tensor cores do in 480.
+    constexpr uint32_t IDESC_S = f16_idesc(kT, kNR, false);
     const uint64_t dK = desc_k(sm + M::K), dV = desc_k(sm + M::V), dQ = desc_k(sm + M::Q),
-                   dO = desc_k(sm + M::O), dQm = desc_mn(sm + M::Q, kQPiece),
-                   dOm = desc_mn(sm + M::O, kQPiece);
+                   dO = desc_k(sm + M::O);
     const uint32_t tm = uniform(tmem);
-    // Step gi's scores overwrite p and ds of step gi - NG, whose products were
-    // issued before them and run in that order.
-    int gi = 0, tk = 0;                 // steps with scores, items
-    int done = 0, item = 0, i_done = 0;  // steps with all products, items, steps of this item
-    uint32_t ends = 0;                  // bit gi % 32: step gi is its item's last
-    auto product_g = [&]() {            // of step `done`
-      const int x = done % NG, si = done % NS;
-      const bool last = (ends >> (done & 31)) & 1u;
-      ok = ok && warp_wait(p_full + x, (done / NG) & 1);
-      if (i_done == 0 && item >= 1) ok = ok && warp_wait(g_empty, (item - 1) & 1);
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tm<kNR>(tm + M::T_ACC, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G,
-                    i_done > 0);
-        mma_tm<kNR>(tm + M::T_ACC + DP, tm + M::T_DP + x * kNR, 16, 16, desc_at(dQm, si * QP),
-                    IDESC_G, i_done > 0);
-        mma_commit(q_empty + si);
-        // (a barrier of its own: a group that has no part in the last steps
-        // would otherwise wait for a phase two ahead, which reads as complete)
-        if (last) mma_commit(g_full);
-      }
-      __syncwarp();
-      ++done;
-      i_done = last ? 0 : i_done + 1;
-      item += last;
-    };
+    int gi = 0, tk = 0;  // steps, items
     for (int ti = 0; ok; ++ti) {
       const int slot = ti & 1;
-      if (!__all_sync(0xffffffffu, mbar_test(item_full + slot, (ti >> 1) & 1))) {
-        while (ok && done < gi) product_g();  // the item may wait for those before it
-        ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
-      }
+      ok = warp_wait(item_full + slot, (ti >> 1) & 1);
       if (!ok) break;
       const int it = uniform(info[slot].item), n = uniform(info[slot].steps);
       __syncwarp();
@@ -768,8 +719,9 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       if (n <= 0) continue;
       ok = warp_wait(kv_full, tk & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
-        const int si = gi % NS, x = gi % NG;
-        if (gi - done == NG) product_g();
+        const int si = gi % NS, x = gi % NG, c = gi - NG;
+        // over p and ds of step gi - NG, whose products have run
+        if (c >= 0) ok = warp_wait(q_empty + c % NS, (c / NS) & 1);
         ok = ok && warp_wait(q_full + si, (gi / NS) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -780,19 +732,51 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
           if (i == n - 1) mma_commit(kv_empty);
         }
         __syncwarp();
-        ends = (ends & ~(1u << (gi & 31))) | (uint32_t(i == n - 1) << (gi & 31));
       }
       ++tk;
     }
-    while (ok && done < gi) product_g();
+    if (!ok)  // what was issued completes before TMEM is given up
+      for (int c = gi; c >= 0 && c > gi - NG - 1; --c)
+        warp_wait(s_full + c % NG, (c / NG) & 1, 200);
+  } else if (warp == kKvWarps + 3) {
+    // ---------------------------------------------------------------- gradients
+    constexpr uint32_t IDESC_G = f16_idesc(kT, DP, true);
+    const uint64_t dQm = desc_mn(sm + M::Q, kQPiece), dOm = desc_mn(sm + M::O, kQPiece);
+    const uint32_t tm = uniform(tmem);
+    int gi = 0, tk = 0;
+    for (int ti = 0; ok; ++ti) {
+      const int slot = ti & 1;
+      ok = warp_wait(item_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const int it = uniform(info[slot].item), n = uniform(info[slot].steps);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + slot);
+      if (it < 0) break;
+      if (n <= 0) continue;
+      if (tk >= 1) ok = warp_wait(g_empty, (tk - 1) & 1);
+      for (int i = 0; i < n && ok; ++i, ++gi) {
+        const int si = gi % NS, x = gi % NG;
+        ok = warp_wait(q_full + si, (gi / NS) & 1) && warp_wait(p_full + x, (gi / NG) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_tm<kNR>(tm + M::T_ACC, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
+          mma_tm<kNR>(tm + M::T_ACC + DP, tm + M::T_DP + x * kNR, 16, 16, desc_at(dQm, si * QP),
+                      IDESC_G, i > 0);
+          mma_commit(q_empty + si);
+          // (a barrier of its own: a group that has no part in the last steps
+          // would otherwise wait for a phase two ahead, which reads as complete)
+          if (i == n - 1) mma_commit(g_full);
+        }
+        __syncwarp();
+      }
+      ++tk;
+    }
     // every product has completed before TMEM is given up
     if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
-    if (!ok) {
-      for (int c = gi; c >= 0 && c > gi - NG - 1; --c) {
-        warp_wait(s_full + c % NG, (c / NG) & 1, 200);
+    if (!ok)
+      for (int c = gi; c >= 0 && c > gi - NG - 1; --c)
         warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
-      }
-    }
   } else {
     // ---------------------------------------------------------------- p and ds
     const int r = (warp & 3) * 32 + lane, part = (warp >> 2) & 1;  // key, 32 of 64 columns
