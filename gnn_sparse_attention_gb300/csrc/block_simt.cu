@@ -15,10 +15,6 @@
 // Measured: 7 graphs of 429 nodes, 4 heads of 32, 8 blocks of 32: forward 25 us,
 // dQ 32 us, dK and dV 63 us (1.4 GFLOP together, in half-empty rounds of the 304
 // CTAs that are resident).
-//
-// Measured: 7 graphs of 429 nodes, 4 heads of 32, 8 blocks of 32: forward 25 us,
-// dQ 32 us, dK and dV 63 us (1.4 GFLOP together, in half-empty rounds of the 304
-// CTAs that are resident).
 #include <algorithm>
 
 #include "attn_launch.cuh"

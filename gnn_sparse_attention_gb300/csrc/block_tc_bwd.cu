@@ -1,8 +1,8 @@
 // block_tc_bwd.cu -- backward of block attention on the tensor cores (bf16).
 //
-// Two kernels, both with the forward's division of labour (compute warps, one
-// warp that issues products, one that resolves lists and issues TMA; every
-// hand-over an mbarrier, every wait bounded):
+// Two kernels, both with the forward's division of labour (compute warps, one or
+// two warps that issue products, one that resolves lists, one that issues TMA;
+// every hand-over an mbarrier, every wait bounded):
 //
 // dQ: a tile of up to 128 (query row, head) pairs walks its unit's block list
 //   in steps of 128 keys,
@@ -30,14 +30,8 @@
 //   its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   272 us, dK and dV 597 us; two causal sequences of 8,191, 16 heads of 128 on 4:
-//   231 and 327 us.  A unit seldom chose all blocks of a key tile: with blocks of
-//   64 and one choice in three, 1.6 times the useful products run (1.9 with one
-//   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
-//
-//   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   272 us, dK and dV 597 us; two causal sequences of 8,191, 16 heads of 128 on 4:
-//   231 and 327 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   272 us, dK and dV 546 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   231 and 311 us.  A unit seldom chose all blocks of a key tile: with blocks of
 //   64 and one choice in three, 1.6 times the useful products run (1.9 with one
 //   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
 //

@@ -47,14 +47,6 @@
 // (32 heads on 8): 167 us, 6.4 TB/s.  What bounds the first three is the
 // softmax's latency: two streams keep the tensor cores 60% busy, and TMEM has no
 // room for a third or for a second score buffer of each.
-//
-// Measured (bf16, blocks of 64): a causal prompt of 32,768 tokens, 32 heads of 128
-// on 8 key heads, 32 blocks a unit: 0.76 ms, 1.40 PFLOP/s; two causal sequences
-// of 8,191, 16 heads of 128 on 4, 16 blocks: 120 us, 1.04; 24 graphs of 2,731
-// nodes, 8 heads of 64, 16 blocks: 187 us, 0.75; 128 tokens against caches of 8,000
-// (32 heads on 8): 167 us, 6.4 TB/s.  What bounds the first three is the
-// softmax's latency: two streams keep the tensor cores 60% busy, and TMEM has no
-// room for a third or for a second score buffer of each.
 #include <algorithm>
 
 #include "attn_launch.cuh"
