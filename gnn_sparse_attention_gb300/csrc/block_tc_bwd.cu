@@ -9,7 +9,8 @@
 //     S = Q K^T, dP = dO V^T                          -> TMEM (two S buffers)
 //     ds = 2^(S scale log2e - lse log2e) (dP - Delta)  -> TMEM, over S
 //     dQ += ds K                                       -> TMEM
-//   The next step's S and dP run while ds of this one is formed.  ds enters the
+//   The next step's S and dP run while ds of this one is formed, and four warps
+//   write a finished tile while the others are at the next.  ds enters the
 //   product as the sum of two bf16: rounded once it would add as much error to
 //   dQ as dQ's own rounding, on top of that of Delta (formed from the rounded
 //   out), and dQ would be half again as far off as the rounding of the result
@@ -30,8 +31,8 @@
 //   its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   272 us, dK and dV 546 us; two causal sequences of 8,191, 16 heads of 128 on 4:
-//   231 and 311 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   234 us, dK and dV 546 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   174 and 311 us.  A unit seldom chose all blocks of a key tile: with blocks of
 //   64 and one choice in three, 1.6 times the useful products run (1.9 with one
 //   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
 //
@@ -71,17 +72,19 @@ template <int DP>
 struct DqSm {
   static constexpr int KB = DP / 64;
   static constexpr int NQ = DP == 64 ? 2 : 1;   // Q and dO buffers
-  static constexpr int NS = DP == 64 ? 4 : 2;   // K and V stages
+  // K and V stages.  A stage of K is free after dQ, right before the scores that
+  // want it next where there are two: a third hides the load (D = 128: 231 -> 174 us)
+  static constexpr int NK = DP == 64 ? 4 : 3, NV = DP == 64 ? 4 : 2;
   static constexpr int NG = DP == 64 ? 2 : 1;   // dQ buffers (tiles in turn)
   static constexpr int OP = KB * kPiece;
   static constexpr int Q = 0;
   static constexpr int O = Q + NQ * OP;
   static constexpr int K = O + NQ * OP;
-  static constexpr int V = K + NS * OP;
-  static constexpr int IDS = V + NS * OP;
+  static constexpr int V = K + NK * OP;
+  static constexpr int IDS = V + NV * OP;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(DqInfo));
-  static constexpr int NBAR = 4 + 2 * NQ + 4 * NS + 2 + 1 + 2 + 2 + NG;
+  static constexpr int NBAR = 4 + 2 * NQ + 2 * NK + 2 * NV + 2 + 1 + 2 + 2 * NG;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -89,8 +92,8 @@ struct DqSm {
   static_assert(384 + NG * DP <= 512, "TMEM columns");
 };
 
-constexpr int kDqWarps = 16;
-constexpr int kDqThr = (kDqWarps + 3) * 32;
+constexpr int kDqWarps = 16, kDqOut = 4;
+constexpr int kDqThr = (kDqWarps + 3 + kDqOut) * 32;
 
 }  // namespace
 
@@ -98,15 +101,15 @@ template <int DP>
 __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__ DqParams p) {
   using namespace tc;
   using M = DqSm<DP>;
-  constexpr int KB = M::KB, NQ = M::NQ, NS = M::NS, NG = M::NG, OP = M::OP;
+  constexpr int KB = M::KB, NQ = M::NQ, NK = M::NK, NV = M::NV, NG = M::NG, OP = M::OP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *tile_full = bar, *tile_empty = tile_full + 2, *q_full = tile_empty + 2,
-           *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NS,
-           *v_full = k_empty + NS, *v_empty = v_full + NS, *s_full = v_empty + NS,
-           *dp_empty = s_full + 2, *d_full = dp_empty + 1, *d_done = d_full + 2,
-           *g_empty = d_done + 2;
+           *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NK,
+           *v_full = k_empty + NK, *v_empty = v_full + NV, *s_full = v_empty + NV,
+           *dp_empty = s_full + 2, *d_full = dp_empty + 1, *g_full = d_full + 2,
+           *g_empty = g_full + NG;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   DqInfo* info = reinterpret_cast<DqInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
@@ -116,20 +119,24 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(tile_full + i, 1);
-      mbar_init(tile_empty + i, kDqWarps + 2);
+      mbar_init(tile_empty + i, kDqWarps + kDqOut + 2);
       mbar_init(s_full + i, 1);
       mbar_init(d_full + i, kDqWarps);
-      mbar_init(d_done + i, 1);
     }
     mbar_init(dp_empty, kDqWarps);
-    for (int i = 0; i < NG; ++i) mbar_init(g_empty + i, kDqWarps);
+    for (int i = 0; i < NG; ++i) {
+      mbar_init(g_full + i, 1);
+      mbar_init(g_empty + i, kDqOut);
+    }
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
     }
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NK; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < NV; ++i) {
       mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, 1);
     }
@@ -202,11 +209,11 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
         }
       }
       for (int st = 0; st < steps; ++st, ++gi) {
-        const int si = gi % NS;
         const int nb = min(per, n - st * per);
         for (int kv = 0; kv < 2; ++kv) {
+          const int ns = kv ? NV : NK, si = gi % ns;
           uint64_t* full = (kv ? v_full : k_full) + si;
-          if (gi >= NS) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / NS) - 1) & 1);
+          if (gi >= ns) ok = ok && warp_wait((kv ? v_empty : k_empty) + si, ((gi / ns) - 1) & 1);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(full, nb * blk_bytes * KB);
           __syncwarp();
@@ -226,10 +233,8 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int i = 1; i <= NQ && i <= tq; ++i)
         warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
-      for (int c = gi; c > gi - NS && c >= 0; --c) {
-        warp_wait(k_full + c % NS, (c / NS) & 1, 200);
-        warp_wait(v_full + c % NS, (c / NS) & 1, 200);
-      }
+      for (int c = gi; c > gi - NK && c >= 0; --c) warp_wait(k_full + c % NK, (c / NK) & 1, 200);
+      for (int c = gi; c > gi - NV && c >= 0; --c) warp_wait(v_full + c % NV, (c / NV) & 1, 200);
     }
   } else if (warp == kDqWarps) {
     // ---------------------------------------------------------------- products
@@ -239,8 +244,9 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     const uint32_t tm = uniform(tmem);
     int gi = 0, ti = 0, tq = 0, done = 0;  // steps with scores, tiles, with dQ products
     int due_tile = 0, due_i = 0;            // of step `done`
+    bool due_last = false;
     auto product_dq = [&]() {
-      const int si = done % NS, b = done & 1, buf = due_tile % NG;
+      const int si = done % NK, b = done & 1, buf = due_tile % NG;
       ok = ok && warp_wait(d_full + b, (done >> 1) & 1);
       if (due_i == 0 && due_tile >= NG)
         ok = ok && warp_wait(g_empty + buf, (due_tile / NG - 1) & 1);
@@ -250,8 +256,8 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
         const uint32_t out = tm + 384 + buf * DP, ds = tm + b * kT;
         mma_tm<kT>(out, ds, 16, 16, desc_at(dKm, si * OP), IDESC_G, due_i > 0);
         mma_tm<kT>(out, ds + 8, 16, 16, desc_at(dKm, si * OP), IDESC_G, true);
-        mma_commit(d_done + b);
         mma_commit(k_empty + si);
+        if (due_last) mma_commit(g_full + buf);
       }
       __syncwarp();
       ++done;
@@ -270,48 +276,90 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       const int qs = tq % NQ;
       ok = warp_wait(q_full + qs, (tq / NQ) & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
-        const int si = gi % NS, b = gi & 1;
-        ok = ok && warp_wait(k_full + si, (gi / NS) & 1);
+        const int sk = gi % NK, sv = gi % NV, b = gi & 1;
+        ok = ok && warp_wait(k_full + sk, (gi / NK) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one())  // over the ds of step gi - 2, whose product was issued before
-          mma_kk<KB>(tm + b * kT, desc_at(dQ, qs * OP), kPiece, desc_at(dK, si * OP), kPiece,
+          mma_kk<KB>(tm + b * kT, desc_at(dQ, qs * OP), kPiece, desc_at(dK, sk * OP), kPiece,
                      IDESC_S);
         __syncwarp();
-        ok = warp_wait(v_full + si, (gi / NS) & 1);
+        ok = warp_wait(v_full + sv, (gi / NV) & 1);
         if (gi >= 1) ok = ok && warp_wait(dp_empty, (gi - 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_kk<KB>(tm + 2 * kT, desc_at(dO, qs * OP), kPiece, desc_at(dV, si * OP), kPiece,
+          mma_kk<KB>(tm + 2 * kT, desc_at(dO, qs * OP), kPiece, desc_at(dV, sv * OP), kPiece,
                      IDESC_S);
           mma_commit(s_full + b);
-          mma_commit(v_empty + si);
+          mma_commit(v_empty + sv);
           if (i == n - 1) mma_commit(q_empty + qs);
         }
         __syncwarp();
         if (done < gi) product_dq();
         due_tile = tq;
         due_i = i;
+        due_last = i == n - 1;
       }
       ++tq;
     }
     if (ok && done < gi) product_dq();
-    if (ok && gi > 0) ok = warp_wait(d_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
+    if (ok && tq > 0) ok = warp_wait(g_full + (tq - 1) % NG, ((tq - 1) / NG) & 1);
     if (!ok) {  // whatever was issued has completed before TMEM is given up
       for (int k = 0; k <= 2 && k <= gi; ++k) {
         const int c = gi - k;
         warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
-        warp_wait(d_done + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(k_empty + c % NK, (c / NK) & 1, 200);
       }
+    }
+  } else if (warp >= kDqWarps + 3) {
+    // ---------------------------------------------------------------- output
+    const int quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    const int th = r % p.ht, tt = r / p.ht;
+    const bool wide = wide_rows(p.b.dQ, g.D);
+    int ti = 0, to = 0;  // tiles, tiles with steps
+    for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
+      const int slot = ti & 1, buf = to % NG;
+      ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const DqInfo& f = info[slot];
+      const bool some = f.steps > 0, valid = r < p.rows && tt < f.rows;
+      const int64_t qrow = int64_t(f.row + tt) * g.H + f.h0 + th;
+      if (some) {
+        ok = warp_wait(g_full + buf, (to / NG) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        float o[32];
+        __syncwarp();
+        if (some) {
+          tmem_ld32(tmem + lanes + 384 + buf * DP + c * 32, o);
+          tmem_wait_ld();
+        }
+        if (c == DP / 32 - 1) {  // the buffer is free before the row's end is written
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && some) mbar_arrive(g_empty + buf);
+        }
+        if (valid) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * g.scale : 0.f;
+          store_row(static_cast<__nv_bfloat16*>(p.b.dQ) + qrow * g.D, c * 32, g.D, o, wide);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_empty + slot);
+      to += some;
     }
   } else {
     // ---------------------------------------------------------------- ds
     const int r = (warp & 3) * 32 + lane, cc = warp >> 2;  // row, 32-column chunk
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const int th = r % p.ht, tt = r / p.ht;
-    const bool wide = wide_rows(p.b.dQ, g.D);
-    int gi = 0, ti = 0, to = 0;
+    int gi = 0, ti = 0;
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
@@ -327,7 +375,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       float2 stat = make_float2(0.f, 0.f);
       if (lim > 0) stat = p.b.stat[qrow];  // a row that sees nothing has lse = -inf
       for (int st = 0; st < steps; ++st, ++gi) {
-        const int si = gi % NS, b = gi & 1;
+        const int b = gi & 1;
         ok = ok && warp_wait(s_full + b, (gi >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -341,7 +389,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
         if (total < (st + 1) * kT) {  // keys behind the list's end: zeros in K
           const int nv = total - st * kT;
           for (int kb = 0; kb < KB; ++kb) {
-            uint4* k = reinterpret_cast<uint4*>(sm + M::K + si * OP + kb * kPiece);
+            uint4* k = reinterpret_cast<uint4*>(sm + M::K + gi % NK * OP + kb * kPiece);
             for (int i = nv * 8 + threadIdx.x; i < kT * 8; i += kDqWarps * 32)
               k[i] = make_uint4(0, 0, 0, 0);
           }
@@ -370,9 +418,11 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
                 f2mul(make_float2(ex2(z.x), ex2(z.y)),
                       f2add(make_float2(dv[h * 16 + 2 * j], dv[h * 16 + 2 * j + 1]), nd));
             const uint32_t hi = bf16x2_bits(y.x, y.y);
+            const float2 lo = f2fma(make_float2(__uint_as_float(hi << 16),
+                                                __uint_as_float(hi & 0xffff0000u)),
+                                    f2s(-1.f), y);
             w[j] = __uint_as_float(hi);
-            w[8 + j] = __uint_as_float(bf16x2_bits(y.x - __uint_as_float(hi << 16),
-                                                   y.y - __uint_as_float(hi & 0xffff0000u)));
+            w[8 + j] = __uint_as_float(bf16x2_bits(lo.x, lo.y));
           }
           tmem_st16(tS + h * 16, w);
         }
@@ -382,31 +432,8 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
         if (lane == 0) mbar_arrive(d_full + b);
       }
       if (!ok) break;
-      const bool some = steps > 0;
-      if (some) {
-        ok = warp_wait(d_done + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if (cc * 32 < DP) {
-        float o[32];
-        if (some) {
-          tmem_ld32(tmem + lanes + 384 + (to % NG) * DP + cc * 32, o);
-          tmem_wait_ld();
-        }
-        if (valid) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * g.scale : 0.f;
-          store_row(static_cast<__nv_bfloat16*>(p.b.dQ) + qrow * g.D, cc * 32, g.D, o, wide);
-        }
-      }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (some) mbar_arrive(g_empty + to % NG);
-        mbar_arrive(tile_empty + slot);
-      }
-      to += some;
+      if (lane == 0) mbar_arrive(tile_empty + slot);
     }
   }
   if (!ok) atomicOr(&g_err, 2);
