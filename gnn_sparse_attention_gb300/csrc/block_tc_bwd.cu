@@ -23,16 +23,17 @@
 //     p, ds as bf16                                    -> TMEM, over S^T and dP^T
 //     dV += p dO, dK += ds Q                           -> TMEM
 //   64 rather than 128 queries a step leave room for several stages of Q and
-//   dO and a second and, at D <= 64, third score buffer next to the two
-//   accumulators; as many groups of eight warps take the steps in turn, so that
-//   one forms p and ds while another waits for its products.  Units
-//   of fewer than 64 pairs share a step, each in a box of its own; a box
+//   dO and a second score buffer next to the two accumulators; two groups of
+//   eight warps take the steps in turn, so that one forms p and ds while the other
+//   waits for its products.  (A third group at D <= 64 left 72 registers a thread:
+//   its spills filled what shared memory leaves of L1, 532 us against 471.)  Four
+//   more warps write a finished item.  Units of fewer than 64 pairs share a step, each in a box of its own; a box
 //   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
 //   its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   234 us, dK and dV 546 us; two causal sequences of 8,191, 16 heads of 128 on 4:
-//   174 and 311 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   234 us, dK and dV 438 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   174 and 300 us.  A unit seldom chose all blocks of a key tile: with blocks of
 //   64 and one choice in three, 1.6 times the useful products run (1.9 with one
 //   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
 //
@@ -447,6 +448,8 @@ namespace {
 
 constexpr int kNR = 64;               // query pairs per step
 constexpr int kQPiece = kNR * 128;    // 64 rows x 64 bf16 columns
+constexpr int kKvWarps = 16, kKvOut = 4;  // two groups of eight, steps in turn
+constexpr int kKvThr = (kKvWarps + 4 + kKvOut) * 32;
 constexpr int kList = 256;            // units resolved at a time (8 bitmap words)
 
 struct DkvParams {
@@ -475,27 +478,25 @@ struct KvInfo {
 template <int DP>
 struct KvSm {
   static constexpr int KB = DP / 64;
-  static constexpr int NG = DP == 64 ? 3 : 2;  // groups of eight warps, score buffers
-  static constexpr int WARPS = NG * 8, THR = (WARPS + 4) * 32;
   static constexpr int NS = DP == 64 ? 6 : 4;  // Q and dO stages
-  static_assert(NS % NG == 0, "a stage belongs to one group, which waits for each of its phases");
+  static constexpr int NB = DP == 64 ? 2 : 1;  // K and V buffers, dK and dV buffers (items in turn)
+  static_assert(NS % 2 == 0, "a stage belongs to one group, which waits for each of its phases");
   static constexpr int OP = KB * kPiece, QP = KB * kQPiece;
   static constexpr int K = 0;
-  static constexpr int V = OP;
-  static constexpr int Q = 2 * OP;
+  static constexpr int V = NB * OP;
+  static constexpr int Q = 2 * NB * OP;
   static constexpr int O = Q + NS * QP;
   static constexpr int STAT = O + NS * QP;       // [NS][64] (lse log2e, Delta)
   static constexpr int BOX = STAT + NS * kNR * 8;
   static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
   static constexpr int INFO = LIST + kList * 8;
   static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
-  static constexpr int NBAR = 4 + 2 + 3 * NS + 2 * NG + 2;
+  static constexpr int NBAR = 4 + 2 * NB + 3 * NS + 4 + 2 * NB;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
-  // TMEM: S^T and dP^T of the groups, dV, dK
-  static constexpr int T_DP = NG * kNR, T_ACC = 2 * T_DP;
-  static_assert(T_ACC + 2 * DP <= 512, "TMEM columns");
+  // TMEM: S^T [0, 128) and dP^T [128, 256) of the groups, then (dV, dK) of each buffer
+  static_assert(256 + NB * 2 * DP <= 512, "TMEM columns");
 };
 
 // arrive once this thread's cp.async copies so far have landed
@@ -507,17 +508,17 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }  // namespace
 
 template <int DP>
-__global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
+__global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant__ DkvParams p) {
   using namespace tc;
   using M = KvSm<DP>;
-  constexpr int KB = M::KB, NS = M::NS, NG = M::NG, QP = M::QP, kKvWarps = M::WARPS;
+  constexpr int KB = M::KB, NS = M::NS, NB = M::NB, OP = M::OP, QP = M::QP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
-           *kv_empty = kv_full + 1, *q_full = kv_empty + 1, *q_empty = q_full + NS,
-           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + NG,
-           *g_full = p_full + NG, *g_empty = g_full + 1;
+           *kv_empty = kv_full + NB, *q_full = kv_empty + NB, *q_empty = q_full + NS,
+           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + 2,
+           *g_full = p_full + 2, *g_empty = g_full + NB;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
   int2* list = reinterpret_cast<int2*>(sm + M::LIST);
@@ -527,21 +528,21 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, kKvWarps + 3);
-    }
-    for (int i = 0; i < NG; ++i) {
+      mbar_init(item_empty + i, kKvWarps + kKvOut + 3);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 8);
     }
-    mbar_init(g_full, 1);
-    mbar_init(kv_full, 1);
-    mbar_init(kv_empty, 1);
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(g_full + i, 1);
+      mbar_init(g_empty + i, kKvOut);
+      mbar_init(kv_full + i, 1);
+      mbar_init(kv_empty + i, 1);
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(q_full + i, 1 + 32);  // the copies' bytes, and each lane's statistics
       mbar_init(q_empty + i, 1);
       mbar_init(box_full + i, 1);
     }
-    mbar_init(g_empty, 16);
     mbar_init_fence();
   }
   if (warp == kKvWarps) tmem_alloc512(s_tmem);
@@ -618,16 +619,19 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
               if (lane >= o) before += x;
             }
             const int all = __shfl_sync(0xffffffffu, before, 7);
-            int at = seen + before - c;
             const int lo = max(seen, q.y), hi = min(seen + all, q.y + q.z);
             __syncwarp();
-            for (uint32_t a = any; a; a &= a - 1, ++at) {
-              if (at < lo || at >= hi) continue;
-              const int bit = __ffs(a) - 1;
+            for (int k = 0; k < 8; ++k) {  // a lane takes a bit of each word
+              const uint32_t a = __shfl_sync(0xffffffffu, any, k);
+              const int at = seen + __shfl_sync(0xffffffffu, before - c, k) +
+                             __popc(a & ((1u << lane) - 1));
+              if (a == 0) continue;
               int mk = 0;
 #pragma unroll
-              for (int b = 0; b < 8; ++b) mk |= int((bits[b] >> bit) & 1u) << b;
-              list[at - lo] = make_int2(w * 32 + bit, mk);
+              for (int b = 0; b < 8; ++b)
+                mk |= int((__shfl_sync(0xffffffffu, bits[b], k) >> lane) & 1u) << b;
+              if (((a >> lane) & 1u) && at >= lo && at < hi)
+                list[at - lo] = make_int2((w0 + k) * 32 + lane, mk);
             }
             __syncwarp();
             have = max(0, hi - lo);
@@ -673,35 +677,45 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       if (lane == 0) mbar_arrive(item_empty + slot);
       if (f.item < 0) break;
       if (f.steps == 0) continue;
-      if (tk >= 1) ok = warp_wait(kv_empty, (tk - 1) & 1);
+      const int kb2 = tk % NB;
+      if (tk >= NB) ok = warp_wait(kv_empty + kb2, (tk / NB - 1) & 1);
       if (!ok) break;
       ++tk;
-      if (lane == 0) mbar_expect_tx(kv_full, 2 * KB * kPiece);
+      if (lane == 0) mbar_expect_tx(kv_full + kb2, 2 * OP);
       __syncwarp();
       if (lane < 2 * KB)
-        tma_tile3d(sm + (lane & 1 ? M::V : M::K) + (lane >> 1) * kPiece, lane & 1 ? &p.mv : &p.mk,
-                   (lane >> 1) * 64, f.kh, f.kbeg, kv_full);
+        tma_tile3d(sm + (lane & 1 ? M::V : M::K) + kb2 * OP + (lane >> 1) * kPiece,
+                   lane & 1 ? &p.mv : &p.mk, (lane >> 1) * 64, f.kh, f.kbeg, kv_full + kb2);
       for (int st = 0; st < f.steps; ++st, ++gi) {
         const int si = gi % NS;
         ok = warp_wait(box_full + si, (gi / NS) & 1);  // it waited for the stage to be free
         if (!ok) break;
         const Box* box = reinterpret_cast<const Box*>(sm + M::BOX) + si * kNR;
-        int full = 0;  // boxes with pairs: all of them but at an item's end
-        if (p.boxes == 1) {
-          full = box[0].rows > 0;
+        if (p.boxes == 1) {  // uniform operands: a copy is one instruction
+          const int row = uniform(box[0].row), h0 = uniform(box[0].h0);
+          const bool some = uniform(box[0].rows) > 0;
+          if (elect_one()) {
+            mbar_expect_tx(q_full + si, some ? kNR * 256 * KB : 0);
+            for (int kb = 0; kb < KB && some; ++kb) {
+              tma_tile3d(sm + M::Q + si * QP + kb * kQPiece, &p.mq, kb * 64, h0, row, q_full + si);
+              tma_tile3d(sm + M::O + si * QP + kb * kQPiece, &p.mo, kb * 64, h0, row, q_full + si);
+            }
+          }
         } else {
+          int full = 0;  // boxes with pairs: all of them but at an item's end
           for (int j = lane; j < p.boxes; j += 32) full += box[j].rows > 0;
           full = __reduce_add_sync(0xffffffffu, full);
+          if (lane == 0) mbar_expect_tx(q_full + si, uint32_t(full * p.br) * 256 * KB);
+          __syncwarp();
+          for (int e = lane; e < p.boxes * 2 * KB; e += 32) {
+            const int j = e / (2 * KB), o = e & 1, kb = (e >> 1) % KB;
+            const Box x = box[j];
+            if (x.rows > 0)
+              tma_tile3d(sm + (o ? M::O : M::Q) + si * QP + kb * kQPiece + j * p.br * 128,
+                         o ? &p.mo : &p.mq, kb * 64, x.h0, x.row, q_full + si);
+          }
         }
-        if (lane == 0) mbar_expect_tx(q_full + si, uint32_t(full * p.br) * 256 * KB);
         __syncwarp();
-        for (int e = lane; e < p.boxes * 2 * KB; e += 32) {
-          const int j = e / (2 * KB), o = e & 1, kb = (e >> 1) % KB;
-          const Box x = box[j];
-          if (x.rows > 0)
-            tma_tile3d(sm + (o ? M::O : M::Q) + si * QP + kb * kQPiece + j * p.br * 128,
-                       o ? &p.mo : &p.mq, kb * 64, x.h0, x.row, q_full + si);
-        }
 #pragma unroll
         for (int e = 0; e < kNR / 32; ++e) {  // the statistics
           const int c = e * 32 + lane, i = c & (p.br - 1);
@@ -717,7 +731,8 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
     }
     cp_async_wait<0>();
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
-      if (tk > 0) warp_wait(kv_full, (tk - 1) & 1, 200);
+      for (int c = tk - 1; c >= 0 && c >= tk - NB; --c)
+        warp_wait(kv_full + c % NB, (c / NB) & 1, 200);
       for (int c = gi; c > gi - NS && c >= 0; --c) warp_wait(q_full + c % NS, (c / NS) & 1, 200);
     }
   } else if (warp == kKvWarps) {
@@ -738,27 +753,29 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       if (lane == 0) mbar_arrive(item_empty + slot);
       if (it < 0) break;
       if (n <= 0) continue;
-      ok = warp_wait(kv_full, tk & 1);
+      const int kb2 = tk % NB;
+      ok = warp_wait(kv_full + kb2, (tk / NB) & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
-        const int si = gi % NS, x = gi % NG, c = gi - NG;
-        // over p and ds of step gi - NG, whose products have run
+        const int si = gi % NS, x = gi & 1, c = gi - 2;
+        // over p and ds of step gi - 2, whose products have run
         if (c >= 0) ok = warp_wait(q_empty + c % NS, (c / NS) & 1);
         ok = ok && warp_wait(q_full + si, (gi / NS) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_kk<KB>(tm + x * kNR, dK, kPiece, desc_at(dQ, si * QP), kQPiece, IDESC_S);
-          mma_kk<KB>(tm + M::T_DP + x * kNR, dV, kPiece, desc_at(dO, si * QP), kQPiece, IDESC_S);
+          mma_kk<KB>(tm + x * kNR, desc_at(dK, kb2 * OP), kPiece, desc_at(dQ, si * QP), kQPiece,
+                     IDESC_S);
+          mma_kk<KB>(tm + 128 + x * kNR, desc_at(dV, kb2 * OP), kPiece, desc_at(dO, si * QP),
+                     kQPiece, IDESC_S);
           mma_commit(s_full + x);
-          if (i == n - 1) mma_commit(kv_empty);
+          if (i == n - 1) mma_commit(kv_empty + kb2);
         }
         __syncwarp();
       }
       ++tk;
     }
     if (!ok)  // what was issued completes before TMEM is given up
-      for (int c = gi; c >= 0 && c > gi - NG - 1; --c)
-        warp_wait(s_full + c % NG, (c / NG) & 1, 200);
+      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
   } else if (warp == kKvWarps + 3) {
     // ---------------------------------------------------------------- gradients
     constexpr uint32_t IDESC_G = f16_idesc(kT, DP, true);
@@ -774,40 +791,93 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       if (lane == 0) mbar_arrive(item_empty + slot);
       if (it < 0) break;
       if (n <= 0) continue;
-      if (tk >= 1) ok = warp_wait(g_empty, (tk - 1) & 1);
+      const int buf = tk % NB;
+      if (tk >= NB) ok = warp_wait(g_empty + buf, (tk / NB - 1) & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
-        const int si = gi % NS, x = gi % NG;
-        ok = warp_wait(q_full + si, (gi / NS) & 1) && warp_wait(p_full + x, (gi / NG) & 1);
+        const int si = gi % NS, x = gi & 1;
+        ok = warp_wait(q_full + si, (gi / NS) & 1) && warp_wait(p_full + x, (gi >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_tm<kNR>(tm + M::T_ACC, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
-          mma_tm<kNR>(tm + M::T_ACC + DP, tm + M::T_DP + x * kNR, 16, 16, desc_at(dQm, si * QP),
-                      IDESC_G, i > 0);
+          const uint32_t acc = tm + 256 + buf * 2 * DP;
+          mma_tm<kNR>(acc, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
+          mma_tm<kNR>(acc + DP, tm + 128 + x * kNR, 16, 16, desc_at(dQm, si * QP), IDESC_G, i > 0);
           mma_commit(q_empty + si);
-          // (a barrier of its own: a group that has no part in the last steps
-          // would otherwise wait for a phase two ahead, which reads as complete)
-          if (i == n - 1) mma_commit(g_full);
+          if (i == n - 1) mma_commit(g_full + buf);
         }
         __syncwarp();
       }
       ++tk;
     }
     // every product has completed before TMEM is given up
-    if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
+    if (ok && tk > 0) ok = warp_wait(g_full + (tk - 1) % NB, ((tk - 1) / NB) & 1);
     if (!ok)
-      for (int c = gi; c >= 0 && c > gi - NG - 1; --c)
-        warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
+      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
+  } else if (warp >= kKvWarps + 4) {
+    // ---------------------------------------------------------------- output
+    const int quad = warp & 3, r = quad * 32 + lane;  // key
+    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
+    int to = 0;  // items with steps
+    for (int ti = 0;; ++ti) {
+      const int slot = ti & 1, buf = to % NB;
+      ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
+      if (!ok) break;
+      const KvInfo f = info[slot];
+      if (f.item < 0) break;
+      const bool some = f.steps > 0, valid = r < f.n;
+      if (some) {
+        ok = warp_wait(g_full + buf, (to / NB) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const int64_t krow = (int64_t(f.kbeg + r) * g.Hkv + f.kh) * g.D;
+#pragma unroll 1
+      for (int c = 0; c < 2 * DP / 32; ++c) {  // dV, then dK
+        const bool k = c >= DP / 32;
+        const int col = c * 32 - (k ? DP : 0);
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        __syncwarp();
+        if (some) {
+          tmem_ld32(tmem + lanes + 256 + buf * 2 * DP + c * 32, o);
+          tmem_wait_ld();
+        }
+        if (c == 2 * DP / 32 - 1) {  // the buffer is free before the row's end is written
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && some) mbar_arrive(g_empty + buf);
+        }
+        if (valid && f.slot < 0) {
+          const float mul = k ? g.scale : 1.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= mul;
+          store_row(static_cast<__nv_bfloat16*>(k ? p.b.dK : p.b.dV) + krow, col, g.D, o,
+                    k ? wide_k : wide_v);
+        } else if (valid) {
+          float* out = p.b.part + (int64_t(f.slot) * 2 + (k ? 0 : 1)) * kT * g.D +
+                       int64_t(r) * g.D + col;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (col + q * 4 < g.D)
+              *reinterpret_cast<float4*>(out + q * 4) =
+                  make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty + slot);
+      to += some;
+    }
   } else {
     // ---------------------------------------------------------------- p and ds
     const int r = (warp & 3) * 32 + lane, part = (warp >> 2) & 1;  // key, 32 of 64 columns
     const int x = warp >> 3;                                       // group
     const int tid = threadIdx.x & 255;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + M::T_DP;
+    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + 128;
     const int blk = r / g.block;
-    const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
-    int gi = 0, to = 0;  // steps, items with steps
+    int gi = 0;
     for (int ti = 0;; ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
@@ -816,7 +886,7 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       if (f.item < 0) break;
       const int pos = f.pos + r;
       const bool valid = r < f.n;
-      for (int i = (x + NG - gi % NG) % NG; i < f.steps; i += NG) {
+      for (int i = (gi ^ x) & 1; i < f.steps; i += 2) {
         const int c = gi + i, si = c % NS;
         // what the statistics and boxes say, while the scores are on their way
         ok = ok && warp_wait(q_full + si, (c / NS) & 1);
@@ -847,7 +917,7 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
           }
           fence_proxy_async();
         }
-        ok = warp_wait(s_full + x, (c / NG) & 1);
+        ok = warp_wait(s_full + x, (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const float4* stat =
@@ -902,51 +972,8 @@ __global__ void __launch_bounds__(KvSm<DP>::THR, 1) block_dkv_tc(const __grid_co
       }
       if (!ok) break;
       gi += f.steps;
-      if (x >= 2) {  // the third group writes nothing and waits for no result
-        __syncwarp();
-        if (lane == 0) mbar_arrive(item_empty + slot);
-        continue;
-      }
-      const bool some = f.steps > 0;
-      if (some) {
-        ok = warp_wait(g_full, to & 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      // group 0 writes dV, group 1 dK; DP / 2 columns a thread
-      const int64_t krow = (int64_t(f.kbeg + r) * g.Hkv + f.kh) * g.D;
-#pragma unroll 1
-      for (int c = 0; c < DP / 64; ++c) {
-        const int col = part * (DP / 2) + c * 32;
-        float o[32];
-        __syncwarp();
-        if (some) {
-          tmem_ld32(tmem + lanes + M::T_ACC + x * DP + col, o);
-          tmem_wait_ld();
-        }
-        if (valid && f.slot < 0) {
-          const float mul = x ? g.scale : 1.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = some ? o[i] * mul : 0.f;
-          store_row(static_cast<__nv_bfloat16*>(x ? p.b.dK : p.b.dV) + krow, col, g.D, o,
-                    x ? wide_k : wide_v);
-        } else if (valid) {
-          float* out = p.b.part + (int64_t(f.slot) * 2 + (x ? 0 : 1)) * kT * g.D +
-                       int64_t(r) * g.D + col;
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (col + q * 4 < g.D)
-              *reinterpret_cast<float4*>(out + q * 4) =
-                  make_float4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
-        }
-      }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (some) mbar_arrive(g_empty);
-        mbar_arrive(item_empty + slot);
-      }
-      to += some;
+      if (lane == 0) mbar_arrive(item_empty + slot);
     }
   }
   if (!ok) atomicOr(&g_err, 2);
@@ -1009,8 +1036,8 @@ gattn_status launch_block_bwd_tc(const BlockBwdParams& b, cudaStream_t st) {
         !encode_heads_map(&p.mv, V, g.Nk, g.Hkv, g.D, 1, kT))
       return GATTN_ERR_CUDA;
     const unsigned grid = unsigned(std::min<int64_t>(b.max_items, sm_count()));
-    s = g.D <= 64 ? go(block_dkv_tc<64>, grid, KvSm<64>::THR, KvSm<64>::BYTES, p)
-                  : go(block_dkv_tc<128>, grid, KvSm<128>::THR, KvSm<128>::BYTES, p);
+    s = g.D <= 64 ? go(block_dkv_tc<64>, grid, kKvThr, KvSm<64>::BYTES, p)
+                  : go(block_dkv_tc<128>, grid, kKvThr, KvSm<128>::BYTES, p);
   }
   return s;
 }
