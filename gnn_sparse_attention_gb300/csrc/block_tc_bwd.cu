@@ -32,7 +32,7 @@
 //   its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   234 us, dK and dV 438 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   234 us, dK and dV 420 us; two causal sequences of 8,191, 16 heads of 128 on 4:
 //   174 and 300 us.  A unit seldom chose all blocks of a key tile: with blocks of
 //   64 and one choice in three, 1.6 times the useful products run (1.9 with one
 //   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
@@ -479,7 +479,10 @@ template <int DP>
 struct KvSm {
   static constexpr int KB = DP / 64;
   static constexpr int NS = DP == 64 ? 6 : 4;  // Q and dO stages
-  static constexpr int NB = DP == 64 ? 2 : 1;  // K and V buffers, dK and dV buffers (items in turn)
+  static constexpr int NB = DP == 64 ? 2 : 1;  // K and V buffers (items in turn)
+  // p and ds beside S^T and dP^T, where TMEM has room: the scores of a group's next
+  // step are then computed while it forms these (64k nodes: 438 -> 420 us)
+  static constexpr bool SEP = DP == 64;
   static_assert(NS % 2 == 0, "a stage belongs to one group, which waits for each of its phases");
   static constexpr int OP = KB * kPiece, QP = KB * kQPiece;
   static constexpr int K = 0;
@@ -491,12 +494,15 @@ struct KvSm {
   static constexpr int LIST = BOX + NS * kNR * int(sizeof(Box));
   static constexpr int INFO = LIST + kList * 8;
   static constexpr int BAR = (INFO + 2 * int(sizeof(KvInfo)) + 7) / 8 * 8;
-  static constexpr int NBAR = 4 + 2 * NB + 3 * NS + 4 + 2 * NB;
+  static constexpr int NBAR = 4 + 2 * NB + 3 * NS + 6 + 2;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
-  // TMEM: S^T [0, 128) and dP^T [128, 256) of the groups, then (dV, dK) of each buffer
-  static_assert(256 + NB * 2 * DP <= 512, "TMEM columns");
+  // TMEM: S^T [0, 128) and dP^T [128, 256) of the groups; p and ds; dV, dK.  16 queries
+  // of p take P16 columns (8, or 16 where they overwrite scores).
+  static constexpr int T_P = SEP ? 256 : 0, T_DS = SEP ? 320 : 128, P16 = SEP ? 8 : 16;
+  static constexpr int T_ACC = SEP ? 384 : 256;
+  static_assert(T_ACC + 2 * DP <= 512, "TMEM columns");
 };
 
 // arrive once this thread's cp.async copies so far have landed
@@ -517,8 +523,8 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + M::BAR);
   uint64_t *item_full = bar, *item_empty = item_full + 2, *kv_full = item_empty + 2,
            *kv_empty = kv_full + NB, *q_full = kv_empty + NB, *q_empty = q_full + NS,
-           *box_full = q_empty + NS, *s_full = box_full + NS, *p_full = s_full + 2,
-           *g_full = p_full + 2, *g_empty = g_full + NB;
+           *box_full = q_empty + NS, *s_full = box_full + NS, *s_empty = s_full + 2,
+           *p_full = s_empty + 2, *g_full = p_full + 2, *g_empty = g_full + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   KvInfo* info = reinterpret_cast<KvInfo*>(sm + M::INFO);
   int2* list = reinterpret_cast<int2*>(sm + M::LIST);
@@ -530,11 +536,12 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       mbar_init(item_full + i, 1);
       mbar_init(item_empty + i, kKvWarps + kKvOut + 3);
       mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 8);
       mbar_init(p_full + i, 8);
     }
+    mbar_init(g_full, 1);
+    mbar_init(g_empty, kKvOut);
     for (int i = 0; i < NB; ++i) {
-      mbar_init(g_full + i, 1);
-      mbar_init(g_empty + i, kKvOut);
       mbar_init(kv_full + i, 1);
       mbar_init(kv_empty + i, 1);
     }
@@ -757,8 +764,11 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       ok = warp_wait(kv_full + kb2, (tk / NB) & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
         const int si = gi % NS, x = gi & 1, c = gi - 2;
-        // over p and ds of step gi - 2, whose products have run
-        if (c >= 0) ok = warp_wait(q_empty + c % NS, (c / NS) & 1);
+        // over the scores of step gi - 2, which have been read, or p and ds of it,
+        // whose products have run
+        if (c >= 0)
+          ok = M::SEP ? warp_wait(s_empty + x, (c >> 1) & 1)
+                      : warp_wait(q_empty + c % NS, (c / NS) & 1);
         ok = ok && warp_wait(q_full + si, (gi / NS) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -791,26 +801,27 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       if (lane == 0) mbar_arrive(item_empty + slot);
       if (it < 0) break;
       if (n <= 0) continue;
-      const int buf = tk % NB;
-      if (tk >= NB) ok = warp_wait(g_empty + buf, (tk / NB - 1) & 1);
+      if (tk >= 1) ok = warp_wait(g_empty, (tk - 1) & 1);
       for (int i = 0; i < n && ok; ++i, ++gi) {
         const int si = gi % NS, x = gi & 1;
         ok = warp_wait(q_full + si, (gi / NS) & 1) && warp_wait(p_full + x, (gi >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t acc = tm + 256 + buf * 2 * DP;
-          mma_tm<kNR>(acc, tm + x * kNR, 16, 16, desc_at(dOm, si * QP), IDESC_G, i > 0);
-          mma_tm<kNR>(acc + DP, tm + 128 + x * kNR, 16, 16, desc_at(dQm, si * QP), IDESC_G, i > 0);
+          const uint32_t pt = tm + x * (4 * M::P16);
+          mma_tm<kNR>(tm + M::T_ACC, pt + M::T_P, 16, M::P16, desc_at(dOm, si * QP), IDESC_G,
+                      i > 0);
+          mma_tm<kNR>(tm + M::T_ACC + DP, pt + M::T_DS, 16, M::P16, desc_at(dQm, si * QP), IDESC_G,
+                      i > 0);
           mma_commit(q_empty + si);
-          if (i == n - 1) mma_commit(g_full + buf);
+          if (i == n - 1) mma_commit(g_full);
         }
         __syncwarp();
       }
       ++tk;
     }
     // every product has completed before TMEM is given up
-    if (ok && tk > 0) ok = warp_wait(g_full + (tk - 1) % NB, ((tk - 1) / NB) & 1);
+    if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
     if (!ok)
       for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
   } else if (warp >= kKvWarps + 4) {
@@ -820,14 +831,14 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     const bool wide_k = wide_rows(p.b.dK, g.D), wide_v = wide_rows(p.b.dV, g.D);
     int to = 0;  // items with steps
     for (int ti = 0;; ++ti) {
-      const int slot = ti & 1, buf = to % NB;
+      const int slot = ti & 1;
       ok = ok && warp_wait(item_full + slot, (ti >> 1) & 1);
       if (!ok) break;
       const KvInfo f = info[slot];
       if (f.item < 0) break;
       const bool some = f.steps > 0, valid = r < f.n;
       if (some) {
-        ok = warp_wait(g_full + buf, (to / NB) & 1);
+        ok = warp_wait(g_full, to & 1);
         if (!ok) break;
         tc_fence_after();
       }
@@ -841,13 +852,13 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
         __syncwarp();
         if (some) {
-          tmem_ld32(tmem + lanes + 256 + buf * 2 * DP + c * 32, o);
+          tmem_ld32(tmem + lanes + M::T_ACC + c * 32, o);
           tmem_wait_ld();
         }
         if (c == 2 * DP / 32 - 1) {  // the buffer is free before the row's end is written
           tc_fence_before();
           __syncwarp();
-          if (lane == 0 && some) mbar_arrive(g_empty + buf);
+          if (lane == 0 && some) mbar_arrive(g_empty);
         }
         if (valid && f.slot < 0) {
           const float mul = k ? g.scale : 1.f;
@@ -875,7 +886,9 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     const int x = warp >> 3;                                       // group
     const int tid = threadIdx.x & 255;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tP = tS + 128;
+    const uint32_t tS = tmem + lanes + x * kNR + part * 32, tD = tS + 128;
+    const uint32_t wP = tmem + lanes + (x * 4 + part * 2) * M::P16 + M::T_P,
+                   wS = wP - M::T_P + M::T_DS;
     const int blk = r / g.block;
     int gi = 0;
     for (int ti = 0;; ++ti) {
@@ -928,8 +941,13 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
           for (int h = 0; h < 2; ++h) {  // 16 columns
             float sv[16], dv[16], wp[8], wd[8];
             tmem_ld16(tS + h * 16, sv);
-            tmem_ld16(tP + h * 16, dv);
+            tmem_ld16(tD + h * 16, dv);
             tmem_wait_ld();
+            if (M::SEP && h == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(s_empty + x);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 a = stat[h * 8 + j];  // (lse, Delta) of columns 2 j, 2 j + 1
@@ -949,10 +967,15 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
               wp[j] = __uint_as_float(bf16x2_bits(y.x, y.y));
               wd[j] = __uint_as_float(bf16x2_bits(ds.x, ds.y));
             }
-            tmem_st8(tS + h * 16, wp);
-            tmem_st8(tP + h * 16, wd);
+            tmem_st8(wP + h * M::P16, wp);
+            tmem_st8(wS + h * M::P16, wd);
           }
         };
+        if (M::SEP && c >= 2) {  // the products with the group's last p and ds have run
+          ok = warp_wait(q_empty + (c - 2) % NS, ((c - 2) / NS) & 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (__all_sync(0xffffffffu, see == 0xffffffffu)) {
           form(std::true_type{});
         } else if (__any_sync(0xffffffffu, see)) {
@@ -961,9 +984,10 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
           const float none[8] = {};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            tmem_st8(tS + h * 16, none);
-            tmem_st8(tP + h * 16, none);
+            tmem_st8(wP + h * M::P16, none);
+            tmem_st8(wS + h * M::P16, none);
           }
+          if (M::SEP && lane == 0) mbar_arrive(s_empty + x);
         }
         tmem_wait_st();
         tc_fence_before();
