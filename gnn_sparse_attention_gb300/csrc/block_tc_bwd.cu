@@ -32,8 +32,8 @@
 //   its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
-//   234 us, dK and dV 420 us; two causal sequences of 8,191, 16 heads of 128 on 4:
-//   174 and 300 us.  A unit seldom chose all blocks of a key tile: with blocks of
+//   233 us, dK and dV 402 us; two causal sequences of 8,191, 16 heads of 128 on 4:
+//   173 and 300 us.  A unit seldom chose all blocks of a key tile: with blocks of
 //   64 and one choice in three, 1.6 times the useful products run (1.9 with one
 //   in eight).  Tiles of 64 keys would run at half the tensor cores' rate.
 //
@@ -478,7 +478,7 @@ struct KvInfo {
 template <int DP>
 struct KvSm {
   static constexpr int KB = DP / 64;
-  static constexpr int NS = DP == 64 ? 6 : 4;  // Q and dO stages
+  static constexpr int NS = DP == 64 ? 8 : 4;  // Q and dO stages (64k nodes, 6: 420 us)
   static constexpr int NB = DP == 64 ? 2 : 1;  // K and V buffers (items in turn)
   // p and ds beside S^T and dP^T, where TMEM has room: the scores of a group's next
   // step are then computed while it forms these (64k nodes: 438 -> 420 us)
