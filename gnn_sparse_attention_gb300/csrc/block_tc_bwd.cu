@@ -20,16 +20,16 @@
 //   chose one of its blocks (block_api.cu builds the items), walked in steps
 //   of 64 (query row, head) pairs,
 //     S^T = K Q^T, dP^T = V dO^T                       -> TMEM, two buffers
-//     p, ds as bf16                                    -> TMEM, over S^T and dP^T
+//     p, ds as bf16                 -> TMEM, over S^T and dP^T (D <= 64: beside them)
 //     dV += p dO, dK += ds Q                           -> TMEM
 //   64 rather than 128 queries a step leave room for several stages of Q and
 //   dO and a second score buffer next to the two accumulators; two groups of
 //   eight warps take the steps in turn, so that one forms p and ds while the other
 //   waits for its products.  (A third group at D <= 64 left 72 registers a thread:
 //   its spills filled what shared memory leaves of L1, 532 us against 471.)  Four
-//   more warps write a finished item.  Units of fewer than 64 pairs share a step, each in a box of its own; a box
-//   knows which of the tile's blocks its unit chose.  A key is a TMEM lane, so
-//   its mask within a box is a range of columns.
+//   more warps write a finished item.  Units of fewer than 64 pairs share a step,
+//   each in a box of its own; a box knows which of the tile's blocks its unit
+//   chose.  A key is a TMEM lane, so its mask within a box is a range of columns.
 //
 //   Measured (as the forward's cases): 24 graphs of 2,731 nodes, 8 heads of 64: dQ
 //   233 us, dK and dV 402 us; two causal sequences of 8,191, 16 heads of 128 on 4:

@@ -45,8 +45,9 @@
 // of 8,191, 16 heads of 128 on 4, 16 blocks: 120 us, 1.04; 24 graphs of 2,731
 // nodes, 8 heads of 64, 16 blocks: 187 us, 0.75; 128 tokens against caches of 8,000
 // (32 heads on 8): 167 us, 6.4 TB/s.  What bounds the first three is the
-// softmax's latency: two streams keep the tensor cores 60% busy, and TMEM has no
-// room for a third or for a second score buffer of each.
+// softmax's latency: two streams keep the tensor cores busy half of the time (a
+// third at D = 64), and TMEM has no room for a third or, at D = 128, for a second
+// score buffer of each.
 #include <algorithm>
 
 #include "attn_launch.cuh"
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
         const float mq = m == neg_inf() ? 0.f : m * g.qmul;
         const int end = (st + 1) * kT;
         const bool tail = total < end, mixed = least < min(total, end);
-        if ((tail || mixed) && (!PAIR || x == 0)) {  // (the other stream's P V comes after this one's)
+        if ((tail || mixed) && (!PAIR || x == 0)) {  // (the other stream's P V comes after)
           const int kv = PAIR ? c >> 1 : c, si = kv % NV;
           ok = warp_wait(v_full + si, (kv / NV) & 1);
           if (!ok) break;
@@ -698,7 +699,8 @@ Shape shape(const BlockGeom& g) {
   // One step a split at least; never more CTAs than SMs (a second round of
   // one CTA costs as much as the first).
   const int64_t steps = (int64_t(g.topk) * g.block + kT - 1) / kT;
-  s.nsplit = int(std::max<int64_t>(1, std::min<int64_t>(steps, sm_count() / std::max<int64_t>(1, s.tiles))));
+  const int64_t fit = sm_count() / std::max<int64_t>(1, s.tiles);
+  s.nsplit = int(std::max<int64_t>(1, std::min(steps, fit)));
   return s;
 }
 
