@@ -63,6 +63,8 @@ __device__ __forceinline__ int64_t stage(float* dst, const float* src, int D, F 
                  : "memory");
   return o;
 }
+// Closes the group of the copies so far.  landed() waits for closed groups alone, so
+// every path from a stage() to a landed() passes one, those that take no step too.
 __device__ __forceinline__ void staged() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void landed() {  // all groups but the last N
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(kThr, kBufs<DQ>) block_fwd_simt(const FwdP p) 
     staged();
   };
   stage(sQ, p.Q, D, [&](int r) { return q_off(g, un, kh, r0 + r); });
+  staged();
   if (NB == 2) fetch(0, 0);
   float m[4], l[4], o[4 * N][4];
 #pragma unroll
@@ -308,6 +311,7 @@ __global__ void __launch_bounds__(kThr, kBufs<DQ>) block_dq_simt(const BlockBwdP
   const auto qo = [&](int r) { return q_off(g, un, kh, r0 + r); };
   stage(sQ, static_cast<const float*>(p.Q), D, qo);
   stage(sO, static_cast<const float*>(p.dO), D, qo);
+  staged();
   if (NB == 2) fetch(0, 0);
   for (int k0 = 0, buf = 0; k0 < total; k0 += kC, buf = NB - 1 - buf) {
     if (k0) __syncthreads();  // the buffer has been read
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kThr, kBufs<DQ>) block_dkv_simt(const BlockBwd
     __syncthreads();
     stage(sK, static_cast<const float*>(p.K), D, ko);
     stage(sV, static_cast<const float*>(p.V), D, ko);
+    staged();
     int blk[4];  // block of this thread's keys within the tile
 #pragma unroll
     for (int j = 0; j < 4; ++j) blk[j] = (half * kC + tx + 16 * j) / g.block;
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kThr, kBufs<DQ>) block_dkv_simt(const BlockBwd
         weighted<DQ, true, false>(sS, sQ + buf * kR * ld, D, gk);
       }
     }
-    landed<0>();  // an item without units has not waited for K and V
+    landed<0>();  // an item without units has not waited for K and V, which the next overwrites
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = ty * 4 + i;

@@ -492,3 +492,24 @@ def test_offsets_outside_the_tensors_stay_inside():
         torch.cuda.synchronize()
     assert (big[:N] == 7.0).all() and (big[2 * N:] == 7.0).all()
     assert (idx[..., 1] == 1000000).all()
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 64), ("bf16", 128)])
+def test_key_tiles_that_nobody_chose_between_others(dtype, D):
+    """Most key tiles are in no list, so a CTA's work items are empty and not empty in turn, over
+    several rounds: an empty item leaves nothing to the next one, and calls repeat bit by bit."""
+    lens = [512 + 37 * (i % 3) for i in range(260)]
+    sq = ref.offsets(lens)
+    g = torch.Generator().manual_seed(21)
+    idx = torch.randint(0, 16, (ref.units(sq[-1], len(lens), 128), 1, 1), generator=g, dtype=torch.int32)
+    for s, n in enumerate(lens):  # (units behind a sequence's end belong to nothing)
+        row = ref.table_row(sq[s], s, 128)
+        idx[row + 1:row + -(-n // 128)] = idx[row]
+    idx = idx.to(DEV)
+    Q, K, V, _, out, lse, first = run(160, lens, lens, 1, 1, D, dtype, 32, 128, 1, idx=idx)
+    G = randn(169, *Q.shape, dtype=DT[dtype])  # the dout of run()
+    off = i32(sq)
+    for _ in range(10):
+        again = gb.gattn_block_bwd(Q, K, V, idx, off, off, out, G, lse, 32, 128)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    gb.gattn_block_check_errors()
