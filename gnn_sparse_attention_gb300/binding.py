@@ -555,6 +555,11 @@ def gattn_fwd_noalloc(plan: Plan, Q, K, V, score: Score, out, lse, stream=None):
 # These calls may take a few microseconds on the GPU (one new token), so their
 # marshalling is lean: descriptors are packed bytes, pointers plain integers,
 # and workspace sizes are kept by shape.
+#
+# `stream` (the current one by default) is where a call runs.  What the call
+# allocates, workspaces too, comes from that stream's memory; as everywhere in
+# torch, the caller has its tensors ready there, keeps them until the call is
+# done, and waits for it before another stream reads the results.
 _BLOCK_PACK = struct.Struct("@11ifi4xPPPqq")   # _BlockDesc
 _NORM_PACK = struct.Struct("@qiiiiffPPPP")     # _NormDesc
 assert _BLOCK_PACK.size == ctypes.sizeof(_BlockDesc)
@@ -582,7 +587,7 @@ def _at(t):
 
 
 def _stream_of(dev, stream):
-    """(handle, stream to tie allocations to or None) of a call on device number dev."""
+    """(handle, the stream where it is not the current one) of a call on device number dev."""
     handle = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None:
         return handle, None
@@ -592,18 +597,22 @@ def _stream_of(dev, stream):
 
 
 def _new(dev, other, shape, dtype):
-    """A tensor that the call allocates, tied to the stream it runs on."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if other is not None:
-        t.record_stream(other)
+    """A tensor that the call allocates and returns.
+
+    With another stream it comes from that stream's memory: memory of the current one may still
+    be in use there by work that was queued before.  The current stream, where the caller goes
+    on with it, is recorded for its release.
+    """
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
 def _like(t, other):
-    r = torch.empty_like(t)
-    if other is not None:
-        r.record_stream(other)
-    return r
+    return torch.empty_like(t) if other is None else _new(t.device, other, t.shape, t.dtype)
 
 
 def _workspace(given, dev, other, fn, desc, key):
@@ -620,7 +629,12 @@ def _workspace(given, dev, other, fn, desc, key):
         if len(_sizes) > 4096:
             _sizes.clear()
         _sizes[(fn, dev, key)] = n
-    return _new(dev, other, (n,), torch.uint8) if n else None
+    if not n:
+        return None
+    if other is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(other):  # used there alone
+        return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
 def _bytes(t):

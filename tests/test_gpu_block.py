@@ -450,6 +450,52 @@ def test_another_stream_and_shared_inputs():
         assert all(torch.equal(x, y) for x, y in zip(r, (*a, *ga)))
 
 
+def test_another_stream_allocates_for_itself():
+    """Memory that the caller has released, but that work queued on the current stream still
+    uses, is not handed to a call on another stream: neither for results nor for workspaces."""
+    N, F, sq = 600, 256, [0, 600]
+    off, one = i32(sq), i32([0, 1])
+    Q, K, V, G = (randn(170 + i, N, 4, 64, dtype=torch.bfloat16) for i in range(4))
+    idx = random_idx(7, sq, [N], 64, 4, 4, 64)
+    x, res, dh = (randn(175 + i, N, F) for i in range(3))
+    w = torch.ones(F, device=DEV)
+    out, lse = gb.gattn_block_fwd(Q, K, V, idx, off, off, 64, 64)
+    sums = gb.gattn_block_sums(K, off, 64)
+    _, _, stats = gb.gattn_norm_fwd(res, x, w_post=w, w_pre=w)
+    token = torch.zeros(1, 4, 2, dtype=torch.int32, device=DEV)
+    calls = [
+        lambda st: [gb.gattn_block_sums(K, off, 64, stream=st)],
+        lambda st: [gb.gattn_block_select(Q, sums, off, off, 4, 64, 64, N, stream=st)],
+        lambda st: gb.gattn_block_fwd(Q, K, V, idx, off, off, 64, 64, stream=st),
+        lambda st: gb.gattn_block_fwd(Q[:1], K, V, token, one, off, 64, 1, stream=st),
+        lambda st: gb.gattn_block_bwd(Q, K, V, idx, off, off, out, G, lse, 64, 64, stream=st),
+        lambda st: gb.gattn_norm_fwd(res, x, w_post=w, w_pre=w, stream=st),
+        lambda st: [t for t in gb.gattn_norm_bwd(res, stats, dh, x, x, w_post=w, w_pre=w,
+                                                 stream=st).values() if t is not None],
+    ]
+    side = torch.cuda.Stream()
+    for n, call in enumerate(calls):
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        # blocks of every size up to 64 MiB, in use by a copy behind a pause of a tenth of a second
+        held = [torch.full((1 << b,), 3, dtype=torch.uint8, device=DEV)
+                for b in range(9, 27) for _ in range(4)]
+        spans = [(t.data_ptr(), t.numel()) for t in held]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)
+        copies = [t.clone() for t in held]
+        del held
+        got = call(side)
+        side.synchronize()
+        for t in got:
+            a, e = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+            assert all(e <= p or a >= p + size for p, size in spans), n
+        torch.cuda.synchronize()
+        assert all((c == 3).all() for c in copies), n
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), n
+
+
 def test_backward_in_a_graph():
     sq = i32([0, 200, 333])
     Q, K, V, G = (randn(120 + i, 333, 2, 64, dtype=torch.bfloat16) for i in range(4))
