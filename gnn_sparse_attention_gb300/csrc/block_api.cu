@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "attn_launch.cuh"
+#include "block_items.cuh"
 #include "block_tc.cuh"
 
 namespace gattn {
@@ -138,6 +139,8 @@ gattn_status check_ptrs(const char* what, std::initializer_list<const void*> lis
 // --------------------------------------------------------------------------
 // backward: workspace and preparation
 // --------------------------------------------------------------------------
+constexpr int64_t kMaxItems = INT32_MAX - 65536;  // every CTA counts one item past the last
+
 BlockBwdWs bwd_ws(const BlockGeom& g, bool f32) {
   BlockBwdWs w{};
   w.words = (g.U + 31) / 32;
@@ -151,8 +154,7 @@ BlockBwdWs bwd_ws(const BlockGeom& g, bool f32) {
       std::max<int64_t>(1, int64_t(f32 ? 1 : 32) * kBlkTile / std::max(rows, kBlkTile));
   const int64_t per = (entries + int64_t(sm_count()) * 4 - 1) / (int64_t(sm_count()) * 4);
   w.chunk = int(std::min<int64_t>(std::max(least, per), INT32_MAX));
-  // a tile of c > chunk units has ceil(c / chunk) <= 2 c / chunk items
-  w.slots = entries / w.chunk * 2 + 2;
+  w.slots = item_slots(entries, w.chunk);
   w.max_items = int64_t(g.KT) * g.Hkv + w.slots;
   size_t o = 0;
   w.stat = o;
@@ -247,13 +249,12 @@ __global__ void __launch_bounds__(256) count_kernel(const BlockBwdParams p) {
 // one CTA: item and slot numbers by a scan over the key tiles, and the items
 __global__ void __launch_bounds__(1024) items_kernel(const BlockBwdParams p, int64_t slots) {
   __shared__ int2 sh[32];
-  __shared__ int2 base;
+  __shared__ longlong2 base;
   const int n = p.g.KT * p.g.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) base = make_int2(0, 0);
+  if (threadIdx.x == 0) base = make_longlong2(0, 0);
   for (int i0 = 0; i0 < n; i0 += 1024) {
     const int i = i0 + threadIdx.x;
-    const int c = i < n ? p.cnt[2 * i] : -1;
-    const int k = c < 0 ? 0 : max(1, (c + p.chunk - 1) / p.chunk);  // items
+    const int k = i < n ? tile_items(p.cnt[2 * i], p.chunk) : 0;
     int2 v = make_int2(k, k > 1 ? k : 0), x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -266,25 +267,19 @@ __global__ void __launch_bounds__(1024) items_kernel(const BlockBwdParams p, int
     __syncthreads();  // the previous round's reads of sh and base are done
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    int2 before = base;
+    longlong2 before = base;
     for (int w = 0; w < warp; ++w) {
       before.x += sh[w].x;
       before.y += sh[w].y;
     }
-    const int item = before.x + x.x - v.x, slot = before.y + x.y - v.y;
-    if (k > 0) {
-      p.cnt[2 * i + 1] = k > 1 ? slot : -1;
-      for (int j = 0; j < k; ++j)
-        if (item + j < p.max_items && (k == 1 || slot + j < slots))
-          p.items[item + j] = make_int4(i, j * p.chunk, min(p.chunk, c - j * p.chunk),
-                                        k > 1 ? slot + j : -1);
-    }
+    put_items(i, k, before.x + x.x - v.x, before.y + x.y - v.y, p.chunk, slots, p.max_items,
+              p.cnt + 2 * i, p.items);
     __syncthreads();
-    if (threadIdx.x == 1023) base = make_int2(before.x + x.x, before.y + x.y);
+    if (threadIdx.x == 1023) base = make_longlong2(before.x + x.x, before.y + x.y);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    p.head[0] = int(min(int64_t(base.x), p.max_items));
+    p.head[0] = int(min(static_cast<long long>(base.x), static_cast<long long>(p.max_items)));
     p.head[1] = 0;
   }
 }
@@ -453,7 +448,9 @@ gattn_status gattn_block_bwd_workspace_size(const gattn_block_desc* desc, size_t
   const gattn_status s = geom(desc, &g);
   if (s != GATTN_OK) return s;
   BLOCK_REQUIRE(bytes, GATTN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = bwd_ws(g, desc->dtype == GATTN_F32).total;
+  const BlockBwdWs w = bwd_ws(g, desc->dtype == GATTN_F32);
+  BLOCK_REQUIRE(w.max_items < kMaxItems, GATTN_ERR_UNSUPPORTED, "too many rows");
+  *bytes = w.total;
   return GATTN_OK;
 }
 
@@ -466,6 +463,7 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   if (s != GATTN_OK) return s;
   if (g.S == 0 || (g.Nq == 0 && g.Nk == 0)) return GATTN_OK;
   const BlockBwdWs w = bwd_ws(g, desc->dtype == GATTN_F32);
+  BLOCK_REQUIRE(w.max_items < kMaxItems, GATTN_ERR_UNSUPPORTED, "too many rows");
   if ((g.Nq > 0 && (s = check_ptrs("gattn_block_bwd", {Q, out, dout, dQ})) != GATTN_OK) ||
       (g.Nk > 0 && (s = check_ptrs("gattn_block_bwd", {K, V, dK, dV})) != GATTN_OK) ||
       (s = check_ws("gattn_block_bwd", workspace, workspace_bytes, w.total)) != GATTN_OK)

@@ -1,5 +1,6 @@
 """Block selection and block attention on the GPU against their definition in
 64 bits (tests/block_ref.py states the bounds)."""
+import ctypes
 import math
 
 import pytest
@@ -559,3 +560,31 @@ def test_key_tiles_that_nobody_chose_between_others(dtype, D):
         again = gb.gattn_block_bwd(Q, K, V, idx, off, off, out, G, lse, 32, 128)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
     gb.gattn_block_check_errors()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [9, 17, 40])
+def test_offsets_out_of_order_that_want_more_items_than_there_are(S, dtype):
+    """Offsets 0, N, 0, N, ...: tiles share blocks, and their work items would not fit the
+    workspace.  Nothing outside the outputs and the workspace is written, and an ordinary call is
+    right afterwards."""
+    N, H, qb, block = 4096, 1, 16, 16
+    Q, K, V, G = (randn(180 + i, N, H, 64, dtype=DT[dtype]) for i in range(4))
+    off = i32([0 if i % 2 == 0 else N for i in range(S + 1)])
+    units = gb.gattn_block_units(N, S, qb)
+    idx = torch.zeros(units, 1, 1, dtype=torch.int32, device=DEV)
+    lse = torch.zeros(N, H, device=DEV)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    desc, size = gb._block_attn(Q, K, V, idx, off, off, block, qb, 0.0, False, None)[1], ctypes.c_size_t()
+    assert gb.load_library().gattn_block_bwd_workspace_size(desc, ctypes.byref(size)) == 0
+    need = size.value
+    ws[need:] = 7
+    big = torch.full((5, N, H, 64), 7.0, device=DEV, dtype=DT[dtype])
+    for _ in range(3):
+        gb.gattn_block_bwd(Q, K, V, idx, off, off, Q, G, lse, block, qb, dQ=big[1], dK=big[2], dV=big[3],
+                           workspace=ws[:need])
+    torch.cuda.synchronize()
+    gb.gattn_block_check_errors()
+    assert (ws[need:] == 7).all() and (big[0] == 7.0).all() and (big[4] == 7.0).all()
+    run(185, [N], [N], H, H, 64, dtype, block, qb, 1,
+        idx=torch.zeros(ref.units(N, 1, qb), 1, 1, dtype=torch.int32, device=DEV))
