@@ -9,7 +9,9 @@
 // Scores run in fp32 FMAs with an error bound
 //   |score - exact| <= e = (D + 32) 2^-23 |q| max|k / n|   (Cauchy-Schwarz),
 // a radix select finds the topk-th score T, blocks above T + 2e are in, below
-// T - 2e out, and only blocks in between are scored again in fp64.
+// T - 2e out, and only blocks in between are scored again in fp64.  Where the
+// norms leave the range in which that bound holds, all are.  Which blocks the
+// causal mask leaves, and which of them come first, follows from positions alone.
 //
 // Measured: sums over 65,536 nodes of 8 heads of 64 (bf16) 19.5 us, 3.4 TB/s, with
 // issue slots half busy with the exact additions; the choice of 16 of 43 blocks for
@@ -183,16 +185,15 @@ __device__ __forceinline__ float trunc32(double x) {
   return __uint_as_float(m | (hi & 0x80000000u));
 }
 
-__device__ __forceinline__ uint32_t order_key(float x) {  // larger score, larger key; NaN lowest
-  if (!(x > neg_inf())) return 0u;
+__device__ __forceinline__ uint32_t order_key(float x) {  // larger score, larger key (finite x)
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are one score
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float key_score(uint32_t k) {
-  return k == 0u ? neg_inf() : __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// The k-th largest of n keys (k <= number of nonzero keys), by one warp; hist: 256 words.
+// The k-th largest of n keys (1 <= k <= n), by one warp; hist: 256 words.
 __device__ uint32_t kth_key(const double* sc, int n, int k, uint32_t* hist) {
   const int lane = threadIdx.x & 31;
   uint32_t prefix = 0, mask = 0;
@@ -312,25 +313,13 @@ __global__ void __launch_bounds__(kThr, 4) select_kernel(const SelParams p) {
         for (int j = 0; j < UT; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
       }
       if (in) {
-        const int kp = b * g.block;
-        const float inv = 1.f / float(min(g.block, ks.len - kp));
+        const float inv = 1.f / float(min(g.block, ks.len - b * g.block));
         big = fmaxf(big, nn * inv * inv);
         if (nn != nn) big = __int_as_float(0x7f800000);
-        if (sub == 0) {
+        if (sub == 0)
 #pragma unroll
-          for (int j = 0; j < UT; ++j) {
-            const int64_t off = int64_t(ub + j - first_unit) * g.qb;
-            float v = acc[j] * inv;
-            if (g.causal) {
-              const int64_t lo = off + ks.len - qs.len;
-              const int64_t hi = min(off + g.qb, int64_t(qs.len)) + ks.len - qs.len - 1;
-              if (kp + g.block > lo) v = -neg_inf();
-              if (kp > hi) v = neg_inf();
-            }
-            if (j >= cnt || off < 0 || off >= qs.len) v = neg_inf();
-            reinterpret_cast<float*>(sc + j * p.cap + b)[0] = v;
-          }
-        }
+          for (int j = 0; j < UT; ++j)
+            reinterpret_cast<float*>(sc + j * p.cap + b)[0] = acc[j] * inv;
       }
     }
 #pragma unroll
@@ -341,111 +330,107 @@ __global__ void __launch_bounds__(kThr, 4) select_kernel(const SelParams p) {
     // one warp per unit
     for (int j = warp; j < cnt; j += kThr / 32) {
       double* s = sc + j * p.cap;
-      int valid = 0;
-      for (int i = lane; i < nb; i += 32)
-        valid += order_key(reinterpret_cast<const float*>(s + i)[0]) != 0u;
-      valid = __reduce_add_sync(0xffffffffu, valid);
-      const int k = min(g.topk, valid);
       int32_t* out = p.idx + (int64_t(ub + j) * g.Hkv + kh) * g.topk;
-      float lo = neg_inf(), hi = neg_inf();  // below lo: out; above hi: in; between: by fp64
-      if (valid > k) {
-        const float kth = key_score(kth_key(s, nb, k, hist + j * 256));
-        float qn = 0.f, kn = 0.f;
-        for (int d = lane; d < D; d += 32) qn = fmaf(q32[j * D + d], q32[j * D + d], qn);
+      // blocks [0, far) compete; [far, end) reach the unit's own positions and come first
+      const int64_t off = int64_t(ub + j - first_unit) * g.qb;
+      int end = off >= 0 && off < qs.len ? nb : 0, far = end;
+      if (g.causal && end > 0) {
+        const int64_t first = off + ks.len - qs.len;
+        const int64_t last = min(off + g.qb, int64_t(qs.len)) + ks.len - qs.len - 1;
+        end = last < 0 ? 0 : int(min(int64_t(end), last / g.block + 1));
+        far = first < 0 ? 0 : int(min(int64_t(end), first / g.block));
+      }
+      end = min(end, far + g.topk);
+      const int k = min(g.topk - (end - far), far);  // of those that compete
+      float qn = 0.f, kn = 0.f;  // |q|^2, largest |k|^2 / n^2
+      for (int d = lane; d < D; d += 32) qn = fmaf(q32[j * D + d], q32[j * D + d], qn);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, o);
+      for (int o = 16; o > 0; o >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, o);
 #pragma unroll
-        for (int w = 0; w < kThr / 32; ++w) kn = fmaxf(kn, wmax[w]);
+      for (int w = 0; w < kThr / 32; ++w) kn = fmaxf(kn, wmax[w]);
+      // Between these norms nothing overflows (a score's sum stays below 2^123) and what
+      // underflows (values below 2^-126, that times the other norm) is far below the bound.
+      // Otherwise -- among them norms of 0, infinite or not a number -- the fp32 scores
+      // say nothing and all that compete are scored in fp64.
+      constexpr float kLeast = 0x1p-116f, kMost = 0x1p116f;
+      const bool sound = qn >= kLeast && qn <= kMost && kn >= kLeast && kn <= kMost;
+      float lo = neg_inf(), hi = -neg_inf();  // below lo: out; above hi: in; between: by fp64
+      bool exact = k > 0 && !sound;
+      int need = k;
+      if (sound && k > 0 && far > k) {
+        const float kth = key_score(kth_key(s, far, k, hist + j * 256));
         const float e = float(D + 32) * 0x1p-23f * sqrtf(qn) * sqrtf(kn) * 1.0001f;
         lo = kth - 2.f * e;
         hi = kth + 2.f * e;
-        if (!(lo == lo) || !(hi == hi)) {  // a non-finite bound: every block by fp64
-          lo = neg_inf();
-          hi = -neg_inf();
-        }
-        if (kth == -neg_inf()) lo = hi = kth;
         // count the sure ones; when those between are exactly what is missing, take them all
         int sure = 0, mid = 0;
-        for (int i = lane; i < nb; i += 32) {
+        for (int i = lane; i < far; i += 32) {
           const float v = reinterpret_cast<const float*>(s + i)[0];
           sure += v > hi;
-          mid += v >= lo && v <= hi && v > neg_inf();
+          mid += v >= lo && v <= hi;
         }
-        sure = __reduce_add_sync(0xffffffffu, sure);
-        mid = __reduce_add_sync(0xffffffffu, mid);
-        int need = k - sure;
-        if (mid > need) {
-          // score those between in fp64: one block at a time, the lanes over D
-          for (int i0 = 0; i0 < nb; i0 += 32) {
-            const int i = i0 + lane;
-            const float v = i < nb ? reinterpret_cast<const float*>(s + i)[0] : neg_inf();
-            unsigned todo = __ballot_sync(0xffffffffu, v >= lo && v <= hi && v > neg_inf());
-            double mine = v > hi ? 2.0 : 0.0;  // tag: 2 sure, 0 out
-            bool scored = false;
-            while (todo) {
-              const int l = __ffs(todo) - 1;
-              todo &= todo - 1;
-              const int b = i0 + l;
-              const double* kk = p.sums + (int64_t(b0 + b) * g.Hkv + kh) * D;
-              double t = 0.0;
-              for (int d = lane; d < D; d += 32) t = fma(q64[j * D + d], kk[d], t);
+        need = k - __reduce_add_sync(0xffffffffu, sure);
+        exact = __reduce_add_sync(0xffffffffu, mid) > need;
+      }
+      constexpr long long kOut = 0x7ff8000000000001LL, kIn = 0x7ff8000000000002LL;
+      if (exact) {
+        // score those between in fp64: one block at a time, the lanes over D
+        for (int i0 = 0; i0 < far; i0 += 32) {
+          const int i = i0 + lane;
+          const float v = i < far ? reinterpret_cast<const float*>(s + i)[0] : 0.f;
+          unsigned todo =
+              __ballot_sync(0xffffffffu, i < far && (!sound || (v >= lo && v <= hi)));
+          long long mine = sound && v > hi ? kIn : kOut;
+          while (todo) {
+            const int l = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int b = i0 + l;
+            const double* kk = p.sums + (int64_t(b0 + b) * g.Hkv + kh) * D;
+            double t = 0.0;
+            for (int d = lane; d < D; d += 32) t = fma(q64[j * D + d], kk[d], t);
 #pragma unroll
-              for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-              t /= double(min(g.block, ks.len - b * g.block));
-              if (lane == l) {
-                mine = v == -neg_inf() ? 1.0 / 0.0 : t;
-                scored = true;
-              }
-            }
-            // keep the fp64 score of a scored block; others as quiet tags
-            if (i < nb) {
-              s[i] = scored ? mine : __longlong_as_double(mine != 0.0 ? 0x7ff8000000000002LL
-                                                                      : 0x7ff8000000000001LL);
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            t /= double(min(g.block, ks.len - b * g.block));
+            // (not a number and -inf are never chosen)
+            if (lane == l) mine = t > -1.0 / 0.0 ? __double_as_longlong(t) : kOut;
+          }
+          // the fp64 score of a scored block; others as quiet tags
+          if (i < far) s[i] = __longlong_as_double(mine);
+        }
+        __syncwarp();
+        // the `need` best by (score, lower id): take the maximum `need` times
+        for (; need > 0; --need) {
+          double best = -1.0 / 0.0;
+          int at = INT32_MAX;
+          for (int i = lane; i < far; i += 32) {
+            const double v = s[i];
+            if (v == v && (at == INT32_MAX || v > best)) {
+              best = v;
+              at = i;
             }
           }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+            const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+            if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) {
+              best = ob;
+              at = oa;
+            }
+          }
+          if (at == INT32_MAX) break;
           __syncwarp();
-          // the `need` best by (score, lower id): take the maximum `need` times
-          for (; need > 0; --need) {
-            double best = -1.0 / 0.0;
-            int at = INT32_MAX;
-            for (int i = lane; i < nb; i += 32) {
-              const double v = s[i];
-              if (v == v && (at == INT32_MAX || v > best)) {
-                best = v;
-                at = i;
-              }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-              const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-              if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) {
-                best = ob;
-                at = oa;
-              }
-            }
-            if (at == INT32_MAX) break;  // scores that are NaN in 64 bits are never chosen
-            __syncwarp();
-            if (lane == 0) s[at] = __longlong_as_double(0x7ff8000000000002LL);
-            __syncwarp();
-          }
-          int n = 0;
-          for (int i0 = 0; i0 < nb; i0 += 32) {
-            const int i = i0 + lane;
-            const bool in = i < nb && __double_as_longlong(s[i]) == 0x7ff8000000000002LL;
-            const unsigned m = __ballot_sync(0xffffffffu, in);
-            if (in) out[n + __popc(m & ((1u << lane) - 1))] = i;
-            n += __popc(m);
-          }
-          for (int i = n + lane; i < g.topk; i += 32) out[i] = -1;
-          continue;
+          if (lane == 0) s[at] = __longlong_as_double(kIn);
+          __syncwarp();
         }
       }
       int n = 0;
-      for (int i0 = 0; i0 < nb; i0 += 32) {
+      for (int i0 = 0; i0 < end; i0 += 32) {
         const int i = i0 + lane;
-        const float v = i < nb ? reinterpret_cast<const float*>(s + i)[0] : neg_inf();
-        const bool in = v >= lo && v > neg_inf();
+        bool in = i < end;
+        if (i < far)
+          in = exact ? __double_as_longlong(s[i]) == kIn
+                     : k > 0 && reinterpret_cast<const float*>(s + i)[0] >= lo;
         const unsigned m = __ballot_sync(0xffffffffu, in);
         if (in) out[n + __popc(m & ((1u << lane) - 1))] = i;
         n += __popc(m);

@@ -515,7 +515,8 @@ GATTN_API gattn_status gattn_block_sums(const gattn_block_desc* desc, const void
  * blocks that reach the unit's own positions come before all others.  The
  * choice is that of scores in 64 bits: scores are computed in 32 bits with an
  * error bound, and blocks within that bound of the last place are scored again
- * in 64.  Blocks whose score is not a number or -inf are never chosen.  The
+ * in 64 (all of them where 32 bits cannot hold the scores or the bound).  Blocks
+ * whose 64-bit score is not a number or -inf are never chosen.  The
  * scores of a unit stay in shared memory: max_len_k (or Nk) / block may be about
  * 27,900 at most (GATTN_ERR_UNSUPPORTED beyond).
  */

@@ -338,6 +338,48 @@ def test_select_non_finite_keys(qb, dtype):
         assert 7 in first and not {3, 9, 11} & set(first)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("qb", [1, 32])
+@pytest.mark.parametrize("q,k", [(1e20, 1e20), (1e-24, 1.0), (1.0, 1e-24), (1e-30, 1e-30), (1e30, 1e-30),
+                                 (1e15, 1e30), (1e-38, 1e4), (0.0, 1.0), (1.0, 0.0)])
+def test_select_at_the_ends_of_fp32(q, k, qb, causal):
+    """Scores beyond the range of fp32, and norms whose squares it cannot hold: the choice is
+    still that of the scores in 64 bits, with its near ties."""
+    n, block = 640, 16
+    # 64 bits see the difference of the last blocks, 32 do not
+    Q, K = randn(77, 64, 2, 16), randn(78, n, 1, 16)
+    K[320:] = K[:16].repeat(20, 1, 1)
+    for i, at in enumerate((7, 3, 11, 2)):
+        K[320 + 16 * at, 0, i] *= 1 + 2.0 ** (i - 22)
+    Q, K = (Q.double() * q).float(), (K.double() * k).float()
+    sums = gb.gattn_block_sums(K, i32([0, n]), block)
+    for topk in (1, 5, 24, 60):
+        idx = gb.gattn_block_select(Q, sums, i32([0, 64]), i32([0, n]), topk, block, qb, n, causal=causal)
+        assert torch.equal(idx.cpu(), ref.select(Q, K, [0, 64], [0, n], topk, block, qb, causal)), topk
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_some_units_and_blocks_out_of_range(dtype):
+    """Units and blocks of ordinary size beside huge, tiny, zero and non-finite ones, eight units
+    to a pass over the sums."""
+    lens, block, qb = [700, 40, 900], 16, 8
+    sq = ref.offsets(lens)
+    Q, K = randn(79, sq[-1], 16, 16, dtype=DT[dtype]), randn(80, sq[-1], 16, 16, dtype=DT[dtype])
+    for s in range(3):
+        Q[sq[s]:sq[s] + 8] *= 1e25
+        Q[sq[s] + 8:sq[s] + 16] *= 1e-30
+        Q[sq[s] + 16:sq[s] + 24] = 0
+    K[100:116] *= 1e30
+    K[740 + 64:740 + 80, 3] = 0
+    K[740 + 80:740 + 96, 4] *= 1e-35
+    K[740 + 100, 5, 7] = float("inf")
+    K[740 + 130, 6, 7] = float("nan")
+    sums = gb.gattn_block_sums(K, i32(sq), block)
+    for causal in (False, True):
+        idx = gb.gattn_block_select(Q, sums, i32(sq), i32(sq), 4, block, qb, sq[-1], causal=causal)
+        assert torch.equal(idx.cpu(), ref.select(Q, K, sq, sq, 4, block, qb, causal))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_offsets_beyond_32_bits(dtype):
     """A sequence at the end of a cache of more than 2^31 elements."""
