@@ -15,6 +15,13 @@
 //   dQ as dQ's own rounding, on top of that of Delta (formed from the rounded
 //   out), and dQ would be half again as far off as the rounding of the result
 //   alone; the second product costs a quarter of the kernel's tensor work.
+//   With few keys a row's ds is a small difference of dP and Delta, and the rounding
+//   of out left dQ and dK two to three times as far off as their own.  A tile
+//   whose rows see one step of keys at most (those of short sequences, and the
+//   first of causal ones) has every p and dP of a row at hand, so it forms Delta =
+//   sum p dP of them and leaves it for the key side.  Rows of several steps keep
+//   the Delta of the rounded out: 1.1 to 1.3 times the result's own rounding for
+//   dQ, where a pass of S and dP before the first ds would cost half the kernel.
 //
 // dK, dV: a work item is a tile of 128 keys and up to `chunk` of the units that
 //   chose one of its blocks (block_api.cu builds the items), walked in steps
@@ -85,7 +92,7 @@ struct DqSm {
   static constexpr int IDS = V + NV * OP;
   static constexpr int INFO = IDS + 2 * kBlkMaxTopk * 4;
   static constexpr int BAR = INFO + 2 * int(sizeof(DqInfo));
-  static constexpr int NBAR = 4 + 2 * NQ + 2 * NK + 2 * NV + 2 + 1 + 2 + 2 * NG;
+  static constexpr int NBAR = 4 + 2 * NQ + 2 * NK + 2 * NV + 2 + 1 + 2 + 2 * NG + 4;
   static constexpr int END = BAR + NBAR * 8 + 8;
   static constexpr int BYTES = END + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
            *q_empty = q_full + NQ, *k_full = q_empty + NQ, *k_empty = k_full + NK,
            *v_full = k_empty + NK, *v_empty = v_full + NV, *s_full = v_empty + NV,
            *dp_empty = s_full + 2, *d_full = dp_empty + 1, *g_full = d_full + 2,
-           *g_empty = g_full + NG;
+           *g_empty = g_full + NG, *row_sum = g_empty + NG;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + M::NBAR);
   DqInfo* info = reinterpret_cast<DqInfo*>(sm + M::INFO);
   int* ids = reinterpret_cast<int*>(sm + M::IDS);
@@ -125,6 +132,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       mbar_init(d_full + i, kDqWarps);
     }
     mbar_init(dp_empty, kDqWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(row_sum + i, kDqWarps / 4);
     for (int i = 0; i < NG; ++i) {
       mbar_init(g_full + i, 1);
       mbar_init(g_empty + i, kDqOut);
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     const int r = (warp & 3) * 32 + lane, cc = warp >> 2;  // row, 32-column chunk
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const int th = r % p.ht, tt = r / p.ht;
-    int gi = 0, ti = 0;
+    int gi = 0, ti = 0, singles = 0;  // steps, tiles, tiles of one step
     for (int64_t t = blockIdx.x; t < p.n_tiles; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = ok && warp_wait(tile_full + slot, (ti >> 1) & 1);
@@ -384,6 +392,41 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
         float dv[32];
         tmem_ld32(tmem + lanes + 2 * kT + cc * 32, dv);
         tmem_wait_ld();
+        const int mine = lim - st * kT - cc * 32;
+        const bool cut = __any_sync(0xffffffffu, mine < 32);
+        const float2 qm = f2s(g.qmul), nl = f2s(-stat.x);
+        if (steps == 1) {  // Delta from the row's own p and dP
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float sv[16];
+            tmem_ld16(tS + h * 16, sv);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int c0 = h * 16 + 2 * j;
+              const float2 z = f2fma(make_float2(sv[2 * j], sv[2 * j + 1]), qm, nl);
+              sum.x = c0 < mine ? fmaf(ex2(z.x), dv[c0], sum.x) : sum.x;
+              sum.y = c0 + 1 < mine ? fmaf(ex2(z.y), dv[c0 + 1], sum.y) : sum.y;
+            }
+          }
+          // the four warps of these rows meet in the dP that they have read
+          const uint32_t tR = tmem + lanes + 2 * kT;
+          tmem_st1(tR + cc * 32, sum.x + sum.y);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(row_sum + (warp & 3));
+          ok = warp_wait(row_sum + (warp & 3), singles & 1);
+          if (!ok) break;
+          ++singles;
+          tc_fence_after();
+          const float d0 = tmem_ld1(tR), d1 = tmem_ld1(tR + 32), d2 = tmem_ld1(tR + 64),
+                      d3 = tmem_ld1(tR + 96);
+          tmem_wait_ld();
+          stat.y = (d0 + d1) + (d2 + d3);
+          if (cc == 0 && lim > 0) p.b.stat[qrow].y = stat.y;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dp_empty);
@@ -397,9 +440,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
           fence_proxy_async();
           __syncwarp();
         }
-        const int mine = lim - st * kT - cc * 32;
-        const bool cut = __any_sync(0xffffffffu, mine < 32);
-        const float2 qm = f2s(g.qmul), nl = f2s(-stat.x), nd = f2s(-stat.y);
+        const float2 nd = f2s(-stat.y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 16 columns: ds rounded, and what the rounding left
           float sv[16], w[16];

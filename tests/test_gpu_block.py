@@ -630,3 +630,53 @@ def test_offsets_out_of_order_that_want_more_items_than_there_are(S, dtype):
     assert (ws[need:] == 7).all() and (big[0] == 7.0).all() and (big[4] == 7.0).all()
     run(185, [N], [N], H, H, 64, dtype, block, qb, 1,
         idx=torch.zeros(ref.units(N, 1, qb), 1, 1, dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D,G,qb", [(16, 2, 128), (64, 1, 64), (64, 4, 32), (128, 2, 64), (128, 1, 1)])
+def test_gradients_of_rows_with_few_keys(D, G, qb, causal):
+    """bf16 rows that see at most one step of 128 keys: ds = p (dP - Delta) is a small difference
+    there, and Delta carries no rounding of out.
+
+    Bounds, relative to |.|: a score is off by c |q||k| scale with c = (n + D + 32) 2^-24, lse by
+    that and 2^-20 (1 + |lse|), so p by e_p, twice their sum and 2^-22 for the exponential; dP by
+    c |dout||v|; Delta = sum p dP by the sum of p's and dP's errors and c for its own sum.  ds
+    enters dQ as two bf16 (2^-16) and dK as one (2^-8); each result is rounded once (2^-8)."""
+    lens, Hkv = [1, 2, 3, 7, 33, 64, 100, 128, 1, 5], 2
+    H, block, sq = Hkv * G, 32, ref.offsets(lens)
+    N = sq[-1]
+    Q, K, V, W = (randn(190 + i, N, H if i in (0, 3) else Hkv, D, dtype=torch.bfloat16) for i in range(4))
+    idx = torch.arange(4, dtype=torch.int32, device=DEV).repeat(gb.gattn_block_units(N, len(lens), qb), Hkv, 1)
+    off, kw = i32(sq), {"block": block, "q_block": qb, "causal": causal}
+    out, lse = gb.gattn_block_fwd(Q, K, V, idx, off, off, **kw)
+    dQ, dK, dV = gb.gattn_block_bwd(Q, K, V, idx, off, off, out, W, lse, **kw)
+    gb.gattn_block_check_errors()
+    scale, u = 1 / math.sqrt(D), 2.0 ** -8
+    for s, n in enumerate(lens):
+        rows = slice(sq[s], sq[s + 1])
+        c = (n * G + D + 32) * 2.0 ** -24
+        ok = torch.ones(n, n, dtype=torch.bool, device=DEV)
+        ok = ok.tril() if causal else ok
+        for g in range(Hkv):
+            k, v = K[rows, g].double(), V[rows, g].double()
+            want, tol = torch.zeros(n, D, dtype=torch.float64, device=DEV), 0.0
+            for h in range(g * G, (g + 1) * G):
+                q, do = Q[rows, h].double(), W[rows, h].double()
+                sc = (q @ k.T * scale).masked_fill(~ok, -math.inf)
+                z = torch.logsumexp(sc, 1, keepdim=True)
+                p = torch.exp(sc - z)
+                err = torch.where(ok, q.abs() @ k.abs().T * scale * c, 0.0)
+                ep = 2 * (err + err.amax(1, keepdim=True) + 2.0 ** -20 * (1 + z.abs())) + 2.0 ** -22
+                dp, dpe = do @ v.T, c * (do.abs() @ v.abs().T)
+                delta = (p * dp).sum(1, keepdim=True)
+                de = (p * (ep * dp.abs() + dpe)).sum(1, keepdim=True) + c * (p * dp.abs()).sum(1, keepdim=True)
+                ds = p * (dp - delta)
+                dse = p * (ep * (dp - delta).abs() + dpe + de) + c * ds.abs()
+                dq = ds @ k * scale
+                t = u * dq.abs() + scale * ((dse + 2.0 ** -16 * ds.abs()) @ k.abs())
+                over = ((dQ[rows, h].double() - dq).abs() - t).max().item()
+                assert over <= 1e-30, (n, h, over)
+                want += ds.T @ q * scale
+                tol = tol + scale * ((dse + u * ds.abs()).T @ q.abs())
+            over = ((dK[rows, g].double() - want).abs() - tol - u * want.abs()).max().item()
+            assert over <= 1e-30, (n, g, over)
