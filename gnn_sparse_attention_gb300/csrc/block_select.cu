@@ -5,7 +5,8 @@
 // it is defined by scores in 64 bits.  Sums run as pairs of fp32 (each
 // addition keeps its exact rounding error in the second member, about 48
 // bits, at fp32 rates: this GPU's fp64 units add two numbers a clock and SM,
-// a fiftieth of what memory delivers); fp64 appears once per finished sum.
+// a fiftieth of what memory delivers); fp64 appears once per finished sum, and
+// for the whole of one that leaves the range of fp32.
 // Scores run in fp32 FMAs with an error bound
 //   |score - exact| <= e = (D + 32) 2^-23 |q| max|k / n|   (Cauchy-Schwarz),
 // a radix select finds the topk-th score T, blocks above T + 2e are in, below
@@ -155,9 +156,18 @@ __global__ void __launch_bounds__(kThr, 4) piece_sums_kernel(const SumParams p) 
         t = make_float2(aa.x, ee.x + f.y);
       }
       const int o = blockIdx.y * cx * V + c;
-      // (an infinite sum has no error to add)
-      if (o < W) p.sums[int64_t(piece) * W + o] =
-          fabsf(t.x) <= 3.4e38f ? double(t.x) + double(t.y) : double(t.x);
+      if (o >= W) continue;
+      double sum = double(t.x) + double(t.y);
+      if (!(fabsf(t.x) <= 3.4e38f)) {  // beyond fp32, on the way at least: again in fp64
+        const int kh = o / g.D, d = o - kh * g.D;
+        const T* x = static_cast<const T*>(p.x) + (((sp.beg + pos) * W) << p.l_heads) +
+                     int64_t(kh) * heads * g.D + d;
+        sum = 0.0;
+        for (int i = 0; i < n << p.l_heads; ++i)
+          sum += double(float(x[((int64_t(i >> p.l_heads) * W) << p.l_heads) +
+                                int64_t(i & (heads - 1)) * g.D]));
+      }
+      p.sums[int64_t(piece) * W + o] = sum;
     }
   }
 }

@@ -495,8 +495,8 @@ typedef struct {
 
 /*
  * Sums of the keys of each block in 64 bits: sums[blocks][Hkv][D] (device
- * double; bf16 keys add up to better than 2^-44 of the largest partial sum; partial
- * sums that leave the range of fp32 are infinite).
+ * double; bf16 keys add up to better than 2^-44 of the largest partial sum; finite
+ * wherever the keys are, also beyond the range of fp32).
  *   since : device int32 [S] or NULL.  NULL writes every row of `sums` (zeros in rows of
  *           no block); otherwise only blocks that hold a position >= since[s] are
  *           renewed, as after appending to a cache.

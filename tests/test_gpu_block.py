@@ -359,6 +359,29 @@ def test_select_at_the_ends_of_fp32(q, k, qb, causal):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qb", [1, 64])
+def test_sums_beyond_fp32(qb, dtype):
+    """Keys and queries whose partial sums, or whole sums, are larger than fp32 can hold: the sums
+    and the choice are those in 64 bits (some that cancel, some that do not)."""
+    n, block, big = 300, 32, 2.0 ** 127
+    Q, K = randn(83, 130, 8, 16, dtype=DT[dtype]), randn(84, n, 2, 16, dtype=DT[dtype])
+    K[64:96, 0, 3] = big                       # 2^132
+    K[96:112, 1, 5], K[112:128, 1, 5] = big, -big  # 0 in the end
+    K[288:, :, 0] = -big                       # the last block is short
+    Q[:, 0:4, 2], Q[0:64, 4:6, 7], Q[0:64, 6:8, 7] = 1.5 * big, big, -big
+    sums = gb.gattn_block_sums(K, i32([0, n]), block)
+    want = ref.block_sums(K, [0, n], block)
+    mag = ref.block_sums(K.abs(), [0, n], block)
+    assert ((sums - want).abs() <= 2.0 ** -40 * mag).all()
+    part = torch.full_like(sums, 5.0)
+    gb.gattn_block_sums(K, i32([0, n]), block, since=i32([70]), sums=part)
+    assert ((part - want).abs()[2:] <= 2.0 ** -40 * mag[2:]).all() and (part[:2] == 5.0).all()
+    for topk in (1, 4, 9):
+        idx = gb.gattn_block_select(Q, sums, i32([0, 130]), i32([0, n]), topk, block, qb, n)
+        assert torch.equal(idx.cpu(), ref.select(Q, K, [0, 130], [0, n], topk, block, qb))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_select_some_units_and_blocks_out_of_range(dtype):
     """Units and blocks of ordinary size beside huge, tiny, zero and non-finite ones, eight units
     to a pass over the sums."""
