@@ -115,6 +115,15 @@ class GATv2Conv(nn.Module):
         return out.reshape(N, self.heads * self.head_dim)
 
 
+def _packed(t: torch.Tensor | None) -> torch.Tensor | None:
+    """t as the kernels read it, contiguous from a 16-byte border on: a copy where it is not, as
+    with a column slice, or with rows of an odd size that start in the middle of a tensor."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _BlockAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, idx, seq_q, seq_k, len_k, block, q_block, scale, causal):
@@ -133,7 +142,7 @@ class _BlockAttention(torch.autograd.Function):
     def backward(ctx, dout, _dlse):
         Q, K, V, idx, seq_q, seq_k, out, lse, *more = ctx.saved_tensors
         dQ, dK, dV = (torch.zeros_like(t) for t in (Q, K, V))
-        gb.gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout.to(Q.dtype).contiguous(), lse,
+        gb.gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, _packed(dout.to(Q.dtype)), lse,
                            len_k=more[0] if ctx.has_len else None, dQ=dQ, dK=dK, dV=dV, **ctx.args)
         return (dQ, dK, dV) + (None,) * 8
 
@@ -153,7 +162,7 @@ def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torc
     (out [Nq, H, D], lse fp32 [Nq, H], idx); differentiable in Q, K and V, not in the choice.
     Rows of no sequence get zeros.
     """
-    Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+    Q, K, V = _packed(Q), _packed(K), _packed(V)
     keys = seq if seq_k is None else seq_k
     if idx is None:
         with torch.no_grad():
@@ -182,7 +191,7 @@ class _GatedResidualNorm(torch.autograd.Function):
         saved = iter(ctx.saved_tensors)
         res, stats, x, gate, w_post, b_post, w_pre, b_pre = (
             next(saved) if there else None for there in ctx.present)
-        dh, dy = (None if t is None else t.to(res.dtype).contiguous() for t in (dh, dy))
+        dh, dy = (None if t is None else _packed(t.to(res.dtype)) for t in (dh, dy))
         if dy is None and w_pre is not None:
             dy = torch.zeros_like(res)
         if dh is None and dy is None:
@@ -198,12 +207,15 @@ def gated_residual_norm(res: torch.Tensor, x: torch.Tensor | None = None,
                         b_pre=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6):
     """(h, y): h = res + alpha * gate * norm(x; w_post, b_post), y = norm(h; w_pre, b_pre).
 
-    res, x: contiguous [N, F] rows (fp32 or bf16); gate: [N, F] like them, or fp32 [F]; weights
-    and biases fp32 [F].  Parts left out are skipped (see gattn_norm_fwd); y is None without
-    w_pre.  Differentiable in every tensor.
+    res, x: [N, F] rows (fp32 or bf16); gate: [N, F] like them, or fp32 [F]; weights and biases
+    fp32 [F].  Parts left out are skipped (see gattn_norm_fwd); y is None without w_pre.
+    Differentiable in every tensor.  Tensors that are not contiguous, or not aligned to 16 bytes,
+    are copied.
     """
-    return _GatedResidualNorm.apply(res.contiguous(), None if x is None else x.contiguous(), gate,
-                                    w_post, b_post, w_pre, b_pre, float(alpha), kind, float(eps))
+    res, x, gate, w_post, b_post, w_pre, b_pre = (
+        _packed(t) for t in (res, x, gate, w_post, b_post, w_pre, b_pre))
+    return _GatedResidualNorm.apply(res, x, gate, w_post, b_post, w_pre, b_pre, float(alpha), kind,
+                                    float(eps))
 
 
 class GraphTransformerBlock(nn.Module):

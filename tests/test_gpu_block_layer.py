@@ -97,6 +97,46 @@ def test_gated_residual_norm_autograd(kind):
         assert relerr(np64(leaf[k].grad), np64(d[k].grad)) < TOL["f32"], k
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_slices_and_gradients_of_slices(dtype):
+    """Columns of a wider tensor, rows and vectors that start off a 16-byte border, and gradients
+    that arrive as such slices: the results of packed copies."""
+    torch.manual_seed(7)
+    N, F = 40, 33
+    # what a network has in hand: two parts of one projection, rows behind the first, a vector's tail
+    both = torch.randn(N + 1, 3 * F, device=DEV).to(dtype).requires_grad_()
+    rows = torch.randn(N + 1, F, device=DEV).to(dtype).requires_grad_()
+    vec = (1 + 0.1 * torch.randn(F + 1, device=DEV)).requires_grad_()
+    gy, gh = torch.randn(2 * N, F, device=DEV).to(dtype), torch.randn(2 * N, F, device=DEV).to(dtype)
+
+    def step(same):
+        x, gate, more = (same(t) for t in both[1:].chunk(3, -1))
+        w = same(vec[1:])
+        h, y = layer.gated_residual_norm(same(rows[1:]), x, gate, w, None, w, None)
+        # (their gradients are slices that begin off a border)
+        top = torch.cat([more[:-1], h[:-1], y[:1]]), torch.cat([more[:1], y[:-1], more[1:]])
+        loss = (top[0] * gh[:2 * N - 1]).sum() + (top[1] * gy[:2 * N - 1]).sum()
+        return (h, y, *torch.autograd.grad(loss, (both, rows, vec)))
+
+    assert rows[1:].data_ptr() % 16 and vec[1:].data_ptr() % 16
+    for a, b in zip(step(lambda t: t), step(lambda t: t.clone(memory_format=torch.contiguous_format))):
+        assert torch.equal(a, b)
+    # attention: a flat buffer's views, off a border
+    sq, n = [0, 70], 70 * 2 * 16
+    flat = torch.randn(3 * n + 1, device=DEV).to(dtype).requires_grad_()
+    wide = torch.randn(n + 1, device=DEV).to(dtype)
+
+    def attend(same):
+        Q, K, V = (same(t).view(70, 2, 16) for t in flat[1:].split(n))
+        out, lse, _ = layer.block_attention(Q, K, V, i32(sq), topk=2, block=16, q_block=16)
+        # (the cut's gradient is a view of the flat gradient)
+        all_ = torch.cat([flat[:1], out.reshape(-1)])
+        return out, lse, *torch.autograd.grad((all_ * wide).sum(), flat)
+
+    for a, b in zip(attend(lambda t: t), attend(lambda t: t.clone())):
+        assert torch.equal(a, b)
+
+
 def test_gated_residual_norm_parts_without_a_gradient():
     """Only one of the two results is used; a gate or a norm is left out."""
     torch.manual_seed(3)
