@@ -124,6 +124,27 @@ def _packed(t: torch.Tensor | None) -> torch.Tensor | None:
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+class _Once(torch.autograd.Function):
+    """The first n tensors, as functions of the others that cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, n, *ts):
+        return tuple(t.view_as(t) for t in ts[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("block_attention and gated_residual_norm are differentiable once only")
+
+
+def _once(grads, *roots):
+    """Gradients of a kernel under create_graph: a second derivative is refused, not left out."""
+    if not torch.is_grad_enabled():
+        return grads
+    some = [g for g in grads if g is not None]
+    done = iter(_Once.apply(len(some), *some, *(t for t in roots if t is not None)))
+    return tuple(None if g is None else next(done) for g in grads)
+
+
 class _BlockAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, idx, seq_q, seq_k, len_k, block, q_block, scale, causal):
@@ -144,7 +165,7 @@ class _BlockAttention(torch.autograd.Function):
         dQ, dK, dV = (torch.zeros_like(t) for t in (Q, K, V))
         gb.gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, _packed(dout.to(Q.dtype)), lse,
                            len_k=more[0] if ctx.has_len else None, dQ=dQ, dK=dK, dV=dV, **ctx.args)
-        return (dQ, dK, dV) + (None,) * 8
+        return _once((dQ, dK, dV), Q, K, V, dout) + (None,) * 8
 
 
 def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor,
@@ -159,8 +180,8 @@ def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torc
     rows; seq_k and len_k (both optional) give the keys their own offsets and lengths.  ``idx``
     (int32 [units, Hkv, blocks], see gattn_block_select) replaces the choice; ``max_len_k``, the
     most keys of one sequence (0: all rows), keeps its score tables small.  Returns
-    (out [Nq, H, D], lse fp32 [Nq, H], idx); differentiable in Q, K and V, not in the choice.
-    Rows of no sequence get zeros.
+    (out [Nq, H, D], lse fp32 [Nq, H], idx).  out is differentiable in Q, K and V, once, and not
+    in the choice; lse carries no gradient.  Rows of no sequence get zeros.
     """
     Q, K, V = _packed(Q), _packed(K), _packed(V)
     keys = seq if seq_k is None else seq_k
@@ -198,8 +219,8 @@ class _GatedResidualNorm(torch.autograd.Function):
             return (None,) * 10
         g = gb.gattn_norm_bwd(res, stats, dh, dy, x, gate, w_post, b_post, w_pre, b_pre,
                               ctx.alpha, ctx.kind)
-        return (g["dres"], g["dx"], g["dgate"], g["dw_post"], g["db_post"], g["dw_pre"],
-                g["db_pre"], None, None, None)
+        return _once((g["dres"], g["dx"], g["dgate"], g["dw_post"], g["db_post"], g["dw_pre"],
+                      g["db_pre"]), res, x, gate, w_post, b_post, w_pre, b_pre, dh, dy) + (None,) * 3
 
 
 def gated_residual_norm(res: torch.Tensor, x: torch.Tensor | None = None,
@@ -209,8 +230,8 @@ def gated_residual_norm(res: torch.Tensor, x: torch.Tensor | None = None,
 
     res, x: [N, F] rows (fp32 or bf16); gate: [N, F] like them, or fp32 [F]; weights and biases
     fp32 [F].  Parts left out are skipped (see gattn_norm_fwd); y is None without w_pre.
-    Differentiable in every tensor.  Tensors that are not contiguous, or not aligned to 16 bytes,
-    are copied.
+    Differentiable in every tensor, once.  Tensors that are not contiguous, or not aligned to 16
+    bytes, are copied.
     """
     res, x, gate, w_post, b_post, w_pre, b_pre = (
         _packed(t) for t in (res, x, gate, w_post, b_post, w_pre, b_pre))

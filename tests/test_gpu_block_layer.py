@@ -137,6 +137,21 @@ def test_slices_and_gradients_of_slices(dtype):
         assert torch.equal(a, b)
 
 
+def test_second_derivatives_are_refused():
+    """A gradient penalty would silently lose the part that goes through these operators."""
+    torch.manual_seed(8)
+    Q, K, V = (torch.randn(40, 2, 16, device=DEV, requires_grad=True) for _ in range(3))
+    out = layer.block_attention(Q, K, V, i32([0, 40]), topk=1, block=16, q_block=16)[0]
+    r, x, w = (torch.randn(*s, device=DEV, requires_grad=True) for s in ((20, 64), (20, 64), (64,)))
+    h, y = layer.gated_residual_norm(r, x, w_pre=w)
+    for res, leaf in ((out, Q), (out.pow(2), V), (y, x), (h + y.pow(2), w)):
+        plain = torch.autograd.grad(res.sum(), leaf, retain_graph=True)[0]
+        g = torch.autograd.grad(res.sum(), leaf, create_graph=True)[0]
+        assert torch.equal(plain, g)
+        with pytest.raises(RuntimeError, match="once"):
+            (g.pow(2).sum() + leaf.sum()).backward()
+
+
 def test_gated_residual_norm_parts_without_a_gradient():
     """Only one of the two results is used; a gate or a norm is left out."""
     torch.manual_seed(3)
