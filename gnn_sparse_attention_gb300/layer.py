@@ -231,10 +231,11 @@ def gated_residual_norm(res: torch.Tensor, x: torch.Tensor | None = None,
     res, x: [N, F] rows (fp32 or bf16); gate: [N, F] like them, or fp32 [F]; weights and biases
     fp32 [F].  Parts left out are skipped (see gattn_norm_fwd); y is None without w_pre.
     Differentiable in every tensor, once.  Tensors that are not contiguous, or not aligned to 16
-    bytes, are copied.
+    bytes, are copied, and vectors of another type (of a module that was cast whole) converted.
     """
     res, x, gate, w_post, b_post, w_pre, b_pre = (
-        _packed(t) for t in (res, x, gate, w_post, b_post, w_pre, b_pre))
+        _packed(t.float() if t is not None and t.dim() == 1 else t)
+        for t in (res, x, gate, w_post, b_post, w_pre, b_pre))
     return _GatedResidualNorm.apply(res, x, gate, w_post, b_post, w_pre, b_pre, float(alpha), kind,
                                     float(eps))
 

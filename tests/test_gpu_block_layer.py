@@ -286,3 +286,25 @@ def test_training_step_in_a_graph():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert relerr(np64(b), np64(a)) < 1e-2
+
+
+def test_transformer_block_cast_whole():
+    """module.to(bfloat16) casts the norms' weights and gates too: the layer still runs, with the
+    results of the same values kept in fp32, and gradients in the parameters' type."""
+    torch.manual_seed(9)
+    seq = i32([0, 100, 180])
+    m = layer.GraphTransformerBlock(64, 2, 32, topk=2, kind="layer", dtype=torch.float32, device=DEV)
+    with torch.no_grad():
+        for p in m.parameters():
+            p.add_(0.1 * torch.randn_like(p))
+    m = m.to(torch.bfloat16)
+    h, g = (torch.randn(180, 64, device=DEV).to(torch.bfloat16) for _ in range(2))
+    out = m(h, seq)
+    got = torch.autograd.grad(out, list(m.parameters()), g)
+    for n, p in list(m.named_parameters()):
+        if p.dim() == 1:
+            setattr(m, n, torch.nn.Parameter(p.detach().float()))
+    want = m(h, seq)
+    assert torch.equal(out, want)
+    for p, a, b in zip(m.parameters(), got, torch.autograd.grad(want, list(m.parameters()), g)):
+        assert a.dtype == torch.bfloat16 and torch.equal(a, b.to(torch.bfloat16))
