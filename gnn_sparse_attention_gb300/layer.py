@@ -280,8 +280,9 @@ class GraphTransformerBlock(nn.Module):
         a, _, _ = block_attention(Q, K, V, seq, idx=idx, max_len_k=max_nodes, **self.choice)
         if plan is not None:
             a = a + graph_attention(plan, Q, K, V, "dot", 1.0 / math.sqrt(self.head_dim))[0]
-        h, y = gated_residual_norm(h, self.o(a.reshape(N, -1)), self.gate_attn, self.w_attn,
-                                   self.b_attn, self.w_mid, self.b_mid, kind=self.kind)
+        a = self.o(a.reshape(N, self.heads * self.head_dim))
+        h, y = gated_residual_norm(h, a, self.gate_attn, self.w_attn, self.b_attn, self.w_mid,
+                                   self.b_mid, kind=self.kind)
         m = self.down(nn.functional.gelu(self.up(y)))
         h, _ = gated_residual_norm(h, m, self.gate_mlp, self.w_mlp, self.b_mlp, kind=self.kind)
         return h

@@ -308,3 +308,15 @@ def test_transformer_block_cast_whole():
     assert torch.equal(out, want)
     for p, a, b in zip(m.parameters(), got, torch.autograd.grad(want, list(m.parameters()), g)):
         assert a.dtype == torch.bfloat16 and torch.equal(a, b.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("seq", [[0], [0, 0, 0]])
+def test_transformer_block_without_nodes(seq):
+    """An empty batch: no rows out, and gradients that are zeros."""
+    m = layer.GraphTransformerBlock(64, 2, 32, topk=2, dtype=torch.float32, device=DEV)
+    h = torch.zeros(0, 64, device=DEV, requires_grad=True)
+    out = m(h, i32(seq))
+    assert out.shape == (0, 64)
+    out.sum().backward()
+    assert h.grad.shape == h.shape
+    assert all(p.grad is not None and not p.grad.any() for p in m.parameters())
