@@ -32,6 +32,7 @@ EXPORTED = ("gattn_plan_create", "gattn_plan_destroy", "gattn_plan_get_info",
             "gattn_plan_set_wait_test", "gattn_block_sums", "gattn_block_select_workspace_size",
             "gattn_block_select", "gattn_block_fwd_workspace_size", "gattn_block_fwd",
             "gattn_block_bwd_workspace_size", "gattn_block_bwd", "gattn_block_check_errors",
+            "gattn_block_set_wait_test",
             "gattn_norm_workspace_size", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_last_error",
             "gattn_version")
 
@@ -143,6 +144,7 @@ def load_library(path: str | None = None):
         lib.gattn_block_bwd_workspace_size.argtypes = [bd, psz]
         lib.gattn_block_bwd.argtypes = [bd] + [P] * 11 + [sz, P]
         lib.gattn_block_check_errors.argtypes = []
+        lib.gattn_block_set_wait_test.argtypes = [i32]
         lib.gattn_norm_workspace_size.argtypes = [nd, psz]
         lib.gattn_norm_fwd.argtypes = [nd] + [P] * 7
         lib.gattn_norm_bwd.argtypes = [nd] + [P] * 14 + [sz, P]
@@ -815,6 +817,13 @@ def gattn_block_bwd(Q, K, V, idx, seq_q, seq_k, out, dout, lse, block: int, q_bl
 def gattn_block_check_errors() -> None:
     """Raise GattnError(GATTN_ERR_TIMEOUT) if a block-attention kernel gave up a bounded wait."""
     _check(load_library().gattn_block_check_errors(), "gattn_block_check_errors")
+
+
+def gattn_block_set_wait_test(fail_first_wait: bool) -> None:
+    """Test hook of the bounded-wait failure path: while set, block-attention kernels (bf16) give
+    up at once, so the next gattn_block_check_errors raises GATTN_ERR_TIMEOUT."""
+    _check(load_library().gattn_block_set_wait_test(int(bool(fail_first_wait))),
+           "gattn_block_set_wait_test")
 
 
 NORM = {"rms": 0, "layer": 1}

@@ -179,10 +179,12 @@ struct BlockBwdParams {
   int4* items;       // (key tile * Hkv + head, first unit, units, slot or -1)
   float* part;       // [slots][2][128][D]: dK, dV of one item
   int words, chunk;
+  int fail;          // failure-path test: the compute warps give up their first wait
   int64_t max_items;
 };
 
 int sm_count();
+int block_wait_test();  // what gattn_block_set_wait_test set
 gattn_status launch_block_fwd_simt(const BlockGeom& g, const float* Q, const float* K,
                                    const float* V, const int32_t* idx, float* out, float* lse,
                                    cudaStream_t st);

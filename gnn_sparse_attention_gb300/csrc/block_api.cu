@@ -37,6 +37,9 @@ int sm_count() {  // of the current device; asked once per device
   return n;
 }
 
+static std::atomic<int> g_wait_test{0};
+int block_wait_test() { return g_wait_test.load(std::memory_order_relaxed); }
+
 namespace {
 
 bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -492,6 +495,7 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   p.words = w.words;
   p.chunk = w.chunk;
   p.max_items = w.max_items;
+  p.fail = block_wait_test();
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const gattn_dtype dt = gattn_dtype(desc->dtype);
   if ((s = bwd_prepare(p, dt, w, ws, st)) != GATTN_OK ||
@@ -502,6 +506,11 @@ gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const 
   if (dt == GATTN_F32) join_kv_kernel<float><<<grid, 256, 0, st>>>(p);
   else join_kv_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
   return launched("gattn_block_bwd (join)");
+}
+
+gattn_status gattn_block_set_wait_test(int32_t fail_first_wait) {
+  g_wait_test.store(fail_first_wait != 0, std::memory_order_relaxed);
+  return GATTN_OK;
 }
 
 gattn_status gattn_block_check_errors(void) {

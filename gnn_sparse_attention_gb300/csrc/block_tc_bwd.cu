@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  bool ok = true;
+  bool ok = !(p.b.fail && warp < kDqWarps);  // false: a wait gave up, leave
 
   if (warp == kDqWarps + 2) {
     // ---------------------------------------------------------------- lists
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     const int per = kT / g.block;
     const uint32_t blk_bytes = uint32_t(g.block) * 128;
     int gi = 0, ti = 0, tq = 0;
+    int nk = 0, nv = 0;  // steps whose K, V have been asked for
     for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = warp_wait(tile_full + slot, (ti >> 1) & 1);
@@ -232,6 +233,8 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
                        kv ? &p.mv : &p.mk, kb * 64, kh, kbeg + list[st * per + b] * g.block,
                        full);
           }
+          if (kv) ++nv;
+          else ++nk;
         }
         if (!ok) break;
       }
@@ -240,10 +243,12 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
       if (lane == 0) mbar_arrive(tile_empty + slot);
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
-      for (int i = 1; i <= NQ && i <= tq; ++i)
-        warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
-      for (int c = gi; c > gi - NK && c >= 0; --c) warp_wait(k_full + c % NK, (c / NK) & 1, 200);
-      for (int c = gi; c > gi - NV && c >= 0; --c) warp_wait(v_full + c % NV, (c / NV) & 1, 200);
+      for (int c = tq - 1; c >= max(0, tq - NQ); --c)  // the newest use of each stage
+        warp_wait(q_full + c % NQ, (c / NQ) & 1, 200);
+      for (int c = nk - 1; c >= max(0, nk - NK); --c)
+        warp_wait(k_full + c % NK, (c / NK) & 1, 200);
+      for (int c = nv - 1; c >= max(0, nv - NV); --c)
+        warp_wait(v_full + c % NV, (c / NV) & 1, 200);
     }
   } else if (warp == kDqWarps) {
     // ---------------------------------------------------------------- products
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  bool ok = true;
+  bool ok = !(p.b.fail && warp < kKvWarps);
 
   if (warp == kKvWarps + 2) {
     // ---------------------------------------------------------------- lists
@@ -779,9 +784,10 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     }
     cp_async_wait<0>();
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
-      for (int c = tk - 1; c >= 0 && c >= tk - NB; --c)
+      for (int c = tk - 1; c >= max(0, tk - NB); --c)
         warp_wait(kv_full + c % NB, (c / NB) & 1, 200);
-      for (int c = gi; c > gi - NS && c >= 0; --c) warp_wait(q_full + c % NS, (c / NS) & 1, 200);
+      for (int c = gi - 1; c >= max(0, gi - NS); --c)
+        warp_wait(q_full + c % NS, (c / NS) & 1, 200);
     }
   } else if (warp == kKvWarps) {
     // ---------------------------------------------------------------- scores

@@ -78,6 +78,7 @@ struct TcFwdParams {
   int ht, hs, rows;        // heads per tile, tiles (PAIR: pairs of them) per unit and key head,
                            // rows per tile
   int nsplit;
+  int fail;                // failure-path test: the softmax warps give up their first wait
   int64_t n_tiles;         // splits counted
 };
 
@@ -181,7 +182,8 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  bool ok = true;  // false: a wait gave up, leave
+  // false: a wait gave up, leave
+  bool ok = !(p.fail && warp < kSoftWarps);
 
   if (warp == kLists) {
     // ---------------------------------------------------------------- lists
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     const int per = kT / g.block;  // blocks per step
     const uint32_t blk_bytes = uint32_t(g.block) * 128;
     int gi = 0, ti = 0, tq = 0;
+    int nk = 0, nv = 0;  // steps whose K, V have been asked for
     for (int64_t t = blockIdx.x; t < p.n_tiles && ok; t += gridDim.x, ++ti) {
       const int slot = ti & 1;
       ok = warp_wait(tile_full + slot, (ti >> 1) & 1);
@@ -276,6 +279,8 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
                        kv ? &p.mv : &p.mk, kb * 64, kh, kbeg + list[st * per + b] * g.block,
                        full);
           }
+          if (kv) ++nv;
+          else ++nk;
         }
         if (!ok) break;
       }
@@ -284,11 +289,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       if (lane == 0) mbar_arrive(tile_empty + slot);
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
-      for (int i = 1; i <= NQ && i <= tq; ++i)
-        warp_wait(q_full + (tq - i) % NQ, ((tq - i) / NQ) & 1, 200);
-      for (int c = gi; c > gi - NS && c >= 0; --c)  // the newest use of each stage
+      for (int c = tq - 1; c >= max(0, tq - NQ); --c)  // the newest use of each stage
+        warp_wait(q_full + c % NQ, (c / NQ) & 1, 200);
+      for (int c = nk - 1; c >= max(0, nk - NS); --c)
         warp_wait(k_full + c % NS, (c / NS) & 1, 200);
-      for (int c = gi; c > gi - NV && c >= 0; --c)
+      for (int c = nv - 1; c >= max(0, nv - NV); --c)
         warp_wait(v_full + c % NV, (c / NV) & 1, 200);
     }
   } else if (warp == kMma) {
@@ -729,6 +734,7 @@ gattn_status launch_block_fwd_tc(const BlockGeom& g, const void* Q, const void* 
   p.hs = s.hs;
   p.rows = s.rows;
   p.nsplit = s.nsplit;
+  p.fail = block_wait_test();
   p.n_tiles = s.tiles * s.nsplit;
   p.part_o = static_cast<float*>(ws);
   p.part_l = p.part_o + (s.nsplit > 1 ? s.tiles * s.nsplit * s.rows * g.D : 0);

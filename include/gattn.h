@@ -560,6 +560,16 @@ GATTN_API gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void*
 GATTN_API gattn_status gattn_block_check_errors(void);
 
 /*
+ * Test hook for the failure path above (not part of the method): with
+ * fail_first_wait nonzero, the computing warps of the bf16 block-attention
+ * kernels launched from then on, by any thread, treat their first wait as
+ * expired; the others run into the limits of theirs, wait for what
+ * they have in flight and return, and gattn_block_check_errors reports
+ * GATTN_ERR_TIMEOUT.  Zero restores normal operation.  Host call.
+ */
+GATTN_API gattn_status gattn_block_set_wait_test(int32_t fail_first_wait);
+
+/*
  * The step between two blocks of a transformer layer, fused:
  *   u = norm(x; w_post, b_post)   (u = x without w_post)
  *   h = res + alpha * gate * u    (h = res without x)
