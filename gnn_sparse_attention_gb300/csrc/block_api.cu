@@ -147,16 +147,8 @@ constexpr int64_t kMaxItems = INT32_MAX - 65536;  // every CTA counts one item p
 BlockBwdWs bwd_ws(const BlockGeom& g, bool f32) {
   BlockBwdWs w{};
   w.words = (g.U + 31) / 32;
-  // Work items: about four per SM when every unit lists topk blocks of other
-  // key tiles, at least 32 tiles of 128 rows each (fp32, whose products take
-  // twenty times as long: 1); more items than that cost partials (128 x 2D fp32
-  // each) without filling the GPU better.
   const int64_t entries = int64_t(g.U) * g.Hkv * g.topk;
-  const int rows = g.qb * g.G;
-  const int64_t least =
-      std::max<int64_t>(1, int64_t(f32 ? 1 : 32) * kBlkTile / std::max(rows, kBlkTile));
-  const int64_t per = (entries + int64_t(sm_count()) * 4 - 1) / (int64_t(sm_count()) * 4);
-  w.chunk = int(std::min<int64_t>(std::max(least, per), INT32_MAX));
+  w.chunk = item_units(entries, g.qb * g.G, sm_count(), f32);
   w.slots = item_slots(entries, w.chunk);
   w.max_items = int64_t(g.KT) * g.Hkv + w.slots;
   size_t o = 0;

@@ -27,9 +27,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait of a whole warp: the same answer in every lane, so that a wait
-// that gives up takes the warp out of its loop together.
+// that gives up takes the warp out of its loop together.  A poll returns after 4 us
+// (measured; kSuspendNs asks for more).  A warp may have to wait for a whole work
+// item, up to 0.1 s, so it gives up after a second.  What a CTA that gave up has in
+// flight lands within microseconds; it waits 20 ms for each.
+constexpr uint32_t kRoleLimit = 250000, kDrainLimit = 5000;
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          uint32_t limit = kWaitLimit) {
+                                          uint32_t limit = kRoleLimit) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
 }
 

@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int c = tq - 1; c >= max(0, tq - NQ); --c)  // the newest use of each stage
-        warp_wait(q_full + c % NQ, (c / NQ) & 1, 200);
+        warp_wait(q_full + c % NQ, (c / NQ) & 1, kDrainLimit);
       for (int c = nk - 1; c >= max(0, nk - NK); --c)
-        warp_wait(k_full + c % NK, (c / NK) & 1, 200);
+        warp_wait(k_full + c % NK, (c / NK) & 1, kDrainLimit);
       for (int c = nv - 1; c >= max(0, nv - NV); --c)
-        warp_wait(v_full + c % NV, (c / NV) & 1, 200);
+        warp_wait(v_full + c % NV, (c / NV) & 1, kDrainLimit);
     }
   } else if (warp == kDqWarps) {
     // ---------------------------------------------------------------- products
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kDqThr, 1) block_dq_tc(const __grid_constant__
     if (!ok) {  // whatever was issued has completed before TMEM is given up
       for (int k = 0; k <= 2 && k <= gi; ++k) {
         const int c = gi - k;
-        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
-        warp_wait(k_empty + c % NK, (c / NK) & 1, 200);
+        warp_wait(s_full + (c & 1), (c >> 1) & 1, kDrainLimit);
+        warp_wait(k_empty + c % NK, (c / NK) & 1, kDrainLimit);
       }
     }
   } else if (warp >= kDqWarps + 3) {
@@ -785,9 +785,9 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     cp_async_wait<0>();
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int c = tk - 1; c >= max(0, tk - NB); --c)
-        warp_wait(kv_full + c % NB, (c / NB) & 1, 200);
+        warp_wait(kv_full + c % NB, (c / NB) & 1, kDrainLimit);
       for (int c = gi - 1; c >= max(0, gi - NS); --c)
-        warp_wait(q_full + c % NS, (c / NS) & 1, 200);
+        warp_wait(q_full + c % NS, (c / NS) & 1, kDrainLimit);
     }
   } else if (warp == kKvWarps) {
     // ---------------------------------------------------------------- scores
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
       ++tk;
     }
     if (!ok)  // what was issued completes before TMEM is given up
-      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
+      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(s_full + (c & 1), (c >> 1) & 1, kDrainLimit);
   } else if (warp == kKvWarps + 3) {
     // ---------------------------------------------------------------- gradients
     constexpr uint32_t IDESC_G = f16_idesc(kT, DP, true);
@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(kKvThr, 1) block_dkv_tc(const __grid_constant_
     // every product has completed before TMEM is given up
     if (ok && tk > 0) ok = warp_wait(g_full, (tk - 1) & 1);
     if (!ok)
-      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(q_empty + c % NS, (c / NS) & 1, 200);
+      for (int c = gi; c >= 0 && c > gi - 3; --c) warp_wait(q_empty + c % NS, (c / NS) & 1, kDrainLimit);
   } else if (warp >= kKvWarps + 4) {
     // ---------------------------------------------------------------- output
     const int quad = warp & 3, r = quad * 32 + lane;  // key

@@ -290,11 +290,11 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
     }
     if (!ok) {  // the copies in flight must land before the CTA's memory is given up
       for (int c = tq - 1; c >= max(0, tq - NQ); --c)  // the newest use of each stage
-        warp_wait(q_full + c % NQ, (c / NQ) & 1, 200);
+        warp_wait(q_full + c % NQ, (c / NQ) & 1, kDrainLimit);
       for (int c = nk - 1; c >= max(0, nk - NS); --c)
-        warp_wait(k_full + c % NS, (c / NS) & 1, 200);
+        warp_wait(k_full + c % NS, (c / NS) & 1, kDrainLimit);
       for (int c = nv - 1; c >= max(0, nv - NV); --c)
-        warp_wait(v_full + c % NV, (c / NV) & 1, 200);
+        warp_wait(v_full + c % NV, (c / NV) & 1, kDrainLimit);
     }
   } else if (warp == kMma) {
     // ---------------------------------------------------------------- products
@@ -374,8 +374,8 @@ __global__ void __launch_bounds__(kThr, 1) block_fwd_tc(const __grid_constant__ 
       const int c = gi - k;
       if (ok) ok = warp_wait(pv_done + (c & 1), (c >> 1) & 1);
       if (!ok) {
-        warp_wait(s_full + (c & 1), (c >> 1) & 1, 200);
-        warp_wait(pv_done + (c & 1), (c >> 1) & 1, 200);
+        warp_wait(s_full + (c & 1), (c >> 1) & 1, kDrainLimit);
+        warp_wait(pv_done + (c & 1), (c >> 1) & 1, kDrainLimit);
       }
     }
   } else if (warp < kSoftWarps) {

@@ -563,7 +563,7 @@ GATTN_API gattn_status gattn_block_check_errors(void);
  * Test hook for the failure path above (not part of the method): with
  * fail_first_wait nonzero, the computing warps of the bf16 block-attention
  * kernels launched from then on, by any thread, treat their first wait as
- * expired; the others run into the limits of theirs, wait for what
+ * expired; the others run into the limit of theirs (a second), wait for what
  * they have in flight and return, and gattn_block_check_errors reports
  * GATTN_ERR_TIMEOUT.  Zero restores normal operation.  Host call.
  */

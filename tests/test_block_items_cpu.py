@@ -16,6 +16,9 @@ TILE, SMS = 128, 152
 DRIVER = r"""
 #include "block_items.cuh"
 struct Item { int x, y, z, w; };
+extern "C" int units_of(int64_t entries, int rows, int sms, int f32) {
+  return gattn::item_units(entries, rows, sms, f32 != 0);
+}
 extern "C" int64_t slots_of(int64_t entries, int chunk) { return gattn::item_slots(entries, chunk); }
 // what items_kernel does, tile after tile instead of by a scan: returns the items to walk
 extern "C" int64_t cut(int n, int chunk, int64_t slots, int64_t max_items, int32_t* cnt, Item* items) {
@@ -41,6 +44,7 @@ def lib(tmp_path_factory):
     lib = ctypes.CDLL(os.fspath(so))
     i64, i32, P = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
     lib.slots_of.argtypes, lib.slots_of.restype = [i64, i32], i64
+    lib.units_of.argtypes = [i64, i32, i32, i32]
     lib.cut.argtypes, lib.cut.restype = [i32, i32, i64, i64, P, P], i64
     return lib
 
@@ -52,14 +56,12 @@ def clamp(x, lo, hi):
 class Case:
     """Sequences, lists and what the mark and count kernels make of them."""
 
-    def __init__(self, sq, sk, Nq, Nk, Hkv, G, block, qb, topk, seed, f32, pick=None):
+    def __init__(self, lib, sq, sk, Nq, Nk, Hkv, G, block, qb, topk, seed, f32, pick=None):
         self.S = S = len(sq) - 1
         self.U = Nq // qb + (S if qb > 1 else 0)
         B, self.KT = Nk // block + S, Nk // TILE + S
         self.Hkv, self.entries = Hkv, self.U * Hkv * topk
-        rows = qb * G
-        least = max(1, (1 if f32 else 32) * TILE // max(rows, TILE))
-        self.chunk = max(least, -(-self.entries // (SMS * 4)))
+        self.chunk = lib.units_of(self.entries, qb * G, SMS, f32)
 
         def base(beg, s, per):
             return max(beg[s], 0) // per + (s if per > 1 else 0)
@@ -169,7 +171,7 @@ def test_offsets_in_order_have_room(lib, seed):
         sq.append(sq[-1] + a)
         sk.append(sk[-1] + b)
     pick = r.choice([None, None, 0])
-    c = Case(sq, sk, sq[-1] + r.randint(0, 200), sk[-1] + r.randint(0, 200), r.choice([1, 2]),
+    c = Case(lib, sq, sk, sq[-1] + r.randint(0, 200), sk[-1] + r.randint(0, 200), r.choice([1, 2]),
              r.choice([1, 4]), block, qb, r.choice([1, 5, 16]), seed, r.random() < 0.7, pick)
     assert c.counts[c.counts > 0].sum() <= c.entries
     for chunk in {c.chunk, 1, 7}:  # (1 and 7: more tiles of several items)
@@ -185,7 +187,7 @@ def test_offsets_out_of_order_stay_inside(lib, S, pick, f32):
     """Offsets 0, N, 0, N, ...: neighbouring tiles count the same bits."""
     N = 4096
     o = [0 if i % 2 == 0 else N for i in range(S + 1)]
-    c = Case(o, o, N, N, 1, 1, 16, 128, 1, 5, f32, pick)
+    c = Case(lib, o, o, N, N, 1, 1, 16, 128, 1, 5, f32, pick)
     walked, _, slots = cut(lib, c.counts, c.chunk, c.entries, 1)
     wanted = sum(-(-x // c.chunk) for x in c.counts.reshape(-1).tolist() if x > c.chunk)
     if f32 and S > 3 and pick == 0:
@@ -200,3 +202,14 @@ def test_any_counts_stay_inside(lib, seed):
     n, chunk, entries = r.randint(1, 400), r.choice([1, 2, 33]), r.randint(0, 3000)
     counts = [r.choice([-1, 0, 1, chunk, chunk + 1, r.randint(0, 500)]) for _ in range(n)]
     cut(lib, counts, chunk, entries, 1)
+
+
+@pytest.mark.parametrize("f32", [0, 1])
+@pytest.mark.parametrize("rows", [1, 16, 128, 16384])
+def test_units_of_an_item(lib, rows, f32):
+    """Four items an SM of large problems, none of them longer than 2^17 steps of 64 rows."""
+    for entries in (0, 1, 607, 100000, 10 ** 7, 10 ** 9, 10 ** 12):
+        n = lib.units_of(entries, rows, SMS, f32)
+        assert 1 <= n and n * rows <= 2 ** 23
+        if entries // (SMS * 4) >= 32 and entries // (SMS * 4) < 2 ** 23 // rows:
+            assert n == -(-entries // (SMS * 4))
