@@ -734,3 +734,22 @@ def test_items_that_take_long():
         rows = slice(k * n, k * n + n)
         for t, name in ((out, "out"), (lse, "lse"), (got[0], "dQ")):
             ref.check(t[rows], r, name)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,D,H,Hkv", [("bf16", 32, 4, 4), ("bf16", 128, 4, 2), ("f32", 16, 2, 2)])
+def test_many_small_graphs(dtype, D, H, Hkv, causal):
+    """A batch of 600 graphs of 0 to 40 nodes: choice, attention and gradients."""
+    g = torch.Generator().manual_seed(31)
+    lens = torch.randint(0, 41, (600,), generator=g).tolist()
+    sq = ref.offsets(lens)
+    Q, K = randn(210, sq[-1], H, D, dtype=DT[dtype]), randn(211, sq[-1], Hkv, D, dtype=DT[dtype])
+    sums = gb.gattn_block_sums(K, i32(sq), 16)
+    idx = gb.gattn_block_select(Q, sums, i32(sq), i32(sq), 2, 16, 32, sq[-1], causal=causal, max_len_k=40)
+    assert torch.equal(idx[:ref.units(sq[-1], 600, 32)].cpu(), ref.select(Q, K, sq, sq, 2, 16, 32, causal))
+
+    def edit(q, k, v, *_):
+        q.copy_(Q)
+        k.copy_(K)
+
+    run(212, lens, lens, H, Hkv, D, dtype, 16, 32, 2, causal, idx=idx, edit=edit)

@@ -142,6 +142,15 @@ def test_row_counts(N, dtype, F):
     check(N, F, dtype, "layer", "channel")
 
 
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,F", [(12000, 257), (9000, 520), (6000, 777), (5000, 1026), (3000, 2048), (2000, 2056),
+                                 (1500, 4095), (1000, 5120), (800, 8191), (800, 8192), (600, 8200), (600, 16384)])
+def test_many_rows_of_every_shape(N, F, dtype, gate):
+    """Rows enough that every CTA walks four and more, at each way that a row is laid out."""
+    check(N, F, dtype, "layer", gate)
+
+
 @pytest.mark.parametrize("F", [64, 1024])
 def test_first_norm_of_a_model(F):
     """Without x: h is res, y its norm; the gradient of res is that of y plus dh."""
