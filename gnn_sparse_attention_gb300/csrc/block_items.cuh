@@ -25,14 +25,15 @@ namespace gattn {
 // Units of an item: about four items per SM when every unit lists topk blocks of
 // other key tiles, at least 32 tiles of 128 rows each (fp32, whose products take
 // twenty times as long: 1); more items than that cost partials (128 x 2D fp32
-// each) without filling the GPU better.  At most 2^23 rows, though: a warp that
-// writes an item's results waits for all of it, 2^17 steps of 64 rows or about
-// 0.1 s then, and gives up after a second.
+// each) without filling the GPU better.  At most 2^23 rows and 2^18 units, though: a
+// warp that writes an item's results waits for all of it, and gives up after a
+// second.  64 rows take 0.6 to 1 us (2^23: 0.13 s), a unit of few rows 0.3 us (2^18:
+// 0.1 s), measured.
 inline int item_units(int64_t entries, int rows, int sms, bool f32) {
   const int tile = rows > 128 ? rows : 128;
   const int64_t some = int64_t(f32 ? 1 : 32) * 128 / tile, least = some > 1 ? some : 1;
   const int64_t per = (entries + int64_t(sms) * 4 - 1) / (int64_t(sms) * 4);
-  const int64_t most = (int64_t(1) << 23) / rows;
+  const int64_t most = (int64_t(1) << 23) / (rows > 32 ? rows : 32);
   return int(per < least ? least : per > most ? most : per);
 }
 

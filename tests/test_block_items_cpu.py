@@ -207,9 +207,9 @@ def test_any_counts_stay_inside(lib, seed):
 @pytest.mark.parametrize("f32", [0, 1])
 @pytest.mark.parametrize("rows", [1, 16, 128, 16384])
 def test_units_of_an_item(lib, rows, f32):
-    """Four items an SM of large problems, none of them longer than 2^17 steps of 64 rows."""
+    """Four items an SM of large problems, none of them of more than 2^23 rows or 2^18 units."""
     for entries in (0, 1, 607, 100000, 10 ** 7, 10 ** 9, 10 ** 12):
         n = lib.units_of(entries, rows, SMS, f32)
-        assert 1 <= n and n * rows <= 2 ** 23
-        if entries // (SMS * 4) >= 32 and entries // (SMS * 4) < 2 ** 23 // rows:
+        assert 1 <= n <= 2 ** 18 and n * rows <= 2 ** 23
+        if 32 <= entries // (SMS * 4) < 2 ** 23 // max(rows, 32):
             assert n == -(-entries // (SMS * 4))
