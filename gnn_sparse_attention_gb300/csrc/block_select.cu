@@ -14,11 +14,11 @@
 // norms leave the range in which that bound holds, all are.  Which blocks the
 // causal mask leaves, and which of them come first, follows from positions alone.
 //
-// Measured: sums over 65,536 nodes of 8 heads of 64 (bf16) 19.5 us, 3.4 TB/s, with
+// Measured: sums over 65,536 nodes of 8 heads of 64 (bf16) 20 us, 3.3 TB/s, with
 // issue slots half busy with the exact additions; the choice of 16 of 43 blocks for
-// 547 units and 8 heads 26 us, a chain of small phases (scores, radix passes,
+// 547 units and 8 heads 21 us, a chain of small phases (scores, radix passes,
 // fp64 scores of the undecided) with one to four CTAs an SM; for 8 single tokens
-// against caches of about 4,000 keys 4.0 and 11 us.
+// against caches of about 4,000 keys 4.2 and 11 us.
 #include <algorithm>
 
 #include "attn_launch.cuh"

@@ -32,7 +32,10 @@
 //   64 rather than 128 queries a step leave room for several stages of Q and
 //   dO and a second score buffer next to the two accumulators; two groups of
 //   eight warps take the steps in turn, so that one forms p and ds while the other
-//   waits for its products.  (A third group at D <= 64 left 72 registers a thread:
+//   waits for its products.  p and ds enter these products as one bf16 each, which
+//   leaves dV and dK 1.4 times as far off as their own rounding (0.0024 against
+//   0.0017); ds as two would be a fifth product of four, and at D <= 64 TMEM has no
+//   64 columns left for it.  (A third group at D <= 64 left 72 registers a thread:
 //   its spills filled what shared memory leaves of L1, 532 us against 471.)  Four
 //   more warps write a finished item.  Units of fewer than 64 pairs share a step,
 //   each in a box of its own; a box knows which of the tile's blocks its unit

@@ -19,13 +19,17 @@
 // as fit run, and each walks its rows; a thread copies its own elements of
 // the next rows into shared memory with cp.async, one or two rows ahead -- it
 // reads back only what it copied, so the ring needs no barrier, and the bytes
-// in flight (about 100 KB an SM) do not cost registers.  Arithmetic is on pairs
+// in flight do not cost registers (80 to 100 KB an SM up to 1,024 columns; the
+// backward of longer rows 40 to 80 KB, none beyond 8,192, whose rows are read
+// where they are used).  Arithmetic is on pairs
 // (fma.rn.f32x2): unpaired, the forward issues 30 instructions an element and
 // is bound by them.  Up to 1,024 elements the forward gives a row to one warp
 // and needs no block barrier.  The backward carries five fp32 column sums per
 // element (dw, db of both norms and the channel gate) over all rows of its
 // CTA and keeps its columns' weights in registers; the CTAs' sums meet in a
 // second small kernel, in CTA order, so results do not vary from run to run.
+// (From 4,097 columns on these sums do not fit its registers: 0.5 to 0.7 KB a
+// thread spilled, beyond 8,192 2 to 2.7 KB.)
 //
 // Measured: 8,192 x 4,096 bf16 forward 52 us (5.1 TB/s); 131,072 x 1,024 bf16 with
 // biases and a gate per node 229 us forward (5.9 TB/s) and 394 + 6 us backward (5.4);

@@ -179,9 +179,12 @@ def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torc
     Q: [Nq, H, D]; K, V: [Nk, Hkv, D]; seq: int32 [S + 1], the sequences' (graphs') first
     rows; seq_k and len_k (both optional) give the keys their own offsets and lengths.  ``idx``
     (int32 [units, Hkv, blocks], see gattn_block_select) replaces the choice; ``max_len_k``, the
-    most keys of one sequence (0: all rows), keeps its score tables small.  Returns
+    most keys of one sequence (0: all rows), keeps its score tables small (without it a batch may
+    have about 27,900 blocks together).  Returns
     (out [Nq, H, D], lse fp32 [Nq, H], idx).  out is differentiable in Q, K and V, once, and not
-    in the choice; lse carries no gradient.  Rows of no sequence get zeros.
+    in the choice; lse carries no gradient.  Rows of no sequence get zeros.  Kernels that give up
+    a bounded wait leave their results undefined and raise nothing here: gattn_block_check_errors,
+    which synchronises, tells.
     """
     Q, K, V = _packed(Q), _packed(K), _packed(V)
     keys = seq if seq_k is None else seq_k
@@ -247,7 +250,7 @@ class GraphTransformerBlock(nn.Module):
     edges (left out without a plan) and global that over the selected blocks of the node's own
     graph, both on the same heads of norm(h); then h = h + gate_m * norm(MLP(norm(h))).  The
     gates are learned per channel.  ``seq`` holds the graphs' first node rows, ``max_nodes``
-    (0: unknown) the size of the largest graph.
+    (0: unknown) the size of the largest graph; see block_attention for both, and for errors.
     """
 
     def __init__(self, dim: int, heads: int, head_dim: int, mlp_dim: int | None = None,

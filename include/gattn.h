@@ -528,10 +528,11 @@ GATTN_API gattn_status gattn_block_select(const gattn_block_desc* desc, const vo
 
 /*
  * Softmax attention of every query over the keys of the blocks that idx names
- * for its unit: out[Nq][H][D], lse fp32 [Nq][H] (natural log).  Units with few
- * rows are split over their blocks and joined when there are fewer of them
+ * for its unit: out[Nq][H][D], lse fp32 [Nq][H] (natural log).  With bf16,
+ * units are split over their blocks and joined when there are fewer of them
  * than the GPU has SMs.  `workspace` (16-byte aligned, no initialisation) may
- * be NULL when the size is 0; calls that may overlap need their own.
+ * be NULL when the size is 0; calls that may overlap need their own.  The weights
+ * enter the product with V in the tensors' type.
  */
 GATTN_API gattn_status gattn_block_fwd_workspace_size(const gattn_block_desc* desc, size_t* bytes);
 GATTN_API gattn_status gattn_block_fwd(const gattn_block_desc* desc, const void* Q, const void* K,
@@ -543,7 +544,11 @@ GATTN_API gattn_status gattn_block_fwd(const gattn_block_desc* desc, const void*
  * Backward of gattn_block_fwd (idx is not differentiated): dQ[Nq][H][D],
  * dK, dV[Nk][Hkv][D] (written, not accumulated; keys that no query sees get 0).
  * The weights are recomputed from lse.  Sums over queries run in a fixed
- * order, so results do not vary from run to run.
+ * order, so results do not vary from run to run.  The workspace holds one bit for
+ * every (block, key head, unit) of the whole call, sequences together: blocks *
+ * Hkv * units / 8 bytes, cleared on every call, which grows with the square of the
+ * rows (131,072 rows in blocks and units of 64 with 8 key heads: 4 MB; a million
+ * rows in blocks and units of 16: 4 GB).  Split large batches of short sequences.
  */
 GATTN_API gattn_status gattn_block_bwd_workspace_size(const gattn_block_desc* desc, size_t* bytes);
 GATTN_API gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void* Q, const void* K,
@@ -554,8 +559,10 @@ GATTN_API gattn_status gattn_block_bwd(const gattn_block_desc* desc, const void*
 
 /*
  * Synchronise the current device and report whether a block-attention kernel
- * on it gave up a bounded wait since the last check (GATTN_ERR_TIMEOUT; its
- * outputs are undefined, the library stays usable).  Clears the record.
+ * on it gave up a bounded wait (of a second; the longest that it waits in
+ * ordinary operation is about a tenth of that) since the last check
+ * (GATTN_ERR_TIMEOUT; its outputs are undefined, the library stays usable).
+ * Clears the record.
  */
 GATTN_API gattn_status gattn_block_check_errors(void);
 
