@@ -152,6 +152,23 @@ def test_second_derivatives_are_refused():
             (g.pow(2).sum() + leaf.sum()).backward()
 
 
+def test_create_graph_alone_changes_nothing():
+    """backward(create_graph=True) without a second derivative: gradients that an optimiser can
+    detach, zero and add to."""
+    torch.manual_seed(10)
+    m = layer.GraphTransformerBlock(64, 2, 32, topk=2, dtype=torch.float32, device=DEV)
+    h, seq = torch.randn(50, 64, device=DEV), i32([0, 50])
+    opt = torch.optim.SGD(m.parameters(), lr=0.0)
+    (m(h, seq).pow(2)).sum().backward()
+    want = [p.grad.clone() for p in m.parameters()]
+    opt.zero_grad(set_to_none=True)
+    for _ in range(2):
+        m(h, seq).pow(2).sum().backward(create_graph=True)
+        assert all(torch.equal(p.grad, w) for p, w in zip(m.parameters(), want))
+        opt.zero_grad(set_to_none=False)
+    assert not any(p.grad.any() for p in m.parameters())
+
+
 def test_gated_residual_norm_parts_without_a_gradient():
     """Only one of the two results is used; a gate or a norm is left out."""
     torch.manual_seed(3)
