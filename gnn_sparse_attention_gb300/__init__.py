@@ -13,7 +13,9 @@ __all__ = ["Score", "Plan", "GattnError", "gattn_plan_create", "gattn_plan_get_i
            "gattn_permute_rows", "gattn_pool_workspace_size", "gattn_pool_fwd", "gattn_pool_bwd",
            "gattn_spmm_workspace_size", "gattn_spmm", "gattn_block_units", "gattn_block_count",
            "gattn_block_sums", "gattn_block_select", "gattn_block_fwd", "gattn_block_bwd",
-           "gattn_block_check_errors", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_version",
+           "gattn_block_check_errors", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_rotary",
+           "gattn_rotary_freqs", "Cache", "gattn_cache_new", "gattn_cache_write",
+           "gattn_cache_read", "gattn_cache_sums", "gattn_cache_fwd", "gattn_version",
            "load_library"]
 
 

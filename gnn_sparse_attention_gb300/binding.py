@@ -33,7 +33,9 @@ EXPORTED = ("gattn_plan_create", "gattn_plan_destroy", "gattn_plan_get_info",
             "gattn_block_select", "gattn_block_fwd_workspace_size", "gattn_block_fwd",
             "gattn_block_bwd_workspace_size", "gattn_block_bwd", "gattn_block_check_errors",
             "gattn_block_set_wait_test",
-            "gattn_norm_workspace_size", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_last_error",
+            "gattn_norm_workspace_size", "gattn_norm_fwd", "gattn_norm_bwd", "gattn_rotary",
+            "gattn_rotary_freqs", "gattn_cache_write", "gattn_cache_read", "gattn_cache_sums",
+            "gattn_cache_fwd_workspace_size", "gattn_cache_fwd", "gattn_last_error",
             "gattn_version")
 
 
@@ -78,6 +80,25 @@ class _NormDesc(ctypes.Structure):
                 ("kind", ctypes.c_int32), ("gate", ctypes.c_int32), ("alpha", ctypes.c_float),
                 ("eps", ctypes.c_float), ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p),
                 ("w_pre", ctypes.c_void_p), ("b_pre", ctypes.c_void_p)]
+
+
+class _RotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "Hkv", "D", "dtype", "width", "layout",
+                                              "inverse", "S")]
+    _fields_ += [("amp", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("freqs", "pos", "seq_q", "seq_k", "len_k")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride",
+                                              "k_out_stride")]
+
+
+class _CacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "N", "Nk", "H", "Hkv", "D", "dtype", "bits",
+                                              "block", "topk", "causal")]
+    _fields_ += [("scale", ctypes.c_float), ("max_len_k", ctypes.c_int32),
+                 ("seq_q", ctypes.c_void_p), ("seq_k", ctypes.c_void_p),
+                 ("len_k", ctypes.c_void_p), ("idx_stride", ctypes.c_int64 * 2),
+                 ("row_stride", ctypes.c_int64 * 2), ("k", ctypes.c_void_p),
+                 ("v", ctypes.c_void_p), ("par", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -148,6 +169,14 @@ def load_library(path: str | None = None):
         lib.gattn_norm_workspace_size.argtypes = [nd, psz]
         lib.gattn_norm_fwd.argtypes = [nd] + [P] * 7
         lib.gattn_norm_bwd.argtypes = [nd] + [P] * 14 + [sz, P]
+        f64 = ctypes.c_double
+        lib.gattn_rotary.argtypes = [P] * 6
+        lib.gattn_rotary_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+        lib.gattn_cache_write.argtypes = [P] * 4
+        lib.gattn_cache_read.argtypes = [P] * 5
+        lib.gattn_cache_sums.argtypes = [P] * 4
+        lib.gattn_cache_fwd_workspace_size.argtypes = [P, psz]
+        lib.gattn_cache_fwd.argtypes = [P] * 6 + [sz, P]
         for name in EXPORTED:
             if name not in ("gattn_last_error", "gattn_version"):
                 getattr(lib, name).restype = st
@@ -917,3 +946,278 @@ def gattn_norm_bwd(res, stats, dh=None, dy=None, x=None, gate=None, w_post=None,
         desc, res.data_ptr(), stats.data_ptr(), _at(dh), _at(dy), _at(x), _at(gate),
         *[_at(t) for t in g.values()], _at(ws), _bytes(ws), handle), "gattn_norm_bwd")
     return g
+
+
+# ----------------------------------------------------------------------------
+# rotary positions, and a cache of keys and values in 4 or 8 bits
+# ----------------------------------------------------------------------------
+_ROTARY_PACK = struct.Struct("@9if5P4q")            # _RotaryDesc
+_CACHE_PACK = struct.Struct("@11ifi4x3P4q3P")       # _CacheDesc
+assert _ROTARY_PACK.size == ctypes.sizeof(_RotaryDesc)
+assert _CACHE_PACK.size == ctypes.sizeof(_CacheDesc)
+ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
+ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+def _row_stride(name, t, H, D, dtype, dev):
+    """Elements between the rows of t [N, H, D], whose heads lie side by side (as in a slice of
+    a joint projection)."""
+    if t.get_device() != dev or t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (H, D):
+        raise ValueError(f"{name} must be a CUDA tensor, {dtype}, of shape (N, {H}, {D}), on "
+                         f"device {dev}")
+    sn, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if t.shape[0] <= 1:
+        return H * D
+    if sn < H * D:
+        raise ValueError(f"{name}: rows must not overlap")
+    return sn
+
+
+def gattn_rotary_freqs(width: int, theta: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, orig_len: float = 0.0, low: float = 1.0,
+                       high: float = 32.0, device="cuda") -> torch.Tensor:
+    """Frequencies of the width / 2 pairs of a head for gattn_rotary, int64 [width / 2]: turns
+    per position in units of 2^-64 (include/gattn.h).  ``scaling``: "none", or for contexts
+    longer than those of training "linear", "base" or "ramp" (with ``orig_len``)."""
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {tuple(ROTARY_SCALING)}, got {scaling!r}")
+    out = (ctypes.c_uint64 * max(width // 2, 1))()
+    _check(load_library().gattn_rotary_freqs(width, theta, ROTARY_SCALING[scaling], factor,
+                                             orig_len, low, high, ctypes.addressof(out)),
+           "gattn_rotary_freqs")
+    return torch.from_numpy(np.frombuffer(out, dtype=np.int64).copy()).to(device)
+
+
+def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "half", pos=None,
+                 seq_q=None, seq_k=None, len_k=None, amp: float = 1.0, inverse: bool = False,
+                 out_q=None, out_k=None, stream=None):
+    """Q [N, H, D] and K [N, Hkv, D] (or None) with the first 2 * len(freqs) elements of every
+    head turned by the rows' positions: (Q', K').
+
+    Positions are ``pos`` (int32 [N]), or those of the rows of sequences as the block and cache
+    attention counts them (``seq_q``, and the keys' ``seq_k`` and ``len_k`` where sequences hold
+    more than the new rows).  Rows of Q and K may lie apart, as slices of a joint projection do;
+    ``out_q`` and ``out_k`` may be Q and K themselves.  ``inverse`` turns back, as a backward does.
+    Rows of no sequence are not written.
+    """
+    if not Q.is_cuda or Q.dim() != 3:
+        raise ValueError(f"Q must be a CUDA tensor [N, H, D], has the shape {tuple(Q.shape)}")
+    dev = Q.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_rotary(Q, freqs, K, layout, pos, seq_q, seq_k, len_k, amp, inverse, out_q,
+                                out_k, stream)
+    N, H, D = Q.shape
+    if layout not in ROTARY_LAYOUT:
+        raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUT)}, got {layout!r}")
+    width = 2 * freqs.numel()
+    _want("freqs", freqs, (width // 2,), torch.int64, dev)
+    qs = _row_stride("Q", Q, H, D, Q.dtype, dev)
+    Hkv, ks, ko = 0, 0, 0
+    if K is not None:
+        if K.dim() != 3 or K.shape[0] != N:
+            raise ValueError(f"K must have the {N} rows of Q, has the shape {tuple(K.shape)}")
+        Hkv = K.shape[1]
+        ks = _row_stride("K", K, Hkv, D, Q.dtype, dev)
+    elif out_k is not None:
+        raise ValueError("out_k needs K")
+    if pos is not None:
+        if seq_q is not None or seq_k is not None or len_k is not None:
+            raise ValueError("give pos or sequences, not both")
+        _want("pos", pos, (N,), torch.int32, dev)
+        S = 0
+    else:
+        if seq_q is None:
+            raise ValueError("positions need pos or seq_q")
+        S = _sequences(seq_q, seq_q if seq_k is None else seq_k, len_k, dev)
+    handle, other = _stream_of(dev, stream)
+    outs = []
+    for name, t, o, h in (("out_q", Q, out_q, H), ("out_k", K, out_k, Hkv)):
+        if t is None:
+            outs.append((None, 0))
+            continue
+        if o is None:
+            o = _new(dev, other, t.shape, t.dtype)
+        elif o.shape != t.shape:
+            raise ValueError(f"{name} must have the shape {tuple(t.shape)}")
+        outs.append((o, _row_stride(name, o, h, D, Q.dtype, dev)))
+    (oq, qos), (ok, kos) = outs
+    desc = _ROTARY_PACK.pack(N, H, Hkv, D, _dtype_code(Q.dtype), width, ROTARY_LAYOUT[layout],
+                             1 if inverse else 0, S, amp, freqs.data_ptr(), _at(pos) or 0,
+                             _at(seq_q) or 0, _at(seq_k) or 0, _at(len_k) or 0, qs, ks, qos, kos)
+    _check((_lib or load_library()).gattn_rotary(desc, Q.data_ptr(), _at(K), oq.data_ptr(),
+                                                 _at(ok), handle), "gattn_rotary")
+    return oq, ok
+
+
+class Cache:
+    """Keys and values in 4 or 8 bits (include/gattn.h): ``k`` and ``v`` uint8
+    [Hkv, rows, D * bits / 8], ``par`` bf16 [Hkv, rows, 4]."""
+
+    __slots__ = ("k", "v", "par", "bits", "rows", "Hkv", "D", "device")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, par: torch.Tensor, bits: int):
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, got {bits}")
+        dev = _cuda_index("k", k, 3)
+        self.Hkv, self.rows, row = k.shape
+        _want("k", k, k.shape, torch.uint8, dev)
+        _want("v", v, k.shape, torch.uint8, dev)
+        _want("par", par, (self.Hkv, self.rows, 4), torch.bfloat16, dev)
+        self.D = row * 8 // bits
+        self.k, self.v, self.par, self.bits, self.device = k, v, par, bits, dev
+
+
+def gattn_cache_new(rows: int, Hkv: int, D: int, bits: int = 4, device="cuda") -> Cache:
+    """An empty cache with room for ``rows`` rows of all sequences together."""
+    if D not in (32, 64, 128):
+        raise ValueError(f"D must be 32, 64 or 128, got {D}")
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    k, v = (torch.zeros(Hkv, rows, D * bits // 8, dtype=torch.uint8, device=device)
+            for _ in range(2))
+    return Cache(k, v, torch.zeros(Hkv, rows, 4, dtype=torch.bfloat16, device=device), bits)
+
+
+def _cache_desc(c, S, N, H, dtype, block, topk, causal, scale, max_len_k, seq_q, seq_k, len_k,
+                su=0, sh=0, ks=0, vs=0):
+    return _CACHE_PACK.pack(S, N, c.rows, H, c.Hkv, c.D, _dtype_code(dtype), c.bits, block, topk,
+                            1 if causal else 0, scale, max_len_k,
+                            0 if seq_q is None else seq_q.data_ptr(), seq_k.data_ptr(),
+                            0 if len_k is None else len_k.data_ptr(), su, sh, ks, vs,
+                            c.k.data_ptr(), c.v.data_ptr(), c.par.data_ptr())
+
+
+def gattn_cache_write(cache: Cache, K: torch.Tensor, V: torch.Tensor, seq_q: torch.Tensor,
+                      seq_k: torch.Tensor, len_k=None, stream=None) -> None:
+    """Append the rows of K and V [N, Hkv, D] to their sequences: ``len_k`` counts them already.
+
+    Rows of K and V may lie apart (16-byte aligned), as slices of a joint projection do.
+    """
+    dev = cache.device
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_cache_write(cache, K, V, seq_q, seq_k, len_k, stream)
+    ks = _row_stride("K", K, cache.Hkv, cache.D, K.dtype, dev)
+    vs = _row_stride("V", V, cache.Hkv, cache.D, K.dtype, dev)
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V must have the same rows")
+    S = _sequences(seq_q, seq_k, len_k, dev)
+    desc = _cache_desc(cache, S, K.shape[0], cache.Hkv, K.dtype, 64, 0, False, 0.0, 0, seq_q, seq_k,
+                       len_k, 0, 0, ks, vs)
+    _check((_lib or load_library()).gattn_cache_write(desc, K.data_ptr(), V.data_ptr(),
+                                                      _stream_of(dev, stream)[0]),
+           "gattn_cache_write")
+
+
+def gattn_cache_read(cache: Cache, seq_q: torch.Tensor, seq_k: torch.Tensor, len_k=None, since=None,
+                     rows=None, dtype=torch.bfloat16, K=None, V=None, stream=None):
+    """Rows of the cache in ``dtype``: (K, V), each [rows, Hkv, D].
+
+    Row i of sequence s's [seq_q[s], seq_q[s+1]) is the one at position i + len_k[s] - lq (the
+    rows that gattn_cache_write appended), or i + since[s].  Rows without such a position are
+    not written; tensors that the call allocates hold anything there.  ``rows`` is needed where
+    neither K nor V is given.
+    """
+    dev = cache.device
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_cache_read(cache, seq_q, seq_k, len_k, since, rows, dtype, K, V, stream)
+    S = _sequences(seq_q, seq_k, len_k, dev)
+    if since is not None:
+        _want("since", since, (S,), torch.int32, dev)
+    given = K if K is not None else V
+    if given is not None:
+        rows, dtype = given.shape[0], given.dtype
+    elif rows is None:
+        raise ValueError("rows is needed where neither K nor V is given")
+    shape = (rows, cache.Hkv, cache.D)
+    handle, other = _stream_of(dev, stream)
+    if given is None:
+        K, V = _new(dev, other, shape, dtype), _new(dev, other, shape, dtype)
+    else:
+        for name, t in (("K", K), ("V", V)):
+            if t is not None:
+                _want(name, t, shape, dtype, dev)
+    desc = _cache_desc(cache, S, rows, cache.Hkv, dtype, 64, 0, False, 0.0, 0, seq_q, seq_k, len_k)
+    _check((_lib or load_library()).gattn_cache_read(desc, _at(since), _at(K), _at(V), handle),
+           "gattn_cache_read")
+    return K, V
+
+
+def gattn_cache_sums(cache: Cache, seq_k: torch.Tensor, block: int, lens=None, since=None, sums=None,
+                     stream=None) -> torch.Tensor:
+    """gattn_block_sums of the cached keys: fp64 sums [blocks, Hkv, D] of what they stand for."""
+    dev = cache.device
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_cache_sums(cache, seq_k, block, lens, since, sums, stream)
+    S = _sequences(seq_k, seq_k, lens, dev)
+    if since is not None:
+        _want("since", since, (S,), torch.int32, dev)
+        if sums is None:
+            raise ValueError("since needs sums, the table to renew")
+    shape = (gattn_block_count(cache.rows, S, block), cache.Hkv, cache.D)
+    handle, other = _stream_of(dev, stream)
+    if sums is None:
+        sums = _new(dev, other, shape, torch.float64)
+    else:
+        _want("sums", sums, shape, torch.float64, dev)
+    desc = _cache_desc(cache, S, 0, cache.Hkv, torch.float32, block, 0, False, 0.0, 0, None, seq_k,
+                       lens)
+    _check((_lib or load_library()).gattn_cache_sums(desc, _at(since), sums.data_ptr(), handle),
+           "gattn_cache_sums")
+    return sums
+
+
+def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: torch.Tensor,
+                    len_k=None, idx=None, block: int = 64, scale: float = 0.0,
+                    causal: bool = False, max_len_k: int = 0, out=None, lse=None, workspace=None,
+                    stream=None):
+    """Softmax attention of every row of Q [N, H, D] over the cache: (out, lse fp32 [N, H]).
+
+    ``idx`` (int32 [N, Hkv, topk]) names blocks of each row's own sequence, as for
+    gattn_block_fwd with q_block = 1; without it the whole sequence is read.  ``max_len_k`` is the
+    most rows of one sequence (0: all rows of the cache): a close bound lets short caches be
+    split well.  Rows of no sequence are not written.
+    """
+    dev = _cuda_index("Q", Q, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gattn_cache_fwd(Q, cache, seq_q, seq_k, len_k, idx, block, scale, causal,
+                                   max_len_k, out, lse, workspace, stream)
+    N, H, D = Q.shape
+    if cache.device != dev or cache.D != D:
+        raise ValueError(f"Q [N, H, {D}] on device {dev} needs a cache of that width there")
+    S = _sequences(seq_q, seq_k, len_k, dev)
+    topk = su = sh = 0
+    if idx is not None:
+        if idx.dim() != 3:
+            raise ValueError("idx must be [N, Hkv, topk]")
+        units, topk = N if S else 0, idx.shape[2]
+        su, sh, sl = idx.stride()
+        if (idx.get_device() != dev or idx.dtype != torch.int32 or idx.shape[0] != units
+                or idx.shape[1] != cache.Hkv or topk < 1 or (topk > 1 and sl != 1)):
+            raise ValueError(f"idx must be int32 of shape ({units}, {cache.Hkv}, topk) on device "
+                             f"{dev}, each list contiguous")
+        if su == 0 and sh == 0 and units * cache.Hkv > 1:
+            raise ValueError("idx repeats one list for all rows and heads; make it contiguous")
+    handle, other = _stream_of(dev, stream)
+    if out is None:
+        out = _like(Q, other)
+    else:
+        _want("out", out, Q.shape, Q.dtype, dev)
+    if lse is None:
+        lse = _new(dev, other, (N, H), torch.float32)
+    else:
+        _want("lse", lse, (N, H), torch.float32, dev)
+    desc = _cache_desc(cache, S, N, H, Q.dtype, block, topk, causal, scale, max_len_k, seq_q, seq_k,
+                       len_k, su, sh)
+    ws = _workspace(workspace, dev, other, "gattn_cache_fwd_workspace_size", desc,
+                    (S > 0, N, cache.rows, H, cache.Hkv, D, Q.dtype, block, topk, max_len_k))
+    _check((_lib or load_library()).gattn_cache_fwd(desc, Q.data_ptr(), _at(idx), out.data_ptr(),
+                                                    lse.data_ptr(), _at(ws), _bytes(ws), handle),
+           "gattn_cache_fwd")
+    return out, lse

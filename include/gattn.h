@@ -632,6 +632,145 @@ GATTN_API gattn_status gattn_norm_bwd(const gattn_norm_desc* desc, const void* r
                                       float* db_pre, void* workspace, size_t workspace_bytes,
                                       gattn_stream_t stream);
 
+/*
+ * Rotary positions: pairs (a, b) of the first `width` elements of every head are turned,
+ *   a' = amp (a cos t - b sin t),  b' = amp (a sin t + b cos t),  t = position * frequency,
+ * the pair i being elements (i, i + width / 2) with GATTN_ROTARY_HALF and (2i, 2i + 1)
+ * with GATTN_ROTARY_INTERLEAVED; the other elements are copied.  With `inverse` t is
+ * negated, which is the backward (applied to gradients).  Q [N, H, D] and K [N, Hkv, D]
+ * (Hkv = 0: none) are turned in one launch; rows may lie `*_stride` elements apart (0:
+ * contiguous), heads are contiguous.  Outputs may be the inputs themselves (same stride),
+ * else they must not overlap them.  Any D up to 1024, any number of heads.  Whole 16-byte
+ * vectors move where addresses, strides, D and width / 2 (HALF) or width (INTERLEAVED)
+ * allow it; other shapes go element by element.
+ *
+ * Position of row r: pos[r] (device int32 [N], any value) where pos is given; else r
+ * belongs to sequence s with seq_q[s] <= r < seq_q[s + 1] and stands at
+ *     r - seq_q[s] + len - (seq_q[s + 1] - seq_q[s]),
+ * len being len_k[s], or seq_k[s + 1] - seq_k[s], or the sequence's own rows, whichever is
+ * given first: the position that the attention over blocks or over a cache gives to that
+ * query.  Rows of no sequence are not written.
+ *
+ * Frequencies: device uint64 [width / 2], turns per position in units of 2^-64, so that
+ * position * frequency wraps to the exact fraction of a turn: an angle is off by less than
+ * 2^-29 of a turn at positions up to 2^22, and beyond by what fp64 leaves of the frequency.
+ */
+typedef enum { GATTN_ROTARY_HALF = 0, GATTN_ROTARY_INTERLEAVED = 1 } gattn_rotary_layout;
+
+typedef struct {
+  int32_t N, H, Hkv, D;
+  int32_t dtype;          /* gattn_dtype */
+  int32_t width, layout;  /* even, 2 .. D; gattn_rotary_layout */
+  int32_t inverse;
+  int32_t S;              /* sequences (where pos is NULL) */
+  float amp;
+  const uint64_t* freqs;  /* device [width / 2] */
+  const int32_t* pos;     /* device [N] or NULL */
+  const int32_t *seq_q, *seq_k, *len_k; /* device [S + 1], [S + 1] or NULL, [S] or NULL */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} gattn_rotary_desc;
+
+GATTN_API gattn_status gattn_rotary(const gattn_rotary_desc* desc, const void* Q, const void* K,
+                                    void* Q_out, void* K_out, gattn_stream_t stream);
+
+/*
+ * The table of frequencies, to HOST memory (copy it to the device once):
+ *   f_i = theta^(-2i / width) radians per position, then by kind
+ *   GATTN_ROTARY_LINEAR : f / factor
+ *   GATTN_ROTARY_BASE   : theta replaced by theta * factor^(width / (width - 2))
+ *   GATTN_ROTARY_RAMP   : f (g + (1 - g) / factor), g = clamp((r - low) / (high - low), 0, 1)
+ *                         with r = orig_len f / (2 pi), the turns within the original length
+ * theta >= 1, factor >= 1, orig_len > 0 and low < high (RAMP).
+ */
+typedef enum {
+  GATTN_ROTARY_PLAIN = 0,
+  GATTN_ROTARY_LINEAR = 1,
+  GATTN_ROTARY_BASE = 2,
+  GATTN_ROTARY_RAMP = 3
+} gattn_rotary_scaling;
+GATTN_API gattn_status gattn_rotary_freqs(int32_t width, double theta, int32_t scaling,
+                                          double factor, double orig_len, double low, double high,
+                                          uint64_t* freqs);
+
+/*
+ * A cache of keys and values in 4 or 8 bits, for serving: rows are quantised as they are
+ * appended (gattn_cache_write), come back in bf16 or fp32 (gattn_cache_read, for several
+ * queries at once through gattn_block_fwd), are summed by blocks for gattn_block_select
+ * (gattn_cache_sums), and are attended to by single tokens as they are (gattn_cache_fwd).
+ *
+ * Format.  Each (row, key head) of K and of V has a least value m and a step s, both bf16, and
+ * a level u in [0, 2^bits) per element, which stands for m + s u.  Device memory of the caller:
+ *   k, v : uint8 [Hkv][Nk][D * bits / 8]; with 4 bits element 2j is in the low half of byte j
+ *   par  : bf16  [Hkv][Nk][4]: m and s of K, m and s of V
+ * all 16-byte aligned.  A row's m is its least element rounded to bf16 towards -inf (not below
+ * the least finite value), s = (max / 2 - m / 2) / (L / 2) for L = 2^bits - 1, rounded to bf16
+ * towards +inf and 0 below 2^-126, and u = clamp(rint(x * inv + c), 0, L) with inv = 1 / s (0 for
+ * s = 0) and c = -m * inv; each of these is one operation in fp32, rounded to nearest (the last
+ * an FMA), so that levels do not hang on who computes them.  |x - (m + s u)| is at most s / 2
+ * but for those roundings.  A row with a non-finite element gets m = s = NaN and reads as NaN.
+ *
+ * Sequences are laid out as for gattn_block_*: sequence s owns the rows [seq_q[s], seq_q[s+1])
+ * of the new tokens and the cache rows [seq_k[s], seq_k[s] + len_k[s]) (len_k NULL: up to
+ * seq_k[s+1]); row i of its lq new ones stands at position i + len_k[s] - lq.  Offsets and
+ * lengths are device arrays.  No call reads or writes outside its tensors, whatever they say.
+ *
+ * Supported: D 32, 64 or 128, bits 4 or 8, H and Hkv powers of two with Hkv <= H <= 128 Hkv,
+ * block and topk as for gattn_block_*.
+ */
+typedef struct {
+  int32_t S;              /* sequences */
+  int32_t N;              /* rows of K, V (write, read), of Q and out (attention) */
+  int32_t Nk;             /* rows of the cache */
+  int32_t H, Hkv, D;      /* query heads (attention), key heads, head width */
+  int32_t dtype;          /* gattn_dtype of K, V, Q and out */
+  int32_t bits;           /* 4 or 8 */
+  int32_t block, topk;    /* sums and attention: rows per block, entries of a list */
+  int32_t causal;
+  float scale;            /* multiplier of q.k, > 0; 0 selects 1/sqrt(D) */
+  int32_t max_len_k;      /* attention: no sequence holds more rows (more are not looked at); 0: Nk */
+  const int32_t *seq_q, *seq_k, *len_k;
+  int64_t idx_stride[2];  /* as in gattn_block_desc */
+  int64_t row_stride[2];  /* write: elements between rows of K and of V; 0: Hkv * D */
+  void *k, *v, *par;      /* the cache */
+} gattn_cache_desc;
+
+/*
+ * Append: row i of K and V of each sequence becomes the cache row of its position (which len_k
+ * counts already).  Rows at positions below 0, or of no sequence, are skipped.
+ */
+GATTN_API gattn_status gattn_cache_write(const gattn_cache_desc* desc, const void* K,
+                                         const void* V, gattn_stream_t stream);
+
+/*
+ * Read back: row i of K and V [N, Hkv, D] of each sequence becomes the value of its position,
+ * m + s u in fp32, rounded once to dtype.  `since` (device int32 [S], or NULL) replaces
+ * the position of row 0, so that 0 reads a sequence from its start.  Rows whose position is not
+ * in [0, len_k[s]), or of no sequence, are not written.  K or V may be NULL.
+ */
+GATTN_API gattn_status gattn_cache_read(const gattn_cache_desc* desc, const int32_t* since, void* K,
+                                        void* V, gattn_stream_t stream);
+
+/*
+ * gattn_block_sums of the values that the cached keys stand for, in the same table: the sum of
+ * each block, exact in 64 bits wherever the rows' steps and least values lie within a factor of
+ * about 2^23 (else rounded as fp64 additions in row order are).
+ */
+GATTN_API gattn_status gattn_cache_sums(const gattn_cache_desc* desc, const int32_t* since,
+                                        double* sums, gattn_stream_t stream);
+
+/*
+ * Softmax attention of every row of Q [N, H, D] over the cache: over the blocks that idx
+ * [N][Hkv][topk] names for it (a unit of gattn_block_fwd with q_block = 1), or over the whole
+ * sequence where idx is NULL.  out [N, H, D], lse fp32 [N, H]; masks, empty rows and rows of no
+ * sequence as for gattn_block_fwd.  Scores and sums are fp32; bf16 queries enter exactly and the
+ * weights with 11 bits, fp32 queries and their weights with 22.  `workspace` (16-byte
+ * aligned, no initialisation) may be NULL when the size is 0; calls that may overlap need their own.
+ */
+GATTN_API gattn_status gattn_cache_fwd_workspace_size(const gattn_cache_desc* desc, size_t* bytes);
+GATTN_API gattn_status gattn_cache_fwd(const gattn_cache_desc* desc, const void* Q,
+                                       const int32_t* idx, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, gattn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
