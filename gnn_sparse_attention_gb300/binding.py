@@ -1216,7 +1216,8 @@ def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: t
     desc = _cache_desc(cache, S, N, H, Q.dtype, block, topk, causal, scale, max_len_k, seq_q, seq_k,
                        len_k, su, sh)
     ws = _workspace(workspace, dev, other, "gattn_cache_fwd_workspace_size", desc,
-                    (S > 0, N, cache.rows, H, cache.Hkv, D, Q.dtype, block, topk, max_len_k))
+                    (S > 0, N, cache.rows, H, cache.Hkv, D, cache.bits, Q.dtype, block, topk,
+                     max_len_k))
     _check((_lib or load_library()).gattn_cache_fwd(desc, Q.data_ptr(), _at(idx), out.data_ptr(),
                                                     lse.data_ptr(), _at(ws), _bytes(ws), handle),
            "gattn_cache_fwd")

@@ -25,14 +25,21 @@
 // or as two for fp32), scaled by a power of two per column that follows its
 // maximum.  Softmax statistics, m's terms and all sums are fp32.
 //
-// Split.  A warp takes tiles of 16 rows, its own running maximum and sum (moved
-// only when a score exceeds it by 2^8, so a tile needs a vote and no shuffles);
-// warps of a CTA, CTAs of a cluster (through distributed shared memory) and, where
-// a few tokens read long caches, clusters (through the workspace) are joined.
-#include <cooperative_groups.h>
+// A warp takes steps of 32 rows (16 where a row has 128 bytes) through a ring of
+// its own in shared memory, filled by cp.async two steps ahead, with its own running
+// maximum and sum.  The maximum moves only when a score exceeds it by 2^4, so a
+// step needs one vote and no shuffles.
+//
+// Split.  The steps of all (query, key head) items are one line that is cut into
+// equal stretches, one for each CTA that the GPU holds at a time, whatever the
+// lengths of the sequences are: CTAs read them and find their stretch themselves.
+// Items that lie within a stretch are finished there; of one that is cut, each CTA
+// leaves its part in the workspace and a second kernel joins them.  With many more
+// items than CTAs each item is a CTA of its own.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.cuh"
 
@@ -40,16 +47,17 @@ namespace gattn {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kWarps = 8;
-constexpr int kTile = 16;       // rows of the cache per step of a warp
+constexpr int kWarps = 4;
+constexpr int kThr = kWarps * 32;
+constexpr int kCtas = 4;        // per SM
 constexpr int kCols = 8;        // columns of a product: query heads (fp32: halves of four)
-constexpr int kMaxCluster = 8;
-constexpr float kNone = -1e30f; // running maximum before any score
+constexpr int kStages = 3;
+constexpr int kMinSteps = 4;    // of a stretch: one for each warp
+constexpr float kNone = -1e30f; // running maximum of no score
+constexpr float kOver = 4.f;    // a score (log2) may exceed the running maximum by this
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
-// 2^-20 of it keeps its 11 bits; set again beyond kYMax.
-constexpr float kYTop = 64.f, kYMax = 32768.f;
+// 2^-19 of it keeps its 11 bits; set again where a step could leave fp16's range.
+constexpr float kYTop = 32.f, kYMax = 65504.f / 16.f;
 
 struct AttnParams {
   CacheParams c;
@@ -57,21 +65,27 @@ struct AttnParams {
   const int32_t* idx;
   void* out;
   float* lse;
-  float* part;   // [units * Hkv * groups][splits][cols][D + 2]
+  float* part;   // [CTAs][2][cols][D + 2]: a stretch's first item if begun before, its last if cut
+  int2* info;    // [items]: first CTA and CTAs of an item that is cut, (0, 0) for others
   int groups;    // column groups of a key head
-  int splits;    // clusters that share a unit
+  int ctas;      // stretches (0: a CTA for each item)
   int max_keys;
 };
 
 template <int BITS, int D>
 struct Lay {
-  static constexpr int RB = D * BITS / 8;   // bytes of a row
-  static constexpr int KW = RB / 16;        // words of a K row that a lane holds
+  static constexpr int RB = D * BITS / 8;     // bytes of a row
+  static constexpr int R = RB > 64 ? 16 : 32; // rows of a step
+  static constexpr int NT = R / 16;
+  static constexpr int KW = RB / 16;          // words of a K row that a lane holds
   static constexpr int KL = KW < 4 ? KW : 4;  // ... in one load
-  static constexpr int VB = RB / 8;         // bytes of a V row that a lane holds
+  static constexpr int VB = RB / 8;           // bytes of a V row that a lane holds
   static constexpr int VW = VB < 4 ? 1 : VB / 4;
-  static constexpr int MT = D / 16;         // 16-row tiles of the output
-  static constexpr int QR = D / 8;          // registers of q per lane
+  static constexpr int MT = D / 16;           // 16-row tiles of the output
+  static constexpr int QR = D / 8;            // registers of q per lane
+  static constexpr int CP = R * RB / 512;     // 16-byte copies of a lane for K, and for V
+  static constexpr int STAGE = R * (2 * RB + 8);
+  static constexpr int RING = kStages * STAGE;  // bytes of a warp
 };
 
 __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -96,468 +110,635 @@ __device__ __forceinline__ float pow2_below(float x) {
   const int e = (__float_as_uint(x) >> 23) & 255;
   return __uint_as_float(uint32_t(254 - clampi(e, 30, 224)) << 23);
 }
+// n bytes to shared memory, zeros where `in` is false (nothing is read then)
+template <int N>
+__device__ __forceinline__ void copy(uint32_t dst, const void* src, bool in) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(in ? 8 : 0) : "memory");
+}
 
-// rows of a tile as a lane holds them
-template <int BITS, int D>
-struct Tile {
-  using L = Lay<BITS, D>;
-  uint32_t k[2][L::KW];  // rows kr(g), kr(g) + 8
-  uint32_t v[4][L::VW];  // rows t, 4 + t, 8 + t, 12 + t
-  uint2 par[2];          // of the rows of k
-};
-
-// Row of the tile that stands in product row r (r < 8; r + 8 likewise): product
+// Row of a tile that stands in product row r (r < 8; r + 8 likewise): product
 // rows 2t, 2t + 1 are rows t, 4 + t, so that a warp's load of V covers four whole rows.
 __device__ __forceinline__ int tile_row(int r) { return (r >> 1) + 4 * (r & 1); }
 
-template <int BITS, int D>
-__device__ __forceinline__ void load_tile(Tile<BITS, D>& x, const uint8_t* __restrict__ k,
-                                          const uint8_t* __restrict__ v,
-                                          const uint2* __restrict__ par, int pos, int last) {
-  using L = Lay<BITS, D>;
-  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t r = min(pos + tile_row(gq) + 8 * h, last);
-    const uint8_t* a = k + r * L::RB + t * (L::KL * 4);
-#pragma unroll
-    for (int c = 0; c < L::KW / L::KL; ++c) {
-      if constexpr (L::KL == 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(a + c * 64);
-        x.k[h][4 * c] = q.x; x.k[h][4 * c + 1] = q.y;
-        x.k[h][4 * c + 2] = q.z; x.k[h][4 * c + 3] = q.w;
-      } else if constexpr (L::KL == 2) {
-        const uint2 q = *reinterpret_cast<const uint2*>(a);
-        x.k[h][0] = q.x; x.k[h][1] = q.y;
-      } else {
-        x.k[h][0] = *reinterpret_cast<const uint32_t*>(a);
-      }
-    }
-    x.par[h] = par[r];
-  }
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int64_t r = min(pos + 4 * h + t, last);
-    const uint8_t* a = v + r * L::RB + gq * L::VB;
-    if constexpr (L::VB == 16) {
-      const uint4 q = *reinterpret_cast<const uint4*>(a);
-      x.v[h][0] = q.x; x.v[h][1] = q.y; x.v[h][2] = q.z; x.v[h][3] = q.w;
-    } else if constexpr (L::VB == 8) {
-      const uint2 q = *reinterpret_cast<const uint2*>(a);
-      x.v[h][0] = q.x; x.v[h][1] = q.y;
-    } else if constexpr (L::VB == 4) {
-      x.v[h][0] = *reinterpret_cast<const uint32_t*>(a);
-    } else {
-      x.v[h][0] = *reinterpret_cast<const uint16_t*>(a);
-    }
-  }
+// Byte of 16-byte chunk `ch` of row `row` in a stage.  The lanes that shared memory
+// serves together (a quarter of a warp for 16 bytes, half of one for 8) read rows a, a + 4
+// of K and four rows of V; the exclusive-ors put those in different banks.
+template <int RB>
+__device__ __forceinline__ int k_byte(int row, int ch) {
+  if (RB == 128) ch ^= ((row >> 2) & 1) << 2;
+  if (RB == 64) row ^= (row >> 2) & 1;
+  if (RB == 32) row ^= ((row >> 2) & 1) << 1;
+  return row * RB + ch * 16;
+}
+template <int RB>
+__device__ __forceinline__ int v_byte(int row, int ch) {
+  if (RB == 128) ch ^= (row & 3) << 1;
+  if (RB == 64) ch ^= ((row >> 1) & 1) << 1;
+  return row * RB + ch * 16;
 }
 
-// first element of word w of a lane's K row
-template <int BITS, int D>
-__device__ __forceinline__ int k_elem(int w, int t) {
-  using L = Lay<BITS, D>;
-  return ((w / L::KL) * 64 + t * (L::KL * 4) + (w % L::KL) * 4) * 8 / BITS;
-}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-__device__ __forceinline__ float to_f32(const float* x) { return *x; }
-__device__ __forceinline__ float to_f32(const __nv_bfloat16* x) { return __bfloat162float(*x); }
-
-// What a warp carries along: per column (a lane's two) the reference, sums, and factors
-struct Cols {
-  float ref[2], l[2], m[2], vf[2];
+// What the CTA works on: steps [s0, s1) of an item's `steps`
+struct Item {
+  int row, s;     // query row, sequence
+  int beg, limit; // first row of the cache, rows that the query may see
+  int len;
+  int steps;      // at least 1
 };
+template <int R>
+__device__ __forceinline__ Item item_at(const AttnParams& p, int u) {
+  const BlockGeom& g = p.c.g;
+  const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, u);
+  Item it{};
+  it.row = u;
+  it.s = x.s;
+  if (x.s < 0) return it;
+  const Span sp = span_k(g, x.s);
+  it.beg = sp.beg;
+  it.len = sp.len;
+  it.limit = min(g.causal ? clampi(x.i + sp.len - x.n + 1, 0, sp.len) : sp.len, p.max_keys);
+  const int keys = p.idx ? min(it.limit, g.topk * g.block) : it.limit;
+  it.steps = max((keys + R - 1) / R, 1);
+  return it;
+}
 
 template <class T, int BITS, int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParams p) {
   using L = Lay<BITS, D>;
+  constexpr int RB = L::RB, R = L::R, NT = L::NT;
   constexpr bool kSplit = sizeof(T) == 4;           // fp32: a head is two columns
   constexpr int HC = kSplit ? kCols / 2 : kCols;    // heads of a column group
+  constexpr int NC = kSplit ? 1 : 2;                // softmax columns of a lane
+  static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
+  extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
   __shared__ int ids[kBlkMaxTopk];
-  __shared__ int n_ids;
-  __shared__ float so[kWarps][HC][D + 4];           // warps' sums; then, in [0], the CTA's
+  __shared__ int n_keys;
   __shared__ float sref[kWarps][HC], sl[kWarps][HC];
-  __shared__ float cref[HC], cl[HC];
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t start_at;
+  __shared__ int start_u;
   const BlockGeom& g = p.c.g;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int csize = int(cluster.num_blocks()), crank = int(cluster.block_rank());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
-  const int64_t cid = blockIdx.x / csize;  // cluster
-  const int split = int(cid % p.splits);
-  const int64_t item = cid / p.splits;     // (unit, key head, column group)
-  const int cgrp = int(item % p.groups);
-  const int kh = int(item / p.groups % g.Hkv);
-  const int u = int(item / p.groups / g.Hkv);
-  const Unit un = unit_at(g, u);
-  // every CTA of a cluster has the same unit, so all leave together
-  if (un.n == 0) return;
-  const Span sp = span_k(g, un.s);
-  const int limit = min(g.causal ? clampi(un.pos + 1, 0, sp.len) : sp.len, p.max_keys);
-  int keys = limit;
-  if (p.idx) {
-    if (warp == 0) {
-      const int nb = (sp.len + g.block - 1) / g.block;
-      const int n = block_list(p.idx + int64_t(u) * g.is_u + int64_t(kh) * g.is_h, g.topk, nb, ids);
-      if (lane == 0) n_ids = list_keys(ids, n, g.block, limit);
+  const int heads_of = g.Hkv * p.groups;  // items of a query row
+
+  // where the stretch begins and ends, on the line of all items' steps
+  int64_t at = 0, end = 0, per = 0;
+  int u, first = 0;  // query row, item of it
+  cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched; it waits for this grid
+  if (p.ctas == 0) {
+    u = blockIdx.x / heads_of;
+    first = blockIdx.x % heads_of;
+  } else {
+    const int k = (g.U + kThr - 1) / kThr, u0 = threadIdx.x * k, u1 = min(u0 + k, g.U);
+    int64_t mine = 0;
+    for (int i = u0; i < u1; ++i) mine += item_at<R>(p, i).steps;
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    if (lane == 31) scan[warp] = x;
     __syncthreads();
-    keys = n_ids;
-  }
-  const int tiles = (keys + kTile - 1) / kTile;
-  const int lb = 31 - __clz(g.block);
-  const int64_t row0 = int64_t(kh) * g.Nk + sp.beg;
-  const uint8_t* kb = p.c.k + row0 * L::RB;
-  const uint8_t* vb = p.c.v + row0 * L::RB;
-  const uint2* pb = p.c.par + row0;
-  const auto tile_pos = [&](int i) {
-    const int at = i * kTile;
-    return p.idx ? (ids[at >> lb] << lb) + (at & (g.block - 1)) : at;
-  };
-
-  // q of this lane's column, scaled to fp16's range, in the order of the words of a K row
-  const int head0 = kh * g.G + cgrp * HC;
-  const int heads = min(HC, g.G - cgrp * HC);
-  uint32_t qf[L::QR];
-  float qmul[2], qsum[2];  // of the lane's columns of a product: 2t, 2t + 1
-  {
-    const int hc = kSplit ? gq >> 1 : gq;
-    const bool on = hc < heads;
-    const T* q = static_cast<const T*>(p.Q) + (int64_t(un.row) * g.H + head0 + (on ? hc : 0)) * D;
-    constexpr int PW = 32 / BITS;  // elements of a word
-    float f[L::KW * PW];
-    float top = 0.f, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < L::KW; ++w)
-#pragma unroll
-      for (int i = 0; i < PW; ++i) {
-        const float x = on ? to_f32(q + k_elem<BITS, D>(w, t) + i) : 0.f;
-        f[w * PW + i] = x;
-        top = fmaxf(top, fabsf(x));
-        sum += x;
-      }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const float up = pow2_below(top) * 8192.f;  // largest element to [2^13, 2^14)
-#pragma unroll
-    for (int w = 0; w < L::KW; ++w)
-#pragma unroll
-      for (int i = 0; i < PW; i += 4) {
-        // 4 bits, by the masked halves of the word: (0, 4) and (1, 5), then (2, 6) and (3, 7);
-        // 8 bits: (0, 2) and (1, 3).  Upper nibbles count 16 times.
-        float x[4];
-        if constexpr (BITS == 4) {
-          x[0] = f[w * PW + i / 2]; x[1] = f[w * PW + 4 + i / 2];
-          x[2] = f[w * PW + i / 2 + 1] * 0.0625f; x[3] = f[w * PW + 4 + i / 2 + 1] * 0.0625f;
-        } else {
-          x[0] = f[w * PW]; x[1] = f[w * PW + 2]; x[2] = f[w * PW + 1]; x[3] = f[w * PW + 3];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] *= up;
-          if (kSplit && (gq & 1)) x[e] -= __half2float(__float2half_rn(x[e]));
-        }
-        const int r = (w * PW + i) / 2;
-        qf[r] = half2_bits(x[0], x[1]);
-        qf[r + 1] = half2_bits(x[2], x[3]);
-      }
-    // columns 2t, 2t + 1 of a product belong to the lanes with gq = 2t, 2t + 1
-    const float mul = g.qmul * 16777216.f / up, qs = sum * g.qmul;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      qmul[c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
-      qsum[c] = __shfl_sync(0xffffffffu, qs, (2 * t + c) * 4);
-    }
-  }
-
-  float acc[L::MT][4];
-#pragma unroll
-  for (int i = 0; i < L::MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  Cols cs;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    cs.ref[c] = kNone;
-    cs.l[c] = cs.m[c] = 0.f;
-    cs.vf[c] = 1.f;
-  }
-
-  const int nwarps = p.splits * csize * kWarps;
-  const int me = (split * csize + crank) * kWarps + warp;
-  constexpr int NC = kSplit ? 1 : 2;  // softmax columns of a lane
-  Tile<BITS, D> cur, nxt;
-  int pos = 0;
-  if (me < tiles) {
-    pos = tile_pos(me);
-    load_tile<BITS, D>(cur, kb, vb, pb, pos, limit - 1);
-  }
-  for (int i = me; i < tiles; i += nwarps) {
-    int npos = 0;
-    if (i + nwarps < tiles) {
-      npos = tile_pos(i + nwarps);
-      load_tile<BITS, D>(nxt, kb, vb, pb, npos, limit - 1);
-    }
-    // scores
-    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < L::KW; ++w) {
-      const uint32_t a = cur.k[0][w], b = cur.k[1][w];
-      if constexpr (BITS == 4) {
-        mma16816(s4, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                 qf[4 * w], qf[4 * w + 1]);
-        const uint32_t c = a >> 8, d = b >> 8;
-        mma16816(s4, c & 0x000f000fu, d & 0x000f000fu, c & 0x00f000f0u, d & 0x00f000f0u,
-                 qf[4 * w + 2], qf[4 * w + 3]);
-      } else {
-        mma16816(s4, a & 0x00ff00ffu, b & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
-                 (b >> 8) & 0x00ff00ffu, qf[2 * w], qf[2 * w + 1]);
-      }
-    }
-    float lg[2][NC], sv[2], mv[2];
-    bool over = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float mk = __uint_as_float(cur.par[h].x << 16);
-      const float sk = __uint_as_float(cur.par[h].x & 0xffff0000u);
-      mv[h] = __uint_as_float(cur.par[h].y << 16);
-      sv[h] = __uint_as_float(cur.par[h].y & 0xffff0000u);
-      const bool in = pos + tile_row(gq) + 8 * h < limit;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float dot = kSplit ? s4[2 * h] + s4[2 * h + 1] : s4[2 * h + c];
-        const float x = fmaf(dot * qmul[c], sk, mk * qsum[c]);
-        lg[h][c] = in ? x : neg_inf();
-        over = over || lg[h][c] > cs.ref[c] + 8.f;
-      }
-    }
-    float y[2][NC];
-    const bool moved = __any_sync(0xffffffffu, over);
-    if (moved) {  // move the references to the maximum, and the factors with them
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float top = fmaxf(fmaxf(lg[0][c], lg[1][c]), cs.ref[c]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float down = ex2(cs.ref[c] - top);
-        float xm = fmaxf(ex2(lg[0][c] - top) * sv[0], ex2(lg[1][c] - top) * sv[1]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
-        const float vf = kYTop * pow2_below(fmaxf(xm, down * kYTop / cs.vf[c]));
-        const float mul = down * vf / cs.vf[c];  // at most 1
-        cs.ref[c] = top;
-        cs.l[c] *= down;
-        cs.m[c] *= down;
-        cs.vf[c] = vf;
-#pragma unroll
-        for (int i2 = 0; i2 < L::MT; ++i2)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (kSplit || (e & 1) == c) acc[i2][e] *= mul;
-      }
-    }
-    over = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float e = ex2(lg[h][c] - cs.ref[c]);
-        cs.l[c] += e;
-        cs.m[c] = fmaf(e, mv[h], cs.m[c]);
-        y[h][c] = e * sv[h];
-        over = over || y[h][c] * cs.vf[c] > kYMax;
-      }
-    if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float xm = fmaxf(fmaxf(y[0][c], y[1][c]), kYTop / cs.vf[c]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
-        const float vf = kYTop * pow2_below(xm), mul = vf / cs.vf[c];
-        cs.vf[c] = vf;
-#pragma unroll
-        for (int i2 = 0; i2 < L::MT; ++i2)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (kSplit || (e & 1) == c) acc[i2][e] *= mul;
-      }
-    }
-    uint32_t b0, b1;
-    if constexpr (kSplit) {
-      const float y0 = y[0][0] * cs.vf[0], y1 = y[1][0] * cs.vf[0];
-      b0 = transposed(half2_bits(y0, y0 - __half2float(__float2half_rn(y0))));
-      b1 = transposed(half2_bits(y1, y1 - __half2float(__float2half_rn(y1))));
-    } else {
-      b0 = transposed(half2_bits(y[0][0] * cs.vf[0], y[0][1] * cs.vf[1]));
-      b1 = transposed(half2_bits(y[1][0] * cs.vf[0], y[1][1] * cs.vf[1]));
-    }
-    // output: product rows g, g + 8 are neighbouring elements of the lane's part of V
-#pragma unroll
-    for (int w = 0; w < L::VW; ++w) {
-#pragma unroll
-      for (int hh = 0; hh < (L::VB < 4 ? 1 : 2); ++hh) {
-        const uint32_t sel = hh ? 0x7632 : 0x5410;
-        const uint32_t a = __byte_perm(cur.v[0][w], cur.v[1][w], sel);
-        const uint32_t b = __byte_perm(cur.v[2][w], cur.v[3][w], sel);
-        if constexpr (BITS == 4) {
-          mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu,
-                   b & 0x00f000f0u, b0, b1);
-          const uint32_t c = a >> 8, d = b >> 8;
-          mma16816(acc[4 * w + 2 * hh + 1], c & 0x000f000fu, c & 0x00f000f0u, d & 0x000f000fu,
-                   d & 0x00f000f0u, b0, b1);
-        } else {
-          mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu, b & 0x00ff00ffu,
-                   (b >> 8) & 0x00ff00ffu, b0, b1);
-        }
-      }
-    }
-    cur = nxt;
-    pos = npos;
-  }
-
-  // the warp's sums
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      cs.l[c] += __shfl_xor_sync(0xffffffffu, cs.l[c], o);
-      cs.m[c] += __shfl_xor_sync(0xffffffffu, cs.m[c], o);
-    }
-    const int h = kSplit ? t : 2 * t + c;
-    if (gq == 0) {
-      sref[warp][h] = cs.ref[c];
-      sl[warp][h] = cs.l[c];
-    }
-    const float back = 16777216.f / cs.vf[c];
-#pragma unroll
-    for (int i = 0; i < L::MT; ++i) {
-      const int d = gq * (D / 8) + 2 * i;
-      const float lo = kSplit ? acc[i][0] + acc[i][1] : acc[i][c];
-      const float hi = kSplit ? acc[i][2] + acc[i][3] : acc[i][2 + c];
-      so[warp][h][d] = fmaf(lo, back, cs.m[c]);
-      so[warp][h][d + 1] = fmaf(hi, BITS == 4 ? back * 0.0625f : back, cs.m[c]);
-    }
-  }
-  __syncthreads();
-  // the CTA's
-  for (int e = threadIdx.x; e < HC * D; e += kWarps * 32) {
-    const int h = e / D, d = e % D;
-    float top = sref[0][h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sref[w][h]);
-    float o = 0.f, l = 0.f;
+    int64_t total = 0, before = x - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(sref[w][h] - top);
-      o = fmaf(so[w][h][d], f, o);
-      l = fmaf(sl[w][h], f, l);
+      if (w < warp) before += scan[w];
+      total += scan[w];
     }
-    so[0][h][d] = o;  // read by this thread alone
-    if (d == 0) {
-      cref[h] = top;
-      cl[h] = l;
+    total *= heads_of;
+    before *= heads_of;
+    mine *= heads_of;
+    per = max((total + p.ctas - 1) / p.ctas, int64_t(kMinSteps));
+    at = per * blockIdx.x;
+    end = min(at + per, total);
+    if (at >= end) return;
+    if (at >= before && at < before + mine) {  // one thread
+      int i = u0;
+      for (;; ++i) {
+        const int64_t n = int64_t(item_at<R>(p, i).steps) * heads_of;
+        if (at < before + n) break;
+        before += n;
+      }
+      start_u = i;
+      start_at = before;
     }
+    __syncthreads();
+    u = start_u;
+    at -= start_at;  // from here on relative to the row's first step
+    end -= start_at;
   }
-  if (csize > 1) cluster.sync();
-  else __syncthreads();
-  // the cluster's: each CTA a part of the elements
-  for (int e = crank * kWarps * 32 + threadIdx.x; e < HC * D; e += csize * kWarps * 32) {
-    const int h = e / D, d = e % D;
-    if (h >= heads) continue;
-    float top = kNone, o = 0.f, l = 0.f;
-    if (csize == 1) {
-      top = cref[h];
-      o = so[0][h][d];
-      l = cl[h];
+
+  const uint32_t my_ring = uint32_t(__cvta_generic_to_shared(ring)) + warp * L::RING;
+  const uint8_t* my_stage = ring + warp * L::RING;
+
+  for (;;) {
+    const Item it = item_at<R>(p, u);
+    if (it.s < 0) {  // rows of no sequence
+      if (p.ctas == 0) return;
+      ++u;
+      continue;
+    }
+    int hi, s0, s1;
+    if (p.ctas == 0) {
+      hi = first;
+      s0 = 0;
+      s1 = it.steps;
     } else {
-      for (int r = 0; r < csize; ++r) top = fmaxf(top, *cluster.map_shared_rank(&cref[h], r));
-      for (int r = 0; r < csize; ++r) {
-        const float f = ex2(*cluster.map_shared_rank(&cref[h], r) - top);
-        o = fmaf(*cluster.map_shared_rank(&so[0][h][d], r), f, o);
-        l = fmaf(*cluster.map_shared_rank(&cl[h], r), f, l);
+      const int64_t row_steps = int64_t(it.steps) * heads_of;
+      if (at >= row_steps) {
+        at -= row_steps;
+        end -= row_steps;
+        ++u;
+        continue;
+      }
+      hi = int(at / it.steps);
+      s0 = int(at - int64_t(hi) * it.steps);
+      s1 = int(min(int64_t(it.steps), s0 + (end - at)));
+    }
+    const int cgrp = hi % p.groups, kh = hi / p.groups;
+    const int head0 = kh * g.G + cgrp * HC, heads = min(HC, g.G - cgrp * HC);
+    const int64_t row0 = int64_t(kh) * g.Nk + it.beg;
+    const uint8_t* kb = p.c.k + row0 * RB;
+    const uint8_t* vb = p.c.v + row0 * RB;
+    const uint2* pb = p.c.par + row0;
+
+    int keys = it.limit;
+    if (p.idx) {
+      if (warp == 0) {
+        const int nb = (it.len + g.block - 1) / g.block;
+        const int n =
+            block_list(p.idx + int64_t(u) * g.is_u + int64_t(kh) * g.is_h, g.topk, nb, ids);
+        if (lane == 0) n_keys = list_keys(ids, n, g.block, it.limit);
+      }
+      __syncthreads();
+      keys = n_keys;
+    }
+    const int lb = 31 - __clz(g.block);
+    const int steps = min(s1, (keys + R - 1) / R);
+    // position of row `i` of the item's rows, the first of a tile
+    const auto tile_pos = [&](int i) {
+      return p.idx ? (i < keys ? (ids[i >> lb] << lb) + (i & (g.block - 1)) : it.limit) : i;
+    };
+    const auto fetch = [&](int step, int stage) {
+      if (step < steps) {
+        int pos[NT];
+        bool whole = true;
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          pos[h] = tile_pos(step * R + 16 * h);
+          whole = whole && pos[h] + 16 <= it.limit;
+        }
+        const uint32_t dst = my_ring + stage * L::STAGE;
+#pragma unroll
+        for (int j = 0; j < L::CP; ++j) {
+          const int b = j * 512 + lane * 16, row = b / RB, h = row / 16, ch = b % RB / 16;
+          const int64_t r = int64_t(NT == 1 || h == 0 ? pos[0] : pos[NT - 1]) + (row & 15);
+          const bool in = whole || r < it.limit;
+          const int64_t from = in ? r * RB + ch * 16 : 0;
+          copy<16>(dst + k_byte<RB>(row, ch), kb + from, in);
+          copy<16>(dst + R * RB + v_byte<RB>(row, ch), vb + from, in);
+        }
+        if (lane < R) {
+          const int64_t r = int64_t(NT == 1 || lane < 16 ? pos[0] : pos[NT - 1]) + (lane & 15);
+          const bool in = whole || r < it.limit;
+          copy<8>(dst + 2 * R * RB + lane * 8, pb + (in ? r : 0), in);
+        }
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(s0 + warp + i * kWarps, i);
+
+    // q of this lane's column, scaled to fp16's range, in the order of the words of a K row
+    uint32_t qf[L::QR];
+    float qmul[2], qsum[2];  // of the lane's columns of a product: 2t, 2t + 1
+    {
+      const int hc = kSplit ? gq >> 1 : gq;
+      const bool on = hc < heads;
+      const T* q = static_cast<const T*>(p.Q) + (int64_t(it.row) * g.H + head0 + (on ? hc : 0)) * D;
+      constexpr int PW = 32 / BITS;           // elements of a word
+      constexpr int RUN = L::KL * PW;         // neighbouring elements of a lane
+      constexpr int VE = 16 / int(sizeof(T));
+      float f[L::KW * PW];
+#pragma unroll
+      for (int c = 0; c < L::KW / L::KL; ++c)
+#pragma unroll
+        for (int i = 0; i < RUN; i += VE) {
+          const uint4 x = *reinterpret_cast<const uint4*>(q + c * (64 * 8 / BITS) + t * RUN + i);
+          const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+          for (int z = 0; z < VE; ++z) f[c * RUN + i + z] = on ? to_f32(e[z]) : 0.f;
+        }
+      float top = 0.f, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < L::KW * PW; ++i) {
+        top = fmaxf(top, fabsf(f[i]));
+        sum += f[i];
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
+      const float up = pow2_below(top) * 8192.f;  // largest element to [2^13, 2^14)
+#pragma unroll
+      for (int w = 0; w < L::KW; ++w)
+#pragma unroll
+        for (int i = 0; i < PW; i += 4) {
+          // 4 bits, by the masked halves of the word: (0, 4) and (1, 5), then (2, 6) and (3, 7);
+          // 8 bits: (0, 2) and (1, 3).  Upper nibbles count 16 times.
+          float x[4];
+          if constexpr (BITS == 4) {
+            x[0] = f[w * PW + i / 2]; x[1] = f[w * PW + 4 + i / 2];
+            x[2] = f[w * PW + i / 2 + 1] * 0.0625f; x[3] = f[w * PW + 4 + i / 2 + 1] * 0.0625f;
+          } else {
+            x[0] = f[w * PW]; x[1] = f[w * PW + 2]; x[2] = f[w * PW + 1]; x[3] = f[w * PW + 3];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] *= up;
+            if (kSplit && (gq & 1)) x[e] -= __half2float(__float2half_rn(x[e]));
+          }
+          const int r = (w * PW + i) / 2;
+          qf[r] = half2_bits(x[0], x[1]);
+          qf[r + 1] = half2_bits(x[2], x[3]);
+        }
+      // columns 2t, 2t + 1 of a product belong to the lanes with gq = 2t, 2t + 1
+      const float mul = g.qmul * 16777216.f / up, qs = sum * g.qmul;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qmul[c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
+        qsum[c] = __shfl_sync(0xffffffffu, qs, (2 * t + c) * 4);
       }
     }
-    if (p.splits > 1) {
-      float* w = p.part + ((item * p.splits + split) * HC + h) * (D + 2);
-      w[d] = o;
-      if (d == 0) {
-        w[D] = top;
-        w[D + 1] = l;
-      }
-    } else {
-      const int64_t r = int64_t(un.row) * g.H + head0 + h;
-      static_cast<T*>(p.out)[r * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
-      if (d == 0) p.lse[r] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
+
+    float acc[L::MT][4];
+#pragma unroll
+    for (int i = 0; i < L::MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    float ref[NC], sum[NC], msum[NC], vf[NC], top_s[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      ref[c] = 0.f;
+      sum[c] = msum[c] = 0.f;
+      vf[c] = 1.f;
+      top_s[c] = 0.f;  // kYMax / vf once vf is set: a step of V beyond sets it again
     }
+
+    int stage = 0;
+    bool fresh = true;  // no step so far; each has a row that is seen
+    for (int step = s0 + warp; step < steps; step += kWarps) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // all lanes' copies are here, and the stage to be filled has been read
+      fetch(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t* sk = my_stage + stage * L::STAGE;
+      const uint8_t* sv = sk + R * RB;
+      const uint2* sp = reinterpret_cast<const uint2*>(sk + 2 * R * RB);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      // scores relative to the running maximum, in log2
+      float x[NT][2][NC], vs[NT][2], vm[NT][2];
+      bool over = fresh;
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t ka[2][L::KW];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int c = 0; c < L::KW / L::KL; ++c) {
+            const int b = t * (L::KL * 4);
+            const uint8_t* a =
+                sk + k_byte<RB>(16 * h + tile_row(gq) + 8 * q, c * 4 + b / 16) + b % 16;
+            if constexpr (L::KL == 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(a);
+              ka[q][4 * c] = w.x; ka[q][4 * c + 1] = w.y;
+              ka[q][4 * c + 2] = w.z; ka[q][4 * c + 3] = w.w;
+            } else if constexpr (L::KL == 2) {
+              const uint2 w = *reinterpret_cast<const uint2*>(a);
+              ka[q][0] = w.x; ka[q][1] = w.y;
+            } else {
+              ka[q][0] = *reinterpret_cast<const uint32_t*>(a);
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < L::KW; ++w) {
+          const uint32_t a = ka[0][w], b = ka[1][w];
+          if constexpr (BITS == 4) {
+            mma16816(s4, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+                     qf[4 * w], qf[4 * w + 1]);
+            const uint32_t c = a >> 8, d = b >> 8;
+            mma16816(s4, c & 0x000f000fu, d & 0x000f000fu, c & 0x00f000f0u, d & 0x00f000f0u,
+                     qf[4 * w + 2], qf[4 * w + 3]);
+          } else {
+            mma16816(s4, a & 0x00ff00ffu, b & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
+                     (b >> 8) & 0x00ff00ffu, qf[2 * w], qf[2 * w + 1]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint2 par = sp[16 * h + tile_row(gq) + 8 * q];
+          const float mk = __uint_as_float(par.x << 16), st = __uint_as_float(par.x & 0xffff0000u);
+          vm[h][q] = __uint_as_float(par.y << 16);
+          vs[h][q] = __uint_as_float(par.y & 0xffff0000u);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float dot = kSplit ? s4[2 * q] + s4[2 * q + 1] : s4[2 * q + c];
+            x[h][q][c] = fmaf(dot * qmul[c], st, fmaf(mk, qsum[c], -ref[c]));
+          }
+        }
+      }
+      // rows behind the last that the query sees
+      if (tile_pos(step * R + R - 16) + 16 > it.limit || (p.idx && step * R + R > keys)) {
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          const int pos = tile_pos(step * R + 16 * h);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (pos + tile_row(gq) + 8 * q >= it.limit) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c) x[h][q][c] = neg_inf();
+            }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            over = over || x[h][q][c] > kOver || vs[h][q] > top_s[c];
+      if (__any_sync(0xffffffffu, over)) {
+        // references to the maxima, and the factors of p s with them
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float top = fresh ? neg_inf() : 0.f;
+#pragma unroll
+          for (int h = 0; h < NT; ++h) top = fmaxf(top, fmaxf(x[h][0][c], x[h][1][c]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (top == neg_inf()) top = 0.f;  // scores that are not numbers
+          float xm = 0.f;
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              x[h][q][c] -= top;
+              xm = fmaxf(xm, ex2(x[h][q][c]) * vs[h][q]);
+            }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
+          const float down = fresh ? 0.f : ex2(-top);
+          const float f = kYTop * pow2_below(fmaxf(xm, down * kYTop / vf[c]));
+          const float mul = down * f / vf[c];  // at most 1
+          ref[c] += top;
+          sum[c] *= down;
+          msum[c] *= down;
+          vf[c] = f;
+          top_s[c] = kYMax / f;
+#pragma unroll
+          for (int i = 0; i < L::MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (kSplit || (e & 1) == c) acc[i][e] *= mul;
+        }
+        fresh = false;
+      }
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        float y[2][NC];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float e = ex2(x[h][q][c]);
+            sum[c] += e;
+            msum[c] = fmaf(e, vm[h][q], msum[c]);
+            y[q][c] = e * (vs[h][q] * vf[c]);
+          }
+        uint32_t b0, b1;
+        if constexpr (kSplit) {
+          b0 = transposed(half2_bits(y[0][0], y[0][0] - __half2float(__float2half_rn(y[0][0]))));
+          b1 = transposed(half2_bits(y[1][0], y[1][0] - __half2float(__float2half_rn(y[1][0]))));
+        } else {
+          b0 = transposed(half2_bits(y[0][0], y[0][1]));
+          b1 = transposed(half2_bits(y[1][0], y[1][1]));
+        }
+        uint32_t va[4][L::VW];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int b = gq * L::VB;
+          const uint8_t* a = sv + v_byte<RB>(16 * h + 4 * q + t, b / 16) + b % 16;
+          if constexpr (L::VB == 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(a);
+            va[q][0] = w.x; va[q][1] = w.y; va[q][2] = w.z; va[q][3] = w.w;
+          } else if constexpr (L::VB == 8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(a);
+            va[q][0] = w.x; va[q][1] = w.y;
+          } else if constexpr (L::VB == 4) {
+            va[q][0] = *reinterpret_cast<const uint32_t*>(a);
+          } else {
+            va[q][0] = *reinterpret_cast<const uint16_t*>(a);
+          }
+        }
+        // output: product rows g, g + 8 are neighbouring elements of the lane's part of V
+#pragma unroll
+        for (int w = 0; w < L::VW; ++w)
+#pragma unroll
+          for (int hh = 0; hh < (L::VB < 4 ? 1 : 2); ++hh) {
+            const uint32_t sel = hh ? 0x7632 : 0x5410;
+            const uint32_t a = __byte_perm(va[0][w], va[1][w], sel);
+            const uint32_t b = __byte_perm(va[2][w], va[3][w], sel);
+            if constexpr (BITS == 4) {
+              mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu,
+                       b & 0x00f000f0u, b0, b1);
+              const uint32_t c = a >> 8, d = b >> 8;
+              mma16816(acc[4 * w + 2 * hh + 1], c & 0x000f000fu, c & 0x00f000f0u, d & 0x000f000fu,
+                       d & 0x00f000f0u, b0, b1);
+            } else {
+              mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu, b & 0x00ff00ffu,
+                       (b >> 8) & 0x00ff00ffu, b0, b1);
+            }
+          }
+      }
+    }
+
+    // the warp's sums, in place of its ring
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
+    float* so = reinterpret_cast<float*>(ring + warp * L::RING);  // [HC][D]
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], o);
+        msum[c] += __shfl_xor_sync(0xffffffffu, msum[c], o);
+      }
+      const int h = kSplit ? t : 2 * t + c;
+      if (gq == 0) {
+        sref[warp][h] = fresh ? kNone : ref[c];
+        sl[warp][h] = sum[c];
+      }
+      const float back = 16777216.f / vf[c];
+#pragma unroll
+      for (int i = 0; i < L::MT; ++i) {
+        const float lo = kSplit ? acc[i][0] + acc[i][1] : acc[i][c];
+        const float up = kSplit ? acc[i][2] + acc[i][3] : acc[i][2 + c];
+        *reinterpret_cast<float2*>(so + h * D + gq * (D / 8) + 2 * i) =
+            make_float2(fmaf(lo, back, msum[c]),
+                        fmaf(up, BITS == 4 ? back * 0.0625f : back, msum[c]));
+      }
+    }
+    __syncthreads();
+    // the CTA's: finished, or its part of the item
+    const bool cut = s0 > 0 || s1 < it.steps;
+    for (int e = threadIdx.x; e < heads * D; e += kThr) {
+      const int h = e / D, d = e % D;
+      float top = sref[0][h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sref[w][h]);
+      float o = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(sref[w][h] - top);
+        o = fmaf(reinterpret_cast<const float*>(ring + w * L::RING)[e], f, o);
+        l = fmaf(sl[w][h], f, l);
+      }
+      if (cut) {
+        float* w = p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 2);
+        w[d] = o;
+        if (d == 0) {
+          w[D] = top;
+          w[D + 1] = l;
+        }
+      } else {
+        const int64_t r = int64_t(it.row) * g.H + head0 + h;
+        static_cast<T*>(p.out)[r * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
+        if (d == 0) p.lse[r] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
+      }
+    }
+    if (p.ctas == 0) return;
+    if (threadIdx.x == 0 && s0 == 0)
+      p.info[int64_t(u) * heads_of + hi] =
+          cut ? make_int2(blockIdx.x, 1 + int((it.steps - s1 + per - 1) / per)) : make_int2(0, 0);
+    at += s1 - s0;
+    if (at >= end) return;
+    __syncthreads();  // ids, statistics and rings have been read
   }
-  if (csize > 1) cluster.sync();  // nobody leaves while its sums are read
 }
 
-// joins the clusters of a unit: one thread an element
+// Joins an item that was cut: 8 warps share its parts, a lane has an element.
 template <class T, int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int hc) {
+  __shared__ float so[8][32], sr[8], sl[8];
   const BlockGeom& g = p.c.g;
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int d = int(e % D);
-  const int64_t q = e / D;  // query row * H + head
-  if (q >= int64_t(g.U) * g.H) return;
-  const int head = int(q % g.H), u = int(q / g.H);
-  const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, u);
-  if (x.s < 0) return;
-  const int kh = head / g.G, in = head % g.G;
-  const int64_t item = (int64_t(u) * g.Hkv + kh) * p.groups + in / hc;
-  const float* w = p.part + (item * p.splits * hc + in % hc) * (D + 2);
-  const int64_t step = int64_t(hc) * (D + 2);
-  float top = kNone, o = 0.f, l = 0.f;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, w[s * step + D]);
-  for (int s = 0; s < p.splits; ++s) {
-    const float f = ex2(w[s * step + D] - top);
-    o = fmaf(w[s * step + d], f, o);
-    l = fmaf(w[s * step + D + 1], f, l);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads_of = g.Hkv * p.groups;
+  const int u = blockIdx.x / heads_of, hi = blockIdx.x % heads_of;
+  const int cgrp = hi % p.groups, kh = hi / p.groups;
+  const int heads = min(hc, g.G - cgrp * hc);
+  const bool live = seq_row(g.seq_q, g.S, g.Nq, u).s >= 0;
+  cudaGridDependencySynchronize();  // the parts are there
+  const int2 in = live ? p.info[blockIdx.x] : make_int2(0, 0);
+  if (in.y == 0) return;
+  // part i: the first CTA's second slot, then the first slots of those that follow
+  const auto part = [&](int i) {
+    return p.part + ((int64_t(in.x) + i) * 2 + (i == 0)) * hc * (D + 2);
+  };
+  for (int e0 = blockIdx.y * 32; e0 < heads * D; e0 += gridDim.y * 32) {
+    const int h = e0 / D, d = e0 % D + lane;
+    float top = kNone, o = 0.f, l = 0.f;
+    for (int i = warp; i < in.y; i += 8) {
+      const float* w = part(i) + h * (D + 2);
+      const float r = w[D], x = w[d], y = w[D + 1], m = fmaxf(top, r);
+      const float f0 = ex2(top - m), f1 = ex2(r - m);
+      o = fmaf(o, f0, x * f1);
+      l = fmaf(l, f0, y * f1);
+      top = m;
+    }
+    so[warp][lane] = o;
+    if (lane == 0) {
+      sr[warp] = top;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      top = sr[0];
+      for (int w = 1; w < 8; ++w) top = fmaxf(top, sr[w]);
+      o = l = 0.f;
+      for (int w = 0; w < 8; ++w) {
+        const float f = ex2(sr[w] - top);
+        o = fmaf(so[w][lane], f, o);
+        l = fmaf(sl[w], f, l);
+      }
+      const int64_t q = int64_t(u) * g.H + kh * g.G + cgrp * hc + h;
+      static_cast<T*>(p.out)[q * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
+      if (d == 0) p.lse[q] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
+    }
+    __syncthreads();
   }
-  static_cast<T*>(p.out)[q * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
-  if (d == 0) p.lse[q] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
 }
 
 struct Shape {
-  int hc, groups, cluster, splits;
+  int hc, groups;
+  int64_t items;
+  int ctas;      // 0: one for each item
+  size_t bytes;  // of the workspace: parts, then the items' table
 };
 Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   const BlockGeom& g = p.g;
   Shape s{};
   s.hc = dt == GATTN_F32 ? kCols / 2 : kCols;
   s.groups = (g.G + s.hc - 1) / s.hc;
-  const int64_t items = int64_t(g.U) * g.Hkv * s.groups;
+  s.items = int64_t(g.U) * g.Hkv * s.groups;
   const int64_t keys = lists ? std::min<int64_t>(int64_t(g.topk) * g.block, max_keys) : max_keys;
-  const int64_t tiles = (keys + kTile - 1) / kTile;
-  const int64_t slots = int64_t(sm_count()) * 2;
-  int64_t n = 1;  // CTAs to an item: a power of two, with a tile at least for each warp
-  while (items * n * 2 <= slots && n * 2 * kWarps <= tiles) n *= 2;
-  s.cluster = int(std::min<int64_t>(n, kMaxCluster));
-  s.splits = int(n / s.cluster);
+  const int rows = g.D * p.bits / 8 > 64 ? 16 : 32;
+  const int64_t steps = std::max<int64_t>((keys + rows - 1) / rows, 1);
+  const int64_t slots = int64_t(sm_count()) * kCtas;
+  // Items of their own: nothing to cut, or so many that the last ones to run weigh little
+  if (steps <= kMinSteps || s.items >= 8 * slots) return s;
+  s.ctas = int(std::min(slots, (s.items * steps + kMinSteps - 1) / kMinSteps));
+  s.bytes = size_t(s.ctas) * 2 * s.hc * (g.D + 2) * 4 + size_t(s.items) * 8;
   return s;
 }
 
 template <class T, int BITS, int D>
 cudaError_t launch(const AttnParams& p, const Shape& s, cudaStream_t st) {
+  using L = Lay<BITS, D>;
+  constexpr int smem = kWarps * L::RING;
+  static std::atomic<uint64_t> set{0};  // devices whose kernel has been given its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(cache_attn_kernel<T, BITS, D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  cache_attn_kernel<T, BITS, D>
+      <<<unsigned(s.ctas ? s.ctas : s.items), kThr, smem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || s.ctas == 0) return e;
+  // the join's launch overlaps the kernel's end
   cudaLaunchConfig_t cfg{};
-  const int64_t items = int64_t(p.c.g.U) * p.c.g.Hkv * s.groups;
-  cfg.gridDim = dim3(unsigned(items * s.splits * s.cluster));
-  cfg.blockDim = dim3(kWarps * 32);
+  const int64_t wide = int64_t(sm_count()) * 4 / s.items;
+  cfg.gridDim = dim3(unsigned(s.items),
+                     unsigned(std::min<int64_t>(std::max<int64_t>(wide, 1), s.hc * D / 32)));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(s.cluster);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<T, BITS, D>, p);
-  if (e != cudaSuccess || s.splits == 1) return e;
-  const int64_t n = int64_t(p.c.g.U) * p.c.g.H * D;
-  cache_join_kernel<T, D><<<unsigned((n + 255) / 256), 256, 0, st>>>(p, s.hc);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, p, s.hc);
 }
-
 template <class T, int BITS>
 cudaError_t by_width(const AttnParams& p, const Shape& s, cudaStream_t st) {
   if (p.c.g.D == 32) return launch<T, BITS, 32>(p, s, st);
@@ -568,9 +749,7 @@ cudaError_t by_width(const AttnParams& p, const Shape& s, cudaStream_t st) {
 }  // namespace
 
 size_t cache_fwd_workspace(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
-  const Shape s = shape(p, dt, max_keys, lists);
-  if (s.splits == 1) return 0;
-  return size_t(p.g.U) * p.g.Hkv * s.groups * s.splits * s.hc * (p.g.D + 2) * 4;
+  return shape(p, dt, max_keys, lists).bytes;
 }
 
 gattn_status launch_cache_fwd(const CacheParams& c, gattn_dtype dt, int max_keys, const void* Q,
@@ -584,10 +763,11 @@ gattn_status launch_cache_fwd(const CacheParams& c, gattn_dtype dt, int max_keys
   p.out = out;
   p.lse = lse;
   p.part = static_cast<float*>(ws);
+  p.info = reinterpret_cast<int2*>(p.part + int64_t(s.ctas) * 2 * s.hc * (c.g.D + 2));
   p.groups = s.groups;
-  p.splits = s.splits;
+  p.ctas = s.ctas;
   p.max_keys = max_keys;
-  if (int64_t(c.g.U) * c.g.Hkv * s.groups * s.splits * s.cluster > INT32_MAX) {
+  if (s.items > INT32_MAX) {
     set_error("gattn_cache_fwd: too many rows and heads");
     return GATTN_ERR_UNSUPPORTED;
   }
