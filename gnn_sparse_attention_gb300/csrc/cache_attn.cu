@@ -50,7 +50,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThr = kWarps * 32;
 constexpr int kCtas = 4;        // per SM
-constexpr int kCols = 8;        // columns of a product: query heads (fp32: halves of four)
 constexpr int kStages = 3;
 constexpr int kMinSteps = 4;    // of a stretch: one for each warp
 constexpr float kNone = -1e30f; // running maximum of no score
@@ -65,7 +64,7 @@ struct AttnParams {
   const int32_t* idx;
   void* out;
   float* lse;
-  float* part;   // [CTAs][2][cols][D + 2]: a stretch's first item if begun before, its last if cut
+  float* part;   // [CTAs][2][heads][D + 4]: a stretch's first item if begun before, its last if cut
   int2* info;    // [items]: first CTA and CTAs of an item that is cut, (0, 0) for others
   int groups;    // column groups of a key head
   int ctas;      // stretches (0: a CTA for each item)
@@ -145,6 +144,13 @@ __device__ __forceinline__ int v_byte(int row, int ch) {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+__device__ __forceinline__ void store4(float* to, float4 x) { *reinterpret_cast<float4*>(to) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* to, float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                             *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // What the CTA works on: steps [s0, s1) of an item's `steps`
 struct Item {
   int row, s;     // query row, sequence
@@ -169,18 +175,21 @@ __device__ __forceinline__ Item item_at(const AttnParams& p, int u) {
   return it;
 }
 
-template <class T, int BITS, int D>
+// NC heads to a lane's two columns of a product.  With two, a group is 8 heads.  With one it is 4:
+// in fp32 the head's two parts, in bf16 the second column is empty, which spares a group of up to
+// 4 heads the softmax of columns that nobody has.
+template <class T, int BITS, int D, int NC>
 __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParams p) {
   using L = Lay<BITS, D>;
   constexpr int RB = L::RB, R = L::R, NT = L::NT;
-  constexpr bool kSplit = sizeof(T) == 4;           // fp32: a head is two columns
-  constexpr int HC = kSplit ? kCols / 2 : kCols;    // heads of a column group
-  constexpr int NC = kSplit ? 1 : 2;                // softmax columns of a lane
+  constexpr bool kSplit = sizeof(T) == 4;  // fp32: a head is two columns
+  constexpr int HC = 4 * NC;               // heads of a column group
+  static_assert(NC == 1 || !kSplit, "");
   static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
   __shared__ int ids[kBlkMaxTopk];
   __shared__ int n_keys;
-  __shared__ float sref[kWarps][HC], sl[kWarps][HC];
+  __shared__ float sref[kWarps][HC], sl[kWarps][HC], sw[kWarps][HC];
   __shared__ int64_t scan[kWarps];
   __shared__ int64_t start_at;
   __shared__ int start_u;
@@ -283,33 +292,37 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     }
     const int lb = 31 - __clz(g.block);
     const int steps = min(s1, (keys + R - 1) / R);
-    // position of row `i` of the item's rows, the first of a tile
-    const auto tile_pos = [&](int i) {
-      return p.idx ? (i < keys ? (ids[i >> lb] << lb) + (i & (g.block - 1)) : it.limit) : i;
-    };
-    const auto fetch = [&](int step, int stage) {
-      if (step < steps) {
-        int pos[NT];
-        bool whole = true;
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          pos[h] = tile_pos(step * R + 16 * h);
-          whole = whole && pos[h] + 16 <= it.limit;
-        }
-        const uint32_t dst = my_ring + stage * L::STAGE;
+    // position of row `i` of the item's rows; rows of a tile lie side by side
+    const auto tile_pos = [&](int i) { return p.idx ? (ids[i >> lb] << lb) + (i & (g.block - 1)) : i; };
+    const auto fetch = [&](int step, int to) {
+      const uint32_t dst = my_ring + to * L::STAGE;
+      if ((step + 1) * R <= keys && step < steps) {
+        const int pos0 = tile_pos(step * R), pos1 = NT == 1 ? 0 : tile_pos(step * R + 16) - 16;
+        const uint8_t *k0 = kb + int64_t(pos0) * RB + lane * 16, *v0 = vb + (k0 - kb);
+        const uint8_t *k1 = NT == 1 ? k0 : kb + int64_t(pos1) * RB + lane * 16;
+        const uint8_t *v1 = vb + (k1 - kb);
 #pragma unroll
         for (int j = 0; j < L::CP; ++j) {
-          const int b = j * 512 + lane * 16, row = b / RB, h = row / 16, ch = b % RB / 16;
-          const int64_t r = int64_t(NT == 1 || h == 0 ? pos[0] : pos[NT - 1]) + (row & 15);
-          const bool in = whole || r < it.limit;
-          const int64_t from = in ? r * RB + ch * 16 : 0;
+          const int c = lane * 16, row = j * 512 / RB + c / RB, ch = c % RB / 16;
+          const bool second = RB == 16 ? lane >= 16 : j >= L::CP / 2;
+          copy<16>(dst + k_byte<RB>(row, ch), (second ? k1 : k0) + j * 512, true);
+          copy<16>(dst + R * RB + v_byte<RB>(row, ch), (second ? v1 : v0) + j * 512, true);
+        }
+        if (lane < R)
+          copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane, true);
+      } else if (step < steps) {  // the last one: zeros behind the rows that the query sees
+#pragma unroll 1
+        for (int j = 0; j < L::CP; ++j) {
+          const int c = j * 512 + lane * 16, row = c / RB, ch = c % RB / 16;
+          const int i = step * R + row;
+          const bool in = i < keys;
+          const int64_t from = in ? int64_t(tile_pos(i)) * RB + ch * 16 : 0;
           copy<16>(dst + k_byte<RB>(row, ch), kb + from, in);
           copy<16>(dst + R * RB + v_byte<RB>(row, ch), vb + from, in);
         }
         if (lane < R) {
-          const int64_t r = int64_t(NT == 1 || lane < 16 ? pos[0] : pos[NT - 1]) + (lane & 15);
-          const bool in = whole || r < it.limit;
-          copy<8>(dst + 2 * R * RB + lane * 8, pb + (in ? r : 0), in);
+          const int i = step * R + lane;
+          copy<8>(dst + 2 * R * RB + lane * 8, pb + (i < keys ? tile_pos(i) : 0), i < keys);
         }
       }
       asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -321,8 +334,8 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     uint32_t qf[L::QR];
     float qmul[2], qsum[2];  // of the lane's columns of a product: 2t, 2t + 1
     {
-      const int hc = kSplit ? gq >> 1 : gq;
-      const bool on = hc < heads;
+      const int hc = NC == 1 ? gq >> 1 : gq;
+      const bool on = hc < heads && (NC == 2 || kSplit || !(gq & 1));
       const T* q = static_cast<const T*>(p.Q) + (int64_t(it.row) * g.H + head0 + (on ? hc : 0)) * D;
       constexpr int PW = 32 / BITS;           // elements of a word
       constexpr int RUN = L::KL * PW;         // neighbouring elements of a lane
@@ -383,14 +396,18 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     float acc[L::MT][4];
 #pragma unroll
     for (int i = 0; i < L::MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float ref[NC], sum[NC], msum[NC], vf[NC], top_s[NC];
+    float ref[NC], sum[NC], msum[NC], vf[NC];
+    float top_s = 0.f;  // a step of V beyond this sets the factors again
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       ref[c] = 0.f;
       sum[c] = msum[c] = 0.f;
       vf[c] = 1.f;
-      top_s[c] = 0.f;  // kYMax / vf once vf is set: a step of V beyond sets it again
     }
+    // what this lane reads of a stage
+    const int ko = k_byte<RB>(tile_row(gq), t * L::KL * 4 / 16) + t * L::KL * 4 % 16;
+    const int vo = R * RB + v_byte<RB>(t, gq * L::VB / 16) + gq * L::VB % 16;
+    const int po = 2 * R * RB + tile_row(gq) * 8;
 
     int stage = 0;
     bool fresh = true;  // no step so far; each has a row that is seen
@@ -398,9 +415,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // all lanes' copies are here, and the stage to be filled has been read
       fetch(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
-      const uint8_t* sk = my_stage + stage * L::STAGE;
-      const uint8_t* sv = sk + R * RB;
-      const uint2* sp = reinterpret_cast<const uint2*>(sk + 2 * R * RB);
+      const uint8_t* st = my_stage + stage * L::STAGE;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       // scores relative to the running maximum, in log2
       float x[NT][2][NC], vs[NT][2], vm[NT][2];
@@ -413,9 +428,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int c = 0; c < L::KW / L::KL; ++c) {
-            const int b = t * (L::KL * 4);
-            const uint8_t* a =
-                sk + k_byte<RB>(16 * h + tile_row(gq) + 8 * q, c * 4 + b / 16) + b % 16;
+            const uint8_t* a = st + (ko ^ (c * 64)) + (16 * h + 8 * q) * RB;
             if constexpr (L::KL == 4) {
               const uint4 w = *reinterpret_cast<const uint4*>(a);
               ka[q][4 * c] = w.x; ka[q][4 * c + 1] = w.y;
@@ -443,39 +456,38 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint2 par = sp[16 * h + tile_row(gq) + 8 * q];
-          const float mk = __uint_as_float(par.x << 16), st = __uint_as_float(par.x & 0xffff0000u);
+          const uint2 par = *reinterpret_cast<const uint2*>(st + po + (16 * h + 8 * q) * 8);
+          const float mk = __uint_as_float(par.x << 16), sk = __uint_as_float(par.x & 0xffff0000u);
           vm[h][q] = __uint_as_float(par.y << 16);
           vs[h][q] = __uint_as_float(par.y & 0xffff0000u);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const float dot = kSplit ? s4[2 * q] + s4[2 * q + 1] : s4[2 * q + c];
-            x[h][q][c] = fmaf(dot * qmul[c], st, fmaf(mk, qsum[c], -ref[c]));
+            const float dot = kSplit ? s4[2 * q] + s4[2 * q + 1] : s4[2 * q + c];  // NC 1: c = 0
+            x[h][q][c] = fmaf(dot * qmul[c], sk, fmaf(mk, qsum[c], -ref[c]));
           }
         }
       }
-      // rows behind the last that the query sees
-      if (tile_pos(step * R + R - 16) + 16 > it.limit || (p.idx && step * R + R > keys)) {
+      if ((step + 1) * R > keys) {  // rows behind the last that the query sees
 #pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          const int pos = tile_pos(step * R + 16 * h);
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            if (pos + tile_row(gq) + 8 * q >= it.limit) {
+            if (step * R + 16 * h + 8 * q + tile_row(gq) >= keys) {
 #pragma unroll
               for (int c = 0; c < NC; ++c) x[h][q][c] = neg_inf();
             }
-        }
       }
 #pragma unroll
       for (int h = 0; h < NT; ++h)
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q) {
+          over = over || vs[h][q] > top_s;
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            over = over || x[h][q][c] > kOver || vs[h][q] > top_s[c];
+          for (int c = 0; c < NC; ++c) over = over || x[h][q][c] > kOver;
+        }
       if (__any_sync(0xffffffffu, over)) {
         // references to the maxima, and the factors of p s with them
+        top_s = __int_as_float(0x7f800000);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           float top = fresh ? neg_inf() : 0.f;
@@ -501,12 +513,12 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           sum[c] *= down;
           msum[c] *= down;
           vf[c] = f;
-          top_s[c] = kYMax / f;
+          top_s = fminf(top_s, kYMax / f);
 #pragma unroll
           for (int i = 0; i < L::MT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (kSplit || (e & 1) == c) acc[i][e] *= mul;
+              if (NC == 1 || (e & 1) == c) acc[i][e] *= mul;
         }
         fresh = false;
       }
@@ -527,14 +539,13 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           b0 = transposed(half2_bits(y[0][0], y[0][0] - __half2float(__float2half_rn(y[0][0]))));
           b1 = transposed(half2_bits(y[1][0], y[1][0] - __half2float(__float2half_rn(y[1][0]))));
         } else {
-          b0 = transposed(half2_bits(y[0][0], y[0][1]));
-          b1 = transposed(half2_bits(y[1][0], y[1][1]));
+          b0 = transposed(half2_bits(y[0][0], NC == 2 ? y[0][NC - 1] : 0.f));
+          b1 = transposed(half2_bits(y[1][0], NC == 2 ? y[1][NC - 1] : 0.f));
         }
         uint32_t va[4][L::VW];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int b = gq * L::VB;
-          const uint8_t* a = sv + v_byte<RB>(16 * h + 4 * q + t, b / 16) + b % 16;
+          const uint8_t* a = st + vo + (16 * h + 4 * q) * RB;
           if constexpr (L::VB == 16) {
             const uint4 w = *reinterpret_cast<const uint4*>(a);
             va[q][0] = w.x; va[q][1] = w.y; va[q][2] = w.z; va[q][3] = w.w;
@@ -580,7 +591,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], o);
         msum[c] += __shfl_xor_sync(0xffffffffu, msum[c], o);
       }
-      const int h = kSplit ? t : 2 * t + c;
+      const int h = NC * t + c;
       if (gq == 0) {
         sref[warp][h] = fresh ? kNone : ref[c];
         sl[warp][h] = sum[c];
@@ -598,30 +609,51 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     __syncthreads();
     // the CTA's: finished, or its part of the item
     const bool cut = s0 > 0 || s1 < it.steps;
-    for (int e = threadIdx.x; e < heads * D; e += kThr) {
-      const int h = e / D, d = e % D;
-      float top = sref[0][h];
+    if (threadIdx.x < HC) {
+      const int h = threadIdx.x;
+      float top = sref[0][h], l = 0.f;
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sref[w][h]);
-      float o = 0.f, l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(sref[w][h] - top);
-        o = fmaf(reinterpret_cast<const float*>(ring + w * L::RING)[e], f, o);
         l = fmaf(sl[w][h], f, l);
+        sw[w][h] = f;
       }
+      // what a finished element is multiplied by, and the statistics
+      const bool some = l > 0.f || l != l;
       if (cut) {
-        float* w = p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 2);
-        w[d] = o;
-        if (d == 0) {
+        if (h < heads) {
+          float* w = p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 4);
           w[D] = top;
           w[D + 1] = l;
         }
       } else {
-        const int64_t r = int64_t(it.row) * g.H + head0 + h;
-        static_cast<T*>(p.out)[r * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
-        if (d == 0) p.lse[r] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
+        const float r = some ? 1.f / l : 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sw[w][h] *= r;
+        if (h < heads)
+          p.lse[int64_t(it.row) * g.H + head0 + h] = some ? (top + lg2(l)) * kLn2 : neg_inf();
       }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < heads * D; e += kThr * 4) {
+      const int h = e / D, d = e % D;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(ring + w * L::RING + e * 4);
+        const float f = sw[w][h];
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+      if (cut)
+        *reinterpret_cast<float4*>(
+            p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 4) + d) = o;
+      else
+        store4(static_cast<T*>(p.out) + (int64_t(it.row) * g.H + head0 + h) * D + d, o);
     }
     if (p.ctas == 0) return;
     if (threadIdx.x == 0 && s0 == 0)
@@ -633,55 +665,63 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   }
 }
 
-// Joins an item that was cut: 8 warps share its parts, a lane has an element.
+// Joins an item that was cut.  A thread has four elements; the threads that the
+// block has more than these share the parts.
 template <class T, int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int hc) {
-  __shared__ float so[8][32], sr[8], sl[8];
+  __shared__ float4 so[256];
+  __shared__ float sr[256], sl[256];
   const BlockGeom& g = p.c.g;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads_of = g.Hkv * p.groups;
+  const int heads_of = g.Hkv * p.groups;
   const int u = blockIdx.x / heads_of, hi = blockIdx.x % heads_of;
   const int cgrp = hi % p.groups, kh = hi / p.groups;
   const int heads = min(hc, g.G - cgrp * hc);
+  const int quads = heads * (D / 4);                        // of the item
+  const int mine = (quads + gridDim.y - 1) / gridDim.y;     // of this block: at most 256
+  const int q = blockIdx.y * mine + threadIdx.x % mine, grp = threadIdx.x / mine, ng = 256 / mine;
   const bool live = seq_row(g.seq_q, g.S, g.Nq, u).s >= 0;
   cudaGridDependencySynchronize();  // the parts are there
   const int2 in = live ? p.info[blockIdx.x] : make_int2(0, 0);
   if (in.y == 0) return;
-  // part i: the first CTA's second slot, then the first slots of those that follow
-  const auto part = [&](int i) {
-    return p.part + ((int64_t(in.x) + i) * 2 + (i == 0)) * hc * (D + 2);
-  };
-  for (int e0 = blockIdx.y * 32; e0 < heads * D; e0 += gridDim.y * 32) {
-    const int h = e0 / D, d = e0 % D + lane;
-    float top = kNone, o = 0.f, l = 0.f;
-    for (int i = warp; i < in.y; i += 8) {
-      const float* w = part(i) + h * (D + 2);
-      const float r = w[D], x = w[d], y = w[D + 1], m = fmaxf(top, r);
-      const float f0 = ex2(top - m), f1 = ex2(r - m);
-      o = fmaf(o, f0, x * f1);
-      l = fmaf(l, f0, y * f1);
+  const int h = q / (D / 4), d = q % (D / 4) * 4;
+  float top = kNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (q < quads && grp < ng) {
+#pragma unroll 4
+    for (int i = grp; i < in.y; i += ng) {
+      // part i: the first CTA's second slot, then the first slots of those that follow
+      const float* w = p.part + (((int64_t(in.x) + i) * 2 + (i == 0)) * hc + h) * (D + 4);
+      const float4 x = *reinterpret_cast<const float4*>(w + d);
+      const float2 st = *reinterpret_cast<const float2*>(w + D);
+      const float m = fmaxf(top, st.x), f0 = ex2(top - m), f1 = ex2(st.x - m);
+      o.x = fmaf(o.x, f0, x.x * f1);
+      o.y = fmaf(o.y, f0, x.y * f1);
+      o.z = fmaf(o.z, f0, x.z * f1);
+      o.w = fmaf(o.w, f0, x.w * f1);
+      l = fmaf(l, f0, st.y * f1);
       top = m;
     }
-    so[warp][lane] = o;
-    if (lane == 0) {
-      sr[warp] = top;
-      sl[warp] = l;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      top = sr[0];
-      for (int w = 1; w < 8; ++w) top = fmaxf(top, sr[w]);
-      o = l = 0.f;
-      for (int w = 0; w < 8; ++w) {
-        const float f = ex2(sr[w] - top);
-        o = fmaf(so[w][lane], f, o);
-        l = fmaf(sl[w], f, l);
-      }
-      const int64_t q = int64_t(u) * g.H + kh * g.G + cgrp * hc + h;
-      static_cast<T*>(p.out)[q * D + d] = T(l > 0.f || l != l ? o / l : 0.f);
-      if (d == 0) p.lse[q] = l > 0.f || l != l ? (top + lg2(l)) * kLn2 : neg_inf();
-    }
-    __syncthreads();
   }
+  so[threadIdx.x] = o;
+  sr[threadIdx.x] = top;
+  sl[threadIdx.x] = l;
+  __syncthreads();
+  if (grp > 0 || q >= quads) return;
+  for (int i = 1; i < ng; ++i) {
+    const int x = threadIdx.x + i * mine;
+    const float m = fmaxf(top, sr[x]), f0 = ex2(top - m), f1 = ex2(sr[x] - m);
+    o.x = fmaf(o.x, f0, so[x].x * f1);
+    o.y = fmaf(o.y, f0, so[x].y * f1);
+    o.z = fmaf(o.z, f0, so[x].z * f1);
+    o.w = fmaf(o.w, f0, so[x].w * f1);
+    l = fmaf(l, f0, sl[x] * f1);
+    top = m;
+  }
+  const bool some = l > 0.f || l != l;
+  const float r = some ? 1.f / l : 0.f;
+  const int64_t row = int64_t(u) * g.H + kh * g.G + cgrp * hc + h;
+  store4(static_cast<T*>(p.out) + row * D + d, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+  if (d == 0) p.lse[row] = some ? (top + lg2(l)) * kLn2 : neg_inf();
 }
 
 struct Shape {
@@ -693,7 +733,7 @@ struct Shape {
 Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   const BlockGeom& g = p.g;
   Shape s{};
-  s.hc = dt == GATTN_F32 ? kCols / 2 : kCols;
+  s.hc = dt == GATTN_F32 || g.G <= 4 ? 4 : 8;
   s.groups = (g.G + s.hc - 1) / s.hc;
   s.items = int64_t(g.U) * g.Hkv * s.groups;
   const int64_t keys = lists ? std::min<int64_t>(int64_t(g.topk) * g.block, max_keys) : max_keys;
@@ -703,33 +743,31 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   // Items of their own: nothing to cut, or so many that the last ones to run weigh little
   if (steps <= kMinSteps || s.items >= 8 * slots) return s;
   s.ctas = int(std::min(slots, (s.items * steps + kMinSteps - 1) / kMinSteps));
-  s.bytes = size_t(s.ctas) * 2 * s.hc * (g.D + 2) * 4 + size_t(s.items) * 8;
+  s.bytes = size_t(s.ctas) * 2 * s.hc * (g.D + 4) * 4 + size_t(s.items) * 8;
   return s;
 }
 
-template <class T, int BITS, int D>
+template <class T, int BITS, int D, int NC>
 cudaError_t launch(const AttnParams& p, const Shape& s, cudaStream_t st) {
   using L = Lay<BITS, D>;
   constexpr int smem = kWarps * L::RING;
+  const auto kernel = cache_attn_kernel<T, BITS, D, NC>;
   static std::atomic<uint64_t> set{0};  // devices whose kernel has been given its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(cache_attn_kernel<T, BITS, D>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  cache_attn_kernel<T, BITS, D>
-      <<<unsigned(s.ctas ? s.ctas : s.items), kThr, smem, st>>>(p);
+  kernel<<<unsigned(s.ctas ? s.ctas : s.items), kThr, smem, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || s.ctas == 0) return e;
-  // the join's launch overlaps the kernel's end
+  // the join's launch overlaps the kernel's end; few items are spread over more blocks each
   cudaLaunchConfig_t cfg{};
-  const int64_t wide = int64_t(sm_count()) * 4 / s.items;
-  cfg.gridDim = dim3(unsigned(s.items),
-                     unsigned(std::min<int64_t>(std::max<int64_t>(wide, 1), s.hc * D / 32)));
+  const int64_t wide = std::max<int64_t>(int64_t(sm_count()) * 4 / s.items, 1);
+  cfg.gridDim = dim3(unsigned(s.items), unsigned(std::min<int64_t>(wide, s.hc * D / 32)));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -739,11 +777,19 @@ cudaError_t launch(const AttnParams& p, const Shape& s, cudaStream_t st) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, p, s.hc);
 }
+
+template <class T, int BITS, int D>
+cudaError_t by_heads(const AttnParams& p, const Shape& s, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (s.hc == 8) return launch<T, BITS, D, 2>(p, s, st);
+  return launch<T, BITS, D, 1>(p, s, st);
+}
+
 template <class T, int BITS>
 cudaError_t by_width(const AttnParams& p, const Shape& s, cudaStream_t st) {
-  if (p.c.g.D == 32) return launch<T, BITS, 32>(p, s, st);
-  if (p.c.g.D == 64) return launch<T, BITS, 64>(p, s, st);
-  return launch<T, BITS, 128>(p, s, st);
+  if (p.c.g.D == 32) return by_heads<T, BITS, 32>(p, s, st);
+  if (p.c.g.D == 64) return by_heads<T, BITS, 64>(p, s, st);
+  return by_heads<T, BITS, 128>(p, s, st);
 }
 
 }  // namespace
@@ -763,7 +809,7 @@ gattn_status launch_cache_fwd(const CacheParams& c, gattn_dtype dt, int max_keys
   p.out = out;
   p.lse = lse;
   p.part = static_cast<float*>(ws);
-  p.info = reinterpret_cast<int2*>(p.part + int64_t(s.ctas) * 2 * s.hc * (c.g.D + 2));
+  p.info = reinterpret_cast<int2*>(p.part + int64_t(s.ctas) * 2 * s.hc * (c.g.D + 4));
   p.groups = s.groups;
   p.ctas = s.ctas;
   p.max_keys = max_keys;
