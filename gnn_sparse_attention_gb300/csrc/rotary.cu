@@ -95,18 +95,20 @@ struct Pack<__nv_bfloat16> {
   }
 };
 
-// Whole vectors.  Thread j of a head: its pair of vectors j, or a vector behind
-// the first R elements, which is copied.
+// Whole vectors.  Thread j of a head has, with halves, vector j of the first half and its partner
+// in the second; else vector j alone, whose pairs are neighbours.  Vectors behind the
+// first R elements are copied.
 template <class T, bool HALF>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) {
   constexpr int V = Pack<T>::V;
-  constexpr int UN = 4;  // heads on their way at a time
+  constexpr int NV = HALF ? 2 : 1;  // vectors of a thread and head
+  constexpr int NP = V * NV / 2;    // pairs
+  constexpr int UN = 8 / NV;        // heads on their way at a time
   const int per_row = p.cph * p.hg;
   const int lr = threadIdx.x / per_row, rem = threadIdx.x - lr * per_row;
   const int64_t row = int64_t(blockIdx.x) * p.rpb + lr;
   if (lr >= p.rpb || row >= p.N) return;
   const int h0 = rem / p.cph, j = rem - h0 * p.cph;
-  const int pairs = p.R / (2 * V);
   int64_t at;
   if (!position(p, int(row), &at)) return;
   const T* q = reinterpret_cast<const T*>(p.q) + row * p.qs;
@@ -115,16 +117,17 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) 
   T* ko = reinterpret_cast<T*>(p.ko) + row * p.kos;
   const auto src = [&](int h) { return h < p.H ? q + h * p.D : k + (h - p.H) * p.D; };
   const auto dst = [&](int h) { return h < p.H ? qo + h * p.D : ko + (h - p.H) * p.D; };
-  if (j >= pairs) {
-    const int o = p.R + (j - pairs) * V;
-    for (int h = h0; h < p.HT; h += p.hg)
-      *reinterpret_cast<uint4*>(dst(h) + o) = *reinterpret_cast<const uint4*>(src(h) + o);
-    return;
-  }
-  const int oa = HALF ? j * V : 2 * j * V, ob = HALF ? oa + p.R / 2 : oa + V;
-  float c[V], s[V];
+  const int turning = p.R / (V * NV);
+  const bool turns = j < turning;
+  const int oa = turns ? j * V : p.R + (j - turning) * V;
+  const int ob = oa + (HALF && turns ? p.R / 2 : 0);
+  float c[NP], s[NP];
 #pragma unroll
-  for (int i = 0; i < V; ++i) turn(p, at, p.freqs[j * V + i], &c[i], &s[i]);
+  for (int i = 0; i < NP; ++i) {
+    c[i] = 1.f;
+    s[i] = 0.f;
+    if (turns) turn(p, at, p.freqs[j * NP + i], &c[i], &s[i]);
+  }
   for (int h = h0; h < p.HT; h += UN * p.hg) {
     uint4 a[UN], b[UN];
 #pragma unroll
@@ -132,23 +135,27 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) 
       if (h + u * p.hg < p.HT) {
         const T* x = src(h + u * p.hg);
         a[u] = *reinterpret_cast<const uint4*>(x + oa);
-        b[u] = *reinterpret_cast<const uint4*>(x + ob);
+        if (HALF) b[u] = *reinterpret_cast<const uint4*>(x + ob);
       }
 #pragma unroll
     for (int u = 0; u < UN; ++u)
       if (h + u * p.hg < p.HT) {
-        float f[2 * V], o[2 * V];
+        T* z = dst(h + u * p.hg);
+        if (!turns) {
+          *reinterpret_cast<uint4*>(z + oa) = a[u];
+          continue;
+        }
+        float f[NV * V], o[NV * V];
         Pack<T>::get(a[u], f);
-        Pack<T>::get(b[u], f + V);
+        if (HALF) Pack<T>::get(b[u], f + V * (NV - 1));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < NP; ++i) {
           const int x = HALF ? i : 2 * i, y = HALF ? i + V : 2 * i + 1;
           o[x] = f[x] * c[i] - f[y] * s[i];
           o[y] = f[x] * s[i] + f[y] * c[i];
         }
-        T* z = dst(h + u * p.hg);
         *reinterpret_cast<uint4*>(z + oa) = Pack<T>::put(o);
-        *reinterpret_cast<uint4*>(z + ob) = Pack<T>::put(o + V);
+        if (HALF) *reinterpret_cast<uint4*>(z + ob) = Pack<T>::put(o + V * (NV - 1));
       }
   }
 }
@@ -208,7 +215,7 @@ void launch(RotParams& p, bool vectors, cudaStream_t st) {
     rotary_any_kernel<T><<<dim3(unsigned(n < 1 << 20 ? n : 1 << 20), heads), kRotThreads, 0, st>>>(p);
     return;
   }
-  p.cph = p.R / (2 * V) + (p.D - p.R) / V;
+  p.cph = p.R / (p.half ? 2 * V : V) + (p.D - p.R) / V;
   // heads side by side: the fewest that give every SM about 1,024 threads, since every thread of a
   // row forms the same sines again
   const int64_t want = int64_t(sm_count()) * 1024;
@@ -291,7 +298,7 @@ gattn_status gattn_rotary(const gattn_rotary_desc* d, const void* Q, const void*
   p.kos = kos;
   const int V = 16 / es;
   const auto vec = [&](const void* x, int64_t stride) { return al(x, 16) && stride % V == 0; };
-  const bool vectors = d->D % V == 0 && d->width % (2 * V) == 0 && vec(Q, qs) && vec(Q_out, qos) &&
+  const bool vectors = d->D % V == 0 && d->width % (p.half ? 2 * V : V) == 0 && vec(Q, qs) && vec(Q_out, qos) &&
                        (d->Hkv == 0 || (vec(K, ks) && vec(K_out, kos))) &&
                        d->D / V <= kRotThreads;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
