@@ -5,15 +5,17 @@
 // bits, two with 8), D / 8 lanes a row, so a warp's load covers whole rows and
 // its store whole rows of levels.  A warp stays with one key head and takes
 // neighbouring tokens, which lie side by side in the cache.  Everything is read
-// and written once: the bound is HBM, next to it the issue slots (about 13
-// instructions an element where HBM leaves 14).
+// and written once: the bound is HBM, next to it the issue slots.  What is
+// formed once a row (bounds, step, place in the cache) is formed by one lane: the
+// lanes of a row hold eight rows (K and V of four tokens) and reduce them so that each
+// lane ends with rows of its own.
 //
-// Sums: levels are whole numbers, and a step is an 8-bit whole number times a
-// power of two, so the sum over a block is one over whole numbers as long as the
-// steps and least values of its rows lie within 2^23 of each other: exact in
-// 64-bit integers, with one multiply-add an element and no fp64 until the end
-// (the GPU adds two fp64 numbers a clock and SM).  Blocks beyond that range are
-// summed in fp64, row by row.
+// Sums: sum (m + s u) over a block is sum m plus sum s u, and the second is a
+// product of levels with a vector: tensor cores, as in the attention (levels are
+// fp16 whole numbers as they lie).  Steps have 8 bits and levels 4 or 8, so the
+// fp32 sums of up to 128 rows are exact as long as the steps' exponents are within
+// 5 (1 with 8 bits) of each other: the eight columns of a product take a class of
+// exponents each.  Blocks beyond all classes are summed in fp64, row by row.
 #include "cache.cuh"
 
 namespace gattn {
@@ -86,126 +88,218 @@ struct Levels<8> {
   using W = uint2;
 };
 
-// A row's (m, s) as a pair of bf16, and the levels of the lane's eight elements.
-// LPR lanes share the row.
-template <int BITS, int LPR>
-__device__ __forceinline__ uint32_t quantise(const float* f, typename Levels<BITS>::W* out) {
-  constexpr float L = BITS == 4 ? 15.f : 255.f;
-  float lo = min_nan(min_nan(min_nan(f[0], f[1]), min_nan(f[2], f[3])),
-                     min_nan(min_nan(f[4], f[5]), min_nan(f[6], f[7])));
-  float hi = max_nan(max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3])),
-                     max_nan(max_nan(f[4], f[5]), max_nan(f[6], f[7])));
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+// least element and minus the greatest, NaN if there is one
+template <class T>
+struct Bounds;
+template <>
+struct Bounds<float> {
+  float lo, nhi;
+  __device__ static Bounds of(const Row8<float>& r) {
+    float f[8];
+    r.get(f);
+    return {min_nan(min_nan(min_nan(f[0], f[1]), min_nan(f[2], f[3])),
+                    min_nan(min_nan(f[4], f[5]), min_nan(f[6], f[7]))),
+            -max_nan(max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3])),
+                     max_nan(max_nan(f[4], f[5]), max_nan(f[6], f[7])))};
   }
+  __device__ Bounds from(int o) const {
+    return {__shfl_xor_sync(0xffffffffu, lo, o), __shfl_xor_sync(0xffffffffu, nhi, o)};
+  }
+  __device__ void join(Bounds x) {
+    lo = min_nan(lo, x.lo);
+    nhi = min_nan(nhi, x.nhi);
+  }
+  __device__ float least() const { return lo; }
+  __device__ float greatest() const { return -nhi; }
+};
+template <>
+struct Bounds<__nv_bfloat16> {
+  uint32_t z;  // both as bf16
+  __device__ static uint32_t least2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static uint32_t greatest2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static Bounds of(const Row8<__nv_bfloat16>& r) {
+    const uint32_t lo = least2(least2(r.a.x, r.a.y), least2(r.a.z, r.a.w));
+    const uint32_t hi = greatest2(greatest2(r.a.x, r.a.y), greatest2(r.a.z, r.a.w)) ^ 0x80008000u;
+    return {least2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632))};
+  }
+  __device__ Bounds from(int o) const { return {__shfl_xor_sync(0xffffffffu, z, o)}; }
+  __device__ void join(Bounds x) { z = least2(z, x.z); }
+  __device__ float least() const { return __uint_as_float(z << 16); }
+  __device__ float greatest() const { return -__uint_as_float(z & 0xffff0000u); }
+};
+
+// (m, s) of a row as a pair of bf16, and the factors of its levels
+struct Steps {
+  uint32_t par;
+  float inv, c;
+  bool clamp;  // levels may leave [0, L] by rounding, or the row is not finite
+};
+template <int BITS>
+__device__ __forceinline__ Steps steps(float lo, float hi) {
+  constexpr float L = BITS == 4 ? 15.f : 255.f;
   // m: bf16 towards -inf, not below the least finite one
   uint32_t mb = __float_as_uint(lo);
   mb = (int32_t(mb) < 0 ? mb + 0xffffu : mb) & 0xffff0000u;
   if (mb == 0xff800000u) mb = 0xff7f0000u;
-  float m = __uint_as_float(mb);
+  const float m = __uint_as_float(mb);
   // s: bf16 towards +inf
   const float st = __fdiv_rn(__fsub_rn(0.5f * hi, 0.5f * m), L / 2);
   uint32_t sb = (__float_as_uint(st) + 0xffffu) & 0xffff0000u;
   if (sb < 0x00800000u) sb = 0;  // below 2^-126
-  const float s = __uint_as_float(sb);
-  const float inv = sb ? __frcp_rn(s) : 0.f;
-  const float c = __fmul_rn(-m, inv);
+  Steps r;
+  r.inv = sb ? __frcp_rn(__uint_as_float(sb)) : 0.f;
+  r.c = __fmul_rn(-m, r.inv);
+  r.par = (mb >> 16) | sb;
+  // c is rounded to 2^-24 of its size: below 2^21 that is less than a quarter of a level
+  r.clamp = !(fabsf(r.c) < 2097152.f);
+  if (!(fabsf(lo) < __int_as_float(0x7f800000) && fabsf(hi) < __int_as_float(0x7f800000))) {
+    r.par = 0x7fc07fc0u;  // a non-finite element: the row is NaN, its levels 0
+    r.inv = r.c = 0.f;
+    r.clamp = true;
+  }
+  return r;
+}
+
+template <int BITS, bool CLAMP>
+__device__ __forceinline__ typename Levels<BITS>::W levels(const float* f, float inv, float c) {
+  constexpr float L = BITS == 4 ? 15.f : 255.f;
   // rounding to a whole number: the low bits of t + 1.5 2^23
   constexpr uint32_t kMagic = 0x4b400000u;
   uint32_t u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    u[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fmaf_rn(f[i], inv, c), 0.f), L), 12582912.f));
-  uint32_t w0 = 0, w1 = 0;
-  if (BITS == 4) {
+  for (int i = 0; i < 8; ++i) {
+    float t = __fmaf_rn(f[i], inv, c);
+    if (CLAMP) t = fminf(fmaxf(t, 0.f), L);
+    u[i] = __float_as_uint(__fadd_rn(t, 12582912.f)) - kMagic;
+  }
+  if constexpr (BITS == 4) {
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w0 += (u[i] - kMagic) << (4 * i);
+    for (int i = 0; i < 8; ++i) w += u[i] << (4 * i);
+    return w;
   } else {
+    uint32_t w0 = 0, w1 = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w0 += (u[i] - kMagic) << (8 * i);
-      w1 += (u[4 + i] - kMagic) << (8 * i);
+      w0 += u[i] << (8 * i);
+      w1 += u[4 + i] << (8 * i);
     }
+    return make_uint2(w0, w1);
   }
-  uint32_t par = (mb >> 16) | sb;
-  if (!(fabsf(lo) < __int_as_float(0x7f800000) && fabsf(hi) < __int_as_float(0x7f800000))) {
-    par = 0x7fc07fc0u;  // a non-finite element: the row is NaN
-    w0 = w1 = 0;
-  }
-  if constexpr (BITS == 4) *out = w0;
-  else *out = make_uint2(w0, w1);
-  return par;
 }
 
-// UN passes of 32 / LPR tokens each for one key head.
+// Tokens t0 + u * (32 / LPR) + (the lane's group), u < UN, for one key head.  Row 2u of a group is
+// K of token u, row 2u + 1 V.
 template <class T, int BITS, int LPR, int UN>
 __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CacheParams p,
                                                                   const T* __restrict__ K,
                                                                   const T* __restrict__ V) {
-  constexpr int RPW = 32 / LPR, D = LPR * 8;
+  constexpr int RPW = 32 / LPR, D = LPR * 8, NR = 2 * UN;
+  constexpr int OWN = NR > LPR ? NR / LPR : 1;  // rows of a lane in the end
   using W = typename Levels<BITS>::W;
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
   const int64_t w = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int kh = int(w % g.Hkv);
-  const int64_t t0 = w / g.Hkv * (RPW * UN);
-  if (t0 >= g.Nq) return;
-  Row8<T> rk[UN], rv[UN];
+  const int64_t t0 = w / g.Hkv * (RPW * UN) + sub;
+  if (t0 - sub >= g.Nq) return;
+  Row8<T> row[NR];
 #pragma unroll
   for (int u = 0; u < UN; ++u) {
-    const int64_t t = min(t0 + u * RPW + sub, int64_t(g.Nq) - 1);
-    rk[u].load(K + t * p.ks + kh * D + j * 8);
-    rv[u].load(V + t * p.vs + kh * D + j * 8);
+    const int64_t t = min(t0 + u * RPW, int64_t(g.Nq) - 1);
+    row[2 * u].load(K + t * p.ks + kh * D + j * 8);
+    row[2 * u + 1].load(V + t * p.vs + kh * D + j * 8);
   }
-  int from = 0;
+  // where the lane's own rows go, while they are on their way
+  const int first = j * NR / LPR;
+  int dst[OWN];
 #pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    const int64_t t = t0 + u * RPW + sub;
-    int64_t dst = -1;
+  for (int o = 0; o < OWN; ++o) {
+    const int64_t t = t0 + (first + o) / 2 * RPW;
+    dst[o] = -1;
     if (t < g.Nq) {
-      const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, int(t), from);
+      const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, int(t));
       if (x.s >= 0) {
-        from = x.s;
         const Span sp = span_k(g, x.s);
-        const int64_t pos = int64_t(x.i) + sp.len - x.n;
-        if (pos >= 0) dst = sp.beg + pos;
+        const int pos = x.i + sp.len - x.n;  // within +-2^31: all three are row counts
+        if (pos >= 0) dst[o] = sp.beg + pos;
       }
     }
-    float f[8];
-    W wk, wv;
-    rk[u].get(f);
-    const uint32_t pk = quantise<BITS, LPR>(f, &wk);
-    rv[u].get(f);
-    const uint32_t pv = quantise<BITS, LPR>(f, &wv);
-    if (dst >= 0) {
-      const int64_t r = int64_t(kh) * g.Nk + dst;
-      reinterpret_cast<W*>(p.k)[r * LPR + j] = wk;
-      reinterpret_cast<W*>(p.v)[r * LPR + j] = wv;
-      if (j == 0) p.par[r] = make_uint2(pk, pv);
+  }
+  Bounds<T> b[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) b[r] = Bounds<T>::of(row[r]);
+  int n = NR;
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    if (n > 1) {  // keep one half of the rows, give the other
+      n /= 2;
+      const bool up = j & o;
+#pragma unroll
+      for (int r = 0; r < NR / 2; ++r)
+        if (r < n) {
+          Bounds<T> keep = up ? b[r + n] : b[r];
+          const Bounds<T> give = up ? b[r] : b[r + n];
+          keep.join(give.from(o));
+          b[r] = keep;
+        }
+    } else {
+      b[0].join(b[0].from(o));
     }
+  }
+  Steps st[OWN];
+  bool clamp = false;
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) {
+    st[o] = steps<BITS>(b[o].least(), b[o].greatest());
+    clamp = clamp || st[o].clamp;
+    // lanes that share a row write it alike
+    if (dst[o] >= 0)
+      reinterpret_cast<uint32_t*>(p.par)[(int64_t(kh) * g.Nk + dst[o]) * 2 + ((first + o) & 1)] =
+          st[o].par;
+  }
+  clamp = __any_sync(0xffffffffu, clamp);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int from = r * LPR / NR, o = OWN > 1 ? r % OWN : 0;
+    const float inv = __shfl_sync(0xffffffffu, st[o].inv, from, LPR);
+    const float c = __shfl_sync(0xffffffffu, st[o].c, from, LPR);
+    const int to = __shfl_sync(0xffffffffu, dst[o], from, LPR);
+    float f[8];
+    row[r].get(f);
+    const W lev = clamp ? levels<BITS, true>(f, inv, c) : levels<BITS, false>(f, inv, c);
+    if (to >= 0)
+      reinterpret_cast<W*>(r & 1 ? p.v : p.k)[(int64_t(kh) * g.Nk + to) * LPR + j] = lev;
   }
 }
 
-// Eight values of a lane
+// Eight values of a lane.  A level, masked in place and put into the low bits of
+// 2^23, is a whole number times 16^i (256^i); the factor is taken out of the step.
 template <int BITS>
 __device__ __forceinline__ void values(typename Levels<BITS>::W w, uint32_t par, float* f) {
   const float m = __uint_as_float(par << 16), s = __uint_as_float(par & 0xffff0000u);
   if constexpr (BITS == 4) {
+    const float sc[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
+    const uint32_t half[2] = {w, w >> 16};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // a whole number in the low bits of 2^23 + n
-      const float n = __uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f;
-      f[i] = __fmaf_rn(s, n, m);
+      const float n = __uint_as_float((half[i / 4] & (15u << (4 * (i % 4)))) | 0x4b000000u);
+      f[i] = __fmaf_rn(sc[i % 4], n - 8388608.f, m);
     }
   } else {
     const uint32_t x[2] = {w.x, w.y};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float n = __uint_as_float(((x[i / 4] >> (8 * (i % 4))) & 255u) | 0x4b000000u) -
-                      8388608.f;
-      f[i] = __fmaf_rn(s, n, m);
+      const float n = __uint_as_float(__byte_perm(x[i / 4], 0x4b000000u, 0x7440 + i % 4));
+      f[i] = __fmaf_rn(s, n - 8388608.f, m);
     }
   }
 }
@@ -216,50 +310,51 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CachePara
                                                                  T* __restrict__ K,
                                                                  T* __restrict__ V) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
+  static_assert(UN <= LPR, "a lane finds one token's row");
   using W = typename Levels<BITS>::W;
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
   const int64_t w = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int kh = int(w % g.Hkv);
-  const int64_t t0 = w / g.Hkv * (RPW * UN);
-  if (t0 >= g.Nq) return;
-  int64_t r[UN];
-  int from = 0;
-#pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    const int64_t t = t0 + u * RPW + sub;
-    r[u] = -1;
+  const int64_t t0 = w / g.Hkv * (RPW * UN) + sub;
+  if (t0 - sub >= g.Nq) return;
+  int mine = -1;
+  {
+    const int64_t t = t0 + j % UN * RPW;
     if (t < g.Nq) {
-      const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, int(t), from);
+      const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, int(t));
       if (x.s >= 0) {
-        from = x.s;
         const Span sp = span_k(g, x.s);
         const int64_t pos = (since ? int64_t(since[x.s]) : int64_t(sp.len) - x.n) + x.i;
-        if (pos >= 0 && pos < sp.len) r[u] = int64_t(kh) * g.Nk + sp.beg + pos;
+        if (pos >= 0 && pos < sp.len) mine = sp.beg + int(pos);
       }
     }
   }
   W wk[UN], wv[UN];
   uint2 par[UN];
+  int r[UN];
 #pragma unroll
-  for (int u = 0; u < UN; ++u)
+  for (int u = 0; u < UN; ++u) {
+    r[u] = __shfl_sync(0xffffffffu, mine, u, LPR);
     if (r[u] >= 0) {
-      if (K) wk[u] = reinterpret_cast<const W*>(p.k)[r[u] * LPR + j];
-      if (V) wv[u] = reinterpret_cast<const W*>(p.v)[r[u] * LPR + j];
-      par[u] = p.par[r[u]];
+      const int64_t at = int64_t(kh) * g.Nk + r[u];
+      if (K) wk[u] = reinterpret_cast<const W*>(p.k)[at * LPR + j];
+      if (V) wv[u] = reinterpret_cast<const W*>(p.v)[at * LPR + j];
+      par[u] = p.par[at];
     }
+  }
+  const int64_t out = (t0 * g.Hkv + kh) * D + j * 8, step = int64_t(RPW) * g.Hkv * D;
 #pragma unroll
   for (int u = 0; u < UN; ++u)
     if (r[u] >= 0) {
-      const int64_t o = ((t0 + u * RPW + sub) * g.Hkv + kh) * D + j * 8;
       float f[8];
       if (K) {
         values<BITS>(wk[u], par[u].x, f);
-        Row8<T>::store(K + o, f);
+        Row8<T>::store(K + out + u * step, f);
       }
       if (V) {
         values<BITS>(wv[u], par[u].y, f);
-        Row8<T>::store(V + o, f);
+        Row8<T>::store(V + out + u * step, f);
       }
     }
 }
@@ -267,27 +362,36 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CachePara
 // --------------------------------------------------------------------------
 // sums
 // --------------------------------------------------------------------------
-// The whole number v times 2^e in fp64 (|v| < 2^53, v 2^e normal or 0), by integer instructions: the
-// conversion instruction runs at the fp64 rate.
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// x 2^e in fp64 (x is 0 or normal, the result normal), by integer instructions: the conversion
+// instruction runs at the fp64 rate, two a clock and SM
+__device__ __forceinline__ double widened(float x, int e) {
+  const uint32_t b = __float_as_uint(x);
+  if (b == 0) return 0.0;
+  return __hiloint2double(int(((b >> 3) & 0x0fffffffu) + (uint32_t(896 + e) << 20)), int(b << 29));
+}
+// the whole number v times 2^e (v 2^e is 0 or normal), rounded if |v| is 2^53 or more
 __device__ __forceinline__ double scaled(int64_t v, int e) {
-  if (v == 0) return 0.0;
-  const uint64_t a = v < 0 ? uint64_t(-v) : uint64_t(v);
-  const int z = __clzll(a);
-  const uint64_t mant = (a << z) >> 11;  // 53 bits, the first set
-  const uint64_t bits = (mant & 0xfffffffffffffull) | (uint64_t(1023 + 63 - z + e) << 52) |
-                        (v < 0 ? 0x8000000000000000ull : 0);
-  return __longlong_as_double(int64_t(bits));
+  return v == 0 ? 0.0 : __ll2double_rn(v) * __hiloint2double((1023 + e) << 20, 0);
 }
 
-// One warp sums one block of one key head: D / 8 lanes a row, 32 / (D / 8)
-// rows side by side, their sums joined by shuffles.
-template <int BITS, int LPR>
+// One warp sums one block of one key head: 16 rows a product, of which a lane
+// holds D / 8 levels of four.
+template <int BITS, int D>
 __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
     const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int zs) {
-  constexpr int RPW = 32 / LPR, D = LPR * 8, MAXR = kBlkTile / 32;
-  using W = typename Levels<BITS>::W;
+  constexpr int RB = D * BITS / 8, VB = RB / 8, VW = VB < 4 ? 1 : VB / 4, MT = D / 16;
+  constexpr int MAXR = kBlkTile / 32;
+  constexpr int kClass = BITS == 4 ? 5 : 1;  // exponents of a class: 8 + 7 + BITS + this is 24 bits
   const BlockGeom& g = p.g;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
   const int64_t wid = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int kh = int(wid % g.Hkv);
   const int64_t item = wid / g.Hkv;
@@ -311,91 +415,142 @@ __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
     const int64_t pos = int64_t(b) * g.block;
     const int n = pos >= 0 && pos < sp.len ? int(min(int64_t(g.block), sp.len - pos)) : 0;
     const int64_t r0 = int64_t(kh) * g.Nk + sp.beg + (n ? pos : 0);
-    const W* lev = reinterpret_cast<const W*>(p.k) + r0 * LPR + j;
-    // exponents of what is not zero: the sums are whole multiples of the least
+    double* out = sums + (int64_t(piece) * g.Hkv + kh) * D;
+    const uint8_t* lev = p.k + r0 * RB + gq * VB;
     uint32_t par[MAXR];
-    int emin = 255, emax = 0;
 #pragma unroll
-    for (int i = 0; i < MAXR; ++i) {
+    for (int i = 0; i < MAXR; ++i)
       par[i] = lane + 32 * i < n ? p.par[r0 + lane + 32 * i].x : 0u;
-      const int em = (par[i] >> 7) & 255, es = (par[i] >> 23) & 255;
-      // a least value below 2^-126 counts as one of that exponent
-      if (par[i] & 0x7fffu) emin = min(emin, max(em, 1));
-      if (es) emin = min(emin, es);
-      emax = max(emax, max(em, es));
-    }
-    emin = __reduce_min_sync(0xffffffffu, emin);
-    emax = __reduce_max_sync(0xffffffffu, emax);
-    double* out = sums + (int64_t(piece) * g.Hkv + kh) * D + j * 8;
-    if (emax - emin <= 23 && emax < 255) {
-      int64_t base_sum = 0;
-      uint32_t wt[MAXR];
+    // levels of 64 rows are on their way while the exponents are looked at
+    uint32_t v[4][4][VW];
+    const auto fetch = [&](int at) {
 #pragma unroll
-      for (int i = 0; i < MAXR; ++i) {
-        const int em = (par[i] >> 7) & 255, es = (par[i] >> 23) & 255;
-        const int64_t mm = int64_t((par[i] & 127u) | (em ? 128u : 0u)) << (par[i] & 0x7fffu ? max(em, 1) - emin : 0);
-        base_sum += par[i] & 0x8000u ? -mm : mm;
-        wt[i] = es ? (((par[i] >> 16) & 127u) | 128u) << (es - emin) : 0u;
-      }
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) base_sum += __shfl_xor_sync(0xffffffffu, base_sum, o);
-      uint64_t a[8];
+        for (int q = 0; q < 4; ++q) {
+          const int r = at + 16 * c + 2 * t + 8 * (q >> 1) + (q & 1);
+          const uint8_t* a = lev + int64_t(r) * RB;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] = 0;
-#pragma unroll
-      for (int i = 0; i < MAXR; ++i)
-        if (32 * i < n) {
-#pragma unroll
-          for (int c = 0; c < LPR; c += 4) {  // four rows on their way at a time
-            W w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int t = 32 * i + (c + q) * RPW + sub;
-              if (t < n) w[q] = lev[int64_t(t) * LPR];
-              else w[q] = W{};
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t x = __shfl_sync(0xffffffffu, wt[i], (c + q) * RPW + sub);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                uint32_t u;
-                if constexpr (BITS == 4) u = (w[q] >> (4 * k)) & 15u;
-                else u = ((k < 4 ? w[q].x : w[q].y) >> (8 * (k % 4))) & 255u;
-                a[k] += uint64_t(x) * u;
-              }
+          for (int w = 0; w < VW; ++w) v[c][q][w] = 0;
+          if (r < n) {
+            if constexpr (VB == 16) {
+              const uint4 x = *reinterpret_cast<const uint4*>(a);
+              v[c][q][0] = x.x; v[c][q][1] = x.y; v[c][q][2] = x.z; v[c][q][3] = x.w;
+            } else if constexpr (VB == 8) {
+              const uint2 x = *reinterpret_cast<const uint2*>(a);
+              v[c][q][0] = x.x; v[c][q][1] = x.y;
+            } else if constexpr (VB == 4) {
+              v[c][q][0] = *reinterpret_cast<const uint32_t*>(a);
+            } else {
+              v[c][q][0] = *reinterpret_cast<const uint16_t*>(a);
             }
           }
         }
+    };
+    fetch(0);
+    // exponents of the steps and of the least values (one below 2^-126 counts as that)
+    int se = 255, sx = 0, me = 255, mx = 0;
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
+    for (int i = 0; i < MAXR; ++i) {
+      const int em = (par[i] >> 7) & 255, es = (par[i] >> 23) & 255;
+      if (par[i] & 0x7fffu) me = min(me, max(em, 1));
+      mx = max(mx, em);
+      if (es) se = min(se, es);
+      sx = max(sx, es);
+    }
+    se = __reduce_min_sync(0xffffffffu, se);
+    sx = __reduce_max_sync(0xffffffffu, sx);
+    me = __reduce_min_sync(0xffffffffu, me);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (sx - se < 8 * kClass && sx < 255 && mx < 255 && mx - me <= 46) {
+      int64_t msum = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
-      if (sub == 0) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2)
-          reinterpret_cast<double2*>(out)[k / 2] =
-              make_double2(scaled(int64_t(a[k]) + base_sum, emin - 134),
-                           scaled(int64_t(a[k + 1]) + base_sum, emin - 134));
+      for (int i = 0; i < MAXR; ++i) {
+        const int em = (par[i] >> 7) & 255;
+        const int64_t x = int64_t((par[i] & 127u) | (em ? 128u : 0u))
+                          << (par[i] & 0x7fffu ? max(em, 1) - me : 0);
+        msum += par[i] & 0x8000u ? -x : x;
       }
-    } else if (sub == 0) {
-      double a[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] = 0.0;
-      for (int t = 0; t < n; ++t) {
-        const uint32_t q = p.par[r0 + t].x;
-        const double m = __uint_as_float(q << 16), st = __uint_as_float(q & 0xffff0000u);
-        const W w = lev[int64_t(t) * LPR];
+      for (int o = 16; o > 0; o >>= 1) msum += __shfl_xor_sync(0xffffffffu, msum, o);
+      const double mt = scaled(msum, me - 134);
+      float acc[MT][4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t u;
-          if constexpr (BITS == 4) u = (w >> (4 * k)) & 15u;
-          else u = ((k < 4 ? w.x : w.y) >> (8 * (k % 4))) & 255u;
-          a[k] += m + st * u;
+      for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+      for (int at = 0; at < kBlkTile; at += 64) {
+        if (at >= n) break;
+        if (at > 0) fetch(at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (at + 16 * c >= n) break;
+          // steps of rows 2t, 2t + 1, 2t + 8, 2t + 9 for column gq, as multiples of its class
+          uint32_t h[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t two = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = __shfl_sync(0xffffffffu, par[(at + 16 * c) / 32],
+                                             (16 * c) % 32 + 2 * t + 8 * q + e);
+              const int k = int((x >> 23) & 255) - se - gq * kClass;
+              // fp16 with exponent k: 8 bits of mantissa
+              const uint32_t f = (uint32_t(k + 15) << 10) | ((x >> 13) & 0x3f8u);
+              two |= (k >= 0 && k < kClass ? f : 0u) << (16 * e);
+            }
+            h[q] = two;
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int hh = 0; hh < (VB < 4 ? 1 : 2); ++hh) {
+              const uint32_t sel = hh ? 0x7632 : 0x5410;
+              const uint32_t a = __byte_perm(v[c][0][w], v[c][1][w], sel);
+              const uint32_t d = __byte_perm(v[c][2][w], v[c][3][w], sel);
+              if constexpr (BITS == 4) {
+                mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, d & 0x000f000fu,
+                         d & 0x00f000f0u, h[0], h[1]);
+                const uint32_t e = a >> 8, f = d >> 8;
+                mma16816(acc[4 * w + 2 * hh + 1], e & 0x000f000fu, e & 0x00f000f0u,
+                         f & 0x000f000fu, f & 0x00f000f0u, h[0], h[1]);
+              } else {
+                mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
+                         d & 0x00ff00ffu, (d >> 8) & 0x00ff00ffu, h[0], h[1]);
+              }
+            }
         }
       }
+      // column 2t + c counts 2^(se - 127 + (2t + c) kClass + 24); upper nibbles 16 times as much
+      const bool one = sx - se < kClass;  // column 0 alone
 #pragma unroll
-      for (int k = 0; k < 8; ++k) out[k] = a[k];
+      for (int i = 0; i < MT; ++i) {
+        double x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = se - 103 + 2 * t * kClass - (BITS == 4 ? 4 * h : 0);
+          x[h] = widened(acc[i][2 * h], e);
+          if (!one) {
+            x[h] += widened(acc[i][2 * h + 1], e + kClass);
+            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 1);
+            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 2);
+          }
+        }
+        if (t == 0)
+          *reinterpret_cast<double2*>(out + gq * (D / 8) + 2 * i) =
+              make_double2(x[0] + mt, x[1] + mt);
+      }
+    } else {
+      for (int d = lane; d < D; d += 32) {
+        double a = 0.0;
+#pragma unroll 4
+        for (int r = 0; r < n; ++r) {
+          const uint32_t q = p.par[r0 + r].x;
+          const uint32_t w = p.k[(r0 + r) * RB + d * BITS / 8];
+          const uint32_t u = BITS == 4 ? (w >> (d % 2 * 4)) & 15u : w;
+          a += double(__uint_as_float(q << 16)) + double(__uint_as_float(q & 0xffff0000u)) * u;
+        }
+        out[d] = a;
+      }
     }
   }
 }
@@ -477,7 +632,7 @@ gattn_status launch_cache_sums(const CacheParams& p, const int32_t* since, doubl
   const int64_t warps = (since ? int64_t(p.g.S) * zs : int64_t(p.g.B)) * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
   by_layout(p, [&](auto bits, auto lpr) {
-    cache_sums_kernel<bits(), lpr()><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+    cache_sums_kernel<bits(), lpr() * 8><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
   });
   return launched("gattn_cache_sums");
 }
