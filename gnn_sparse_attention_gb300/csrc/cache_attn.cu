@@ -109,7 +109,14 @@ __device__ __forceinline__ float pow2_below(float x) {
   const int e = (__float_as_uint(x) >> 23) & 255;
   return __uint_as_float(uint32_t(254 - clampi(e, 30, 224)) << 23);
 }
-// n bytes to shared memory, zeros where `in` is false (nothing is read then)
+template <int N>
+__device__ __forceinline__ void copy(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// N bytes to shared memory, zeros where `in` is false (nothing is read then)
 template <int N>
 __device__ __forceinline__ void copy(uint32_t dst, const void* src, bool in) {
   if constexpr (N == 16)
@@ -294,6 +301,9 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     const int steps = min(s1, (keys + R - 1) / R);
     // position of row `i` of the item's rows; rows of a tile lie side by side
     const auto tile_pos = [&](int i) { return p.idx ? (ids[i >> lb] << lb) + (i & (g.block - 1)) : i; };
+    // where a lane's copies go: the exclusive-ors hang on the lane alone, but for rows of 128 bytes
+    const int kc = k_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
+    const int vc = R * RB + v_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
     const auto fetch = [&](int step, int to) {
       const uint32_t dst = my_ring + to * L::STAGE;
       if ((step + 1) * R <= keys && step < steps) {
@@ -303,13 +313,12 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         const uint8_t *v1 = vb + (k1 - kb);
 #pragma unroll
         for (int j = 0; j < L::CP; ++j) {
-          const int c = lane * 16, row = j * 512 / RB + c / RB, ch = c % RB / 16;
           const bool second = RB == 16 ? lane >= 16 : j >= L::CP / 2;
-          copy<16>(dst + k_byte<RB>(row, ch), (second ? k1 : k0) + j * 512, true);
-          copy<16>(dst + R * RB + v_byte<RB>(row, ch), (second ? v1 : v0) + j * 512, true);
+          copy<16>(dst + (kc ^ (RB == 128 ? (j & 1) * 64 : 0)) + j * 512, (second ? k1 : k0) + j * 512);
+          copy<16>(dst + vc + j * 512, (second ? v1 : v0) + j * 512);
         }
         if (lane < R)
-          copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane, true);
+          copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane);
       } else if (step < steps) {  // the last one: zeros behind the rows that the query sees
 #pragma unroll 1
         for (int j = 0; j < L::CP; ++j) {
