@@ -89,15 +89,14 @@ struct Lay {
 
 __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -429,10 +428,11 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       // scores relative to the running maximum, in log2
       float x[NT][2][NC], vs[NT][2], vm[NT][2];
       bool over = fresh;
+      float s4[NT][4];
+      uint32_t ka[NT][2][L::KW];
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t ka[2][L::KW];
+        s4[h][0] = s4[h][1] = s4[h][2] = s4[h][3] = 0.f;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -440,29 +440,34 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
             const uint8_t* a = st + (ko ^ (c * 64)) + (16 * h + 8 * q) * RB;
             if constexpr (L::KL == 4) {
               const uint4 w = *reinterpret_cast<const uint4*>(a);
-              ka[q][4 * c] = w.x; ka[q][4 * c + 1] = w.y;
-              ka[q][4 * c + 2] = w.z; ka[q][4 * c + 3] = w.w;
+              ka[h][q][4 * c] = w.x; ka[h][q][4 * c + 1] = w.y;
+              ka[h][q][4 * c + 2] = w.z; ka[h][q][4 * c + 3] = w.w;
             } else if constexpr (L::KL == 2) {
               const uint2 w = *reinterpret_cast<const uint2*>(a);
-              ka[q][0] = w.x; ka[q][1] = w.y;
+              ka[h][q][0] = w.x; ka[h][q][1] = w.y;
             } else {
-              ka[q][0] = *reinterpret_cast<const uint32_t*>(a);
+              ka[h][q][0] = *reinterpret_cast<const uint32_t*>(a);
             }
           }
+      }
 #pragma unroll
-        for (int w = 0; w < L::KW; ++w) {
-          const uint32_t a = ka[0][w], b = ka[1][w];
+      for (int w = 0; w < L::KW; ++w)
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          const uint32_t a = ka[h][0][w], b = ka[h][1][w];
           if constexpr (BITS == 4) {
-            mma16816(s4, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+            mma16816(s4[h], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
                      qf[4 * w], qf[4 * w + 1]);
             const uint32_t c = a >> 8, d = b >> 8;
-            mma16816(s4, c & 0x000f000fu, d & 0x000f000fu, c & 0x00f000f0u, d & 0x00f000f0u,
+            mma16816(s4[h], c & 0x000f000fu, d & 0x000f000fu, c & 0x00f000f0u, d & 0x00f000f0u,
                      qf[4 * w + 2], qf[4 * w + 3]);
           } else {
-            mma16816(s4, a & 0x00ff00ffu, b & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
+            mma16816(s4[h], a & 0x00ff00ffu, b & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
                      (b >> 8) & 0x00ff00ffu, qf[2 * w], qf[2 * w + 1]);
           }
         }
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint2 par = *reinterpret_cast<const uint2*>(st + po + (16 * h + 8 * q) * 8);
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           vs[h][q] = __uint_as_float(par.y & 0xffff0000u);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const float dot = kSplit ? s4[2 * q] + s4[2 * q + 1] : s4[2 * q + c];  // NC 1: c = 0
+            const float dot = kSplit ? s4[h][2 * q] + s4[h][2 * q + 1] : s4[h][2 * q + c];
             x[h][q][c] = fmaf(dot * qmul[c], sk, fmaf(mk, qsum[c], -ref[c]));
           }
         }
