@@ -34,8 +34,11 @@
 // equal stretches, one for each CTA that the GPU holds at a time, whatever the
 // lengths of the sequences are: CTAs read them and find their stretch themselves.
 // Items that lie within a stretch are finished there; of one that is cut, each CTA
-// leaves its part in the workspace and a second kernel joins them.  With many more
-// items than CTAs each item is a CTA of its own.
+// leaves its part in the workspace and a second kernel joins them.  While a CTA is at
+// one item, a warp of it finds the next, whose first steps are fetched before the
+// sums of the old one are joined.  With many more items than CTAs each item is a CTA of
+// its own, and few short ones are a cluster's each, joined through its shared memory.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -47,11 +50,14 @@ namespace gattn {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kWarps = 4;
 constexpr int kThr = kWarps * 32;
 constexpr int kCtas = 4;        // per SM
 constexpr int kStages = 3;
 constexpr int kMinSteps = 4;    // of a stretch: one for each warp
+constexpr int kMaxCluster = 8;
 constexpr float kNone = -1e30f; // running maximum of no score
 constexpr float kOver = 4.f;    // a score (log2) may exceed the running maximum by this
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
@@ -67,7 +73,8 @@ struct AttnParams {
   float* part;   // [CTAs][2][heads][D + 4]: a stretch's first item if begun before, its last if cut
   int2* info;    // [items]: first CTA and CTAs of an item that is cut, (0, 0) for others
   int groups;    // column groups of a key head
-  int ctas;      // stretches (0: a CTA for each item)
+  int ctas;      // stretches (0: a cluster for each item)
+  int cluster;   // CTAs of that
   int max_keys;
 };
 
@@ -157,29 +164,42 @@ __device__ __forceinline__ void store4(__nv_bfloat16* to, float4 x) {
                                              *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// What the CTA works on: steps [s0, s1) of an item's `steps`
-struct Item {
-  int row, s;     // query row, sequence
-  int beg, limit; // first row of the cache, rows that the query may see
-  int len;
-  int steps;      // at least 1
+// A query row: where its sequence's rows lie in the cache, how many of them it
+// may see, and the steps that takes (at least one; none for rows of no sequence).
+struct Row {
+  int beg, len, limit, steps;
 };
 template <int R>
-__device__ __forceinline__ Item item_at(const AttnParams& p, int u) {
+__device__ __forceinline__ Row row_at(const AttnParams& p, int u) {
   const BlockGeom& g = p.c.g;
-  const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, u);
-  Item it{};
-  it.row = u;
-  it.s = x.s;
-  if (x.s < 0) return it;
-  const Span sp = span_k(g, x.s);
-  it.beg = sp.beg;
-  it.len = sp.len;
-  it.limit = min(g.causal ? clampi(x.i + sp.len - x.n + 1, 0, sp.len) : sp.len, p.max_keys);
-  const int keys = p.idx ? min(it.limit, g.topk * g.block) : it.limit;
-  it.steps = max((keys + R - 1) / R, 1);
-  return it;
+  // with one row a sequence, as in serving, row u is sequence u: looked at first, since a search
+  // is a chain of loads
+  int s = min(u, g.S - 1);
+  const int b = clampi(g.seq_q[s], 0, g.Nq), e = clampi(g.seq_q[s + 1], b, g.Nq);
+  Span sp = span_k(g, s);
+  int i = u - b, n = e - b;
+  Row r{};
+  if (u < b || u >= e) {
+    const SeqRow x = seq_row(g.seq_q, g.S, g.Nq, u);
+    if (x.s < 0) return r;
+    sp = span_k(g, x.s);
+    i = x.i;
+    n = x.n;
+  }
+  r.beg = sp.beg;
+  r.len = sp.len;
+  r.limit = min(g.causal ? clampi(i + sp.len - n + 1, 0, sp.len) : sp.len, p.max_keys);
+  const int keys = p.idx ? min(r.limit, g.topk * g.block) : r.limit;
+  r.steps = max((keys + R - 1) / R, 1);
+  return r;
 }
+
+// What a CTA works on: steps [s0, s1) of the `steps` of an item (row u, hi: key head and column
+// group).  `keys` rows are seen, listed in ids or all; none left: steps = 0.
+struct Seg {
+  int u, hi, s0, s1, steps, keys, beg;
+  int ids[kBlkMaxTopk];
+};
 
 // NC heads to a lane's two columns of a product.  With two, a group is 8 heads.  With one it is 4:
 // in fp32 the head's two parts, in bf16 the second column is empty, which spares a group of up to
@@ -193,27 +213,25 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   static_assert(NC == 1 || !kSplit, "");
   static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
-  __shared__ int ids[kBlkMaxTopk];
-  __shared__ int n_keys;
+  __shared__ Seg segs[2];                           // this one and the next
   __shared__ float sref[kWarps][HC], sl[kWarps][HC], sw[kWarps][HC];
+  __shared__ int so_at[kWarps];
   __shared__ int64_t scan[kWarps];
-  __shared__ int64_t start_at;
-  __shared__ int start_u;
+  __shared__ int64_t cur_at, cur_end;  // the stretch, relative to row cur_u's first step
+  __shared__ int cur_u;
   const BlockGeom& g = p.c.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
   const int heads_of = g.Hkv * p.groups;  // items of a query row
+  const int rank = p.ctas ? 0 : blockIdx.x % p.cluster;
+  const int wide = kWarps * (p.ctas ? 1 : p.cluster);  // warps that share an item's steps
 
   // where the stretch begins and ends, on the line of all items' steps
-  int64_t at = 0, end = 0, per = 0;
-  int u, first = 0;  // query row, item of it
+  int64_t per = 0;
   cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched; it waits for this grid
-  if (p.ctas == 0) {
-    u = blockIdx.x / heads_of;
-    first = blockIdx.x % heads_of;
-  } else {
+  if (p.ctas) {
     const int k = (g.U + kThr - 1) / kThr, u0 = threadIdx.x * k, u1 = min(u0 + k, g.U);
     int64_t mine = 0;
-    for (int i = u0; i < u1; ++i) mine += item_at<R>(p, i).steps;
+    for (int i = u0; i < u1; ++i) mine += row_at<R>(p, i).steps;
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -232,119 +250,155 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     before *= heads_of;
     mine *= heads_of;
     per = max((total + p.ctas - 1) / p.ctas, int64_t(kMinSteps));
-    at = per * blockIdx.x;
-    end = min(at + per, total);
+    const int64_t at = per * blockIdx.x, end = min(at + per, total);
     if (at >= end) return;
     if (at >= before && at < before + mine) {  // one thread
       int i = u0;
-      for (;; ++i) {
-        const int64_t n = int64_t(item_at<R>(p, i).steps) * heads_of;
+      for (; k > 1; ++i) {
+        const int64_t n = int64_t(row_at<R>(p, i).steps) * heads_of;
         if (at < before + n) break;
         before += n;
       }
-      start_u = i;
-      start_at = before;
+      cur_u = i;
+      cur_at = at - before;
+      cur_end = end - before;
     }
     __syncthreads();
-    u = start_u;
-    at -= start_at;  // from here on relative to the row's first step
-    end -= start_at;
   }
 
-  const uint32_t my_ring = uint32_t(__cvta_generic_to_shared(ring)) + warp * L::RING;
-  const uint8_t* my_stage = ring + warp * L::RING;
-
-  for (;;) {
-    const Item it = item_at<R>(p, u);
-    if (it.s < 0) {  // rows of no sequence
-      if (p.ctas == 0) return;
-      ++u;
-      continue;
-    }
-    int hi, s0, s1;
-    if (p.ctas == 0) {
-      hi = first;
-      s0 = 0;
-      s1 = it.steps;
-    } else {
-      const int64_t row_steps = int64_t(it.steps) * heads_of;
-      if (at >= row_steps) {
+  // The next stretch of an item, by the first warp.
+  const auto next = [&](Seg& to, bool first) {
+    int u, hi = 0, s0 = 0, s1 = 0;
+    Row r{};
+    if (p.ctas) {
+      int64_t at = cur_at, end = cur_end;
+      u = cur_u;
+      while (at < end) {
+        r = row_at<R>(p, u);
+        const int64_t row_steps = int64_t(r.steps) * heads_of;
+        if (at < row_steps) break;
         at -= row_steps;
         end -= row_steps;
         ++u;
-        continue;
       }
-      hi = int(at / it.steps);
-      s0 = int(at - int64_t(hi) * it.steps);
-      s1 = int(min(int64_t(it.steps), s0 + (end - at)));
+      if (at < end) {
+        hi = int(at / r.steps);
+        s0 = int(at - int64_t(hi) * r.steps);
+        s1 = int(min(int64_t(r.steps), s0 + (end - at)));
+      } else {
+        r.steps = 0;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        cur_u = u;
+        cur_at = at + (s1 - s0);
+        cur_end = end;
+      }
+    } else {
+      const int item = blockIdx.x / p.cluster;
+      u = item / heads_of;
+      hi = item % heads_of;
+      if (first) r = row_at<R>(p, u);
+      s1 = r.steps;
     }
-    const int cgrp = hi % p.groups, kh = hi / p.groups;
-    const int head0 = kh * g.G + cgrp * HC, heads = min(HC, g.G - cgrp * HC);
-    const int64_t row0 = int64_t(kh) * g.Nk + it.beg;
-    const uint8_t* kb = p.c.k + row0 * RB;
-    const uint8_t* vb = p.c.v + row0 * RB;
-    const uint2* pb = p.c.par + row0;
+    int keys = r.limit;
+    if (p.idx && r.steps) {
+      const int nb = (r.len + g.block - 1) / g.block;
+      const int n = block_list(
+          p.idx + int64_t(u) * g.is_u + int64_t(hi / p.groups) * g.is_h, g.topk, nb, to.ids);
+      keys = list_keys(to.ids, n, g.block, r.limit);
+    }
+    if (lane == 0) {
+      to.u = u;
+      to.hi = hi;
+      to.s0 = s0;
+      to.s1 = s1;
+      to.steps = r.steps;
+      to.keys = keys;
+      to.beg = r.beg;
+    }
+    __syncwarp();
+  };
 
-    int keys = it.limit;
-    if (p.idx) {
-      if (warp == 0) {
-        const int nb = (it.len + g.block - 1) / g.block;
-        const int n =
-            block_list(p.idx + int64_t(u) * g.is_u + int64_t(kh) * g.is_h, g.topk, nb, ids);
-        if (lane == 0) n_keys = list_keys(ids, n, g.block, it.limit);
-      }
-      __syncthreads();
-      keys = n_keys;
-    }
-    const int lb = 31 - __clz(g.block);
-    const int steps = min(s1, (keys + R - 1) / R);
-    // position of row `i` of the item's rows; rows of a tile lie side by side
-    const auto tile_pos = [&](int i) { return p.idx ? (ids[i >> lb] << lb) + (i & (g.block - 1)) : i; };
-    // where a lane's copies go: the exclusive-ors hang on the lane alone, but for rows of 128 bytes
-    const int kc = k_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
-    const int vc = R * RB + v_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
-    const auto fetch = [&](int step, int to) {
-      const uint32_t dst = my_ring + to * L::STAGE;
-      if ((step + 1) * R <= keys && step < steps) {
-        const int pos0 = tile_pos(step * R), pos1 = NT == 1 ? 0 : tile_pos(step * R + 16) - 16;
-        const uint8_t *k0 = kb + int64_t(pos0) * RB + lane * 16, *v0 = vb + (k0 - kb);
-        const uint8_t *k1 = NT == 1 ? k0 : kb + int64_t(pos1) * RB + lane * 16;
-        const uint8_t *v1 = vb + (k1 - kb);
+  const uint32_t my_ring = uint32_t(__cvta_generic_to_shared(ring)) + warp * L::RING;
+  const uint8_t* my_stage = ring + warp * L::RING;
+  const int lb = 31 - __clz(g.block);
+  // where a lane's copies go: the exclusive-ors hang on the lane alone, but for rows of 128 bytes
+  const int kc = k_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
+  const int vc = R * RB + v_byte<RB>(lane * 16 / RB, lane * 16 % RB / 16);
+  // what a lane reads of a stage
+  const int ko = k_byte<RB>(tile_row(gq), t * L::KL * 4 / 16) + t * L::KL * 4 % 16;
+  const int vo = R * RB + v_byte<RB>(t, gq * L::VB / 16) + gq * L::VB % 16;
+  const int po = 2 * R * RB + tile_row(gq) * 8;
+
+  const Seg* seg = segs;
+  const uint8_t *kb, *vb;  // the item's rows
+  const uint2* pb;
+  int keys, steps;
+  const auto open = [&]() {
+    const int64_t row0 = int64_t(seg->hi / p.groups) * g.Nk + seg->beg;
+    kb = p.c.k + row0 * RB;
+    vb = p.c.v + row0 * RB;
+    pb = p.c.par + row0;
+    keys = seg->keys;
+    steps = min(seg->s1, (keys + R - 1) / R);
+  };
+  // position of row `i` of the item's rows; rows of a tile lie side by side
+  const auto tile_pos = [&](int i) {
+    return p.idx ? (seg->ids[i >> lb] << lb) + (i & (g.block - 1)) : i;
+  };
+  const auto fetch = [&](int step, int to) {
+    const uint32_t dst = my_ring + to * L::STAGE;
+    if ((step + 1) * R <= keys && step < steps) {
+      const int pos0 = tile_pos(step * R), pos1 = NT == 1 ? 0 : tile_pos(step * R + 16) - 16;
+      const uint8_t *k0 = kb + int64_t(pos0) * RB + lane * 16, *v0 = vb + (k0 - kb);
+      const uint8_t *k1 = NT == 1 ? k0 : kb + int64_t(pos1) * RB + lane * 16;
+      const uint8_t *v1 = vb + (k1 - kb);
 #pragma unroll
-        for (int j = 0; j < L::CP; ++j) {
-          const bool second = RB == 16 ? lane >= 16 : j >= L::CP / 2;
-          copy<16>(dst + (kc ^ (RB == 128 ? (j & 1) * 64 : 0)) + j * 512, (second ? k1 : k0) + j * 512);
-          copy<16>(dst + vc + j * 512, (second ? v1 : v0) + j * 512);
-        }
-        if (lane < R)
-          copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane);
-      } else if (step < steps) {  // the last one: zeros behind the rows that the query sees
+      for (int j = 0; j < L::CP; ++j) {
+        const bool second = RB == 16 ? lane >= 16 : j >= L::CP / 2;
+        copy<16>(dst + (kc ^ (RB == 128 ? (j & 1) * 64 : 0)) + j * 512, (second ? k1 : k0) + j * 512);
+        copy<16>(dst + vc + j * 512, (second ? v1 : v0) + j * 512);
+      }
+      if (lane < R) copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane);
+    } else if (step < steps) {  // the last one: zeros behind the rows that the query sees
 #pragma unroll 1
-        for (int j = 0; j < L::CP; ++j) {
-          const int c = j * 512 + lane * 16, row = c / RB, ch = c % RB / 16;
-          const int i = step * R + row;
-          const bool in = i < keys;
-          const int64_t from = in ? int64_t(tile_pos(i)) * RB + ch * 16 : 0;
-          copy<16>(dst + k_byte<RB>(row, ch), kb + from, in);
-          copy<16>(dst + R * RB + v_byte<RB>(row, ch), vb + from, in);
-        }
-        if (lane < R) {
-          const int i = step * R + lane;
-          copy<8>(dst + 2 * R * RB + lane * 8, pb + (i < keys ? tile_pos(i) : 0), i < keys);
-        }
+      for (int j = 0; j < L::CP; ++j) {
+        const int c = j * 512 + lane * 16, row = c / RB, ch = c % RB / 16;
+        const int i = step * R + row;
+        const bool in = i < keys;
+        const int64_t from = in ? int64_t(tile_pos(i)) * RB + ch * 16 : 0;
+        copy<16>(dst + k_byte<RB>(row, ch), kb + from, in);
+        copy<16>(dst + R * RB + v_byte<RB>(row, ch), vb + from, in);
       }
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(s0 + warp + i * kWarps, i);
+      if (lane < R) {
+        const int i = step * R + lane;
+        copy<8>(dst + 2 * R * RB + lane * 8, pb + (i < keys ? tile_pos(i) : 0), i < keys);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  const auto follow = [&](int stage) { return stage + 1 == kStages ? 0 : stage + 1; };
 
+  if (warp == 0) next(segs[0], true);
+  __syncthreads();
+  if (segs[0].steps == 0) return;  // a row of no sequence
+  open();
+  int stage = 0;
+  fetch(seg->s0 + rank * kWarps + warp, 0);
+  fetch(seg->s0 + rank * kWarps + warp + wide, 1);
+
+  for (;;) {
+    if (warp == 0) next(segs[seg == segs], false);
+    const int kh = seg->hi / p.groups, cgrp = seg->hi % p.groups;
+    const int head0 = kh * g.G + cgrp * HC, heads = min(HC, g.G - cgrp * HC);
     // q of this lane's column, scaled to fp16's range, in the order of the words of a K row
     uint32_t qf[L::QR];
     float qmul[2], qsum[2];  // of the lane's columns of a product: 2t, 2t + 1
     {
       const int hc = NC == 1 ? gq >> 1 : gq;
       const bool on = hc < heads && (NC == 2 || kSplit || !(gq & 1));
-      const T* q = static_cast<const T*>(p.Q) + (int64_t(it.row) * g.H + head0 + (on ? hc : 0)) * D;
+      const T* q = static_cast<const T*>(p.Q) + (int64_t(seg->u) * g.H + head0 + (on ? hc : 0)) * D;
       constexpr int PW = 32 / BITS;           // elements of a word
       constexpr int RUN = L::KL * PW;         // neighbouring elements of a lane
       constexpr int VE = 16 / int(sizeof(T));
@@ -412,19 +466,14 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       sum[c] = msum[c] = 0.f;
       vf[c] = 1.f;
     }
-    // what this lane reads of a stage
-    const int ko = k_byte<RB>(tile_row(gq), t * L::KL * 4 / 16) + t * L::KL * 4 % 16;
-    const int vo = R * RB + v_byte<RB>(t, gq * L::VB / 16) + gq * L::VB % 16;
-    const int po = 2 * R * RB + tile_row(gq) * 8;
 
-    int stage = 0;
     bool fresh = true;  // no step so far; each has a row that is seen
-    for (int step = s0 + warp; step < steps; step += kWarps) {
+    for (int step = seg->s0 + rank * kWarps + warp; step < steps; step += wide) {
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // all lanes' copies are here, and the stage to be filled has been read
-      fetch(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+      fetch(step + 2 * wide, stage == 0 ? kStages - 1 : stage - 1);
       const uint8_t* st = my_stage + stage * L::STAGE;
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = follow(stage);
       // scores relative to the running maximum, in log2
       float x[NT][2][NC], vs[NT][2], vm[NT][2];
       bool over = fresh;
@@ -594,10 +643,12 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       }
     }
 
-    // the warp's sums, in place of its ring
-    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    // The warp's sums, in the stage that the next item's first steps leave free.  No copy is under
+    // way: there were none beyond the last step.
     __syncwarp();
-    float* so = reinterpret_cast<float*>(ring + warp * L::RING);  // [HC][D]
+    const int free_at = warp * L::RING + follow(follow(stage)) * L::STAGE;
+    float* so = reinterpret_cast<float*>(ring + free_at);  // [HC][D]
+    if (lane == 0) so_at[warp] = free_at;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
@@ -621,8 +672,19 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       }
     }
     __syncthreads();
+    const Seg* const done = seg;
+    const bool more = segs[seg == segs].steps != 0;
+    if (more) {
+      seg = segs + (seg == segs);
+      open();
+      fetch(seg->s0 + warp, stage);
+      fetch(seg->s0 + warp + kWarps, follow(stage));
+    }
     // the CTA's: finished, or its part of the item
-    const bool cut = s0 > 0 || s1 < it.steps;
+    const bool cut = done->s1 - done->s0 < done->steps;
+    const bool shared = p.ctas == 0 && p.cluster > 1;
+    const int64_t out0 = int64_t(done->u) * g.H + head0;
+    float* part = p.part + (int64_t(blockIdx.x) * 2 + (done->s0 == 0)) * HC * (D + 4);
     if (threadIdx.x < HC) {
       const int h = threadIdx.x;
       float top = sref[0][h], l = 0.f;
@@ -636,18 +698,16 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       }
       // what a finished element is multiplied by, and the statistics
       const bool some = l > 0.f || l != l;
-      if (cut) {
-        if (h < heads) {
-          float* w = p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 4);
-          w[D] = top;
-          w[D + 1] = l;
-        }
+      if (shared) {
+        sref[0][h] = top;
+        sl[0][h] = l;
+      } else if (cut) {
+        if (h < heads) *reinterpret_cast<float2*>(part + h * (D + 4) + D) = make_float2(top, l);
       } else {
         const float r = some ? 1.f / l : 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) sw[w][h] *= r;
-        if (h < heads)
-          p.lse[int64_t(it.row) * g.H + head0 + h] = some ? (top + lg2(l)) * kLn2 : neg_inf();
+        if (h < heads) p.lse[out0 + h] = some ? (top + lg2(l)) * kLn2 : neg_inf();
       }
     }
     __syncthreads();
@@ -656,26 +716,50 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(ring + w * L::RING + e * 4);
+        const float4 x = *reinterpret_cast<const float4*>(ring + so_at[w] + e * 4);
         const float f = sw[w][h];
         o.x = fmaf(x.x, f, o.x);
         o.y = fmaf(x.y, f, o.y);
         o.z = fmaf(x.z, f, o.z);
         o.w = fmaf(x.w, f, o.w);
       }
-      if (cut)
-        *reinterpret_cast<float4*>(
-            p.part + ((int64_t(blockIdx.x) * 2 + (s0 == 0)) * HC + h) * (D + 4) + d) = o;
-      else
-        store4(static_cast<T*>(p.out) + (int64_t(it.row) * g.H + head0 + h) * D + d, o);
+      if (shared) *reinterpret_cast<float4*>(ring + so_at[0] + e * 4) = o;  // read by this thread alone
+      else if (cut) *reinterpret_cast<float4*>(part + h * (D + 4) + d) = o;
+      else store4(static_cast<T*>(p.out) + (out0 + h) * D + d, o);
     }
-    if (p.ctas == 0) return;
-    if (threadIdx.x == 0 && s0 == 0)
-      p.info[int64_t(u) * heads_of + hi] =
-          cut ? make_int2(blockIdx.x, 1 + int((it.steps - s1 + per - 1) / per)) : make_int2(0, 0);
-    at += s1 - s0;
-    if (at >= end) return;
-    __syncthreads();  // ids, statistics and rings have been read
+    if (shared) {  // the cluster's: each CTA a part of the elements
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      for (int e = (rank * kThr + threadIdx.x) * 4; e < heads * D; e += p.cluster * kThr * 4) {
+        const int h = e / D, d = e % D;
+        float top = kNone, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < p.cluster; ++r)
+          top = fmaxf(top, *cluster.map_shared_rank(&sref[0][h], r));
+        for (int r = 0; r < p.cluster; ++r) {
+          const float f = ex2(*cluster.map_shared_rank(&sref[0][h], r) - top);
+          const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(
+              ring + *cluster.map_shared_rank(&so_at[0], r) + e * 4, r));
+          o.x = fmaf(x.x, f, o.x);
+          o.y = fmaf(x.y, f, o.y);
+          o.z = fmaf(x.z, f, o.z);
+          o.w = fmaf(x.w, f, o.w);
+          l = fmaf(*cluster.map_shared_rank(&sl[0][h], r), f, l);
+        }
+        const bool some = l > 0.f || l != l;
+        const float r = some ? 1.f / l : 0.f;
+        store4(static_cast<T*>(p.out) + (out0 + h) * D + d,
+               make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+        if (d == 0) p.lse[out0 + h] = some ? (top + lg2(l)) * kLn2 : neg_inf();
+      }
+      cluster.sync();  // nobody leaves while its sums are read
+    }
+    if (p.ctas && threadIdx.x == 0 && done->s0 == 0)
+      p.info[int64_t(done->u) * heads_of + done->hi] =
+          cut ? make_int2(blockIdx.x, 1 + int((done->steps - done->s1 + per - 1) / per))
+              : make_int2(0, 0);
+    if (!more) return;
+    __syncthreads();  // statistics, sums and the old item have been read
   }
 }
 
@@ -741,8 +825,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int
 struct Shape {
   int hc, groups;
   int64_t items;
-  int ctas;      // 0: one for each item
-  size_t bytes;  // of the workspace: parts, then the items' table
+  int ctas, cluster;  // see AttnParams
+  size_t bytes;       // of the workspace: parts, then the items' table
 };
 Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   const BlockGeom& g = p.g;
@@ -750,12 +834,20 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   s.hc = dt == GATTN_F32 || g.G <= 4 ? 4 : 8;
   s.groups = (g.G + s.hc - 1) / s.hc;
   s.items = int64_t(g.U) * g.Hkv * s.groups;
+  s.cluster = 1;
   const int64_t keys = lists ? std::min<int64_t>(int64_t(g.topk) * g.block, max_keys) : max_keys;
   const int rows = g.D * p.bits / 8 > 64 ? 16 : 32;
   const int64_t steps = std::max<int64_t>((keys + rows - 1) / rows, 1);
   const int64_t slots = int64_t(sm_count()) * kCtas;
-  // Items of their own: nothing to cut, or so many that the last ones to run weigh little
-  if (steps <= kMinSteps || s.items >= 8 * slots) return s;
+  // So many items that the last ones to run weigh little: a CTA for each.
+  if (s.items >= 8 * slots) return s;
+  // Few short ones: a cluster for each, up to four steps to a warp, joined in shared memory.
+  int c = 1;
+  while (c < kMaxCluster && c * kWarps < steps && s.items * c * 2 <= slots) c *= 2;
+  if (steps <= c * kWarps * 4) {
+    s.cluster = c;
+    return s;
+  }
   s.ctas = int(std::min(slots, (s.items * steps + kMinSteps - 1) / kMinSteps));
   s.bytes = size_t(s.ctas) * 2 * s.hc * (g.D + 4) * 4 + size_t(s.items) * 8;
   return s;
@@ -775,19 +867,26 @@ cudaError_t launch(const AttnParams& p, const Shape& s, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  kernel<<<unsigned(s.ctas ? s.ctas : s.items), kThr, smem, st>>>(p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(s.ctas ? s.ctas : s.items * s.cluster));
+  cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = unsigned(s.cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = s.cluster > 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess || s.ctas == 0) return e;
   // the join's launch overlaps the kernel's end; few items are spread over more blocks each
-  cudaLaunchConfig_t cfg{};
   const int64_t wide = std::max<int64_t>(int64_t(sm_count()) * 4 / s.items, 1);
   cfg.gridDim = dim3(unsigned(s.items), unsigned(std::min<int64_t>(wide, s.hc * D / 32)));
   cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
+  cfg.dynamicSmemBytes = 0;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, p, s.hc);
 }
@@ -826,8 +925,9 @@ gattn_status launch_cache_fwd(const CacheParams& c, gattn_dtype dt, int max_keys
   p.info = reinterpret_cast<int2*>(p.part + int64_t(s.ctas) * 2 * s.hc * (c.g.D + 4));
   p.groups = s.groups;
   p.ctas = s.ctas;
+  p.cluster = s.cluster;
   p.max_keys = max_keys;
-  if (s.items > INT32_MAX) {
+  if (s.items * s.cluster > INT32_MAX) {
     set_error("gattn_cache_fwd: too many rows and heads");
     return GATTN_ERR_UNSUPPORTED;
   }
