@@ -59,10 +59,10 @@ constexpr int kStages = 3;
 constexpr int kMinSteps = 4;    // of a stretch: one for each warp
 constexpr int kMaxCluster = 8;
 constexpr float kNone = -1e30f; // running maximum of no score
-constexpr float kOver = 4.f;    // a score (log2) may exceed the running maximum by this
+constexpr float kOver = 64.f;   // weights relative to the running maximum: of a step's rows together
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
 // 2^-19 of it keeps its 11 bits; set again where a step could leave fp16's range.
-constexpr float kYTop = 32.f, kYMax = 65504.f / 16.f;
+constexpr float kYTop = 32.f, kYMax = 65504.f;
 
 struct AttnParams {
   CacheParams c;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     const int head0 = kh * g.G + cgrp * HC, heads = min(HC, g.G - cgrp * HC);
     // q of this lane's column, scaled to fp16's range, in the order of the words of a K row
     uint32_t qf[L::QR];
-    float qmul[2], qsum[2];  // of the lane's columns of a product: 2t, 2t + 1
+    float qmul[NC], qsum[NC];  // of the lane's heads
     {
       const int hc = NC == 1 ? gq >> 1 : gq;
       const bool on = hc < heads && (NC == 2 || kSplit || !(gq & 1));
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       constexpr int PW = 32 / BITS;           // elements of a word
       constexpr int RUN = L::KL * PW;         // neighbouring elements of a lane
       constexpr int VE = 16 / int(sizeof(T));
-      float f[L::KW * PW];
+      float f[L::KW * PW], top = 0.f;
 #pragma unroll
       for (int c = 0; c < L::KW / L::KL; ++c)
 #pragma unroll
@@ -410,20 +410,14 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           const uint4 x = *reinterpret_cast<const uint4*>(q + c * (64 * 8 / BITS) + t * RUN + i);
           const T* e = reinterpret_cast<const T*>(&x);
 #pragma unroll
-          for (int z = 0; z < VE; ++z) f[c * RUN + i + z] = on ? to_f32(e[z]) : 0.f;
+          for (int z = 0; z < VE; ++z) f[c * RUN + i + z] = to_f32(e[z]);
         }
-      float top = 0.f, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < L::KW * PW; ++i) {
-        top = fmaxf(top, fabsf(f[i]));
-        sum += f[i];
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      }
-      const float up = pow2_below(top) * 8192.f;  // largest element to [2^13, 2^14)
+      for (int i = 0; i < L::KW * PW; ++i) top = fmaxf(top, fabsf(f[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float scale = pow2_below(top) * 8192.f;  // largest element to [2^13, 2^14)
+      const float up = on ? scale : 0.f, up16 = up * 0.0625f;
 #pragma unroll
       for (int w = 0; w < L::KW; ++w)
 #pragma unroll
@@ -432,26 +426,33 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           // 8 bits: (0, 2) and (1, 3).  Upper nibbles count 16 times.
           float x[4];
           if constexpr (BITS == 4) {
-            x[0] = f[w * PW + i / 2]; x[1] = f[w * PW + 4 + i / 2];
-            x[2] = f[w * PW + i / 2 + 1] * 0.0625f; x[3] = f[w * PW + 4 + i / 2 + 1] * 0.0625f;
+            x[0] = f[w * PW + i / 2] * up; x[1] = f[w * PW + 4 + i / 2] * up;
+            x[2] = f[w * PW + i / 2 + 1] * up16; x[3] = f[w * PW + 4 + i / 2 + 1] * up16;
           } else {
-            x[0] = f[w * PW]; x[1] = f[w * PW + 2]; x[2] = f[w * PW + 1]; x[3] = f[w * PW + 3];
+            x[0] = f[w * PW] * up; x[1] = f[w * PW + 2] * up;
+            x[2] = f[w * PW + 1] * up; x[3] = f[w * PW + 3] * up;
           }
+          if (kSplit && (gq & 1)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] *= up;
-            if (kSplit && (gq & 1)) x[e] -= __half2float(__float2half_rn(x[e]));
+            for (int e = 0; e < 4; ++e) x[e] -= __half2float(__float2half_rn(x[e]));
           }
           const int r = (w * PW + i) / 2;
           qf[r] = half2_bits(x[0], x[1]);
           qf[r + 1] = half2_bits(x[2], x[3]);
         }
-      // columns 2t, 2t + 1 of a product belong to the lanes with gq = 2t, 2t + 1
-      const float mul = g.qmul * 16777216.f / up, qs = sum * g.qmul;
+      // columns 2t, 2t + 1 of a product belong to the lanes with gq = 2t, 2t + 1; the sum of q is
+      // its product with levels of 1
+      const float mul = g.qmul * 16777216.f / scale;
+      float one[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int r = 0; r < L::QR; r += 2) {
+        constexpr uint32_t kUp = BITS == 4 ? 0x00100010u : 0x00010001u;
+        mma16816(one, 0x00010001u, 0x00010001u, kUp, kUp, qf[r], qf[r + 1]);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
         qmul[c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
-        qsum[c] = __shfl_sync(0xffffffffu, qs, (2 * t + c) * 4);
+        qsum[c] = (kSplit ? one[0] + one[1] : one[c]) * qmul[c];
       }
     }
 
@@ -459,7 +460,6 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
 #pragma unroll
     for (int i = 0; i < L::MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     float ref[NC], sum[NC], msum[NC], vf[NC];
-    float top_s = 0.f;  // a step of V beyond this sets the factors again
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       ref[c] = 0.f;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       stage = follow(stage);
       // scores relative to the running maximum, in log2
       float x[NT][2][NC], vs[NT][2], vm[NT][2];
-      bool over = fresh;
+      bool over;
       float s4[NT][4];
       uint32_t ka[NT][2][L::KW];
 #pragma unroll
@@ -540,17 +540,32 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
               for (int c = 0; c < NC; ++c) x[h][q][c] = neg_inf();
             }
       }
+      // Weights and p s.  A score beyond kOver shows in the step's sum of weights, a p s beyond fp16 in
+      // theirs.
+      float e[NT][2][NC], y[NT][2][NC];
+      float step_sum[NC];
+      const auto weigh = [&]() {
+        bool far = false;
 #pragma unroll
-      for (int h = 0; h < NT; ++h)
+        for (int c = 0; c < NC; ++c) {
+          float es = 0.f, ys = 0.f;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          over = over || vs[h][q] > top_s;
+          for (int h = 0; h < NT; ++h)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) over = over || x[h][q][c] > kOver;
+            for (int q = 0; q < 2; ++q) {
+              e[h][q][c] = ex2(x[h][q][c]);
+              y[h][q][c] = e[h][q][c] * (vs[h][q] * vf[c]);
+              es += e[h][q][c];
+              ys += y[h][q][c];
+            }
+          far = far || es > kOver || ys > kYMax;
+          step_sum[c] = es;
         }
+        return far;
+      };
+      over = weigh() || fresh;
       if (__any_sync(0xffffffffu, over)) {
         // references to the maxima, and the factors of p s with them
-        top_s = __int_as_float(0x7f800000);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           float top = fresh ? neg_inf() : 0.f;
@@ -576,7 +591,6 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           sum[c] *= down;
           msum[c] *= down;
           vf[c] = f;
-          top_s = fminf(top_s, kYMax / f);
 #pragma unroll
           for (int i = 0; i < L::MT; ++i)
 #pragma unroll
@@ -584,26 +598,23 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
               if (NC == 1 || (e & 1) == c) acc[i][e] *= mul;
         }
         fresh = false;
+        weigh();
       }
 #pragma unroll
+      for (int c = 0; c < NC; ++c) sum[c] += step_sum[c];
+#pragma unroll
       for (int h = 0; h < NT; ++h) {
-        float y[2][NC];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float e = ex2(x[h][q][c]);
-            sum[c] += e;
-            msum[c] = fmaf(e, vm[h][q], msum[c]);
-            y[q][c] = e * (vs[h][q] * vf[c]);
-          }
+          for (int c = 0; c < NC; ++c) msum[c] = fmaf(e[h][q][c], vm[h][q], msum[c]);
         uint32_t b0, b1;
         if constexpr (kSplit) {
-          b0 = transposed(half2_bits(y[0][0], y[0][0] - __half2float(__float2half_rn(y[0][0]))));
-          b1 = transposed(half2_bits(y[1][0], y[1][0] - __half2float(__float2half_rn(y[1][0]))));
+          b0 = transposed(half2_bits(y[h][0][0], y[h][0][0] - __half2float(__float2half_rn(y[h][0][0]))));
+          b1 = transposed(half2_bits(y[h][1][0], y[h][1][0] - __half2float(__float2half_rn(y[h][1][0]))));
         } else {
-          b0 = transposed(half2_bits(y[0][0], NC == 2 ? y[0][NC - 1] : 0.f));
-          b1 = transposed(half2_bits(y[1][0], NC == 2 ? y[1][NC - 1] : 0.f));
+          b0 = transposed(half2_bits(y[h][0][0], NC == 2 ? y[h][0][NC - 1] : 0.f));
+          b1 = transposed(half2_bits(y[h][1][0], NC == 2 ? y[h][1][NC - 1] : 0.f));
         }
         uint32_t va[4][L::VW];
 #pragma unroll
