@@ -957,14 +957,42 @@ assert _ROTARY_PACK.size == ctypes.sizeof(_RotaryDesc)
 assert _CACHE_PACK.size == ctypes.sizeof(_CacheDesc)
 ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+_CODES = {torch.float32: GATTN_F32, torch.bfloat16: GATTN_BF16}
+_INT32, _empty, _empty_like = torch.int32, torch.empty, torch.empty_like
+_device = torch._C._cuda_getDevice              # of tensors that are on a GPU already
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _offsets(name, t, n, dev):
+    """_want for the int32 vectors of a call, without a call's way to its message."""
+    if (t.get_device() != dev or t.dtype is not _INT32 or t.numel() != n or t.dim() != 1
+            or not t.is_contiguous()):
+        _want(name, t, (n,), _INT32, dev)
+
+
+def _seq_args(seq_q, seq_k, len_k, dev):
+    """Checked offsets and lengths (each but one may be None): S."""
+    S = (seq_q if seq_k is None else seq_k).numel() - 1
+    if S < 0:
+        raise ValueError("seq_q and seq_k need S + 1 entries and len_k S")
+    if seq_q is not None:
+        _offsets("seq_q", seq_q, S + 1, dev)
+    if seq_k is not None:
+        _offsets("seq_k", seq_k, S + 1, dev)
+    if len_k is not None:
+        _offsets("len_k", len_k, S, dev)
+    return S
 
 
 def _row_stride(name, t, H, D, dtype, dev):
     """Elements between the rows of t [N, H, D], whose heads lie side by side (as in a slice of
     a joint projection)."""
-    if t.get_device() != dev or t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (H, D):
+    if (t.get_device() != dev or t.dtype is not dtype or t.dim() != 3 or t.size(1) != H
+            or t.size(2) != D):
         raise ValueError(f"{name} must be a CUDA tensor, {dtype}, of shape (N, {H}, {D}), on "
                          f"device {dev}")
+    if t.is_contiguous():
+        return H * D
     sn, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
@@ -1002,54 +1030,80 @@ def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "ha
     ``out_q`` and ``out_k`` may be Q and K themselves.  ``inverse`` turns back, as a backward does.
     Rows of no sequence are not written.
     """
-    if not Q.is_cuda or Q.dim() != 3:
-        raise ValueError(f"Q must be a CUDA tensor [N, H, D], has the shape {tuple(Q.shape)}")
     dev = Q.get_device()
-    if dev != torch.cuda.current_device():
+    if dev < 0 or Q.dim() != 3:
+        raise ValueError(f"Q must be a CUDA tensor [N, H, D], has the shape {tuple(Q.shape)}")
+    if dev != _device():
         with torch.cuda.device(dev):
             return gattn_rotary(Q, freqs, K, layout, pos, seq_q, seq_k, len_k, amp, inverse, out_q,
                                 out_k, stream)
     N, H, D = Q.shape
-    if layout not in ROTARY_LAYOUT:
+    dt = Q.dtype
+    order = ROTARY_LAYOUT.get(layout)
+    if order is None:
         raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUT)}, got {layout!r}")
-    width = 2 * freqs.numel()
-    _want("freqs", freqs, (width // 2,), torch.int64, dev)
-    qs = _row_stride("Q", Q, H, D, Q.dtype, dev)
-    Hkv, ks, ko = 0, 0, 0
+    pairs = freqs.numel()
+    if freqs.get_device() != dev or freqs.dtype is not torch.int64 or not freqs.is_contiguous():
+        _want("freqs", freqs, (pairs,), torch.int64, dev)
+    qs = qos = H * D
+    if not Q.is_contiguous():
+        qs = _row_stride("Q", Q, H, D, dt, dev)
+    Hkv = ks = kos = 0
     if K is not None:
-        if K.dim() != 3 or K.shape[0] != N:
+        if K.dim() != 3 or K.size(0) != N:
             raise ValueError(f"K must have the {N} rows of Q, has the shape {tuple(K.shape)}")
-        Hkv = K.shape[1]
-        ks = _row_stride("K", K, Hkv, D, Q.dtype, dev)
+        Hkv = K.size(1)
+        kos = Hkv * D
+        ks = _row_stride("K", K, Hkv, D, dt, dev)
     elif out_k is not None:
         raise ValueError("out_k needs K")
+    S = p_pos = p_sq = p_sk = p_len = 0
     if pos is not None:
         if seq_q is not None or seq_k is not None or len_k is not None:
             raise ValueError("give pos or sequences, not both")
-        _want("pos", pos, (N,), torch.int32, dev)
-        S = 0
+        _offsets("pos", pos, N, dev)
+        p_pos = pos.data_ptr()
     else:
         if seq_q is None:
             raise ValueError("positions need pos or seq_q")
-        S = _sequences(seq_q, seq_q if seq_k is None else seq_k, len_k, dev)
-    handle, other = _stream_of(dev, stream)
-    outs = []
-    for name, t, o, h in (("out_q", Q, out_q, H), ("out_k", K, out_k, Hkv)):
-        if t is None:
-            outs.append((None, 0))
-            continue
-        if o is None:
-            o = _new(dev, other, t.shape, t.dtype)
-        elif o.shape != t.shape:
-            raise ValueError(f"{name} must have the shape {tuple(t.shape)}")
-        outs.append((o, _row_stride(name, o, h, D, Q.dtype, dev)))
-    (oq, qos), (ok, kos) = outs
-    desc = _ROTARY_PACK.pack(N, H, Hkv, D, _dtype_code(Q.dtype), width, ROTARY_LAYOUT[layout],
-                             1 if inverse else 0, S, amp, freqs.data_ptr(), _at(pos) or 0,
-                             _at(seq_q) or 0, _at(seq_k) or 0, _at(len_k) or 0, qs, ks, qos, kos)
-    _check((_lib or load_library()).gattn_rotary(desc, Q.data_ptr(), _at(K), oq.data_ptr(),
-                                                 _at(ok), handle), "gattn_rotary")
-    return oq, ok
+        S = _seq_args(seq_q, seq_k, len_k, dev)
+        p_sq = seq_q.data_ptr()
+        if seq_k is not None:
+            p_sk = seq_k.data_ptr()
+        if len_k is not None:
+            p_len = len_k.data_ptr()
+    other = None
+    if stream is None:
+        handle = _raw_stream(dev)
+    else:
+        handle, other = _stream_of(dev, stream)
+    if out_q is None:
+        out_q = _empty(Q.shape, dtype=dt, device=Q.device) if other is None else \
+            _new(dev, other, Q.shape, dt)
+    else:
+        if out_q.shape != Q.shape:
+            raise ValueError(f"out_q must have the shape {tuple(Q.shape)}")
+        qos = _row_stride("out_q", out_q, H, D, dt, dev)
+    if K is None:
+        p_k = p_ko = None
+    else:
+        if out_k is None:
+            out_k = _empty(K.shape, dtype=dt, device=K.device) if other is None else \
+                _new(dev, other, K.shape, dt)
+        else:
+            if out_k.shape != K.shape:
+                raise ValueError(f"out_k must have the shape {tuple(K.shape)}")
+            kos = _row_stride("out_k", out_k, Hkv, D, dt, dev)
+        p_k, p_ko = K.data_ptr(), out_k.data_ptr()
+    code = _CODES.get(dt)
+    desc = _ROTARY_PACK.pack(N, H, Hkv, D, _dtype_code(dt) if code is None else code, 2 * pairs,
+                             order, 1 if inverse else 0, S, amp, freqs.data_ptr(), p_pos, p_sq,
+                             p_sk, p_len, qs, ks, qos, kos)
+    status = (_lib or load_library()).gattn_rotary(desc, Q.data_ptr(), p_k, out_q.data_ptr(), p_ko,
+                                                   handle)
+    if status:
+        _check(status, "gattn_rotary")
+    return out_q, out_k
 
 
 class Cache:
@@ -1083,8 +1137,9 @@ def gattn_cache_new(rows: int, Hkv: int, D: int, bits: int = 4, device="cuda") -
 
 def _cache_desc(c, S, N, H, dtype, block, topk, causal, scale, max_len_k, seq_q, seq_k, len_k,
                 su=0, sh=0, ks=0, vs=0):
-    return _CACHE_PACK.pack(S, N, c.rows, H, c.Hkv, c.D, _dtype_code(dtype), c.bits, block, topk,
-                            1 if causal else 0, scale, max_len_k,
+    code = _CODES.get(dtype)
+    return _CACHE_PACK.pack(S, N, c.rows, H, c.Hkv, c.D, _dtype_code(dtype) if code is None else code,
+                            c.bits, block, topk, 1 if causal else 0, scale, max_len_k,
                             0 if seq_q is None else seq_q.data_ptr(), seq_k.data_ptr(),
                             0 if len_k is None else len_k.data_ptr(), su, sh, ks, vs,
                             c.k.data_ptr(), c.v.data_ptr(), c.par.data_ptr())
@@ -1097,19 +1152,20 @@ def gattn_cache_write(cache: Cache, K: torch.Tensor, V: torch.Tensor, seq_q: tor
     Rows of K and V may lie apart (16-byte aligned), as slices of a joint projection do.
     """
     dev = cache.device
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return gattn_cache_write(cache, K, V, seq_q, seq_k, len_k, stream)
     ks = _row_stride("K", K, cache.Hkv, cache.D, K.dtype, dev)
     vs = _row_stride("V", V, cache.Hkv, cache.D, K.dtype, dev)
     if V.shape[0] != K.shape[0]:
         raise ValueError("K and V must have the same rows")
-    S = _sequences(seq_q, seq_k, len_k, dev)
+    S = _seq_args(seq_q, seq_k, len_k, dev)
+    handle = _raw_stream(dev) if stream is None else _stream_of(dev, stream)[0]
     desc = _cache_desc(cache, S, K.shape[0], cache.Hkv, K.dtype, 64, 0, False, 0.0, 0, seq_q, seq_k,
                        len_k, 0, 0, ks, vs)
-    _check((_lib or load_library()).gattn_cache_write(desc, K.data_ptr(), V.data_ptr(),
-                                                      _stream_of(dev, stream)[0]),
-           "gattn_cache_write")
+    status = (_lib or load_library()).gattn_cache_write(desc, K.data_ptr(), V.data_ptr(), handle)
+    if status:
+        _check(status, "gattn_cache_write")
 
 
 def gattn_cache_read(cache: Cache, seq_q: torch.Tensor, seq_k: torch.Tensor, len_k=None, since=None,
@@ -1122,28 +1178,30 @@ def gattn_cache_read(cache: Cache, seq_q: torch.Tensor, seq_k: torch.Tensor, len
     neither K nor V is given.
     """
     dev = cache.device
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return gattn_cache_read(cache, seq_q, seq_k, len_k, since, rows, dtype, K, V, stream)
-    S = _sequences(seq_q, seq_k, len_k, dev)
+    S = _seq_args(seq_q, seq_k, len_k, dev)
     if since is not None:
-        _want("since", since, (S,), torch.int32, dev)
+        _offsets("since", since, S, dev)
     given = K if K is not None else V
     if given is not None:
         rows, dtype = given.shape[0], given.dtype
     elif rows is None:
         raise ValueError("rows is needed where neither K nor V is given")
     shape = (rows, cache.Hkv, cache.D)
-    handle, other = _stream_of(dev, stream)
+    handle, other = (_raw_stream(dev), None) if stream is None else _stream_of(dev, stream)
     if given is None:
-        K, V = _new(dev, other, shape, dtype), _new(dev, other, shape, dtype)
+        K = _new(dev, other, shape, dtype)
+        V = _empty_like(K) if other is None else _new(dev, other, shape, dtype)
     else:
         for name, t in (("K", K), ("V", V)):
             if t is not None:
                 _want(name, t, shape, dtype, dev)
     desc = _cache_desc(cache, S, rows, cache.Hkv, dtype, 64, 0, False, 0.0, 0, seq_q, seq_k, len_k)
-    _check((_lib or load_library()).gattn_cache_read(desc, _at(since), _at(K), _at(V), handle),
-           "gattn_cache_read")
+    status = (_lib or load_library()).gattn_cache_read(desc, _at(since), _at(K), _at(V), handle)
+    if status:
+        _check(status, "gattn_cache_read")
     return K, V
 
 
@@ -1151,24 +1209,25 @@ def gattn_cache_sums(cache: Cache, seq_k: torch.Tensor, block: int, lens=None, s
                      stream=None) -> torch.Tensor:
     """gattn_block_sums of the cached keys: fp64 sums [blocks, Hkv, D] of what they stand for."""
     dev = cache.device
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return gattn_cache_sums(cache, seq_k, block, lens, since, sums, stream)
-    S = _sequences(seq_k, seq_k, lens, dev)
+    S = _seq_args(None, seq_k, lens, dev)
     if since is not None:
-        _want("since", since, (S,), torch.int32, dev)
+        _offsets("since", since, S, dev)
         if sums is None:
             raise ValueError("since needs sums, the table to renew")
     shape = (gattn_block_count(cache.rows, S, block), cache.Hkv, cache.D)
-    handle, other = _stream_of(dev, stream)
+    handle, other = (_raw_stream(dev), None) if stream is None else _stream_of(dev, stream)
     if sums is None:
         sums = _new(dev, other, shape, torch.float64)
     else:
         _want("sums", sums, shape, torch.float64, dev)
     desc = _cache_desc(cache, S, 0, cache.Hkv, torch.float32, block, 0, False, 0.0, 0, None, seq_k,
                        lens)
-    _check((_lib or load_library()).gattn_cache_sums(desc, _at(since), sums.data_ptr(), handle),
-           "gattn_cache_sums")
+    status = (_lib or load_library()).gattn_cache_sums(desc, _at(since), sums.data_ptr(), handle)
+    if status:
+        _check(status, "gattn_cache_sums")
     return sums
 
 
@@ -1184,14 +1243,14 @@ def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: t
     split well.  Rows of no sequence are not written.
     """
     dev = _cuda_index("Q", Q, 3)
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return gattn_cache_fwd(Q, cache, seq_q, seq_k, len_k, idx, block, scale, causal,
                                    max_len_k, out, lse, workspace, stream)
     N, H, D = Q.shape
     if cache.device != dev or cache.D != D:
         raise ValueError(f"Q [N, H, {D}] on device {dev} needs a cache of that width there")
-    S = _sequences(seq_q, seq_k, len_k, dev)
+    S = _seq_args(seq_q, seq_k, len_k, dev)
     topk = su = sh = 0
     if idx is not None:
         if idx.dim() != 3:
@@ -1204,7 +1263,7 @@ def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: t
                              f"{dev}, each list contiguous")
         if su == 0 and sh == 0 and units * cache.Hkv > 1:
             raise ValueError("idx repeats one list for all rows and heads; make it contiguous")
-    handle, other = _stream_of(dev, stream)
+    handle, other = (_raw_stream(dev), None) if stream is None else _stream_of(dev, stream)
     if out is None:
         out = _like(Q, other)
     else:
@@ -1218,7 +1277,8 @@ def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: t
     ws = _workspace(workspace, dev, other, "gattn_cache_fwd_workspace_size", desc,
                     (S > 0, N, cache.rows, H, cache.Hkv, D, cache.bits, Q.dtype, block, topk,
                      max_len_k))
-    _check((_lib or load_library()).gattn_cache_fwd(desc, Q.data_ptr(), _at(idx), out.data_ptr(),
-                                                    lse.data_ptr(), _at(ws), _bytes(ws), handle),
-           "gattn_cache_fwd")
+    status = (_lib or load_library()).gattn_cache_fwd(desc, Q.data_ptr(), _at(idx), out.data_ptr(),
+                                                      lse.data_ptr(), _at(ws), _bytes(ws), handle)
+    if status:
+        _check(status, "gattn_cache_fwd")
     return out, lse

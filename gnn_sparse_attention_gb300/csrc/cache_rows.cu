@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CachePara
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -382,17 +382,18 @@ __device__ __forceinline__ double scaled(int64_t v, int e) {
   return v == 0 ? 0.0 : __ll2double_rn(v) * __hiloint2double((1023 + e) << 20, 0);
 }
 
-// One warp sums one block of one key head: 16 rows a product, of which a lane
+// One warp sums one block (of at most NR rows) of one key head: 16 rows a product, of which a lane
 // holds D / 8 levels of four.
-template <int BITS, int D>
-__global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
+template <int BITS, int D, int NR>
+__global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 256 ? 3 : 4) cache_sums_kernel(
     const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int zs) {
   constexpr int RB = D * BITS / 8, VB = RB / 8, VW = VB < 4 ? 1 : VB / 4, MT = D / 16;
-  constexpr int MAXR = kBlkTile / 32;
+  constexpr int CH = VB == 16 ? 2 : 4;       // 16-row pieces on their way at a time
   constexpr int kClass = BITS == 4 ? 5 : 1;  // exponents of a class: 8 + 7 + BITS + this is 24 bits
+  __shared__ __align__(16) uint16_t weight[kRowThreads / 32][NR];
   const BlockGeom& g = p.g;
-  const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  const int64_t wid = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
+  const int64_t wid = int64_t(blockIdx.x) * (kRowThreads / 32) + warp;
   const int kh = int(wid % g.Hkv);
   const int64_t item = wid / g.Hkv;
   int s, b, step = 1, last;
@@ -416,23 +417,23 @@ __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
     const int n = pos >= 0 && pos < sp.len ? int(min(int64_t(g.block), sp.len - pos)) : 0;
     const int64_t r0 = int64_t(kh) * g.Nk + sp.beg + (n ? pos : 0);
     double* out = sums + (int64_t(piece) * g.Hkv + kh) * D;
-    const uint8_t* lev = p.k + r0 * RB + gq * VB;
-    uint32_t par[MAXR];
+    uint32_t par[NR / 32];
 #pragma unroll
-    for (int i = 0; i < MAXR; ++i)
+    for (int i = 0; i < NR / 32; ++i)
       par[i] = lane + 32 * i < n ? p.par[r0 + lane + 32 * i].x : 0u;
-    // levels of 64 rows are on their way while the exponents are looked at
-    uint32_t v[4][4][VW];
+    // levels of 16 CH rows are on their way while the exponents are looked at
+    const uint8_t* lev = p.k + (r0 + 2 * t) * RB + gq * VB;
+    uint32_t v[CH][4][VW];
     const auto fetch = [&](int at) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int r = at + 16 * c + 2 * t + 8 * (q >> 1) + (q & 1);
-          const uint8_t* a = lev + int64_t(r) * RB;
+          const int r = at + 16 * c + 8 * (q >> 1) + (q & 1);
+          const uint8_t* a = lev + r * RB;
 #pragma unroll
           for (int w = 0; w < VW; ++w) v[c][q][w] = 0;
-          if (r < n) {
+          if (r + 2 * t < n) {
             if constexpr (VB == 16) {
               const uint4 x = *reinterpret_cast<const uint4*>(a);
               v[c][q][0] = x.x; v[c][q][1] = x.y; v[c][q][2] = x.z; v[c][q][3] = x.w;
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
     // exponents of the steps and of the least values (one below 2^-126 counts as that)
     int se = 255, sx = 0, me = 255, mx = 0;
 #pragma unroll
-    for (int i = 0; i < MAXR; ++i) {
+    for (int i = 0; i < NR / 32; ++i) {
       const int em = (par[i] >> 7) & 255, es = (par[i] >> 23) & 255;
       if (par[i] & 0x7fffu) me = min(me, max(em, 1));
       mx = max(mx, em);
@@ -462,84 +463,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
     sx = __reduce_max_sync(0xffffffffu, sx);
     me = __reduce_min_sync(0xffffffffu, me);
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if (sx - se < 8 * kClass && sx < 255 && mx < 255 && mx - me <= 46) {
-      int64_t msum = 0;
-#pragma unroll
-      for (int i = 0; i < MAXR; ++i) {
-        const int em = (par[i] >> 7) & 255;
-        const int64_t x = int64_t((par[i] & 127u) | (em ? 128u : 0u))
-                          << (par[i] & 0x7fffu ? max(em, 1) - me : 0);
-        msum += par[i] & 0x8000u ? -x : x;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) msum += __shfl_xor_sync(0xffffffffu, msum, o);
-      const double mt = scaled(msum, me - 134);
-      float acc[MT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll
-      for (int at = 0; at < kBlkTile; at += 64) {
-        if (at >= n) break;
-        if (at > 0) fetch(at);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (at + 16 * c >= n) break;
-          // steps of rows 2t, 2t + 1, 2t + 8, 2t + 9 for column gq, as multiples of its class
-          uint32_t h[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t two = 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = __shfl_sync(0xffffffffu, par[(at + 16 * c) / 32],
-                                             (16 * c) % 32 + 2 * t + 8 * q + e);
-              const int k = int((x >> 23) & 255) - se - gq * kClass;
-              // fp16 with exponent k: 8 bits of mantissa
-              const uint32_t f = (uint32_t(k + 15) << 10) | ((x >> 13) & 0x3f8u);
-              two |= (k >= 0 && k < kClass ? f : 0u) << (16 * e);
-            }
-            h[q] = two;
-          }
-#pragma unroll
-          for (int w = 0; w < VW; ++w)
-#pragma unroll
-            for (int hh = 0; hh < (VB < 4 ? 1 : 2); ++hh) {
-              const uint32_t sel = hh ? 0x7632 : 0x5410;
-              const uint32_t a = __byte_perm(v[c][0][w], v[c][1][w], sel);
-              const uint32_t d = __byte_perm(v[c][2][w], v[c][3][w], sel);
-              if constexpr (BITS == 4) {
-                mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, d & 0x000f000fu,
-                         d & 0x00f000f0u, h[0], h[1]);
-                const uint32_t e = a >> 8, f = d >> 8;
-                mma16816(acc[4 * w + 2 * hh + 1], e & 0x000f000fu, e & 0x00f000f0u,
-                         f & 0x000f000fu, f & 0x00f000f0u, h[0], h[1]);
-              } else {
-                mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
-                         d & 0x00ff00ffu, (d >> 8) & 0x00ff00ffu, h[0], h[1]);
-              }
-            }
-        }
-      }
-      // column 2t + c counts 2^(se - 127 + (2t + c) kClass + 24); upper nibbles 16 times as much
-      const bool one = sx - se < kClass;  // column 0 alone
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        double x[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int e = se - 103 + 2 * t * kClass - (BITS == 4 ? 4 * h : 0);
-          x[h] = widened(acc[i][2 * h], e);
-          if (!one) {
-            x[h] += widened(acc[i][2 * h + 1], e + kClass);
-            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 1);
-            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 2);
-          }
-        }
-        if (t == 0)
-          *reinterpret_cast<double2*>(out + gq * (D / 8) + 2 * i) =
-              make_double2(x[0] + mt, x[1] + mt);
-      }
-    } else {
+    if (sx - se >= 8 * kClass || sx == 255 || mx == 255 || mx - me > 46) {
       for (int d = lane; d < D; d += 32) {
         double a = 0.0;
 #pragma unroll 4
@@ -550,6 +474,103 @@ __global__ void __launch_bounds__(kRowThreads) cache_sums_kernel(
           a += double(__uint_as_float(q << 16)) + double(__uint_as_float(q & 0xffff0000u)) * u;
         }
         out[d] = a;
+      }
+      continue;
+    }
+    // least values: whole multiples of 2^(me - 134)
+    int64_t msum = 0;
+#pragma unroll
+    for (int i = 0; i < NR / 32; ++i) {
+      const int em = (par[i] >> 7) & 255;
+      const int64_t x = int64_t((par[i] & 127u) | (em ? 128u : 0u))
+                        << (par[i] & 0x7fffu ? max(em, 1) - me : 0);
+      msum += par[i] & 0x8000u ? -x : x;
+    }
+    if (mx - me <= 15) {
+      msum = __reduce_add_sync(0xffffffffu, int(msum));  // 128 rows of 2^23
+    } else {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) msum += __shfl_xor_sync(0xffffffffu, msum, o);
+    }
+    // Steps in fp16, as multiples of their class's 2^(se + class kClass - 127), with the class in
+    // what that leaves free: an exponent below kClass takes three of the five bits.
+    const bool one = sx - se < kClass;
+#pragma unroll
+    for (int i = 0; i < NR / 32; ++i) {
+      const uint32_t es = (par[i] >> 23) & 255;
+      const int k = int(es) - se, cls = max(k, 0) / kClass;
+      weight[warp][lane + 32 * i] =
+          es ? uint16_t((cls << 13) | ((k - cls * kClass) << 10) | ((par[i] >> 13) & 0x3f8u)) : 0xffff;
+    }
+    __syncwarp();
+    float acc[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int at = 0; at < NR; at += 16 * CH) {
+      if (at >= n) break;
+      if (at > 0) fetch(at);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (at + 16 * c >= n) break;
+        uint32_t h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(&weight[warp][at + 16 * c + 2 * t + 8 * q]);
+          // column gq takes class gq; with a single class all columns may be alike
+          const uint32_t lo = x & 0xffffu, hi = x >> 16;
+          const bool a = lo != 0xffffu && (one || int(lo >> 13) == gq);
+          const bool d = hi != 0xffffu && (one || int(hi >> 13) == gq);
+          h[q] = (a ? (lo & 0x1fffu) + (15u << 10) : 0u) | (d ? ((hi & 0x1fffu) + (15u << 10)) << 16 : 0u);
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int hh = 0; hh < (VB < 4 ? 1 : 2); ++hh) {
+            const uint32_t sel = hh ? 0x7632 : 0x5410;
+            const uint32_t a = __byte_perm(v[c][0][w], v[c][1][w], sel);
+            const uint32_t d = __byte_perm(v[c][2][w], v[c][3][w], sel);
+            if constexpr (BITS == 4) {
+              mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, d & 0x000f000fu,
+                       d & 0x00f000f0u, h[0], h[1]);
+              const uint32_t e = a >> 8, f = d >> 8;
+              mma16816(acc[4 * w + 2 * hh + 1], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu,
+                       f & 0x00f000f0u, h[0], h[1]);
+            } else {
+              mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu, d & 0x00ff00ffu,
+                       (d >> 8) & 0x00ff00ffu, h[0], h[1]);
+            }
+          }
+      }
+    }
+    __syncwarp();  // the weights have been read
+    // column c counts 2^(se - 127 + c kClass + 24); upper nibbles 16 times as much
+    const double mt = scaled(msum, me - 134);
+    const int e0 = se - 103, up = BITS == 4 ? 4 : 0;
+    double* const o = out + gq * (D / 8);
+    if (one) {  // every column has the sums: the four lanes of a row group share the elements
+#pragma unroll
+      for (int j = 0; j < (MT + 3) / 4; ++j) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int i = 4 * j; i < (4 * j + 4 < MT ? 4 * j + 4 : MT); ++i)
+          if (i % 4 == t) x = acc[i][0], y = acc[i][2];
+        if (4 * j + t < MT)
+          *reinterpret_cast<double2*>(o + 2 * (4 * j + t)) =
+              make_double2(widened(x, e0) + mt, widened(y, e0 - up) + mt);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        double x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = e0 + 2 * t * kClass - up * h;
+          x[h] = widened(acc[i][2 * h], e) + widened(acc[i][2 * h + 1], e + kClass);
+          x[h] += __shfl_xor_sync(0xffffffffu, x[h], 1);
+          x[h] += __shfl_xor_sync(0xffffffffu, x[h], 2);
+        }
+        if (t == 0) *reinterpret_cast<double2*>(o + 2 * i) = make_double2(x[0] + mt, x[1] + mt);
       }
     }
   }
@@ -632,7 +653,10 @@ gattn_status launch_cache_sums(const CacheParams& p, const int32_t* since, doubl
   const int64_t warps = (since ? int64_t(p.g.S) * zs : int64_t(p.g.B)) * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
   by_layout(p, [&](auto bits, auto lpr) {
-    cache_sums_kernel<bits(), lpr() * 8><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+    if (p.g.block <= 64)
+      cache_sums_kernel<bits(), lpr() * 8, 64><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+    else
+      cache_sums_kernel<bits(), lpr() * 8, 128><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
   });
   return launched("gattn_cache_sums");
 }
