@@ -958,7 +958,7 @@ assert _CACHE_PACK.size == ctypes.sizeof(_CacheDesc)
 ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 _CODES = {torch.float32: GATTN_F32, torch.bfloat16: GATTN_BF16}
-_INT32, _empty, _empty_like = torch.int32, torch.empty, torch.empty_like
+_INT32, _empty_like = torch.int32, torch.empty_like
 _device = torch._C._cuda_getDevice              # of tensors that are on a GPU already
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -1078,8 +1078,7 @@ def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "ha
     else:
         handle, other = _stream_of(dev, stream)
     if out_q is None:
-        out_q = _empty(Q.shape, dtype=dt, device=Q.device) if other is None else \
-            _new(dev, other, Q.shape, dt)
+        out_q = _new(dev, other, Q.shape, dt) if other is not None or qs != qos else _empty_like(Q)
     else:
         if out_q.shape != Q.shape:
             raise ValueError(f"out_q must have the shape {tuple(Q.shape)}")
@@ -1088,8 +1087,8 @@ def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "ha
         p_k = p_ko = None
     else:
         if out_k is None:
-            out_k = _empty(K.shape, dtype=dt, device=K.device) if other is None else \
-                _new(dev, other, K.shape, dt)
+            out_k = _new(dev, other, K.shape, dt) if other is not None or ks != kos else \
+                _empty_like(K)
         else:
             if out_k.shape != K.shape:
                 raise ValueError(f"out_k must have the shape {tuple(K.shape)}")

@@ -13,9 +13,9 @@
 // Sums: sum (m + s u) over a block is sum m plus sum s u, and the second is a
 // product of levels with a vector: tensor cores, as in the attention (levels are
 // fp16 whole numbers as they lie).  Steps have 8 bits and levels 4 or 8, so the
-// fp32 sums of up to 128 rows are exact as long as the steps' exponents are within
-// 5 (1 with 8 bits) of each other: the eight columns of a product take a class of
-// exponents each.  Blocks beyond all classes are summed in fp64, row by row.
+// fp32 sums of 64 rows are exact as long as the steps' exponents are within 6 (2 with 8
+// bits) of each other, of 128 within one less: the eight columns of a product take a class
+// of exponents each.  Blocks beyond all classes are summed in fp64, row by row.
 #include "cache.cuh"
 
 namespace gattn {
@@ -377,9 +377,10 @@ __device__ __forceinline__ double widened(float x, int e) {
   if (b == 0) return 0.0;
   return __hiloint2double(int(((b >> 3) & 0x0fffffffu) + (uint32_t(896 + e) << 20)), int(b << 29));
 }
-// the whole number v times 2^e (v 2^e is 0 or normal), rounded if |v| is 2^53 or more
+// the whole number v (of at most 53 bits) times 2^e, 0 or normal
 __device__ __forceinline__ double scaled(int64_t v, int e) {
-  return v == 0 ? 0.0 : __ll2double_rn(v) * __hiloint2double((1023 + e) << 20, 0);
+  const double x = __ll2double_rn(v);
+  return v == 0 ? 0.0 : __hiloint2double(__double2hiint(x) + e * 0x100000, __double2loint(x));
 }
 
 // One warp sums one block (of at most NR rows) of one key head: 16 rows a product, of which a lane
@@ -389,7 +390,9 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
     const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int zs) {
   constexpr int RB = D * BITS / 8, VB = RB / 8, VW = VB < 4 ? 1 : VB / 4, MT = D / 16;
   constexpr int CH = VB == 16 ? 2 : 4;       // 16-row pieces on their way at a time
-  constexpr int kClass = BITS == 4 ? 5 : 1;  // exponents of a class: 8 + 7 + BITS + this is 24 bits
+  // exponents of a class: with 8 bits of the step, those of a level and of the rows, 24 together
+  constexpr int kClass = 16 - BITS - (NR > 64 ? 7 : 6);
+  constexpr int kSpread = 8 * kClass < 29 ? 8 * kClass : 29;  // 24 bits and the classes in 53
   __shared__ __align__(16) uint16_t weight[kRowThreads / 32][NR];
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
     sx = __reduce_max_sync(0xffffffffu, sx);
     me = __reduce_min_sync(0xffffffffu, me);
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if (sx - se >= 8 * kClass || sx == 255 || mx == 255 || mx - me > 46) {
+    if (sx - se >= kSpread || sx == 255 || mx == 255 || mx - me > 38) {
       for (int d = lane; d < D; d += 32) {
         double a = 0.0;
 #pragma unroll 4
@@ -544,11 +547,11 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
       }
     }
     __syncwarp();  // the weights have been read
-    // column c counts 2^(se - 127 + c kClass + 24); upper nibbles 16 times as much
+    // column c counts 2^(se - 127 + c kClass + 24), upper nibbles 16 times as much
     const double mt = scaled(msum, me - 134);
-    const int e0 = se - 103, up = BITS == 4 ? 4 : 0;
     double* const o = out + gq * (D / 8);
     if (one) {  // every column has the sums: the four lanes of a row group share the elements
+      const int e0 = se - 103, up = BITS == 4 ? 4 : 0;
 #pragma unroll
       for (int j = 0; j < (MT + 3) / 4; ++j) {
         float x = 0.f, y = 0.f;
@@ -560,17 +563,24 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
               make_double2(widened(x, e0) + mt, widened(y, e0 - up) + mt);
       }
     } else {
+      // whole multiples of 2^(se - 134), the columns' together
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        double x[2];
+        int64_t v[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int e = e0 + 2 * t * kClass - up * h;
-          x[h] = widened(acc[i][2 * h], e) + widened(acc[i][2 * h + 1], e + kClass);
-          x[h] += __shfl_xor_sync(0xffffffffu, x[h], 1);
-          x[h] += __shfl_xor_sync(0xffffffffu, x[h], 2);
+          const float unit = BITS == 4 && h ? 0x1p27f : 0x1p31f;
+          const int sh = 2 * t * kClass;
+          v[h] = sh > kSpread ? 0 : int64_t(__float2int_rn(acc[i][2 * h] * unit)) << sh;
+          if (sh + kClass <= kSpread)
+            v[h] += int64_t(__float2int_rn(acc[i][2 * h + 1] * unit)) << (sh + kClass);
+          v[h] += __shfl_xor_sync(0xffffffffu, v[h], 1);
+          v[h] += __shfl_xor_sync(0xffffffffu, v[h], 2);
         }
-        if (t == 0) *reinterpret_cast<double2*>(o + 2 * i) = make_double2(x[0] + mt, x[1] + mt);
+        if (i % 4 == t) {  // the lanes share the elements
+          *reinterpret_cast<double2*>(o + 2 * i) =
+              make_double2(scaled(v[0], se - 134) + mt, scaled(v[1], se - 134) + mt);
+        }
       }
     }
   }

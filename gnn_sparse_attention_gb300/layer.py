@@ -27,6 +27,9 @@ selects, ``gattn_block_select`` / ``gattn_block_fwd`` / ``gattn_block_bwd``),
 ``gattn_norm_fwd`` / ``gattn_norm_bwd``), and ``GraphTransformerBlock``, which
 puts them together: local attention over the edges plus global attention over
 the selected blocks, then an MLP, each behind a norm and added through a gate.
+``rotary`` gives queries and keys their positions (``gattn_rotary``), in the block too where it is
+asked for, and ``BlockCache`` is the serving side: a cache of keys and values in 4 or 8 bits
+(``gattn_cache_*``) that grows by new rows and is attended to by them.
 """
 from __future__ import annotations
 
@@ -198,6 +201,105 @@ def block_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torc
     return out, lse, idx
 
 
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, inverse, layout, amp, freqs, pos, seq, seq_k, len_k, Q, K):
+        ctx.how = (inverse, layout, amp)
+        ctx.save_for_backward(freqs, pos, seq, seq_k, len_k)
+        # rows of no sequence are not written by the kernel: zeros
+        new = torch.empty if seq is None else torch.zeros
+        out = [None if t is None else new(t.shape, dtype=t.dtype, device=t.device) for t in (Q, K)]
+        gb.gattn_rotary(Q, freqs, K=K, layout=layout, pos=pos, seq_q=seq, seq_k=seq_k, len_k=len_k,
+                        amp=amp, inverse=inverse, out_q=out[0], out_k=out[1])
+        return tuple(out)
+
+    @staticmethod
+    def backward(ctx, dQ, dK):
+        # turning is linear: its gradient turns back, and can be differentiated itself
+        inverse, layout, amp = ctx.how
+        dQ, dK = _Rotary.apply(not inverse, layout, amp, *ctx.saved_tensors, _rows(dQ), _rows(dK))
+        return (None,) * 8 + (dQ, dK)
+
+
+def _rows(t: torch.Tensor | None) -> torch.Tensor | None:
+    """t [N, H, D] with the heads of a row side by side: a copy where they are not."""
+    if t is None:
+        return None
+    sn, sh, sd = t.stride()
+    ok = (t.shape[2] == 1 or sd == 1) and (t.shape[1] == 1 or sh == t.shape[2]) and (
+        t.shape[0] <= 1 or sn >= t.shape[1] * t.shape[2])
+    return t if ok else t.contiguous()
+
+
+def rotary(Q: torch.Tensor, K: torch.Tensor | None, freqs: torch.Tensor, layout: str = "half",
+           pos: torch.Tensor | None = None, seq: torch.Tensor | None = None,
+           seq_k: torch.Tensor | None = None, len_k: torch.Tensor | None = None, amp: float = 1.0):
+    """(Q', K'): rotary positions of the first 2 * len(freqs) elements of every head.
+
+    Q [N, H, D], K [N, Hkv, D] or None, of one type; freqs from ``gattn_rotary_freqs``.  Positions
+    are ``pos`` (int32 [N]) or those of the rows of sequences (``seq``, and the keys' ``seq_k``,
+    ``len_k``: see gattn_rotary).  Rows may be slices of a joint projection.  Differentiable in Q and K,
+    any number of times.  Rows of no sequence get zeros.
+    """
+    if K is not None and K.dtype != Q.dtype:
+        raise ValueError(f"Q and K must be of one type, are {Q.dtype} and {K.dtype}")
+    return _Rotary.apply(False, layout, float(amp), freqs, pos, seq, seq_k, len_k, _rows(Q), _rows(K))
+
+
+class BlockCache:
+    """Keys and values of S sequences in 4 or 8 bits, for serving: each has ``room`` rows.
+
+    ``step`` appends new rows and attends from them, over the ``topk`` blocks that score highest
+    for each row and key head, or over the whole sequence with ``topk=0``.  ``length`` (int32 [S], on
+    the device) counts the rows; nothing is read back, so steps of one row a sequence can be
+    captured into a graph.  A sequence must not outgrow its room.
+    """
+
+    def __init__(self, S: int, room: int, Hkv: int, D: int, bits: int = 4, topk: int = 16,
+                 block: int = 64, device="cuda"):
+        self.room, self.topk, self.block = room, topk, block
+        self.cache = gb.gattn_cache_new(S * room, Hkv, D, bits, device)
+        self.seq_k = torch.arange(S + 1, dtype=torch.int32, device=device) * room
+        self.length = torch.zeros(S, dtype=torch.int32, device=device)
+        blocks = gb.gattn_block_count(S * room, S, block)
+        self.sums = torch.zeros(blocks, Hkv, D, dtype=torch.float64, device=device)
+
+    @torch.no_grad()
+    def append(self, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor) -> None:
+        """Rows [seq[s], seq[s+1]) of K and V [N, Hkv, D] become the next ones of sequence s, as after a
+        prompt that was attended to otherwise (K with its positions)."""
+        old = self.length.clone()
+        self.length += seq[1:] - seq[:-1]
+        self._append(_packed(K), _packed(V), seq, old)
+
+    def _append(self, K, V, seq, old):
+        gb.gattn_cache_write(self.cache, K, V, seq, self.seq_k, self.length)
+        gb.gattn_cache_sums(self.cache, self.seq_k, self.block, lens=self.length, since=old,
+                            sums=self.sums)
+
+    @torch.no_grad()
+    def step(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor,
+             freqs: torch.Tensor | None = None, layout: str = "half", amp: float = 1.0,
+             scale: float = 0.0):
+        """(out [N, H, D], lse [N, H]) of the new rows [seq[s], seq[s+1]) of every sequence, each of
+        which sees what stands before it and itself.  With ``freqs`` Q and K are given their
+        positions first.  Every row reads the cache for itself: meant for a few rows a sequence."""
+        old = self.length.clone()
+        self.length += seq[1:] - seq[:-1]
+        if freqs is not None:
+            Q, K = gb.gattn_rotary(_rows(Q), freqs, K=_rows(K), layout=layout, seq_q=seq,
+                                   seq_k=self.seq_k, len_k=self.length, amp=amp)
+        Q = _packed(Q)
+        self._append(_packed(K), _packed(V), seq, old)
+        idx = None
+        if self.topk:
+            idx = gb.gattn_block_select(Q, self.sums, seq, self.seq_k, self.topk, self.block, 1,
+                                        self.cache.rows, len_k=self.length, causal=True,
+                                        max_len_k=self.room)
+        return gb.gattn_cache_fwd(Q, self.cache, seq, self.seq_k, self.length, idx=idx,
+                                  block=self.block, scale=scale, causal=True, max_len_k=self.room)
+
+
 class _GatedResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, res, x, gate, w_post, b_post, w_pre, b_pre, alpha, kind, eps):
@@ -251,13 +353,18 @@ class GraphTransformerBlock(nn.Module):
     graph, both on the same heads of norm(h); then h = h + gate_m * norm(MLP(norm(h))).  The
     gates are learned per channel.  ``seq`` holds the graphs' first node rows, ``max_nodes``
     (0: unknown) the size of the largest graph; see block_attention for both, and for errors.
+    ``rotary`` (elements of each head, 0: none) turns queries and keys by the nodes' positions within
+    their graphs before both attentions, with frequencies of base ``theta``.
     """
 
     def __init__(self, dim: int, heads: int, head_dim: int, mlp_dim: int | None = None,
                  topk: int = 16, block: int = 64, q_block: int = 64, causal: bool = False,
-                 kind: str = "rms", gate_init: float = 1.0, dtype=torch.bfloat16, device=None):
+                 kind: str = "rms", gate_init: float = 1.0, dtype=torch.bfloat16, device=None,
+                 rotary: int = 0, theta: float = 10000.0):
         super().__init__()
         self.heads, self.head_dim, self.kind = heads, head_dim, kind
+        freqs = gb.gattn_rotary_freqs(rotary, theta, device=device or "cpu") if rotary else None
+        self.register_buffer("freqs", freqs, persistent=False)
         self.choice = {"topk": topk, "block": block, "q_block": q_block, "causal": causal}
         kw = {"dtype": dtype, "device": device}
         hd = heads * head_dim
@@ -278,7 +385,9 @@ class GraphTransformerBlock(nn.Module):
                 idx: torch.Tensor | None = None, max_nodes: int = 0) -> torch.Tensor:
         N = h.shape[0]
         h, y = gated_residual_norm(h, w_pre=self.w_in, b_pre=self.b_in, kind=self.kind)
-        Q, K, V = (t.reshape(N, self.heads, self.head_dim) for t in self.qkv(y).chunk(3, -1))
+        Q, K, V = (t.unflatten(1, (self.heads, self.head_dim)) for t in self.qkv(y).chunk(3, -1))
+        if self.freqs is not None:
+            Q, K = rotary(Q, K, self.freqs, seq=seq)
         Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
         a, _, _ = block_attention(Q, K, V, seq, idx=idx, max_len_k=max_nodes, **self.choice)
         if plan is not None:

@@ -751,9 +751,10 @@ GATTN_API gattn_status gattn_cache_read(const gattn_cache_desc* desc, const int3
                                         void* V, gattn_stream_t stream);
 
 /*
- * gattn_block_sums of the values that the cached keys stand for, in the same table: the sum of
- * each block, exact in 64 bits wherever the rows' steps and least values lie within a factor of
- * about 2^23 (else rounded as fp64 additions in row order are).
+ * gattn_block_sums of the values that the cached keys stand for, in the same table.  Each sum is
+ * exact but for its last rounding to 64 bits, as long as the steps of the block's rows are
+ * within 2^8 of each other (2^28 with 4 bits) and their least values within 2^38; else it is that
+ * of fp64 additions in row order.
  */
 GATTN_API gattn_status gattn_cache_sums(const gattn_cache_desc* desc, const int32_t* since,
                                         double* sums, gattn_stream_t stream);
