@@ -23,7 +23,14 @@
 // Precision.  q enters in fp16 after scaling each head by a power of two: exact
 // for bf16, as a sum of two (two columns) for fp32.  p s enters in fp16 (11 bits,
 // or as two for fp32), scaled by a power of two per column that follows its
-// maximum.  Softmax statistics, m's terms and all sums are fp32.
+// maximum.  Softmax statistics, m's terms and all sums are fp32.  The tensor cores
+// align products by the operands' exponent fields, so a level at the bottom of the
+// denormals loses the bits above it: K's are raised by three bits (lse of 128
+// tokens off by 7e-8 instead of 1.2e-6, for 0.3 us of 62).  And sums about 0 round
+// less than sums about q . middle level: scores start from minus that, with m + the
+// middle's steps for m.  In fp32 both operands are moved about zero before their
+// products (1024 + u in fp16 less 1024 + middle, one more instruction for two
+// levels, 9 us of 62 where that was tried with bf16): out off by 2.3e-7, which was 2.3e-5.
 //
 // A warp takes steps of 32 rows (16 where a row has 128 bytes) through a ring of
 // its own in shared memory, filled by cp.async two steps ahead, with its own running
@@ -133,6 +140,23 @@ __device__ __forceinline__ void copy(uint32_t dst, const void* src, bool in) {
                  "r"(in ? 8 : 0) : "memory");
 }
 
+// Levels as fp16 numbers about zero: the bits `m` of x in the low bits of 1024, less 1024 and the
+// middle level.  BITS 4: m names a nibble of each half, which counts 16 times if it is the upper one.
+__device__ __forceinline__ uint32_t less(uint32_t x, uint32_t bias) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t nibble(uint32_t x) {
+  return less((x & 0x000f000fu) | 0x64006400u, 0x64086408u);
+}
+__device__ __forceinline__ uint32_t nibble16(uint32_t x) {
+  return less((x & 0x00f000f0u) | 0x64006400u, 0x64806480u);
+}
+// bytes as they stand in the halves of x
+__device__ __forceinline__ uint32_t byte(uint32_t x) {
+  return less((x & 0x00ff00ffu) | 0x64006400u, 0x64806480u);
+}
+
 // Row of a tile that stands in product row r (r < 8; r + 8 likewise): product
 // rows 2t, 2t + 1 are rows t, 4 + t, so that a warp's load of V covers four whole rows.
 __device__ __forceinline__ int tile_row(int r) { return (r >> 1) + 4 * (r & 1); }
@@ -210,6 +234,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   constexpr int RB = L::RB, R = L::R, NT = L::NT;
   constexpr bool kSplit = sizeof(T) == 4;  // fp32: a head is two columns
   constexpr int HC = 4 * NC;               // heads of a column group
+  constexpr float kMid = BITS == 4 ? 8.f : 128.f;  // middle level
   static_assert(NC == 1 || !kSplit, "");
   static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     const int head0 = kh * g.G + cgrp * HC, heads = min(HC, g.G - cgrp * HC);
     // q of this lane's column, scaled to fp16's range, in the order of the words of a K row
     uint32_t qf[L::QR];
-    float qmul[NC], qsum[NC];  // of the lane's heads
+    float qmul[NC], qsum[NC], qmid[NC];  // of the lane's heads
     {
       const int hc = NC == 1 ? gq >> 1 : gq;
       const bool on = hc < heads && (NC == 2 || kSplit || !(gq & 1));
@@ -442,17 +467,20 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         }
       // columns 2t, 2t + 1 of a product belong to the lanes with gq = 2t, 2t + 1; the sum of q is
       // its product with levels of 1
-      const float mul = g.qmul * 16777216.f / scale;
+      const float mul = g.qmul * (kSplit ? 1.f : 0x1p21f) / scale;
       float one[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int r = 0; r < L::QR; r += 2) {
-        constexpr uint32_t kUp = BITS == 4 ? 0x00100010u : 0x00010001u;
-        mma16816(one, 0x00010001u, 0x00010001u, kUp, kUp, qf[r], qf[r + 1]);
+        constexpr uint32_t kOne = kSplit ? 0x3c003c00u : 0x00080008u;
+        constexpr uint32_t kUp = BITS == 8 ? kOne : kSplit ? 0x4c004c00u : 0x00800080u;
+        mma16816(one, kOne, kOne, kUp, kUp, qf[r], qf[r + 1]);
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        const float x = kSplit ? one[0] + one[1] : one[c];
         qmul[c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
-        qsum[c] = (kSplit ? one[0] + one[1] : one[c]) * qmul[c];
+        qsum[c] = x * qmul[c];
+        qmid[c] = -kMid * x;
       }
     }
 
@@ -504,15 +532,29 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
           const uint32_t a = ka[h][0][w], b = ka[h][1][w];
-          if constexpr (BITS == 4) {
-            mma16816(s4[h], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                     qf[4 * w], qf[4 * w + 1]);
+          const uint32_t* const q = qf + w * (L::QR / L::KW);
+          if constexpr (kSplit && BITS == 4) {
+            mma16816(s4[h], nibble(a), nibble(b), nibble16(a), nibble16(b), q[0], q[1]);
             const uint32_t c = a >> 8, d = b >> 8;
-            mma16816(s4[h], c & 0x000f000fu, d & 0x000f000fu, c & 0x00f000f0u, d & 0x00f000f0u,
-                     qf[4 * w + 2], qf[4 * w + 3]);
+            mma16816(s4[h], nibble(c), nibble(d), nibble16(c), nibble16(d), q[2], q[3]);
+          } else if constexpr (kSplit) {
+            mma16816(s4[h], byte(a), byte(b), byte(a >> 8), byte(b >> 8), q[0], q[1]);
           } else {
-            mma16816(s4[h], a & 0x00ff00ffu, b & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu,
-                     (b >> 8) & 0x00ff00ffu, qf[2 * w], qf[2 * w + 1]);
+            if (w == 0) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s4[h][e] = NC == 2 || e % 2 == 0 ? qmid[NC == 2 ? e % 2 : 0] : 0.f;
+            }
+            if constexpr (BITS == 4) {
+              const uint32_t c = a << 3, d = b << 3, e = a >> 5, f = b >> 5;
+              mma16816(s4[h], c & 0x00780078u, d & 0x00780078u, c & 0x07800780u, d & 0x07800780u,
+                       q[0], q[1]);
+              mma16816(s4[h], e & 0x00780078u, f & 0x00780078u, e & 0x07800780u, f & 0x07800780u,
+                       q[2], q[3]);
+            } else {
+              const uint32_t c = a << 3, d = b << 3, e = a >> 5, f = b >> 5;
+              mma16816(s4[h], c & 0x07f807f8u, d & 0x07f807f8u, e & 0x07f807f8u, f & 0x07f807f8u,
+                       q[0], q[1]);
+            }
           }
         }
 #pragma unroll
@@ -521,12 +563,13 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         for (int q = 0; q < 2; ++q) {
           const uint2 par = *reinterpret_cast<const uint2*>(st + po + (16 * h + 8 * q) * 8);
           const float mk = __uint_as_float(par.x << 16), sk = __uint_as_float(par.x & 0xffff0000u);
-          vm[h][q] = __uint_as_float(par.y << 16);
           vs[h][q] = __uint_as_float(par.y & 0xffff0000u);
+          vm[h][q] = __uint_as_float(par.y << 16);
+          if (kSplit) vm[h][q] = fmaf(kMid, vs[h][q], vm[h][q]);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float dot = kSplit ? s4[h][2 * q] + s4[h][2 * q + 1] : s4[h][2 * q + c];
-            x[h][q][c] = fmaf(dot * qmul[c], sk, fmaf(mk, qsum[c], -ref[c]));
+            x[h][q][c] = fmaf(dot * qmul[c], sk, fmaf(fmaf(kMid, sk, mk), qsum[c], -ref[c]));
           }
         }
       }
@@ -641,11 +684,17 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
             const uint32_t a = __byte_perm(va[0][w], va[1][w], sel);
             const uint32_t b = __byte_perm(va[2][w], va[3][w], sel);
             if constexpr (BITS == 4) {
-              mma16816(acc[4 * w + 2 * hh], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu,
-                       b & 0x00f000f0u, b0, b1);
               const uint32_t c = a >> 8, d = b >> 8;
-              mma16816(acc[4 * w + 2 * hh + 1], c & 0x000f000fu, c & 0x00f000f0u, d & 0x000f000fu,
-                       d & 0x00f000f0u, b0, b1);
+              float *o = acc[4 * w + 2 * hh], *o2 = acc[4 * w + 2 * hh + 1];
+              if constexpr (kSplit) {
+                mma16816(o, nibble(a), nibble16(a), nibble(b), nibble16(b), b0, b1);
+                mma16816(o2, nibble(c), nibble16(c), nibble(d), nibble16(d), b0, b1);
+              } else {
+                mma16816(o, a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
+                mma16816(o2, c & 0x000f000fu, c & 0x00f000f0u, d & 0x000f000fu, d & 0x00f000f0u, b0, b1);
+              }
+            } else if constexpr (kSplit) {
+              mma16816(acc[2 * w + hh], byte(a), byte(a >> 8), byte(b), byte(b >> 8), b0, b1);
             } else {
               mma16816(acc[2 * w + hh], a & 0x00ff00ffu, (a >> 8) & 0x00ff00ffu, b & 0x00ff00ffu,
                        (b >> 8) & 0x00ff00ffu, b0, b1);
@@ -672,7 +721,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         sref[warp][h] = fresh ? kNone : ref[c];
         sl[warp][h] = sum[c];
       }
-      const float back = 16777216.f / vf[c];
+      const float back = (kSplit ? 1.f : 16777216.f) / vf[c];
 #pragma unroll
       for (int i = 0; i < L::MT; ++i) {
         const float lo = kSplit ? acc[i][0] + acc[i][1] : acc[i][c];

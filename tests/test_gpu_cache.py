@@ -252,6 +252,36 @@ def test_sums_of_unlike_rows(bits):
     assert bool(((got - want).abs()[ok] <= 64 * 2.0 ** -52 * mag[ok]).all())
 
 
+@pytest.mark.parametrize("bits,spread", [(4, 1), (4, 3), (4, 6), (4, 7), (4, 13), (4, 28), (8, 1), (8, 2), (8, 3), (8, 8)])
+@pytest.mark.parametrize("block", [16, 64, 128])
+def test_sums_are_exact(block, bits, spread):
+    """Steps of any mantissa over `spread` exponents, any levels (all the highest, all odd, random): no bit is
+    lost.  All products and sums of a block are whole multiples of the least step's last bit below 2^53."""
+    n, Hkv, D = 256, 2, 128
+    g = torch.Generator().manual_seed(spread * 100 + block)
+    c = gb.gattn_cache_new(n, Hkv, D, bits)
+    for kind in range(4):
+        mant = torch.randint(0, 128, (Hkv, n), generator=g)
+        if kind == 0:
+            mant.fill_(127)
+        e = torch.randint(0, spread, (Hkv, n), generator=g)
+        if kind == 1:
+            e[:, ::2] = 0
+            e[:, 1::2] = spread - 1
+            mant[:, ::2] |= 1
+        step = (1 + mant / 128) * torch.exp2(e.double() - 5)
+        least = torch.randint(-255, 256, (Hkv, n), generator=g) / 64.0
+        c.par.copy_(torch.stack([least.double(), step, least.double(), step], -1).to(torch.bfloat16))
+        lev = torch.randint(0, 256, c.k.shape, generator=g)
+        if kind == 0:
+            lev.fill_(255)
+        elif kind == 1:
+            lev |= 0x11
+        c.k.copy_(lev.to(torch.uint8))
+        want, _ = sums_ref(c, [0, n], [n], block)
+        assert torch.equal(gb.gattn_cache_sums(c, i32([0, n]), block).cpu(), want), kind
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
