@@ -39,25 +39,39 @@ template <class T>
 struct Row8;  // eight elements of a lane
 template <>
 struct Row8<float> {
-  uint4 a, b;
-  __device__ void load(const float* x) {
-    a = reinterpret_cast<const uint4*>(x)[0];
-    b = reinterpret_cast<const uint4*>(x)[1];
+  float f[8];
+  // wide: rows start on 32-byte borders, one instruction
+  __device__ void load(const float* x, bool wide) {
+    if (wide) {
+      asm volatile("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                   : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
+                     "=f"(f[6]), "=f"(f[7])
+                   : "l"(x));
+    } else {
+      const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
   }
-  __device__ void get(float* f) const {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  __device__ void get(float* to) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 8; ++i) to[i] = f[i];
   }
-  __device__ static void store(float* x, const float* f) {
-    reinterpret_cast<float4*>(x)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(x)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ static void store(float* x, const float* f, bool wide) {
+    if (wide) {
+      asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(x), "f"(f[0]),
+                   "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(x)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(x)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   }
 };
 template <>
 struct Row8<__nv_bfloat16> {
   uint4 a;
-  __device__ void load(const __nv_bfloat16* x) { a = *reinterpret_cast<const uint4*>(x); }
+  __device__ void load(const __nv_bfloat16* x, bool) { a = *reinterpret_cast<const uint4*>(x); }
   __device__ void get(float* f) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -66,7 +80,7 @@ struct Row8<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ static void store(__nv_bfloat16* x, const float* f) {
+  __device__ static void store(__nv_bfloat16* x, const float* f, bool) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -201,7 +215,8 @@ __device__ __forceinline__ typename Levels<BITS>::W levels(const float* f, float
 template <class T, int BITS, int LPR, int UN>
 __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CacheParams p,
                                                                   const T* __restrict__ K,
-                                                                  const T* __restrict__ V) {
+                                                                  const T* __restrict__ V,
+                                                                  bool wide) {
   constexpr int RPW = 32 / LPR, D = LPR * 8, NR = 2 * UN;
   constexpr int OWN = NR > LPR ? NR / LPR : 1;  // rows of a lane in the end
   using W = typename Levels<BITS>::W;
@@ -215,8 +230,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CachePar
 #pragma unroll
   for (int u = 0; u < UN; ++u) {
     const int64_t t = min(t0 + u * RPW, int64_t(g.Nq) - 1);
-    row[2 * u].load(K + t * p.ks + kh * D + j * 8);
-    row[2 * u + 1].load(V + t * p.vs + kh * D + j * 8);
+    row[2 * u].load(K + t * p.ks + kh * D + j * 8, wide);
+    row[2 * u + 1].load(V + t * p.vs + kh * D + j * 8, wide);
   }
   // where the lane's own rows go, while they are on their way
   const int first = j * NR / LPR;
@@ -308,7 +323,7 @@ template <class T, int BITS, int LPR, int UN>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheParams p,
                                                                  const int32_t* __restrict__ since,
                                                                  T* __restrict__ K,
-                                                                 T* __restrict__ V) {
+                                                                 T* __restrict__ V, bool wide) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   static_assert(UN <= LPR, "a lane finds one token's row");
   using W = typename Levels<BITS>::W;
@@ -350,11 +365,11 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CachePara
       float f[8];
       if (K) {
         values<BITS>(wk[u], par[u].x, f);
-        Row8<T>::store(K + out + u * step, f);
+        Row8<T>::store(K + out + u * step, f, wide);
       }
       if (V) {
         values<BITS>(wv[u], par[u].y, f);
-        Row8<T>::store(V + out + u * step, f);
+        Row8<T>::store(V + out + u * step, f, wide);
       }
     }
 }
@@ -389,7 +404,7 @@ template <int BITS, int D, int NR>
 __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 256 ? 3 : 4) cache_sums_kernel(
     const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int zs) {
   constexpr int RB = D * BITS / 8, VB = RB / 8, VW = VB < 4 ? 1 : VB / 4, MT = D / 16;
-  constexpr int CH = VB == 16 ? 2 : 4;       // 16-row pieces on their way at a time
+  constexpr int CH = VB == 16 || NR == 32 ? 2 : 4;  // 16-row pieces on their way at a time
   // exponents of a class: with 8 bits of the step, those of a level and of the rows, 24 together
   constexpr int kClass = 16 - BITS - (NR > 64 ? 7 : 6);
   constexpr int kSpread = 8 * kClass < 29 ? 8 * kClass : 29;  // 24 bits and the classes in 53
@@ -595,17 +610,20 @@ gattn_status launched(const char* what) {
   return GATTN_OK;
 }
 
+bool al32(const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
 template <class T, int BITS, int LPR>
 void write_rows(const CacheParams& p, const void* K, const void* V, cudaStream_t st) {
   constexpr int RPW = 32 / LPR, UN = 4;
   const T *k = static_cast<const T*>(K), *v = static_cast<const T*>(V);
+  const bool wide = al32(K) && al32(V) && p.ks % 8 == 0 && p.vs % 8 == 0;
   // few rows: a warp for each RPW of them
   const bool few = int64_t(p.g.Nq) * p.g.Hkv < int64_t(sm_count()) * 64 * RPW;
   const int64_t tok = few ? RPW : RPW * UN;
   const int64_t warps = (p.g.Nq + tok - 1) / tok * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
-  if (few) cache_write_kernel<T, BITS, LPR, 1><<<grid, kRowThreads, 0, st>>>(p, k, v);
-  else cache_write_kernel<T, BITS, LPR, UN><<<grid, kRowThreads, 0, st>>>(p, k, v);
+  if (few) cache_write_kernel<T, BITS, LPR, 1><<<grid, kRowThreads, 0, st>>>(p, k, v, wide);
+  else cache_write_kernel<T, BITS, LPR, UN><<<grid, kRowThreads, 0, st>>>(p, k, v, wide);
 }
 
 template <class T, int BITS, int LPR>
@@ -616,8 +634,9 @@ void read_rows(const CacheParams& p, const int32_t* since, void* K, void* V, cud
   const int64_t warps = (p.g.Nq + tok - 1) / tok * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
   T *k = static_cast<T*>(K), *v = static_cast<T*>(V);
-  if (few) cache_read_kernel<T, BITS, LPR, 1><<<grid, kRowThreads, 0, st>>>(p, since, k, v);
-  else cache_read_kernel<T, BITS, LPR, UN><<<grid, kRowThreads, 0, st>>>(p, since, k, v);
+  const bool wide = al32(K) && al32(V);
+  if (few) cache_read_kernel<T, BITS, LPR, 1><<<grid, kRowThreads, 0, st>>>(p, since, k, v, wide);
+  else cache_read_kernel<T, BITS, LPR, UN><<<grid, kRowThreads, 0, st>>>(p, since, k, v, wide);
 }
 
 // f(type, bits, lanes per row)
@@ -663,7 +682,9 @@ gattn_status launch_cache_sums(const CacheParams& p, const int32_t* since, doubl
   const int64_t warps = (since ? int64_t(p.g.S) * zs : int64_t(p.g.B)) * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
   by_layout(p, [&](auto bits, auto lpr) {
-    if (p.g.block <= 64)
+    if (p.g.block <= 32)
+      cache_sums_kernel<bits(), lpr() * 8, 32><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+    else if (p.g.block <= 64)
       cache_sums_kernel<bits(), lpr() * 8, 64><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
     else
       cache_sums_kernel<bits(), lpr() * 8, 128><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);

@@ -23,6 +23,7 @@ constexpr int kRotThreads = 256;
 struct RotParams {
   int N, H, HT, D, R, S;  // HT: heads of Q and K together
   int cph, hg, rpb;       // threads per head, heads side by side, rows per block
+  int flat;               // elements of a head from here on move as vectors (D: none)
   bool half;
   float amp, sign;
   const uint64_t* freqs;
@@ -160,9 +161,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) 
   }
 }
 
-// Any alignment and width: thread j of a head turns pair j, or copies an element.
+// Any alignment and width.  Thread j of a head turns pair j, copies an element behind the pairs, or,
+// from element `flat` on, a whole vector.
 template <class T>
 __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotParams p) {
+  constexpr int V = Pack<T>::V;
+  constexpr int UN = 4;  // heads on their way at a time
   const int64_t n = int64_t(p.N) * p.cph;
   for (int64_t e = int64_t(blockIdx.x) * kRotThreads + threadIdx.x; e < n;
        e += int64_t(gridDim.x) * kRotThreads) {
@@ -174,22 +178,48 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotParams
     const T* k = reinterpret_cast<const T*>(p.k) + row * p.ks;
     T* qo = reinterpret_cast<T*>(p.qo) + row * p.qos;
     T* ko = reinterpret_cast<T*>(p.ko) + row * p.kos;
+    const auto src = [&](int h) { return h < p.H ? q + h * p.D : k + (h - p.H) * p.D; };
+    const auto dst = [&](int h) { return h < p.H ? qo + h * p.D : ko + (h - p.H) * p.D; };
+    const int singles = p.R / 2 + p.flat - p.R;  // pairs, and elements behind them
+    const int step = gridDim.y;
+    if (j >= singles) {
+      const int o = p.flat + (j - singles) * V;
+      for (int h = blockIdx.y; h < p.HT; h += UN * step) {
+        uint4 a[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+          if (h + u * step < p.HT) a[u] = *reinterpret_cast<const uint4*>(src(h + u * step) + o);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+          if (h + u * step < p.HT) *reinterpret_cast<uint4*>(dst(h + u * step) + o) = a[u];
+      }
+      continue;
+    }
     const bool pair = j < p.R / 2;
     const int oa = !pair ? p.R / 2 + j : p.half ? j : 2 * j;
     const int ob = !pair ? oa : p.half ? j + p.R / 2 : 2 * j + 1;
     float c = 1.f, s = 0.f;
     if (pair) turn(p, at, p.freqs[j], &c, &s);
-    for (int h = blockIdx.y; h < p.HT; h += gridDim.y) {
-      const T* x = h < p.H ? q + h * p.D : k + (h - p.H) * p.D;
-      T* z = h < p.H ? qo + h * p.D : ko + (h - p.H) * p.D;
-      const T ta = x[oa], tb = x[ob];
-      if (!pair) {
-        z[oa] = ta;
-        continue;
-      }
-      const float a = float(ta), b = float(tb);
-      z[oa] = T(a * c - b * s);
-      z[ob] = T(a * s + b * c);
+    for (int h = blockIdx.y; h < p.HT; h += UN * step) {
+      T a[UN], b[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+        if (h + u * step < p.HT) {
+          a[u] = src(h + u * step)[oa];
+          b[u] = src(h + u * step)[ob];
+        }
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+        if (h + u * step < p.HT) {
+          T* z = dst(h + u * step);
+          if (!pair) {
+            z[oa] = a[u];
+            continue;
+          }
+          const float x = float(a[u]), y = float(b[u]);
+          z[oa] = T(x * c - y * s);
+          z[ob] = T(x * s + y * c);
+        }
     }
   }
 }
@@ -205,13 +235,15 @@ bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) =
   } while (0)
 
 template <class T>
-void launch(RotParams& p, bool vectors, cudaStream_t st) {
+void launch(RotParams& p, bool vectors, bool whole, cudaStream_t st) {
   constexpr int V = Pack<T>::V;
-  if (!vectors) {
-    p.cph = p.D - p.R / 2;
+  if (!whole) {
+    p.flat = vectors ? (p.R + V - 1) / V * V : p.D;
+    p.cph = p.R / 2 + (p.flat - p.R) + (p.D - p.flat) / V;
     const int64_t n = (int64_t(p.N) * p.cph + kRotThreads - 1) / kRotThreads;
-    // few rows: a thread for every head as well
-    const int heads = n * 8 >= sm_count() * 8 ? 1 : p.HT < 64 ? p.HT : 64;
+    // heads in groups of blocks as long as the rows alone do not fill the GPU eight times
+    int heads = 1;
+    while (heads < p.HT && heads < 64 && n * heads < int64_t(sm_count()) * 64) heads *= 2;
     rotary_any_kernel<T><<<dim3(unsigned(n < 1 << 20 ? n : 1 << 20), heads), kRotThreads, 0, st>>>(p);
     return;
   }
@@ -298,12 +330,13 @@ gattn_status gattn_rotary(const gattn_rotary_desc* d, const void* Q, const void*
   p.kos = kos;
   const int V = 16 / es;
   const auto vec = [&](const void* x, int64_t stride) { return al(x, 16) && stride % V == 0; };
-  const bool vectors = d->D % V == 0 && d->width % (p.half ? 2 * V : V) == 0 && vec(Q, qs) && vec(Q_out, qos) &&
-                       (d->Hkv == 0 || (vec(K, ks) && vec(K_out, kos))) &&
-                       d->D / V <= kRotThreads;
+  // vectors: rows and heads start on 16-byte borders; whole: what turns together does too
+  const bool vectors = d->D % V == 0 && vec(Q, qs) && vec(Q_out, qos) &&
+                       (d->Hkv == 0 || (vec(K, ks) && vec(K_out, kos)));
+  const bool whole = vectors && d->width % (p.half ? 2 * V : V) == 0 && d->D / V <= kRotThreads;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (es == 4) launch<float>(p, vectors, st);
-  else launch<__nv_bfloat16>(p, vectors, st);
+  if (es == 4) launch<float>(p, vectors, whole, st);
+  else launch<__nv_bfloat16>(p, vectors, whole, st);
   const cudaError_t e = cudaGetLastError();
   ROT_REQUIRE(e == cudaSuccess, GATTN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
   return GATTN_OK;

@@ -156,6 +156,29 @@ def test_write_slices(dtype):
         gb.gattn_cache_write(d, K[:1].expand(n, -1, -1), V, i32([0, n]), i32([0, n]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sixteen_byte_borders(dtype):
+    """Rows that start on 16-byte borders that are no 32-byte ones, in and out."""
+    n, Hkv, D, dt = 40, 2, 32, DT[dtype]
+    pad = 16 // torch.empty((), dtype=dt).element_size()
+    K, V = randn(80, n, Hkv, D, dtype=dt), randn(81, n, Hkv, D, dtype=dt)
+    want = write(K, V, [0, n], [0, n], None, 8, n)
+    for off, extra in ((pad, pad), (0, pad), (pad, 0)):
+        buf = torch.zeros(n * (Hkv * D + extra) + off, dtype=dt, device=DEV)
+        views = []
+        for x in (K, V):
+            v = torch.zeros_like(buf)[off:].view(n, Hkv * D + extra)[:, :Hkv * D].unflatten(1, (Hkv, D))
+            v.copy_(x)
+            views.append(v)
+        c = marked(n, Hkv, D, 8)
+        gb.gattn_cache_write(c, *views, i32([0, n]), i32([0, n]))
+        assert torch.equal(c.k, want.k) and torch.equal(c.v, want.v) and torch.equal(c.par, want.par)
+    ref_k, ref_v = gb.gattn_cache_read(want, i32([0, n]), i32([0, n]), rows=n, dtype=dt)
+    outs = [torch.zeros(n * Hkv * D + pad, dtype=dt, device=DEV)[pad:].view(n, Hkv, D) for _ in range(2)]
+    gb.gattn_cache_read(want, i32([0, n]), i32([0, n]), K=outs[0], V=outs[1])
+    assert torch.equal(outs[0], ref_k) and torch.equal(outs[1], ref_v)
+
+
 @pytest.mark.parametrize("sq,sk,lk", [([0, 5], [0, 4], None), ([0, 5], [0, 9], [3]), ([0, 3, 6], [2, 4, 9], [2, 9]),
                                       ([2, 4], [3, 9], [6]), ([0, 0, 4], [0, 0, 8], [0, 4])])
 def test_write_more_rows_than_room(sq, sk, lk):

@@ -30,7 +30,7 @@ def near(got, x, pos, rad, layout, amp=1.0, inverse=False):
 
 
 WIDTHS = [(128, 128), (128, 64), (64, 64), (64, 16), (32, 32), (16, 16), (128, 96), (64, 10), (10, 6), (7, 2),
-          (256, 128), (1024, 1024)]
+          (256, 128), (1024, 1024), (64, 62), (128, 100), (72, 34), (8, 4)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
