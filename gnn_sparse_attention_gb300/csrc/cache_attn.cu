@@ -32,7 +32,7 @@
 // products (1024 + u in fp16 less 1024 + middle, one more instruction for two
 // levels, 9 us of 62 where that was tried with bf16): out off by 2.3e-7, which was 2.3e-5.
 //
-// A warp takes steps of 32 rows (16 where a row has 128 bytes) through a ring of
+// A warp takes steps of 32 rows (16 where a row has 128 bytes, 64 up to 32) through a ring of
 // its own in shared memory, filled by cp.async two steps ahead, with its own running
 // maximum and sum.  The maximum moves only when a score exceeds it by 2^4, so a
 // step needs one vote and no shuffles.
@@ -88,7 +88,7 @@ struct AttnParams {
 template <int BITS, int D>
 struct Lay {
   static constexpr int RB = D * BITS / 8;     // bytes of a row
-  static constexpr int R = RB > 64 ? 16 : 32; // rows of a step
+  static constexpr int R = RB > 64 ? 16 : RB > 32 ? 32 : 64;  // rows of a step
   static constexpr int NT = R / 16;
   static constexpr int KW = RB / 16;          // words of a K row that a lane holds
   static constexpr int KL = KW < 4 ? KW : 4;  // ... in one load
@@ -375,17 +375,23 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   const auto fetch = [&](int step, int to) {
     const uint32_t dst = my_ring + to * L::STAGE;
     if ((step + 1) * R <= keys && step < steps) {
-      const int pos0 = tile_pos(step * R), pos1 = NT == 1 ? 0 : tile_pos(step * R + 16) - 16;
-      const uint8_t *k0 = kb + int64_t(pos0) * RB + lane * 16, *v0 = vb + (k0 - kb);
-      const uint8_t *k1 = NT == 1 ? k0 : kb + int64_t(pos1) * RB + lane * 16;
-      const uint8_t *v1 = vb + (k1 - kb);
+      int pos[NT];  // where the tile's rows lie, less those before it in the step
+#pragma unroll
+      for (int h = 0; h < NT; ++h) pos[h] = tile_pos(step * R + 16 * h) - 16 * h;
 #pragma unroll
       for (int j = 0; j < L::CP; ++j) {
-        const bool second = RB == 16 ? lane >= 16 : j >= L::CP / 2;
-        copy<16>(dst + (kc ^ (RB == 128 ? (j & 1) * 64 : 0)) + j * 512, (second ? k1 : k0) + j * 512);
-        copy<16>(dst + vc + j * 512, (second ? v1 : v0) + j * 512);
+        const int h = RB == 16 ? 2 * j : j * 512 / RB / 16;
+        const int at = RB == 16 && lane >= 16 ? pos[h + 1 < NT ? h + 1 : h] : pos[h];
+        const int64_t from = int64_t(at) * RB + lane * 16 + j * 512;
+        copy<16>(dst + (kc ^ (RB == 128 ? (j & 1) * 64 : 0)) + j * 512, kb + from);
+        copy<16>(dst + vc + j * 512, vb + from);
       }
-      if (lane < R) copy<8>(dst + 2 * R * RB + lane * 8, pb + (lane < 16 ? pos0 : pos1) + lane);
+#pragma unroll
+      for (int j = 0; j < (R + 31) / 32; ++j) {
+        const int at = lane < 16 ? pos[2 * j] : pos[2 * j + 1 < NT ? 2 * j + 1 : 2 * j];
+        if (R >= 32 || lane < R)
+          copy<8>(dst + 2 * R * RB + lane * 8 + j * 256, pb + at + lane + 32 * j);
+      }
     } else if (step < steps) {  // the last one: zeros behind the rows that the query sees
 #pragma unroll 1
       for (int j = 0; j < L::CP; ++j) {
@@ -396,9 +402,9 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         copy<16>(dst + k_byte<RB>(row, ch), kb + from, in);
         copy<16>(dst + R * RB + v_byte<RB>(row, ch), vb + from, in);
       }
-      if (lane < R) {
-        const int i = step * R + lane;
-        copy<8>(dst + 2 * R * RB + lane * 8, pb + (i < keys ? tile_pos(i) : 0), i < keys);
+      for (int r = lane; r < R; r += 32) {
+        const int i = step * R + r;
+        copy<8>(dst + 2 * R * RB + r * 8, pb + (i < keys ? tile_pos(i) : 0), i < keys);
       }
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -896,7 +902,7 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   s.items = int64_t(g.U) * g.Hkv * s.groups;
   s.cluster = 1;
   const int64_t keys = lists ? std::min<int64_t>(int64_t(g.topk) * g.block, max_keys) : max_keys;
-  const int rows = g.D * p.bits / 8 > 64 ? 16 : 32;
+  const int row = g.D * p.bits / 8, rows = row > 64 ? 16 : row > 32 ? 32 : 64;  // Lay::R
   const int64_t steps = std::max<int64_t>((keys + rows - 1) / rows, 1);
   const int64_t slots = int64_t(sm_count()) * kCtas;
   // So many items that the last ones to run weigh little: a CTA for each.

@@ -97,8 +97,8 @@ struct Pack<__nv_bfloat16> {
 };
 
 // Whole vectors.  Thread j of a head has, with halves, vector j of the first half and its partner
-// in the second; else vector j alone, whose pairs are neighbours.  Vectors behind the
-// first R elements are copied.
+// in the second; else vector j alone, whose pairs are neighbours.  What lies behind the
+// first R elements is copied.
 template <class T, bool HALF>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) {
   constexpr int V = Pack<T>::V;
@@ -118,16 +118,18 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) 
   T* ko = reinterpret_cast<T*>(p.ko) + row * p.kos;
   const auto src = [&](int h) { return h < p.H ? q + h * p.D : k + (h - p.H) * p.D; };
   const auto dst = [&](int h) { return h < p.H ? qo + h * p.D : ko + (h - p.H) * p.D; };
-  const int turning = p.R / (V * NV);
-  const bool turns = j < turning;
-  const int oa = turns ? j * V : p.R + (j - turning) * V;
+  // pairs of the thread that turn: with halves all or none, else those within R
+  const int turning = HALF ? p.R / (2 * V) : 0;
+  const int live = HALF ? (j < turning ? NP : 0) : clampi(p.R / 2 - j * NP, 0, NP);
+  const bool turns = live > 0;
+  const int oa = !HALF || turns ? j * V : p.R + (j - turning) * V;
   const int ob = oa + (HALF && turns ? p.R / 2 : 0);
   float c[NP], s[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     c[i] = 1.f;
     s[i] = 0.f;
-    if (turns) turn(p, at, p.freqs[j * NP + i], &c[i], &s[i]);
+    if (i < live) turn(p, at, p.freqs[j * NP + i], &c[i], &s[i]);
   }
   for (int h = h0; h < p.HT; h += UN * p.hg) {
     uint4 a[UN], b[UN];
@@ -152,8 +154,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) 
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const int x = HALF ? i : 2 * i, y = HALF ? i + V : 2 * i + 1;
-          o[x] = f[x] * c[i] - f[y] * s[i];
-          o[y] = f[x] * s[i] + f[y] * c[i];
+          const bool on = HALF || i < live;
+          o[x] = on ? f[x] * c[i] - f[y] * s[i] : f[x];
+          o[y] = on ? f[x] * s[i] + f[y] * c[i] : f[y];
         }
         *reinterpret_cast<uint4*>(z + oa) = Pack<T>::put(o);
         if (HALF) *reinterpret_cast<uint4*>(z + ob) = Pack<T>::put(o + V * (NV - 1));
@@ -247,7 +250,7 @@ void launch(RotParams& p, bool vectors, bool whole, cudaStream_t st) {
     rotary_any_kernel<T><<<dim3(unsigned(n < 1 << 20 ? n : 1 << 20), heads), kRotThreads, 0, st>>>(p);
     return;
   }
-  p.cph = p.R / (p.half ? 2 * V : V) + (p.D - p.R) / V;
+  p.cph = p.half ? p.R / (2 * V) + (p.D - p.R) / V : p.D / V;
   // heads side by side: the fewest that give every SM about 1,024 threads, since every thread of a
   // row forms the same sines again
   const int64_t want = int64_t(sm_count()) * 1024;
@@ -333,7 +336,7 @@ gattn_status gattn_rotary(const gattn_rotary_desc* d, const void* Q, const void*
   // vectors: rows and heads start on 16-byte borders; whole: what turns together does too
   const bool vectors = d->D % V == 0 && vec(Q, qs) && vec(Q_out, qos) &&
                        (d->Hkv == 0 || (vec(K, ks) && vec(K_out, kos)));
-  const bool whole = vectors && d->width % (p.half ? 2 * V : V) == 0 && d->D / V <= kRotThreads;
+  const bool whole = vectors && (!p.half || d->width % (2 * V) == 0) && d->D / V <= kRotThreads;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (es == 4) launch<float>(p, vectors, whole, st);
   else launch<__nv_bfloat16>(p, vectors, whole, st);

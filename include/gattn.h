@@ -640,9 +640,9 @@ GATTN_API gattn_status gattn_norm_bwd(const gattn_norm_desc* desc, const void* r
  * negated, which is the backward (applied to gradients).  Q [N, H, D] and K [N, Hkv, D]
  * (Hkv = 0: none) are turned in one launch; rows may lie `*_stride` elements apart (0:
  * contiguous), heads are contiguous.  Outputs may be the inputs themselves (same stride),
- * else they must not overlap them.  Any D up to 1024, any number of heads.  Whole 16-byte
- * vectors move where addresses, strides, D and width / 2 (HALF) or width (INTERLEAVED)
- * allow it; other shapes go element by element.
+ * else they must not overlap them.  Any D up to 1024, any number of heads.  16-byte vectors
+ * move where addresses and strides allow it, and with HALF where width / 2 does too (what does not
+ * turn moves as vectors all the same); else elements go one by one.
  *
  * Position of row r: pos[r] (device int32 [N], any value) where pos is given; else r
  * belongs to sequence s with seq_q[s] <= r < seq_q[s + 1] and stands at
