@@ -34,8 +34,8 @@
 //
 // A warp takes steps of 32 rows (16 where a row has 128 bytes, 64 up to 32) through a ring of
 // its own in shared memory, filled by cp.async two steps ahead, with its own running
-// maximum and sum.  The maximum moves only when a score exceeds it by 2^4, so a
-// step needs one vote and no shuffles.
+// maximum and sum.  The maximum moves only when weights relative to it pass 2^6, seen in
+// a step's sum of them, so a step needs one vote and no shuffles.
 //
 // Split.  The steps of all (query, key head) items are one line that is cut into
 // equal stretches, one for each CTA that the GPU holds at a time, whatever the
@@ -43,8 +43,8 @@
 // Items that lie within a stretch are finished there; of one that is cut, each CTA
 // leaves its part in the workspace and a second kernel joins them.  While a CTA is at
 // one item, a warp of it finds the next, whose first steps are fetched before the
-// sums of the old one are joined.  With many more items than CTAs each item is a CTA of
-// its own, and few short ones are a cluster's each, joined through its shared memory.
+// sums of the old one are joined.  Short items are a cluster's (or a CTA's) each and
+// joined through its shared memory; see shape() for where that is better.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -65,6 +65,7 @@ constexpr int kCtas = 4;        // per SM
 constexpr int kStages = 3;
 constexpr int kMinSteps = 4;    // of a stretch: one for each warp
 constexpr int kMaxCluster = 8;
+constexpr int kMaxShared = 32;  // steps of a warp where items are not cut
 constexpr float kNone = -1e30f; // running maximum of no score
 constexpr float kOver = 64.f;   // weights relative to the running maximum: of a step's rows together
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
@@ -905,12 +906,16 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   const int row = g.D * p.bits / 8, rows = row > 64 ? 16 : row > 32 ? 32 : 64;  // Lay::R
   const int64_t steps = std::max<int64_t>((keys + rows - 1) / rows, 1);
   const int64_t slots = int64_t(sm_count()) * kCtas;
-  // So many items that the last ones to run weigh little: a CTA for each.
-  if (s.items >= 8 * slots) return s;
-  // Few short ones: a cluster for each, up to four steps to a warp, joined in shared memory.
+  // A cluster for each item, of as many CTAs as fill the GPU, where that leaves a warp at most
+  // kMaxShared steps (or where there are so many items that the last to run weigh little); else
+  // stretches.  Stretches keep long sequences of unlike lengths from waiting for the longest and use
+  // all SMs for few; but each CTA reads all lengths, goes through more items, and a second kernel
+  // joins.  Measured at D 128, 32 heads on 8, 4 bits: 128 lists of 2,048 rows (16 steps a warp)
+  // 53.8 us by clusters, 62.5 by stretches; of 4,096 rows 96 and 106; of 8,192 rows 183 and 176; 128
+  // whole caches of about 8,000 rows 202 and 190.
   int c = 1;
   while (c < kMaxCluster && c * kWarps < steps && s.items * c * 2 <= slots) c *= 2;
-  if (steps <= c * kWarps * 4) {
+  if (steps <= int64_t(c) * kWarps * kMaxShared || s.items >= 64 * slots) {
     s.cluster = c;
     return s;
   }

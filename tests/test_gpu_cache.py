@@ -392,6 +392,26 @@ def test_long(H, Hkv, dtype):
     attend(29, [1, 1], [9000, 17], H, Hkv, 64, dtype, 8, max_len=False)
 
 
+@pytest.mark.parametrize("lk,H,Hkv,lq", [([17000], 2, 1, 1), ([17000, 40000, 1, 0, 300], 4, 1, 1), ([20000], 16, 1, 2),
+                                         ([1, 18000, 16], 2, 2, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_stretches(lk, H, Hkv, lq, dtype):
+    """Few long caches of unlike lengths: items are cut between CTAs and joined by a second kernel."""
+    lq = [min(lq, n) for n in lk]
+    attend(90, lq, lk, H, Hkv, 128, dtype, 8, causal=True)
+
+
+def test_stretches_over_many_items():
+    """More items than CTAs, each of several: whole ones, cut ones, rows of no sequence, empty ones."""
+    g = torch.Generator().manual_seed(91)
+    lk = torch.randint(0, 3300, (170,), generator=g).tolist()
+    attend(91, [1] * 170, lk, 2, 2, 128, "bf16", 8, extra=9)
+
+
+def test_stretches_over_lists():
+    attend(92, [1] * 41, [20000] + [3000] * 39 + [17], 2, 2, 128, "bf16", 8, topk=128, block=128, extra=1)
+
+
 def test_sharp_scores():
     """One key outweighs all others, wherever it stands: the running maximum moves late."""
     for at in (0, 7, 100, 499):
@@ -528,10 +548,10 @@ def test_repeats_bit_by_bit():
 
 
 def test_another_stream():
-    Q, c, sq, sk, lk, kw, out, lse = attend(45, [1], [20000], 8, 1, 64, "bf16", 4)
+    Q, c, sq, sk, lk, kw, out, lse = attend(45, [1], [20000], 8, 1, 128, "bf16", 8)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
-    K, V = randn(46, 1, 1, 64), randn(47, 1, 1, 64)
+    K, V = randn(46, 1, 1, 128), randn(47, 1, 1, 128)
     st.wait_stream(torch.cuda.current_stream())
     o, z = gb.gattn_cache_fwd(Q, c, sq, sk, lk, stream=st, **kw)
     k, v = gb.gattn_cache_read(c, i32([0, 20000]), sk, lk, rows=20000, stream=st)
@@ -630,7 +650,7 @@ def test_two_graphs():
     """Two captured graphs of the split form, replayed at the same time, keep apart."""
     calls = []
     for seed in (60, 61):
-        Q, c, sq, sk, lk, kw, out, lse = attend(seed, [1], [20000], 4, 1, 64, "bf16", 4, extra=0)
+        Q, c, sq, sk, lk, kw, out, lse = attend(seed, [1], [18000], 4, 1, 128, "bf16", 8, extra=0)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             o, z = gb.gattn_cache_fwd(Q, c, sq, sk, lk, **kw)
