@@ -118,11 +118,12 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 2^(127 - exponent) as a factor: x * pow2_below(x) is in [1, 2)
-__device__ __forceinline__ float pow2_below(float x) {
+// 2^(127 - exponent) as a factor: x * pow2_below(x) is in [1, 2) for x in [2^-97, 2^(top - 126))
+__device__ __forceinline__ float pow2_below(float x, int top) {
   const int e = (__float_as_uint(x) >> 23) & 255;
-  return __uint_as_float(uint32_t(254 - clampi(e, 30, 224)) << 23);
+  return __uint_as_float(uint32_t(254 - clampi(e, 30, top)) << 23);
 }
+constexpr int kQTop = 253, kVTop = 224;  // of q: all of fp32; of p s: sums stay in it too
 template <int N>
 __device__ __forceinline__ void copy(uint32_t dst, const void* src) {
   if constexpr (N == 16)
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     if (at >= end) return;
     if (at >= before && at < before + mine) {  // one thread
       int i = u0;
-      for (; k > 1; ++i) {
+      for (; i + 1 < u1; ++i) {
         const int64_t n = int64_t(row_at<R>(p, i).steps) * heads_of;
         if (at < before + n) break;
         before += n;
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     if (p.ctas) {
       int64_t at = cur_at, end = cur_end;
       u = cur_u;
-      while (at < end) {
+      while (at < end && u < g.U) {
         r = row_at<R>(p, u);
         const int64_t row_steps = int64_t(r.steps) * heads_of;
         if (at < row_steps) break;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
         end -= row_steps;
         ++u;
       }
-      if (at < end) {
+      if (at < end && u < g.U) {
         hi = int(at / r.steps);
         s0 = int(at - int64_t(hi) * r.steps);
         s1 = int(min(int64_t(r.steps), s0 + (end - at)));
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       for (int i = 0; i < L::KW * PW; ++i) top = fmaxf(top, fabsf(f[i]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float scale = pow2_below(top) * 8192.f;  // largest element to [2^13, 2^14)
+      const float scale = pow2_below(top, kQTop) * 8192.f;  // largest element to [2^13, 2^14)
       const float up = on ? scale : 0.f, up16 = up * 0.0625f;
 #pragma unroll
       for (int w = 0; w < L::KW; ++w)
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
           const float down = fresh ? 0.f : ex2(-top);
-          const float f = kYTop * pow2_below(fmaxf(xm, down * kYTop / vf[c]));
+          const float f = kYTop * pow2_below(fmaxf(xm, down * kYTop / vf[c]), kVTop);
           const float mul = down * f / vf[c];  // at most 1
           ref[c] += top;
           sum[c] *= down;
@@ -823,7 +824,8 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
     }
     if (p.ctas && threadIdx.x == 0 && done->s0 == 0)
       p.info[int64_t(done->u) * heads_of + done->hi] =
-          cut ? make_int2(blockIdx.x, 1 + int((done->steps - done->s1 + per - 1) / per))
+          cut ? make_int2(blockIdx.x, 1 + min(int((done->steps - done->s1 + per - 1) / per),
+                                              p.ctas - 1 - int(blockIdx.x)))
               : make_int2(0, 0);
     if (!more) return;
     __syncthreads();  // statistics, sums and the old item have been read

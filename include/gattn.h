@@ -764,8 +764,10 @@ GATTN_API gattn_status gattn_cache_sums(const gattn_cache_desc* desc, const int3
  * [N][Hkv][topk] names for it (a unit of gattn_block_fwd with q_block = 1), or over the whole
  * sequence where idx is NULL.  out [N, H, D], lse fp32 [N, H]; masks, empty rows and rows of no
  * sequence as for gattn_block_fwd.  Scores and sums are fp32; bf16 queries enter exactly and the
- * weights with 11 bits, fp32 queries and their weights with 22.  `workspace` (16-byte
- * aligned, no initialisation) may be NULL when the size is 0; calls that may overlap need their own.
+ * weights with 11 bits, fp32 queries and their weights with 22.  Cached values beyond 2^96 in size
+ * may overflow.  N * H is at most 2^30.  Sums run in a fixed order, so results do not vary from
+ * run to run.  `workspace` (16-byte aligned, no initialisation) may be NULL when the size is 0; calls
+ * that may overlap need their own.
  */
 GATTN_API gattn_status gattn_cache_fwd_workspace_size(const gattn_cache_desc* desc, size_t* bytes);
 GATTN_API gattn_status gattn_cache_fwd(const gattn_cache_desc* desc, const void* Q,

@@ -432,7 +432,7 @@ def test_steps_of_any_size():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("scale", [1e-12, 1e12])
+@pytest.mark.parametrize("scale", [1e-12, 1e12, 1e-28, 3e36])
 def test_sizes_of_queries(scale, dtype):
     def edit(Q, K, V):
         Q.mul_(scale)
