@@ -402,7 +402,7 @@ __device__ __forceinline__ double scaled(int64_t v, int e) {
 // holds D / 8 levels of four.
 template <int BITS, int D, int NR>
 __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 256 ? 3 : 4) cache_sums_kernel(
-    const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int zs) {
+    const CacheParams p, const int32_t* __restrict__ since, double* __restrict__ sums, int lz) {
   constexpr int RB = D * BITS / 8, VB = RB / 8, VW = VB < 4 ? 1 : VB / 4, MT = D / 16;
   constexpr int CH = VB == 16 || NR == 32 ? 2 : 4;  // 16-row pieces on their way at a time
   // exponents of a class: with 8 bits of the step, those of a level and of the rows, 24 together
@@ -411,27 +411,38 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
   __shared__ __align__(16) uint16_t weight[kRowThreads / 32][NR];
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
+  // all divisors are powers of two
+  const int lb = 31 - __clz(g.block), lh = 31 - __clz(g.Hkv);
   const int64_t wid = int64_t(blockIdx.x) * (kRowThreads / 32) + warp;
-  const int kh = int(wid % g.Hkv);
-  const int64_t item = wid / g.Hkv;
+  const int kh = int(wid) & (g.Hkv - 1);
+  const int64_t item = wid >> lh;
+  const auto base_of = [&](int i) { return (max(g.seq_k[i], 0) >> lb) + i; };  // piece_base
   int s, b, step = 1, last;
-  if (since) {  // warps zs apart share a sequence's blocks from there on
-    if (item >= int64_t(g.S) * zs) return;
-    s = int(item / zs);
-    b = max(since[s], 0) / g.block + int(item % zs);
-    step = zs;
-    last = (span_k(g, s).len + g.block - 1) / g.block - 1;
+  if (since) {  // 2^lz warps share a sequence's blocks from there on
+    if (item >> lz >= g.S) return;
+    s = int(item >> lz);
+    b = (max(since[s], 0) >> lb) + (int(item) & ((1 << lz) - 1));
+    step = 1 << lz;
+    last = ((span_k(g, s).len + g.block - 1) >> lb) - 1;
   } else {
     if (item >= g.B) return;
-    s = piece_seq(g.seq_k, g.S, g.block, int(item));
-    b = last = int(item) - piece_base(g.seq_k, s, g.block);
+    int lo = 0;
+    for (int n = g.S; n > 1;) {  // piece_seq
+      const int st = (n + 31) >> 5, i = lo + lane * st;
+      const unsigned m = __ballot_sync(0xffffffffu, i < lo + n && base_of(i) <= int(item));
+      const int hi = m ? 31 - __clz(m) : 0;
+      n = min(st, n - hi * st);
+      lo += hi * st;
+    }
+    s = lo;
+    b = last = int(item) - base_of(s);
   }
   const Span sp = span_k(g, s);
-  const int base = piece_base(g.seq_k, s, g.block);
+  const int base = base_of(s);
   for (; b <= last; b += step) {
     const int piece = base + b;
     if (piece < 0 || piece >= g.B) break;
-    const int64_t pos = int64_t(b) * g.block;
+    const int64_t pos = int64_t(b) << lb;
     const int n = pos >= 0 && pos < sp.len ? int(min(int64_t(g.block), sp.len - pos)) : 0;
     const int64_t r0 = int64_t(kh) * g.Nk + sp.beg + (n ? pos : 0);
     double* out = sums + (int64_t(piece) * g.Hkv + kh) * D;
@@ -510,15 +521,16 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) msum += __shfl_xor_sync(0xffffffffu, msum, o);
     }
-    // Steps in fp16, as multiples of their class's 2^(se + class kClass - 127), with the class in
+    // Steps in fp16, as multiples of 2^(se + class kClass - 127); with several classes, the class in
     // what that leaves free: an exponent below kClass takes three of the five bits.
     const bool one = sx - se < kClass;
 #pragma unroll
     for (int i = 0; i < NR / 32; ++i) {
-      const uint32_t es = (par[i] >> 23) & 255;
+      const uint32_t es = (par[i] >> 23) & 255, mant = (par[i] >> 13) & 0x3f8u;
       const int k = int(es) - se, cls = max(k, 0) / kClass;
       weight[warp][lane + 32 * i] =
-          es ? uint16_t((cls << 13) | ((k - cls * kClass) << 10) | ((par[i] >> 13) & 0x3f8u)) : 0xffff;
+          one ? uint16_t(es ? ((k + 15) << 10) | mant : 0)
+              : uint16_t(es ? (cls << 13) | ((k - cls * kClass) << 10) | mant : 0xffff);
     }
     __syncwarp();
     float acc[MT][4];
@@ -535,11 +547,12 @@ __global__ void __launch_bounds__(kRowThreads, D * BITS > 512 ? 2 : D * BITS > 2
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint32_t x = *reinterpret_cast<const uint32_t*>(&weight[warp][at + 16 * c + 2 * t + 8 * q]);
-          // column gq takes class gq; with a single class all columns may be alike
-          const uint32_t lo = x & 0xffffu, hi = x >> 16;
-          const bool a = lo != 0xffffu && (one || int(lo >> 13) == gq);
-          const bool d = hi != 0xffffu && (one || int(hi >> 13) == gq);
-          h[q] = (a ? (lo & 0x1fffu) + (15u << 10) : 0u) | (d ? ((hi & 0x1fffu) + (15u << 10)) << 16 : 0u);
+          h[q] = x;  // with a single class all columns are alike
+          if (!one) {  // column gq takes class gq
+            const uint32_t lo = x & 0xffffu, hi = x >> 16;
+            h[q] = (lo != 0xffffu && int(lo >> 13) == gq ? (lo & 0x1fffu) + (15u << 10) : 0u) |
+                   (hi != 0xffffu && int(hi >> 13) == gq ? ((hi & 0x1fffu) + (15u << 10)) << 16 : 0u);
+          }
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w)
@@ -675,19 +688,19 @@ gattn_status launch_cache_sums(const CacheParams& p, const int32_t* since, doubl
                                cudaStream_t st) {
   // since: as many warps to a sequence as blocks of it would fill the GPU, since a call may renew
   // one block of each or all of one
-  int zs = 1;
-  while (since && zs < 64 && int64_t(zs) * p.g.S * p.g.Hkv < int64_t(sm_count()) * 32 &&
-         int64_t(zs) * p.g.block < p.g.Nk)
-    zs *= 2;
-  const int64_t warps = (since ? int64_t(p.g.S) * zs : int64_t(p.g.B)) * p.g.Hkv;
+  int lz = 0;
+  while (since && lz < 6 && (int64_t(p.g.S) * p.g.Hkv << lz) < int64_t(sm_count()) * 32 &&
+         int64_t(p.g.block) << lz < p.g.Nk)
+    ++lz;
+  const int64_t warps = (since ? int64_t(p.g.S) << lz : int64_t(p.g.B)) * p.g.Hkv;
   const unsigned grid = unsigned((warps + 7) / 8);
   by_layout(p, [&](auto bits, auto lpr) {
     if (p.g.block <= 32)
-      cache_sums_kernel<bits(), lpr() * 8, 32><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+      cache_sums_kernel<bits(), lpr() * 8, 32><<<grid, kRowThreads, 0, st>>>(p, since, sums, lz);
     else if (p.g.block <= 64)
-      cache_sums_kernel<bits(), lpr() * 8, 64><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+      cache_sums_kernel<bits(), lpr() * 8, 64><<<grid, kRowThreads, 0, st>>>(p, since, sums, lz);
     else
-      cache_sums_kernel<bits(), lpr() * 8, 128><<<grid, kRowThreads, 0, st>>>(p, since, sums, zs);
+      cache_sums_kernel<bits(), lpr() * 8, 128><<<grid, kRowThreads, 0, st>>>(p, since, sums, lz);
   });
   return launched("gattn_cache_sums");
 }
