@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CachePar
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
   const int64_t w = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int kh = int(w % g.Hkv);
-  const int64_t t0 = w / g.Hkv * (RPW * UN) + sub;
+  const int kh = int(w) & (g.Hkv - 1);  // a power of two
+  const int64_t t0 = (w >> (31 - __clz(g.Hkv))) * (RPW * UN) + sub;
   if (t0 - sub >= g.Nq) return;
   Row8<T> row[NR];
 #pragma unroll
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CachePara
   const BlockGeom& g = p.g;
   const int lane = threadIdx.x & 31, sub = lane / LPR, j = lane % LPR;
   const int64_t w = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int kh = int(w % g.Hkv);
-  const int64_t t0 = w / g.Hkv * (RPW * UN) + sub;
+  const int kh = int(w) & (g.Hkv - 1);  // a power of two
+  const int64_t t0 = (w >> (31 - __clz(g.Hkv))) * (RPW * UN) + sub;
   if (t0 - sub >= g.Nq) return;
   int mine = -1;
   {
