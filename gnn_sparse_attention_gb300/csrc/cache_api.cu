@@ -33,7 +33,8 @@ gattn_status params(const gattn_cache_desc* d, Use use, CacheParams* p) {
                 "D must be 32, 64 or 128 (got %d)", d->D);
   CACHE_REQUIRE(pow2(d->Hkv) && d->Hkv <= 1024, GATTN_ERR_UNSUPPORTED,
                 "Hkv must be a power of two up to 1024 (got %d)", d->Hkv);
-  CACHE_REQUIRE(int64_t(d->N) + d->S < INT32_MAX && int64_t(d->Nk) + d->S < INT32_MAX &&
+  // the attention counts rows a few steps beyond the last in 32 bits
+  CACHE_REQUIRE(int64_t(d->N) + d->S < INT32_MAX && int64_t(d->Nk) + d->S < INT32_MAX - 65536 &&
                     int64_t(d->N) * d->Hkv < (int64_t(1) << 33) &&
                     int64_t(d->Nk) * d->Hkv < (int64_t(1) << 33),
                 GATTN_ERR_UNSUPPORTED, "too many rows");

@@ -45,6 +45,12 @@
 // one item, a warp of it finds the next, whose first steps are fetched before the
 // sums of the old one are joined.  Short items are a cluster's (or a CTA's) each and
 // joined through its shared memory; see shape() for where that is better.
+//
+// Measured (32 heads of 128 on 8, 4 bits): 128 lists of 2,048 rows 54 us (285 MB, 5.3 TB/s), 8 whole
+// caches of about 32,000 rows 58 us (5.3 TB/s; 6.4 at 128,000), 4 lists of 1,024 rows 8.7 us,
+// all in captured graphs; in bf16 the first takes 172.  Half the issue slots and logic units are
+// busy; what keeps short calls from the rate of long ones is fixed: 2.5 us to find the work, 4
+// until the first rows are there, 2.4 for the join.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -65,7 +71,8 @@ constexpr int kCtas = 4;        // per SM
 constexpr int kStages = 3;
 constexpr int kMinSteps = 4;    // of a stretch: one for each warp
 constexpr int kMaxCluster = 8;
-constexpr int kMaxShared = 32;  // steps of a warp where items are not cut
+constexpr int kMaxShared = 32;  // steps of a warp where items are not cut,
+constexpr int kMaxSharedFew = 12;  // and where they fill less than a quarter of the GPU
 constexpr float kNone = -1e30f; // running maximum of no score
 constexpr float kOver = 64.f;   // weights relative to the running maximum: of a step's rows together
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
@@ -914,10 +921,13 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   // all SMs for few; but each CTA reads all lengths, goes through more items, and a second kernel
   // joins.  Measured at D 128, 32 heads on 8, 4 bits: 128 lists of 2,048 rows (16 steps a warp)
   // 53.8 us by clusters, 62.5 by stretches; of 4,096 rows 96 and 106; of 8,192 rows 183 and 176; 128
-  // whole caches of about 8,000 rows 202 and 190.
+  // whole caches of about 8,000 rows 202 and 190.  With few items the clusters leave SMs idle: 4 caches
+  // of 24,000 rows (256 CTAs, 24 steps a warp) 27.8 and 29.1 us, one of 12,000 (64 CTAs, 12 steps)
+  // 13.1 and 13.4, one of 30,000 23.4 and 17.8.
   int c = 1;
   while (c < kMaxCluster && c * kWarps < steps && s.items * c * 2 <= slots) c *= 2;
-  if (steps <= int64_t(c) * kWarps * kMaxShared || s.items >= 64 * slots) {
+  const int most = s.items * c * 4 >= slots ? kMaxShared : kMaxSharedFew;
+  if (steps <= int64_t(c) * kWarps * most || s.items >= 64 * slots) {
     s.cluster = c;
     return s;
   }

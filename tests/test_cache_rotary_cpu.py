@@ -48,7 +48,7 @@ ALL = ("write", "read", "sums", "size", "fwd")
     (dict(Nk=-1), INVALID, ALL), (dict(bits=2), UNSUPPORTED, ALL), (dict(bits=0), UNSUPPORTED, ALL),
     (dict(D=16), UNSUPPORTED, ALL), (dict(D=96), UNSUPPORTED, ALL), (dict(D=256), UNSUPPORTED, ALL),
     (dict(Hkv=0), UNSUPPORTED, ALL), (dict(Hkv=3), UNSUPPORTED, ALL), (dict(Hkv=2048), UNSUPPORTED, ALL),
-    (dict(Nk=2 ** 31 - 1), UNSUPPORTED, ALL), (dict(seq_k=None), INVALID, ALL),
+    (dict(Nk=2 ** 31 - 1), UNSUPPORTED, ALL), (dict(Nk=2 ** 31 - 65537, Hkv=1), UNSUPPORTED, ALL), (dict(seq_k=None), INVALID, ALL),
     (dict(seq_q=None), INVALID, ("write", "read", "size", "fwd")), (dict(seq_k=P + 1), INVALID, ALL),
     (dict(k=None), INVALID, ALL), (dict(v=P + 8), INVALID, ALL), (dict(par=None), INVALID, ALL),
     (dict(block=8), UNSUPPORTED, ("sums", "size", "fwd")), (dict(block=48), UNSUPPORTED, ("sums", "size", "fwd")),

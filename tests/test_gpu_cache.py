@@ -100,7 +100,10 @@ def test_write_values(bits):
             torch.linspace(-1000.25, -1000, D), torch.full((D,), 1e30), torch.linspace(1e-30, 2e-30, D),
             torch.tensor([0.0] * (D - 1) + [1e6]), torch.tensor([-1e-20] + [1.0] * (D - 1)),
             torch.arange(D) * (1 / 32) - 1, torch.tensor([3.4028235e38] * D),
-            torch.tensor([-3.4028235e38] * (D - 1) + [0.0]), torch.tensor([-0.0] * D)]
+            torch.tensor([-3.4028235e38] * (D - 1) + [0.0]), torch.tensor([-0.0] * D),
+            # steps so small next to the least value that levels leave their range by rounding
+            torch.linspace(1, 1 + 2.0 ** -20, D), -torch.linspace(1, 1 + 2.0 ** -22, D),
+            torch.full((D,), 7e10) + torch.arange(D) % 2 * 8192]
     x = torch.stack(rows).to(DEV)
     for dt in (torch.float32, torch.bfloat16):
         K = x.clamp(-3.38e38, 3.38e38).to(dt) if dt == torch.bfloat16 else x
@@ -110,6 +113,23 @@ def test_write_values(bits):
         got, _ = gb.gattn_cache_read(c, i32([0, n]), i32([0, n]), rows=n, dtype=torch.float32)
         exact = K[[0, 1, 2, 8, 15]].float()  # constant rows lose what bf16 loses of them
         assert bool(((got[[0, 1, 2, 8, 15]] - exact).abs() <= 2.0 ** -7 * exact.abs()).all())
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_rows_do_not_hang_on_their_neighbours(bits):
+    """A row at the end of the range, or with levels that rounding moves out of theirs, among ordinary
+    ones and alone: the same bytes."""
+    D = 32
+    odd = [torch.tensor([-3.4028235e38] * (D - 1) + [0.0]), torch.linspace(1, 1 + 2.0 ** -20, D),
+           torch.full((D,), 7e10) + torch.arange(D) % 2 * 8192, torch.full((D,), float("nan"))]
+    for row in odd:
+        for n in (1, 40):
+            K = randn(82, n, 1, D)
+            for at in (0, n // 2):
+                X = K.clone()
+                X[at, 0] = row.to(DEV)
+                write(X, K, [0, n], [0, n], None, bits, n)
+                write(K, X, [0, n], [0, n], None, bits, n)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
