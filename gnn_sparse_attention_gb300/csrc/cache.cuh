@@ -15,21 +15,27 @@ struct CacheParams {
 };
 
 // The sequence that row `r` belongs to, its number within and the rows of
-// that sequence; s = -1 for none.  Every lane searches for a row of its own.
+// that sequence; s = -1 for none.  Every lane searches for a row of its own.  With one
+// row a sequence, as in serving, row r is sequence r: looked at first, since a search is
+// a chain of loads.
 struct SeqRow {
   int s, i, n;
 };
-__device__ __forceinline__ SeqRow seq_row(const int32_t* __restrict__ beg, int S, int N, int r,
-                                          int from = 0) {
-  int lo = from, hi = S;  // the last s with beg[s] <= r, if beg[from] is one
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (beg[mid] <= r) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ SeqRow seq_row(const int32_t* __restrict__ beg, int S, int N, int r) {
+  if (S <= 0) return {-1, 0, 0};
+  int lo = min(r, S - 1), b = beg[lo], e = beg[lo + 1];
+  if (r < b || r >= e) {
+    lo = 0;  // the last s with beg[s] <= r, if beg[0] is one
+    for (int hi = S; hi - lo > 1;) {
+      const int mid = lo + (hi - lo) / 2;
+      if (beg[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    b = beg[lo];
+    e = beg[lo + 1];
   }
-  if (lo >= S) return {-1, 0, 0};
-  const int b = clampi(beg[lo], 0, N), n = clampi(beg[lo + 1], b, N) - b;
-  const int i = r - b;
+  b = clampi(b, 0, N);
+  const int n = clampi(e, b, N) - b, i = r - b;
   return {i >= 0 && i < n ? lo : -1, i, n};
 }
 
