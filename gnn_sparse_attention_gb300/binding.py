@@ -958,7 +958,7 @@ assert _CACHE_PACK.size == ctypes.sizeof(_CacheDesc)
 ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 _CODES = {torch.float32: GATTN_F32, torch.bfloat16: GATTN_BF16}
-_INT32, _empty_like = torch.int32, torch.empty_like
+_INT32, _F32, _empty, _empty_like = torch.int32, torch.float32, torch.empty, torch.empty_like
 _device = torch._C._cuda_getDevice              # of tensors that are on a GPU already
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -1078,7 +1078,10 @@ def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "ha
     else:
         handle, other = _stream_of(dev, stream)
     if out_q is None:
-        out_q = _new(dev, other, Q.shape, dt) if other is not None or qs != qos else _empty_like(Q)
+        if other is not None:
+            out_q = _new(dev, other, Q.shape, dt)
+        else:
+            out_q = _empty_like(Q) if qs == qos else _empty((N, H, D), dtype=dt, device=dev)
     else:
         if out_q.shape != Q.shape:
             raise ValueError(f"out_q must have the shape {tuple(Q.shape)}")
@@ -1087,8 +1090,10 @@ def gattn_rotary(Q: torch.Tensor, freqs: torch.Tensor, K=None, layout: str = "ha
         p_k = p_ko = None
     else:
         if out_k is None:
-            out_k = _new(dev, other, K.shape, dt) if other is not None or ks != kos else \
-                _empty_like(K)
+            if other is not None:
+                out_k = _new(dev, other, K.shape, dt)
+            else:
+                out_k = _empty_like(K) if ks == kos else _empty((N, Hkv, D), dtype=dt, device=dev)
         else:
             if out_k.shape != K.shape:
                 raise ValueError(f"out_k must have the shape {tuple(K.shape)}")
@@ -1191,8 +1196,11 @@ def gattn_cache_read(cache: Cache, seq_q: torch.Tensor, seq_k: torch.Tensor, len
     shape = (rows, cache.Hkv, cache.D)
     handle, other = (_raw_stream(dev), None) if stream is None else _stream_of(dev, stream)
     if given is None:
-        K = _new(dev, other, shape, dtype)
-        V = _empty_like(K) if other is None else _new(dev, other, shape, dtype)
+        if other is None:
+            K = _empty(shape, dtype=dtype, device=dev)
+            V = _empty_like(K)
+        else:
+            K, V = _new(dev, other, shape, dtype), _new(dev, other, shape, dtype)
     else:
         for name, t in (("K", K), ("V", V)):
             if t is not None:
@@ -1264,13 +1272,14 @@ def gattn_cache_fwd(Q: torch.Tensor, cache: Cache, seq_q: torch.Tensor, seq_k: t
             raise ValueError("idx repeats one list for all rows and heads; make it contiguous")
     handle, other = (_raw_stream(dev), None) if stream is None else _stream_of(dev, stream)
     if out is None:
-        out = _like(Q, other)
+        out = _empty_like(Q) if other is None else _new(dev, other, Q.shape, Q.dtype)
     else:
         _want("out", out, Q.shape, Q.dtype, dev)
     if lse is None:
-        lse = _new(dev, other, (N, H), torch.float32)
+        lse = _empty((N, H), dtype=_F32, device=dev) if other is None else \
+            _new(dev, other, (N, H), _F32)
     else:
-        _want("lse", lse, (N, H), torch.float32, dev)
+        _want("lse", lse, (N, H), _F32, dev)
     desc = _cache_desc(cache, S, N, H, Q.dtype, block, topk, causal, scale, max_len_k, seq_q, seq_k,
                        len_k, su, sh)
     ws = _workspace(workspace, dev, other, "gattn_cache_fwd_workspace_size", desc,

@@ -12,7 +12,7 @@
 // rows it takes fewer heads, so that there are threads enough.
 //
 // Measured: 32,768 rows of 32 + 8 heads of 128 in bf16 102 us (6.6 TB/s of reads and writes, 0.98 of
-// a copy); 20,013 rows of 8 + 8 heads of 64 in fp32 27 us (6.0 TB/s); 16 rows 4.2 us, latency.  A width
+// a copy); 20,013 rows of 8 + 8 heads of 64 in fp32 27 us (6.0 TB/s); 16 rows 3.8 us, latency.  A width
 // of 10 in halves, whose partners lie on no border: 150 us for the first.
 #include <cmath>
 
