@@ -73,7 +73,6 @@ constexpr int kMinSteps = 4;    // of a stretch: one for each warp
 constexpr int kMaxCluster = 8;
 constexpr int kMaxShared = 32;  // steps of a warp where items are not cut,
 constexpr int kMaxSharedFew = 12;  // and where they fill less than a quarter of the GPU
-constexpr float kNone = -1e30f; // running maximum of no score
 constexpr float kOver = 64.f;   // weights relative to the running maximum: of a step's rows together
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
 // 2^-19 of it keeps its 11 bits; set again where a step could leave fp16's range.
@@ -186,6 +185,10 @@ __device__ __forceinline__ int v_byte(int row, int ch) {
   if (RB == 64) ch ^= ((row >> 1) & 1) << 1;
   return row * RB + ch * 16;
 }
+
+// What weights are taken relative to where the greatest score is `top`: -inf stands for no score, and
+// finite scores may be as low as fp32 goes.
+__device__ __forceinline__ float base_of(float top) { return top == neg_inf() ? 0.f : top; }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       }
       const int h = NC * t + c;
       if (gq == 0) {
-        sref[warp][h] = fresh ? kNone : ref[c];
+        sref[warp][h] = fresh ? neg_inf() : ref[c];
         sl[warp][h] = sum[c];
       }
       const float back = (kSplit ? 1.f : 16777216.f) / vf[c];
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sref[w][h]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(sref[w][h] - top);
+        const float f = ex2(sref[w][h] - base_of(top));
         l = fmaf(sl[w][h], f, l);
         sw[w][h] = f;
       }
@@ -807,12 +810,12 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
       cluster.sync();
       for (int e = (rank * kThr + threadIdx.x) * 4; e < heads * D; e += p.cluster * kThr * 4) {
         const int h = e / D, d = e % D;
-        float top = kNone, l = 0.f;
+        float top = neg_inf(), l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < p.cluster; ++r)
           top = fmaxf(top, *cluster.map_shared_rank(&sref[0][h], r));
         for (int r = 0; r < p.cluster; ++r) {
-          const float f = ex2(*cluster.map_shared_rank(&sref[0][h], r) - top);
+          const float f = ex2(*cluster.map_shared_rank(&sref[0][h], r) - base_of(top));
           const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(
               ring + *cluster.map_shared_rank(&so_at[0], r) + e * 4, r));
           o.x = fmaf(x.x, f, o.x);
@@ -858,7 +861,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int
   const int2 in = live ? p.info[blockIdx.x] : make_int2(0, 0);
   if (in.y == 0) return;
   const int h = q / (D / 4), d = q % (D / 4) * 4;
-  float top = kNone, l = 0.f;
+  float top = neg_inf(), l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (q < quads && grp < ng) {
 #pragma unroll 4
@@ -867,7 +870,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int
       const float* w = p.part + (((int64_t(in.x) + i) * 2 + (i == 0)) * hc + h) * (D + 4);
       const float4 x = *reinterpret_cast<const float4*>(w + d);
       const float2 st = *reinterpret_cast<const float2*>(w + D);
-      const float m = fmaxf(top, st.x), f0 = ex2(top - m), f1 = ex2(st.x - m);
+      const float m = fmaxf(top, st.x), f0 = ex2(top - base_of(m)), f1 = ex2(st.x - base_of(m));
       o.x = fmaf(o.x, f0, x.x * f1);
       o.y = fmaf(o.y, f0, x.y * f1);
       o.z = fmaf(o.z, f0, x.z * f1);
@@ -883,7 +886,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int
   if (grp > 0 || q >= quads) return;
   for (int i = 1; i < ng; ++i) {
     const int x = threadIdx.x + i * mine;
-    const float m = fmaxf(top, sr[x]), f0 = ex2(top - m), f1 = ex2(sr[x] - m);
+    const float m = fmaxf(top, sr[x]), f0 = ex2(top - base_of(m)), f1 = ex2(sr[x] - base_of(m));
     o.x = fmaf(o.x, f0, so[x].x * f1);
     o.y = fmaf(o.y, f0, so[x].y * f1);
     o.z = fmaf(o.z, f0, so[x].z * f1);
