@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               e[h][q][c] = ex2(x[h][q][c]);
-              y[h][q][c] = e[h][q][c] * (vs[h][q] * vf[c]);
+              // in this order a weight of 0 gives 0 whatever the factor makes of the step alone
+              y[h][q][c] = e[h][q][c] * vs[h][q] * vf[c];
               es += e[h][q][c];
               ys += y[h][q][c];
             }

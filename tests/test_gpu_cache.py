@@ -492,6 +492,26 @@ def test_scores_far_below_zero(n, topk, dtype):
     assert bool(lse.isfinite().all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [2, 8])
+@pytest.mark.parametrize("D,bits,rows", [(128, 8, 16), (64, 4, 64)])
+def test_weightless_keys_of_large_steps(D, bits, rows, H, dtype):
+    """Constant rows of V carry all weight, and a key 200 nats below has steps of 2^30, 2^90 or none: 0 times its
+    row is 0.  In the same step of a warp, and in a later one of it (32 steps on)."""
+    n = 33 * rows
+    for at in (5, 32 * rows + 3):
+        for step in (2.0 ** 30, 2.0 ** 90, 0.0):
+            def edit(Q, K, V):
+                Q.fill_(1.0)
+                K.zero_()
+                K[at] = -200.0 / math.sqrt(D)
+                V.fill_(1.5)
+                V[at] = torch.arange(D, device=DEV) % 2 ** bits * step
+            *_, out, lse = attend(101, [1], [n], H, 1, D, dtype, bits, edit=edit, extra=0)
+            # the mean of equal values: one rounding, and fp32 ones of a weight, a product and a few sums
+            assert bool(((out.double() - 1.5).abs() <= ref.HALF[DT[dtype]] * 1.5 + 2.0 ** -19).all())
+
+
 def test_one_key_is_returned():
     _, c, _, sk, lk, _, out, _ = attend(34, [1, 1], [1, 1], 4, 2, 64, "f32", 4, extra=0)
     val = ref.values(c, 1)[0].float()
