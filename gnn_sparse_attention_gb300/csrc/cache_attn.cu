@@ -74,6 +74,9 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxShared = 32;  // steps of a warp where items are not cut,
 constexpr int kMaxSharedFew = 12;  // and where they fill less than a quarter of the GPU
 constexpr float kOver = 64.f;   // weights relative to the running maximum: of a step's rows together
+// A column whose scores stay within kStay (in log2) keeps its maximum when others move: a lane's 8 rows
+// or fewer then weigh kOver or less.
+constexpr float kStay = 3.f;
 // Largest p s of a column in fp16: to [kYTop, 2 kYTop) when the factor is set, so that what is
 // 2^-19 of it keeps its 11 bits; set again where a step could leave fp16's range.
 constexpr float kYTop = 32.f, kYMax = 65504.f;
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;  // middle level
   static_assert(NC == 1 || !kSplit, "");
   static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
+  static_assert(2 * NT * 8.f <= kOver, "a lane's rows, each of weight 2^kStay");
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
   __shared__ Seg segs[2];                           // this one and the next
   __shared__ float sref[kWarps][HC], sl[kWarps][HC], sw[kWarps][HC];
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           for (int h = 0; h < NT; ++h) top = fmaxf(top, fmaxf(x[h][0][c], x[h][1][c]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (top == neg_inf()) top = 0.f;  // scores that are not numbers
+          if (top == neg_inf() || (!fresh && top <= kStay)) top = 0.f;  // -inf: no score is a number
           float xm = 0.f;
 #pragma unroll
           for (int h = 0; h < NT; ++h)
@@ -648,7 +652,10 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
           for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
           const float down = fresh ? 0.f : ex2(-top);
           const float f = kYTop * pow2_below(fmaxf(xm, down * kYTop / vf[c]), kVTop);
-          const float mul = down * f / vf[c];  // at most 1
+          // Below 2, and 1 or less for a column that stays.  One that moves loses 2^kStay at least, which
+          // vf gains besides mul: vf is at its limit after 49 moves, before acc grows by 2^49 (it starts
+          // below 2^23 for a row).
+          const float mul = down * f / vf[c];
           ref[c] += top;
           sum[c] *= down;
           msum[c] *= down;

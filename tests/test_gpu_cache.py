@@ -512,6 +512,27 @@ def test_weightless_keys_of_large_steps(D, bits, rows, H, dtype):
             assert bool(((out.double() - 1.5).abs() <= ref.HALF[DT[dtype]] * 1.5 + 2.0 ** -19).all())
 
 
+@pytest.mark.parametrize("H,dtype", [(2, "f32"), (2, "bf16"), (8, "bf16")])
+def test_slowly_rising_scores(H, dtype):
+    """Each step raises one head's scores by a factor of 400 and the others' by 1%, and only the first rows have
+    values: what the others hold is scaled with their own maximum, however often a neighbour's moves."""
+    D, R, W = 128, 16, 200
+    n, N = 4 * R * W, 256 * torch.cuda.get_device_properties(0).multi_processor_count  # a CTA for each item
+    c = gb.gattn_cache_new(n, 1, D, 8)
+    K, V = torch.zeros(n, 1, D), torch.zeros(n, 1, D)
+    K[:] = (torch.arange(n) // (4 * R)).reshape(n, 1, 1)  # a warp takes every fourth step
+    V[:4 * R] = (torch.arange(D) * 255 // (D - 1)) * (2.0 ** 30 if dtype == "f32" else 2.0 ** 50)
+    ref.filled(c, K, V)
+    Q = torch.full((N, H, D), 6.0 / 512, device=DEV, dtype=DT[dtype])
+    Q[:, 0] = 6.0
+    sq, sk = i32([0, N]), i32([0, n])
+    out, lse = gb.gattn_cache_fwd(Q, c, sq, sk, scale=1 / D)
+    r = ref.attention(Q[:1], c, [0, 1], [0, n], [n], scale=1 / D)
+    ref.check(out[:1], r, "out", 7.0)
+    ref.check(lse[:1], r, "lse", 7.0)
+    assert bool((out == out[:1]).all()) and bool((lse == lse[:1]).all())
+
+
 def test_one_key_is_returned():
     _, c, _, sk, lk, _, out, _ = attend(34, [1, 1], [1, 1], 4, 2, 64, "f32", 4, extra=0)
     val = ref.values(c, 1)[0].float()
