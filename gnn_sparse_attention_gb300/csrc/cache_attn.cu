@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
   constexpr int HC = 4 * NC;               // heads of a column group
   constexpr float kMid = BITS == 4 ? 8.f : 128.f;  // middle level
   static_assert(NC == 1 || !kSplit, "");
-  static_assert(HC * D * 4 <= L::RING, "a warp's sums take the place of its ring");
+  static_assert(HC * D * 4 <= L::STAGE, "a warp's sums take the place of one stage, beside the next item's copies");
   static_assert(2 * NT * 8.f <= kOver, "a lane's rows, each of weight 2^kStay");
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage]: K, V, par of R rows
   __shared__ Seg segs[2];                           // this one and the next

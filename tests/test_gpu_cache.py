@@ -1,4 +1,5 @@
 """The key/value cache in 4 and 8 bits on the GPU against its definition (tests/cache_ref.py)."""
+import ctypes
 import math
 
 import numpy as np
@@ -419,6 +420,33 @@ def test_stretches(lk, H, Hkv, lq, dtype):
     """Few long caches of unlike lengths: items are cut between CTAs and joined by a second kernel."""
     lq = [min(lq, n) for n in lk]
     attend(90, lq, lk, H, Hkv, 128, dtype, 8, causal=True)
+
+
+def workspace_bytes(Q, c, S, kw):
+    topk, n = 0 if kw["idx"] is None else kw["idx"].shape[2], ctypes.c_size_t()
+    some = i32([0])  # sizes hang on no offset
+    desc = gb._cache_desc(c, S, Q.shape[0], Q.shape[1], Q.dtype, kw["block"], topk, kw["causal"], kw["scale"],
+                          kw["max_len_k"], some, some, some)
+    assert gb.load_library().gattn_cache_fwd_workspace_size(desc, ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("H,dtype", [(4, "f32"), (4, "bf16"), (16, "bf16")])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_stretches_of_every_layout(D, bits, H, dtype):
+    """The form that cuts items and joins them, in every layout: a few long caches, and many items of one to 135
+    steps, of which a CTA has several (the next one's copies are under way beside the old one's sums)."""
+    row = D * bits // 8
+    R = 16 if row > 64 else 32 if row > 32 else 64  # rows of a step
+    Q, c, *_, kw, out, lse = attend(102, [1] * 4, [450 * R + 7, 3, 0, 100 * R + 1], H, 2, D, dtype, bits, extra=2)
+    assert workspace_bytes(Q, c, 4, kw) > 0
+    g = torch.Generator().manual_seed(103)
+    lk = torch.randint(0, 3 * R, (159,), generator=g).tolist()
+    lk[::9] = torch.randint(0, 20 * R, (len(lk[::9]),), generator=g).tolist()
+    lk.insert(70, 135 * R - 5)
+    Q, c, *_, kw, out, lse = attend(104, [1] * 160, lk, H, 2, D, dtype, bits, extra=5)
+    assert workspace_bytes(Q, c, 160, kw) > 0
 
 
 def test_stretches_over_many_items():
