@@ -625,6 +625,81 @@ def test_offsets_about_the_cache(seq_k, len_k):
     assert all(g.shape == t.shape for g, t in zip(guard, (c.k, c.v, c.par)))
 
 
+class Fenced:
+    """Tensors in the middle of marked memory."""
+
+    MARGIN, MARK = 1 << 16, 0xc3
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, dtype, *shape):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 2 * self.MARGIN,), self.MARK, dtype=torch.uint8, device=DEV)
+        self.all.append((buf, n))
+        return buf[self.MARGIN:self.MARGIN + n].view(dtype).view(shape)
+
+    def whole(self):
+        torch.cuda.synchronize()
+        return all(bool((b[:self.MARGIN] == self.MARK).all()) and bool((b[self.MARGIN + n:] == self.MARK).all())
+                   for b, n in self.all)
+
+
+ODD_OFFSETS = [([-5, 1 << 30, 70], [50, 50]), ([60, 20, 10], [99, -3]), ([0, 90, 2000], [1 << 30, 1 << 30]),
+               ([0, 60, 100], [60, 40])]
+
+
+@pytest.mark.parametrize("seq_k,len_k", ODD_OFFSETS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,D,bits", [(100, 32, 4), (100, 64, 8), (20000, 128, 8)])
+def test_memory_around_the_tensors(rows, D, bits, dtype, seq_k, len_k):
+    """Whatever the offsets and lists say, what stands before and behind each tensor that a call writes stays, and
+    read, sums and attention leave the cache as it is.  With 20,000 rows items are cut, through a workspace."""
+    fence, dt = Fenced(), DT[dtype]
+    c = gb.Cache(fence(torch.uint8, 2, rows, D * bits // 8), fence(torch.uint8, 2, rows, D * bits // 8),
+                 fence(torch.bfloat16, 2, rows, 4), bits)
+    ref.filled(c, randn(105, rows, 2, D), randn(106, rows, 2, D))
+    new = randn(107, 3, 2, D, dtype=dt)
+    Q = randn(108, 3, 4, D, dtype=dt)
+    idx = torch.arange(-2, 6, dtype=torch.int32, device=DEV).expand(3, 2, 8).contiguous()
+    K, V = fence(dt, 3, 2, D), fence(dt, 3, 2, D)
+    sums = fence(torch.float64, rows // 16 + 2, 2, D)
+    out, lse = fence(dt, 3, 4, D), fence(torch.float32, 3, 4)
+    kw = {"idx": None, "block": 16, "causal": False, "scale": 0.0, "max_len_k": 0}
+    n = max(workspace_bytes(Q, c, 2, kw), workspace_bytes(Q, c, 2, {**kw, "idx": idx}))
+    assert (n > 0) == (rows == 20000)
+    ws = fence(torch.uint8, n) if n else None
+    far = [min(max(x * rows // 100, -(1 << 31)), (1 << 31) - 1) for x in seq_k]
+    for sq in ([0, 1, 3], [0, 2, 1 << 30], [-4, 1, 2], [2, 1, 0], [3, 3, 3]):
+        for k, ln in ((seq_k, len_k), (far, None), (far, len_k)):
+            args = i32(sq), i32(k), None if ln is None else i32(ln)
+            gb.gattn_cache_write(c, new, new, *args)
+            assert fence.whole()
+            kept = [t.clone() for t in (c.k, c.v, c.par.view(torch.int16))]
+            for since in (None, i32([-7, 1 << 30]), i32([(1 << 31) - 1, 0])):
+                gb.gattn_cache_read(c, *args, since=since, K=K, V=V)
+                gb.gattn_cache_sums(c, args[1], 16, lens=args[2], since=since, sums=sums)
+            for causal in (False, True):
+                for choice in (None, idx):
+                    gb.gattn_cache_fwd(Q, c, *args, idx=choice, block=16, causal=causal, out=out, lse=lse, workspace=ws)
+            assert fence.whole()
+            assert all(torch.equal(a, b) for a, b in zip(kept, (c.k, c.v, c.par.view(torch.int16))))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("width", [64, 10])
+def test_memory_around_rotary(width, layout, dtype):
+    fence, dt = Fenced(), DT[dtype]
+    Q, K = randn(109, 70, 4, 64, dtype=dt), randn(110, 70, 2, 64, dtype=dt)
+    q, k = fence(dt, 70, 4, 64), fence(dt, 70, 2, 64)
+    f = gb.gattn_rotary_freqs(width)
+    for sq in ([0, 30, 70], [0, 30, 1 << 30], [-5, 20, 71], [70, 30, 0], [71, 80, 90]):
+        for kw in ({}, {"seq_k": i32([0, -9, 1 << 30])}, {"len_k": i32([-(1 << 31), (1 << 31) - 1])}):
+            gb.gattn_rotary(Q, f, K=K, layout=layout, seq_q=i32(sq), out_q=q, out_k=k, **kw)
+    assert fence.whole()
+
+
 def test_offsets_beyond_32_bits():
     """A cache whose bytes pass 2^31 and rows 2^25: written, read, summed and attended to near its end."""
     rows, Hkv, D = (1 << 25) + 300, 2, 64
