@@ -268,13 +268,13 @@ class BlockCache:
     def append(self, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor) -> None:
         """Rows [seq[s], seq[s+1]) of K and V [N, Hkv, D] become the next ones of sequence s, as after a
         prompt that was attended to otherwise (K with its positions)."""
-        old = self.length.clone()
-        self.length += seq[1:] - seq[:-1]
-        self._append(_packed(K), _packed(V), seq, old)
+        length = self.length + (seq[1:] - seq[:-1])
+        self._append(_packed(K), _packed(V), seq, length)
+        self.length.copy_(length)
 
-    def _append(self, K, V, seq, old):
-        gb.gattn_cache_write(self.cache, K, V, seq, self.seq_k, self.length)
-        gb.gattn_cache_sums(self.cache, self.seq_k, self.block, lens=self.length, since=old,
+    def _append(self, K, V, seq, length):
+        gb.gattn_cache_write(self.cache, K, V, seq, self.seq_k, length)
+        gb.gattn_cache_sums(self.cache, self.seq_k, self.block, lens=length, since=self.length,
                             sums=self.sums)
 
     @torch.no_grad()
@@ -284,20 +284,21 @@ class BlockCache:
         """(out [N, H, D], lse [N, H]) of the new rows [seq[s], seq[s+1]) of every sequence, each of
         which sees what stands before it and itself.  With ``freqs`` Q and K are given their
         positions first.  Every row reads the cache for itself: meant for a few rows a sequence."""
-        old = self.length.clone()
-        self.length += seq[1:] - seq[:-1]
+        length = self.length + (seq[1:] - seq[:-1])
         if freqs is not None:
             Q, K = gb.gattn_rotary(_rows(Q), freqs, K=_rows(K), layout=layout, seq_q=seq,
-                                   seq_k=self.seq_k, len_k=self.length, amp=amp)
+                                   seq_k=self.seq_k, len_k=length, amp=amp)
         Q = _packed(Q)
-        self._append(_packed(K), _packed(V), seq, old)
+        self._append(_packed(K), _packed(V), seq, length)
         idx = None
         if self.topk:
             idx = gb.gattn_block_select(Q, self.sums, seq, self.seq_k, self.topk, self.block, 1,
-                                        self.cache.rows, len_k=self.length, causal=True,
+                                        self.cache.rows, len_k=length, causal=True,
                                         max_len_k=self.room)
-        return gb.gattn_cache_fwd(Q, self.cache, seq, self.seq_k, self.length, idx=idx,
-                                  block=self.block, scale=scale, causal=True, max_len_k=self.room)
+        out = gb.gattn_cache_fwd(Q, self.cache, seq, self.seq_k, length, idx=idx, block=self.block,
+                                 scale=scale, causal=True, max_len_k=self.room)
+        self.length.copy_(length)  # a call that is refused leaves the lengths
+        return out
 
 
 class _GatedResidualNorm(torch.autograd.Function):

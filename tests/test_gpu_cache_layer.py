@@ -241,3 +241,31 @@ def test_block_cache_step_in_a_graph():
             a.copy_(b)
         g.replay()
         assert torch.equal(out, want[t][0]) and torch.equal(lse, want[t][1])
+
+
+def test_block_cache_refused_calls_leave_it():
+    """A call that is refused, early or late in its chain, leaves lengths as they were, and the call put right gives
+    what it gives without the refused one."""
+    S, H, Hkv, D, room = 2, 4, 2, 64, 64
+    f = gb.gattn_rotary_freqs(D)
+    seq = i32([0, 1, 2])
+    K0, V0 = randn(60, 40, Hkv, D, dtype=torch.bfloat16), randn(61, 40, Hkv, D, dtype=torch.bfloat16)
+    Q, K, V = (randn(62 + i, S, h, D, dtype=torch.bfloat16) for i, h in enumerate((H, Hkv, Hkv)))
+    outs = []
+    for refused in (False, True):
+        c = layer.BlockCache(S, room, Hkv, D, topk=2, block=16)
+        c.append(K0, V0, i32([0, 20, 40]))
+        if refused:
+            for q, k, v, s, kw in ((Q, K[:, :1], V, seq, {}), (Q, K, V.float(), seq, {}), (Q, K, V, seq.long(), {}),
+                                   (Q, K, V, i32([0, 2]), {}), (Q[:, :3], K, V, seq, {}), (Q, K, V, seq, {"scale": -1.0}),
+                                   (Q.half(), K.half(), V.half(), seq, {}), (Q, K, V, seq, {"layout": "other"})):
+                with pytest.raises((ValueError, gb.GattnError)):
+                    c.step(q, k, v, s, freqs=f, **kw)
+                assert c.length.dtype == torch.int32 and c.length.tolist() == [20, 20]
+            for k, v, s in ((K[:, :1], V, seq), (K, V, seq.long()), (K, V, i32([0, 2])), (K, V[:1], seq)):
+                with pytest.raises((ValueError, gb.GattnError)):
+                    c.append(k, v, s)
+                assert c.length.tolist() == [20, 20]
+        outs.append((*c.step(Q, K, V, seq, freqs=f), c.length.clone(), c.sums.clone()))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
