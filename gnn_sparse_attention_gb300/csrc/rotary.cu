@@ -44,9 +44,11 @@ __device__ __forceinline__ bool position(const RotParams& p, int r, int64_t* at)
   }
   const SeqRow x = seq_row(p.seq_q, p.S, p.N, r);
   if (x.s < 0) return false;
-  const int64_t len = p.len_k ? int64_t(p.len_k[x.s])
-                      : p.seq_k ? int64_t(p.seq_k[x.s + 1]) - p.seq_k[x.s]
-                                : x.n;
+  int64_t len = p.len_k ? int64_t(p.len_k[x.s]) : x.n;
+  if (p.seq_k) {  // the attention cuts lengths to the room
+    const int64_t room = max(int64_t(p.seq_k[x.s + 1]) - p.seq_k[x.s], int64_t(0));
+    len = p.len_k ? max(min(len, room), int64_t(0)) : room;
+  }
   *at = len - x.n + x.i;
   return true;
 }

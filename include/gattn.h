@@ -648,8 +648,9 @@ GATTN_API gattn_status gattn_norm_bwd(const gattn_norm_desc* desc, const void* r
  * belongs to sequence s with seq_q[s] <= r < seq_q[s + 1] and stands at
  *     r - seq_q[s] + len - (seq_q[s + 1] - seq_q[s]),
  * len being len_k[s], or seq_k[s + 1] - seq_k[s], or the sequence's own rows, whichever is
- * given first: the position that the attention over blocks or over a cache gives to that
- * query.  Rows of no sequence are not written.
+ * given first, and len_k[s] cut to 0 .. seq_k[s + 1] - seq_k[s] where both are: the position that
+ * the attention over blocks or over a cache gives to that query, as long as seq_k stays
+ * within the keys' rows.  Rows of no sequence are not written.
  *
  * Frequencies: device uint64 [width / 2], turns per position in units of 2^-64, so that
  * position * frequency wraps to the exact fraction of a turn: an angle is off by less than

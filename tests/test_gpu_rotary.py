@@ -100,6 +100,25 @@ def test_sequences(cached, width):
         assert torch.equal(y, out)
 
 
+@pytest.mark.parametrize("width", [64, 10])
+def test_lengths_beyond_the_room(width):
+    """The position is that of the attention, which cuts lengths to the room that seq_k leaves."""
+    sq, sk, lk, cut = [0, 3, 5, 6], [0, 40, 45, 45], [41, 1000, 7], [40, 5, 0]
+    x = randn(14, 6, 2, 64)
+    f, rad = gb.gattn_rotary_freqs(width), ref.frequencies(width)
+    pos = [i + cut[s] - (sq[s + 1] - sq[s]) for s in range(3) for i in range(sq[s + 1] - sq[s])]
+    got, _ = gb.gattn_rotary(x, f, seq_q=i32(sq), seq_k=i32(sk), len_k=i32(lk))
+    near(got, x, pos, rad, "half")
+    same, _ = gb.gattn_rotary(x, f, seq_q=i32(sq), seq_k=i32(sk), len_k=i32(cut))
+    assert torch.equal(got, same)
+    less, _ = gb.gattn_rotary(x, f, seq_q=i32(sq), seq_k=i32(sk), len_k=i32([-1, -5, 0]))
+    none, _ = gb.gattn_rotary(x, f, seq_q=i32(sq), seq_k=i32(sk), len_k=i32([0, 0, 0]))
+    assert torch.equal(less, none)
+    # without the room there is nothing to cut by
+    pos = [i + lk[s] - (sq[s + 1] - sq[s]) for s in range(3) for i in range(sq[s + 1] - sq[s])]
+    near(gb.gattn_rotary(x, f, seq_q=i32(sq), len_k=i32(lk))[0], x, pos, rad, "half")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_slices_and_in_place(layout, dtype):
