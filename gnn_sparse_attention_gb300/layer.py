@@ -252,7 +252,8 @@ class BlockCache:
     ``step`` appends new rows and attends from them, over the ``topk`` blocks that score highest
     for each row and key head, or over the whole sequence with ``topk=0``.  ``length`` (int32 [S], on
     the device) counts the rows; nothing is read back, so steps of one row a sequence can be
-    captured into a graph.  A sequence must not outgrow its room.
+    captured into a graph.  A sequence must not outgrow its room: nothing of its neighbours changes, but
+    its own results are undefined from then on, and ``check_errors`` raises.
     """
 
     def __init__(self, S: int, room: int, Hkv: int, D: int, bits: int = 4, topk: int = 16,
@@ -263,6 +264,13 @@ class BlockCache:
         self.length = torch.zeros(S, dtype=torch.int32, device=device)
         blocks = gb.gattn_block_count(S * room, S, block)
         self.sums = torch.zeros(blocks, Hkv, D, dtype=torch.float64, device=device)
+
+    def check_errors(self) -> None:
+        """Raise RuntimeError if a sequence has outgrown its room.  Reads the lengths back: waits for
+        the GPU, and must not be called while a graph is captured."""
+        full = (self.length > self.room).nonzero().flatten().tolist()
+        if full:
+            raise RuntimeError(f"BlockCache: sequences {full} have more than {self.room} rows")
 
     @torch.no_grad()
     def append(self, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor) -> None:
@@ -283,7 +291,8 @@ class BlockCache:
              scale: float = 0.0):
         """(out [N, H, D], lse [N, H]) of the new rows [seq[s], seq[s+1]) of every sequence, each of
         which sees what stands before it and itself.  With ``freqs`` Q and K are given their
-        positions first.  Every row reads the cache for itself: meant for a few rows a sequence."""
+        positions first.  Every row reads the cache for itself: meant for a few rows a sequence.
+        Rows of no sequence hold anything."""
         length = self.length + (seq[1:] - seq[:-1])
         if freqs is not None:
             Q, K = gb.gattn_rotary(_rows(Q), freqs, K=_rows(K), layout=layout, seq_q=seq,

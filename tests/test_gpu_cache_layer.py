@@ -269,3 +269,22 @@ def test_block_cache_refused_calls_leave_it():
         outs.append((*c.step(Q, K, V, seq, freqs=f), c.length.clone(), c.sums.clone()))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_block_cache_says_when_it_is_full():
+    """A sequence that outgrows its room is told, and its neighbours keep their rows."""
+    S, Hkv, D, room = 3, 2, 64, 32
+    c = layer.BlockCache(S, room, Hkv, D, topk=0, block=16)
+    K, V = randn(65, 96, Hkv, D), randn(66, 96, Hkv, D)
+    c.append(K, V, i32([0, 32, 63, 95]))  # the first and the last are full
+    c.check_errors()
+    kept = [t.clone() for t in (c.cache.k, c.cache.v)]
+    q = randn(67, 3, 4, D)
+    c.step(q, K[:3], V[:3], i32([0, 0, 1, 1]))
+    c.check_errors()
+    c.step(q, K[:3], V[:3], i32([0, 1, 1, 1]))
+    with pytest.raises(RuntimeError, match="0"):
+        c.check_errors()
+    for t, was in zip((c.cache.k, c.cache.v), kept):
+        assert torch.equal(t[:, 2 * room:], was[:, 2 * room:])
+        assert torch.equal(t[:, room:2 * room - 1], was[:, room:2 * room - 1])
