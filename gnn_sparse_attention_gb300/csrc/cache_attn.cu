@@ -15,7 +15,7 @@
 // from registers (mma.sync m16n8k16: 16 rows of the cache by 8 query heads).
 // Through tcgen05 every level would have to be stored to shared memory as 16
 // bits first, 2 to 4 times the bytes that arrive, for products that fill a
-// tenth of the legacy pipe.  S^T = K Q^T has rows of the cache as rows; P^T is
+// fifth of the legacy pipe.  S^T = K Q^T has rows of the cache as rows; P^T is
 // turned by movmatrix into the right operand of O^T = V^T P^T.  A lane's elements
 // of K and V are whole words of a row, since any order of the head's elements
 // will do for K as long as q has the same, and for V it only names output rows.
@@ -46,11 +46,14 @@
 // sums of the old one are joined.  Short items are a cluster's (or a CTA's) each and
 // joined through its shared memory; see shape() for where that is better.
 //
-// Measured (32 heads of 128 on 8, 4 bits): 128 lists of 2,048 rows 54 us (285 MB, 5.3 TB/s), 8 whole
-// caches of about 32,000 rows 58 us (5.3 TB/s; 6.4 at 128,000), 4 lists of 1,024 rows 8.7 us,
+// Measured (32 heads of 128 on 8, 4 bits): 128 lists of 2,048 rows 55 us (285 MB, 5.2 TB/s), 8 whole
+// caches of about 32,000 rows 59 us (5.2 TB/s; 6.3 at 128,000), 4 lists of 1,024 rows 8.1 us,
 // all in captured graphs; in bf16 the first takes 172.  Half the issue slots and logic units are
 // busy; what keeps short calls from the rate of long ones is fixed: 2.5 us to find the work, 4
-// until the first rows are there, 2.4 for the join.
+// until the first rows are there, 2.4 for the join.  The first with fp32 queries 74 us (twice the columns,
+// levels moved about zero), 64 heads on 8 62, 128 heads (a second pass) 110, D 64 39, in 8 bits 94.
+// Queries of one sequence read it once each: 4 sequences of 6,000 rows with 5 each 32 us, of 4.1 that
+// reading once would take.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -930,11 +933,19 @@ Shape shape(const CacheParams& p, gattn_dtype dt, int max_keys, bool lists) {
   // kMaxShared steps (or where there are so many items that the last to run weigh little); else
   // stretches.  Stretches keep long sequences of unlike lengths from waiting for the longest and use
   // all SMs for few; but each CTA reads all lengths, goes through more items, and a second kernel
-  // joins.  Measured at D 128, 32 heads on 8, 4 bits: 128 lists of 2,048 rows (16 steps a warp)
-  // 53.8 us by clusters, 62.5 by stretches; of 4,096 rows 96 and 106; of 8,192 rows 183 and 176; 128
-  // whole caches of about 8,000 rows 202 and 190.  With few items the clusters leave SMs idle: 4 caches
-  // of 24,000 rows (256 CTAs, 24 steps a warp) 27.8 and 29.1 us, one of 12,000 (64 CTAs, 12 steps)
-  // 13.1 and 13.4, one of 30,000 23.4 and 17.8.
+  // joins.  Measured, us by clusters / by stretches (32 heads on 8; steps of 32 rows at D 128 with 4 bits
+  // and D 64 with 8, of 64 at D 64 with 4 bits, of 16 at D 128 with 8):
+  //                               D 128, 4 bits   8 bits          D 64, 4 bits    8 bits          D 128, 4 bits, fp32
+  //   128 lists of 2,048 rows     55.0 / 62.4     93.0 / 100      39.0 / 45.1     54.6 / 57.4     73.3 / 82.0
+  //   of 4,096 rows               97.0 / 105      172 / 183       61.7 / 68.6     95.7 / 101      131 / 140
+  //   of 8,192 rows               179 / 188       329 / 345       109 / 117       177 / 187       246 / 254
+  //   128 caches of ~8,000 rows   206 / 190       351 / 335       122 / 111       184 / 190       269 / 245
+  //   4 caches of 24,000          27.3 / 28.7     41.5 / 39.5     18.9 / 22.2     23.5 / 25.4     36.1 / 36.1
+  //   one of 12,000               12.9 / 12.7     17.3 / 13.4     9.8 / 9.7       11.1 / 11.3     15.1 / 14.1
+  //   one of 30,000               23.6 / 17.6     34.6 / 19.7     15.4 / 12.3     19.8 / 15.3     28.3 / 20.3
+  //   4 caches of 8,000           13.6 / 17.3     19.8 / 20.7     10.2 / 14.2     11.7 / 14.8     17.3 / 20.7
+  // Lists are all of one length, so clusters are up to 6% better for long ones too, which the rule, made
+  // for lengths that it does not know, leaves to stretches.
   int c = 1;
   while (c < kMaxCluster && c * kWarps < steps && s.items * c * 2 <= slots) c *= 2;
   const int most = s.items * c * 4 >= slots ? kMaxShared : kMaxSharedFew;

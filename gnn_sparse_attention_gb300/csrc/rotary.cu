@@ -6,14 +6,14 @@
 // quarter and a rest in [-1/8, 1/8) turns that fp32 holds to 2^-28, and sine and
 // cosine of the rest are taken in fp32.
 //
-// The rows are read and written once: the bound is HBM.  A thread owns a pair
-// of 16-byte vectors of one row (the two halves that turn together, or two
-// neighbours) and walks over heads with the sines that it formed once; with few
-// rows it takes fewer heads, so that there are threads enough.
+// The rows are read and written once: the bound is HBM.  A thread owns the two
+// 16-byte vectors of a row that turn together (halves), or one (neighbours), and
+// walks over heads with the sines that it formed once; with few rows it takes
+// fewer heads, so that there are threads enough.
 //
-// Measured: 32,768 rows of 32 + 8 heads of 128 in bf16 102 us (6.6 TB/s of reads and writes, 0.98 of
-// a copy); 20,013 rows of 8 + 8 heads of 64 in fp32 27 us (6.0 TB/s); 16 rows 3.8 us, latency.  A width
-// of 10 in halves, whose partners lie on no border: 150 us for the first.
+// Measured: 32,768 rows of 32 + 8 heads of 128 in bf16 103 us (6.5 TB/s of reads and writes, 0.97 of
+// a copy), in fp32 198; 20,013 rows of 8 + 8 heads of 64 in fp32 27 us (5.9 TB/s); 16 rows 3.9 us,
+// latency.  The first with a width of 96 119 us, of 10 in halves, whose partners lie on no border, 154, of 10 with neighbours 105.
 #include <cmath>
 
 #include "cache.cuh"

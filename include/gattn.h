@@ -654,7 +654,8 @@ GATTN_API gattn_status gattn_norm_bwd(const gattn_norm_desc* desc, const void* r
  *
  * Frequencies: device uint64 [width / 2], turns per position in units of 2^-64, so that
  * position * frequency wraps to the exact fraction of a turn: an angle is off by less than
- * 2^-29 of a turn at positions up to 2^22, and beyond by what fp64 leaves of the frequency.
+ * 2^-27 of a turn at positions up to 2^22 (the rest of a quarter turn is rounded to fp32, 2^-28),
+ * and beyond by what fp64 leaves of the frequency.
  */
 typedef enum { GATTN_ROTARY_HALF = 0, GATTN_ROTARY_INTERLEAVED = 1 } gattn_rotary_layout;
 
@@ -708,7 +709,8 @@ GATTN_API gattn_status gattn_rotary_freqs(int32_t width, double theta, int32_t s
  * towards +inf and 0 below 2^-126, and u = clamp(rint(x * inv + c), 0, L) with inv = 1 / s (0 for
  * s = 0) and c = -m * inv; each of these is one operation in fp32, rounded to nearest (the last
  * an FMA), so that levels do not hang on who computes them.  |x - (m + s u)| is at most s / 2
- * but for those roundings.  A row with a non-finite element gets m = s = NaN and reads as NaN.
+ * but for those roundings.  A row with a non-finite element gets m = s = NaN and reads as NaN; elements
+ * beyond 2^126 in size may stand for more than fp32 holds and read as infinite.
  *
  * Sequences are laid out as for gattn_block_*: sequence s owns the rows [seq_q[s], seq_q[s+1])
  * of the new tokens and the cache rows [seq_k[s], seq_k[s] + len_k[s]) (len_k NULL: up to
@@ -754,7 +756,7 @@ GATTN_API gattn_status gattn_cache_read(const gattn_cache_desc* desc, const int3
 /*
  * gattn_block_sums of the values that the cached keys stand for, in the same table.  Each sum is
  * exact but for its last rounding to 64 bits, as long as the steps of the block's rows are
- * within 2^8 of each other (2^28 with 4 bits) and their least values within 2^38; else it is that
+ * within 2^7 of each other (2^28 with 4 bits) and their least values within 2^38; else it is that
  * of fp64 additions in row order.
  */
 GATTN_API gattn_status gattn_cache_sums(const gattn_cache_desc* desc, const int32_t* since,
@@ -764,9 +766,10 @@ GATTN_API gattn_status gattn_cache_sums(const gattn_cache_desc* desc, const int3
  * Softmax attention of every row of Q [N, H, D] over the cache: over the blocks that idx
  * [N][Hkv][topk] names for it (a unit of gattn_block_fwd with q_block = 1), or over the whole
  * sequence where idx is NULL.  out [N, H, D], lse fp32 [N, H]; masks, empty rows and rows of no
- * sequence as for gattn_block_fwd.  Scores and sums are fp32; bf16 queries enter exactly and the
- * weights with 11 bits, fp32 queries and their weights with 22.  Cached values beyond 2^96 in size
- * may overflow.  N * H is at most 2^30.  Sums run in a fixed order, so results do not vary from
+ * sequence as for gattn_block_fwd.  Scores and sums are fp32; bf16 queries enter exactly (elements below
+ * 2^-26 of their head's largest to within 2^-34 of it) and the weights with 11 bits, fp32 queries and
+ * their weights with 22; weights below 2^-126 of a row's greatest count as 0.  Cached values and queries
+ * beyond 2^96 in size may overflow.  N * H is at most 2^30.  Sums run in a fixed order, so results do not vary from
  * run to run.  `workspace` (16-byte aligned, no initialisation) may be NULL when the size is 0; calls
  * that may overlap need their own.
  */
