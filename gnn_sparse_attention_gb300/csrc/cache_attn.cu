@@ -432,7 +432,21 @@ __global__ void __launch_bounds__(kThr, kCtas) cache_attn_kernel(const AttnParam
 
   if (warp == 0) next(segs[0], true);
   __syncthreads();
-  if (segs[0].steps == 0) return;  // a row of no sequence
+  if (segs[0].steps == 0) {  // a row of no sequence
+    if (p.ctas == 0 && p.cluster > 1) {
+      // If offsets change meanwhile, others of the cluster may have seen one: they read this
+      // CTA's sums, so it stays, with none.
+      if (threadIdx.x < HC) {
+        sref[0][threadIdx.x] = neg_inf();
+        sl[0][threadIdx.x] = 0.f;
+      }
+      if (threadIdx.x == 0) so_at[0] = 0;
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      cluster.sync();
+    }
+    return;
+  }
   open();
   int stage = 0;
   fetch(seg->s0 + rank * kWarps + warp, 0);

@@ -755,6 +755,18 @@ def test_another_stream():
     assert not torch.equal(k3, k2[-1:])
 
 
+@pytest.mark.parametrize("n", [300, 2000])
+def test_rows_of_no_sequence_between_clusters(n):
+    """Rows of no sequence, among and behind those of sequences, where an item is a cluster's."""
+    Q, c, sq, sk, lens, kw, out, lse = attend(112, [1, 0, 1], [n, n, 5], 4, 2, 64, "bf16", 4, extra=4)
+    assert workspace_bytes(Q, c, 3, kw) == 0
+    far = i32([2, 3, 3, 4])  # rows 0, 1 and behind 3 are nobody's
+    o, z = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    gb.gattn_cache_fwd(Q.roll(2, 0), c, far, sk, lens, out=o, lse=z, **kw)
+    assert torch.equal(o[2:4], out[:2]) and torch.equal(z[2:4], lse[:2])
+    assert bool((o[:2] == 7.0).all()) and bool((o[4:] == 7.0).all()) and bool((z[:2] == 7.0).all())
+
+
 def test_no_sequences_and_no_rows():
     c = gb.gattn_cache_new(0, 2, 64, 4)
     z = i32([0])
