@@ -883,7 +883,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const AttnParams p, int
   const int q = blockIdx.y * mine + threadIdx.x % mine, grp = threadIdx.x / mine, ng = 256 / mine;
   const bool live = seq_row(g.seq_q, g.S, g.Nq, u).s >= 0;
   cudaGridDependencySynchronize();  // the parts are there
-  const int2 in = live ? p.info[blockIdx.x] : make_int2(0, 0);
+  int2 in = live ? p.info[blockIdx.x] : make_int2(0, 0);
+  // parts that exist, also where offsets changed meanwhile and nobody wrote the item's entry
+  in.x = clampi(in.x, 0, p.ctas - 1);
+  in.y = clampi(in.y, 0, p.ctas - in.x);
   if (in.y == 0) return;
   const int h = q / (D / 4), d = q % (D / 4) * 4;
   float top = neg_inf(), l = 0.f;

@@ -755,6 +755,19 @@ def test_another_stream():
     assert not torch.equal(k3, k2[-1:])
 
 
+@pytest.mark.parametrize("fill", [0x00, 0x7f, 0xff])
+def test_workspaces_of_any_content(fill):
+    """Nothing hangs on what a workspace holds: few items and many, rows of no sequence among them."""
+    for lk, extra in (([18000, 3, 0], 2), ([9000] * 39 + [17], 5)):
+        Q, c, sq, sk, lens, kw, out, lse = attend(111, [1] * len(lk), lk, 4, 2, 128, "bf16", 8, extra=extra)
+        n = workspace_bytes(Q, c, len(lk), kw)
+        assert n > 0
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        o, z = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+        gb.gattn_cache_fwd(Q, c, sq, sk, lens, out=o, lse=z, workspace=ws, **kw)
+        assert torch.equal(o, out) and torch.equal(z, lse)
+
+
 @pytest.mark.parametrize("n", [300, 2000])
 def test_rows_of_no_sequence_between_clusters(n):
     """Rows of no sequence, among and behind those of sequences, where an item is a cluster's."""
